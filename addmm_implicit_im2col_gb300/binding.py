@@ -29,7 +29,10 @@ NOALLOC_SCRATCH_BYTES = 32 << 20
 
 MODES = {"default": 0, "tf32": 1, "simt": 2, "force_tc3": 3, "force_tc1": 4, "direct": 5}
 ACT_RELU = 0x100
-KERNELS = {0: "none", 1: "tc3", 2: "tc1", 3: "simt", 4: "fill", 5: "direct"}
+KERNELS = {0: "none", 1: "tc3", 2: "tc1", 3: "simt", 4: "fill", 5: "direct", 6: "mxfp4",
+           7: "experts"}
+F32, F16, BF16, MXFP4 = 0, 1, 2, 3
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 # Every symbol the header declares, with (restype, argtypes).
 _i64, _dbl, _vp, _int = ctypes.c_int64, ctypes.c_double, ctypes.c_void_p, ctypes.c_int
@@ -54,6 +57,26 @@ SIGNATURES = {
     "gemm_addmm_f32_host": (_int, [_vp, _int, _vp, _vp, _vp, _i64, _i64, _i64, _dbl, _dbl, _int,
                                    _vp]),
     "conv2d_gemm_f32_host": (_int, [_vp, _vp, _vp, _vp] + [_i64] * 13 + [_int, _vp]),
+    "mxfp4_bytes": (ctypes.c_size_t, [_i64] * 3),
+    "mxfp4_quantize": (_int, [_vp, _int] + [_i64] * 5 + [_int, _vp, _vp]),
+    "mxfp4_dequantize": (_int, [_vp] + [_i64] * 3 + [_int, _vp, _vp]),
+    "mxfp4_linear_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _int]),
+    "mxfp4_linear": (_int, [_vp, _int, _i64, _vp, _vp, _vp, _int, _i64, _i64, _i64, _int, _vp,
+                            ctypes.c_size_t, _vp]),
+    "mxfp4_linear_backward_workspace_bytes": (ctypes.c_size_t, [_i64] * 3),
+    "mxfp4_linear_backward": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp,
+                                     ctypes.c_size_t, _vp]),
+    "moe_route": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _i64, _i64, _int, _dbl, _vp,
+                         _vp, _vp]),
+    "moe_route_backward": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _int, _dbl,
+                                  _vp, _vp]),
+    "moe_layout_size": (_i64, [_i64] * 3),
+    "moe_layout": (_int, [_vp, _i64, _i64, _i64, _vp, _vp]),
+    "mxfp4_experts_linear_workspace_bytes": (ctypes.c_size_t, [_i64] * 4),
+    "mxfp4_experts_linear": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _int] + [_i64] * 5
+                             + [_int, _vp, ctypes.c_size_t, _vp]),
+    "moe_combine": (_int, [_vp, _int, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "moe_combine_backward": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "imc_status_string": (ctypes.c_char_p, [_int]),
     "imc_last_kernel": (_int, []),
     "imc_last_kernel_name": (ctypes.c_char_p, []),
@@ -173,6 +196,80 @@ def conv2d_gemm_f32_host(x, w, bias, out, B, IC, H, W, OC, KH, KW, sH, sW, pH, p
                          stream) -> int:
     return load().conv2d_gemm_f32_host(x, w, bias, out, B, IC, H, W, OC, KH, KW, sH, sW, pH, pW,
                                        dH, dW, mode, stream)
+
+
+def mxfp4_bytes(batch, rows, cols) -> int:
+    return int(load().mxfp4_bytes(batch, rows, cols))
+
+
+def mxfp4_quantize(x, dtype, batch, rows, cols, batch_stride, row_stride, transpose, q,
+                   stream) -> int:
+    return load().mxfp4_quantize(x, dtype, batch, rows, cols, batch_stride, row_stride, transpose,
+                                 q, stream)
+
+
+def mxfp4_dequantize(q, batch, rows, cols, dtype, out, stream) -> int:
+    return load().mxfp4_dequantize(q, batch, rows, cols, dtype, out, stream)
+
+
+def mxfp4_linear_workspace_bytes(M, K, x_dtype) -> int:
+    return int(load().mxfp4_linear_workspace_bytes(M, K, x_dtype))
+
+
+def mxfp4_linear(x, x_dtype, row_stride, w, bias, out, out_dtype, M, N, K, flags, workspace,
+                 workspace_bytes, stream) -> int:
+    return load().mxfp4_linear(x, x_dtype, row_stride, w, bias, out, out_dtype, M, N, K, flags,
+                               workspace, workspace_bytes, stream)
+
+
+def mxfp4_linear_backward_workspace_bytes(M, N, K) -> int:
+    return int(load().mxfp4_linear_backward_workspace_bytes(M, N, K))
+
+
+def mxfp4_linear_backward(grad, x, w, dtype, M, N, K, grad_x, grad_w, workspace, workspace_bytes,
+                          stream) -> int:
+    return load().mxfp4_linear_backward(grad, x, w, dtype, M, N, K, grad_x, grad_w, workspace,
+                                        workspace_bytes, stream)
+
+
+def moe_route(logits, dtype, T, E, row_stride, bias, k, score, groups, top_groups, renormalize,
+              scale, weights, experts, stream) -> int:
+    return load().moe_route(logits, dtype, T, E, row_stride, bias, k, score, groups, top_groups,
+                            renormalize, scale, weights, experts, stream)
+
+
+def moe_route_backward(grad_weights, logits, dtype, T, E, row_stride, experts, k, score,
+                       renormalize, scale, grad_logits, stream) -> int:
+    return load().moe_route_backward(grad_weights, logits, dtype, T, E, row_stride, experts, k,
+                                     score, renormalize, scale, grad_logits, stream)
+
+
+def moe_layout_size(T, k, E) -> int:
+    return int(load().moe_layout_size(T, k, E))
+
+
+def moe_layout(experts, T, k, E, layout, stream) -> int:
+    return load().moe_layout(experts, T, k, E, layout, stream)
+
+
+def mxfp4_experts_linear_workspace_bytes(T, k, E, K) -> int:
+    return int(load().mxfp4_experts_linear_workspace_bytes(T, k, E, K))
+
+
+def mxfp4_experts_linear(x, x_dtype, x_rows, row_stride, w, bias, layout, out, out_dtype, T, k, E,
+                         N, K, flags, workspace, workspace_bytes, stream) -> int:
+    return load().mxfp4_experts_linear(x, x_dtype, x_rows, row_stride, w, bias, layout, out,
+                                       out_dtype, T, k, E, N, K, flags, workspace,
+                                       workspace_bytes, stream)
+
+
+def moe_combine(y, dtype, weights, T, k, N, out, stream) -> int:
+    return load().moe_combine(y, dtype, weights, T, k, N, out, stream)
+
+
+def moe_combine_backward(grad, y, dtype, weights, T, k, N, grad_y, grad_weights, stream) -> int:
+    return load().moe_combine_backward(grad, y, dtype, weights, T, k, N, grad_y, grad_weights,
+                                       stream)
 
 
 def selftest_wait_timeout(limit_us, stream=None) -> int:
@@ -416,3 +513,324 @@ def conv2d_host(x, w, bias=None, stride=1, padding=0, dilation=1, *, mode="defau
     if rc != IMC_OK:
         raise ImcError(rc, "conv2d_gemm_f32_host")
     return out
+
+
+# -------------------------------------- 4-bit products and experts (torch level)
+_DTYPE_IDS = {}
+
+
+def _dtype_id(dtype, name):
+    if not _DTYPE_IDS:
+        import torch
+        _DTYPE_IDS.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    try:
+        return _DTYPE_IDS[dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, got {dtype}") from None
+
+
+def _check_rows(t, name, ndim=2):
+    """A CUDA tensor of a float type with contiguous last dimension; its type's id."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dim() != ndim:
+        raise ValueError(f"{name} must be a CUDA tensor of {ndim} dimensions")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return _dtype_id(t.dtype, name)
+
+
+def _row_stride(t):
+    """Elements between two rows; a single row's stride is its length."""
+    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+
+
+def _check_plain(t, name, dtype, shape, like):
+    """A contiguous CUDA tensor of this type and shape on the device of `like`."""
+    import torch
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {like.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _raise(rc, what):
+    if rc != IMC_OK:
+        raise ImcError(rc, what)
+
+
+class MxFp4:
+    """A matrix [rows, cols] (or ``batch`` of them) in MXFP4, as quantize_mxfp4 writes it.
+
+    ``data`` is the device buffer (codes, then scales; imc.h has its layout);
+    ``shape`` the shape of the values it stands for.
+    """
+
+    __slots__ = ("data", "batch", "rows", "cols", "batched")
+
+    def __init__(self, data, batch, rows, cols, batched):
+        self.data, self.batch, self.rows, self.cols, self.batched = data, batch, rows, cols, batched
+
+    @property
+    def shape(self):
+        return (self.batch, self.rows, self.cols) if self.batched else (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return self.data.device
+
+
+def quantize_mxfp4(x, *, transpose=False):
+    """x [rows, cols] or [batch, rows, cols] in MXFP4 (a scale for every 32 values of a row).
+
+    x is float32, float16 or bfloat16, its rows may be strided.  ``transpose``
+    quantises x^T instead (blocks down the columns of x), without a transposed
+    copy: the operand of a product that sums over the rows of x.
+    """
+    import torch
+    dt = _check_rows(x, "x", 3 if getattr(x, "ndim", 2) == 3 else 2)
+    batched = x.dim() == 3
+    batch = x.shape[0] if batched else 1
+    rows, cols = x.shape[-2:]
+    size = mxfp4_bytes(batch, cols, rows) if transpose else mxfp4_bytes(batch, rows, cols)
+    q = torch.empty(size, dtype=torch.uint8, device=x.device)
+    _raise(mxfp4_quantize(x.data_ptr(), dt, batch, rows, cols, x.stride(0) if batched else 0,
+                          _row_stride(x), 1 if transpose else 0, q.data_ptr(),
+                          _stream_ptr(x.device)), "mxfp4_quantize")
+    return MxFp4(q, batch, cols, rows, batched) if transpose else MxFp4(q, batch, rows, cols, batched)
+
+
+def dequantize_mxfp4(q, *, dtype=None):
+    """The values an MxFp4 stands for, as a tensor of ``dtype`` (default float32)."""
+    import torch
+    if not isinstance(q, MxFp4):
+        raise TypeError("q must be an MxFp4")
+    dtype = torch.float32 if dtype is None else dtype
+    dt = _dtype_id(dtype, "dtype")
+    out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    _raise(mxfp4_dequantize(q.data.data_ptr(), q.batch, q.rows, q.cols, dt, out.data_ptr(),
+                            _stream_ptr(q.device)), "mxfp4_dequantize")
+    return out
+
+
+def linear_mxfp4(x, w, bias=None, *, relu=False, out_dtype=None, out=None):
+    """out = x @ w^T (+ bias) with both operands in MXFP4, summed in fp32.
+
+    x [M, K] and w [N, K] are MxFp4, or float tensors that the call quantises
+    (a weight that is used again is better quantised once, by quantize_mxfp4).
+    bias [N] float32; ``relu`` fuses max(v, 0); out is [M, N] of ``out_dtype``
+    (default: x's type, float32 for an MxFp4).
+    """
+    import torch
+    if not isinstance(w, MxFp4):
+        _check_rows(w, "w")
+        w = quantize_mxfp4(w)
+    if w.batched:
+        raise ValueError("w must be [N, K]")
+    if isinstance(x, MxFp4):
+        if x.batched:
+            raise ValueError("x must be [M, K]")
+        xp, dt, ld, M, K = x.data.data_ptr(), MXFP4, 0, x.rows, x.cols
+        default = torch.float32
+    else:
+        dt = _check_rows(x, "x")
+        M, K = x.shape
+        xp, ld, default = x.data_ptr(), _row_stride(x), x.dtype
+    N = w.rows
+    if w.cols != K:
+        raise ValueError(f"w must be [N, K] = [N, {K}], got {list(w.shape)}")
+    if w.device != x.device:
+        raise ValueError("x and w must be on one device")
+    _check_plain(bias, "bias", torch.float32, (N,), x)
+    out_dtype = (out.dtype if out is not None else default) if out_dtype is None else out_dtype
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    else:
+        _check_plain(out, "out", out_dtype, (M, N), x)
+    nbytes = 0 if dt == MXFP4 else mxfp4_bytes(1, M, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    _raise(mxfp4_linear(xp, dt, ld, w.data.data_ptr(), _ptr(bias), out.data_ptr(),
+                        _dtype_id(out_dtype, "out_dtype"), M, N, K, ACT_RELU if relu else 0,
+                        _ptr(ws), nbytes, _stream_ptr(x.device)), "mxfp4_linear")
+    return out
+
+
+def linear_mxfp4_backward(grad, x, w):
+    """Gradients of ``linear_mxfp4(x, w)`` for grad [M, N], x [M, K], w [N, K].
+
+    Returns (grad_x [M, K], grad_w [N, K]), each a 4-bit product whose operands
+    are quantised along the axis that it sums over.  All tensors are contiguous
+    and of one float type.
+    """
+    import torch
+    dt = _check_rows(grad, "grad")
+    M, N = grad.shape
+    _check_rows(x, "x")
+    K = x.shape[1]
+    _check_plain(grad, "grad", grad.dtype, (M, N), grad)
+    _check_plain(x, "x", grad.dtype, (M, K), grad)
+    _check_plain(w, "w", grad.dtype, (N, K), grad)
+    grad_x = torch.empty((M, K), dtype=grad.dtype, device=grad.device)
+    grad_w = torch.empty((N, K), dtype=grad.dtype, device=grad.device)
+    nbytes = mxfp4_linear_backward_workspace_bytes(M, N, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=grad.device)
+    _raise(mxfp4_linear_backward(grad.data_ptr(), x.data_ptr(), w.data_ptr(), dt, M, N, K,
+                                 grad_x.data_ptr(), grad_w.data_ptr(), ws.data_ptr(), nbytes,
+                                 _stream_ptr(grad.device)), "mxfp4_linear_backward")
+    return grad_x, grad_w
+
+
+def route_experts(logits, k, bias=None, *, score="softmax", groups=1, top_groups=1,
+                  renormalize=True, scale=1.0):
+    """The k experts of each token and their weights, from router logits [T, E].
+
+    Scores are softmax or sigmoid of the logits; the choice is by score + bias
+    (bias [E] float32), within the ``top_groups`` best of ``groups`` equal runs of
+    experts (a group counts by its two best); ties go to the lowest index.
+    Returns (weights [T, k] float32, experts [T, k] int32), best first; the
+    weights are the chosen scores, divided by their sum (``renormalize``), times
+    ``scale``.
+    """
+    import torch
+    dt = _check_rows(logits, "logits")
+    T, E = logits.shape
+    _check_plain(bias, "bias", torch.float32, (E,), logits)
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    experts = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    _raise(moe_route(logits.data_ptr(), dt, T, E, _row_stride(logits), _ptr(bias), k, SCORES[score],
+                     groups, top_groups, 1 if renormalize else 0, float(scale), weights.data_ptr(),
+                     experts.data_ptr(), _stream_ptr(logits.device)), "moe_route")
+    return weights, experts
+
+
+def route_experts_backward(grad_weights, logits, experts, *, score="softmax", renormalize=True,
+                           scale=1.0):
+    """Gradient of route_experts' weights with respect to the logits, [T, E] of their type."""
+    import torch
+    dt = _check_rows(logits, "logits")
+    T, E = logits.shape
+    k = experts.shape[-1]
+    _check_plain(experts, "experts", torch.int32, (T, k), logits)
+    _check_plain(grad_weights, "grad_weights", torch.float32, (T, k), logits)
+    grad = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _raise(moe_route_backward(grad_weights.data_ptr(), logits.data_ptr(), dt, T, E,
+                              _row_stride(logits), experts.data_ptr(), k, SCORES[score],
+                              1 if renormalize else 0, float(scale), grad.data_ptr(),
+                              _stream_ptr(logits.device)), "moe_route_backward")
+    return grad
+
+
+class ExpertsLayout:
+    """The slots (token * k + i) in expert order, as experts_layout writes them.
+
+    ``offsets`` [E + 1]: where each expert's slots begin in ``order`` (slots of no
+    expert come after offsets[E]); ``order`` [T * k].
+    """
+
+    __slots__ = ("data", "T", "k", "E")
+
+    def __init__(self, data, T, k, E):
+        self.data, self.T, self.k, self.E = data, T, k, E
+
+    @property
+    def offsets(self):
+        return self.data[: self.E + 1]
+
+    @property
+    def order(self):
+        return self.data[2 * self.E + 3: 2 * self.E + 3 + self.T * self.k]
+
+
+def experts_layout(experts, num_experts):
+    """Sorts the slots of experts [T, k] int32 by expert (stable).
+
+    An expert index outside [0, num_experts) leaves its slot out.
+    """
+    import torch
+    if not isinstance(experts, torch.Tensor):
+        raise TypeError("experts must be a torch.Tensor")
+    if experts.dim() != 2:
+        raise ValueError("experts must be [T, k]")
+    _check_plain(experts, "experts", torch.int32, experts.shape, experts)
+    T, k = experts.shape
+    size = moe_layout_size(T, k, num_experts)
+    data = torch.empty(size, dtype=torch.int32, device=experts.device)
+    _raise(moe_layout(experts.data_ptr(), T, k, num_experts, data.data_ptr(),
+                      _stream_ptr(experts.device)), "moe_layout")
+    return ExpertsLayout(data, T, k, num_experts)
+
+
+def experts_linear_mxfp4(x, w, layout, bias=None, *, relu=False, out_dtype=None):
+    """Each slot's row times its expert's weight: out[slot] = x[row] @ w[e]^T (+ bias[e]).
+
+    x is [T, K] (every slot of a token takes its row) or [T * k, K] (a row for
+    each slot); w an MxFp4 [E, N, K]; bias [E, N] float32; layout of
+    experts_layout.  Returns [T * k, N] in slot order, of ``out_dtype`` (default:
+    x's type); slots of no expert are 0.
+    """
+    import torch
+    dt = _check_rows(x, "x")
+    if not isinstance(w, MxFp4) or not w.batched:
+        raise TypeError("w must be an MxFp4 [E, N, K]")
+    if not isinstance(layout, ExpertsLayout):
+        raise TypeError("layout must be an ExpertsLayout")
+    T, k, E = layout.T, layout.k, layout.E
+    rows, K = x.shape
+    if w.batch != E or w.cols != K:
+        raise ValueError(f"w must be [{E}, N, {K}], got {list(w.shape)}")
+    if rows != T and rows != T * k:
+        raise ValueError(f"x must have {T} or {T * k} rows, got {rows}")
+    if w.device != x.device or layout.data.device != x.device:
+        raise ValueError("x, w and layout must be on one device")
+    N = w.rows
+    _check_plain(bias, "bias", torch.float32, (E, N), x)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    out = torch.empty((T * k, N), dtype=out_dtype, device=x.device)
+    nbytes = mxfp4_experts_linear_workspace_bytes(T, k, E, K)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _raise(mxfp4_experts_linear(x.data_ptr(), dt, rows, _row_stride(x), w.data.data_ptr(),
+                                _ptr(bias), layout.data.data_ptr(), out.data_ptr(),
+                                _dtype_id(out_dtype, "out_dtype"), T, k, E, N, K,
+                                ACT_RELU if relu else 0, ws.data_ptr(), nbytes,
+                                _stream_ptr(x.device)), "mxfp4_experts_linear")
+    return out
+
+
+def experts_combine(y, weights):
+    """out[t] = sum_i weights[t, i] * y[t * k + i] for y [T * k, N], weights [T, k] float32."""
+    import torch
+    dt = _check_rows(y, "y")
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 2:
+        raise ValueError("weights must be a tensor [T, k]")
+    T, k = weights.shape
+    N = y.shape[1]
+    _check_plain(y, "y", y.dtype, (T * k, N), y)
+    _check_plain(weights, "weights", torch.float32, (T, k), y)
+    out = torch.empty((T, N), dtype=y.dtype, device=y.device)
+    _raise(moe_combine(y.data_ptr(), dt, weights.data_ptr(), T, k, N, out.data_ptr(),
+                       _stream_ptr(y.device)), "moe_combine")
+    return out
+
+
+def experts_combine_backward(grad, y, weights):
+    """Gradients of experts_combine for grad [T, N]: (grad_y [T * k, N], grad_weights [T, k])."""
+    import torch
+    dt = _check_rows(y, "y")
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 2:
+        raise ValueError("weights must be a tensor [T, k]")
+    T, k = weights.shape
+    N = y.shape[1]
+    _check_plain(y, "y", y.dtype, (T * k, N), y)
+    _check_plain(grad, "grad", y.dtype, (T, N), y)
+    _check_plain(weights, "weights", torch.float32, (T, k), y)
+    grad_y = torch.empty((T * k, N), dtype=y.dtype, device=y.device)
+    grad_weights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    _raise(moe_combine_backward(grad.data_ptr(), y.data_ptr(), dt, weights.data_ptr(), T, k, N,
+                                grad_y.data_ptr(), grad_weights.data_ptr(),
+                                _stream_ptr(y.device)), "moe_combine_backward")
+    return grad_y, grad_weights

@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libimc.so")
-SOURCES = ["imc_api.cu", "k_simt.cu", "k_tc_gemm.cu", "k_tc_conv.cu", "noalloc.cu"]
+SOURCES = ["imc_api.cu", "k_simt.cu", "k_tc_gemm.cu", "k_tc_conv.cu", "noalloc.cu", "mx_api.cu",
+           "k_mx_quant.cu", "k_mx_gemm.cu", "k_experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

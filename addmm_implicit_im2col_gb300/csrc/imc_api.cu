@@ -701,14 +701,15 @@ uint64_t imc_launch_count(void) { return g_launches.load(std::memory_order_relax
 int imc_check_device_error(void* stream) {
   const int dev = check_device();
   if (dev != IMC_OK) return dev;
-  int vg = 0, vc = 0;
+  int vg = 0, vc = 0, vm = 0;
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess ||
-      gemm_take_watchdog(&vg) != cudaSuccess || conv_take_watchdog(&vc) != cudaSuccess)
+      gemm_take_watchdog(&vg) != cudaSuccess || conv_take_watchdog(&vc) != cudaSuccess ||
+      mx::product_take_watchdog(&vm) != cudaSuccess)
     return IMC_ERR_CUDA;
-  return (vg != 0 || vc != 0) ? IMC_ERR_TIMEOUT : IMC_OK;
+  return (vg != 0 || vc != 0 || vm != 0) ? IMC_ERR_TIMEOUT : IMC_OK;
 }
 
-int imc_version(void) { return 103; }
+int imc_version(void) { return 104; }
 
 int imc_selftest_wait_timeout(int limit_us, void* stream) {
   if (limit_us < 1000 || limit_us > 1000000) return IMC_ERR_ARG;
@@ -756,5 +757,14 @@ int gemm_with_scratch(const float* self, int self_2d, const float* mat1, const f
 }
 
 int require_device() { return check_device(); }
+int finish_call(cudaError_t e, int kernel) { return finish(e, kernel); }
+int finish_empty() {
+  set_none();
+  return IMC_OK;
+}
+bool ranges_overlap(const void* a, uint64_t abytes, const void* b, uint64_t bbytes) {
+  return overlaps(a, abytes, b, bbytes);
+}
+cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t s) { return pool_alloc(p, bytes, s); }
 
 }  // namespace imc

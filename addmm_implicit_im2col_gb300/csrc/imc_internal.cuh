@@ -103,6 +103,18 @@ int gemm_with_scratch(const float* self, int self_2d, const float* mat1, const f
                       int mode, void* scratch, size_t scratch_bytes, void* stream);
 int require_device();
 
+// Used by the 4-bit and expert entry points (mx_api.cu): the end of a call
+// (records the kernel for imc_last_kernel*), the end of one with nothing to
+// do, the overlap test of the argument checks, scratch from the library's
+// stream-ordered pool, and the watchdog word of the 4-bit product.
+int finish_call(cudaError_t e, int kernel);
+int finish_empty();
+bool ranges_overlap(const void* a, uint64_t abytes, const void* b, uint64_t bbytes);
+cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t s);
+namespace mx {
+cudaError_t product_take_watchdog(int* value);
+}
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 

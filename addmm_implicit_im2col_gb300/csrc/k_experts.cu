@@ -1,0 +1,549 @@
+// Routing of tokens to experts: scores and choice, their gradient, the order
+// of the chosen rows by expert, and the weighted sum of the experts' results
+// with its gradient.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "mx_internal.cuh"
+#include "ptx.cuh"
+
+namespace imc {
+namespace mx {
+namespace {
+
+namespace cg = cooperative_groups;
+constexpr uint32_t kAll = 0xffffffffu;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+// A float as an unsigned number in the same order; NaN below every number.
+// 0 stays free for "not to be chosen".
+__device__ __forceinline__ uint32_t ordered(float v) {
+  if (v != v) return 1u;
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 becomes 0
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  if (u <= 1u) return __uint_as_float(u ? 0x7FC00000u : 0xFF800000u);
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+
+// Scores of one token: lane l holds experts l, l + 32, ... (VPT of them).
+// softmax: exp(x - max) / sum; a row of -inf alone has scores 0.
+template <int VPT, typename T>
+__device__ __forceinline__ void scores(const T* row, int E, int sigmoid, float (&s)[VPT]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int e = lane + 32 * j;
+    s[j] = e < E ? to_f32<T>(row[e]) : -INFINITY;
+  }
+  if (sigmoid) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) s[j] = 1.0f / (1.0f + expf(-s[j]));
+  } else {
+    float m = s[0];
+#pragma unroll
+    for (int j = 1; j < VPT; ++j) m = fmaxf(m, s[j]);
+    m = warp_max(m);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      s[j] = m == -INFINITY && s[j] == m ? 0.0f : expf(s[j] - m);
+      sum += s[j];
+    }
+    sum = warp_sum(sum);
+    if (sum == 0.0f) sum = 1.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) s[j] = s[j] / sum;
+  }
+}
+
+template <int VPT>
+__device__ __forceinline__ float pick(const float (&s)[VPT], int j) {
+  float v = s[0];
+#pragma unroll
+  for (int i = 1; i < VPT; ++i)
+    if (i == j) v = s[i];
+  return v;
+}
+
+constexpr int kRouteWarps = 4;
+
+// One warp per token.
+template <int VPT, typename T>
+__global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
+  extern __shared__ uint32_t sm_keys[];  // groups > 1: [warp][E] keys
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+  if (t >= a.T) return;
+  float s[VPT];
+  scores<VPT, T>(static_cast<const T*>(a.logits) + t * a.ld, a.E, a.sigmoid, s);
+  uint32_t key[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int e = lane + 32 * j;
+    key[j] = e < a.E ? ordered(a.bias ? s[j] + __ldg(a.bias + e) : s[j]) : 0u;
+  }
+  if (a.groups > 1) {
+    // the sum of each group's two best; the best top_groups groups stay
+    uint32_t* keys = sm_keys + warp * a.E;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (lane + 32 * j < a.E) keys[lane + 32 * j] = key[j];
+    __syncwarp();
+    const int size = a.E / a.groups;
+    uint32_t gkey = 0;
+    if (lane < a.groups) {
+      uint32_t b1 = 0, b2 = 0;
+      for (int i = 0; i < size; ++i) {
+        const uint32_t k = keys[lane * size + i];
+        if (k > b1) {
+          b2 = b1;
+          b1 = k;
+        } else if (k > b2) {
+          b2 = k;
+        }
+      }
+      gkey = ordered(size > 1 ? from_ordered(b1) + from_ordered(b2) : from_ordered(b1));
+    }
+    uint32_t kept = 0;
+    for (int i = 0; i < a.top_groups; ++i) {
+      const uint32_t best = __reduce_max_sync(kAll, gkey);
+      const int g = __ffs(__ballot_sync(kAll, gkey == best)) - 1;
+      kept |= 1u << g;
+      if (lane == g) gkey = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int e = lane + 32 * j;
+      if (e < a.E && !((kept >> (e / size)) & 1u)) key[j] = 0;
+    }
+  }
+  float mine = 0.0f, total = 0.0f;
+  int id = 0;
+  for (int i = 0; i < a.k; ++i) {
+    uint32_t best = key[0];
+    int bj = 0;
+    float bs = s[0];
+#pragma unroll
+    for (int j = 1; j < VPT; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        bj = j;
+        bs = s[j];
+      }
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    const uint32_t e = __reduce_min_sync(kAll, best == top ? (uint32_t)(lane + 32 * bj) : 0x7FFFFFFFu);
+    const float w = __shfl_sync(kAll, bs, e & 31);
+    if (lane == (int)(e & 31)) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (j == bj) key[j] = 0;
+    }
+    total += w;
+    if (lane == i) {
+      mine = w;
+      id = (int)e;
+    }
+  }
+  if (lane < a.k) {
+    if (a.renorm) mine = total == 0.0f ? 0.0f : mine / total;
+    a.weights[t * a.k + lane] = mine * a.scale;
+    a.experts[t * a.k + lane] = id;
+  }
+}
+
+// Gradient of the weights with respect to the logits; the choice is constant.
+//   w_i = scale * s_i / S (S = sum over the chosen, or 1),
+//   ds_i = scale * (g_i - sum_j g_j s_j / S) / S,   or scale * g_i,
+//   softmax: dx_e = s_e * (ds_e - sum_i ds_i s_i),  sigmoid: dx_e = ds_e s_e (1 - s_e).
+template <int VPT, typename T>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+    k_route_backward(const RouteArgs a, const float* __restrict__ g, T* __restrict__ grad) {
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+  if (t >= a.T) return;
+  float s[VPT];
+  scores<VPT, T>(static_cast<const T*>(a.logits) + t * a.ld, a.E, a.sigmoid, s);
+  int id = -1;
+  float gi = 0.0f;
+  if (lane < a.k) {
+    id = a.experts[t * a.k + lane];
+    gi = g[t * a.k + lane];
+    if (id < 0 || id >= a.E) id = -1;
+  }
+  float total = 0.0f, dot = 0.0f, si = 0.0f;
+  for (int i = 0; i < a.k; ++i) {
+    const int e = __shfl_sync(kAll, id, i);
+    if (e < 0) continue;
+    const float p = __shfl_sync(kAll, pick<VPT>(s, e >> 5), e & 31);
+    total += p;
+    dot += p * __shfl_sync(kAll, gi, i);
+    if (lane == i) si = p;
+  }
+  float di = id >= 0 ? gi : 0.0f;
+  if (a.renorm) di = total == 0.0f || id < 0 ? 0.0f : (gi - dot / total) / total;
+  di *= a.scale;
+  const float inner = a.sigmoid ? 0.0f : warp_sum(di * si);
+  float d[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) d[j] = 0.0f;
+  for (int i = 0; i < a.k; ++i) {
+    const int e = __shfl_sync(kAll, id, i);
+    const float v = __shfl_sync(kAll, di, i);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (e == lane + 32 * j) d[j] += v;
+  }
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int e = lane + 32 * j;
+    if (e < a.E)
+      grad[t * a.E + e] = from_f32<T>(a.sigmoid ? d[j] * s[j] * (1.0f - s[j]) : s[j] * (d[j] - inner));
+  }
+}
+
+// ------------------------------------------------------------------ layout
+// Stable counting sort of n slots by expert, in one launch of one cluster of
+// CTAs.  Each warp owns a contiguous run of slots: it counts them per expert,
+// the counts are summed over warps (shared memory) and CTAs (distributed
+// shared memory), and the warp then places its slots in order.  Equal experts
+// within 32 slots are ranked with match_any, so nothing depends on the timing
+// of atomics.  Experts outside [0, E) fall into bucket E.
+constexpr int kLayoutThreads = 1024, kLayoutWarps = kLayoutThreads / 32;
+
+__global__ void __launch_bounds__(kLayoutThreads, 1)
+    k_layout(const int32_t* __restrict__ experts, const int n, const int E,
+             int32_t* __restrict__ offsets, int32_t* __restrict__ starts,
+             int32_t* __restrict__ order, int32_t* __restrict__ dest) {
+  extern __shared__ int32_t sm[];
+  const int B = E + 1;                    // buckets
+  int32_t* hist = sm;                     // [warps][B]: counts, then next positions
+  int32_t* total = sm + kLayoutWarps * B; // [B] this CTA's counts
+  int32_t* shift = total + B;             // [B] starts[e] - offsets[e]
+  __shared__ int32_t sums[2][kLayoutWarps];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kLayoutWarps * B; i += kLayoutThreads) hist[i] = 0;
+  __syncthreads();
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  // this warp's slots: a multiple of 32 of them
+  const int64_t per = ((int64_t)n + 32 * kLayoutWarps * ranks - 1) / (32 * kLayoutWarps * ranks) * 32;
+  const int64_t w0 = ((int64_t)rank * kLayoutWarps + warp) * per;
+  const int64_t w1 = w0 + per < n ? w0 + per : n;
+  int32_t* mine = hist + warp * B;
+  for (int64_t i = w0; i < w1; i += 32) {
+    int e = i + lane < w1 ? experts[i + lane] : -2;
+    if (e != -2 && (e < 0 || e >= E)) e = E;
+    if (i + lane >= w1) e = B;  // no slot
+    const uint32_t same = __match_any_sync(kAll, e);
+    if (e < B && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < B; e += kLayoutThreads) {  // exclusive over warps
+    int sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < kLayoutWarps; ++w) {
+      const int c = hist[w * B + e];
+      hist[w * B + e] = sum;
+      sum += c;
+    }
+    total[e] = sum;
+  }
+  cluster.sync();
+  // Thread e: bucket e's count over all CTAs, and before this CTA; then the
+  // exclusive sums over buckets of the counts and of the counts rounded up to
+  // 128 rows (B <= 1025: one bucket a thread, bucket 1024 on thread 0 of a
+  // second pass that needs only the sums so far).
+  int carry = 0, carry_pad = 0;
+  for (int e0 = 0; e0 < B; e0 += kLayoutThreads) {
+    const int e = e0 + threadIdx.x;
+    int all = 0, before = 0;
+    if (e < B)
+      for (int r = 0; r < ranks; ++r) {
+        const int c = cluster.map_shared_rank(total, r)[e];
+        if (r < rank) before += c;
+        all += c;
+      }
+    const int pad = (all + ATOM_ROWS - 1) / ATOM_ROWS * ATOM_ROWS;
+    int x = all, y = pad;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int ox = __shfl_up_sync(kAll, x, d), oy = __shfl_up_sync(kAll, y, d);
+      if (lane >= d) {
+        x += ox;
+        y += oy;
+      }
+    }
+    if (lane == 31) {
+      sums[0][warp] = x;
+      sums[1][warp] = y;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int u = sums[0][lane], v = sums[1][lane];
+      const int u0 = u, v0 = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int ou = __shfl_up_sync(kAll, u, d), ov = __shfl_up_sync(kAll, v, d);
+        if (lane >= d) {
+          u += ou;
+          v += ov;
+        }
+      }
+      sums[0][lane] = u - u0;
+      sums[1][lane] = v - v0;
+    }
+    __syncthreads();
+    if (e < B) {
+      const int off = carry + sums[0][warp] + x - all, start = carry_pad + sums[1][warp] + y - pad;
+      if (rank == 0) {
+        offsets[e] = off;
+        if (e < E + 1) starts[e] = start;
+        if (e == E) offsets[E + 1] = n;
+      }
+      shift[e] = start - off;
+      for (int w = 0; w < kLayoutWarps; ++w) hist[w * B + e] += off + before;
+    }
+    if (e0 + kLayoutThreads < B) {  // sums of this pass's buckets, for the next
+      __syncthreads();
+      if (threadIdx.x == kLayoutThreads - 1) {
+        sums[0][0] = sums[0][warp] + x;
+        sums[1][0] = sums[1][warp] + y;
+      }
+      __syncthreads();
+      carry += sums[0][0];
+      carry_pad += sums[1][0];
+    }
+    __syncthreads();
+  }
+  for (int64_t i = w0; i < w1; i += 32) {
+    const bool in = i + lane < w1;
+    int e = in ? experts[i + lane] : B;
+    if (in && (e < 0 || e >= E)) e = E;
+    const uint32_t same = __match_any_sync(kAll, e);
+    const int place = __popc(same & ((1u << lane) - 1u));
+    int pos = 0;
+    if (in) pos = mine[e] + place;
+    __syncwarp();
+    if (in) {
+      if (place == 0) mine[e] = pos + __popc(same);
+      order[pos] = (int32_t)(i + lane);
+      dest[i + lane] = e < E ? pos + shift[e] : -1;
+    }
+    __syncwarp();
+  }
+  cluster.sync();  // no CTA leaves while another may read its totals
+}
+
+// ------------------------------------------------------------ weighted sum
+// out[t] = sum_s w[t,s] * y[t*k + s], in the order of s, fp32; a thread has 8
+// columns of one token.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_combine(const T* __restrict__ y, const float* __restrict__ w, const int64_t T_, const int k,
+              const int64_t N, T* __restrict__ out, const bool vec) {
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int64_t per = ceil_div(N, 8), items = T_ * per;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < items;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t t = i / per, c = (i - t * per) * 8;
+    const int n = (int)(N - c < 8 ? N - c : 8);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const T* row = y + t * k * N + c;
+    int s = 0;
+    for (; s + 4 <= k; s += 4) {
+      float v[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) load8<T>(row + (s + u) * N, n, vec, v[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float ws = __ldg(w + t * k + s + u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = fmaf(ws, v[u][j], acc[j]);
+      }
+    }
+    for (; s < k; ++s) {
+      float v[8];
+      load8<T>(row + s * N, n, vec, v);
+      const float ws = __ldg(w + t * k + s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = fmaf(ws, v[j], acc[j]);
+    }
+    store8<T>(out + t * N + c, n, vec, acc);
+  }
+}
+
+// grad_y[t*k + s] = w[t,s] * grad[t], grad_w[t,s] = <grad[t], y[t*k + s]>: one
+// warp per slot (the warps of a token's slots share its gradient row in L1).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_combine_backward(const T* __restrict__ grad, const T* __restrict__ y,
+                       const float* __restrict__ w, const int64_t slots, const int k,
+                       const int64_t N, T* __restrict__ grad_y, float* __restrict__ grad_w,
+                       const bool vec) {
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; i < slots; i += warps) {
+    const float ws = w[i];
+    const T *g = grad + i / k * N, *yr = y + i * N;
+    float dot = 0.0f;
+#pragma unroll 2
+    for (int64_t c = lane * 8; c < N; c += 256) {
+      const int n = (int)(N - c < 8 ? N - c : 8);
+      float gv[8], yv[8];
+      load8<T>(g + c, n, vec, gv);
+      load8<T>(yr + c, n, vec, yv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dot = fmaf(gv[j], yv[j], dot);
+        gv[j] *= ws;
+      }
+      store8<T>(grad_y + i * N + c, n, vec, gv);
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) grad_w[i] = dot;
+  }
+}
+
+// ------------------------------------------------------------------- host
+template <typename T>
+cudaError_t route(const RouteArgs& a, const float* g, void* grad, cudaStream_t s) {
+  const dim3 grid((unsigned)ceil_div(a.T, kRouteWarps)), block(kRouteWarps * 32);
+  const size_t smem = !g && a.groups > 1 ? (size_t)kRouteWarps * a.E * 4 : 0;
+  cudaError_t e;
+#define IMC_ROUTE(V)                                                                            \
+  e = g ? launch_after_previous(k_route_backward<V, T>, grid, block, 0, s, a, g,                \
+                                static_cast<T*>(grad))                                          \
+        : launch_after_previous(k_route<V, T>, grid, block, smem, s, a)
+  if (a.E <= 32) IMC_ROUTE(1);
+  else if (a.E <= 64) IMC_ROUTE(2);
+  else if (a.E <= 128) IMC_ROUTE(4);
+  else if (a.E <= 256) IMC_ROUTE(8);
+  else if (a.E <= 512) IMC_ROUTE(16);
+  else IMC_ROUTE(32);
+#undef IMC_ROUTE
+  note_launch();
+  return e;
+}
+
+template <typename T>
+cudaError_t combine(const void* y, const float* w, int64_t tokens, int k, int64_t N, void* out,
+                    cudaStream_t s) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 &&
+                   (N * (int64_t)sizeof(T)) % 16 == 0;
+  const int64_t blocks = ceil_div(tokens * ceil_div(N, 8), 256), cap = (int64_t)device_sm_count() * 8;
+  const cudaError_t e = launch_after_previous(
+      k_combine<T>, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, s,
+      static_cast<const T*>(y), w, tokens, k, N, static_cast<T*>(out), vec);
+  note_launch();
+  return e;
+}
+
+template <typename T>
+cudaError_t combine_backward(const void* grad, const void* y, const float* w, int64_t tokens, int k,
+                             int64_t N, void* grad_y, float* grad_w, cudaStream_t s) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(grad) | reinterpret_cast<uintptr_t>(y) |
+                     reinterpret_cast<uintptr_t>(grad_y)) & 15u) == 0 &&
+                   (N * (int64_t)sizeof(T)) % 16 == 0;
+  const int64_t blocks = ceil_div(tokens * k, 8), cap = (int64_t)device_sm_count() * 8;
+  const cudaError_t e = launch_after_previous(
+      k_combine_backward<T>, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, s,
+      static_cast<const T*>(grad), static_cast<const T*>(y), w, tokens * k, k, N,
+      static_cast<T*>(grad_y), grad_w, vec);
+  note_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& a, int dtype, cudaStream_t s) {
+  note_kernel_name("k_route");
+  if (dtype == IMC_F32) return route<float>(a, nullptr, nullptr, s);
+  if (dtype == IMC_F16) return route<__half>(a, nullptr, nullptr, s);
+  return route<__nv_bfloat16>(a, nullptr, nullptr, s);
+}
+
+cudaError_t launch_route_backward(const RouteArgs& a, int dtype, const float* g, void* grad_logits,
+                                  cudaStream_t s) {
+  note_kernel_name("k_route_backward");
+  if (dtype == IMC_F32) return route<float>(a, g, grad_logits, s);
+  if (dtype == IMC_F16) return route<__half>(a, g, grad_logits, s);
+  return route<__nv_bfloat16>(a, g, grad_logits, s);
+}
+
+cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets, int32_t* starts,
+                          int32_t* order, int32_t* dest, cudaStream_t s) {
+  note_kernel_name("k_layout");
+  const int smem = (kLayoutWarps + 2) * (E + 1) * 4;
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(k_layout, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (kLayoutWarps + 2) * (1024 + 1) * 4);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  // one CTA places 1024 slots per step of its warps
+  const unsigned ranks = n <= 4096 ? 1 : (n <= 16384 ? 2 : (n <= 32768 ? 4 : 8));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ranks);
+  cfg.blockDim = dim3(kLayoutThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ranks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, k_layout, experts, n, E, offsets, starts, order, dest);
+  note_launch();
+  return e;
+}
+
+cudaError_t launch_combine(const void* y, const float* w, int dtype, int64_t T, int k, int64_t N,
+                           void* out, cudaStream_t s) {
+  note_kernel_name("k_combine");
+  if (dtype == IMC_F32) return combine<float>(y, w, T, k, N, out, s);
+  if (dtype == IMC_F16) return combine<__half>(y, w, T, k, N, out, s);
+  return combine<__nv_bfloat16>(y, w, T, k, N, out, s);
+}
+
+cudaError_t launch_combine_backward(const void* grad, const void* y, const float* w, int dtype,
+                                    int64_t T, int k, int64_t N, void* grad_y, float* grad_w,
+                                    cudaStream_t s) {
+  note_kernel_name("k_combine_backward");
+  if (dtype == IMC_F32) return combine_backward<float>(grad, y, w, T, k, N, grad_y, grad_w, s);
+  if (dtype == IMC_F16) return combine_backward<__half>(grad, y, w, T, k, N, grad_y, grad_w, s);
+  return combine_backward<__nv_bfloat16>(grad, y, w, T, k, N, grad_y, grad_w, s);
+}
+
+}  // namespace mx
+}  // namespace imc

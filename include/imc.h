@@ -1,11 +1,13 @@
 /*
  * imc.h -- C ABI of libimc: fp32 addmm and groups==1 NCHW conv2d, both run as
- * one tiled GEMM with a fused epilogue on NVIDIA sm_103a (GB300).
+ * one tiled GEMM with a fused epilogue on NVIDIA sm_103a (GB300); 4-bit
+ * (MXFP4) products; routing to experts and the experts' products.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - All tensor pointers are DEVICE pointers to contiguous row-major fp32
- *    data owned by the caller.  The library never frees or keeps a pointer to
+ *    data owned by the caller (the 4-bit and expert entry points also take
+ *    fp16 and bf16 data and row strides, as they say).  The library never frees or keeps a pointer to
  *    them beyond the call; it may cache CUDA function attributes per device.
  *  - Device memory: the tensor-core kernels need scratch -- addmm a copy of
  *    mat2 transposed and split into TF32 hi / lo parts, conv2d the weight
@@ -101,6 +103,14 @@ extern "C" {
 #define IMC_KERNEL_SIMT 3 /* fp32 FFMA SIMT kernel                         */
 #define IMC_KERNEL_FILL 4 /* epilogue only: K == 0 or alpha == 0           */
 #define IMC_KERNEL_DIRECT 5 /* direct conv2d kernel (IMC_MODE_DIRECT)      */
+#define IMC_KERNEL_MXFP4 6 /* 4-bit quantisation or product                */
+#define IMC_KERNEL_EXPERTS 7 /* routing, layout or weighted sum of experts */
+
+/* ---------------------------------------- element types of the 4-bit and expert operators */
+#define IMC_F32 0
+#define IMC_F16 1
+#define IMC_BF16 2
+#define IMC_MXFP4 3 /* an operand that quantize_mxfp4 has written */
 
 /*
  * gemm_addmm_f32 -- aten.addmm semantics.
@@ -345,6 +355,141 @@ int conv2d_gemm_f32_host(const float* x, const float* w, const float* bias, floa
                          int64_t B, int64_t IC, int64_t H, int64_t W, int64_t OC, int64_t KH,
                          int64_t KW, int64_t sH, int64_t sW, int64_t pH, int64_t pW, int64_t dH,
                          int64_t dW, int mode, void* stream);
+
+/*
+ * Microscaled 4-bit products (MXFP4).
+ *
+ * A matrix [rows, cols] in MXFP4 holds, for every 32 consecutive values of a
+ * row, one scale 2^e and 32 E2M1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign):
+ *
+ *   e = floor(log2(max |x|)) - 2, clamped to -127 .. 127 (a block of zeros: -127)
+ *   code = the E2M1 number nearest to x * 2^-e, halfway cases to the even code,
+ *          magnitudes above 6 to 6
+ *
+ * A block that holds an infinity or a NaN gets the scale NaN and stands for 32
+ * NaNs.  A row's last block is filled up with zeros.  Element types of the
+ * unquantised operands: IMC_F32, IMC_F16, IMC_BF16.
+ *
+ * Storage: one device buffer of mxfp4_bytes(batch, rows, cols), 16-byte
+ * aligned, for `batch` matrices: codes [batch][rows][16 * ceil(cols / 32)]
+ * bytes (two codes a byte, the even column in the low half), then from the next
+ * multiple of 512 bytes the scales, a byte 127 + e each (255: NaN), in atoms of
+ * 512 bytes for 128 rows x 4 blocks, [batch][ceil(rows / 128)][ceil(ceil(cols /
+ * 32) / 4)]; the byte of row r, block b of an atom is (r % 32) * 16 + (r / 32)
+ * * 4 + b.  mxfp4_bytes is 0 for sizes that are out of range.
+ */
+size_t mxfp4_bytes(int64_t batch, int64_t rows, int64_t cols);
+
+/* Quantises x [batch][rows][cols] (row_stride and batch_stride in elements,
+ * columns contiguous; row_stride >= cols) into q.  transpose == 0: q holds
+ * MXFP4 of x, blocks along the rows.  transpose == 1: q holds MXFP4 of x^T,
+ * that is [batch][cols][rows] with blocks down the columns of x -- the operand
+ * of a product that sums over the rows of x, as a weight's gradient does.
+ * q: mxfp4_bytes of the result, not overlapping x. */
+int mxfp4_quantize(const void* x, int dtype, int64_t batch, int64_t rows, int64_t cols,
+                   int64_t batch_stride, int64_t row_stride, int transpose, void* q,
+                   void* stream);
+
+/* out [batch][rows][cols] (contiguous, of type dtype) = the values q stands
+ * for, rounded to dtype once (exact in fp32 and bf16). */
+int mxfp4_dequantize(const void* q, int64_t batch, int64_t rows, int64_t cols, int dtype,
+                     void* out, void* stream);
+
+/* out[m,n] = sum_k x[m,k] * w[n,k] (+ bias[n]), both operands in MXFP4, the sum
+ * in fp32, rounded to out_dtype once.
+ *   x     [M,K]: x_dtype IMC_MXFP4 (a buffer of mxfp4_quantize; row_stride is
+ *         not read), or unquantised rows row_stride elements apart, quantised
+ *         within the call into its scratch.
+ *   w     [N,K] in MXFP4 (mxfp4_quantize with batch 1).   bias [N] fp32 or NULL.
+ *   out   [M,N] contiguous, of out_dtype; it may not overlap an input.
+ *   M, N >= 0, K >= 1.  flags: 0 or IMC_ACT_RELU.
+ *   workspace  mxfp4_linear_workspace_bytes(M, K, x_dtype) bytes, 16-byte
+ *         aligned (rules as gemm_addmm_f32_ws); NULL: from the library's pool.
+ * Non-finite values: a block with a NaN scale makes its row's (w: its
+ * column's) outputs NaN; IMC_ACT_RELU turns a NaN into 0, as in the fp32
+ * products' epilogue. */
+size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K, int x_dtype);
+int mxfp4_linear(const void* x, int x_dtype, int64_t row_stride, const void* w, const float* bias,
+                 void* out, int out_dtype, int64_t M, int64_t N, int64_t K, int flags,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of mxfp4_linear (without bias and ReLU), each itself a 4-bit
+ * product whose operands are quantised along the axis it sums over:
+ *   grad_x [M,K] = q(grad [M,N]) . q(w^T)^T,   grad_w [N,K] = q(grad^T) . q(x^T)^T.
+ * grad, x [M,K], w [N,K], grad_x and grad_w are contiguous and of type dtype.
+ * grad_x or grad_w may be NULL (not computed; then w, respectively x, may be).
+ * M, N, K >= 1.  workspace as above. */
+size_t mxfp4_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int mxfp4_linear_backward(const void* grad, const void* x, const void* w, int dtype,
+                          int64_t M, int64_t N, int64_t K, void* grad_x, void* grad_w,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Experts: routing of T tokens to k of E experts each (E <= 1024, k <= 32,
+ * T * k < 2^31 - 1), products with the chosen experts' weights, weighted sum.
+ * A "slot" is t * k + i, the i-th choice of token t.
+ */
+#define IMC_SCORE_SOFTMAX 0
+#define IMC_SCORE_SIGMOID 1
+
+/* Scores s = softmax(logits) or sigmoid(logits) in fp32; choice by c = s +
+ * bias (bias [E] or NULL).  With groups > 1 the E experts form that many runs
+ * of E / groups (groups <= 32, dividing E), a group's score is the sum of its
+ * two highest c, and only the experts of the top_groups best groups are
+ * candidates.  experts[t,i]: the i-th highest c; equal values go to the lowest
+ * index, NaN counts as lower than every number.
+ * weights[t,i] = scale * s[experts[t,i]], divided by the sum of the k chosen s
+ * when renormalize is 1 (0 where that sum is 0).  A softmax row of -inf alone
+ * has scores 0.
+ *   logits [T,E], rows row_stride elements apart; weights, experts [T,k]. */
+int moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t row_stride,
+              const float* bias, int64_t k, int score, int64_t groups, int64_t top_groups,
+              int renormalize, double scale, float* weights, int32_t* experts, void* stream);
+
+/* grad_logits [T,E] (contiguous, of type dtype): gradient of the weights [T,k]
+ * with respect to the logits, the choice and the bias taken as constant.
+ * Slots whose expert is outside [0, E) have no gradient. */
+int moe_route_backward(const float* grad_weights, const void* logits, int dtype, int64_t T,
+                       int64_t E, int64_t row_stride, const int32_t* experts, int64_t k, int score,
+                       int renormalize, double scale, void* grad_logits, void* stream);
+
+/* The slots in expert order.  layout (moe_layout_size(T, k, E) int32 values):
+ *   offsets [E+2]  expert e's slots are order[offsets[e]] .. order[offsets[e+1] - 1];
+ *                  slots whose expert is outside [0, E) (a caller's way to leave
+ *                  them out) come last, from offsets[E] on; offsets[E+1] = T*k
+ *   starts  [E+1]  row at which expert e's run starts when every run is filled up
+ *                  to a multiple of 128 rows
+ *   order   [T*k]  the slots, by expert, in slot order within one
+ *   dest    [T*k]  a slot's row among the filled-up runs, -1 without an expert */
+int64_t moe_layout_size(int64_t T, int64_t k, int64_t E);
+int moe_layout(const int32_t* experts, int64_t T, int64_t k, int64_t E, int32_t* layout,
+               void* stream);
+
+/* out[slot,n] = sum_c x[row(slot),c] * w[e,n,c] (+ bias[e,n]) (ReLU) for the
+ * slot's expert e, operands and rounding as mxfp4_linear; slots without an
+ * expert give 0.
+ *   x       x_rows rows of K, row_stride elements apart, of x_dtype (not
+ *           IMC_MXFP4): x_rows == T, row(slot) = its token, or x_rows == T*k,
+ *           row(slot) = slot.
+ *   w       [E][N,K] in MXFP4 (mxfp4_quantize with batch E); bias [E,N] or NULL.
+ *   layout  of moe_layout for the same T, k, E.     out [T*k,N] contiguous.
+ *   N >= 0, K >= 1; workspace as mxfp4_linear. */
+size_t mxfp4_experts_linear_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t K);
+int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row_stride,
+                         const void* w, const float* bias, const int32_t* layout, void* out,
+                         int out_dtype, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K,
+                         int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* out[t] = sum_i weights[t,i] * y[t*k + i], in the order of i, summed in fp32.
+ * y [T*k,N], out [T,N] contiguous, of type dtype. */
+int moe_combine(const void* y, int dtype, const float* weights, int64_t T, int64_t k, int64_t N,
+                void* out, void* stream);
+
+/* Its gradients: grad_y[t*k + i] = weights[t,i] * grad[t] (of type dtype),
+ * grad_weights[t,i] = sum_n grad[t,n] * y[t*k + i, n] (fp32). */
+int moe_combine_backward(const void* grad, const void* y, int dtype, const float* weights,
+                         int64_t T, int64_t k, int64_t N, void* grad_y, float* grad_weights,
+                         void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* imc_status_string(int status);
