@@ -10,6 +10,7 @@ and loading it raises otherwise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -516,52 +517,63 @@ def conv2d_host(x, w, bias=None, stride=1, padding=0, dilation=1, *, mode="defau
 
 
 # -------------------------------------- 4-bit products and experts (torch level)
+# These calls take a few microseconds on the GPU when a model decodes, so their
+# wrappers avoid what costs microseconds on the host: repeated imports, stream
+# objects, a library call for a size that was asked for before.
+_torch = None
 _DTYPE_IDS = {}
+_size = functools.lru_cache(maxsize=4096)(mxfp4_bytes)
+_layout_size = functools.lru_cache(maxsize=4096)(moe_layout_size)
+_experts_size = functools.lru_cache(maxsize=4096)(mxfp4_experts_linear_workspace_bytes)
+_backward_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_backward_workspace_bytes)
+
+
+def _setup():
+    """Imports torch and loads the library, once."""
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPE_IDS.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+        load()
+        _torch = torch
+    return _torch
 
 
 def _dtype_id(dtype, name):
-    if not _DTYPE_IDS:
-        import torch
-        _DTYPE_IDS.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
     try:
         return _DTYPE_IDS[dtype]
     except KeyError:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {dtype}") from None
 
 
-def _check_rows(t, name, ndim=2):
-    """A CUDA tensor of a float type with contiguous last dimension; its type's id."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+def _rows_of(t, name, ndim=2):
+    """Type id, shape and strides of a CUDA tensor of a float type with contiguous last dimension."""
+    if not isinstance(t, (_torch or _setup()).Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dim() != ndim:
+    shape = t.shape
+    if not t.is_cuda or len(shape) != ndim:
         raise ValueError(f"{name} must be a CUDA tensor of {ndim} dimensions")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    stride = t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return _dtype_id(t.dtype, name)
-
-
-def _row_stride(t):
-    """Elements between two rows; a single row's stride is its length."""
-    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+    return _dtype_id(t.dtype, name), shape, (stride if shape[-2] > 1 else stride[:-2] + (shape[-1], 1))
 
 
 def _check_plain(t, name, dtype, shape, like):
     """A contiguous CUDA tensor of this type and shape on the device of `like`."""
-    import torch
     if t is None:
         return
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.device != like.device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on {like.device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _raise(rc, what):
-    if rc != IMC_OK:
-        raise ImcError(rc, what)
+def _stream_of(t):
+    """The current stream's handle on t's device (what _stream_ptr returns, without its objects)."""
+    return _torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 class MxFp4:
@@ -592,29 +604,30 @@ def quantize_mxfp4(x, *, transpose=False):
     quantises x^T instead (blocks down the columns of x), without a transposed
     copy: the operand of a product that sums over the rows of x.
     """
-    import torch
-    dt = _check_rows(x, "x", 3 if getattr(x, "ndim", 2) == 3 else 2)
-    batched = x.dim() == 3
-    batch = x.shape[0] if batched else 1
-    rows, cols = x.shape[-2:]
-    size = mxfp4_bytes(batch, cols, rows) if transpose else mxfp4_bytes(batch, rows, cols)
-    q = torch.empty(size, dtype=torch.uint8, device=x.device)
-    _raise(mxfp4_quantize(x.data_ptr(), dt, batch, rows, cols, x.stride(0) if batched else 0,
-                          _row_stride(x), 1 if transpose else 0, q.data_ptr(),
-                          _stream_ptr(x.device)), "mxfp4_quantize")
-    return MxFp4(q, batch, cols, rows, batched) if transpose else MxFp4(q, batch, rows, cols, batched)
+    batched = getattr(x, "ndim", 2) == 3
+    dt, shape, stride = _rows_of(x, "x", 3 if batched else 2)
+    batch, step = (shape[0], stride[0]) if batched else (1, 0)
+    rows, cols = shape[-2:]
+    r, c = (cols, rows) if transpose else (rows, cols)
+    q = _torch.empty(_size(batch, r, c), dtype=_torch.uint8, device=x.device)
+    rc = _lib.mxfp4_quantize(x.data_ptr(), dt, batch, rows, cols, step, stride[-2],
+                             1 if transpose else 0, q.data_ptr(), _stream_of(x))
+    if rc:
+        raise ImcError(rc, "mxfp4_quantize")
+    return MxFp4(q, batch, r, c, batched)
 
 
 def dequantize_mxfp4(q, *, dtype=None):
     """The values an MxFp4 stands for, as a tensor of ``dtype`` (default float32)."""
-    import torch
     if not isinstance(q, MxFp4):
         raise TypeError("q must be an MxFp4")
-    dtype = torch.float32 if dtype is None else dtype
-    dt = _dtype_id(dtype, "dtype")
-    out = torch.empty(q.shape, dtype=dtype, device=q.device)
-    _raise(mxfp4_dequantize(q.data.data_ptr(), q.batch, q.rows, q.cols, dt, out.data_ptr(),
-                            _stream_ptr(q.device)), "mxfp4_dequantize")
+    dtype = _torch.float32 if dtype is None else dtype
+    dt, data = _dtype_id(dtype, "dtype"), q.data
+    out = _torch.empty(q.shape, dtype=dtype, device=data.device)
+    rc = _lib.mxfp4_dequantize(data.data_ptr(), q.batch, q.rows, q.cols, dt, out.data_ptr(),
+                               _stream_of(data))
+    if rc:
+        raise ImcError(rc, "mxfp4_dequantize")
     return out
 
 
@@ -626,37 +639,39 @@ def linear_mxfp4(x, w, bias=None, *, relu=False, out_dtype=None, out=None):
     bias [N] float32; ``relu`` fuses max(v, 0); out is [M, N] of ``out_dtype``
     (default: x's type, float32 for an MxFp4).
     """
-    import torch
-    if not isinstance(w, MxFp4):
-        _check_rows(w, "w")
-        w = quantize_mxfp4(w)
-    if w.batched:
-        raise ValueError("w must be [N, K]")
     if isinstance(x, MxFp4):
         if x.batched:
             raise ValueError("x must be [M, K]")
-        xp, dt, ld, M, K = x.data.data_ptr(), MXFP4, 0, x.rows, x.cols
-        default = torch.float32
+        like, dt, ld, M, K, default = x.data, MXFP4, 0, x.rows, x.cols, _torch.float32
     else:
-        dt = _check_rows(x, "x")
-        M, K = x.shape
-        xp, ld, default = x.data_ptr(), _row_stride(x), x.dtype
-    N = w.rows
-    if w.cols != K:
+        dt, (M, K), (ld, _) = _rows_of(x, "x")
+        like, default = x, x.dtype
+    if not isinstance(w, MxFp4):
+        _rows_of(w, "w")
+        w = quantize_mxfp4(w)
+    wd, N = w.data, w.rows
+    if w.batched or w.cols != K:
         raise ValueError(f"w must be [N, K] = [N, {K}], got {list(w.shape)}")
-    if w.device != x.device:
+    device = like.device
+    if wd.device != device:
         raise ValueError("x and w must be on one device")
-    _check_plain(bias, "bias", torch.float32, (N,), x)
-    out_dtype = (out.dtype if out is not None else default) if out_dtype is None else out_dtype
+    if bias is not None:
+        _check_plain(bias, "bias", _torch.float32, (N,), like)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        out_dtype = default if out_dtype is None else out_dtype
+        out = _torch.empty((M, N), dtype=out_dtype, device=device)
     else:
-        _check_plain(out, "out", out_dtype, (M, N), x)
-    nbytes = 0 if dt == MXFP4 else mxfp4_bytes(1, M, K)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
-    _raise(mxfp4_linear(xp, dt, ld, w.data.data_ptr(), _ptr(bias), out.data_ptr(),
-                        _dtype_id(out_dtype, "out_dtype"), M, N, K, ACT_RELU if relu else 0,
-                        _ptr(ws), nbytes, _stream_ptr(x.device)), "mxfp4_linear")
+        out_dtype = out.dtype if out_dtype is None else out_dtype
+        _check_plain(out, "out", out_dtype, (M, N), like)
+    nbytes, ws = 0, None
+    if dt != MXFP4:
+        nbytes = _size(1, M, K)
+        ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    rc = _lib.mxfp4_linear(like.data_ptr(), dt, ld, wd.data_ptr(), _ptr(bias), out.data_ptr(),
+                           _dtype_id(out_dtype, "out_dtype"), M, N, K, ACT_RELU if relu else 0,
+                           _ptr(ws), nbytes, _stream_of(like))
+    if rc:
+        raise ImcError(rc, "mxfp4_linear")
     return out
 
 
@@ -667,21 +682,21 @@ def linear_mxfp4_backward(grad, x, w):
     are quantised along the axis that it sums over.  All tensors are contiguous
     and of one float type.
     """
-    import torch
-    dt = _check_rows(grad, "grad")
-    M, N = grad.shape
-    _check_rows(x, "x")
-    K = x.shape[1]
-    _check_plain(grad, "grad", grad.dtype, (M, N), grad)
-    _check_plain(x, "x", grad.dtype, (M, K), grad)
-    _check_plain(w, "w", grad.dtype, (N, K), grad)
-    grad_x = torch.empty((M, K), dtype=grad.dtype, device=grad.device)
-    grad_w = torch.empty((N, K), dtype=grad.dtype, device=grad.device)
-    nbytes = mxfp4_linear_backward_workspace_bytes(M, N, K)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=grad.device)
-    _raise(mxfp4_linear_backward(grad.data_ptr(), x.data_ptr(), w.data_ptr(), dt, M, N, K,
-                                 grad_x.data_ptr(), grad_w.data_ptr(), ws.data_ptr(), nbytes,
-                                 _stream_ptr(grad.device)), "mxfp4_linear_backward")
+    dt, (M, N), _ = _rows_of(grad, "grad")
+    K = _rows_of(x, "x")[1][1]
+    dtype, device = grad.dtype, grad.device
+    _check_plain(grad, "grad", dtype, (M, N), grad)
+    _check_plain(x, "x", dtype, (M, K), grad)
+    _check_plain(w, "w", dtype, (N, K), grad)
+    grad_x = _torch.empty((M, K), dtype=dtype, device=device)
+    grad_w = _torch.empty((N, K), dtype=dtype, device=device)
+    nbytes = _backward_size(M, N, K)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    rc = _lib.mxfp4_linear_backward(grad.data_ptr(), x.data_ptr(), w.data_ptr(), dt, M, N, K,
+                                    grad_x.data_ptr(), grad_w.data_ptr(), ws.data_ptr(), nbytes,
+                                    _stream_of(grad))
+    if rc:
+        raise ImcError(rc, "mxfp4_linear_backward")
     return grad_x, grad_w
 
 
@@ -696,32 +711,33 @@ def route_experts(logits, k, bias=None, *, score="softmax", groups=1, top_groups
     weights are the chosen scores, divided by their sum (``renormalize``), times
     ``scale``.
     """
-    import torch
-    dt = _check_rows(logits, "logits")
-    T, E = logits.shape
-    _check_plain(bias, "bias", torch.float32, (E,), logits)
-    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    experts = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    _raise(moe_route(logits.data_ptr(), dt, T, E, _row_stride(logits), _ptr(bias), k, SCORES[score],
-                     groups, top_groups, 1 if renormalize else 0, float(scale), weights.data_ptr(),
-                     experts.data_ptr(), _stream_ptr(logits.device)), "moe_route")
+    dt, (T, E), (ld, _) = _rows_of(logits, "logits")
+    device = logits.device
+    if bias is not None:
+        _check_plain(bias, "bias", _torch.float32, (E,), logits)
+    weights = _torch.empty((T, k), dtype=_torch.float32, device=device)
+    experts = _torch.empty((T, k), dtype=_torch.int32, device=device)
+    rc = _lib.moe_route(logits.data_ptr(), dt, T, E, ld, _ptr(bias), k, SCORES[score], groups,
+                        top_groups, 1 if renormalize else 0, scale, weights.data_ptr(),
+                        experts.data_ptr(), _stream_of(logits))
+    if rc:
+        raise ImcError(rc, "moe_route")
     return weights, experts
 
 
 def route_experts_backward(grad_weights, logits, experts, *, score="softmax", renormalize=True,
                            scale=1.0):
     """Gradient of route_experts' weights with respect to the logits, [T, E] of their type."""
-    import torch
-    dt = _check_rows(logits, "logits")
-    T, E = logits.shape
+    dt, (T, E), (ld, _) = _rows_of(logits, "logits")
     k = experts.shape[-1]
-    _check_plain(experts, "experts", torch.int32, (T, k), logits)
-    _check_plain(grad_weights, "grad_weights", torch.float32, (T, k), logits)
-    grad = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _raise(moe_route_backward(grad_weights.data_ptr(), logits.data_ptr(), dt, T, E,
-                              _row_stride(logits), experts.data_ptr(), k, SCORES[score],
-                              1 if renormalize else 0, float(scale), grad.data_ptr(),
-                              _stream_ptr(logits.device)), "moe_route_backward")
+    _check_plain(experts, "experts", _torch.int32, (T, k), logits)
+    _check_plain(grad_weights, "grad_weights", _torch.float32, (T, k), logits)
+    grad = _torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    rc = _lib.moe_route_backward(grad_weights.data_ptr(), logits.data_ptr(), dt, T, E, ld,
+                                 experts.data_ptr(), k, SCORES[score], 1 if renormalize else 0,
+                                 scale, grad.data_ptr(), _stream_of(logits))
+    if rc:
+        raise ImcError(rc, "moe_route_backward")
     return grad
 
 
@@ -751,17 +767,16 @@ def experts_layout(experts, num_experts):
 
     An expert index outside [0, num_experts) leaves its slot out.
     """
-    import torch
-    if not isinstance(experts, torch.Tensor):
+    if not isinstance(experts, (_torch or _setup()).Tensor):
         raise TypeError("experts must be a torch.Tensor")
     if experts.dim() != 2:
         raise ValueError("experts must be [T, k]")
-    _check_plain(experts, "experts", torch.int32, experts.shape, experts)
     T, k = experts.shape
-    size = moe_layout_size(T, k, num_experts)
-    data = torch.empty(size, dtype=torch.int32, device=experts.device)
-    _raise(moe_layout(experts.data_ptr(), T, k, num_experts, data.data_ptr(),
-                      _stream_ptr(experts.device)), "moe_layout")
+    _check_plain(experts, "experts", _torch.int32, (T, k), experts)
+    data = _torch.empty(_layout_size(T, k, num_experts), dtype=_torch.int32, device=experts.device)
+    rc = _lib.moe_layout(experts.data_ptr(), T, k, num_experts, data.data_ptr(), _stream_of(experts))
+    if rc:
+        raise ImcError(rc, "moe_layout")
     return ExpertsLayout(data, T, k, num_experts)
 
 
@@ -773,64 +788,63 @@ def experts_linear_mxfp4(x, w, layout, bias=None, *, relu=False, out_dtype=None)
     experts_layout.  Returns [T * k, N] in slot order, of ``out_dtype`` (default:
     x's type); slots of no expert are 0.
     """
-    import torch
-    dt = _check_rows(x, "x")
+    dt, (rows, K), (ld, _) = _rows_of(x, "x")
     if not isinstance(w, MxFp4) or not w.batched:
         raise TypeError("w must be an MxFp4 [E, N, K]")
     if not isinstance(layout, ExpertsLayout):
         raise TypeError("layout must be an ExpertsLayout")
-    T, k, E = layout.T, layout.k, layout.E
-    rows, K = x.shape
+    T, k, E, N = layout.T, layout.k, layout.E, w.rows
     if w.batch != E or w.cols != K:
         raise ValueError(f"w must be [{E}, N, {K}], got {list(w.shape)}")
     if rows != T and rows != T * k:
         raise ValueError(f"x must have {T} or {T * k} rows, got {rows}")
-    if w.device != x.device or layout.data.device != x.device:
+    device, wd, ld_data = x.device, w.data, layout.data
+    if wd.device != device or ld_data.device != device:
         raise ValueError("x, w and layout must be on one device")
-    N = w.rows
-    _check_plain(bias, "bias", torch.float32, (E, N), x)
+    if bias is not None:
+        _check_plain(bias, "bias", _torch.float32, (E, N), x)
     out_dtype = x.dtype if out_dtype is None else out_dtype
-    out = torch.empty((T * k, N), dtype=out_dtype, device=x.device)
-    nbytes = mxfp4_experts_linear_workspace_bytes(T, k, E, K)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _raise(mxfp4_experts_linear(x.data_ptr(), dt, rows, _row_stride(x), w.data.data_ptr(),
-                                _ptr(bias), layout.data.data_ptr(), out.data_ptr(),
-                                _dtype_id(out_dtype, "out_dtype"), T, k, E, N, K,
-                                ACT_RELU if relu else 0, ws.data_ptr(), nbytes,
-                                _stream_ptr(x.device)), "mxfp4_experts_linear")
+    out = _torch.empty((T * k, N), dtype=out_dtype, device=device)
+    nbytes = _experts_size(T, k, E, K)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    rc = _lib.mxfp4_experts_linear(x.data_ptr(), dt, rows, ld, wd.data_ptr(), _ptr(bias),
+                                   ld_data.data_ptr(), out.data_ptr(),
+                                   _dtype_id(out_dtype, "out_dtype"), T, k, E, N, K,
+                                   ACT_RELU if relu else 0, ws.data_ptr(), nbytes, _stream_of(x))
+    if rc:
+        raise ImcError(rc, "mxfp4_experts_linear")
     return out
+
+
+def _combine_dims(y, weights):
+    dt, (rows, N), _ = _rows_of(y, "y")
+    if not isinstance(weights, _torch.Tensor) or weights.dim() != 2:
+        raise ValueError("weights must be a tensor [T, k]")
+    T, k = weights.shape
+    _check_plain(y, "y", y.dtype, (T * k, N), y)
+    _check_plain(weights, "weights", _torch.float32, (T, k), y)
+    return dt, T, k, N
 
 
 def experts_combine(y, weights):
     """out[t] = sum_i weights[t, i] * y[t * k + i] for y [T * k, N], weights [T, k] float32."""
-    import torch
-    dt = _check_rows(y, "y")
-    if not isinstance(weights, torch.Tensor) or weights.dim() != 2:
-        raise ValueError("weights must be a tensor [T, k]")
-    T, k = weights.shape
-    N = y.shape[1]
-    _check_plain(y, "y", y.dtype, (T * k, N), y)
-    _check_plain(weights, "weights", torch.float32, (T, k), y)
-    out = torch.empty((T, N), dtype=y.dtype, device=y.device)
-    _raise(moe_combine(y.data_ptr(), dt, weights.data_ptr(), T, k, N, out.data_ptr(),
-                       _stream_ptr(y.device)), "moe_combine")
+    dt, T, k, N = _combine_dims(y, weights)
+    out = _torch.empty((T, N), dtype=y.dtype, device=y.device)
+    rc = _lib.moe_combine(y.data_ptr(), dt, weights.data_ptr(), T, k, N, out.data_ptr(),
+                          _stream_of(y))
+    if rc:
+        raise ImcError(rc, "moe_combine")
     return out
 
 
 def experts_combine_backward(grad, y, weights):
     """Gradients of experts_combine for grad [T, N]: (grad_y [T * k, N], grad_weights [T, k])."""
-    import torch
-    dt = _check_rows(y, "y")
-    if not isinstance(weights, torch.Tensor) or weights.dim() != 2:
-        raise ValueError("weights must be a tensor [T, k]")
-    T, k = weights.shape
-    N = y.shape[1]
-    _check_plain(y, "y", y.dtype, (T * k, N), y)
+    dt, T, k, N = _combine_dims(y, weights)
     _check_plain(grad, "grad", y.dtype, (T, N), y)
-    _check_plain(weights, "weights", torch.float32, (T, k), y)
-    grad_y = torch.empty((T * k, N), dtype=y.dtype, device=y.device)
-    grad_weights = torch.empty((T, k), dtype=torch.float32, device=y.device)
-    _raise(moe_combine_backward(grad.data_ptr(), y.data_ptr(), dt, weights.data_ptr(), T, k, N,
-                                grad_y.data_ptr(), grad_weights.data_ptr(),
-                                _stream_ptr(y.device)), "moe_combine_backward")
+    grad_y = _torch.empty((T * k, N), dtype=y.dtype, device=y.device)
+    grad_weights = _torch.empty((T, k), dtype=_torch.float32, device=y.device)
+    rc = _lib.moe_combine_backward(grad.data_ptr(), y.data_ptr(), dt, weights.data_ptr(), T, k, N,
+                                   grad_y.data_ptr(), grad_weights.data_ptr(), _stream_of(y))
+    if rc:
+        raise ImcError(rc, "moe_combine_backward")
     return grad_y, grad_weights

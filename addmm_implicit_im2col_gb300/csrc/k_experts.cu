@@ -63,9 +63,9 @@ __device__ __forceinline__ void scores(const T* row, int E, int sigmoid, float (
       sum += s[j];
     }
     sum = warp_sum(sum);
-    if (sum == 0.0f) sum = 1.0f;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) s[j] = s[j] / sum;
+    for (int j = 0; j < VPT; ++j) s[j] *= inv;
   }
 }
 
@@ -79,11 +79,23 @@ __device__ __forceinline__ float pick(const float (&s)[VPT], int j) {
 }
 
 constexpr int kRouteWarps = 4;
+// Shared-memory place of expert e: a word skipped every 32, so that lanes that
+// read groups of 32 experts side by side meet different banks.
+__host__ __device__ constexpr int padded(int e) { return e + (e >> 5); }
 
-// One warp per token.
+// The two highest of two pairs (a1 >= a2, b1 >= b2).
+__device__ __forceinline__ void best_two(uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
+  a2 = max(min(a1, b1), max(a2, b2));
+  a1 = max(a1, b1);
+}
+
+// One warp per token.  Scores and keys stay in registers (VPT per lane) for the
+// k rounds of the choice: the highest key of each lane, the highest of the warp
+// (redux), and the lowest index that has it (redux).  The chosen scores are
+// picked up from shared memory at the end.
 template <int VPT, typename T>
 __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
-  extern __shared__ uint32_t sm_keys[];  // groups > 1: [warp][E] keys
+  extern __shared__ uint32_t sm_words[];  // [warp][padded E] keys, then scores
   ptx::griddep_wait();
   ptx::griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -97,71 +109,70 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     const int e = lane + 32 * j;
     key[j] = e < a.E ? ordered(a.bias ? s[j] + __ldg(a.bias + e) : s[j]) : 0u;
   }
+  uint32_t* words = sm_words + warp * padded(a.E);
   if (a.groups > 1) {
-    // the sum of each group's two best; the best top_groups groups stay
-    uint32_t* keys = sm_keys + warp * a.E;
+    // The sum of each group's two best; the best top_groups groups stay.
+    // 2^ls lanes share a group.
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
-      if (lane + 32 * j < a.E) keys[lane + 32 * j] = key[j];
+      if (lane + 32 * j < a.E) words[padded(lane + 32 * j)] = key[j];
     __syncwarp();
     const int size = a.E / a.groups;
-    uint32_t gkey = 0;
-    if (lane < a.groups) {
-      uint32_t b1 = 0, b2 = 0;
-      for (int i = 0; i < size; ++i) {
-        const uint32_t k = keys[lane * size + i];
-        if (k > b1) {
-          b2 = b1;
-          b1 = k;
-        } else if (k > b2) {
-          b2 = k;
-        }
-      }
-      gkey = ordered(size > 1 ? from_ordered(b1) + from_ordered(b2) : from_ordered(b1));
+    int ls = 0;
+    while ((a.groups << (ls + 1)) <= 32) ++ls;
+    const int g = lane >> ls;
+    uint32_t b1 = 0, b2 = 0;
+    if (g < a.groups)
+      for (int i = lane & ((1 << ls) - 1); i < size; i += 1 << ls)
+        best_two(b1, b2, words[padded(g * size + i)], 0u);
+    for (int d = 1; d < (1 << ls); d <<= 1) {
+      const uint32_t o1 = __shfl_xor_sync(kAll, b1, d), o2 = __shfl_xor_sync(kAll, b2, d);
+      best_two(b1, b2, o1, o2);
     }
+    uint32_t gkey = 0;
+    if (g < a.groups)
+      gkey = ordered(size > 1 ? from_ordered(b1) + from_ordered(b2) : from_ordered(b1));
     uint32_t kept = 0;
     for (int i = 0; i < a.top_groups; ++i) {
       const uint32_t best = __reduce_max_sync(kAll, gkey);
-      const int g = __ffs(__ballot_sync(kAll, gkey == best)) - 1;
-      kept |= 1u << g;
-      if (lane == g) gkey = 0;
+      const int at = (__ffs(__ballot_sync(kAll, gkey == best)) - 1) >> ls;
+      kept |= 1u << at;
+      if (g == at) gkey = 0;
     }
+    // e / size by a product: exact for e * (size - 1) < 2^20
+    const uint32_t inv = ((1u << 20) + size - 1) / size;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int e = lane + 32 * j;
-      if (e < a.E && !((kept >> (e / size)) & 1u)) key[j] = 0;
-    }
+    for (int j = 0; j < VPT; ++j)
+      if (!((kept >> (((lane + 32 * j) * inv) >> 20)) & 1u)) key[j] = 0;
+    __syncwarp();
   }
-  float mine = 0.0f, total = 0.0f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+    if (lane + 32 * j < a.E) words[padded(lane + 32 * j)] = __float_as_uint(s[j]);
+  __syncwarp();
   int id = 0;
   for (int i = 0; i < a.k; ++i) {
-    uint32_t best = key[0];
-    int bj = 0;
-    float bs = s[0];
+    uint32_t best = key[0], at = lane;
 #pragma unroll
     for (int j = 1; j < VPT; ++j)
       if (key[j] > best) {
         best = key[j];
-        bj = j;
-        bs = s[j];
+        at = lane + 32 * j;
       }
     const uint32_t top = __reduce_max_sync(kAll, best);
-    const uint32_t e = __reduce_min_sync(kAll, best == top ? (uint32_t)(lane + 32 * bj) : 0x7FFFFFFFu);
-    const float w = __shfl_sync(kAll, bs, e & 31);
-    if (lane == (int)(e & 31)) {
+    const uint32_t e = __reduce_min_sync(kAll, best == top ? at : 0x7FFFFFFFu);
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
-        if (j == bj) key[j] = 0;
-    }
-    total += w;
-    if (lane == i) {
-      mine = w;
-      id = (int)e;
-    }
+    for (int j = 0; j < VPT; ++j)
+      if (e == (uint32_t)(lane + 32 * j)) key[j] = 0;
+    if (lane == i) id = (int)e;
+  }
+  float w = lane < a.k ? __uint_as_float(words[padded(id)]) : 0.0f;
+  if (a.renorm) {
+    const float total = warp_sum(w);
+    w = total == 0.0f ? 0.0f : w / total;
   }
   if (lane < a.k) {
-    if (a.renorm) mine = total == 0.0f ? 0.0f : mine / total;
-    a.weights[t * a.k + lane] = mine * a.scale;
+    a.weights[t * a.k + lane] = w * a.scale;
     a.experts[t * a.k + lane] = id;
   }
 }
@@ -220,22 +231,26 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 
 // ------------------------------------------------------------------ layout
 // Stable counting sort of n slots by expert, in one launch of one cluster of
-// CTAs.  Each warp owns a contiguous run of slots: it counts them per expert,
-// the counts are summed over warps (shared memory) and CTAs (distributed
-// shared memory), and the warp then places its slots in order.  Equal experts
-// within 32 slots are ranked with match_any, so nothing depends on the timing
-// of atomics.  Experts outside [0, E) fall into bucket E.
+// CTAs.  Each warp owns a contiguous run of slots and walks it 32 at a time: a
+// slot's rank among the warp's slots of its expert is what the warp has counted
+// so far plus the equal experts on lower lanes (found with one ballot per bit of
+// the expert's number, so nothing depends on the timing of atomics).  The counts
+// are summed over warps (shared memory) and CTAs (distributed shared memory);
+// a slot's place is then the expert's first place + the slots of lower CTAs and
+// warps + its rank, which waits in `dest` meanwhile.  Experts outside [0, E)
+// fall into bucket E.
 constexpr int kLayoutThreads = 1024, kLayoutWarps = kLayoutThreads / 32;
 
 __global__ void __launch_bounds__(kLayoutThreads, 1)
     k_layout(const int32_t* __restrict__ experts, const int n, const int E,
              int32_t* __restrict__ offsets, int32_t* __restrict__ starts,
-             int32_t* __restrict__ order, int32_t* __restrict__ dest) {
+             int32_t* __restrict__ order, int32_t* dest) {
   extern __shared__ int32_t sm[];
   const int B = E + 1;                    // buckets
-  int32_t* hist = sm;                     // [warps][B]: counts, then next positions
+  int32_t* hist = sm;                     // [warps][B]: counts, then slots of lower warps
   int32_t* total = sm + kLayoutWarps * B; // [B] this CTA's counts
-  int32_t* shift = total + B;             // [B] starts[e] - offsets[e]
+  int32_t* first = total + B;             // [B] place of this CTA's first slot of a bucket
+  int32_t* shift = first + B;             // [B] starts[e] - offsets[e]
   __shared__ int32_t sums[2][kLayoutWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -249,13 +264,35 @@ __global__ void __launch_bounds__(kLayoutThreads, 1)
   const int64_t w0 = ((int64_t)rank * kLayoutWarps + warp) * per;
   const int64_t w1 = w0 + per < n ? w0 + per : n;
   int32_t* mine = hist + warp * B;
-  for (int64_t i = w0; i < w1; i += 32) {
-    int e = i + lane < w1 ? experts[i + lane] : -2;
-    if (e != -2 && (e < 0 || e >= E)) e = E;
-    if (i + lane >= w1) e = B;  // no slot
-    const uint32_t same = __match_any_sync(kAll, e);
-    if (e < B && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
+  const int bits = 32 - __clz(B);  // of bucket numbers 0 .. B (B: no slot)
+  constexpr int U = 8;             // steps whose loads are in flight together
+  auto bucket = [&](int64_t i) {
+    if (i >= w1) return B;
+    const int e = __ldg(experts + i);
+    return e < 0 || e >= E ? E : e;
+  };
+  for (int64_t i0 = w0; i0 < w1; i0 += 32 * U) {
+    int ids[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) ids[u] = bucket(i0 + 32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i0 + 32 * u >= w1) break;
+      const int e = ids[u];
+      uint32_t same = kAll;
+      for (int b = 0; b < bits; ++b) {
+        const uint32_t set = __ballot_sync(kAll, (e >> b) & 1);
+        same &= (e >> b) & 1 ? set : ~set;
+      }
+      const int place = __popc(same & ((1u << lane) - 1u));
+      const int before = e < B ? mine[e] : 0;
+      __syncwarp();
+      if (e < B) {
+        if (place == 0) mine[e] = before + __popc(same);
+        dest[i0 + 32 * u + lane] = before + place;
+      }
+      __syncwarp();
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < B; e += kLayoutThreads) {  // exclusive over warps
@@ -271,8 +308,7 @@ __global__ void __launch_bounds__(kLayoutThreads, 1)
   cluster.sync();
   // Thread e: bucket e's count over all CTAs, and before this CTA; then the
   // exclusive sums over buckets of the counts and of the counts rounded up to
-  // 128 rows (B <= 1025: one bucket a thread, bucket 1024 on thread 0 of a
-  // second pass that needs only the sums so far).
+  // 128 rows (B <= 1025 buckets: a second pass for the last one).
   int carry = 0, carry_pad = 0;
   for (int e0 = 0; e0 < B; e0 += kLayoutThreads) {
     const int e = e0 + threadIdx.x;
@@ -313,43 +349,46 @@ __global__ void __launch_bounds__(kLayoutThreads, 1)
       sums[1][lane] = v - v0;
     }
     __syncthreads();
+    const int upto = carry + sums[0][warp] + x, upto_pad = carry_pad + sums[1][warp] + y;
     if (e < B) {
-      const int off = carry + sums[0][warp] + x - all, start = carry_pad + sums[1][warp] + y - pad;
+      const int off = upto - all, start = upto_pad - pad;
       if (rank == 0) {
         offsets[e] = off;
-        if (e < E + 1) starts[e] = start;
+        starts[e] = start;
         if (e == E) offsets[E + 1] = n;
       }
       shift[e] = start - off;
-      for (int w = 0; w < kLayoutWarps; ++w) hist[w * B + e] += off + before;
+      first[e] = off + before;
     }
-    if (e0 + kLayoutThreads < B) {  // sums of this pass's buckets, for the next
+    if (e0 + kLayoutThreads < B) {  // the sums so far, for the next pass
       __syncthreads();
       if (threadIdx.x == kLayoutThreads - 1) {
-        sums[0][0] = sums[0][warp] + x;
-        sums[1][0] = sums[1][warp] + y;
+        sums[0][0] = upto;
+        sums[1][0] = upto_pad;
       }
       __syncthreads();
-      carry += sums[0][0];
-      carry_pad += sums[1][0];
+      carry = sums[0][0];
+      carry_pad = sums[1][0];
     }
     __syncthreads();
   }
-  for (int64_t i = w0; i < w1; i += 32) {
-    const bool in = i + lane < w1;
-    int e = in ? experts[i + lane] : B;
-    if (in && (e < 0 || e >= E)) e = E;
-    const uint32_t same = __match_any_sync(kAll, e);
-    const int place = __popc(same & ((1u << lane) - 1u));
-    int pos = 0;
-    if (in) pos = mine[e] + place;
-    __syncwarp();
-    if (in) {
-      if (place == 0) mine[e] = pos + __popc(same);
-      order[pos] = (int32_t)(i + lane);
-      dest[i + lane] = e < E ? pos + shift[e] : -1;
+  for (int64_t i0 = w0; i0 < w1; i0 += 32 * U) {
+    int ids[U], ranked[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + 32 * u + lane;
+      ids[u] = bucket(i);
+      ranked[u] = i < w1 ? dest[i] : 0;  // this thread's own write
     }
-    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + 32 * u + lane;
+      const int e = ids[u];
+      if (i >= w1) break;
+      const int pos = first[e] + mine[e] + ranked[u];
+      order[pos] = (int32_t)i;
+      dest[i] = e < E ? pos + shift[e] : -1;
+    }
   }
   cluster.sync();  // no CTA leaves while another may read its totals
 }
@@ -431,7 +470,7 @@ __global__ void __launch_bounds__(256)
 template <typename T>
 cudaError_t route(const RouteArgs& a, const float* g, void* grad, cudaStream_t s) {
   const dim3 grid((unsigned)ceil_div(a.T, kRouteWarps)), block(kRouteWarps * 32);
-  const size_t smem = !g && a.groups > 1 ? (size_t)kRouteWarps * a.E * 4 : 0;
+  const size_t smem = g ? 0 : (size_t)kRouteWarps * padded(a.E) * 4;
   cudaError_t e;
 #define IMC_ROUTE(V)                                                                            \
   e = g ? launch_after_previous(k_route_backward<V, T>, grid, block, 0, s, a, g,                \
@@ -496,19 +535,19 @@ cudaError_t launch_route_backward(const RouteArgs& a, int dtype, const float* g,
 cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets, int32_t* starts,
                           int32_t* order, int32_t* dest, cudaStream_t s) {
   note_kernel_name("k_layout");
-  const int smem = (kLayoutWarps + 2) * (E + 1) * 4;
+  const int smem = (kLayoutWarps + 3) * (E + 1) * 4;
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(k_layout, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (kLayoutWarps + 2) * (1024 + 1) * 4);
+                             (kLayoutWarps + 3) * (1024 + 1) * 4);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
-  // one CTA places 1024 slots per step of its warps
-  const unsigned ranks = n <= 4096 ? 1 : (n <= 16384 ? 2 : (n <= 32768 ? 4 : 8));
+  // a CTA's warps take 1024 slots per step
+  const unsigned ranks = n <= 2048 ? 1 : (n <= 4096 ? 2 : (n <= 8192 ? 4 : 8));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks);
   cfg.blockDim = dim3(kLayoutThreads);

@@ -10,17 +10,25 @@
 // 32 consecutive outputs, and the bias is one value per thread.
 //
 //   warp 0      TMA producer: per 256 values of K the weight tile (128 rows x
-//               128 bytes of codes), the token tile (BN rows x 128 bytes), both
-//               128-byte swizzled, and their scales (one contiguous copy per
-//               128 rows) into a ring of stages
-//   warp 1      TMEM owner + MMA issuer: copies the stage's scales to the
-//               stage's own TMEM columns (tcgen05.cp), then one MMA per 64
-//               values of K into an fp32 accumulator
-//   warps 2-5   epilogue: tcgen05.ld, bias, ReLU, rounding, store
+//               128 bytes of codes), the token tile, both 128-byte swizzled, and
+//               their scales into a ring of stages
+//   warp 1      TMEM owner + MMA issuer: copies the stage's scales to TMEM
+//               (tcgen05.cp), then one MMA per 64 values of K into an fp32
+//               accumulator
+//   warps 2-5   epilogue: tcgen05.ld, bias, ReLU, rounding, a staging row of 128
+//               outputs per token in shared memory, one bulk copy per token row
 //
-// One persistent CTA per SM walks the tiles.  In the experts' form a tile is
-// (expert, rows of that expert, 128 n); the row counts are only known on the
-// GPU, so every CTA sums them up at its start.
+// More than 128 tokens run as CTA pairs (cta_group::2): 256 rows of the weight x
+// 256 tokens per pair, each CTA loading its 128 rows and half of the tokens, so
+// that a CTA reads 32 KB per 256 values of K instead of 48 KB -- one CTA's
+// shared memory cannot feed 128 x 256 tiles of 4-bit MMAs (both operands
+// written once and read once: 192 bytes a cycle against 128).  The pair's two
+// accumulators of 256 columns overlap in 64 of them, which leaves room for the
+// scales: the epilogue drains the shared columns first and hands them back.
+//
+// Persistent CTAs walk the tiles.  In the experts' form a tile is (expert, rows
+// of that expert, n); the row counts are only known on the GPU, so every CTA
+// sums them up at its start.
 #include <atomic>
 #include <mutex>
 
@@ -43,57 +51,93 @@ __device__ int g_watchdog_mx;
 
 template <int BN>
 struct Form {
-  static constexpr int B_BYTES = BN * KB / 2;
+  static constexpr bool PAIR = BN > 128;
+  static constexpr int BNW = PAIR ? 2 * BM : BM;               // weight rows of a tile
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;            // token rows a CTA loads
+  static constexpr int B_BYTES = B_ROWS * KB / 2;
   static constexpr int B_ATOMS = BN > 128 ? BN / 128 : 1;      // row atoms of a token tile
   static constexpr int ATOM_TOKENS = BN < 128 ? BN : 128;      // token rows of a scale atom
   static constexpr int SA_BYTES = 2 * ATOM_BYTES, SB_BYTES = 2 * ATOM_BYTES * B_ATOMS;
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-  static constexpr int STAGES = BN > 128 ? 4 : (BN > 64 ? 6 : 8);
-  static constexpr int NACC = 2 * BN + STAGES * (8 + 8 * B_ATOMS) <= 512 ? 2 : 1;
-  static constexpr int SF_COL0 = NACC * BN;                    // scales after the accumulators
-  static constexpr int SF_COLS = 8 + 8 * B_ATOMS;              // TMEM columns of a stage's scales
-  static_assert(SF_COL0 + STAGES * SF_COLS <= 512, "TMEM");
+  static constexpr int STAGES = BN >= 128 ? 5 : (BN > 32 ? 6 : 8);
+  // TMEM columns: two accumulators (ACC1 apart), then the scales of SETS stages
+  static constexpr int SF_COLS = 8 + 8 * B_ATOMS;
+  static constexpr int SETS = PAIR ? 2 : STAGES;
+  static constexpr int SF_COL0 = 512 - SETS * SF_COLS;
+  static constexpr int ACC1 = PAIR ? 192 : BN;
+  static_assert(ACC1 + BN <= SF_COL0, "TMEM");
+  // chunks of 32 columns that hold what the two accumulators share
+  static constexpr int SHARED = PAIR ? (BN - ACC1 + 31) / 32 : 0;
+  static constexpr uint32_t TX = (PAIR ? 2 : 1) * STAGE;       // bytes a stage's barrier waits for
 };
+
+constexpr int ROW_BUF = 32 * BM * 4;  // staging of 32 tokens x 128 outputs
 
 struct Ctl {
   uint64_t full[8], empty[8], accf[2], acce[2], drain;
   uint32_t tmem_base;
   int abort;
-  int tiles_before[MAX_EXPERTS + 2];  // experts' form: tiles of the experts before e
+  // experts' form: tiles of the experts before e, first slot and first row of e
+  int tiles_before[MAX_EXPERTS + 2], offset[MAX_EXPERTS + 2], start[MAX_EXPERTS + 1];
 };
 
 template <int BN>
 constexpr int smem_bytes() {
-  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + (int)sizeof(Ctl);
+  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + 2 * ROW_BUF + (int)sizeof(Ctl);
 }
 static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448 &&
                   smem_bytes<64>() <= 232448 && smem_bytes<32>() <= 232448,
               "shared memory");
 
-// One tile: n rows n0.. of expert e's weight, token rows m0.. of x (`rows` of
-// them count).
+// One tile: n rows n0.. of expert e's weight (this CTA's 128), token rows m0..
+// of x (`rows` of them count).
 struct Tile {
   int e, n0, m0, rows;
   int first;  // experts' form: place of row m0 in `order`
 };
 
-template <typename T>
-__device__ __forceinline__ void put(void* out, int64_t at, float v) {
-  static_cast<T*>(out)[at] = from_f32<T>(v);
+// wait_bar at cluster scope for the barriers that both CTAs of a pair signal.
+template <bool PAIR>
+__device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         int site, int* watchdog) {
+  if (!PAIR) return wait_bar(bar, parity, abort, site, watchdog);
+  if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    if ((it & 127u) == 0) {
+      if (*abort) return false;
+      if (ptx::globaltimer_ns() - t0 > tc::kWaitLimitNs) {
+        *abort = 1;
+        atomicCAS(watchdog, 0, site);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 template <int BN, bool EXPERTS>
 __global__ void __launch_bounds__(192, 1)
     k_mx_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+              const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
               const ProductArgs p, const int num_m, const int num_n, const int group,
-              const int64_t x_scales_off, const int64_t w_scales_off) {
+              const int row_copies) {
   using F = Form<BN>;
+  constexpr bool PAIR = F::PAIR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::STAGES * F::STAGE);
+  uint8_t* rows_buf = smem + F::STAGES * F::STAGE;
+  Ctl* ctl = reinterpret_cast<Ctl*>(rows_buf + 2 * ROW_BUF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
+  const int unit = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+  const int units = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
   const int num_kb = (int)((p.K + KB - 1) / KB);
-  const int block_atoms = (int)((p.K + 127) / 128), w_row_atoms = (int)((p.N + 127) / 128);
   int* wd = &g_watchdog_mx;
 
   if (threadIdx.x == 0) {
@@ -103,7 +147,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ctl->accf[b], 1);
-      ptx::mbar_init(&ctl->acce[b], 128);
+      ptx::mbar_init(&ctl->acce[b], PAIR ? 8 : 4);
     }
     ptx::mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
@@ -112,11 +156,10 @@ __global__ void __launch_bounds__(192, 1)
   if (warp == 0 && lane == 0) {
     ptx::tma_prefetch_desc(&tmW);
     ptx::tma_prefetch_desc(&tmX);
+    ptx::tma_prefetch_desc(&tmWs);
+    ptx::tma_prefetch_desc(&tmXs);
   }
-  if (warp == 1) {
-    ptx::tmem_alloc(&ctl->tmem_base, 512);
-    ptx::tmem_relinquish();
-  }
+  if (warp == 1) ptx::tmem_alloc_g<PAIR>(&ctl->tmem_base, 512);
   if (EXPERTS) {
     ptx::griddep_wait();
     // tiles of each expert (the slots of no expert count as expert E)
@@ -125,7 +168,12 @@ __global__ void __launch_bounds__(192, 1)
       for (int e0 = 0; e0 <= p.E; e0 += 32) {
         const int e = e0 + lane;
         int n = 0;
-        if (e <= p.E) n = (p.offsets[e + 1] - p.offsets[e] + BN - 1) / BN * num_n;
+        if (e <= p.E) {
+          const int off = p.offsets[e];
+          ctl->offset[e] = off;
+          ctl->start[e] = p.starts[e];
+          n = (p.offsets[e + 1] - off + BN - 1) / BN * num_n;
+        }
         int sum = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -135,11 +183,15 @@ __global__ void __launch_bounds__(192, 1)
         if (e <= p.E) ctl->tiles_before[e] = before + sum - n;
         before += __shfl_sync(0xffffffffu, sum, 31);
       }
-      if (lane == 0) ctl->tiles_before[p.E + 1] = before;
+      if (lane == 0) {
+        ctl->tiles_before[p.E + 1] = before;
+        ctl->offset[p.E + 1] = p.slots;
+      }
     }
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (PAIR) ptx::cluster_sync();  // the peer's barriers are ready
   ptx::tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   volatile int* abort = &ctl->abort;
@@ -151,7 +203,7 @@ __global__ void __launch_bounds__(192, 1)
       int mt, nt;
       tc::tile_coords(t, num_m, num_n, group, mt, nt);
       r.e = 0;
-      r.n0 = nt * BM;
+      r.n0 = nt * F::BNW + rank * BM;
       r.m0 = mt * BN;
       r.rows = (int)(p.M - r.m0 < BN ? p.M - r.m0 : BN);
       r.first = 0;
@@ -162,14 +214,14 @@ __global__ void __launch_bounds__(192, 1)
         if (ctl->tiles_before[mid] <= t) lo = mid;
         else hi = mid - 1;
       }
-      const int count = p.offsets[lo + 1] - p.offsets[lo];
+      const int count = ctl->offset[lo + 1] - ctl->offset[lo];
       const int mts = (count + BN - 1) / BN, in = t - ctl->tiles_before[lo];
       const int mt = in % mts;  // the expert's token tiles share a weight tile
       r.e = lo;
-      r.n0 = in / mts * BM;
-      r.m0 = lo < p.E ? p.starts[lo] + mt * BN : 0;
+      r.n0 = in / mts * F::BNW + rank * BM;
+      r.m0 = lo < p.E ? ctl->start[lo] + mt * BN : 0;
       r.rows = count - mt * BN < BN ? count - mt * BN : BN;
-      r.first = p.offsets[lo] + mt * BN;
+      r.first = ctl->offset[lo] + mt * BN;
     }
     return r;
   };
@@ -182,32 +234,31 @@ __global__ void __launch_bounds__(192, 1)
       bool tokens_ready = EXPERTS || !p.inputs_ready;
       int s = 0, issued = 0;
       uint32_t ph = 0;
-      for (int t = blockIdx.x; t < num_tiles && !*abort; t += gridDim.x) {
+      for (int t = unit; t < num_tiles && !*abort; t += units) {
         const Tile r = tile_of(t);
         if (EXPERTS && r.e == p.E) break;  // only tiles of no expert follow
-        const uint8_t* wsf = p.w + w_scales_off +
-                             ((int64_t)r.e * w_row_atoms + r.n0 / 128) * block_atoms * ATOM_BYTES;
-        const uint8_t* xsf =
-            p.x + x_scales_off + (int64_t)(r.m0 / F::ATOM_TOKENS) * block_atoms * ATOM_BYTES;
-        const int b_atoms = F::B_ATOMS > 1 && r.rows > 128 ? F::B_ATOMS : 1;
         for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_bar(&ctl->empty[s], ph ^ 1u, abort, tc::kSiteProducerEmpty, wd)) break;
+          if (!wait_any<PAIR>(&ctl->empty[s], ph ^ 1u, abort, tc::kSiteProducerEmpty, wd)) break;
           uint8_t* st = smem + s * F::STAGE;
-          const uint32_t sf = (uint32_t)min(2, block_atoms - 2 * kb) * ATOM_BYTES;
-          ptx::mbar_arrive_expect_tx(&ctl->full[s],
-                                     (uint32_t)(A_BYTES + F::B_BYTES) + sf * (1 + b_atoms));
-          ptx::tma_load_3d(st, &tmW, &ctl->full[s], kb * (KB / 2), r.n0, r.e);
-          ptx::bulk_load(st + A_BYTES + F::B_BYTES, wsf + (int64_t)kb * 2 * ATOM_BYTES, sf,
-                         &ctl->full[s]);
-          if (!tokens_ready) {
-            ptx::griddep_wait();
-            tokens_ready = true;
+          uint8_t* sf = st + A_BYTES + F::B_BYTES;
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&ctl->full[s], F::TX);
+          const int xa = r.m0 / F::ATOM_TOKENS;
+          if (PAIR) {
+            const uint32_t bar = ptx::cluster_addr(&ctl->full[s], 0);
+            ptx::tma_load_3d_pair(st, &tmW, bar, kb * (KB / 2), r.n0, r.e);
+            ptx::tma_load_3d_pair(sf, &tmWs, bar, kb * KB, r.n0 / BM, r.e);
+            if (!tokens_ready) ptx::griddep_wait();
+            ptx::tma_load_2d_pair(st + A_BYTES, &tmX, bar, kb * (KB / 2),
+                                  r.m0 + rank * F::B_ROWS);
+            ptx::tma_load_2d_pair(sf + F::SA_BYTES, &tmXs, bar, kb * KB, xa);
+          } else {
+            ptx::tma_load_3d(st, &tmW, &ctl->full[s], kb * (KB / 2), r.n0, r.e);
+            ptx::tma_load_3d(sf, &tmWs, &ctl->full[s], kb * KB, r.n0 / BM, r.e);
+            if (!tokens_ready) ptx::griddep_wait();
+            ptx::tma_load_2d(st + A_BYTES, &tmX, &ctl->full[s], kb * (KB / 2), r.m0);
+            ptx::tma_load_2d(sf + F::SA_BYTES, &tmXs, &ctl->full[s], kb * KB, xa);
           }
-          ptx::tma_load_2d(st + A_BYTES, &tmX, &ctl->full[s], kb * (KB / 2), r.m0);
-          for (int a = 0; a < b_atoms; ++a)
-            ptx::bulk_load(st + A_BYTES + F::B_BYTES + F::SA_BYTES + a * 2 * ATOM_BYTES,
-                           xsf + ((int64_t)a * block_atoms + kb * 2) * ATOM_BYTES, sf,
-                           &ctl->full[s]);
+          tokens_ready = true;
           ++issued;
           if (++s == F::STAGES) {
             s = 0;
@@ -215,127 +266,196 @@ __global__ void __launch_bounds__(192, 1)
           }
         }
       }
-      // Every copy issued must have landed before the CTA's shared memory is released.
-      for (int j = (issued > F::STAGES ? issued - F::STAGES : 0); j < issued; ++j)
-        tc::drain_wait(&ctl->full[j % F::STAGES], (uint32_t)((j / F::STAGES) & 1));
+      // Every copy issued must have landed before the CTA's shared memory is
+      // released (a pair's copies count on CTA 0's barriers, and both CTAs meet
+      // at the end), and so must every signal the MMAs send to a pair's barriers.
+      for (int j = (issued > F::STAGES ? issued - F::STAGES : 0); j < issued; ++j) {
+        const uint32_t parity = (uint32_t)((j / F::STAGES) & 1);
+        if (rank == 0) tc::drain_wait(&ctl->full[j % F::STAGES], parity);
+        if (PAIR) tc::drain_wait(&ctl->empty[j % F::STAGES], parity);
+      }
     }
+    __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id0 = ptx::idesc_mxf4(BM, BN, 0), id1 = ptx::idesc_mxf4(BM, BN, 2);
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t id0 = ptx::idesc_mxf4(F::BNW, BN, 0), id1 = ptx::idesc_mxf4(F::BNW, BN, 2);
       const int num_ks = (int)((p.K + KSTEP - 1) / KSTEP);
-      int s = 0, tl = 0;
+      int s = 0, tl = 0, block = 0;
       uint32_t ph = 0;
-      for (int t = blockIdx.x; t < num_tiles; t += gridDim.x, ++tl) {
+      for (int t = unit; t < num_tiles; t += units, ++tl) {
         if (EXPERTS && tile_of(t).e == p.E) break;
-        const int buf = tl % F::NACC;
-        const uint32_t use = (uint32_t)(tl / F::NACC);
-        if (!wait_bar(&ctl->acce[buf], (use & 1u) ^ 1u, abort, tc::kSiteMmaAccEmpty, wd)) break;
+        const int buf = tl & 1;
+        // the accumulator is free: the tile two before (a pair: the part shared
+        // with the tile before) has been read
+        const bool free_ =
+            PAIR ? tl == 0 || wait_any<true>(&ctl->acce[0], (uint32_t)(tl - 1) & 1u, abort,
+                                             tc::kSiteMmaAccEmpty, wd)
+                 : wait_any<false>(&ctl->acce[buf], ((uint32_t)(tl >> 1) & 1u) ^ 1u, abort,
+                                   tc::kSiteMmaAccEmpty, wd);
+        if (!free_) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * BN);
+        const uint32_t d = tmem + (uint32_t)(buf * F::ACC1);
         bool ok = true;
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_bar(&ctl->full[s], ph, abort, tc::kSiteMmaOperands, wd)) {
-            ok = false;
-            break;
+        for (int kb = 0; kb < num_kb; ++kb, ++block) {
+          ok = wait_any<PAIR>(&ctl->full[s], ph, abort, tc::kSiteMmaOperands, wd);
+          // the scale columns are free: the MMAs of the block that had them are done
+          if (F::SETS < F::STAGES && ok && block >= F::SETS) {
+            const int b = block - F::SETS;
+            ok = wait_any<PAIR>(&ctl->empty[b % F::STAGES], (uint32_t)(b / F::STAGES) & 1u, abort,
+                                tc::kSiteMmaOperands, wd);
           }
+          if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t base = ptx::smem_addr(smem + s * F::STAGE);
           const uint64_t da = ptx::smem_desc(base, 16, 1024, ptx::kSwizzle128B);
           const uint64_t db = ptx::smem_desc(base + A_BYTES, 16, 1024, ptx::kSwizzle128B);
           const uint64_t ds = ptx::smem_desc(base + A_BYTES + F::B_BYTES, 16, 128, 0);
-          const uint32_t sfa = tmem + (uint32_t)(F::SF_COL0 + s * F::SF_COLS), sfb = sfa + 8;
+          const uint32_t sfa = tmem + (uint32_t)(F::SF_COL0 + block % F::SETS * F::SF_COLS),
+                         sfb = sfa + 8;
 #pragma unroll
           for (int a = 0; a < 2; ++a) {  // block atoms of the stage
-            ptx::tmem_cp_scales(sfa + a * 4, ds + (uint64_t)(a * ATOM_BYTES >> 4));
+            ptx::tmem_cp_scales<PAIR>(sfa + a * 4, ds + (uint64_t)(a * ATOM_BYTES >> 4));
 #pragma unroll
             for (int b = 0; b < F::B_ATOMS; ++b)
-              ptx::tmem_cp_scales(sfb + a * 4 * F::B_ATOMS + b * 4,
-                                  ds + (uint64_t)((F::SA_BYTES + (2 * b + a) * ATOM_BYTES) >> 4));
+              ptx::tmem_cp_scales<PAIR>(
+                  sfb + a * 4 * F::B_ATOMS + b * 4,
+                  ds + (uint64_t)((F::SA_BYTES + (2 * b + a) * ATOM_BYTES) >> 4));
           }
           const int steps = min(4, num_ks - 4 * kb);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j < steps)
-              ptx::mma_mxf4(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0, sfa + (j >> 1) * 4,
-                            sfb + (j >> 1) * 4 * F::B_ATOMS, kb + j > 0 ? 1u : 0u);
+              ptx::mma_mxf4<PAIR>(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0,
+                                  sfa + (j >> 1) * 4, sfb + (j >> 1) * 4 * F::B_ATOMS,
+                                  kb + j > 0 ? 1u : 0u);
           }
-          ptx::mma_commit(&ctl->empty[s]);
+          ptx::mma_commit_g<PAIR>(&ctl->empty[s]);
           if (++s == F::STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
         if (!ok) break;
-        ptx::mma_commit(&ctl->accf[buf]);
+        ptx::mma_commit_g<PAIR>(&ctl->accf[buf]);
       }
       // Every MMA issued must be done before TMEM is released.
-      ptx::mma_commit(&ctl->drain);
-      tc::drain_wait(&ctl->drain, 0);
+      ptx::mma_commit_g<PAIR>(&ctl->drain);
     }
+    if (lane == 0) tc::drain_wait(&ctl->drain, 0);
     __syncwarp();
   } else {
     // ----------------------------------------------------------- epilogue
     ptx::griddep_wait();  // bias, and the order of output writes
     const int q = warp & 3;  // TMEM lane quadrant this warp may read
-    int tl = 0;
-    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+    const int esize = p.out_dtype == IMC_F32 ? 4 : 2;
+    const uint32_t acce0 = PAIR ? ptx::cluster_addr(&ctl->acce[0], 0) : 0u;
+    int tl = 0, chunk = 0;  // chunks so far: the staging buffers alternate
+    for (int t = unit; t < num_tiles; t += units) {
       const Tile r = tile_of(t);
       const bool none = EXPERTS && r.e == p.E;  // slots of no expert: zeros
-      const int buf = tl % F::NACC;
+      const int buf = tl & 1;
       const int64_t n = r.n0 + q * 32 + lane;
-      const bool in = n < p.N;
-      const float bias = p.bias && in && !none ? p.bias[(int64_t)r.e * p.N + n] : 0.0f;
+      const int width = (int)(p.N - r.n0 < BM ? p.N - r.n0 : BM);  // outputs of a row; <= 0: none
+      const float bias = p.bias && n < p.N && !none ? __ldg(p.bias + (int64_t)r.e * p.N + n) : 0.0f;
       if (!none) {
-        const bool ok = tc::warp_wait_bar(&ctl->accf[buf], (uint32_t)(tl / F::NACC) & 1u, abort,
-                                          tc::kSiteEpilogueAccFull, wd);
+        int ok = 1;
+        if (lane == 0)
+          ok = wait_any<PAIR>(&ctl->accf[buf], (uint32_t)(tl >> 1) & 1u, abort,
+                              tc::kSiteEpilogueAccFull, wd)
+                   ? 1
+                   : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (tc::epi_any(!ok)) break;
         ptx::tc_fence_after();
         ++tl;
       }
-      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * F::ACC1);
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
+      for (int i = 0; i < BN / 32; ++i) {
+        // accumulator 0 shares its last columns with 1, which shares its first
+        const int c = 32 * (PAIR && buf == 0 ? (i + BN / 32 - F::SHARED) % (BN / 32) : i);
+        const int live = min(32, r.rows - c);  // the same for all four warps
         uint32_t v[32];
-        if (!none) {
+        int64_t row = 0;  // the row that lanes 0-7 will store
+        if (live > 0 && lane < 8 && q * 8 + lane < live)
+          row = EXPERTS ? (int64_t)__ldg(p.order + r.first + c + q * 8 + lane)
+                        : (int64_t)r.m0 + c + q * 8 + lane;
+        if (live > 0 && !none) {
           ptx::tmem_ld32(tbase + (uint32_t)c, v);
           ptx::tmem_ld_wait();
-          if (c + 32 == BN) {  // the accumulator is read: the MMA may have it back
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(&ctl->acce[buf]);
-          }
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0u;
         }
-        const int live = min(32, r.rows - c);  // warp-uniform
-        if (live <= 0) continue;
-        int slot = 0;
-        if (EXPERTS) slot = lane < live ? p.order[r.first + c + lane] : 0;
+        if (!none && i == (PAIR ? F::SHARED : BN / 32) - 1) {  // the MMA may have it back
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR) ptx::mbar_arrive_cluster(acce0);
+            else ptx::mbar_arrive(&ctl->acce[buf]);
+          }
+        }
+        if (live <= 0 || width <= 0) continue;
+        uint8_t* stage = rows_buf + (chunk & 1) * ROW_BUF;
+        ++chunk;
+        if (!none) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j < live) {
-            const int64_t row = EXPERTS ? (int64_t)__shfl_sync(0xffffffffu, slot, j)
-                                        : (int64_t)r.m0 + c + j;
-            float y = none ? 0.0f : __uint_as_float(v[j]) + bias;
+          for (int j = 0; j < 32; ++j) {
+            float y = __uint_as_float(v[j]) + bias;
             if (p.relu) y = fmaxf(y, 0.0f);
-            if (in) {
-              const int64_t at = row * p.N + n;
-              if (p.out_dtype == IMC_F32) put<float>(p.out, at, y);
-              else if (p.out_dtype == IMC_F16) put<__half>(p.out, at, y);
-              else put<__nv_bfloat16>(p.out, at, y);
+            v[j] = __float_as_uint(y);
+          }
+        }
+        if (esize == 4) {
+          uint32_t* d = reinterpret_cast<uint32_t*>(stage) + q * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) d[j * BM] = v[j];
+        } else {
+          uint16_t* d = reinterpret_cast<uint16_t*>(stage) + q * 32 + lane;
+          if (p.out_dtype == IMC_BF16) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) d[j * BM] = (uint16_t)bf16_bits(__uint_as_float(v[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) d[j * BM] = (uint16_t)half_bits(__uint_as_float(v[j]));
+          }
+        }
+        // The buffer's rows are copied out by the eight lanes that also wait, one
+        // chunk later and before the barrier, until the copies have read them.
+        if (lane < 8) ptx::bulk_wait_read0();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        tc::epi_sync();
+        if (row_copies) {
+          if (lane < 8 && q * 8 + lane < live)
+            ptx::bulk_store(static_cast<uint8_t*>(p.out) + (row * p.N + r.n0) * esize,
+                            stage + (q * 8 + lane) * BM * esize, (uint32_t)(width * esize));
+          if (lane < 8) ptx::bulk_commit();
+        } else {  // rows that are no multiples of 16 bytes
+          for (int j = 0; j < 8 && q * 8 + j < live; ++j) {
+            const int64_t at = __shfl_sync(0xffffffffu, row, j) * p.N + r.n0;
+            for (int x = lane; x < width; x += 32) {
+              if (esize == 4)
+                static_cast<uint32_t*>(p.out)[at + x] =
+                    reinterpret_cast<const uint32_t*>(stage)[(q * 8 + j) * BM + x];
+              else
+                static_cast<uint16_t*>(p.out)[at + x] =
+                    reinterpret_cast<const uint16_t*>(stage)[(q * 8 + j) * BM + x];
             }
           }
         }
       }
     }
+    if (lane < 8) ptx::bulk_wait_all();  // every copy has landed before the CTA ends
   }
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (PAIR) ptx::cluster_sync();  // neither CTA leaves while the other may signal it
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc_g<PAIR>(tmem, 512);
   }
 }
 
@@ -375,10 +495,27 @@ bool encode_codes(CUtensorMap* m, const uint8_t* base, const Store& st, uint32_t
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale atoms [batch][row_atoms][block_atoms][512 bytes] -> tensor map with a box
+// of two block atoms x `box_atoms` row atoms, as 32-bit words.
+bool encode_scales(CUtensorMap* m, const uint8_t* q, const Store& st, uint32_t box_atoms, int rank) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = (cuuint64_t)(st.block_atoms * ATOM_BYTES);
+  const cuuint64_t dims[3] = {row / 4, (cuuint64_t)st.row_atoms, (cuuint64_t)st.batch};
+  const cuuint64_t strides[2] = {row, row * (cuuint64_t)st.row_atoms};
+  const cuuint32_t box[3] = {2 * ATOM_BYTES / 4, box_atoms, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, (cuuint32_t)rank,
+            const_cast<uint8_t*>(q + st.scales_off), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxDev = 64;
 
 template <int BN, bool EXPERTS>
 cudaError_t run(const ProductArgs& p, cudaStream_t s) {
+  using F = Form<BN>;
   constexpr int smem = smem_bytes<BN>();
   static std::atomic<bool> ready[kMaxDev];  // per device: the attribute is set (calls may race)
   auto k = k_mx_gemm<BN, EXPERTS>;
@@ -390,22 +527,40 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < kMaxDev) ready[dev].store(true, std::memory_order_release);
   }
-  const int sms = device_sm_count();
+  const int ctas = F::PAIR ? 2 : 1, units = device_sm_count() / ctas;
   // a dense product of fewer than 128 rows a tile has one tile of tokens
   const Store sw = store_of(EXPERTS ? p.E : 1, p.N, p.K),
               sx = store_of(1, p.x_rows, p.K,
                             EXPERTS ? experts_atom_shift(p.slots, p.E) : 7);
-  CUtensorMap tw, tx;
-  if (!encode_codes(&tw, p.w, sw, BM, 3) || !encode_codes(&tx, p.x, sx, BN, 2))
+  CUtensorMap tw, tx, tws, txs;
+  if (!encode_codes(&tw, p.w, sw, BM, 3) || !encode_codes(&tx, p.x, sx, F::B_ROWS, 2) ||
+      !encode_scales(&tws, p.w, sw, 1, 3) || !encode_scales(&txs, p.x, sx, F::B_ATOMS, 2))
     return cudaErrorInvalidValue;
-  const int num_n = (int)ceil_div(p.N, BM), num_m = EXPERTS ? 0 : (int)ceil_div(p.M, BN);
+  const int num_n = (int)ceil_div(p.N, F::BNW), num_m = EXPERTS ? 0 : (int)ceil_div(p.M, BN);
   // experts: at most one partly filled tile per expert beyond the full ones
   const int64_t tiles = EXPERTS ? (p.slots / BN + (p.slots < p.E + 1 ? p.slots : p.E + 1)) *
                                       (int64_t)num_n
                                 : (int64_t)num_m * num_n;
-  const int grid = (int)(tiles < sms ? tiles : sms);
-  e = launch_after_previous(k, dim3(grid), dim3(192), (size_t)smem, s, tw, tx, p, num_m, num_n,
-                            -8, sx.scales_off, sw.scales_off);
+  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int grid = (int)(tiles < units ? tiles : units) * ctas;
+  const int esize = p.out_dtype == IMC_F32 ? 4 : 2;
+  const int row_copies =
+      (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && (p.N * esize) % 16 == 0 ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = F::PAIR ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, k, tw, tx, tws, txs, p, num_m, num_n, 8, row_copies);
   note_launch();
   return e;
 }
