@@ -1,8 +1,6 @@
 // Routing of tokens to experts: scores and choice, their gradient, the order
 // of the chosen rows by expert, and the weighted sum of the experts' results
 // with its gradient.
-#include <cooperative_groups.h>
-
 #include <atomic>
 
 #include "mx_internal.cuh"
@@ -12,7 +10,6 @@ namespace imc {
 namespace mx {
 namespace {
 
-namespace cg = cooperative_groups;
 constexpr uint32_t kAll = 0xffffffffu;
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -230,51 +227,46 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 }
 
 // ------------------------------------------------------------------ layout
-// Stable counting sort of n slots by expert, in one launch of one cluster of
-// CTAs.  Each warp owns a contiguous run of slots and walks it 32 at a time: a
-// slot's rank among the warp's slots of its expert is what the warp has counted
-// so far plus the equal experts on lower lanes (found with one ballot per bit of
-// the expert's number, so nothing depends on the timing of atomics).  The counts
-// are summed over warps (shared memory) and CTAs (distributed shared memory);
-// a slot's place is then the expert's first place + the slots of lower CTAs and
-// warps + its rank, which waits in `dest` meanwhile.  Experts outside [0, E)
-// fall into bucket E.
-constexpr int kLayoutThreads = 1024, kLayoutWarps = kLayoutThreads / 32;
+// Stable counting sort of n slots by expert.  Each warp owns a contiguous run
+// of slots and walks it 32 at a time: a slot's rank among its CTA's slots of the
+// same expert is what lower warps and steps have counted plus the equal experts
+// on lower lanes, found with one ballot per bit of the expert's number (nothing
+// depends on the timing of atomics).  A slot's place is the expert's first place
+// + the slots of lower CTAs + its rank.  Experts outside [0, E) fall into
+// bucket E.
+//
+// Up to kLayoutOne slots one CTA does all of it.  More slots take two launches
+// over many CTAs: k_layout_count leaves ranks in `dest` and each CTA's counts in
+// `counts` [CTA][E + 1], k_layout_place sums those up (every CTA for itself, a
+// bucket a thread) and places the slots.  One launch over a cluster of eight
+// CTAs measured 26 us for 131072 slots of 256 experts: too few warps for the
+// ~60 instructions per 32 slots.
+constexpr int kLayoutThreads = 512, kLayoutWarps = kLayoutThreads / 32;
+constexpr int kLayoutOne = 4096;
 
-__global__ void __launch_bounds__(kLayoutThreads, 1)
-    k_layout(const int32_t* __restrict__ experts, const int n, const int E,
-             int32_t* __restrict__ offsets, int32_t* __restrict__ starts,
-             int32_t* __restrict__ order, int32_t* dest) {
-  extern __shared__ int32_t sm[];
-  const int B = E + 1;                    // buckets
-  int32_t* hist = sm;                     // [warps][B]: counts, then slots of lower warps
-  int32_t* total = sm + kLayoutWarps * B; // [B] this CTA's counts
-  int32_t* first = total + B;             // [B] place of this CTA's first slot of a bucket
-  int32_t* shift = first + B;             // [B] starts[e] - offsets[e]
-  __shared__ int32_t sums[2][kLayoutWarps];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kLayoutWarps * B; i += kLayoutThreads) hist[i] = 0;
-  __syncthreads();
-  ptx::griddep_wait();
-  ptx::griddep_launch();
-  // this warp's slots: a multiple of 32 of them
-  const int64_t per = ((int64_t)n + 32 * kLayoutWarps * ranks - 1) / (32 * kLayoutWarps * ranks) * 32;
-  const int64_t w0 = ((int64_t)rank * kLayoutWarps + warp) * per;
-  const int64_t w1 = w0 + per < n ? w0 + per : n;
-  int32_t* mine = hist + warp * B;
+struct LayoutArgs {
+  const int32_t* experts;
+  int n, E, per;  // per: slots of a warp, a multiple of 32
+  int32_t *offsets, *starts, *order, *dest, *counts;
+};
+
+__device__ __forceinline__ int layout_bucket(const LayoutArgs& a, int64_t i, int64_t end) {
+  if (i >= end) return a.E + 1;  // no slot
+  const int e = __ldg(a.experts + i);
+  return e < 0 || e >= a.E ? a.E : e;
+}
+
+// The slots [w0, w1) of this warp: their ranks within the warp go to `dest`,
+// the warp's counts to mine [E + 1] (zero before).
+__device__ __forceinline__ void layout_rank(const LayoutArgs& a, int64_t w0, int64_t w1,
+                                            int32_t* mine) {
+  const int lane = threadIdx.x & 31, B = a.E + 1;
   const int bits = 32 - __clz(B);  // of bucket numbers 0 .. B (B: no slot)
-  constexpr int U = 8;             // steps whose loads are in flight together
-  auto bucket = [&](int64_t i) {
-    if (i >= w1) return B;
-    const int e = __ldg(experts + i);
-    return e < 0 || e >= E ? E : e;
-  };
+  constexpr int U = 4;             // steps whose loads are in flight together
   for (int64_t i0 = w0; i0 < w1; i0 += 32 * U) {
     int ids[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) ids[u] = bucket(i0 + 32 * u + lane);
+    for (int u = 0; u < U; ++u) ids[u] = layout_bucket(a, i0 + 32 * u + lane, w1);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i0 + 32 * u >= w1) break;
@@ -289,15 +281,19 @@ __global__ void __launch_bounds__(kLayoutThreads, 1)
       __syncwarp();
       if (e < B) {
         if (place == 0) mine[e] = before + __popc(same);
-        dest[i0 + 32 * u + lane] = before + place;
+        a.dest[i0 + 32 * u + lane] = before + place;
       }
       __syncwarp();
     }
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < B; e += kLayoutThreads) {  // exclusive over warps
+}
+
+// hist [warps][B] to exclusive sums over the warps; their total of bucket e goes
+// to total[e].
+__device__ __forceinline__ void layout_over_warps(int32_t* hist, int B, int32_t* total) {
+  for (int e = threadIdx.x; e < B; e += blockDim.x) {
     int sum = 0;
-#pragma unroll 8
+#pragma unroll
     for (int w = 0; w < kLayoutWarps; ++w) {
       const int c = hist[w * B + e];
       hist[w * B + e] = sum;
@@ -305,22 +301,22 @@ __global__ void __launch_bounds__(kLayoutThreads, 1)
     }
     total[e] = sum;
   }
-  cluster.sync();
-  // Thread e: bucket e's count over all CTAs, and before this CTA; then the
-  // exclusive sums over buckets of the counts and of the counts rounded up to
-  // 128 rows (B <= 1025 buckets: a second pass for the last one).
+}
+
+// From `all(e)`, bucket e's slots: offsets and starts (written by the CTA that
+// has `write`), first[e] = the expert's first place, shift[e] = starts - offsets.
+template <typename All>
+__device__ __forceinline__ void layout_scan(const LayoutArgs& a, bool write, int32_t* first,
+                                            int32_t* shift, All all) {
+  __shared__ int32_t sums[2][32];
+  const int B = a.E + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warps = (int)blockDim.x >> 5;
   int carry = 0, carry_pad = 0;
-  for (int e0 = 0; e0 < B; e0 += kLayoutThreads) {
+  for (int e0 = 0; e0 < B; e0 += blockDim.x) {
     const int e = e0 + threadIdx.x;
-    int all = 0, before = 0;
-    if (e < B)
-      for (int r = 0; r < ranks; ++r) {
-        const int c = cluster.map_shared_rank(total, r)[e];
-        if (r < rank) before += c;
-        all += c;
-      }
-    const int pad = (all + ATOM_ROWS - 1) / ATOM_ROWS * ATOM_ROWS;
-    int x = all, y = pad;
+    const int n = e < B ? all(e) : 0;
+    const int pad = (n + ATOM_ROWS - 1) / ATOM_ROWS * ATOM_ROWS;
+    int x = n, y = pad;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int ox = __shfl_up_sync(kAll, x, d), oy = __shfl_up_sync(kAll, y, d);
@@ -329,56 +325,48 @@ __global__ void __launch_bounds__(kLayoutThreads, 1)
         y += oy;
       }
     }
+    __syncthreads();
     if (lane == 31) {
       sums[0][warp] = x;
       sums[1][warp] = y;
     }
     __syncthreads();
-    if (warp == 0) {
-      int u = sums[0][lane], v = sums[1][lane];
-      const int u0 = u, v0 = v;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int ou = __shfl_up_sync(kAll, u, d), ov = __shfl_up_sync(kAll, v, d);
-        if (lane >= d) {
-          u += ou;
-          v += ov;
-        }
+    int upto = carry + x, upto_pad = carry_pad + y;
+    for (int w = 0; w < warps; ++w) {
+      const int u = sums[0][w], v = sums[1][w];
+      if (w < warp) {
+        upto += u;
+        upto_pad += v;
       }
-      sums[0][lane] = u - u0;
-      sums[1][lane] = v - v0;
+      carry += u;
+      carry_pad += v;
     }
-    __syncthreads();
-    const int upto = carry + sums[0][warp] + x, upto_pad = carry_pad + sums[1][warp] + y;
     if (e < B) {
-      const int off = upto - all, start = upto_pad - pad;
-      if (rank == 0) {
-        offsets[e] = off;
-        starts[e] = start;
-        if (e == E) offsets[E + 1] = n;
+      const int off = upto - n, start = upto_pad - pad;
+      if (write) {
+        a.offsets[e] = off;
+        a.starts[e] = start;
+        if (e == a.E) a.offsets[e + 1] = a.n;
       }
       shift[e] = start - off;
-      first[e] = off + before;
+      first[e] = off;
     }
-    if (e0 + kLayoutThreads < B) {  // the sums so far, for the next pass
-      __syncthreads();
-      if (threadIdx.x == kLayoutThreads - 1) {
-        sums[0][0] = upto;
-        sums[1][0] = upto_pad;
-      }
-      __syncthreads();
-      carry = sums[0][0];
-      carry_pad = sums[1][0];
-    }
-    __syncthreads();
   }
+}
+
+// Every slot of [w0, w1) to its place: first[e] + mine[e] + its rank.
+__device__ __forceinline__ void layout_place(const LayoutArgs& a, int64_t w0, int64_t w1,
+                                             const int32_t* first, const int32_t* mine,
+                                             const int32_t* shift) {
+  constexpr int U = 4;
+  const int lane = threadIdx.x & 31;
   for (int64_t i0 = w0; i0 < w1; i0 += 32 * U) {
     int ids[U], ranked[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t i = i0 + 32 * u + lane;
-      ids[u] = bucket(i);
-      ranked[u] = i < w1 ? dest[i] : 0;  // this thread's own write
+      ids[u] = layout_bucket(a, i, w1);
+      ranked[u] = i < w1 ? a.dest[i] : 0;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -386,11 +374,62 @@ __global__ void __launch_bounds__(kLayoutThreads, 1)
       const int e = ids[u];
       if (i >= w1) break;
       const int pos = first[e] + mine[e] + ranked[u];
-      order[pos] = (int32_t)i;
-      dest[i] = e < E ? pos + shift[e] : -1;
+      a.order[pos] = (int32_t)i;
+      a.dest[i] = e < a.E ? pos + shift[e] : -1;
     }
   }
-  cluster.sync();  // no CTA leaves while another may read its totals
+}
+
+// ONE: the whole sort in one CTA; else the first of the two launches.
+template <bool ONE>
+__global__ void __launch_bounds__(kLayoutThreads) k_layout_count(const LayoutArgs a) {
+  extern __shared__ int32_t sm[];
+  const int B = a.E + 1, warp = threadIdx.x >> 5;
+  int32_t *hist = sm, *total = sm + kLayoutWarps * B, *first = total + B, *shift = first + B;
+  for (int i = threadIdx.x; i < kLayoutWarps * B; i += blockDim.x) hist[i] = 0;
+  __syncthreads();
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int64_t w0 = ((int64_t)blockIdx.x * kLayoutWarps + warp) * a.per;
+  const int64_t w1 = w0 + a.per < a.n ? w0 + a.per : a.n;
+  int32_t* mine = hist + warp * B;
+  layout_rank(a, w0, w1, mine);
+  __syncthreads();
+  layout_over_warps(hist, B, total);
+  __syncthreads();
+  if (ONE) {
+    layout_scan(a, true, first, shift, [&](int e) { return total[e]; });
+    __syncthreads();
+    layout_place(a, w0, w1, first, mine, shift);
+  } else {
+    for (int e = threadIdx.x; e < B; e += blockDim.x)
+      a.counts[(int64_t)blockIdx.x * B + e] = total[e];
+    for (int64_t i = w0 + (threadIdx.x & 31); i < w1; i += 32)  // ranks within the CTA
+      a.dest[i] += mine[layout_bucket(a, i, w1)];
+  }
+}
+
+__global__ void __launch_bounds__(kLayoutThreads) k_layout_place(const LayoutArgs a) {
+  extern __shared__ int32_t sm[];
+  const int B = a.E + 1, warp = threadIdx.x >> 5;
+  int32_t *first = sm, *shift = first + B, *before = shift + B;
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  layout_scan(a, blockIdx.x == 0, first, shift, [&](int e) {
+    int all = 0, low = 0;
+#pragma unroll 8
+    for (int c = 0; c < (int)gridDim.x; ++c) {
+      const int v = __ldg(a.counts + (int64_t)c * B + e);
+      all += v;
+      if (c < (int)blockIdx.x) low += v;
+    }
+    before[e] = low;
+    return all;
+  });
+  __syncthreads();
+  const int64_t w0 = ((int64_t)blockIdx.x * kLayoutWarps + warp) * a.per;
+  const int64_t w1 = w0 + a.per < a.n ? w0 + a.per : a.n;
+  layout_place(a, w0, w1, first, before, shift);
 }
 
 // ------------------------------------------------------------ weighted sum
@@ -532,37 +571,42 @@ cudaError_t launch_route_backward(const RouteArgs& a, int dtype, const float* g,
   return route<__nv_bfloat16>(a, g, grad_logits, s);
 }
 
+// CTAs of a layout: enough for four steps of 32 slots a warp, at most
+// kLayoutMaxCtas (every CTA of the second launch reads all of their counts).
+int layout_ctas(int64_t n) {
+  if (n <= kLayoutOne) return 1;
+  const int64_t c = ceil_div(n, kLayoutWarps * 128);
+  return (int)(c < kLayoutMaxCtas ? c : kLayoutMaxCtas);
+}
+
 cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets, int32_t* starts,
-                          int32_t* order, int32_t* dest, cudaStream_t s) {
+                          int32_t* order, int32_t* dest, int32_t* counts, cudaStream_t s) {
   note_kernel_name("k_layout");
-  const int smem = (kLayoutWarps + 3) * (E + 1) * 4;
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const int most = (kLayoutWarps + 3) * (1024 + 1) * 4;
   if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(k_layout, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (kLayoutWarps + 3) * (1024 + 1) * 4);
-    if (e != cudaSuccess) return e;
+    for (auto k : {k_layout_count<true>, k_layout_count<false>}) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (e != cudaSuccess) return e;
+    }
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
-  // a CTA's warps take 1024 slots per step
-  const unsigned ranks = n <= 2048 ? 1 : (n <= 4096 ? 2 : (n <= 8192 ? 4 : 8));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ranks);
-  cfg.blockDim = dim3(kLayoutThreads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ranks;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, k_layout, experts, n, E, offsets, starts, order, dest);
+  const int ctas = layout_ctas(n);
+  LayoutArgs a = {experts, n, E, 0, offsets, starts, order, dest, counts};
+  a.per = (int)(ceil_div(n, (int64_t)32 * kLayoutWarps * ctas) * 32);
+  const size_t smem = (size_t)(kLayoutWarps + 3) * (E + 1) * 4;
+  if (ctas == 1) {
+    e = launch_after_previous(k_layout_count<true>, dim3(1), dim3(kLayoutThreads), smem, s, a);
+  } else {
+    e = launch_after_previous(k_layout_count<false>, dim3(ctas), dim3(kLayoutThreads), smem, s, a);
+    note_launch();
+    if (e == cudaSuccess)
+      e = launch_after_previous(k_layout_place, dim3(ctas), dim3(kLayoutThreads),
+                                (size_t)3 * (E + 1) * 4, s, a);
+  }
   note_launch();
   return e;
 }

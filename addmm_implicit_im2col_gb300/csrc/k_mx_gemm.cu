@@ -15,8 +15,12 @@
 //   warp 1      TMEM owner + MMA issuer: copies the stage's scales to TMEM
 //               (tcgen05.cp), then one MMA per 64 values of K into an fp32
 //               accumulator
-//   warps 2-5   epilogue: tcgen05.ld, bias, ReLU, rounding, a staging row of 128
-//               outputs per token in shared memory, one bulk copy per token row
+//   warps 2-9   epilogue, two warps per TMEM lane quadrant that take turns by 32
+//               tokens: tcgen05.ld, bias, ReLU, rounding, and one store of 32
+//               consecutive outputs per token straight from the registers (a
+//               staging tile and a bulk copy per token row measured 1.7 times
+//               the time per tile: a warp issues the copies of its lanes one by
+//               one, ~130 cycles each)
 //
 // More than 128 tokens run as CTA pairs (cta_group::2): 256 rows of the weight x
 // 256 tokens per pair, each CTA loading its 128 rows and half of the tokens, so
@@ -59,7 +63,7 @@ struct Form {
   static constexpr int ATOM_TOKENS = BN < 128 ? BN : 128;      // token rows of a scale atom
   static constexpr int SA_BYTES = 2 * ATOM_BYTES, SB_BYTES = 2 * ATOM_BYTES * B_ATOMS;
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-  static constexpr int STAGES = BN >= 128 ? 5 : (BN > 32 ? 6 : 8);
+  static constexpr int STAGES = BN >= 128 ? 6 : (BN > 32 ? 7 : 8);
   // TMEM columns: two accumulators (ACC1 apart), then the scales of SETS stages
   static constexpr int SF_COLS = 8 + 8 * B_ATOMS;
   static constexpr int SETS = PAIR ? 2 : STAGES;
@@ -71,7 +75,7 @@ struct Form {
   static constexpr uint32_t TX = (PAIR ? 2 : 1) * STAGE;       // bytes a stage's barrier waits for
 };
 
-constexpr int ROW_BUF = 32 * BM * 4;  // staging of 32 tokens x 128 outputs
+constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
 
 struct Ctl {
   uint64_t full[8], empty[8], accf[2], acce[2], drain;
@@ -83,7 +87,7 @@ struct Ctl {
 
 template <int BN>
 constexpr int smem_bytes() {
-  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + 2 * ROW_BUF + (int)sizeof(Ctl);
+  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + (int)sizeof(Ctl);
 }
 static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448 &&
                   smem_bytes<64>() <= 232448 && smem_bytes<32>() <= 232448,
@@ -116,23 +120,46 @@ __device__ __forceinline__ bool wait_any(uint64_t* bar, uint32_t parity, volatil
   }
 }
 
-__device__ __forceinline__ uint32_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
+__device__ __forceinline__ uint16_t half_bits(float v) { return __half_as_ushort(__float2half_rn(v)); }
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Stores one output of each of 32 tokens (`live` of them) per lane: token j's is
+// at out[j * N], or in the experts' form at out[slot of lane j * N].  `in`: this
+// lane's column exists.
+template <bool EXPERTS, typename O, typename Bits>
+__device__ __forceinline__ void store_tokens(O* out, int64_t N, int slot, int live, bool in,
+                                             const uint32_t (&v)[32], Bits bits) {
+  if (live == 32) {  // no branch per token
+    O* o = out;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (EXPERTS) o = out + (int64_t)__shfl_sync(0xffffffffu, slot, j) * N;
+      if (in) *o = bits(v[j]);
+      o += N;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j < live) {
+        O* o = out + (EXPERTS ? (int64_t)__shfl_sync(0xffffffffu, slot, j) : (int64_t)j) * N;
+        if (in) *o = bits(v[j]);
+      }
+    }
+  }
+}
+
 template <int BN, bool EXPERTS>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(THREADS, 1)
     k_mx_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
-              const ProductArgs p, const int num_m, const int num_n, const int group,
-              const int row_copies) {
+              const ProductArgs p, const int num_m, const int num_n, const int group) {
   using F = Form<BN>;
   constexpr bool PAIR = F::PAIR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
-  uint8_t* rows_buf = smem + F::STAGES * F::STAGE;
-  Ctl* ctl = reinterpret_cast<Ctl*>(rows_buf + 2 * ROW_BUF);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::STAGES * F::STAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
   const int unit = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
@@ -147,7 +174,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ctl->accf[b], 1);
-      ptx::mbar_init(&ctl->acce[b], PAIR ? 8 : 4);
+      ptx::mbar_init(&ctl->acce[b], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
     }
     ptx::mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
@@ -347,17 +374,17 @@ __global__ void __launch_bounds__(192, 1)
   } else {
     // ----------------------------------------------------------- epilogue
     ptx::griddep_wait();  // bias, and the order of output writes
-    const int q = warp & 3;  // TMEM lane quadrant this warp may read
-    const int esize = p.out_dtype == IMC_F32 ? 4 : 2;
+    const int q = warp & 3;               // TMEM lane quadrant this warp may read
+    const int turn = (warp - 2) >> 2;     // it takes every other chunk of 32 tokens
     const uint32_t acce0 = PAIR ? ptx::cluster_addr(&ctl->acce[0], 0) : 0u;
-    int tl = 0, chunk = 0;  // chunks so far: the staging buffers alternate
+    int tl = 0;
     for (int t = unit; t < num_tiles; t += units) {
       const Tile r = tile_of(t);
       const bool none = EXPERTS && r.e == p.E;  // slots of no expert: zeros
       const int buf = tl & 1;
       const int64_t n = r.n0 + q * 32 + lane;
-      const int width = (int)(p.N - r.n0 < BM ? p.N - r.n0 : BM);  // outputs of a row; <= 0: none
-      const float bias = p.bias && n < p.N && !none ? __ldg(p.bias + (int64_t)r.e * p.N + n) : 0.0f;
+      const bool in = n < p.N;
+      const float bias = p.bias && in && !none ? __ldg(p.bias + (int64_t)r.e * p.N + n) : 0.0f;
       if (!none) {
         int ok = 1;
         if (lane == 0)
@@ -365,22 +392,19 @@ __global__ void __launch_bounds__(192, 1)
                               tc::kSiteEpilogueAccFull, wd)
                    ? 1
                    : 0;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (tc::epi_any(!ok)) break;
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         ptx::tc_fence_after();
         ++tl;
       }
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * F::ACC1);
 #pragma unroll 1
-      for (int i = 0; i < BN / 32; ++i) {
+      for (int i = turn; i < BN / 32 || i == turn; i += 2) {
         // accumulator 0 shares its last columns with 1, which shares its first
         const int c = 32 * (PAIR && buf == 0 ? (i + BN / 32 - F::SHARED) % (BN / 32) : i);
-        const int live = min(32, r.rows - c);  // the same for all four warps
+        const int live = min(32, r.rows - c);  // the same for all lanes
         uint32_t v[32];
-        int64_t row = 0;  // the row that lanes 0-7 will store
-        if (live > 0 && lane < 8 && q * 8 + lane < live)
-          row = EXPERTS ? (int64_t)__ldg(p.order + r.first + c + q * 8 + lane)
-                        : (int64_t)r.m0 + c + q * 8 + lane;
+        int slot = 0;
+        if (EXPERTS && lane < live) slot = __ldg(p.order + r.first + c + lane);
         if (live > 0 && !none) {
           ptx::tmem_ld32(tbase + (uint32_t)c, v);
           ptx::tmem_ld_wait();
@@ -388,7 +412,9 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0u;
         }
-        if (!none && i == (PAIR ? F::SHARED : BN / 32) - 1) {  // the MMA may have it back
+        // after this warp's last chunk (a pair: its last that is shared) the MMA
+        // may have the accumulator back
+        if (!none && (PAIR ? i == F::SHARED - 2 + turn : i + 2 >= BN / 32)) {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -396,9 +422,7 @@ __global__ void __launch_bounds__(192, 1)
             else ptx::mbar_arrive(&ctl->acce[buf]);
           }
         }
-        if (live <= 0 || width <= 0) continue;
-        uint8_t* stage = rows_buf + (chunk & 1) * ROW_BUF;
-        ++chunk;
+        if (live <= 0 || c >= BN) continue;
         if (!none) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -407,47 +431,18 @@ __global__ void __launch_bounds__(192, 1)
             v[j] = __float_as_uint(y);
           }
         }
-        if (esize == 4) {
-          uint32_t* d = reinterpret_cast<uint32_t*>(stage) + q * 32 + lane;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) d[j * BM] = v[j];
-        } else {
-          uint16_t* d = reinterpret_cast<uint16_t*>(stage) + q * 32 + lane;
-          if (p.out_dtype == IMC_BF16) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) d[j * BM] = (uint16_t)bf16_bits(__uint_as_float(v[j]));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) d[j * BM] = (uint16_t)half_bits(__uint_as_float(v[j]));
-          }
-        }
-        // The buffer's rows are copied out by the eight lanes that also wait, one
-        // chunk later and before the barrier, until the copies have read them.
-        if (lane < 8) ptx::bulk_wait_read0();
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        tc::epi_sync();
-        if (row_copies) {
-          if (lane < 8 && q * 8 + lane < live)
-            ptx::bulk_store(static_cast<uint8_t*>(p.out) + (row * p.N + r.n0) * esize,
-                            stage + (q * 8 + lane) * BM * esize, (uint32_t)(width * esize));
-          if (lane < 8) ptx::bulk_commit();
-        } else {  // rows that are no multiples of 16 bytes
-          for (int j = 0; j < 8 && q * 8 + j < live; ++j) {
-            const int64_t at = __shfl_sync(0xffffffffu, row, j) * p.N + r.n0;
-            for (int x = lane; x < width; x += 32) {
-              if (esize == 4)
-                static_cast<uint32_t*>(p.out)[at + x] =
-                    reinterpret_cast<const uint32_t*>(stage)[(q * 8 + j) * BM + x];
-              else
-                static_cast<uint16_t*>(p.out)[at + x] =
-                    reinterpret_cast<const uint16_t*>(stage)[(q * 8 + j) * BM + x];
-            }
-          }
-        }
+        const int64_t at = (EXPERTS ? 0 : (int64_t)(r.m0 + c) * p.N) + n;
+        if (p.out_dtype == IMC_F32)
+          store_tokens<EXPERTS>(static_cast<uint32_t*>(p.out) + at, p.N, slot, live, in, v,
+                                [](uint32_t b) { return b; });
+        else if (p.out_dtype == IMC_BF16)
+          store_tokens<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, slot, live, in, v,
+                                [](uint32_t b) { return bf16_bits(__uint_as_float(b)); });
+        else
+          store_tokens<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, slot, live, in, v,
+                                [](uint32_t b) { return half_bits(__uint_as_float(b)); });
       }
     }
-    if (lane < 8) ptx::bulk_wait_all();  // every copy has landed before the CTA ends
   }
 
   ptx::tc_fence_before();
@@ -543,12 +538,9 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s) {
                                 : (int64_t)num_m * num_n;
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int grid = (int)(tiles < units ? tiles : units) * ctas;
-  const int esize = p.out_dtype == IMC_F32 ? 4 : 2;
-  const int row_copies =
-      (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 && (p.N * esize) % 16 == 0 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(192);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -560,7 +552,7 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = F::PAIR ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, k, tw, tx, tws, txs, p, num_m, num_n, 8, row_copies);
+  e = cudaLaunchKernelEx(&cfg, k, tw, tx, tws, txs, p, num_m, num_n, 8);
   note_launch();
   return e;
 }

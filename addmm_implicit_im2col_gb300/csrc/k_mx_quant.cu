@@ -51,86 +51,136 @@ __device__ __forceinline__ uint32_t max_bits8(const float (&v)[8]) {
   return m;
 }
 
-// Which rows and columns a half-warp takes: 16 lanes cover 128 columns of a row
-// (a lane 8 columns, four lanes a block of 32).  A CTA's 16 half-warps cover
-// 2^cs chunks of 128 columns of 2^(4-cs) rows, and each goes on to U rows; with
-// powers of two, no index is divided (64-bit divisions per item had cost more
-// than the memory traffic: 59 us against 12.5 us at 8192 x 4096 bf16).
+// Sixteen scaled values to sixteen codes.
+__device__ __forceinline__ uint2 codes16(const float (&v)[16], float up) {
+  float lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo[i] = v[i];
+    hi[i] = v[8 + i];
+  }
+  return make_uint2(codes8(lo, up), codes8(hi, up));
+}
+
+// Which rows and columns a lane takes: 8 lanes cover 128 columns of a row (a
+// lane 16 columns, two lanes a block of 32).  A CTA's 32 such groups cover 2^cs
+// chunks of 128 columns of 2^(5-cs) rows, and each goes on to U rows, rows_step
+// apart; with powers of two, no index is divided (with 64-bit divisions per 8
+// values, 8192 x 4096 bf16 took 59 us, with 8 values a lane 34 us, against 12.5
+// us of memory traffic: both bound by instructions).
 struct RowMap {
   int chunk_shift;   // cs
   int64_t chunks;    // block atoms of a row
 };
-template <int U>
-__device__ __forceinline__ int64_t map_row(const RowMap& m, int u) {
-  const int half = threadIdx.x >> 4, rows_shift = 4 - m.chunk_shift;
-  return ((((int64_t)blockIdx.x * U + u) << rows_shift)) + (half >> m.chunk_shift);
-}
-// Matrix and row within it of flat row r (one matrix: no division).
-__device__ __forceinline__ void split_row(int64_t r, int64_t rows, int64_t batch, int64_t& b,
-                                          int64_t& rr) {
-  b = 0;
-  rr = r;
-  if (batch > 1) {
-    b = r / rows;
-    rr = r - b * rows;
-  }
-}
+constexpr int GROUPS_SHIFT = 5;  // log2 of a CTA's groups of 8 lanes
 
-// Rows: a half-warp writes 64 bytes of codes and one scale word per row; the U
-// rows' loads are in flight together.
+// A lane's 16 values of one row: loaded raw, so that the U rows' loads are in
+// flight together, and widened later.
+template <typename T>
+struct Raw16 {
+  static constexpr int N = (int)sizeof(T);  // 16-byte words
+  uint4 w[N];
+  __device__ __forceinline__ void load(const T* p, int n, bool vec) {
+    if (vec && n == 16) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+      alignas(16) T e[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) e[i] = i < n ? p[i] : from_f32<T>(0.0f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(e)[i];
+    }
+  }
+  __device__ __forceinline__ void widen(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (sizeof(T) == 4) {
+          v[4 * i + j] = __uint_as_float(u[j]);
+        } else {
+          const float2 f = two(u[j]);
+          v[8 * i + 2 * j] = f.x;
+          v[8 * i + 2 * j + 1] = f.y;
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ float2 two(uint32_t u) {
+    if (sizeof(T) == 2 && is_bf16(T()))
+      return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  }
+  static __device__ __forceinline__ bool is_bf16(__nv_bfloat16) { return true; }
+  static __device__ __forceinline__ bool is_bf16(__half) { return false; }
+  static __device__ __forceinline__ bool is_bf16(float) { return false; }
+};
+
+// Rows: a group of 8 lanes writes 64 bytes of codes and one scale word per row.
 template <typename T, int U>
 __global__ void __launch_bounds__(256) k_mx_quant_rows(const QuantArgs a, const RowMap map,
                                                        const bool vec) {
   ptx::griddep_wait();
   ptx::griddep_launch();
   const Store& st = a.st;
-  const T* x = static_cast<const T*>(a.x);
   uint8_t* scales = a.q + st.scales_off;
-  const int l16 = threadIdx.x & 15;
-  const int64_t all_rows = a.batch * a.rows;
-  const int chunk = (threadIdx.x >> 4) & ((1 << map.chunk_shift) - 1);
-  for (int64_t ba = ((int64_t)blockIdx.y << map.chunk_shift) + chunk;
-       ba - (chunk & 1) < map.chunks;  // the same for both halves of a warp, which shuffle together
-       ba += (int64_t)gridDim.y << map.chunk_shift) {
-    const int64_t col = ba * 128 + l16 * 8, blk = ba * ATOM_BLOCKS + (l16 >> 2);
-    const int n = (int)(a.cols - col > 8 ? 8 : (a.cols > col ? a.cols - col : 0));
-    float v[U][8];
+  const int l8 = threadIdx.x & 7, group = threadIdx.x >> 3, cs = map.chunk_shift;
+  const int64_t all_rows = a.batch * a.rows, step = 1 << (GROUPS_SHIFT - cs);
+  const int64_t row0 = (int64_t)blockIdx.x * (step * U) + (group >> cs);
+  const int chunk = group & ((1 << cs) - 1);
+  for (int64_t y = blockIdx.y; (y << cs) < map.chunks; y += gridDim.y) {  // the same for the CTA
+    const int64_t ba = (y << cs) + chunk, col = ba * 128 + l8 * 16;
+    const int n = (int)(a.cols - col > 16 ? 16 : (a.cols > col ? a.cols - col : 0));
+    const T* x = static_cast<const T*>(a.x) + row0 * a.row_stride + col;
+    Raw16<T> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t r = map_row<U>(map, u);
-      int64_t b, rr;
-      split_row(r, a.rows, a.batch, b, rr);
-      load8<T>(x + b * a.batch_stride + rr * a.row_stride + col, r < all_rows ? n : 0, vec, v[u]);
+      const int64_t r = row0 + u * step;
+      const T* p = x + u * (step * a.row_stride);
+      if (a.batch > 1 && r < all_rows) {  // matrices need not be row_stride * rows apart
+        const int64_t b = r / a.rows;
+        p = static_cast<const T*>(a.x) + b * a.batch_stride + (r - b * a.rows) * a.row_stride + col;
+      }
+      raw[u].load(p, r < all_rows ? n : 0, vec);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      uint32_t m = max_bits8(v[u]);
+      float v[16];
+      raw[u].widen(v);
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const uint32_t sb = scale_byte(m);
-      const uint32_t code = codes8(v[u], scale_up(sb));
+      const uint2 code = codes16(v, scale_up(sb));
       // the four blocks' bytes to one word (blocks past cols hold zeros: byte 0)
-      uint32_t word = sb << ((l16 >> 2) * 8);
+      uint32_t word = sb << ((l8 >> 1) * 8);
+      word |= __shfl_xor_sync(0xffffffffu, word, 2);
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
-      word |= __shfl_xor_sync(0xffffffffu, word, 8);
-      const int64_t r = map_row<U>(map, u);
+      const int64_t r = row0 + u * step, blk = ba * ATOM_BLOCKS + (l8 >> 1);
       if (r >= all_rows || ba >= map.chunks) continue;
+      uint8_t* codes = a.q + blk * 16 + (l8 & 1) * 8;
       if (a.dest) {
         for (int d = 0; d < a.share; ++d) {
           const int64_t to = __ldg(a.dest + r * a.share + d);
           if (to < 0) continue;
-          if (blk < st.blocks)
-            *reinterpret_cast<uint32_t*>(a.q + to * st.pitch + blk * 16 + (l16 & 3) * 4) = code;
-          if (l16 == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(st, to, ba)) = word;
+          if (blk < st.blocks) *reinterpret_cast<uint2*>(codes + to * st.pitch) = code;
+          if (l8 == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(st, to, ba)) = word;
         }
       } else {
-        int64_t b, rr;
-        split_row(r, a.rows, a.batch, b, rr);
-        if (blk < st.blocks)
-          *reinterpret_cast<uint32_t*>(a.q + r * st.pitch + blk * 16 + (l16 & 3) * 4) = code;
-        if (l16 == 0)
-          *reinterpret_cast<uint32_t*>(scales + b * st.row_atoms * st.block_atoms * ATOM_BYTES +
-                                       scale_word(st, rr, ba)) = word;
+        if (blk < st.blocks) *reinterpret_cast<uint2*>(codes + r * st.pitch) = code;
+        if (l8 == 0) {
+          int64_t rr = r;
+          uint8_t* sc = scales;
+          if (a.batch > 1) {
+            const int64_t b = r / a.rows;
+            rr = r - b * a.rows;
+            sc += b * st.row_atoms * st.block_atoms * ATOM_BYTES;
+          }
+          *reinterpret_cast<uint32_t*>(sc + scale_word(st, rr, ba)) = word;
+        }
       }
     }
   }
@@ -170,7 +220,7 @@ __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a,
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int at = threadIdx.x + 256 * i;
-        T e[W];
+        alignas(16) T e[W];
         *reinterpret_cast<uint4*>(e) = u[i];
 #pragma unroll
         for (int j = 0; j < W; ++j) tile[t_index(at / PER_ROW, at % PER_ROW * W + j)] = to_f32<T>(e[j]);
@@ -220,47 +270,59 @@ __device__ __forceinline__ float e2m1(uint32_t c) {
   return __uint_as_float(bits | ((c & 8u) << 28));
 }
 
-// The row quantiser's mapping; U rows' loads in flight together.
+// The row quantiser's mapping.
 template <typename T, int U>
 __global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t* __restrict__ q, const Store st,
                                                     T* __restrict__ out, const RowMap map,
                                                     const bool vec) {
   ptx::griddep_wait();
   ptx::griddep_launch();
-  const int l16 = threadIdx.x & 15;
-  const int64_t all_rows = st.batch * st.rows;
-  for (int64_t ba = ((int64_t)blockIdx.y << map.chunk_shift) +
-                    ((threadIdx.x >> 4) & ((1 << map.chunk_shift) - 1));
-       ba < map.chunks; ba += (int64_t)gridDim.y << map.chunk_shift) {
-    const int64_t blk = ba * ATOM_BLOCKS + (l16 >> 2), col = ba * 128 + l16 * 8;
+  const int l8 = threadIdx.x & 7, group = threadIdx.x >> 3, cs = map.chunk_shift;
+  const int64_t all_rows = st.batch * st.rows, step = 1 << (GROUPS_SHIFT - cs);
+  const int64_t row0 = (int64_t)blockIdx.x * (step * U) + (group >> cs);
+  const int chunk = group & ((1 << cs) - 1);
+  for (int64_t y = blockIdx.y; (y << cs) < map.chunks; y += gridDim.y) {
+    const int64_t ba = (y << cs) + chunk, col = ba * 128 + l8 * 16;
+    const int64_t blk = ba * ATOM_BLOCKS + (l8 >> 1);
     if (col >= st.cols) continue;
-    uint32_t code[U];
+    uint2 code[U];
     uint8_t sb[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t r = map_row<U>(map, u);
+      const int64_t r = row0 + u * step;
       if (r >= all_rows) continue;
-      int64_t b, rr;
-      split_row(r, st.rows, st.batch, b, rr);
-      code[u] = __ldg(reinterpret_cast<const uint32_t*>(q + r * st.pitch + blk * 16 + (l16 & 3) * 4));
-      sb[u] = __ldg(q + st.scales_off + b * st.row_atoms * st.block_atoms * ATOM_BYTES +
-                    scale_word(st, rr, ba) + (l16 >> 2));
+      int64_t rr = r;
+      const uint8_t* sc = q + st.scales_off;
+      if (st.batch > 1) {
+        const int64_t b = r / st.rows;
+        rr = r - b * st.rows;
+        sc += b * st.row_atoms * st.block_atoms * ATOM_BYTES;
+      }
+      code[u] = __ldg(reinterpret_cast<const uint2*>(q + r * st.pitch + blk * 16 + (l8 & 1) * 8));
+      sb[u] = __ldg(sc + scale_word(st, rr, ba) + (l8 >> 1));
     }
+    const int n = (int)(st.cols - col > 16 ? 16 : st.cols - col);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t r = map_row<U>(map, u);
+      const int64_t r = row0 + u * step;
       if (r >= all_rows) continue;
       const float s = scale_down(sb[u]);
+      T* o = out + r * st.cols + col;
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = e2m1(code[u] >> (4 * j)) * s;
-      store8<T>(out + r * st.cols + col, (int)(st.cols - col > 8 ? 8 : st.cols - col), vec, v);
+      for (int j = 0; j < 8; ++j) v[j] = e2m1(code[u].x >> (4 * j)) * s;
+      store8<T>(o, n, vec, v);
+      if (n > 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = e2m1(code[u].y >> (4 * j)) * s;
+        store8<T>(o + 8, n - 8, vec, v);
+      }
     }
   }
 }
 
 // Grid of the row kernels: chunks of 128 columns on y, rows on x, U rows per
-// half-warp when that still leaves four CTAs for every SM.
+// group when that still leaves four CTAs for every SM.
 struct RowGrid {
   RowMap map;
   dim3 grid;
@@ -270,9 +332,9 @@ RowGrid row_grid(int64_t rows, int64_t chunks) {
   RowGrid g;
   g.map.chunks = chunks;
   g.map.chunk_shift = 0;
-  while (g.map.chunk_shift < 4 && (1 << g.map.chunk_shift) < chunks) ++g.map.chunk_shift;
+  while (g.map.chunk_shift < GROUPS_SHIFT && (1 << g.map.chunk_shift) < chunks) ++g.map.chunk_shift;
   const int64_t y = ceil_div(chunks, 1 << g.map.chunk_shift);
-  const int64_t per = 1 << (4 - g.map.chunk_shift);  // rows of a CTA at U == 1
+  const int64_t per = 1 << (GROUPS_SHIFT - g.map.chunk_shift);  // rows of a CTA at U == 1
   g.many = ceil_div(rows, per * 4) * y >= 4 * (int64_t)device_sm_count();
   g.grid = dim3((unsigned)ceil_div(rows, per * (g.many ? 4 : 1)), (unsigned)(y < 65535 ? y : 65535));
   return g;

@@ -348,7 +348,8 @@ int64_t moe_layout_size(int64_t T, int64_t k, int64_t E) {
   if (T < 0 || T > kMaxDim || E < 1 || E > kMaxExperts || k < 1 || k > kMaxChosen ||
       T * k > kMaxDim - 1)
     return 0;
-  return 2 * E + 3 + 2 * T * k;
+  const int64_t n = T * k, ctas = layout_ctas(n);
+  return 2 * E + 3 + 2 * n + (ctas > 1 ? ctas * (E + 1) : 0);
 }
 
 int moe_layout(const int32_t* experts, int64_t T, int64_t k, int64_t E, int32_t* layout,
@@ -363,7 +364,7 @@ int moe_layout(const int32_t* experts, int64_t T, int64_t k, int64_t E, int32_t*
   if (dev != IMC_OK) return dev;
   int32_t *offsets = layout, *starts = offsets + E + 2, *order = starts + E + 1, *dest = order + n;
   return finish_call(launch_layout(experts, (int)n, (int)E, offsets, starts, order, dest,
-                                   (cudaStream_t)stream),
+                                   dest + n, (cudaStream_t)stream),
                      IMC_KERNEL_EXPERTS);
 }
 

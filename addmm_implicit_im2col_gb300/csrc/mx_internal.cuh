@@ -112,7 +112,7 @@ __device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]
 #pragma unroll
     for (int j = 0; j < 8 / W; ++j) {
       const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + j);
-      T t[W];
+      alignas(16) T t[W];
       *reinterpret_cast<uint4*>(t) = u;
 #pragma unroll
       for (int i = 0; i < W; ++i) v[j * W + i] = to_f32<T>(t[i]);
@@ -128,7 +128,7 @@ __device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&v)[8
     constexpr int W = 16 / (int)sizeof(T);
 #pragma unroll
     for (int j = 0; j < 8 / W; ++j) {
-      T t[W];
+      alignas(16) T t[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) t[i] = from_f32<T>(v[j * W + i]);
       reinterpret_cast<uint4*>(p)[j] = *reinterpret_cast<const uint4*>(t);
@@ -165,8 +165,12 @@ cudaError_t launch_route(const RouteArgs& a, int dtype, cudaStream_t s);
 // grad_logits [T,E] of the weights' gradient g [T,k] (a.experts is an input).
 cudaError_t launch_route_backward(const RouteArgs& a, int dtype, const float* g, void* grad_logits,
                                   cudaStream_t s);
+// `counts`: scratch of layout_ctas(n) * (E + 1) words when that is more than
+// one CTA.
+constexpr int kLayoutMaxCtas = 128;
+int layout_ctas(int64_t n);
 cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets, int32_t* starts,
-                          int32_t* order, int32_t* dest, cudaStream_t s);
+                          int32_t* order, int32_t* dest, int32_t* counts, cudaStream_t s);
 cudaError_t launch_combine(const void* y, const float* w, int dtype, int64_t T, int k, int64_t N,
                            void* out, cudaStream_t s);
 cudaError_t launch_combine_backward(const void* grad, const void* y, const float* w, int dtype,

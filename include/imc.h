@@ -460,7 +460,8 @@ int moe_route_backward(const float* grad_weights, const void* logits, int dtype,
  *   starts  [E+1]  row at which expert e's run starts when every run is filled up
  *                  to a multiple of 128 rows
  *   order   [T*k]  the slots, by expert, in slot order within one
- *   dest    [T*k]  a slot's row among the filled-up runs, -1 without an expert */
+ *   dest    [T*k]  a slot's row among the filled-up runs, -1 without an expert
+ * and, for many slots, counts that the call itself needs. */
 int64_t moe_layout_size(int64_t T, int64_t k, int64_t E);
 int moe_layout(const int32_t* experts, int64_t T, int64_t k, int64_t E, int32_t* layout,
                void* stream);

@@ -226,7 +226,7 @@ def test_layout(T, k, E):
     assert np.array_equal(got.order.cpu().numpy(), order)
     starts = np.concatenate([[0], (-(-counts[:E] // 128) * 128).cumsum()])
     assert np.array_equal(data[E + 2: 2 * E + 3], starts)
-    dest = data[2 * E + 3 + T * k:]
+    dest = data[2 * E + 3 + T * k: 2 * E + 3 + 2 * T * k]
     key = np.where((experts.reshape(-1) >= 0) & (experts.reshape(-1) < E), experts.reshape(-1), E)
     place = np.empty(T * k, dtype=np.int64)
     place[order] = np.arange(T * k)
