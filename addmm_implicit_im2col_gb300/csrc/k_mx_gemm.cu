@@ -160,7 +160,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::STAGES * F::STAGE);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Known to be the same for a warp's lanes: what follows from it stays in
+  // uniform registers, where the tcgen05 and TMA instructions want their operands.
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
   const int unit = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
   const int units = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
@@ -220,9 +222,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   if (PAIR) ptx::cluster_sync();  // the peer's barriers are ready
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   volatile int* abort = &ctl->abort;
-  const int num_tiles = EXPERTS ? ctl->tiles_before[p.E + 1] : num_m * num_n;
+  const int num_tiles =
+      EXPERTS ? __shfl_sync(0xffffffffu, ctl->tiles_before[p.E + 1], 0) : num_m * num_n;
 
   auto tile_of = [&](int t) {
     Tile r;
@@ -255,63 +258,81 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      // after a pre-pass of this call the weight is known to be there
-      if (!EXPERTS && !p.inputs_ready) ptx::griddep_wait();
-      bool tokens_ready = EXPERTS || !p.inputs_ready;
-      int s = 0, issued = 0;
-      uint32_t ph = 0;
-      for (int t = unit; t < num_tiles && !*abort; t += units) {
-        const Tile r = tile_of(t);
-        if (EXPERTS && r.e == p.E) break;  // only tiles of no expert follow
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_any<PAIR>(&ctl->empty[s], ph ^ 1u, abort, tc::kSiteProducerEmpty, wd)) break;
-          uint8_t* st = smem + s * F::STAGE;
-          uint8_t* sf = st + A_BYTES + F::B_BYTES;
+    // The whole warp walks the loop and one elected lane issues: a loop inside
+    // `if (lane == 0)` has its descriptors and coordinates moved to uniform
+    // registers one by one before every instruction (measured in the MMA warp:
+    // 690 against the 512 cycles that the MMAs of a stage take).
+    // After a pre-pass of this call the weight is known to be there.
+    if (!EXPERTS && !p.inputs_ready) ptx::griddep_wait();
+    bool tokens_ready = EXPERTS || !p.inputs_ready;
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    for (int t = unit; t < num_tiles && !*abort; t += units) {
+      const Tile r = tile_of(t);
+      if (EXPERTS && r.e == p.E) break;  // only tiles of no expert follow
+      const int xa = r.m0 / F::ATOM_TOKENS;
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!wait_any<PAIR>(&ctl->empty[s], ph ^ 1u, abort, tc::kSiteProducerEmpty, wd)) break;
+        __syncwarp();
+        uint8_t* st = smem + s * F::STAGE;
+        uint8_t* sf = st + A_BYTES + F::B_BYTES;
+        if (ptx::elect_one()) {
           if (rank == 0) ptx::mbar_arrive_expect_tx(&ctl->full[s], F::TX);
-          const int xa = r.m0 / F::ATOM_TOKENS;
           if (PAIR) {
             const uint32_t bar = ptx::cluster_addr(&ctl->full[s], 0);
             ptx::tma_load_3d_pair(st, &tmW, bar, kb * (KB / 2), r.n0, r.e);
             ptx::tma_load_3d_pair(sf, &tmWs, bar, kb * KB, r.n0 / BM, r.e);
-            if (!tokens_ready) ptx::griddep_wait();
-            ptx::tma_load_2d_pair(st + A_BYTES, &tmX, bar, kb * (KB / 2),
-                                  r.m0 + rank * F::B_ROWS);
-            ptx::tma_load_2d_pair(sf + F::SA_BYTES, &tmXs, bar, kb * KB, xa);
           } else {
             ptx::tma_load_3d(st, &tmW, &ctl->full[s], kb * (KB / 2), r.n0, r.e);
             ptx::tma_load_3d(sf, &tmWs, &ctl->full[s], kb * KB, r.n0 / BM, r.e);
-            if (!tokens_ready) ptx::griddep_wait();
+          }
+        }
+        if (!tokens_ready) ptx::griddep_wait();
+        tokens_ready = true;
+        if (ptx::elect_one()) {
+          if (PAIR) {
+            const uint32_t bar = ptx::cluster_addr(&ctl->full[s], 0);
+            ptx::tma_load_2d_pair(st + A_BYTES, &tmX, bar, kb * (KB / 2), r.m0 + rank * F::B_ROWS);
+            ptx::tma_load_2d_pair(sf + F::SA_BYTES, &tmXs, bar, kb * KB, xa);
+          } else {
             ptx::tma_load_2d(st + A_BYTES, &tmX, &ctl->full[s], kb * (KB / 2), r.m0);
             ptx::tma_load_2d(sf + F::SA_BYTES, &tmXs, &ctl->full[s], kb * KB, xa);
           }
-          tokens_ready = true;
-          ++issued;
-          if (++s == F::STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == F::STAGES) {
+          s = 0;
+          ph ^= 1u;
         }
       }
-      // Every copy issued must have landed before the CTA's shared memory is
-      // released (a pair's copies count on CTA 0's barriers, and both CTAs meet
-      // at the end), and so must every signal the MMAs send to a pair's barriers.
-      for (int j = (issued > F::STAGES ? issued - F::STAGES : 0); j < issued; ++j) {
-        const uint32_t parity = (uint32_t)((j / F::STAGES) & 1);
-        if (rank == 0) tc::drain_wait(&ctl->full[j % F::STAGES], parity);
-        if (PAIR) tc::drain_wait(&ctl->empty[j % F::STAGES], parity);
-      }
+    }
+    // Every copy issued must have landed before the CTA's shared memory is
+    // released (a pair's copies count on CTA 0's barriers, and both CTAs meet
+    // at the end), and so must every signal the MMAs send to a pair's barriers.
+    for (int j = (issued > F::STAGES ? issued - F::STAGES : 0); j < issued; ++j) {
+      const uint32_t parity = (uint32_t)((j / F::STAGES) & 1);
+      if (rank == 0) tc::drain_wait(&ctl->full[j % F::STAGES], parity);
+      if (PAIR) tc::drain_wait(&ctl->empty[j % F::STAGES], parity);
     }
     __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t id0 = ptx::idesc_mxf4(F::BNW, BN, 0), id1 = ptx::idesc_mxf4(F::BNW, BN, 2);
+      // Descriptors of stage 0 (their low bits hold the shared address >> 4, so
+      // a stage, a k-step and a scale atom are plain sums).
+      const uint32_t base = ptx::smem_addr(smem);
+      const uint64_t da0 = ptx::smem_desc(base, 16, 1024, ptx::kSwizzle128B);
+      const uint64_t db0 = ptx::smem_desc(base + A_BYTES, 16, 1024, ptx::kSwizzle128B);
+      const uint64_t ds0 = ptx::smem_desc(base + A_BYTES + F::B_BYTES, 16, 128, 0);
       const int num_ks = (int)((p.K + KSTEP - 1) / KSTEP);
-      int s = 0, tl = 0, block = 0;
-      uint32_t ph = 0;
+      int s = 0, tl = 0, set = 0;
+      int old = 0;             // the stage whose block had this block's scale columns
+      uint32_t ph = 0, old_ph = 0;
+      int block = 0;
       for (int t = unit; t < num_tiles; t += units, ++tl) {
-        if (EXPERTS && tile_of(t).e == p.E) break;
+        if (EXPERTS && t >= ctl->tiles_before[p.E]) break;
         const int buf = tl & 1;
         // the accumulator is free: the tile two before (a pair: the part shared
         // with the tile before) has been read
@@ -328,48 +349,60 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = wait_any<PAIR>(&ctl->full[s], ph, abort, tc::kSiteMmaOperands, wd);
           // the scale columns are free: the MMAs of the block that had them are done
           if (F::SETS < F::STAGES && ok && block >= F::SETS) {
-            const int b = block - F::SETS;
-            ok = wait_any<PAIR>(&ctl->empty[b % F::STAGES], (uint32_t)(b / F::STAGES) & 1u, abort,
-                                tc::kSiteMmaOperands, wd);
+            ok = wait_any<PAIR>(&ctl->empty[old], old_ph, abort, tc::kSiteMmaOperands, wd);
+            if (++old == F::STAGES) {
+              old = 0;
+              old_ph ^= 1u;
+            }
           }
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t base = ptx::smem_addr(smem + s * F::STAGE);
-          const uint64_t da = ptx::smem_desc(base, 16, 1024, ptx::kSwizzle128B);
-          const uint64_t db = ptx::smem_desc(base + A_BYTES, 16, 1024, ptx::kSwizzle128B);
-          const uint64_t ds = ptx::smem_desc(base + A_BYTES + F::B_BYTES, 16, 128, 0);
-          const uint32_t sfa = tmem + (uint32_t)(F::SF_COL0 + block % F::SETS * F::SF_COLS),
-                         sfb = sfa + 8;
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {  // block atoms of the stage
-            ptx::tmem_cp_scales<PAIR>(sfa + a * 4, ds + (uint64_t)(a * ATOM_BYTES >> 4));
-#pragma unroll
-            for (int b = 0; b < F::B_ATOMS; ++b)
-              ptx::tmem_cp_scales<PAIR>(
-                  sfb + a * 4 * F::B_ATOMS + b * 4,
-                  ds + (uint64_t)((F::SA_BYTES + (2 * b + a) * ATOM_BYTES) >> 4));
-          }
+          __syncwarp();
+          const uint64_t off = (uint64_t)(uint32_t)(s * (F::STAGE >> 4));
+          const uint64_t da = da0 + off, db = db0 + off, ds = ds0 + off;
+          const uint32_t sfa = tmem + (uint32_t)(F::SF_COL0 + set * F::SF_COLS), sfb = sfa + 8;
           const int steps = min(4, num_ks - 4 * kb);
+          if (ptx::elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j < steps)
-              ptx::mma_mxf4<PAIR>(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0,
-                                  sfa + (j >> 1) * 4, sfb + (j >> 1) * 4 * F::B_ATOMS,
-                                  kb + j > 0 ? 1u : 0u);
+            for (int a = 0; a < 2; ++a) {  // block atoms of the stage
+              ptx::tmem_cp_scales<PAIR>(sfa + a * 4, ds + (uint64_t)(a * ATOM_BYTES >> 4));
+#pragma unroll
+              for (int b = 0; b < F::B_ATOMS; ++b)
+                ptx::tmem_cp_scales<PAIR>(
+                    sfb + a * 4 * F::B_ATOMS + b * 4,
+                    ds + (uint64_t)((F::SA_BYTES + (2 * b + a) * ATOM_BYTES) >> 4));
+            }
+            if (steps == 4) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                ptx::mma_mxf4<PAIR>(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0,
+                                    sfa + (j >> 1) * 4, sfb + (j >> 1) * 4 * F::B_ATOMS,
+                                    kb + j > 0 ? 1u : 0u);
+            } else {  // the last block of a K that is no multiple of 256
+#pragma unroll
+              for (int j = 0; j < 3; ++j)
+                if (j < steps)
+                  ptx::mma_mxf4<PAIR>(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0,
+                                      sfa + (j >> 1) * 4, sfb + (j >> 1) * 4 * F::B_ATOMS,
+                                      kb + j > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit_g<PAIR>(&ctl->empty[s]);
+            if (kb == num_kb - 1) ptx::mma_commit_g<PAIR>(&ctl->accf[buf]);
           }
-          ptx::mma_commit_g<PAIR>(&ctl->empty[s]);
+          __syncwarp();
+          if (++set == F::SETS) set = 0;
           if (++s == F::STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
         if (!ok) break;
-        ptx::mma_commit_g<PAIR>(&ctl->accf[buf]);
       }
       // Every MMA issued must be done before TMEM is released.
-      ptx::mma_commit_g<PAIR>(&ctl->drain);
+      __syncwarp();
+      if (ptx::elect_one()) ptx::mma_commit_g<PAIR>(&ctl->drain);
     }
-    if (lane == 0) tc::drain_wait(&ctl->drain, 0);
+    tc::drain_wait(&ctl->drain, 0);
     __syncwarp();
   } else {
     // ----------------------------------------------------------- epilogue
