@@ -86,6 +86,30 @@ __device__ __forceinline__ void best_two(uint32_t& a1, uint32_t& a2, uint32_t b1
   a1 = max(a1, b1);
 }
 
+// The k rounds of a choice among 32 * R keys (lane l: keys l, l + 32, ...): the
+// highest key of the warp, the lowest index that has it; lane i gets the i-th.
+template <int R, int V>
+__device__ __forceinline__ int choose(uint32_t (&key)[V], int k) {
+  const int lane = threadIdx.x & 31;
+  int id = 0;
+  for (int i = 0; i < k; ++i) {
+    uint32_t best = key[0], at = lane;
+#pragma unroll
+    for (int j = 1; j < R; ++j)
+      if (key[j] > best) {
+        best = key[j];
+        at = lane + 32 * j;
+      }
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    const uint32_t e = __reduce_min_sync(kAll, best == top ? at : 0x7FFFFFFFu);
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      if (e == (uint32_t)(lane + 32 * j)) key[j] = 0;
+    if (lane == i) id = (int)e;
+  }
+  return id;
+}
+
 // One warp per token.  Scores and keys stay in registers (VPT per lane) for the
 // k rounds of the choice: the highest key of each lane, the highest of the warp
 // (redux), and the lowest index that has it (redux).  The chosen scores are
@@ -107,6 +131,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     key[j] = e < a.E ? ordered(a.bias ? s[j] + __ldg(a.bias + e) : s[j]) : 0u;
   }
   uint32_t* words = sm_words + warp * padded(a.E);
+  __shared__ int groups[kRouteWarps][32];  // the groups that stay, in order
+  const int size = a.E / a.groups;
+  uint32_t inv = 0;
+  int vpt = VPT;  // keys of a lane that the rounds look at
+  auto expert_of = [&](int c) {
+    if (a.groups == 1) return c;
+    const int g = (int)((c * inv) >> 20);
+    return groups[warp][g] * size + c - g * size;
+  };
   if (a.groups > 1) {
     // The sum of each group's two best; the best top_groups groups stay.
     // 2^ls lanes share a group.
@@ -114,7 +147,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     for (int j = 0; j < VPT; ++j)
       if (lane + 32 * j < a.E) words[padded(lane + 32 * j)] = key[j];
     __syncwarp();
-    const int size = a.E / a.groups;
     int ls = 0;
     while ((a.groups << (ls + 1)) <= 32) ++ls;
     const int g = lane >> ls;
@@ -136,33 +168,26 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
       kept |= 1u << at;
       if (g == at) gkey = 0;
     }
-    // e / size by a product: exact for e * (size - 1) < 2^20
-    const uint32_t inv = ((1u << 20) + size - 1) / size;
+    // The rounds run over the candidates only: candidate c is the c-th expert of
+    // the groups that stay.  c / size by a product, exact for c * (size - 1) < 2^20.
+    inv = ((1u << 20) + size - 1) / size;
+    vpt = (a.top_groups * size + 31) >> 5;
+    if ((kept >> lane) & 1u) groups[warp][__popc(kept & ((1u << lane) - 1u))] = lane;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (!((kept >> (((lane + 32 * j) * inv) >> 20)) & 1u)) key[j] = 0;
+    for (int j = 0; j < VPT; ++j) {
+      if (j >= vpt) break;
+      const int c = lane + 32 * j;
+      key[j] = c < a.top_groups * size ? words[padded(expert_of(c))] : 0u;
+    }
     __syncwarp();
   }
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
     if (lane + 32 * j < a.E) words[padded(lane + 32 * j)] = __float_as_uint(s[j]);
   __syncwarp();
-  int id = 0;
-  for (int i = 0; i < a.k; ++i) {
-    uint32_t best = key[0], at = lane;
-#pragma unroll
-    for (int j = 1; j < VPT; ++j)
-      if (key[j] > best) {
-        best = key[j];
-        at = lane + 32 * j;
-      }
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    const uint32_t e = __reduce_min_sync(kAll, best == top ? at : 0x7FFFFFFFu);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (e == (uint32_t)(lane + 32 * j)) key[j] = 0;
-    if (lane == i) id = (int)e;
-  }
+  int id = vpt * 2 <= VPT ? choose<(VPT + 1) / 2>(key, a.k) : choose<VPT>(key, a.k);
+  id = expert_of(id);
   float w = lane < a.k ? __uint_as_float(words[padded(id)]) : 0.0f;
   if (a.renorm) {
     const float total = warp_sum(w);
@@ -417,7 +442,7 @@ __global__ void __launch_bounds__(kLayoutThreads) k_layout_place(const LayoutArg
   ptx::griddep_launch();
   layout_scan(a, blockIdx.x == 0, first, shift, [&](int e) {
     int all = 0, low = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int c = 0; c < (int)gridDim.x; ++c) {
       const int v = __ldg(a.counts + (int64_t)c * B + e);
       all += v;

@@ -30,6 +30,11 @@
 // accumulators of 256 columns overlap in 64 of them, which leaves room for the
 // scales: the epilogue drains the shared columns first and hands them back.
 //
+// Few tokens and a long K: the sum over K is split over a cluster of S <= 8 CTAs.
+// Each takes a run of K, writes its partial tile to the others' shared memory
+// (CTA r sums rows r * 128 / S .. of n) and the sums are taken in the order of
+// the CTAs, so a result does not depend on timing (the rule: pick_splits).
+//
 // Persistent CTAs walk the tiles.  In the experts' form a tile is (expert, rows
 // of that expert, n); the row counts are only known on the GPU, so every CTA
 // sums them up at its start.
@@ -78,19 +83,21 @@ struct Form {
 constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
 
 struct Ctl {
-  uint64_t full[8], empty[8], accf[2], acce[2], drain;
+  uint64_t full[8], empty[8], accf[2], acce[2], drain, part;
   uint32_t tmem_base;
   int abort;
   // experts' form: tiles of the experts before e, first slot and first row of e
   int tiles_before[MAX_EXPERTS + 2], offset[MAX_EXPERTS + 2], start[MAX_EXPERTS + 1];
 };
 
-template <int BN>
+// SPLIT: room for the cluster's partial sums.
+template <int BN, bool SPLIT>
 constexpr int smem_bytes() {
-  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + (int)sizeof(Ctl);
+  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + (SPLIT ? BN * BM * 4 : 0) + (int)sizeof(Ctl);
 }
-static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448 &&
-                  smem_bytes<64>() <= 232448 && smem_bytes<32>() <= 232448,
+static_assert(smem_bytes<256, false>() <= 232448 && smem_bytes<128, false>() <= 232448 &&
+                  smem_bytes<64, false>() <= 232448 && smem_bytes<32, false>() <= 232448 &&
+                  smem_bytes<32, true>() <= 232448,
               "shared memory");
 
 // One tile: n rows n0.. of expert e's weight (this CTA's 128), token rows m0..
@@ -150,27 +157,36 @@ __device__ __forceinline__ void store_tokens(O* out, int64_t N, int slot, int li
   }
 }
 
-template <int BN, bool EXPERTS>
+template <int BN, bool EXPERTS, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     k_mx_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
-              const ProductArgs p, const int num_m, const int num_n, const int group) {
+              const ProductArgs p, const int num_m, const int num_n, const int group,
+              const int log_splits) {
   using F = Form<BN>;
   constexpr bool PAIR = F::PAIR;
+  constexpr int STAGES = F::STAGES;
+  const int splits = SPLIT ? 1 << log_splits : 1;
+  static_assert(!SPLIT || (!PAIR && !EXPERTS), "split form");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + F::STAGES * F::STAGE);
+  float* part = reinterpret_cast<float*>(smem + STAGES * F::STAGE);  // SPLIT: [src][token][128 / S]
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * F::STAGE + (SPLIT ? BN * BM * 4 : 0));
   // Known to be the same for a warp's lanes: what follows from it stays in
   // uniform registers, where the tcgen05 and TMA instructions want their operands.
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = PAIR ? (int)ptx::cluster_rank() : 0;
-  const int unit = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
-  const int units = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
-  const int num_kb = (int)((p.K + KB - 1) / KB);
+  const int slice = SPLIT ? (int)ptx::cluster_rank() : 0;
+  const int unit = PAIR ? (int)blockIdx.x >> 1 : (SPLIT ? (int)blockIdx.x >> log_splits : (int)blockIdx.x);
+  const int units = PAIR ? (int)gridDim.x >> 1 : (SPLIT ? (int)gridDim.x >> log_splits : (int)gridDim.x);
+  // this CTA's blocks of K
+  const int all_kb = (int)((p.K + KB - 1) / KB);
+  const int kb0 = SPLIT ? (int)(((int64_t)all_kb * slice) >> log_splits) : 0;
+  const int num_kb = SPLIT ? (int)(((int64_t)all_kb * (slice + 1)) >> log_splits) : all_kb;
   int* wd = &g_watchdog_mx;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < F::STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       ptx::mbar_init(&ctl->full[s], 1);
       ptx::mbar_init(&ctl->empty[s], 1);
     }
@@ -179,6 +195,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       ptx::mbar_init(&ctl->acce[b], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
     }
     ptx::mbar_init(&ctl->drain, 1);
+    if (SPLIT) ptx::mbar_init(&ctl->part, (uint32_t)(splits * EPI_WARPS));
     ctl->abort = 0;
     ptx::fence_mbar_init();
   }
@@ -220,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (PAIR) ptx::cluster_sync();  // the peer's barriers are ready
+  if (PAIR || SPLIT) ptx::cluster_sync();  // the other CTAs' barriers are ready
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   volatile int* abort = &ctl->abort;
@@ -271,7 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Tile r = tile_of(t);
       if (EXPERTS && r.e == p.E) break;  // only tiles of no expert follow
       const int xa = r.m0 / F::ATOM_TOKENS;
-      for (int kb = 0; kb < num_kb; ++kb) {
+      for (int kb = kb0; kb < num_kb; ++kb) {
         if (!wait_any<PAIR>(&ctl->empty[s], ph ^ 1u, abort, tc::kSiteProducerEmpty, wd)) break;
         __syncwarp();
         uint8_t* st = smem + s * F::STAGE;
@@ -301,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
         ++issued;
-        if (++s == F::STAGES) {
+        if (++s == STAGES) {
           s = 0;
           ph ^= 1u;
         }
@@ -310,10 +327,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Every copy issued must have landed before the CTA's shared memory is
     // released (a pair's copies count on CTA 0's barriers, and both CTAs meet
     // at the end), and so must every signal the MMAs send to a pair's barriers.
-    for (int j = (issued > F::STAGES ? issued - F::STAGES : 0); j < issued; ++j) {
-      const uint32_t parity = (uint32_t)((j / F::STAGES) & 1);
-      if (rank == 0) tc::drain_wait(&ctl->full[j % F::STAGES], parity);
-      if (PAIR) tc::drain_wait(&ctl->empty[j % F::STAGES], parity);
+    for (int j = (issued > STAGES ? issued - STAGES : 0); j < issued; ++j) {
+      const uint32_t parity = (uint32_t)((j / STAGES) & 1);
+      if (rank == 0) tc::drain_wait(&ctl->full[j % STAGES], parity);
+      if (PAIR) tc::drain_wait(&ctl->empty[j % STAGES], parity);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -345,12 +362,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         ptx::tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf * F::ACC1);
         bool ok = true;
-        for (int kb = 0; kb < num_kb; ++kb, ++block) {
+        for (int kb = kb0; kb < num_kb; ++kb, ++block) {
           ok = wait_any<PAIR>(&ctl->full[s], ph, abort, tc::kSiteMmaOperands, wd);
           // the scale columns are free: the MMAs of the block that had them are done
-          if (F::SETS < F::STAGES && ok && block >= F::SETS) {
+          if (F::SETS < STAGES && ok && block >= F::SETS) {
             ok = wait_any<PAIR>(&ctl->empty[old], old_ph, abort, tc::kSiteMmaOperands, wd);
-            if (++old == F::STAGES) {
+            if (++old == STAGES) {
               old = 0;
               old_ph ^= 1u;
             }
@@ -377,21 +394,21 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int j = 0; j < 4; ++j)
                 ptx::mma_mxf4<PAIR>(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0,
                                     sfa + (j >> 1) * 4, sfb + (j >> 1) * 4 * F::B_ATOMS,
-                                    kb + j > 0 ? 1u : 0u);
+                                    kb + j > kb0 ? 1u : 0u);
             } else {  // the last block of a K that is no multiple of 256
 #pragma unroll
               for (int j = 0; j < 3; ++j)
                 if (j < steps)
                   ptx::mma_mxf4<PAIR>(d, da + 2 * j, db + 2 * j, (j & 1) ? id1 : id0,
                                       sfa + (j >> 1) * 4, sfb + (j >> 1) * 4 * F::B_ATOMS,
-                                      kb + j > 0 ? 1u : 0u);
+                                      kb + j > kb0 ? 1u : 0u);
             }
             ptx::mma_commit_g<PAIR>(&ctl->empty[s]);
             if (kb == num_kb - 1) ptx::mma_commit_g<PAIR>(&ctl->accf[buf]);
           }
           __syncwarp();
           if (++set == F::SETS) set = 0;
-          if (++s == F::STAGES) {
+          if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
           }
@@ -456,6 +473,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         if (live <= 0 || c >= BN) continue;
+        if (SPLIT) {  // to the CTA that sums this row of n
+          const int nl = (q * 32 + lane) & ((BM >> log_splits) - 1);
+          uint32_t to = ptx::cluster_addr(part + (((slice * BN + c) << 7) >> log_splits) + nl,
+                                          (uint32_t)((q * 32 + lane) >> (7 - log_splits)));
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j < live) ptx::st_cluster(to, v[j]);
+            to += (uint32_t)(BM * 4) >> log_splits;
+          }
+          continue;
+        }
         if (!none) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -475,12 +503,35 @@ __global__ void __launch_bounds__(THREADS, 1)
           store_tokens<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, slot, live, in, v,
                                 [](uint32_t b) { return half_bits(__uint_as_float(b)); });
       }
+      if (SPLIT) {
+        __syncwarp();
+        if (lane == 0)
+          for (int r2 = 0; r2 < splits; ++r2)
+            ptx::mbar_arrive_cluster(ptx::cluster_addr(&ctl->part, (uint32_t)r2));
+        if (!wait_any<true>(&ctl->part, 0, abort, tc::kSiteEpilogueAccFull, wd)) break;
+        // row x >> lp, column x & (per - 1) of this CTA's share
+        const int lp = 7 - log_splits, live = r.rows << lp;
+#pragma unroll 4
+        for (int x = (int)threadIdx.x - 64; x < live; x += 32 * EPI_WARPS) {
+          const int64_t nn = r.n0 + (slice << lp) + (x & ((1 << lp) - 1));
+          float y = 0.0f;
+          for (int src = 0; src < splits; ++src) y += part[((src * BN) << lp) + x];
+          if (nn >= p.N) continue;
+          if (p.bias) y += __ldg(p.bias + nn);
+          if (p.relu) y = fmaxf(y, 0.0f);
+          const int64_t at = (int64_t)(r.m0 + (x >> lp)) * p.N + nn;
+          if (p.out_dtype == IMC_F32) static_cast<float*>(p.out)[at] = y;
+          else if (p.out_dtype == IMC_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+          else static_cast<__half*>(p.out)[at] = __float2half_rn(y);
+        }
+        break;  // one tile
+      }
     }
   }
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (PAIR) ptx::cluster_sync();  // neither CTA leaves while the other may signal it
+  if (PAIR || SPLIT) ptx::cluster_sync();  // no CTA leaves while another may signal it
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_g<PAIR>(tmem, 512);
@@ -541,12 +592,12 @@ bool encode_scales(CUtensorMap* m, const uint8_t* q, const Store& st, uint32_t b
 
 constexpr int kMaxDev = 64;
 
-template <int BN, bool EXPERTS>
-cudaError_t run(const ProductArgs& p, cudaStream_t s) {
+template <int BN, bool EXPERTS, bool SPLIT = false>
+cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
   using F = Form<BN>;
-  constexpr int smem = smem_bytes<BN>();
+  constexpr int smem = smem_bytes<BN, SPLIT>();
   static std::atomic<bool> ready[kMaxDev];  // per device: the attribute is set (calls may race)
-  auto k = k_mx_gemm<BN, EXPERTS>;
+  auto k = k_mx_gemm<BN, EXPERTS, SPLIT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -555,7 +606,7 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < kMaxDev) ready[dev].store(true, std::memory_order_release);
   }
-  const int ctas = F::PAIR ? 2 : 1, units = device_sm_count() / ctas;
+  const int ctas = F::PAIR ? 2 : splits, units = device_sm_count() / ctas;
   // a dense product of fewer than 128 rows a tile has one tile of tokens
   const Store sw = store_of(EXPERTS ? p.E : 1, p.N, p.K),
               sx = store_of(1, p.x_rows, p.K,
@@ -569,7 +620,7 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s) {
   const int64_t tiles = EXPERTS ? (p.slots / BN + (p.slots < p.E + 1 ? p.slots : p.E + 1)) *
                                       (int64_t)num_n
                                 : (int64_t)num_m * num_n;
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (tiles > 0x7fffffffLL || (SPLIT && tiles > units)) return cudaErrorInvalidValue;
   const int grid = (int)(tiles < units ? tiles : units) * ctas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -584,8 +635,8 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = F::PAIR ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, k, tw, tx, tws, txs, p, num_m, num_n, 8);
+  cfg.numAttrs = F::PAIR || SPLIT ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, k, tw, tx, tws, txs, p, num_m, num_n, 8, splits == 8 ? 3 : splits / 2);
   note_launch();
   return e;
 }
@@ -605,14 +656,43 @@ int experts_atom_shift(int64_t slots, int64_t E) {
   return t < 7 ? t : 7;
 }
 
+namespace {
+// CTAs that share the K of a tile of at most 32 tokens: as many as find an SM
+// each and at least eight blocks of 256 values.  Measured in a row, weights
+// larger than L2 (us for 1 / 2 / 4 CTAs): 1 x 1024 x 8192 8.1 / 6.9 / 6.0,
+// 1 x 4096 x 16384 15.0 / 11.6 / 10.6, 1 x 4096 x 4096 5.5 / 5.7 / 5.7.  More
+// tokens make the sum of the partial tiles cost more than the split saves (64 x
+// 4096 x 4096 5.6 / 9.5 / 7.5, 128 x 1024 x 8192 9.4 / 15.3 / 10.5).
+int pick_splits(const ProductArgs& p) {
+  const int64_t tiles = ceil_div(p.N, BM), blocks = ceil_div(p.K, KB);
+  const int sms = device_sm_count();
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= sms && blocks >= s * 16) s *= 2;
+  return s;
+}
+}  // namespace
+
 cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
   note_kernel_name(p.E ? "k_mx_gemm<experts>" : "k_mx_gemm");
-  switch (tile_shift(p.E ? ceil_div(p.slots, p.E) : p.M)) {
-    case 5: return p.E ? run<32, true>(p, s) : run<32, false>(p, s);
-    case 6: return p.E ? run<64, true>(p, s) : run<64, false>(p, s);
-    case 7: return p.E ? run<128, true>(p, s) : run<128, false>(p, s);
-    default: return p.E ? run<256, true>(p, s) : run<256, false>(p, s);
+  if (p.E) {
+    switch (tile_shift(ceil_div(p.slots, p.E))) {
+      case 5: return run<32, true>(p, s);
+      case 6: return run<64, true>(p, s);
+      case 7: return run<128, true>(p, s);
+      default: return run<256, true>(p, s);
+    }
   }
+  // Pairs that would leave more than half of the SMs without a tile give way to
+  // single CTAs of 128 x 128.
+  const int64_t pair_tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);
+  const int shift = tile_shift(p.M);
+  if (shift == 5) {
+    const int splits = pick_splits(p);
+    return splits > 1 ? run<32, false, true>(p, s, splits) : run<32, false>(p, s);
+  }
+  if (shift == 6) return run<64, false>(p, s);
+  if (shift == 7 || pair_tiles * 4 <= device_sm_count()) return run<128, false>(p, s);
+  return run<256, false>(p, s);
 }
 
 cudaError_t product_take_watchdog(int* value) {

@@ -227,24 +227,28 @@ int mxfp4_linear_backward(const void* grad, const void* x, const void* w, int dt
   cudaStream_t s = (cudaStream_t)stream;
   Scratch sc(s);
   if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
+  // grad along its rows and, transposed, along its columns: read once for both
   uint8_t* at = static_cast<uint8_t*>(sc.p);
-  cudaError_t e = cudaSuccess;
-  // one product: out[rows, cols] from two operands quantised along `depth`
-  auto product = [&](const void* a, bool at_t, int64_t rows, const void* c, bool c_t, int64_t cols,
-                     int64_t depth, void* out) {
-    ProductArgs p = {};
-    p.x = at;
-    if (e == cudaSuccess)
-      e = launch_quantize(at_t ? quant_args(a, 1, depth, rows, 0, rows, true, at)
-                               : quant_args(a, 1, rows, depth, 0, depth, false, at),
-                          dtype, at_t, s);
+  auto room = [&](int64_t rows, int64_t depth) {
+    uint8_t* q = at;
     at += ceil_div(store_of(1, rows, depth).bytes, 512) * 512;
-    p.w = at;
-    if (e == cudaSuccess)
-      e = launch_quantize(c_t ? quant_args(c, 1, depth, cols, 0, cols, true, at)
-                              : quant_args(c, 1, cols, depth, 0, depth, false, at),
-                          dtype, c_t, s);
-    at += ceil_div(store_of(1, cols, depth).bytes, 512) * 512;
+    return q;
+  };
+  uint8_t *g_rows = room(M, N), *g_cols = room(N, M), *w_cols = room(K, N), *x_cols = room(K, M);
+  cudaError_t e;
+  if (grad_w) {
+    QuantArgs a = quant_args(grad, 1, M, N, 0, N, true, g_cols);
+    a.q_rows = grad_x ? g_rows : nullptr;
+    e = launch_quantize(a, dtype, true, s);
+  } else {
+    e = launch_quantize(quant_args(grad, 1, M, N, 0, N, false, g_rows), dtype, false, s);
+  }
+  // out[rows, cols]: the contraction of two operands quantised along `depth`
+  auto product = [&](const uint8_t* a, int64_t rows, const uint8_t* c, int64_t cols, int64_t depth,
+                     void* out) {
+    ProductArgs p = {};
+    p.x = a;
+    p.w = c;
     p.out = out;
     p.out_dtype = dtype;
     p.M = p.x_rows = rows;
@@ -252,8 +256,16 @@ int mxfp4_linear_backward(const void* grad, const void* x, const void* w, int dt
     p.K = depth;
     if (e == cudaSuccess) e = launch_product(p, s);
   };
-  if (grad_x) product(grad, false, M, w, true, K, N, grad_x);  // grad [M,N] . w [N,K]
-  if (grad_w) product(grad, true, N, x, true, K, M, grad_w);   // grad^T [N,M] . x [M,K]
+  if (grad_x) {  // grad [M,N] . w [N,K]
+    if (e == cudaSuccess)
+      e = launch_quantize(quant_args(w, 1, N, K, 0, K, true, w_cols), dtype, true, s);
+    product(g_rows, M, w_cols, K, N, grad_x);
+  }
+  if (grad_w) {  // grad^T [N,M] . x [M,K]
+    if (e == cudaSuccess)
+      e = launch_quantize(quant_args(x, 1, M, K, 0, K, true, x_cols), dtype, true, s);
+    product(g_cols, N, x_cols, K, M, grad_w);
+  }
   return finish_call(sc.give(e), IMC_KERNEL_MXFP4);
 }
 

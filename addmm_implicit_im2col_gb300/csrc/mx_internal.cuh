@@ -69,6 +69,7 @@ struct QuantArgs {
   Store st;               // its layout (transposed: of [cols, rows])
   const int32_t* dest;    // rows of the result that row r is written to: dest[r*share ..), or null
   int share;
+  uint8_t* q_rows;        // transposed: MXFP4 of x itself as well, or null
 };
 
 // One product: out[token, n] = sum_k x[token, k] * w[n, k] (+ bias[n]) (ReLU).
