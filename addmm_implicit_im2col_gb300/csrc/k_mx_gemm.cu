@@ -16,11 +16,11 @@
 //               (tcgen05.cp), then one MMA per 64 values of K into an fp32
 //               accumulator
 //   warps 2-9   epilogue, two warps per TMEM lane quadrant that take turns by 32
-//               tokens: tcgen05.ld, bias, ReLU, rounding, and one store of 32
-//               consecutive outputs per token straight from the registers (a
-//               staging tile and a bulk copy per token row measured 1.7 times
-//               the time per tile: a warp issues the copies of its lanes one by
-//               one, ~130 cycles each)
+//               tokens: tcgen05.ld, bias, ReLU, rounding, 32 x 32 outputs through
+//               the warp's own shared memory, and 16-byte stores of whole rows
+//               (one bulk copy per token row took 1.7 times the time: a warp
+//               issues the copies of its lanes one by one, ~130 cycles each;
+//               a store of 32 registers per token 2 times in the experts' form)
 //
 // More than 128 tokens run as CTA pairs (cta_group::2): 256 rows of the weight x
 // 256 tokens per pair, each CTA loading its 128 rows and half of the tokens, so
@@ -68,7 +68,7 @@ struct Form {
   static constexpr int ATOM_TOKENS = BN < 128 ? BN : 128;      // token rows of a scale atom
   static constexpr int SA_BYTES = 2 * ATOM_BYTES, SB_BYTES = 2 * ATOM_BYTES * B_ATOMS;
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-  static constexpr int STAGES = BN >= 128 ? 6 : (BN > 32 ? 7 : 8);
+  static constexpr int STAGES = BN >= 128 ? 5 : (BN > 32 ? 6 : 8);
   // TMEM columns: two accumulators (ACC1 apart), then the scales of SETS stages
   static constexpr int SF_COLS = 8 + 8 * B_ATOMS;
   static constexpr int SETS = PAIR ? 2 : STAGES;
@@ -81,6 +81,7 @@ struct Form {
 };
 
 constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+constexpr int ROWS_BYTES = 32 * 32 * 4;  // a warp's 32 tokens x 32 outputs
 
 struct Ctl {
   uint64_t full[8], empty[8], accf[2], acce[2], drain, part;
@@ -90,10 +91,14 @@ struct Ctl {
   int tiles_before[MAX_EXPERTS + 2], offset[MAX_EXPERTS + 2], start[MAX_EXPERTS + 1];
 };
 
-// SPLIT: room for the cluster's partial sums.
+// After the stages: the epilogue warps' rows or (SPLIT) the cluster's partial sums.
+template <int BN, bool SPLIT>
+constexpr int extra_bytes() {
+  return SPLIT ? BN * BM * 4 : EPI_WARPS * ROWS_BYTES;
+}
 template <int BN, bool SPLIT>
 constexpr int smem_bytes() {
-  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + (SPLIT ? BN * BM * 4 : 0) + (int)sizeof(Ctl);
+  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + extra_bytes<BN, SPLIT>() + (int)sizeof(Ctl);
 }
 static_assert(smem_bytes<256, false>() <= 232448 && smem_bytes<128, false>() <= 232448 &&
                   smem_bytes<64, false>() <= 232448 && smem_bytes<32, false>() <= 232448 &&
@@ -134,27 +139,41 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 
 // Stores one output of each of 32 tokens (`live` of them) per lane: token j's is
 // at out[j * N], or in the experts' form at out[slot of lane j * N].  `in`: this
-// lane's column exists.
+// lane's column exists.  For rows that 16-byte stores cannot reach.
 template <bool EXPERTS, typename O, typename Bits>
 __device__ __forceinline__ void store_tokens(O* out, int64_t N, int slot, int live, bool in,
                                              const uint32_t (&v)[32], Bits bits) {
-  if (live == 32) {  // no branch per token
-    O* o = out;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (EXPERTS) o = out + (int64_t)__shfl_sync(0xffffffffu, slot, j) * N;
+  for (int j = 0; j < 32; ++j) {
+    if (j < live) {
+      O* o = out + (EXPERTS ? (int64_t)__shfl_sync(0xffffffffu, slot, j) : (int64_t)j) * N;
       if (in) *o = bits(v[j]);
-      o += N;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j < live) {
-        O* o = out + (EXPERTS ? (int64_t)__shfl_sync(0xffffffffu, slot, j) : (int64_t)j) * N;
-        if (in) *o = bits(v[j]);
-      }
     }
   }
+}
+
+// The same by rows: lane l's outputs (column l of the warp's 32) of the tokens go
+// to `rows` [32][32], and 16 bytes of a row at a time to out, whose column 0 is
+// the warp's; cols of the 32 exist.  N * sizeof(O) and out are multiples of 16.
+template <bool EXPERTS, typename O, typename Bits>
+__device__ __forceinline__ void store_rows(O* out, int64_t N, int slot, int live, int cols,
+                                           const uint32_t (&v)[32], uint8_t* rows, Bits bits) {
+  constexpr int PER_ROW = 32 * (int)sizeof(O) / 16, AT_ONCE = 32 / PER_ROW;  // lanes, rows
+  const int lane = threadIdx.x & 31, r0 = lane / PER_ROW, unit = lane % PER_ROW;
+  O* own = reinterpret_cast<O*>(rows) + lane;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) own[j * 32] = bits(v[j]);
+  __syncwarp();
+  const bool in = unit * (16 / (int)sizeof(O)) < cols;
+#pragma unroll
+  for (int k = 0; k < PER_ROW; ++k) {
+    const int row = k * AT_ONCE + r0;
+    const int64_t to = EXPERTS ? (int64_t)__shfl_sync(0xffffffffu, slot, row) : (int64_t)row;
+    if (in && row < live)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(out + to * N) + unit * 16) =
+          *reinterpret_cast<const uint4*>(rows + row * 32 * (int)sizeof(O) + unit * 16);
+  }
+  __syncwarp();
 }
 
 template <int BN, bool EXPERTS, bool SPLIT>
@@ -162,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     k_mx_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
               const ProductArgs p, const int num_m, const int num_n, const int group,
-              const int log_splits) {
+              const int log_splits, const int wide_rows) {
   using F = Form<BN>;
   constexpr bool PAIR = F::PAIR;
   constexpr int STAGES = F::STAGES;
@@ -171,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
   float* part = reinterpret_cast<float*>(smem + STAGES * F::STAGE);  // SPLIT: [src][token][128 / S]
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * F::STAGE + (SPLIT ? BN * BM * 4 : 0));
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * F::STAGE + extra_bytes<BN, SPLIT>());
   // Known to be the same for a warp's lanes: what follows from it stays in
   // uniform registers, where the tcgen05 and TMA instructions want their operands.
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -435,6 +454,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int64_t n = r.n0 + q * 32 + lane;
       const bool in = n < p.N;
       const float bias = p.bias && in && !none ? __ldg(p.bias + (int64_t)r.e * p.N + n) : 0.0f;
+      // accumulator 0 shares its last columns with 1, which shares its first
+      auto chunk = [&](int i) {
+        return 32 * (PAIR && buf == 0 ? (i + BN / 32 - F::SHARED) % (BN / 32) : i);
+      };
+      // the slots of a chunk's tokens, loaded one chunk ahead
+      auto slots = [&](int i) {
+        const int c = chunk(i) + lane;
+        return EXPERTS && i < BN / 32 && c < r.rows ? __ldg(p.order + r.first + c) : 0;
+      };
+      int slot = slots(turn);
       if (!none) {
         int ok = 1;
         if (lane == 0)
@@ -449,12 +478,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * F::ACC1);
 #pragma unroll 1
       for (int i = turn; i < BN / 32 || i == turn; i += 2) {
-        // accumulator 0 shares its last columns with 1, which shares its first
-        const int c = 32 * (PAIR && buf == 0 ? (i + BN / 32 - F::SHARED) % (BN / 32) : i);
+        const int c = chunk(i);
         const int live = min(32, r.rows - c);  // the same for all lanes
         uint32_t v[32];
-        int slot = 0;
-        if (EXPERTS && lane < live) slot = __ldg(p.order + r.first + c + lane);
+        const int this_slot = slot;
+        slot = slots(i + 2);
         if (live > 0 && !none) {
           ptx::tmem_ld32(tbase + (uint32_t)c, v);
           ptx::tmem_ld_wait();
@@ -492,16 +520,32 @@ __global__ void __launch_bounds__(THREADS, 1)
             v[j] = __float_as_uint(y);
           }
         }
-        const int64_t at = (EXPERTS ? 0 : (int64_t)(r.m0 + c) * p.N) + n;
-        if (p.out_dtype == IMC_F32)
-          store_tokens<EXPERTS>(static_cast<uint32_t*>(p.out) + at, p.N, slot, live, in, v,
-                                [](uint32_t b) { return b; });
-        else if (p.out_dtype == IMC_BF16)
-          store_tokens<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, slot, live, in, v,
-                                [](uint32_t b) { return bf16_bits(__uint_as_float(b)); });
-        else
-          store_tokens<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, slot, live, in, v,
-                                [](uint32_t b) { return half_bits(__uint_as_float(b)); });
+        const int64_t at = (EXPERTS ? 0 : (int64_t)(r.m0 + c) * p.N) + r.n0 + q * 32;
+        auto f32 = [](uint32_t b) { return b; };
+        auto bf16 = [](uint32_t b) { return bf16_bits(__uint_as_float(b)); };
+        auto f16 = [](uint32_t b) { return half_bits(__uint_as_float(b)); };
+        if (wide_rows) {
+          uint8_t* rows = smem + STAGES * F::STAGE + (warp - 2) * ROWS_BYTES;
+          const int cols = (int)(p.N - r.n0 - q * 32 < 32 ? p.N - r.n0 - q * 32 : 32);
+          if (p.out_dtype == IMC_F32)
+            store_rows<EXPERTS>(static_cast<uint32_t*>(p.out) + at, p.N, this_slot, live, cols, v,
+                                rows, f32);
+          else if (p.out_dtype == IMC_BF16)
+            store_rows<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, this_slot, live, cols, v,
+                                rows, bf16);
+          else
+            store_rows<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, this_slot, live, cols, v,
+                                rows, f16);
+        } else if (p.out_dtype == IMC_F32) {
+          store_tokens<EXPERTS>(static_cast<uint32_t*>(p.out) + at + lane, p.N, this_slot, live, in,
+                                v, f32);
+        } else if (p.out_dtype == IMC_BF16) {
+          store_tokens<EXPERTS>(static_cast<uint16_t*>(p.out) + at + lane, p.N, this_slot, live, in,
+                                v, bf16);
+        } else {
+          store_tokens<EXPERTS>(static_cast<uint16_t*>(p.out) + at + lane, p.N, this_slot, live, in,
+                                v, f16);
+        }
       }
       if (SPLIT) {
         __syncwarp();
@@ -622,6 +666,9 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
                                 : (int64_t)num_m * num_n;
   if (tiles > 0x7fffffffLL || (SPLIT && tiles > units)) return cudaErrorInvalidValue;
   const int grid = (int)(tiles < units ? tiles : units) * ctas;
+  // rows that 16-byte stores can write
+  const int wide_rows = (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0 &&
+                        (p.N * dtype_bytes(p.out_dtype)) % 16 == 0 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(THREADS);
@@ -636,7 +683,8 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = F::PAIR || SPLIT ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, k, tw, tx, tws, txs, p, num_m, num_n, 8, splits == 8 ? 3 : splits / 2);
+  e = cudaLaunchKernelEx(&cfg, k, tw, tx, tws, txs, p, num_m, num_n, 8, splits == 8 ? 3 : splits / 2,
+                         wide_rows);
   note_launch();
   return e;
 }
