@@ -15,12 +15,14 @@
 //   warp 1      TMEM owner + MMA issuer: copies the stage's scales to TMEM
 //               (tcgen05.cp), then one MMA per 64 values of K into an fp32
 //               accumulator
-//   warps 2-9   epilogue, two warps per TMEM lane quadrant that take turns by 32
-//               tokens: tcgen05.ld, bias, ReLU, rounding, 32 x 32 outputs through
-//               the warp's own shared memory, and 16-byte stores of whole rows
-//               (one bulk copy per token row took 1.7 times the time: a warp
-//               issues the copies of its lanes one by one, ~130 cycles each;
-//               a store of 32 registers per token 2 times in the experts' form)
+//   warps 2 on  epilogue, two or four warps per TMEM lane quadrant that take turns
+//               by 32 tokens: tcgen05.ld, bias, ReLU, rounding, and per token one
+//               store of 32 consecutive outputs straight from the registers; in
+//               the experts' form, whose rows are scattered, 32 x 32 outputs
+//               through the warp's own shared memory and 16-byte stores (75
+//               against 90 us for 64 experts, 32768 rows, 2048 x 1024).  One bulk
+//               copy per token row had taken 1.7 times the time: a warp issues
+//               the copies of its lanes one by one, ~130 cycles each
 //
 // More than 128 tokens run as CTA pairs (cta_group::2): 256 rows of the weight x
 // 256 tokens per pair, each CTA loading its 128 rows and half of the tokens, so
@@ -28,7 +30,9 @@
 // shared memory cannot feed 128 x 256 tiles of 4-bit MMAs (both operands
 // written once and read once: 192 bytes a cycle against 128).  The pair's two
 // accumulators of 256 columns overlap in 64 of them, which leaves room for the
-// scales: the epilogue drains the shared columns first and hands them back.
+// scales: the epilogue drains the shared columns first and hands them back.  The
+// MMAs run at 9.2 PFLOP/s (7.5 us per 1024 of K at 8192 x 4096, with the
+// epilogue taken out); what is left is the hand-over, ~1.2 us per tile.
 //
 // Few tokens and a long K: the sum over K is split over a cluster of S <= 8 CTAs.
 // Each takes a run of K, writes its partial tile to the others' shared memory
@@ -58,9 +62,16 @@ constexpr int MAX_EXPERTS = 1024;
 
 __device__ int g_watchdog_mx;
 
-template <int BN>
+// Epilogue warps: four per TMEM lane quadrant in the experts' form, whose tiles
+// are short and whose rows are scattered, two otherwise (measured us with 8 / 16:
+// 64 experts, 32768 rows, 2048 x 1024 82.6 / 74.8, dense 8192 x 4096 x 4096 46.5 /
+// 47.5).
+constexpr int epi_warps(bool experts) { return experts ? 16 : 8; }
+constexpr int threads_of(bool experts) { return 64 + 32 * epi_warps(experts); }
+constexpr int ROWS_BYTES = 2048;  // a warp's staged rows (experts' form)
+
+template <int BN, bool PAIR, bool EXPERTS>
 struct Form {
-  static constexpr bool PAIR = BN > 128;
   static constexpr int BNW = PAIR ? 2 * BM : BM;               // weight rows of a tile
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;            // token rows a CTA loads
   static constexpr int B_BYTES = B_ROWS * KB / 2;
@@ -68,20 +79,18 @@ struct Form {
   static constexpr int ATOM_TOKENS = BN < 128 ? BN : 128;      // token rows of a scale atom
   static constexpr int SA_BYTES = 2 * ATOM_BYTES, SB_BYTES = 2 * ATOM_BYTES * B_ATOMS;
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-  static constexpr int STAGES = BN >= 128 ? 5 : (BN > 32 ? 6 : 8);
+  static constexpr int STAGES = BN >= 128 ? (EXPERTS ? 5 : 6) : (BN > 32 ? 6 : (EXPERTS ? 7 : 8));
   // TMEM columns: two accumulators (ACC1 apart), then the scales of SETS stages
   static constexpr int SF_COLS = 8 + 8 * B_ATOMS;
-  static constexpr int SETS = PAIR ? 2 : STAGES;
+  static constexpr bool OVERLAP = BN > 128;
+  static constexpr int SETS = OVERLAP ? 2 : STAGES;
   static constexpr int SF_COL0 = 512 - SETS * SF_COLS;
-  static constexpr int ACC1 = PAIR ? 192 : BN;
+  static constexpr int ACC1 = OVERLAP ? 192 : BN;
   static_assert(ACC1 + BN <= SF_COL0, "TMEM");
   // chunks of 32 columns that hold what the two accumulators share
-  static constexpr int SHARED = PAIR ? (BN - ACC1 + 31) / 32 : 0;
+  static constexpr int SHARED = OVERLAP ? (BN - ACC1 + 31) / 32 : 0;
   static constexpr uint32_t TX = (PAIR ? 2 : 1) * STAGE;       // bytes a stage's barrier waits for
 };
-
-constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
-constexpr int ROWS_BYTES = 32 * 32 * 4;  // a warp's 32 tokens x 32 outputs
 
 struct Ctl {
   uint64_t full[8], empty[8], accf[2], acce[2], drain, part;
@@ -92,18 +101,18 @@ struct Ctl {
 };
 
 // After the stages: the epilogue warps' rows or (SPLIT) the cluster's partial sums.
-template <int BN, bool SPLIT>
+template <int BN, bool EXPERTS, bool SPLIT>
 constexpr int extra_bytes() {
-  return SPLIT ? BN * BM * 4 : EPI_WARPS * ROWS_BYTES;
+  return SPLIT ? BN * BM * 4 : (EXPERTS ? epi_warps(true) * ROWS_BYTES : 0);
 }
-template <int BN, bool SPLIT>
+template <int BN, bool PAIR, bool EXPERTS, bool SPLIT>
 constexpr int smem_bytes() {
-  return 1024 + Form<BN>::STAGES * Form<BN>::STAGE + extra_bytes<BN, SPLIT>() + (int)sizeof(Ctl);
+  using F = Form<BN, PAIR, EXPERTS>;
+  constexpr int bytes =
+      1024 + F::STAGES * F::STAGE + extra_bytes<BN, EXPERTS, SPLIT>() + (int)sizeof(Ctl);
+  static_assert(bytes <= 232448, "shared memory");
+  return bytes;
 }
-static_assert(smem_bytes<256, false>() <= 232448 && smem_bytes<128, false>() <= 232448 &&
-                  smem_bytes<64, false>() <= 232448 && smem_bytes<32, false>() <= 232448 &&
-                  smem_bytes<32, true>() <= 232448,
-              "shared memory");
 
 // One tile: n rows n0.. of expert e's weight (this CTA's 128), token rows m0..
 // of x (`rows` of them count).
@@ -143,54 +152,68 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
 template <bool EXPERTS, typename O, typename Bits>
 __device__ __forceinline__ void store_tokens(O* out, int64_t N, int slot, int live, bool in,
                                              const uint32_t (&v)[32], Bits bits) {
+  if (live == 32) {  // no branch per token
+    O* o = out;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (j < live) {
-      O* o = out + (EXPERTS ? (int64_t)__shfl_sync(0xffffffffu, slot, j) : (int64_t)j) * N;
+    for (int j = 0; j < 32; ++j) {
+      if (EXPERTS) o = out + (int64_t)__shfl_sync(0xffffffffu, slot, j) * N;
       if (in) *o = bits(v[j]);
+      o += N;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j < live) {
+        O* o = out + (EXPERTS ? (int64_t)__shfl_sync(0xffffffffu, slot, j) : (int64_t)j) * N;
+        if (in) *o = bits(v[j]);
+      }
     }
   }
 }
 
 // The same by rows: lane l's outputs (column l of the warp's 32) of the tokens go
-// to `rows` [32][32], and 16 bytes of a row at a time to out, whose column 0 is
-// the warp's; cols of the 32 exist.  N * sizeof(O) and out are multiples of 16.
-template <bool EXPERTS, typename O, typename Bits>
+// to `rows` (ROWS_BYTES: 32 tokens of 16-bit outputs or half of them in fp32),
+// and 16 bytes of a row at a time to out, whose column 0 is the warp's; cols of
+// the 32 exist.  N * sizeof(O) and out are multiples of 16.
+template <typename O, typename Bits>
 __device__ __forceinline__ void store_rows(O* out, int64_t N, int slot, int live, int cols,
                                            const uint32_t (&v)[32], uint8_t* rows, Bits bits) {
   constexpr int PER_ROW = 32 * (int)sizeof(O) / 16, AT_ONCE = 32 / PER_ROW;  // lanes, rows
+  constexpr int HELD = ROWS_BYTES / (32 * (int)sizeof(O));                   // tokens in `rows`
   const int lane = threadIdx.x & 31, r0 = lane / PER_ROW, unit = lane % PER_ROW;
+  const bool in = unit * (16 / (int)sizeof(O)) < cols;
   O* own = reinterpret_cast<O*>(rows) + lane;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) own[j * 32] = bits(v[j]);
-  __syncwarp();
-  const bool in = unit * (16 / (int)sizeof(O)) < cols;
+  for (int h = 0; h < 32; h += HELD) {
 #pragma unroll
-  for (int k = 0; k < PER_ROW; ++k) {
-    const int row = k * AT_ONCE + r0;
-    const int64_t to = EXPERTS ? (int64_t)__shfl_sync(0xffffffffu, slot, row) : (int64_t)row;
-    if (in && row < live)
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(out + to * N) + unit * 16) =
-          *reinterpret_cast<const uint4*>(rows + row * 32 * (int)sizeof(O) + unit * 16);
+    for (int j = 0; j < HELD; ++j) own[j * 32] = bits(v[h + j]);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < HELD / AT_ONCE; ++k) {
+      const int row = k * AT_ONCE + r0;
+      const int64_t to = (int64_t)__shfl_sync(0xffffffffu, slot, h + row);
+      if (in && h + row < live)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(out + to * N) + unit * 16) =
+            *reinterpret_cast<const uint4*>(rows + row * 32 * (int)sizeof(O) + unit * 16);
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
-template <int BN, bool EXPERTS, bool SPLIT>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int BN, bool PAIR, bool EXPERTS, bool SPLIT>
+__global__ void __launch_bounds__(threads_of(EXPERTS), 1)
     k_mx_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
               const ProductArgs p, const int num_m, const int num_n, const int group,
               const int log_splits, const int wide_rows) {
-  using F = Form<BN>;
-  constexpr bool PAIR = F::PAIR;
-  constexpr int STAGES = F::STAGES;
+  using F = Form<BN, PAIR, EXPERTS>;
+  constexpr int STAGES = F::STAGES, EPI_WARPS = epi_warps(EXPERTS), TURNS = EPI_WARPS / 4;
   const int splits = SPLIT ? 1 << log_splits : 1;
   static_assert(!SPLIT || (!PAIR && !EXPERTS), "split form");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
   float* part = reinterpret_cast<float*>(smem + STAGES * F::STAGE);  // SPLIT: [src][token][128 / S]
-  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * F::STAGE + extra_bytes<BN, SPLIT>());
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + STAGES * F::STAGE + extra_bytes<BN, EXPERTS, SPLIT>());
   // Known to be the same for a warp's lanes: what follows from it stays in
   // uniform registers, where the tcgen05 and TMA instructions want their operands.
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -370,12 +393,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int t = unit; t < num_tiles; t += units, ++tl) {
         if (EXPERTS && t >= ctl->tiles_before[p.E]) break;
         const int buf = tl & 1;
-        // the accumulator is free: the tile two before (a pair: the part shared
-        // with the tile before) has been read
+        // the accumulator is free: the tile two before (overlapping ones: the
+        // part shared with the tile before) has been read
         const bool free_ =
-            PAIR ? tl == 0 || wait_any<true>(&ctl->acce[0], (uint32_t)(tl - 1) & 1u, abort,
-                                             tc::kSiteMmaAccEmpty, wd)
-                 : wait_any<false>(&ctl->acce[buf], ((uint32_t)(tl >> 1) & 1u) ^ 1u, abort,
+            F::OVERLAP ? tl == 0 || wait_any<true>(&ctl->acce[0], (uint32_t)(tl - 1) & 1u, abort,
+                                                   tc::kSiteMmaAccEmpty, wd)
+                       : wait_any<PAIR>(&ctl->acce[buf], ((uint32_t)(tl >> 1) & 1u) ^ 1u, abort,
                                    tc::kSiteMmaAccEmpty, wd);
         if (!free_) break;
         ptx::tc_fence_after();
@@ -444,8 +467,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ----------------------------------------------------------- epilogue
     ptx::griddep_wait();  // bias, and the order of output writes
     const int q = warp & 3;               // TMEM lane quadrant this warp may read
-    const int turn = (warp - 2) >> 2;     // it takes every other chunk of 32 tokens
-    const uint32_t acce0 = PAIR ? ptx::cluster_addr(&ctl->acce[0], 0) : 0u;
+    const int turn = (warp - 2) >> 2;     // it takes every TURNS-th chunk of 32 tokens
     int tl = 0;
     for (int t = unit; t < num_tiles; t += units) {
       const Tile r = tile_of(t);
@@ -456,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float bias = p.bias && in && !none ? __ldg(p.bias + (int64_t)r.e * p.N + n) : 0.0f;
       // accumulator 0 shares its last columns with 1, which shares its first
       auto chunk = [&](int i) {
-        return 32 * (PAIR && buf == 0 ? (i + BN / 32 - F::SHARED) % (BN / 32) : i);
+        return 32 * (F::OVERLAP && buf == 0 ? (i + BN / 32 - F::SHARED) % (BN / 32) : i);
       };
       // the slots of a chunk's tokens, loaded one chunk ahead
       auto slots = [&](int i) {
@@ -477,12 +499,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * F::ACC1);
 #pragma unroll 1
-      for (int i = turn; i < BN / 32 || i == turn; i += 2) {
+      for (int i = turn; i < BN / 32 || i == turn; i += TURNS) {
         const int c = chunk(i);
         const int live = min(32, r.rows - c);  // the same for all lanes
         uint32_t v[32];
         const int this_slot = slot;
-        slot = slots(i + 2);
+        slot = slots(i + TURNS);
         if (live > 0 && !none) {
           ptx::tmem_ld32(tbase + (uint32_t)c, v);
           ptx::tmem_ld_wait();
@@ -490,13 +512,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0u;
         }
-        // after this warp's last chunk (a pair: its last that is shared) the MMA
+        // after this warp's last chunk (overlapping: its last shared one) the MMA
         // may have the accumulator back
-        if (!none && (PAIR ? i == F::SHARED - 2 + turn : i + 2 >= BN / 32)) {
+        if (!none && (F::OVERLAP ? i == turn : i + TURNS >= BN / 32)) {
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (PAIR) ptx::mbar_arrive_cluster(acce0);
+            if (PAIR)
+              ptx::mbar_arrive_cluster(ptx::cluster_addr(&ctl->acce[F::OVERLAP ? 0 : buf], 0));
             else ptx::mbar_arrive(&ctl->acce[buf]);
           }
         }
@@ -524,17 +547,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto f32 = [](uint32_t b) { return b; };
         auto bf16 = [](uint32_t b) { return bf16_bits(__uint_as_float(b)); };
         auto f16 = [](uint32_t b) { return half_bits(__uint_as_float(b)); };
-        if (wide_rows) {
+        if (EXPERTS && wide_rows) {
           uint8_t* rows = smem + STAGES * F::STAGE + (warp - 2) * ROWS_BYTES;
           const int cols = (int)(p.N - r.n0 - q * 32 < 32 ? p.N - r.n0 - q * 32 : 32);
           if (p.out_dtype == IMC_F32)
-            store_rows<EXPERTS>(static_cast<uint32_t*>(p.out) + at, p.N, this_slot, live, cols, v,
+            store_rows(static_cast<uint32_t*>(p.out) + at, p.N, this_slot, live, cols, v,
                                 rows, f32);
           else if (p.out_dtype == IMC_BF16)
-            store_rows<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, this_slot, live, cols, v,
+            store_rows(static_cast<uint16_t*>(p.out) + at, p.N, this_slot, live, cols, v,
                                 rows, bf16);
           else
-            store_rows<EXPERTS>(static_cast<uint16_t*>(p.out) + at, p.N, this_slot, live, cols, v,
+            store_rows(static_cast<uint16_t*>(p.out) + at, p.N, this_slot, live, cols, v,
                                 rows, f16);
         } else if (p.out_dtype == IMC_F32) {
           store_tokens<EXPERTS>(static_cast<uint32_t*>(p.out) + at + lane, p.N, this_slot, live, in,
@@ -636,12 +659,12 @@ bool encode_scales(CUtensorMap* m, const uint8_t* q, const Store& st, uint32_t b
 
 constexpr int kMaxDev = 64;
 
-template <int BN, bool EXPERTS, bool SPLIT = false>
+template <int BN, bool PAIR, bool EXPERTS, bool SPLIT = false>
 cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
-  using F = Form<BN>;
-  constexpr int smem = smem_bytes<BN, SPLIT>();
+  using F = Form<BN, PAIR, EXPERTS>;
+  constexpr int smem = smem_bytes<BN, PAIR, EXPERTS, SPLIT>();
   static std::atomic<bool> ready[kMaxDev];  // per device: the attribute is set (calls may race)
-  auto k = k_mx_gemm<BN, EXPERTS, SPLIT>;
+  auto k = k_mx_gemm<BN, PAIR, EXPERTS, SPLIT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -650,7 +673,7 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
     if (e != cudaSuccess) return e;
     if (dev < kMaxDev) ready[dev].store(true, std::memory_order_release);
   }
-  const int ctas = F::PAIR ? 2 : splits, units = device_sm_count() / ctas;
+  const int ctas = PAIR ? 2 : splits, units = device_sm_count() / ctas;
   // a dense product of fewer than 128 rows a tile has one tile of tokens
   const Store sw = store_of(EXPERTS ? p.E : 1, p.N, p.K),
               sx = store_of(1, p.x_rows, p.K,
@@ -671,7 +694,7 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
                         (p.N * dtype_bytes(p.out_dtype)) % 16 == 0 ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(threads_of(EXPERTS));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -682,7 +705,7 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = F::PAIR || SPLIT ? 2 : 1;
+  cfg.numAttrs = PAIR || SPLIT ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, k, tw, tx, tws, txs, p, num_m, num_n, 8, splits == 8 ? 3 : splits / 2,
                          wide_rows);
   note_launch();
@@ -724,10 +747,10 @@ cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
   note_kernel_name(p.E ? "k_mx_gemm<experts>" : "k_mx_gemm");
   if (p.E) {
     switch (tile_shift(ceil_div(p.slots, p.E))) {
-      case 5: return run<32, true>(p, s);
-      case 6: return run<64, true>(p, s);
-      case 7: return run<128, true>(p, s);
-      default: return run<256, true>(p, s);
+      case 5: return run<32, false, true>(p, s);
+      case 6: return run<64, false, true>(p, s);
+      case 7: return run<128, false, true>(p, s);
+      default: return run<256, true, true>(p, s);
     }
   }
   // Pairs that would leave more than half of the SMs without a tile give way to
@@ -736,11 +759,11 @@ cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
   const int shift = tile_shift(p.M);
   if (shift == 5) {
     const int splits = pick_splits(p);
-    return splits > 1 ? run<32, false, true>(p, s, splits) : run<32, false>(p, s);
+    return splits > 1 ? run<32, false, false, true>(p, s, splits) : run<32, false, false>(p, s);
   }
-  if (shift == 6) return run<64, false>(p, s);
-  if (shift == 7 || pair_tiles * 4 <= device_sm_count()) return run<128, false>(p, s);
-  return run<256, false>(p, s);
+  if (shift == 6) return run<64, false, false>(p, s);
+  if (shift == 7 || pair_tiles * 4 <= device_sm_count()) return run<128, false, false>(p, s);
+  return run<256, true, false>(p, s);
 }
 
 cudaError_t product_take_watchdog(int* value) {
