@@ -523,6 +523,7 @@ def conv2d_host(x, w, bias=None, stride=1, padding=0, dilation=1, *, mode="defau
 _torch = None
 _DTYPE_IDS = {}
 _size = functools.lru_cache(maxsize=4096)(mxfp4_bytes)
+_linear_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_workspace_bytes)
 _layout_size = functools.lru_cache(maxsize=4096)(moe_layout_size)
 _experts_size = functools.lru_cache(maxsize=4096)(mxfp4_experts_linear_workspace_bytes)
 _backward_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_backward_workspace_bytes)
@@ -663,10 +664,8 @@ def linear_mxfp4(x, w, bias=None, *, relu=False, out_dtype=None, out=None):
     else:
         out_dtype = out.dtype if out_dtype is None else out_dtype
         _check_plain(out, "out", out_dtype, (M, N), like)
-    nbytes, ws = 0, None
-    if dt != MXFP4:
-        nbytes = _size(1, M, K)
-        ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    nbytes = _linear_size(M, K, dt)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device) if nbytes else None
     rc = _lib.mxfp4_linear(like.data_ptr(), dt, ld, wd.data_ptr(), _ptr(bias), out.data_ptr(),
                            _dtype_id(out_dtype, "out_dtype"), M, N, K, ACT_RELU if relu else 0,
                            _ptr(ws), nbytes, _stream_of(like))
@@ -806,11 +805,11 @@ def experts_linear_mxfp4(x, w, layout, bias=None, *, relu=False, out_dtype=None)
     out_dtype = x.dtype if out_dtype is None else out_dtype
     out = _torch.empty((T * k, N), dtype=out_dtype, device=device)
     nbytes = _experts_size(T, k, E, K)
-    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device) if nbytes else None
     rc = _lib.mxfp4_experts_linear(x.data_ptr(), dt, rows, ld, wd.data_ptr(), _ptr(bias),
                                    ld_data.data_ptr(), out.data_ptr(),
                                    _dtype_id(out_dtype, "out_dtype"), T, k, E, N, K,
-                                   ACT_RELU if relu else 0, ws.data_ptr(), nbytes, _stream_of(x))
+                                   ACT_RELU if relu else 0, _ptr(ws), nbytes, _stream_of(x))
     if rc:
         raise ImcError(rc, "mxfp4_experts_linear")
     return out

@@ -39,6 +39,11 @@
 // (CTA r sums rows r * 128 / S .. of n) and the sums are taken in the order of
 // the CTAs, so a result does not depend on timing (the rule: pick_splits).
 //
+// A handful of tokens (FUSED): the epilogue warps, idle until the accumulator is
+// done, quantise the token rows of a stage themselves into the stage's shared
+// memory, so that a decoding step's product is one launch without scratch; every
+// CTA repeats that small work (the rule: product_fused).
+//
 // Persistent CTAs walk the tiles.  In the experts' form a tile is (expert, rows
 // of that expert, n); the row counts are only known on the GPU, so every CTA
 // sums them up at its start.
@@ -46,6 +51,7 @@
 #include <mutex>
 
 #include "mx_internal.cuh"
+#include "mx_quant.cuh"
 #include "tc_common.cuh"
 
 namespace imc {
@@ -200,7 +206,32 @@ __device__ __forceinline__ void store_rows(O* out, int64_t N, int slot, int live
   }
 }
 
-template <int BN, bool PAIR, bool EXPERTS, bool SPLIT>
+// One 256-wide block of a token's row, 16 values a lane, quantised into row r of
+// the swizzled token tile (128 bytes a row) and its scale atoms.
+template <typename T>
+__device__ __forceinline__ void quantize_row(const ProductArgs& p, int64_t row, int kb, int r,
+                                             uint8_t* tile, uint8_t* scales) {
+  const int l = threadIdx.x & 15;  // two rows per warp
+  const int64_t col = (int64_t)kb * KB + l * 16;
+  const int n = (int)(p.K - col > 16 ? 16 : (p.K > col ? p.K - col : 0));
+  const T* x = static_cast<const T*>(p.raw) + row * p.raw_stride + col;
+  Raw16<T> raw;
+  raw.load(x, row >= 0 ? n : 0, (reinterpret_cast<uintptr_t>(x) & 15u) == 0);
+  float v[16];
+  raw.widen(v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const uint32_t sb = scale_byte(m);
+  const uint2 code = codes16(v, scale_up(sb));
+  if (row < 0) return;
+  const int b = l >> 1;  // block of 32, one 16-byte unit of the row
+  *reinterpret_cast<uint2*>(tile + r * 128 + ((b ^ (r & 7)) << 4) + (l & 1) * 8) = code;
+  if ((l & 1) == 0) scales[(b >> 2) * ATOM_BYTES + r * 16 + (b & 3)] = (uint8_t)sb;
+}
+
+template <int BN, bool PAIR, bool EXPERTS, bool SPLIT, bool FUSED>
 __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
     k_mx_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
@@ -210,6 +241,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
   constexpr int STAGES = F::STAGES, EPI_WARPS = epi_warps(EXPERTS), TURNS = EPI_WARPS / 4;
   const int splits = SPLIT ? 1 << log_splits : 1;
   static_assert(!SPLIT || (!PAIR && !EXPERTS), "split form");
+  static_assert(!FUSED || BN == 32, "fused form");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
   float* part = reinterpret_cast<float*>(smem + STAGES * F::STAGE);  // SPLIT: [src][token][128 / S]
@@ -229,7 +261,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(&ctl->full[s], 1);
+      ptx::mbar_init(&ctl->full[s], FUSED ? 2 : 1);
       ptx::mbar_init(&ctl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -336,7 +368,8 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
         uint8_t* st = smem + s * F::STAGE;
         uint8_t* sf = st + A_BYTES + F::B_BYTES;
         if (ptx::elect_one()) {
-          if (rank == 0) ptx::mbar_arrive_expect_tx(&ctl->full[s], F::TX);
+          if (rank == 0)
+            ptx::mbar_arrive_expect_tx(&ctl->full[s], FUSED ? A_BYTES + F::SA_BYTES : F::TX);
           if (PAIR) {
             const uint32_t bar = ptx::cluster_addr(&ctl->full[s], 0);
             ptx::tma_load_3d_pair(st, &tmW, bar, kb * (KB / 2), r.n0, r.e);
@@ -348,7 +381,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
         }
         if (!tokens_ready) ptx::griddep_wait();
         tokens_ready = true;
-        if (ptx::elect_one()) {
+        if (!FUSED && ptx::elect_one()) {
           if (PAIR) {
             const uint32_t bar = ptx::cluster_addr(&ctl->full[s], 0);
             ptx::tma_load_2d_pair(st + A_BYTES, &tmX, bar, kb * (KB / 2), r.m0 + rank * F::B_ROWS);
@@ -486,6 +519,31 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
         return EXPERTS && i < BN / 32 && c < r.rows ? __ldg(p.order + r.first + c) : 0;
       };
       int slot = slots(turn);
+      if (FUSED && !none) {
+        // this warp's blocks of K: wait for the stage, write the tokens' rows
+        bool ok = true;
+        for (int kb = kb0 + warp - 2; kb < num_kb; kb += EPI_WARPS) {
+          const int block = tl * (num_kb - kb0) + kb - kb0, st = block % STAGES;
+          ok = wait_any<false>(&ctl->empty[st], ((uint32_t)(block / STAGES) & 1u) ^ 1u, abort,
+                               tc::kSiteProducerEmpty, wd);
+          if (!ok) break;
+          __syncwarp();
+          uint8_t* tile = smem + st * F::STAGE + A_BYTES;
+          uint8_t* scales = tile + F::B_BYTES + F::SA_BYTES;
+          for (int j = 0; j < r.rows; j += 2) {
+            const int m = j + (lane >> 4);  // half-warps take neighbouring rows
+            int64_t row = -1;
+            if (m < r.rows) row = EXPERTS ? __ldg(p.order + r.first + m) / p.share : r.m0 + m;
+            if (p.raw_dtype == IMC_F32) quantize_row<float>(p, row, kb, m, tile, scales);
+            else if (p.raw_dtype == IMC_BF16) quantize_row<__nv_bfloat16>(p, row, kb, m, tile, scales);
+            else quantize_row<__half>(p, row, kb, m, tile, scales);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&ctl->full[st]);
+        }
+        if (!ok) break;
+      }
       if (!none) {
         int ok = 1;
         if (lane == 0)
@@ -659,12 +717,12 @@ bool encode_scales(CUtensorMap* m, const uint8_t* q, const Store& st, uint32_t b
 
 constexpr int kMaxDev = 64;
 
-template <int BN, bool PAIR, bool EXPERTS, bool SPLIT = false>
+template <int BN, bool PAIR, bool EXPERTS, bool SPLIT = false, bool FUSED = false>
 cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
   using F = Form<BN, PAIR, EXPERTS>;
   constexpr int smem = smem_bytes<BN, PAIR, EXPERTS, SPLIT>();
   static std::atomic<bool> ready[kMaxDev];  // per device: the attribute is set (calls may race)
-  auto k = k_mx_gemm<BN, PAIR, EXPERTS, SPLIT>;
+  auto k = k_mx_gemm<BN, PAIR, EXPERTS, SPLIT, FUSED>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -679,9 +737,15 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
               sx = store_of(1, p.x_rows, p.K,
                             EXPERTS ? experts_atom_shift(p.slots, p.E) : 7);
   CUtensorMap tw, tx, tws, txs;
-  if (!encode_codes(&tw, p.w, sw, BM, 3) || !encode_codes(&tx, p.x, sx, F::B_ROWS, 2) ||
-      !encode_scales(&tws, p.w, sw, 1, 3) || !encode_scales(&txs, p.x, sx, F::B_ATOMS, 2))
+  if (!encode_codes(&tw, p.w, sw, BM, 3) || !encode_scales(&tws, p.w, sw, 1, 3))
     return cudaErrorInvalidValue;
+  if (FUSED) {  // not read
+    tx = tw;
+    txs = tws;
+  } else if (!encode_codes(&tx, p.x, sx, F::B_ROWS, 2) ||
+             !encode_scales(&txs, p.x, sx, F::B_ATOMS, 2)) {
+    return cudaErrorInvalidValue;
+  }
   const int num_n = (int)ceil_div(p.N, F::BNW), num_m = EXPERTS ? 0 : (int)ceil_div(p.M, BN);
   // experts: at most one partly filled tile per expert beyond the full ones
   const int64_t tiles = EXPERTS ? (p.slots / BN + (p.slots < p.E + 1 ? p.slots : p.E + 1)) *
@@ -722,6 +786,9 @@ namespace {
 int tile_shift(int64_t rows) { return rows <= 32 ? 5 : (rows <= 64 ? 6 : (rows <= 128 ? 7 : 8)); }
 }  // namespace
 
+bool product_fused(int64_t tokens) { return tokens <= 8; }
+bool experts_fused(int64_t slots, int64_t E) { return slots <= 4 * E && slots <= 256; }
+
 int experts_atom_shift(int64_t slots, int64_t E) {
   const int t = tile_shift(ceil_div(slots, E));
   return t < 7 ? t : 7;
@@ -744,10 +811,12 @@ int pick_splits(const ProductArgs& p) {
 }  // namespace
 
 cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
-  note_kernel_name(p.E ? "k_mx_gemm<experts>" : "k_mx_gemm");
+  note_kernel_name(p.raw ? (p.E ? "k_mx_gemm<experts,fused>" : "k_mx_gemm<fused>")
+                         : (p.E ? "k_mx_gemm<experts>" : "k_mx_gemm"));
   if (p.E) {
     switch (tile_shift(ceil_div(p.slots, p.E))) {
-      case 5: return run<32, false, true>(p, s);
+      case 5:
+        return p.raw ? run<32, false, true, false, true>(p, s) : run<32, false, true>(p, s);
       case 6: return run<64, false, true>(p, s);
       case 7: return run<128, false, true>(p, s);
       default: return run<256, true, true>(p, s);
@@ -759,6 +828,9 @@ cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
   const int shift = tile_shift(p.M);
   if (shift == 5) {
     const int splits = pick_splits(p);
+    if (p.raw)
+      return splits > 1 ? run<32, false, false, true, true>(p, s, splits)
+                        : run<32, false, false, false, true>(p, s);
     return splits > 1 ? run<32, false, false, true>(p, s, splits) : run<32, false, false>(p, s);
   }
   if (shift == 6) return run<64, false, false>(p, s);

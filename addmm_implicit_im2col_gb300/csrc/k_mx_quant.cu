@@ -8,52 +8,12 @@
 // step but the final rounding is exact.  A block that holds an infinity or a
 // NaN gets the scale byte 255 (NaN): it stands for 32 NaNs.
 #include "mx_internal.cuh"
+#include "mx_quant.cuh"
 #include "ptx.cuh"
 
 namespace imc {
 namespace mx {
 namespace {
-
-// Scale byte of a block from the bits of its largest magnitude.
-__device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits) {
-  const uint32_t e = max_bits >> 23;
-  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
-}
-// 2^(127 - byte), the factor that brings a block into [0, 8); 0 for a NaN
-// block (its codes are then 0).
-__device__ __forceinline__ float scale_up(uint32_t byte) {
-  return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
-}
-// 2^(byte - 127) (a denormal for byte 0), NaN for 255.
-__device__ __forceinline__ float scale_down(uint32_t byte) {
-  if (byte == 255u) return __uint_as_float(0x7FC00000u);
-  return byte == 0u ? __uint_as_float(1u << 22) : __uint_as_float(byte << 23);
-}
-
-// Eight scaled values to eight E2M1 codes, the first in the lowest four bits.
-__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float up) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "f"(v[0] * up), "f"(v[1] * up), "f"(v[2] * up), "f"(v[3] * up), "f"(v[4] * up),
-        "f"(v[5] * up), "f"(v[6] * up), "f"(v[7] * up));
-  return r;
-}
-// Sixteen scaled values to sixteen codes.
-__device__ __forceinline__ uint2 codes16(const float (&v)[16], float up) {
-  float lo[8], hi[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo[i] = v[i];
-    hi[i] = v[8 + i];
-  }
-  return make_uint2(codes8(lo, up), codes8(hi, up));
-}
 
 // Which rows and columns a lane takes: 8 lanes cover 128 columns of a row (a
 // lane 16 columns, two lanes a block of 32).  A CTA's 32 such groups cover 2^cs
@@ -66,50 +26,6 @@ struct RowMap {
   int64_t chunks;    // block atoms of a row
 };
 constexpr int GROUPS_SHIFT = 5;  // log2 of a CTA's groups of 8 lanes
-
-// A lane's 16 values of one row: loaded raw, so that the U rows' loads are in
-// flight together, and widened later.
-template <typename T>
-struct Raw16 {
-  static constexpr int N = (int)sizeof(T);  // 16-byte words
-  uint4 w[N];
-  __device__ __forceinline__ void load(const T* p, int n, bool vec) {
-    if (vec && n == 16) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    } else {
-      alignas(16) T e[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) e[i] = i < n ? p[i] : from_f32<T>(0.0f);
-#pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(e)[i];
-    }
-  }
-  __device__ __forceinline__ void widen(float (&v)[16]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (sizeof(T) == 4) {
-          v[4 * i + j] = __uint_as_float(u[j]);
-        } else {
-          const float2 f = two(u[j]);
-          v[8 * i + 2 * j] = f.x;
-          v[8 * i + 2 * j + 1] = f.y;
-        }
-      }
-    }
-  }
-  static __device__ __forceinline__ float2 two(uint32_t u) {
-    if (sizeof(T) == 2 && is_bf16(T()))
-      return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-    return __half22float2(*reinterpret_cast<const __half2*>(&u));
-  }
-  static __device__ __forceinline__ bool is_bf16(__nv_bfloat16) { return true; }
-  static __device__ __forceinline__ bool is_bf16(__half) { return false; }
-  static __device__ __forceinline__ bool is_bf16(float) { return false; }
-};
 
 // Rows: a group of 8 lanes writes 64 bytes of codes and one scale word per row.
 template <typename T, int U>

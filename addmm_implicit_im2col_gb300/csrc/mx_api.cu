@@ -125,7 +125,7 @@ int mxfp4_dequantize(const void* q, int64_t batch, int64_t rows, int64_t cols, i
 }
 
 size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K, int x_dtype) {
-  return x_dtype == IMC_MXFP4 ? 0 : mxfp4_bytes(1, M, K);
+  return x_dtype == IMC_MXFP4 || product_fused(M) ? 0 : mxfp4_bytes(1, M, K);
 }
 
 int mxfp4_linear(const void* x, int x_dtype, int64_t row_stride, const void* w, const float* bias,
@@ -150,7 +150,7 @@ int mxfp4_linear(const void* x, int x_dtype, int64_t row_stride, const void* w, 
       ranges_overlap(out, out_bytes, bias, (uint64_t)N * 4))
     return IMC_ERR_ALIAS;
   const size_t need = mxfp4_linear_workspace_bytes(M, K, x_dtype);
-  if (raw) {
+  if (need) {
     const int ws = check_workspace(workspace, workspace_bytes, need);
     if (ws != IMC_OK) return ws;
     if (ranges_overlap(workspace, need, out, out_bytes) ||
@@ -175,7 +175,12 @@ int mxfp4_linear(const void* x, int x_dtype, int64_t row_stride, const void* w, 
   p.K = K;
   Scratch sc(s);
   cudaError_t e = cudaSuccess;
-  if (raw) {
+  if (raw && need == 0) {
+    p.raw = x;
+    p.raw_dtype = x_dtype;
+    p.raw_stride = row_stride;
+    p.share = 1;
+  } else if (raw) {
     if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
     e = launch_quantize(quant_args(x, 1, M, K, 0, row_stride, false, sc.p), x_dtype, false, s);
     p.x = static_cast<const uint8_t*>(sc.p);
@@ -382,6 +387,7 @@ int moe_layout(const int32_t* experts, int64_t T, int64_t k, int64_t E, int32_t*
 
 size_t mxfp4_experts_linear_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t K) {
   if (moe_layout_size(T, k, E) == 0 || T == 0) return 0;
+  if (experts_fused(T * k, E)) return 0;
   const int64_t rows = sorted_rows(T * k, E);
   if (rows > kMaxDim || !dims_ok(0, 0, K) || !store_ok(4, rows, K)) return 0;
   return (size_t)store_of(1, rows, K, experts_atom_shift(T * k, E)).bytes;
@@ -432,6 +438,13 @@ int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row
   p.starts = layout + E + 2;
   p.order = p.starts + E + 1;
   p.x_rows = sorted_rows(n, E);
+  if (need == 0) {
+    p.raw = x;
+    p.raw_dtype = x_dtype;
+    p.raw_stride = row_stride;
+    p.share = x_rows == n ? 1 : (int)k;
+    return finish_call(launch_product(p, s), IMC_KERNEL_MXFP4);
+  }
   Scratch sc(s);
   if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
   p.x = static_cast<const uint8_t*>(sc.p);

@@ -85,6 +85,10 @@ struct ProductArgs {
   const int32_t *offsets, *starts, *order;
   int slots;              // T * k
   bool inputs_ready;      // a pre-pass of this call has waited for earlier kernels
+  // few tokens: unquantised x instead of p.x (product_fused)
+  const void* raw;        // row of token m, or of slot s: raw + (m or s / share) * raw_stride
+  int raw_dtype, share;
+  int64_t raw_stride;
 };
 
 template <typename T>
@@ -147,6 +151,10 @@ cudaError_t launch_quantize(const QuantArgs& a, int dtype, bool transpose, cudaS
 cudaError_t launch_dequantize(const uint8_t* q, const Store& st, int dtype, void* out,
                               cudaStream_t s);
 bool product_supported();
+// Whether the product quantises its tokens itself (args.raw) instead of reading
+// quantised ones: few tokens, or few slots per expert.
+bool product_fused(int64_t tokens);
+bool experts_fused(int64_t slots, int64_t E);
 // Token rows of a tile of the experts' product, as log2: the scale atoms of
 // its sorted rows hold that many rows (at most 128).
 int experts_atom_shift(int64_t slots, int64_t E);

@@ -29,7 +29,7 @@ def dequantize(q=P1, batch=1, rows=8, cols=64, dtype=0, out=P2):
     return binding.mxfp4_dequantize(q, batch, rows, cols, dtype, out, None)
 
 
-def linear(x=P1, x_dtype=0, row_stride=64, w=P2, bias=P3, out=P4, out_dtype=0, M=8, N=8, K=64,
+def linear(x=P1, x_dtype=0, row_stride=64, w=P2, bias=P3, out=P4, out_dtype=0, M=9, N=8, K=64,
            flags=0, ws=P5, nbytes=1 << 20):
     return binding.mxfp4_linear(x, x_dtype, row_stride, w, bias, out, out_dtype, M, N, K, flags, ws,
                                 nbytes, None)
@@ -51,8 +51,8 @@ def route_backward(g=P1, logits=P2, dtype=0, T=4, E=16, row_stride=16, experts=P
                                       scale, out, None)
 
 
-def experts_linear(x=P1, x_dtype=0, rows=4, row_stride=64, w=P2, bias=None, layout=P3, out=P4,
-                   out_dtype=0, T=4, k=2, E=16, N=8, K=64, flags=0, ws=P5, nbytes=1 << 22):
+def experts_linear(x=P1, x_dtype=0, rows=400, row_stride=64, w=P2, bias=None, layout=P3, out=P4,
+                   out_dtype=0, T=400, k=2, E=16, N=8, K=64, flags=0, ws=P5, nbytes=1 << 22):
     return binding.mxfp4_experts_linear(x, x_dtype, rows, row_stride, w, bias, layout, out,
                                         out_dtype, T, k, E, N, K, flags, ws, nbytes, None)
 
@@ -95,7 +95,7 @@ BAD = [
     (route_backward, dict(dtype=9), ARG), (route_backward, dict(E=0), SHAPE), (route_backward, dict(g=None), NULL),
     (route_backward, dict(out=None), NULL), (route_backward, dict(out=P2), ALIAS),
     (experts_linear, dict(x_dtype=3), ARG), (experts_linear, dict(flags=2), ARG),
-    (experts_linear, dict(rows=5), SHAPE), (experts_linear, dict(E=0), SHAPE), (experts_linear, dict(k=33), SHAPE),
+    (experts_linear, dict(rows=401), SHAPE), (experts_linear, dict(E=0), SHAPE), (experts_linear, dict(k=33), SHAPE),
     (experts_linear, dict(K=0), SHAPE), (experts_linear, dict(layout=None), NULL),
     (experts_linear, dict(w=None), NULL), (experts_linear, dict(nbytes=100), ARG),
     (experts_linear, dict(out=P1), ALIAS), (experts_linear, dict(out=P3), ALIAS), (experts_linear, dict(ws=P4), ALIAS),
@@ -127,7 +127,8 @@ def test_sizes():
     assert binding.mxfp4_bytes(1, 1, 1) == 512 + 512
     assert binding.mxfp4_bytes(2, 129, 129) == -(-2 * 129 * 80 // 512) * 512 + 2 * 2 * 2 * 512
     assert binding.mxfp4_bytes(1, -1, 4) == 0 and binding.mxfp4_bytes(1, 2 ** 31 - 1, 2 ** 31 - 1) == 0
-    assert binding.mxfp4_linear_workspace_bytes(8, 64, 0) == binding.mxfp4_bytes(1, 8, 64)
+    assert binding.mxfp4_linear_workspace_bytes(9, 64, 0) == binding.mxfp4_bytes(1, 9, 64)
+    assert binding.mxfp4_linear_workspace_bytes(8, 64, 0) == 0  # quantised within the product
     assert binding.mxfp4_linear_workspace_bytes(8, 64, binding.MXFP4) == 0
     assert binding.moe_layout_size(4, 2, 8) == 2 * 8 + 3 + 16
     assert binding.mxfp4_experts_linear_workspace_bytes(4, 33, 8, 64) == 0
