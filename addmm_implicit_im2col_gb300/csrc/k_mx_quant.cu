@@ -56,18 +56,9 @@ __global__ void __launch_bounds__(256) k_mx_quant_rows(const QuantArgs a, const 
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float v[16];
-      raw[u].widen(v);
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      const uint32_t sb = scale_byte(m);
-      const uint2 code = codes16(v, scale_up(sb));
-      // the four blocks' bytes to one word (blocks past cols hold zeros: byte 0)
-      uint32_t word = sb << ((l8 >> 1) * 8);
-      word |= __shfl_xor_sync(0xffffffffu, word, 2);
-      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+      uint2 code;
+      uint32_t word;  // blocks past cols hold zeros: byte 0
+      quantize_128(raw[u], code, word);
       const int64_t r = row0 + u * step, blk = ba * ATOM_BLOCKS + (l8 >> 1);
       if (r >= all_rows || ba >= map.chunks) continue;
       uint8_t* codes = a.q + blk * 16 + (l8 & 1) * 8;
@@ -96,21 +87,114 @@ __global__ void __launch_bounds__(256) k_mx_quant_rows(const QuantArgs a, const 
 }
 
 // Transposed: x [rows, cols] to MXFP4 of x^T [cols, rows], blocks down the
-// columns.  A CTA takes 128 rows x 64 columns through shared memory; four
-// neighbouring lanes then take the four blocks of one column (64 contiguous
-// bytes of codes and one scale word).  Each 32-row band of the staging tile is
-// shifted by 8 floats, so that the four lanes' column reads fall into
-// different banks.
+// columns.  A lane takes one column (two neighbouring ones of 16-bit values) and
+// NB blocks of 32 rows of it: a warp's loads are whole 128-byte row pieces, a
+// block never leaves its lane's registers, and there is no shared memory (through
+// a staged tile, 8192 x 4096 bf16 took 24 us).
+template <typename T>
+struct ColTile {
+  static constexpr int PER = 4 / (int)sizeof(T);  // columns of a lane
+  static constexpr int COLS = 32 * PER, CTA_COLS = 8 * COLS;
+};
+
+template <typename T, int NB>
+__global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, const bool words) {
+  using C = ColTile<T>;
+  constexpr int PER = C::PER;
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const Store& st = a.st;  // of [cols, rows]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // row tiles cover whole scale atoms: the bytes past the last row are 0
+  const int64_t tiles_r = ceil_div(a.rows, 128) * (4 / NB), tiles_c = ceil_div(a.cols, C::CTA_COLS);
+  const int64_t tiles = a.batch * tiles_r * tiles_c;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t b = t / (tiles_r * tiles_c), rem = t - b * tiles_r * tiles_c;
+    const int64_t r0 = rem / tiles_c * (32 * NB), cta_c0 = rem % tiles_c * C::CTA_COLS;
+    const T* base = static_cast<const T*>(a.x) + b * a.batch_stride;
+    const int64_t c = cta_c0 + warp * C::COLS + lane * PER;
+    const int64_t atoms = b * st.row_atoms * st.block_atoms * ATOM_BYTES;
+    uint32_t word[PER] = {};
+    uint4 code[PER][NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int64_t r = r0 + nb * 32;
+      const T* p = base + r * a.row_stride + c;
+      uint32_t u[32];
+      if (words && c + PER <= a.cols && r + 32 <= a.rows) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          u[j] = __ldg(reinterpret_cast<const uint32_t*>(p + j * a.row_stride));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          alignas(4) T e[PER];
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            e[i] = r + j < a.rows && c + i < a.cols ? p[j * a.row_stride + i] : from_f32<T>(0.0f);
+          u[j] = *reinterpret_cast<const uint32_t*>(e);
+        }
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        m = PER == 1 ? max(m, u[j] & 0x7FFFFFFFu) : __vmaxu2(m, u[j] & 0x7FFF7FFFu);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const uint32_t mb = PER == 1 ? m : Raw16<T>::top16(i ? m >> 16 : m & 0xFFFFu);
+        const uint32_t sb = scale_byte(mb);
+        const float up = scale_up(sb);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (PER == 1) {
+              v[j] = __uint_as_float(u[8 * k + j]);
+            } else {
+              const float2 f = Raw16<T>::two(u[8 * k + j]);
+              v[j] = i ? f.y : f.x;
+            }
+          }
+          w[k] = codes8(v, up);
+        }
+        code[i][nb] = make_uint4(w[0], w[1], w[2], w[3]);
+        word[i] |= sb << (8 * nb);
+      }
+    }
+    const int64_t blk = r0 / BLOCK;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (c + i >= a.cols) continue;
+      uint8_t* to = a.q + (b * a.cols + c + i) * st.pitch + blk * 16;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        if (blk + nb < st.blocks) *reinterpret_cast<uint4*>(to + nb * 16) = code[i][nb];
+      uint8_t* sc = a.q + st.scales_off + atoms + scale_word(st, c + i, blk / ATOM_BLOCKS);
+      if (NB == 4) *reinterpret_cast<uint32_t*>(sc) = word[i];
+      else
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) sc[blk % ATOM_BLOCKS + nb] = (uint8_t)(word[i] >> (8 * nb));
+    }
+  }
+}
+
+// x along its columns (as above) and along its rows, read once: a CTA takes 128
+// rows x 64 columns through shared memory; four neighbouring lanes take the four
+// blocks of one column (64 contiguous bytes of codes and one scale word), then a
+// thread one block of one row.  Each 32-row band of the staging tile is shifted
+// by 8 floats, so that the four lanes' column reads fall into different banks.
+// 39 us at 8192 x 4096 fp32, against 53 us for the two kernels apart; with the
+// second reading left to L1 and L2 instead of shared memory 50 us.
 constexpr int TC = 64, TPITCH = 65;
 // tiles over the columns: whole scale atoms of 128 columns (an atom's bytes past
 // the last column are 0)
 __host__ __device__ constexpr int64_t cols_tiles(int64_t cols) { return ceil_div(cols, 128) * (128 / TC); }
 __device__ __forceinline__ int t_index(int r, int c) { return r * TPITCH + (r >> 5) * 8 + c; }
-// BOTH: x itself is quantised too, along its rows, from the same tile (a thread
-// takes one block of one row), so that x is read once.
-template <typename T, bool BOTH>
-__global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, uint8_t* q_rows,
-                                                       const Store sr, const bool vec) {
+template <typename T>
+__global__ void __launch_bounds__(256) k_mx_quant_both(const QuantArgs a, const Store sr,
+                                                       const bool vec) {
   __shared__ float tile[128 * TPITCH + 32];
   ptx::griddep_wait();
   ptx::griddep_launch();
@@ -171,7 +255,7 @@ __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, uint8_
                                      b * st.row_atoms * st.block_atoms * ATOM_BYTES +
                                      scale_word(st, row, r0 / 128)) = word;
     }
-    if (BOTH) {
+    {
       const int r = threadIdx.x & 127, cb = threadIdx.x >> 7;
       uint32_t mr = 0;
 #pragma unroll
@@ -184,9 +268,9 @@ __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, uint8_
       const int64_t rblk = c0 / BLOCK + cb, rrow = r0 + r;
       if (rrow < a.rows) {
         if (rblk < sr.blocks)
-          *reinterpret_cast<uint4*>(q_rows + (b * a.rows + rrow) * sr.pitch + rblk * 16) = make_uint4(
+          *reinterpret_cast<uint4*>(a.q_rows + (b * a.rows + rrow) * sr.pitch + rblk * 16) = make_uint4(
               codes8(v[0], upr), codes8(v[1], upr), codes8(v[2], upr), codes8(v[3], upr));
-        q_rows[sr.scales_off + b * sr.row_atoms * sr.block_atoms * ATOM_BYTES +
+        a.q_rows[sr.scales_off + b * sr.row_atoms * sr.block_atoms * ATOM_BYTES +
                scale_word(sr, rrow, rblk / ATOM_BLOCKS) + rblk % ATOM_BLOCKS] = (uint8_t)srb;
       }
     }
@@ -194,13 +278,23 @@ __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, uint8_
   }
 }
 
-// The value of one code: 0 .5 1 1.5 2 3 4 6, bit 3 the sign.
-__device__ __forceinline__ float e2m1(uint32_t c) {
-  const uint32_t m = c & 7u;
-  // m >= 2: exponent (m >> 1) - 1, mantissa m & 1 -- an fp32 number directly
-  const uint32_t bits = m >= 2u ? (((m >> 1) + 126u) << 23) | ((m & 1u) << 22)
-                                : (m ? 0x3F000000u : 0u);
-  return __uint_as_float(bits | ((c & 8u) << 28));
+// The values of eight codes, the first in the lowest four bits.
+__device__ __forceinline__ void values8(uint32_t codes, float scale, float (&v)[8]) {
+  uint32_t h[4];  // pairs of fp16, which holds every E2M1 value
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+    v[2 * j] = f.x * scale;
+    v[2 * j + 1] = f.y * scale;
+  }
 }
 
 // As the row quantiser, with 16 lanes for 128 columns (8 values a lane: with 16
@@ -209,7 +303,7 @@ __device__ __forceinline__ float e2m1(uint32_t c) {
 template <typename T, int U>
 __global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t* __restrict__ q, const Store st,
                                                     T* __restrict__ out, const RowMap map,
-                                                    const bool vec) {
+                                                    const bool vec, const bool wide) {
   ptx::griddep_wait();
   ptx::griddep_launch();
   const int l16 = threadIdx.x & 15, group = threadIdx.x >> 4, cs = map.chunk_shift;
@@ -241,11 +335,16 @@ __global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t* __restrict__ 
     for (int u = 0; u < U; ++u) {
       const int64_t r = row0 + u * step;
       if (r >= all_rows) continue;
-      const float s = scale_down(sb[u]);
       float v[8];
+      values8(code[u], scale_down(sb[u]), v);
+      if (wide && n == 8) {  // fp32: whole 32-byte sectors
+        uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = e2m1(code[u] >> (4 * j)) * s;
-      store8<T>(out + r * st.cols + col, n, vec, v);
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[j]);
+        ptx::st_global_v8(out + r * st.cols + col, w);
+      } else {
+        store8<T>(out + r * st.cols + col, n, vec, v);
+      }
     }
   }
 }
@@ -255,17 +354,17 @@ __global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t* __restrict__ 
 struct RowGrid {
   RowMap map;
   dim3 grid;
-  bool many;  // U == 4
+  bool many;  // U rows a group, else one
 };
-RowGrid row_grid(int64_t rows, int64_t chunks, int groups_shift) {
+RowGrid row_grid(int64_t rows, int64_t chunks, int groups_shift, int u) {
   RowGrid g;
   g.map.chunks = chunks;
   g.map.chunk_shift = 0;
   while (g.map.chunk_shift < groups_shift && (1 << g.map.chunk_shift) < chunks) ++g.map.chunk_shift;
   const int64_t y = ceil_div(chunks, 1 << g.map.chunk_shift);
   const int64_t per = 1 << (groups_shift - g.map.chunk_shift);  // rows of a CTA at U == 1
-  g.many = ceil_div(rows, per * 4) * y >= 4 * (int64_t)device_sm_count();
-  g.grid = dim3((unsigned)ceil_div(rows, per * (g.many ? 4 : 1)), (unsigned)(y < 65535 ? y : 65535));
+  g.many = ceil_div(rows, per * u) * y >= 4 * (int64_t)device_sm_count();
+  g.grid = dim3((unsigned)ceil_div(rows, per * (g.many ? u : 1)), (unsigned)(y < 65535 ? y : 65535));
   return g;
 }
 
@@ -276,17 +375,29 @@ cudaError_t quantize(const QuantArgs& a, bool transpose, cudaStream_t s) {
                    (a.batch_stride * (int64_t)sizeof(T)) % 16 == 0;
   cudaError_t e;
   if (transpose) {
-    const int64_t tiles = a.batch * ceil_div(a.rows, 128) * cols_tiles(a.cols);
-    const int64_t cap = (int64_t)device_sm_count() * 6;
-    const dim3 grid((unsigned)(tiles < cap ? tiles : cap));
-    const Store sr = store_of(a.batch, a.rows, a.cols);
-    e = a.q_rows ? launch_after_previous(k_mx_quant_cols<T, true>, grid, dim3(256), 0, s, a, a.q_rows,
-                                         sr, vec)
-                 : launch_after_previous(k_mx_quant_cols<T, false>, grid, dim3(256), 0, s, a,
-                                         (uint8_t*)nullptr, sr, vec);
+    // 32-bit loads of whole columns or pairs of them
+    const bool words = (reinterpret_cast<uintptr_t>(a.x) & 3u) == 0 &&
+                       (a.row_stride * (int64_t)sizeof(T)) % 4 == 0 &&
+                       (a.batch_stride * (int64_t)sizeof(T)) % 4 == 0;
+    const int64_t sms = device_sm_count(), across = a.batch * ceil_div(a.cols, ColTile<T>::CTA_COLS);
+    const int64_t four = across * ceil_div(a.rows, 128);  // CTAs of four blocks a lane
+    const int64_t cap = sms * 8;
+    if (a.q_rows) {
+      const int64_t tiles = a.batch * ceil_div(a.rows, 128) * cols_tiles(a.cols);
+      e = launch_after_previous(k_mx_quant_both<T>,
+                                dim3((unsigned)(tiles < sms * 6 ? tiles : sms * 6)), dim3(256), 0, s,
+                                a, store_of(a.batch, a.rows, a.cols), vec);
+    } else if (four >= 2 * sms) {
+      e = launch_after_previous(k_mx_quant_cols<T, 4>, dim3((unsigned)(four < cap ? four : cap)),
+                                dim3(256), 0, s, a, words);
+    } else {
+      e = launch_after_previous(k_mx_quant_cols<T, 1>,
+                                dim3((unsigned)(four * 4 < cap ? four * 4 : cap)), dim3(256), 0, s,
+                                a, words);
+    }
   } else {
-    const RowGrid g = row_grid(a.batch * a.rows, a.st.block_atoms, GROUPS_SHIFT);
-    e = launch_after_previous(g.many ? k_mx_quant_rows<T, 4> : k_mx_quant_rows<T, 1>, g.grid,
+    const RowGrid g = row_grid(a.batch * a.rows, a.st.block_atoms, GROUPS_SHIFT, 2);
+    e = launch_after_previous(g.many ? k_mx_quant_rows<T, 2> : k_mx_quant_rows<T, 1>, g.grid,
                               dim3(256), 0, s, a, g.map, vec);
   }
   note_launch();
@@ -297,10 +408,12 @@ template <typename T>
 cudaError_t dequantize(const uint8_t* q, const Store& st, void* out, cudaStream_t s) {
   const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 &&
                    (st.cols * (int64_t)sizeof(T)) % 16 == 0;
-  const RowGrid g = row_grid(st.batch * st.rows, st.block_atoms, 4);
+  const bool wide = sizeof(T) == 4 && vec && (reinterpret_cast<uintptr_t>(out) & 31u) == 0 &&
+                    st.cols % 8 == 0;
+  const RowGrid g = row_grid(st.batch * st.rows, st.block_atoms, 4, 4);
   const cudaError_t e =
       launch_after_previous(g.many ? k_mx_dequant<T, 4> : k_mx_dequant<T, 1>, g.grid, dim3(256), 0,
-                            s, q, st, static_cast<T*>(out), g.map, vec);
+                            s, q, st, static_cast<T*>(out), g.map, vec, wide);
   note_launch();
   return e;
 }

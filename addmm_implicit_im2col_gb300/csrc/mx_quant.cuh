@@ -66,6 +66,23 @@ struct Raw16 {
       for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint4*>(e)[i];
     }
   }
+  // Bits of the largest magnitude as a float (NaN above infinity above numbers);
+  // 16-bit values are compared two at a time.
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        m = sizeof(T) == 4 ? max(m, u[j] & 0x7FFFFFFFu) : __vmaxu2(m, u[j] & 0x7FFF7FFFu);
+    }
+    return sizeof(T) == 4 ? m : top16(max(m & 0xFFFFu, m >> 16));
+  }
+  // A magnitude's 16 bits as the bits of a float.
+  static __device__ __forceinline__ uint32_t top16(uint32_t h) {
+    return is_bf16(T()) ? h << 16 : __float_as_uint(__half2float(__ushort_as_half((uint16_t)h)));
+  }
   __device__ __forceinline__ void widen(float (&v)[16]) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -91,6 +108,21 @@ struct Raw16 {
   static __device__ __forceinline__ bool is_bf16(__half) { return false; }
   static __device__ __forceinline__ bool is_bf16(float) { return false; }
 };
+
+// The codes of a lane's 16 values and the scale word of its row's 128 columns:
+// eight neighbouring lanes hold them (two lanes a block).
+template <typename T>
+__device__ __forceinline__ void quantize_128(const Raw16<T>& raw, uint2& code, uint32_t& word) {
+  uint32_t m = raw.max_bits();
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const uint32_t sb = scale_byte(m);
+  float v[16];
+  raw.widen(v);
+  code = codes16(v, scale_up(sb));
+  word = sb << (((threadIdx.x & 7) >> 1) * 8);
+  word |= __shfl_xor_sync(0xffffffffu, word, 2);
+  word |= __shfl_xor_sync(0xffffffffu, word, 4);
+}
 
 }  // namespace mx
 }  // namespace imc
