@@ -405,6 +405,8 @@ int mxfp4_dequantize(const void* q, int64_t batch, int64_t rows, int64_t cols, i
  *   M, N >= 0, K >= 1.  flags: 0 or IMC_ACT_RELU.
  *   workspace  mxfp4_linear_workspace_bytes(M, K, x_dtype) bytes, 16-byte
  *         aligned (rules as gemm_addmm_f32_ws); NULL: from the library's pool.
+ *         0 bytes are needed for an MXFP4 x and for a handful of tokens, which
+ *         the product quantises itself.
  * Non-finite values: a block with a NaN scale makes its row's (w: its
  * column's) outputs NaN; IMC_ACT_RELU turns a NaN into 0, as in the fp32
  * products' epilogue. */
