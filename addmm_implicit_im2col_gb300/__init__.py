@@ -12,7 +12,7 @@ def __getattr__(name):
     if name in ("addmm", "conv2d", "linear", "gemm_addmm_f32", "conv2d_gemm_f32", "linear_f32",
                 "quantize_mxfp4", "dequantize_mxfp4", "linear_mxfp4", "linear_mxfp4_backward",
                 "route_experts", "route_experts_backward", "experts_layout",
-                "experts_linear_mxfp4", "experts_combine", "experts_combine_backward"):
+                "experts_linear_mxfp4", "experts_linear_mxfp4_backward", "experts_combine", "experts_combine_backward"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

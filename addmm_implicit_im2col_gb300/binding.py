@@ -76,6 +76,9 @@ SIGNATURES = {
     "mxfp4_experts_linear_workspace_bytes": (ctypes.c_size_t, [_i64] * 4),
     "mxfp4_experts_linear": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _int] + [_i64] * 5
                              + [_int, _vp, ctypes.c_size_t, _vp]),
+    "mxfp4_experts_weight_grad_workspace_bytes": (ctypes.c_size_t, [_i64] * 5),
+    "mxfp4_experts_weight_grad": (_int, [_vp, _vp, _int, _i64, _vp, _vp] + [_i64] * 5
+                                  + [_vp, ctypes.c_size_t, _vp]),
     "moe_combine": (_int, [_vp, _int, _vp, _i64, _i64, _i64, _vp, _vp]),
     "moe_combine_backward": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "imc_status_string": (ctypes.c_char_p, [_int]),
@@ -262,6 +265,16 @@ def mxfp4_experts_linear(x, x_dtype, x_rows, row_stride, w, bias, layout, out, o
     return load().mxfp4_experts_linear(x, x_dtype, x_rows, row_stride, w, bias, layout, out,
                                        out_dtype, T, k, E, N, K, flags, workspace,
                                        workspace_bytes, stream)
+
+
+def mxfp4_experts_weight_grad_workspace_bytes(T, k, E, N, K) -> int:
+    return int(load().mxfp4_experts_weight_grad_workspace_bytes(T, k, E, N, K))
+
+
+def mxfp4_experts_weight_grad(grad, x, dtype, x_rows, layout, grad_w, T, k, E, N, K, workspace,
+                              workspace_bytes, stream) -> int:
+    return load().mxfp4_experts_weight_grad(grad, x, dtype, x_rows, layout, grad_w, T, k, E, N, K,
+                                            workspace, workspace_bytes, stream)
 
 
 def moe_combine(y, dtype, weights, T, k, N, out, stream) -> int:
@@ -813,6 +826,47 @@ def experts_linear_mxfp4(x, w, layout, bias=None, *, relu=False, out_dtype=None)
     if rc:
         raise ImcError(rc, "mxfp4_experts_linear")
     return out
+
+
+def experts_linear_mxfp4_backward(grad, x, w, layout):
+    """Gradients of ``experts_linear_mxfp4(x, quantize_mxfp4(w), layout)`` (without bias and ReLU).
+
+    grad [T * k, N], x [T, K] or [T * k, K], w [E, N, K] are contiguous and of one
+    float type.  Returns (grad_x of x's shape, grad_w [E, N, K]), 4-bit products whose
+    operands are quantised along the axis that they sum over; a token's gradient is the
+    sum over its slots, an expert without slots has a gradient of 0.
+    """
+    dt, (slots, N), _ = _rows_of(grad, "grad")
+    if not isinstance(layout, ExpertsLayout):
+        raise TypeError("layout must be an ExpertsLayout")
+    T, k, E = layout.T, layout.k, layout.E
+    _, (rows, K), _ = _rows_of(x, "x")
+    dtype, device = grad.dtype, grad.device
+    if rows != T and rows != T * k:
+        raise ValueError(f"x must have {T} or {T * k} rows, got {rows}")
+    _check_plain(grad, "grad", dtype, (T * k, N), grad)
+    _check_plain(x, "x", dtype, (rows, K), grad)
+    _check_plain(w, "w", dtype, (E, N, K), grad)
+    if layout.data.device != device:
+        raise ValueError("grad and layout must be on one device")
+    if T == 0:
+        return _torch.zeros_like(x), _torch.zeros_like(w)
+    grad_x = experts_linear_mxfp4(grad, quantize_mxfp4(w, transpose=True), layout)
+    if rows != T * k:
+        slot_grads, grad_x = grad_x, _torch.empty((T, K), dtype=dtype, device=device)
+        rc = _lib.moe_combine(slot_grads.data_ptr(), dt, None, T, k, K, grad_x.data_ptr(),
+                              _stream_of(grad))
+        if rc:
+            raise ImcError(rc, "moe_combine")
+    grad_w = _torch.empty((E, N, K), dtype=dtype, device=device)
+    nbytes = mxfp4_experts_weight_grad_workspace_bytes(T, k, E, N, K)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    rc = _lib.mxfp4_experts_weight_grad(grad.data_ptr(), x.data_ptr(), dt, rows,
+                                        layout.data.data_ptr(), grad_w.data_ptr(), T, k, E, N, K,
+                                        ws.data_ptr(), nbytes, _stream_of(grad))
+    if rc:
+        raise ImcError(rc, "mxfp4_experts_weight_grad")
+    return grad_x, grad_w
 
 
 def _combine_dims(y, weights):

@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(kLayoutThreads) k_layout_place(const LayoutArg
 }
 
 // ------------------------------------------------------------ weighted sum
-// out[t] = sum_s w[t,s] * y[t*k + s], in the order of s, fp32; a thread has 8
-// columns of one token.
+// out[t] = sum_s w[t,s] * y[t*k + s] (w null: ones), in the order of s, fp32; a
+// thread has 8 columns of one token.
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_combine(const T* __restrict__ y, const float* __restrict__ w, const int64_t T_, const int k,
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(256)
       for (int u = 0; u < 4; ++u) load8<T>(row + (s + u) * N, n, vec, v[u]);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float ws = __ldg(w + t * k + s + u);
+        const float ws = w ? __ldg(w + t * k + s + u) : 1.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = fmaf(ws, v[u][j], acc[j]);
       }
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(256)
     for (; s < k; ++s) {
       float v[8];
       load8<T>(row + s * N, n, vec, v);
-      const float ws = __ldg(w + t * k + s);
+      const float ws = w ? __ldg(w + t * k + s) : 1.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = fmaf(ws, v[j], acc[j]);
     }

@@ -44,6 +44,9 @@
 // memory, so that a decoding step's product is one launch without scratch; every
 // CTA repeats that small work (the rule: product_fused).
 //
+// The gradient of the experts' weights (GROUPS) has both operands along the rows
+// in expert order; every expert sums over its own run of them.
+//
 // Persistent CTAs walk the tiles.  In the experts' form a tile is (expert, rows
 // of that expert, n); the row counts are only known on the GPU, so every CTA
 // sums them up at its start.
@@ -231,7 +234,7 @@ __device__ __forceinline__ void quantize_row(const ProductArgs& p, int64_t row, 
   if ((l & 1) == 0) scales[(b >> 2) * ATOM_BYTES + r * 16 + (b & 3)] = (uint8_t)sb;
 }
 
-template <int BN, bool PAIR, bool EXPERTS, bool SPLIT, bool FUSED>
+template <int BN, bool PAIR, bool EXPERTS, bool SPLIT, bool FUSED, bool GROUPS>
 __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
     k_mx_gemm(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
               const __grid_constant__ CUtensorMap tmWs, const __grid_constant__ CUtensorMap tmXs,
@@ -242,6 +245,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
   const int splits = SPLIT ? 1 << log_splits : 1;
   static_assert(!SPLIT || (!PAIR && !EXPERTS), "split form");
   static_assert(!FUSED || BN == 32, "fused form");
+  static_assert(!GROUPS || (!EXPERTS && !SPLIT && !FUSED), "groups form");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = tc::smem_align1024(smem_raw);
   float* part = reinterpret_cast<float*>(smem + STAGES * F::STAGE);  // SPLIT: [src][token][128 / S]
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
   // this CTA's blocks of K
   const int all_kb = (int)((p.K + KB - 1) / KB);
   const int kb0 = SPLIT ? (int)(((int64_t)all_kb * slice) >> log_splits) : 0;
-  const int num_kb = SPLIT ? (int)(((int64_t)all_kb * (slice + 1)) >> log_splits) : all_kb;
+  const int own_kb = SPLIT ? (int)(((int64_t)all_kb * (slice + 1)) >> log_splits) : all_kb;
   int* wd = &g_watchdog_mx;
 
   if (threadIdx.x == 0) {
@@ -309,6 +313,10 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
       }
     }
   }
+  if (GROUPS) {
+    ptx::griddep_wait();
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) ctl->start[e] = p.starts[e];
+  }
   ptx::tc_fence_before();
   __syncthreads();
   if (PAIR || SPLIT) ptx::cluster_sync();  // the other CTAs' barriers are ready
@@ -316,13 +324,21 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   volatile int* abort = &ctl->abort;
   const int num_tiles =
-      EXPERTS ? __shfl_sync(0xffffffffu, ctl->tiles_before[p.E + 1], 0) : num_m * num_n;
+      EXPERTS ? __shfl_sync(0xffffffffu, ctl->tiles_before[p.E + 1], 0) : num_m * num_n * (GROUPS ? p.E : 1);
+  // first value and number of values of K that a tile sums over
+  auto first_k = [&](int t) { return GROUPS ? ctl->start[t / (num_m * num_n)] : 0; };
+  auto depth = [&](int t) {
+    if (!GROUPS) return p.K;
+    const int e = t / (num_m * num_n);
+    return (int64_t)(ctl->start[e + 1] - ctl->start[e]);
+  };
+  auto blocks_of = [&](int t) { return GROUPS ? (int)((depth(t) + KB - 1) / KB) : own_kb; };
 
   auto tile_of = [&](int t) {
     Tile r;
     if (!EXPERTS) {
       int mt, nt;
-      tc::tile_coords(t, num_m, num_n, group, mt, nt);
+      tc::tile_coords(GROUPS ? t % (num_m * num_n) : t, num_m, num_n, group, mt, nt);
       r.e = 0;
       r.n0 = nt * F::BNW + rank * BM;
       r.m0 = mt * BN;
@@ -354,15 +370,16 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
     // registers one by one before every instruction (measured in the MMA warp:
     // 690 against the 512 cycles that the MMAs of a stage take).
     // After a pre-pass of this call the weight is known to be there.
-    if (!EXPERTS && !p.inputs_ready) ptx::griddep_wait();
-    bool tokens_ready = EXPERTS || !p.inputs_ready;
+    if (!EXPERTS && !GROUPS && !p.inputs_ready) ptx::griddep_wait();
+    bool tokens_ready = EXPERTS || GROUPS || !p.inputs_ready;
     int s = 0, issued = 0;
     uint32_t ph = 0;
     for (int t = unit; t < num_tiles && !*abort; t += units) {
       const Tile r = tile_of(t);
       if (EXPERTS && r.e == p.E) break;  // only tiles of no expert follow
-      const int xa = r.m0 / F::ATOM_TOKENS;
+      const int xa = r.m0 / F::ATOM_TOKENS, k0 = first_k(t), num_kb = blocks_of(t);
       for (int kb = kb0; kb < num_kb; ++kb) {
+        const int kc = k0 / 2 + kb * (KB / 2), ks = k0 + kb * KB;  // bytes of codes, words of scales
         if (!wait_any<PAIR>(&ctl->empty[s], ph ^ 1u, abort, tc::kSiteProducerEmpty, wd)) break;
         __syncwarp();
         uint8_t* st = smem + s * F::STAGE;
@@ -372,11 +389,11 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
             ptx::mbar_arrive_expect_tx(&ctl->full[s], FUSED ? A_BYTES + F::SA_BYTES : F::TX);
           if (PAIR) {
             const uint32_t bar = ptx::cluster_addr(&ctl->full[s], 0);
-            ptx::tma_load_3d_pair(st, &tmW, bar, kb * (KB / 2), r.n0, r.e);
-            ptx::tma_load_3d_pair(sf, &tmWs, bar, kb * KB, r.n0 / BM, r.e);
+            ptx::tma_load_3d_pair(st, &tmW, bar, kc, r.n0, r.e);
+            ptx::tma_load_3d_pair(sf, &tmWs, bar, ks, r.n0 / BM, r.e);
           } else {
-            ptx::tma_load_3d(st, &tmW, &ctl->full[s], kb * (KB / 2), r.n0, r.e);
-            ptx::tma_load_3d(sf, &tmWs, &ctl->full[s], kb * KB, r.n0 / BM, r.e);
+            ptx::tma_load_3d(st, &tmW, &ctl->full[s], kc, r.n0, r.e);
+            ptx::tma_load_3d(sf, &tmWs, &ctl->full[s], ks, r.n0 / BM, r.e);
           }
         }
         if (!tokens_ready) ptx::griddep_wait();
@@ -384,11 +401,11 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
         if (!FUSED && ptx::elect_one()) {
           if (PAIR) {
             const uint32_t bar = ptx::cluster_addr(&ctl->full[s], 0);
-            ptx::tma_load_2d_pair(st + A_BYTES, &tmX, bar, kb * (KB / 2), r.m0 + rank * F::B_ROWS);
-            ptx::tma_load_2d_pair(sf + F::SA_BYTES, &tmXs, bar, kb * KB, xa);
+            ptx::tma_load_2d_pair(st + A_BYTES, &tmX, bar, kc, r.m0 + rank * F::B_ROWS);
+            ptx::tma_load_2d_pair(sf + F::SA_BYTES, &tmXs, bar, ks, xa);
           } else {
-            ptx::tma_load_2d(st + A_BYTES, &tmX, &ctl->full[s], kb * (KB / 2), r.m0);
-            ptx::tma_load_2d(sf + F::SA_BYTES, &tmXs, &ctl->full[s], kb * KB, xa);
+            ptx::tma_load_2d(st + A_BYTES, &tmX, &ctl->full[s], kc, r.m0);
+            ptx::tma_load_2d(sf + F::SA_BYTES, &tmXs, &ctl->full[s], ks, xa);
           }
         }
         __syncwarp();
@@ -418,13 +435,15 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
       const uint64_t da0 = ptx::smem_desc(base, 16, 1024, ptx::kSwizzle128B);
       const uint64_t db0 = ptx::smem_desc(base + A_BYTES, 16, 1024, ptx::kSwizzle128B);
       const uint64_t ds0 = ptx::smem_desc(base + A_BYTES + F::B_BYTES, 16, 128, 0);
-      const int num_ks = (int)((p.K + KSTEP - 1) / KSTEP);
       int s = 0, tl = 0, set = 0;
       int old = 0;             // the stage whose block had this block's scale columns
       uint32_t ph = 0, old_ph = 0;
       int block = 0;
-      for (int t = unit; t < num_tiles; t += units, ++tl) {
+      for (int t = unit; t < num_tiles; t += units) {
         if (EXPERTS && t >= ctl->tiles_before[p.E]) break;
+        const int num_kb = __shfl_sync(0xffffffffu, blocks_of(t), 0);
+        const int num_ks = __shfl_sync(0xffffffffu, (int)((depth(t) + KSTEP - 1) / KSTEP), 0);
+        if (GROUPS && num_kb == 0) continue;  // an expert without rows: zeros
         const int buf = tl & 1;
         // the accumulator is free: the tile two before (overlapping ones: the
         // part shared with the tile before) has been read
@@ -489,6 +508,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
           }
         }
         if (!ok) break;
+        ++tl;
       }
       // Every MMA issued must be done before TMEM is released.
       __syncwarp();
@@ -504,7 +524,8 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
     int tl = 0;
     for (int t = unit; t < num_tiles; t += units) {
       const Tile r = tile_of(t);
-      const bool none = EXPERTS && r.e == p.E;  // slots of no expert: zeros
+      // zeros: slots of no expert, the gradient of an expert without rows
+      const bool none = (EXPERTS && r.e == p.E) || (GROUPS && depth(t) == 0);
       const int buf = tl & 1;
       const int64_t n = r.n0 + q * 32 + lane;
       const bool in = n < p.N;
@@ -522,8 +543,8 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
       if (FUSED && !none) {
         // this warp's blocks of K: wait for the stage, write the tokens' rows
         bool ok = true;
-        for (int kb = kb0 + warp - 2; kb < num_kb; kb += EPI_WARPS) {
-          const int block = tl * (num_kb - kb0) + kb - kb0, st = block % STAGES;
+        for (int kb = kb0 + warp - 2; kb < own_kb; kb += EPI_WARPS) {
+          const int block = tl * (own_kb - kb0) + kb - kb0, st = block % STAGES;
           ok = wait_any<false>(&ctl->empty[st], ((uint32_t)(block / STAGES) & 1u) ^ 1u, abort,
                                tc::kSiteProducerEmpty, wd);
           if (!ok) break;
@@ -601,7 +622,8 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
             v[j] = __float_as_uint(y);
           }
         }
-        const int64_t at = (EXPERTS ? 0 : (int64_t)(r.m0 + c) * p.N) + r.n0 + q * 32;
+        const int64_t at =
+            (EXPERTS ? 0 : ((GROUPS ? t / (num_m * num_n) * p.M : 0) + r.m0 + c) * p.N) + r.n0 + q * 32;
         auto f32 = [](uint32_t b) { return b; };
         auto bf16 = [](uint32_t b) { return bf16_bits(__uint_as_float(b)); };
         auto f16 = [](uint32_t b) { return half_bits(__uint_as_float(b)); };
@@ -717,12 +739,13 @@ bool encode_scales(CUtensorMap* m, const uint8_t* q, const Store& st, uint32_t b
 
 constexpr int kMaxDev = 64;
 
-template <int BN, bool PAIR, bool EXPERTS, bool SPLIT = false, bool FUSED = false>
+template <int BN, bool PAIR, bool EXPERTS, bool SPLIT = false, bool FUSED = false,
+          bool GROUPS = false>
 cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
   using F = Form<BN, PAIR, EXPERTS>;
   constexpr int smem = smem_bytes<BN, PAIR, EXPERTS, SPLIT>();
   static std::atomic<bool> ready[kMaxDev];  // per device: the attribute is set (calls may race)
-  auto k = k_mx_gemm<BN, PAIR, EXPERTS, SPLIT, FUSED>;
+  auto k = k_mx_gemm<BN, PAIR, EXPERTS, SPLIT, FUSED, GROUPS>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -750,7 +773,7 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
   // experts: at most one partly filled tile per expert beyond the full ones
   const int64_t tiles = EXPERTS ? (p.slots / BN + (p.slots < p.E + 1 ? p.slots : p.E + 1)) *
                                       (int64_t)num_n
-                                : (int64_t)num_m * num_n;
+                                : (int64_t)num_m * num_n * (GROUPS ? p.E : 1);
   if (tiles > 0x7fffffffLL || (SPLIT && tiles > units)) return cudaErrorInvalidValue;
   const int grid = (int)(tiles < units ? tiles : units) * ctas;
   // rows that 16-byte stores can write
@@ -813,6 +836,7 @@ int pick_splits(const ProductArgs& p) {
 cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
   note_kernel_name(p.raw ? (p.E ? "k_mx_gemm<experts,fused>" : "k_mx_gemm<fused>")
                          : (p.E ? "k_mx_gemm<experts>" : "k_mx_gemm"));
+  if (p.groups) return run<256, true, false, false, false, true>(p, s);
   if (p.E) {
     switch (tile_shift(ceil_div(p.slots, p.E))) {
       case 5:

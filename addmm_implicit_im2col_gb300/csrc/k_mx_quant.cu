@@ -97,8 +97,11 @@ struct ColTile {
   static constexpr int COLS = 32 * PER, CTA_COLS = 8 * COLS;
 };
 
-template <typename T, int NB>
+// GATHER (NB == 4): the rows are slots in expert order, every expert's run padded
+// to a multiple of 128, so that a lane's 128 rows belong to one expert.
+template <typename T, int NB, bool GATHER>
 __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, const bool words) {
+  static_assert(!GATHER || NB == 4, "one expert's rows");
   using C = ColTile<T>;
   constexpr int PER = C::PER;
   ptx::griddep_wait();
@@ -116,12 +119,41 @@ __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, const 
     const int64_t atoms = b * st.row_atoms * st.block_atoms * ATOM_BYTES;
     uint32_t word[PER] = {};
     uint4 code[PER][NB];
+    int64_t first = 0, last = 0;  // GATHER: places in `order` of row r0, and past the expert's end
+    if (GATHER) {
+      if (r0 >= a.starts[a.E]) continue;  // rows of no expert
+      int lo = 0, hi = a.E - 1;           // the last expert whose run begins at or before r0
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a.starts[mid] <= r0) lo = mid;
+        else hi = mid - 1;
+      }
+      first = a.offsets[lo] + r0 - a.starts[lo];
+      last = a.offsets[lo + 1];
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int64_t r = r0 + nb * 32;
       const T* p = base + r * a.row_stride + c;
       uint32_t u[32];
-      if (words && c + PER <= a.cols && r + 32 <= a.rows) {
+      if (GATHER) {
+        const int64_t at = first + nb * 32 + lane;
+        const int src = at < last ? a.order[at] / a.share : -1;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int row = __shfl_sync(0xffffffffu, src, j);
+          const T* q = base + (int64_t)row * a.row_stride + c;
+          if (words && row >= 0 && c + PER <= a.cols) {
+            u[j] = __ldg(reinterpret_cast<const uint32_t*>(q));
+          } else {
+            alignas(4) T e[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              e[i] = row >= 0 && c + i < a.cols ? q[i] : from_f32<T>(0.0f);
+            u[j] = *reinterpret_cast<const uint32_t*>(e);
+          }
+        }
+      } else if (words && c + PER <= a.cols && r + 32 <= a.rows) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
           u[j] = __ldg(reinterpret_cast<const uint32_t*>(p + j * a.row_stride));
@@ -387,11 +419,14 @@ cudaError_t quantize(const QuantArgs& a, bool transpose, cudaStream_t s) {
       e = launch_after_previous(k_mx_quant_both<T>,
                                 dim3((unsigned)(tiles < sms * 6 ? tiles : sms * 6)), dim3(256), 0, s,
                                 a, store_of(a.batch, a.rows, a.cols), vec);
+    } else if (a.order) {
+      e = launch_after_previous(k_mx_quant_cols<T, 4, true>,
+                                dim3((unsigned)(four < cap ? four : cap)), dim3(256), 0, s, a, words);
     } else if (four >= 2 * sms) {
-      e = launch_after_previous(k_mx_quant_cols<T, 4>, dim3((unsigned)(four < cap ? four : cap)),
+      e = launch_after_previous(k_mx_quant_cols<T, 4, false>, dim3((unsigned)(four < cap ? four : cap)),
                                 dim3(256), 0, s, a, words);
     } else {
-      e = launch_after_previous(k_mx_quant_cols<T, 1>,
+      e = launch_after_previous(k_mx_quant_cols<T, 1, false>,
                                 dim3((unsigned)(four * 4 < cap ? four * 4 : cap)), dim3(256), 0, s,
                                 a, words);
     }

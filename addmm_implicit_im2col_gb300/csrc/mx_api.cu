@@ -458,13 +458,82 @@ int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row
   return finish_call(sc.give(e), IMC_KERNEL_MXFP4);
 }
 
+size_t mxfp4_experts_weight_grad_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N,
+                                                 int64_t K) {
+  if (moe_layout_size(T, k, E) == 0 || T == 0 || !dims_ok(0, N, K)) return 0;
+  const int64_t rows = sorted_rows(T * k, E);
+  if (rows > kMaxDim || !store_ok(1, N, rows) || !store_ok(1, K, rows)) return 0;
+  return (size_t)(ceil_div(store_of(1, N, rows).bytes, 512) * 512 + store_of(1, K, rows).bytes);
+}
+
+int mxfp4_experts_weight_grad(const void* grad, const void* x, int dtype, int64_t x_rows,
+                              const int32_t* layout, void* grad_w, int64_t T, int64_t k, int64_t E,
+                              int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (!float_type(dtype)) return IMC_ERR_ARG;
+  const int64_t size = moe_layout_size(T, k, E), n = T * k;
+  if (size == 0 || T == 0 || !dims_ok(x_rows, N, K) || N == 0 || K == 0 ||
+      (x_rows != T && x_rows != n) || sorted_rows(n, E) > kMaxDim ||
+      !store_ok(1, N, sorted_rows(n, E)) || !store_ok(1, K, sorted_rows(n, E)) ||
+      (double)E * N * K > kMaxBytes)
+    return IMC_ERR_SHAPE;
+  if (!grad || !x || !layout || !grad_w) return IMC_ERR_NULL;
+  const uint64_t b = (uint64_t)dtype_bytes(dtype);
+  if (!aligned(grad, b) || !aligned(x, b) || !aligned(grad_w, b) || !aligned(layout, 4))
+    return IMC_ERR_ARG;
+  const size_t need = mxfp4_experts_weight_grad_workspace_bytes(T, k, E, N, K);
+  const int ws = check_workspace(workspace, workspace_bytes, need);
+  if (ws != IMC_OK) return ws;
+  const uint64_t out_bytes = (uint64_t)E * N * K * b;
+  const void* in[3] = {grad, x, layout};
+  const uint64_t in_bytes[3] = {(uint64_t)n * N * b, (uint64_t)x_rows * K * b, (uint64_t)size * 4};
+  for (int i = 0; i < 3; ++i)
+    if (ranges_overlap(grad_w, out_bytes, in[i], in_bytes[i]) ||
+        ranges_overlap(workspace, need, in[i], in_bytes[i]))
+      return IMC_ERR_ALIAS;
+  if (ranges_overlap(workspace, need, grad_w, out_bytes)) return IMC_ERR_ALIAS;
+  const int dev = require_device();
+  if (dev != IMC_OK) return dev;
+  if (!product_supported()) return IMC_ERR_DEVICE;
+  cudaStream_t s = (cudaStream_t)stream;
+  Scratch sc(s);
+  if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
+  const int64_t rows = sorted_rows(n, E);
+  uint8_t* g_cols = static_cast<uint8_t*>(sc.p);
+  uint8_t* x_cols = g_cols + ceil_div(store_of(1, N, rows).bytes, 512) * 512;
+  auto quantize = [&](const void* src, int64_t cols, int share, uint8_t* q) {
+    QuantArgs a = quant_args(src, 1, rows, cols, 0, cols, true, q);
+    a.offsets = layout;
+    a.starts = layout + E + 2;
+    a.order = a.starts + E + 1;
+    a.E = (int)E;
+    a.share = share;
+    return launch_quantize(a, dtype, true, s);
+  };
+  cudaError_t e = quantize(grad, N, 1, g_cols);
+  if (e == cudaSuccess) e = quantize(x, K, x_rows == n ? 1 : (int)k, x_cols);
+  ProductArgs p = {};
+  p.x = g_cols;
+  p.w = x_cols;
+  p.out = grad_w;
+  p.out_dtype = dtype;
+  p.M = p.x_rows = N;
+  p.N = K;
+  p.K = rows;
+  p.E = (int)E;
+  p.starts = layout + E + 2;
+  p.groups = true;
+  if (e == cudaSuccess) e = launch_product(p, s);
+  return finish_call(sc.give(e), IMC_KERNEL_MXFP4);
+}
+
 int moe_combine(const void* y, int dtype, const float* weights, int64_t T, int64_t k, int64_t N,
                 void* out, void* stream) {
   if (!float_type(dtype)) return IMC_ERR_ARG;
   if (!dims_ok(T, k, N) || k < 1 || k > kMaxChosen || (double)T * k * N > kMaxBytes)
     return IMC_ERR_SHAPE;
   if (T == 0 || N == 0) return finish_empty();
-  if (!y || !weights || !out) return IMC_ERR_NULL;
+  if (!y || !out) return IMC_ERR_NULL;
   const uint64_t b = (uint64_t)dtype_bytes(dtype), out_bytes = (uint64_t)T * N * b;
   if (!aligned(y, b) || !aligned(out, b) || !aligned(weights, 4)) return IMC_ERR_ARG;
   if (ranges_overlap(out, out_bytes, y, (uint64_t)T * k * N * b) ||

@@ -70,6 +70,10 @@ struct QuantArgs {
   const int32_t* dest;    // rows of the result that row r is written to: dest[r*share ..), or null
   int share;
   uint8_t* q_rows;        // transposed: MXFP4 of x itself as well, or null
+  // transposed, rows in expert order: row r of the `rows` padded ones is row
+  // order[...] / share of x, or zeros (layout of moe_layout; null: x's own rows)
+  const int32_t *offsets, *starts, *order;
+  int E;
 };
 
 // One product: out[token, n] = sum_k x[token, k] * w[n, k] (+ bias[n]) (ReLU).
@@ -84,6 +88,9 @@ struct ProductArgs {
   int E;
   const int32_t *offsets, *starts, *order;
   int slots;              // T * k
+  // weights' gradient: both operands lie along the sorted rows, out is [E][M][N]
+  // and its part e sums over rows starts[e] .. starts[e + 1]
+  bool groups;
   bool inputs_ready;      // a pre-pass of this call has waited for earlier kernels
   // few tokens: unquantised x instead of p.x (product_fused)
   const void* raw;        // row of token m, or of slot s: raw + (m or s / share) * raw_stride

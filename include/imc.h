@@ -483,8 +483,23 @@ int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row
                          int out_dtype, int64_t T, int64_t k, int64_t E, int64_t N, int64_t K,
                          int flags, void* workspace, size_t workspace_bytes, void* stream);
 
-/* out[t] = sum_i weights[t,i] * y[t*k + i], in the order of i, summed in fp32.
- * y [T*k,N], out [T,N] contiguous, of type dtype. */
+/* Gradient of mxfp4_experts_linear's weights: grad_w[e] = q(G^T) . q(X^T)^T, where
+ * the rows of G [.,N] and X [.,K] are grad and x rows of expert e's slots, in the
+ * order of the layout, and both operands are quantised along them (blocks of 32
+ * slots of one expert).  grad [T*k,N], x [x_rows,K] (T or T*k rows), grad_w
+ * [E,N,K] are contiguous and of type dtype; an expert without slots gets 0.
+ * T, N, K >= 1; workspace as above.  (The gradient of x is mxfp4_experts_linear
+ * of grad with the transposed weights, and for x_rows == T moe_combine of that
+ * without weights.) */
+size_t mxfp4_experts_weight_grad_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N,
+                                                 int64_t K);
+int mxfp4_experts_weight_grad(const void* grad, const void* x, int dtype, int64_t x_rows,
+                              const int32_t* layout, void* grad_w, int64_t T, int64_t k, int64_t E,
+                              int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* out[t] = sum_i weights[t,i] * y[t*k + i], in the order of i, summed in fp32
+ * (weights NULL: all 1).  y [T*k,N], out [T,N] contiguous, of type dtype. */
 int moe_combine(const void* y, int dtype, const float* weights, int64_t T, int64_t k, int64_t N,
                 void* out, void* stream);
 

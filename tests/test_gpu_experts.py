@@ -314,6 +314,69 @@ def test_experts_linear_empty():
     assert got.shape == (12, 20) and bool((got == 0).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("per_slot,absent", [(False, False), (True, True), (False, True)])
+@pytest.mark.parametrize("T,k,E,N,K", [(1, 1, 1, 1, 1), (9, 2, 3, 64, 257), (70, 3, 5, 200, 96), (40, 8, 64, 129, 33),
+                                       (500, 2, 2, 300, 600), (700, 1, 3, 257, 130)])
+def test_experts_linear_backward_is_the_formula(T, k, E, N, K, per_slot, absent, dtype):
+    experts = some_experts(T + 1, T, k, E, absent)
+    layout = binding.experts_layout(experts, E)
+    grad, x = spread(1, T * k, N, dtype), spread(2, T * k if per_slot else T, K, dtype)
+    w = spread(3, E * N, K, dtype).view(E, N, K)
+    gx, gw = binding.experts_linear_mxfp4_backward(grad, x, w, layout)
+    flat, g64, x64 = experts.reshape(-1).cpu().numpy(), f64(grad), f64(x)
+    y, s = np.zeros((T * k, K)), np.zeros((T * k, K))
+    gq = mx_blocks(g64)[0]
+    for e in range(E):
+        at = np.nonzero(flat == e)[0]
+        if len(at) == 0:
+            assert bool((gw[e] == 0).all())
+            continue
+        y[at], s[at] = product_case(gq[at], mx_blocks(f64(w[e]).T)[0])
+        want, size = product_case(mx_blocks(g64[at].T)[0], mx_blocks(x64[at if per_slot else at // k].T)[0])
+        check(gw[e], want, size, len(at), dtype)
+    if per_slot:
+        check(gx, y, s, N, dtype)
+    else:  # each slot's product is rounded to the type, then the slots are summed
+        y3, s3 = y.reshape(T, k, K), s.reshape(T, k, K)
+        tol = ((N / 64 + 2) * 2.0 ** -23 * s3 + HALF_ULP[dtype] * np.abs(y3)).sum(1)
+        tol = 1.02 * tol + k * EPS * np.abs(y3).sum(1) + HALF_ULP[dtype] * np.abs(y3).sum(1)
+        assert (np.abs(f64(gx) - y3.sum(1)) <= tol).all()
+    assert binding.check_device_error() == binding.IMC_OK
+
+
+def test_experts_linear_backward_is_the_difference():
+    """On values that MXFP4 holds along both axes, gradients are exact differences."""
+    T, k, E, N, K = 40, 2, 3, 32, 64
+    g = torch.Generator().manual_seed(7)
+
+    def values(rows, cols):
+        v = torch.tensor([-4.0, -2.0, -1.0, 1.0, 2.0, 4.0])[torch.randint(0, 6, (rows, cols), generator=g)]
+        v[::2, ::2] = 4.0  # a largest value in every block, whatever the order of the rows
+        v[1::2, 1::2] = -4.0
+        return v
+
+    experts = some_experts(3, T, k, E)
+    layout = binding.experts_layout(experts, E)
+    x, grad = values(T, K).cuda(), values(T * k, N).cuda()
+    w = values(E * N, K).view(E, N, K).cuda()
+    gx, gw = binding.experts_linear_mxfp4_backward(grad, x, w, layout)
+
+    def f(x_, w_):
+        y = binding.experts_linear_mxfp4(x_, binding.quantize_mxfp4(w_), layout)
+        return (grad.double() * y.double()).sum().item()
+
+    base = f(x, w)
+    for i, j in ((0, 1), (17, 4), (39, 62)):
+        x2 = x.clone()
+        x2[i, j] = 3.0
+        assert f(x2, w) - base == gx[i, j].item() * (3.0 - x[i, j].item())
+    for e, i, j in ((0, 0, 1), (1, 31, 62), (2, 6, 33)):
+        w2 = w.clone()
+        w2[e, i, j] = -3.0
+        assert f(x, w2) - base == gw[e, i, j].item() * (-3.0 - w[e, i, j].item())
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("T,k,N", [(1, 1, 1), (1, 8, 2048), (33, 3, 7), (100, 5, 129), (300, 8, 512), (9, 32, 40)])
 def test_combine_and_gradients(T, k, N, dtype):

@@ -57,6 +57,12 @@ def experts_linear(x=P1, x_dtype=0, rows=400, row_stride=64, w=P2, bias=None, la
                                         out_dtype, T, k, E, N, K, flags, ws, nbytes, None)
 
 
+def weight_grad(grad=P1, x=P2, dtype=0, rows=4, layout=P3, gw=P4, T=4, k=2, E=16, N=8, K=64, ws=P5,
+                nbytes=1 << 22):
+    return binding.mxfp4_experts_weight_grad(grad, x, dtype, rows, layout, gw, T, k, E, N, K, ws,
+                                             nbytes, None)
+
+
 def combine(y=P1, dtype=0, w=P2, T=4, k=2, N=8, out=P3):
     return binding.moe_combine(y, dtype, w, T, k, N, out, None)
 
@@ -100,7 +106,10 @@ BAD = [
     (experts_linear, dict(w=None), NULL), (experts_linear, dict(nbytes=100), ARG),
     (experts_linear, dict(out=P1), ALIAS), (experts_linear, dict(out=P3), ALIAS), (experts_linear, dict(ws=P4), ALIAS),
     (combine, dict(dtype=3), ARG), (combine, dict(k=0), SHAPE), (combine, dict(y=None), NULL),
-    (combine, dict(out=P1), ALIAS), (combine, dict(w=None), NULL),
+    (combine, dict(out=P1), ALIAS), (combine, dict(out=None), NULL),
+    (weight_grad, dict(dtype=3), ARG), (weight_grad, dict(rows=5), SHAPE), (weight_grad, dict(T=0), SHAPE),
+    (weight_grad, dict(N=0), SHAPE), (weight_grad, dict(x=None), NULL), (weight_grad, dict(layout=None), NULL),
+    (weight_grad, dict(nbytes=64), ARG), (weight_grad, dict(gw=P1), ALIAS), (weight_grad, dict(ws=P4), ALIAS),
     (combine_backward, dict(dtype=3), ARG), (combine_backward, dict(T=-1), SHAPE),
     (combine_backward, dict(gy=None), NULL), (combine_backward, dict(gy=P2), ALIAS),
     (combine_backward, dict(gw=P4), ALIAS),
@@ -150,6 +159,7 @@ def test_without_a_gpu_calls_fail_loudly():
              ("moe_route_backward", [P1, P2, 0, 4, 16, 16, P3, 2, 0, 1, 1.0, P4, None]),
              ("moe_layout", [P1, 4, 2, 8, P2, None]),
              ("mxfp4_experts_linear", [P1, 0, 4, 64, P2, None, P3, P4, 0, 4, 2, 16, 8, 64, 0, P5, 1 << 22, None]),
+             ("mxfp4_experts_weight_grad", [P1, P2, 0, 4, P3, P4, 4, 2, 16, 8, 64, P5, 1 << 22, None]),
              ("moe_combine", [P1, 0, P2, 4, 2, 8, P3, None]),
              ("moe_combine_backward", [P1, P2, 0, P3, 4, 2, 8, P4, P5, None])]
     assert without_gpu(calls) == [binding.IMC_ERR_DEVICE] * len(calls)
