@@ -39,10 +39,12 @@
 // (CTA r sums rows r * 128 / S .. of n) and the sums are taken in the order of
 // the CTAs, so a result does not depend on timing (the rule: pick_splits).
 //
-// A handful of tokens (FUSED): the epilogue warps, idle until the accumulator is
-// done, quantise the token rows of a stage themselves into the stage's shared
-// memory, so that a decoding step's product is one launch without scratch; every
-// CTA repeats that small work (the rule: product_fused).
+// A handful of tokens (FUSED): warps that are idle until an accumulator is done
+// (in the experts' form all but four of the epilogue's, which then run ahead of
+// the tile being drained) quantise the token rows of a stage themselves into the
+// stage's shared memory, so that a decoding step's product is one launch without
+// scratch; every CTA repeats that small work (the rules: product_fused,
+// experts_fused).
 //
 // The gradient of the experts' weights (GROUPS) has both operands along the rows
 // in expert order; every expert sums over its own run of them.
@@ -242,6 +244,9 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
               const int log_splits, const int wide_rows) {
   using F = Form<BN, PAIR, EXPERTS>;
   constexpr int STAGES = F::STAGES, EPI_WARPS = epi_warps(EXPERTS), TURNS = EPI_WARPS / 4;
+  // the experts' fused form: a tile has one chunk, so all but four epilogue warps
+  // are free to quantise, ahead of the tiles being drained
+  constexpr bool QUANTISERS = FUSED && EXPERTS;
   const int splits = SPLIT ? 1 << log_splits : 1;
   static_assert(!SPLIT || (!PAIR && !EXPERTS), "split form");
   static_assert(!FUSED || BN == 32, "fused form");
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&ctl->accf[b], 1);
-      ptx::mbar_init(&ctl->acce[b], PAIR ? 2 * EPI_WARPS : EPI_WARPS);
+      ptx::mbar_init(&ctl->acce[b], QUANTISERS ? 4 : (PAIR ? 2 * EPI_WARPS : EPI_WARPS));
     }
     ptx::mbar_init(&ctl->drain, 1);
     if (SPLIT) ptx::mbar_init(&ctl->part, (uint32_t)(splits * EPI_WARPS));
@@ -522,7 +527,44 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
     const int q = warp & 3;               // TMEM lane quadrant this warp may read
     const int turn = (warp - 2) >> 2;     // it takes every TURNS-th chunk of 32 tokens
     int tl = 0;
-    for (int t = unit; t < num_tiles; t += units) {
+    // FUSED: the blocks of K of a tile that are warp `w`'s, every one whose stage is
+    // w (a warp that skipped a use of its stage would take an old phase of the
+    // stage's barrier for the one it waits for): wait for the stage, write the
+    // tokens' rows.  `before`: blocks of earlier tiles.
+    auto quantize_tile = [&](const Tile& r, int before, int w) {
+      int kb = kb0 + (w - before % STAGES + STAGES) % STAGES;
+      for (; kb < own_kb; kb += STAGES) {
+        const int block = before + kb - kb0;
+        if (!wait_any<false>(&ctl->empty[w], ((uint32_t)(block / STAGES) & 1u) ^ 1u, abort,
+                             tc::kSiteProducerEmpty, wd))
+          return false;
+        __syncwarp();
+        uint8_t* tile = smem + w * F::STAGE + A_BYTES;
+        uint8_t* scales = tile + F::B_BYTES + F::SA_BYTES;
+        for (int j = 0; j < r.rows; j += 2) {
+          const int m = j + (lane >> 4);  // half-warps take neighbouring rows
+          int64_t row = -1;
+          if (m < r.rows) row = EXPERTS ? __ldg(p.order + r.first + m) / p.share : r.m0 + m;
+          if (p.raw_dtype == IMC_F32) quantize_row<float>(p, row, kb, m, tile, scales);
+          else if (p.raw_dtype == IMC_BF16) quantize_row<__nv_bfloat16>(p, row, kb, m, tile, scales);
+          else quantize_row<__half>(p, row, kb, m, tile, scales);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ctl->full[w]);
+      }
+      return true;
+    };
+    if (QUANTISERS && turn > 0) {
+      const int w = warp - 2 - 4;
+      int before = 0;
+      for (int t = unit; w < STAGES && t < num_tiles; t += units) {
+        const Tile r = tile_of(t);
+        if (r.e == p.E || !quantize_tile(r, before, w)) break;
+        before += own_kb - kb0;
+      }
+    }
+    for (int t = unit; (!QUANTISERS || turn == 0) && t < num_tiles; t += units) {
       const Tile r = tile_of(t);
       // zeros: slots of no expert, the gradient of an expert without rows
       const bool none = (EXPERTS && r.e == p.E) || (GROUPS && depth(t) == 0);
@@ -540,30 +582,9 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
         return EXPERTS && i < BN / 32 && c < r.rows ? __ldg(p.order + r.first + c) : 0;
       };
       int slot = slots(turn);
-      if (FUSED && !none) {
-        // this warp's blocks of K: wait for the stage, write the tokens' rows
-        bool ok = true;
-        for (int kb = kb0 + warp - 2; kb < own_kb; kb += EPI_WARPS) {
-          const int block = tl * (own_kb - kb0) + kb - kb0, st = block % STAGES;
-          ok = wait_any<false>(&ctl->empty[st], ((uint32_t)(block / STAGES) & 1u) ^ 1u, abort,
-                               tc::kSiteProducerEmpty, wd);
-          if (!ok) break;
-          __syncwarp();
-          uint8_t* tile = smem + st * F::STAGE + A_BYTES;
-          uint8_t* scales = tile + F::B_BYTES + F::SA_BYTES;
-          for (int j = 0; j < r.rows; j += 2) {
-            const int m = j + (lane >> 4);  // half-warps take neighbouring rows
-            int64_t row = -1;
-            if (m < r.rows) row = EXPERTS ? __ldg(p.order + r.first + m) / p.share : r.m0 + m;
-            if (p.raw_dtype == IMC_F32) quantize_row<float>(p, row, kb, m, tile, scales);
-            else if (p.raw_dtype == IMC_BF16) quantize_row<__nv_bfloat16>(p, row, kb, m, tile, scales);
-            else quantize_row<__half>(p, row, kb, m, tile, scales);
-          }
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&ctl->full[st]);
-        }
-        if (!ok) break;
+      if (FUSED && !QUANTISERS && !none) {
+        static_assert(!FUSED || EXPERTS || EPI_WARPS == STAGES, "a stage belongs to one warp");
+        if (!quantize_tile(r, tl * (own_kb - kb0), warp - 2)) break;
       }
       if (!none) {
         int ok = 1;
@@ -809,7 +830,13 @@ namespace {
 int tile_shift(int64_t rows) { return rows <= 32 ? 5 : (rows <= 64 ? 6 : (rows <= 128 ? 7 : 8)); }
 }  // namespace
 
+// Measured fused / with a quantising launch before, us on the GPU in a graph and
+// per call from Python (bf16, K x N = 4096 x 4096): 1 token 5.9 / 6.3 and 11.5 /
+// 16.0, 4 tokens 6.4 / 6.3, 8 tokens 7.3 / 6.5 and 11.1 / 16.5, 16 tokens 9.1 / 7.1.
 bool product_fused(int64_t tokens) { return tokens <= 8; }
+// 64 experts, 2048 x 1024, 4 slots a token: 2 tokens 4.8 / 6.7, 8 tokens 7.3 / 9.3,
+// 32 tokens 11.1 / 13.2; 32 tokens of 8 slots, 1024 x 1024 11.0 / 11.1; 8 experts,
+// 4096 x 2048, 32 slots 9.1 / 8.6.
 bool experts_fused(int64_t slots, int64_t E) { return slots <= 4 * E && slots <= 256; }
 
 int experts_atom_shift(int64_t slots, int64_t E) {

@@ -41,7 +41,9 @@ class ExpertsBlock:
 
     def __call__(self, x):
         """x [tokens, width] float32 -> [tokens, width]."""
-        weights, experts = binding.route_experts(binding.linear(x, self.router), self.k)
+        # few columns and long rows: the tensor cores, whatever the number of tokens
+        logits = binding.linear(x, self.router, mode="force_tc3")
+        weights, experts = binding.route_experts(logits, self.k)
         layout = binding.experts_layout(experts, self.experts)
         h = binding.experts_linear_mxfp4(x, self.up, layout, relu=True)
         y = binding.experts_linear_mxfp4(h, self.down, layout)

@@ -253,7 +253,8 @@ def some_experts(seed, T, k, E, absent=False):
 
 
 EXPERTS = [(1, 1, 1, 1, 1), (1, 4, 16, 130, 100), (9, 2, 3, 64, 257), (70, 3, 5, 200, 96), (40, 8, 64, 129, 320),
-           (300, 4, 7, 260, 64), (500, 2, 2, 128, 600), (700, 1, 2, 300, 129), (130, 6, 8, 100, 1000)]
+           (300, 4, 7, 260, 64), (500, 2, 2, 128, 600), (700, 1, 2, 300, 129), (130, 6, 8, 100, 1000),
+           (2, 2, 4, 200, 4100), (3, 4, 16, 1024, 4096), (1, 8, 64, 2100, 520), (1, 2, 4, 40, 9000)]
 
 
 @pytest.mark.parametrize("per_slot", [False, True])

@@ -159,7 +159,7 @@ MNK = [(1, 1, 1), (1, 129, 33), (2, 7, 64), (31, 128, 256), (32, 127, 257), (33,
        (64, 300, 130), (65, 128, 512), (127, 130, 1000), (128, 256, 63), (129, 100, 128),
        (255, 129, 320), (256, 1, 1056), (257, 257, 257), (700, 520, 2080), (1, 4096, 4096),
        (17, 1001, 1100), (513, 640, 4128), (2000, 1300, 160), (2100, 1100, 700), (4100, 515, 300),
-       (1537, 2050, 1056), (3000, 2000, 31)]
+       (1537, 2050, 1056), (3000, 2000, 31), (3, 40000, 700), (8, 20500, 2100), (5, 300, 6000)]
 
 
 @pytest.mark.parametrize("M,N,K", MNK)
