@@ -176,8 +176,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if (j >= vpt) break;
-      const int c = lane + 32 * j;
+      const int c = lane + 32 * j;  // past the candidates: 0, never chosen
       key[j] = c < a.top_groups * size ? words[padded(expert_of(c))] : 0u;
     }
     __syncwarp();

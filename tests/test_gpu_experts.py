@@ -6,6 +6,8 @@ covers them, with the choice's sum of k scores.  Products as in the MXFP4
 tests.  Weighted sums: k (forward) or N / 32 + 8 (backward, a warp's tree)
 roundings of 2^-24 of the sum of magnitudes, one rounding to the output's type.
 """
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -78,7 +80,9 @@ ROUTES = [(1, 1, 1, "softmax", False, 1, 1), (5, 8, 2, "softmax", False, 1, 1),
           (257, 64, 6, "sigmoid", True, 8, 3), (100, 48, 4, "softmax", False, 4, 2),
           (50, 128, 8, "sigmoid", True, 4, 2), (77, 100, 7, "sigmoid", False, 5, 5),
           (40, 256, 8, "sigmoid", True, 8, 4), (3, 32, 4, "softmax", True, 32, 8),
-          (19, 24, 3, "softmax", False, 24, 4)]
+          (19, 24, 3, "softmax", False, 24, 4), (8, 132, 3, "softmax", True, 4, 2),
+          (30, 255, 6, "sigmoid", True, 5, 1), (12, 300, 4, "sigmoid", True, 10, 2),
+          (9, 1024, 8, "sigmoid", True, 32, 3)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
@@ -98,6 +102,43 @@ def test_route(T, E, k, score, use_bias, groups, top_groups, renormalize, dtype)
     assert np.array_equal(experts.cpu().numpy(), e64)
     assert np.abs(f64(w) - w64).max() <= 16 * EPS * 2.5
     assert (np.abs(f64(w) - w64) <= 16 * EPS * np.abs(w64) + 1e-30).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_route_of_any_sizes(seed):
+    """Sizes, groups and forms drawn over their whole range."""
+    r = random.Random(seed)
+    groups = r.choice([1, 2, 3, 4, 5, 7, 8, 16, 32])
+    E = groups * r.randint(1, (512 if seed % 3 else 1024) // groups)
+    top_groups = r.randint(1, groups)
+    k = r.randint(1, min(32, E // groups * top_groups))
+    score = r.choice(["softmax", "sigmoid"])
+    bias = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(seed))
+    T = r.randint(1, 40)
+    x = clear_logits(seed, T, E, f64(bias), k, score, groups, top_groups, torch.float32)
+    w, experts = binding.route_experts(x, k, bias.cuda(), score=score, groups=groups, top_groups=top_groups)
+    w64, e64 = route64(f64(x), k, f64(bias), score, groups, top_groups, True, 1.0)
+    assert np.array_equal(experts.cpu().numpy(), e64)
+    assert (np.abs(f64(w) - w64) <= 16 * EPS * np.abs(w64) + 1e-30).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_experts_linear_of_any_sizes(seed):
+    r = random.Random(100 + seed)
+    E, T = r.randint(1, 40), int(2 ** r.uniform(0, 9.5))
+    k, N, K = r.randint(1, min(8, E)), int(2 ** r.uniform(0, 9)), int(2 ** r.uniform(0, 11))
+    per_slot, dtype = r.random() < 0.5, r.choice([torch.float32, torch.bfloat16])
+    experts = some_experts(seed, T, k, E, r.random() < 0.5)
+    x, w = spread(1, T * k if per_slot else T, K, dtype), spread(2, E * N, K).view(E, N, K)
+    got = binding.experts_linear_mxfp4(x, binding.quantize_mxfp4(w), binding.experts_layout(experts, E))
+    xq, flat = mx_blocks(f64(x))[0], experts.reshape(-1).cpu().numpy()
+    y, s = np.zeros((T * k, N)), np.zeros((T * k, N))
+    for e in range(E):
+        at = np.nonzero(flat == e)[0]
+        if len(at):
+            y[at], s[at] = product_case(xq[at if per_slot else at // k], mx_blocks(f64(w[e]))[0])
+    check(got, y, s, K, dtype)
+    assert binding.check_device_error() == binding.IMC_OK
 
 
 @pytest.mark.parametrize("E", [300, 512, 1024])
