@@ -32,7 +32,9 @@
 // accumulators of 256 columns overlap in 64 of them, which leaves room for the
 // scales: the epilogue drains the shared columns first and hands them back.  The
 // MMAs run at 9.2 PFLOP/s (7.5 us per 1024 of K at 8192 x 4096, with the
-// epilogue taken out); what is left is the hand-over, ~1.2 us per tile.
+// epilogue taken out); what is left is the hand-over, ~1.2 us per tile.  Tokens
+// that are quantised within the call can be tiled by 224 instead: two accumulators
+// of 224 columns leave room for the scales without overlapping.
 //
 // Few tokens and a long K: the sum over K is split over a cluster of S <= 8 CTAs.
 // Each takes a run of K, writes its partial tile to the others' shared memory
@@ -86,15 +88,15 @@ struct Form {
   static constexpr int BNW = PAIR ? 2 * BM : BM;               // weight rows of a tile
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;            // token rows a CTA loads
   static constexpr int B_BYTES = B_ROWS * KB / 2;
-  static constexpr int B_ATOMS = BN > 128 ? BN / 128 : 1;      // row atoms of a token tile
-  static constexpr int ATOM_TOKENS = BN < 128 ? BN : 128;      // token rows of a scale atom
+  static constexpr int B_ATOMS = (BN + 127) / 128;             // row atoms of a token tile
+  static constexpr int ATOM_TOKENS = BN / B_ATOMS;             // m0 / this: a tile's first atom
   static constexpr int SA_BYTES = 2 * ATOM_BYTES, SB_BYTES = 2 * ATOM_BYTES * B_ATOMS;
   static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static constexpr int STAGES = BN >= 128 ? (EXPERTS ? 5 : 6) : (BN > 32 ? 6 : (EXPERTS ? 7 : 8));
   // TMEM columns: two accumulators (ACC1 apart), then the scales of SETS stages
   static constexpr int SF_COLS = 8 + 8 * B_ATOMS;
-  static constexpr bool OVERLAP = BN > 128;
-  static constexpr int SETS = OVERLAP ? 2 : STAGES;
+  static constexpr bool OVERLAP = 2 * BN + 2 * SF_COLS > 512;
+  static constexpr int SETS = BN > 128 ? 2 : STAGES;
   static constexpr int SF_COL0 = 512 - SETS * SF_COLS;
   static constexpr int ACC1 = OVERLAP ? 192 : BN;
   static_assert(ACC1 + BN <= SF_COL0, "TMEM");
@@ -779,7 +781,7 @@ cudaError_t run(const ProductArgs& p, cudaStream_t s, int splits = 1) {
   // a dense product of fewer than 128 rows a tile has one tile of tokens
   const Store sw = store_of(EXPERTS ? p.E : 1, p.N, p.K),
               sx = store_of(1, p.x_rows, p.K,
-                            EXPERTS ? experts_atom_shift(p.slots, p.E) : 7);
+                            EXPERTS ? experts_atom_shift(p.slots, p.E) : p.x_shift);
   CUtensorMap tw, tx, tws, txs;
   if (!encode_codes(&tw, p.w, sw, BM, 3) || !encode_scales(&tws, p.w, sw, 1, 3))
     return cudaErrorInvalidValue;
@@ -860,6 +862,18 @@ int pick_splits(const ProductArgs& p) {
 }
 }  // namespace
 
+// Pair tiles of 224 tokens have two accumulators without a shared part, so the
+// MMAs of a tile do not wait for the epilogue of the one before; tiles of 256 do
+// (~2300 cycles) but there are fewer of them.  Taken: the form with the shorter
+// last pair, in cycles of 2 (1.75) per value of K and tile.
+int product_atom_shift(int64_t M, int64_t N, int64_t K) {
+  const int64_t n = ceil_div(N, 256), pairs = device_sm_count() / 2;
+  if (tile_shift(M) < 8 || ceil_div(M, 256) * n * 4 <= 2 * pairs) return 7;
+  const double wide = (double)ceil_div(ceil_div(M, 256) * n, pairs) * (2.0 * (double)K + 2300.0);
+  const double narrow = (double)ceil_div(ceil_div(M, 224) * n, pairs) * (1.75 * (double)K + 300.0);
+  return narrow < wide ? TILES_224 : 7;
+}
+
 cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
   note_kernel_name(p.raw ? (p.E ? "k_mx_gemm<experts,fused>" : "k_mx_gemm<fused>")
                          : (p.E ? "k_mx_gemm<experts>" : "k_mx_gemm"));
@@ -873,6 +887,7 @@ cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
       default: return run<256, true, true>(p, s);
     }
   }
+  if (p.x_shift == TILES_224) return run<224, true, false>(p, s);
   // Pairs that would leave more than half of the SMs without a tile give way to
   // single CTAs of 128 x 128.
   const int64_t pair_tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);

@@ -225,12 +225,11 @@ constexpr int TC = 64, TPITCH = 65;
 __host__ __device__ constexpr int64_t cols_tiles(int64_t cols) { return ceil_div(cols, 128) * (128 / TC); }
 __device__ __forceinline__ int t_index(int r, int c) { return r * TPITCH + (r >> 5) * 8 + c; }
 template <typename T>
-__global__ void __launch_bounds__(256) k_mx_quant_both(const QuantArgs a, const Store sr,
-                                                       const bool vec) {
+__global__ void __launch_bounds__(256) k_mx_quant_both(const QuantArgs a, const bool vec) {
   __shared__ float tile[128 * TPITCH + 32];
   ptx::griddep_wait();
   ptx::griddep_launch();
-  const Store st = a.st;  // of [cols, rows]
+  const Store &st = a.st, &sr = a.st_rows;  // of [cols, rows] and of [rows, cols]
   const T* x = static_cast<const T*>(a.x);
   const int64_t tiles_r = ceil_div(a.rows, 128), tiles_c = cols_tiles(a.cols);
   const int64_t tiles = a.batch * tiles_r * tiles_c;
@@ -418,7 +417,7 @@ cudaError_t quantize(const QuantArgs& a, bool transpose, cudaStream_t s) {
       const int64_t tiles = a.batch * ceil_div(a.rows, 128) * cols_tiles(a.cols);
       e = launch_after_previous(k_mx_quant_both<T>,
                                 dim3((unsigned)(tiles < sms * 6 ? tiles : sms * 6)), dim3(256), 0, s,
-                                a, store_of(a.batch, a.rows, a.cols), vec);
+                                a, vec);
     } else if (a.order) {
       e = launch_after_previous(k_mx_quant_cols<T, 4, true>,
                                 dim3((unsigned)(four < cap ? four : cap)), dim3(256), 0, s, a, words);

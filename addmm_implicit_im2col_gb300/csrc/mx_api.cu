@@ -36,6 +36,13 @@ int64_t sorted_rows(int64_t slots, int64_t E) {
   return ceil_div(slots + 127 * (slots < E ? slots : E), ATOM_ROWS) * ATOM_ROWS;
 }
 
+// Room for M tokens quantised for a product, whichever layout it takes.
+size_t tokens_bytes(int64_t M, int64_t K) {
+  const int64_t a = store_of(1, M, K).bytes;
+  const int64_t b = M > ATOM_ROWS ? store_of(1, M, K, TILES_224).bytes : a;
+  return (size_t)(a > b ? a : b);
+}
+
 QuantArgs quant_args(const void* x, int64_t batch, int64_t rows, int64_t cols,
                      int64_t batch_stride, int64_t row_stride, bool transpose, void* q) {
   QuantArgs a = {};
@@ -125,7 +132,8 @@ int mxfp4_dequantize(const void* q, int64_t batch, int64_t rows, int64_t cols, i
 }
 
 size_t mxfp4_linear_workspace_bytes(int64_t M, int64_t K, int x_dtype) {
-  return x_dtype == IMC_MXFP4 || product_fused(M) ? 0 : mxfp4_bytes(1, M, K);
+  if (x_dtype == IMC_MXFP4 || product_fused(M) || mxfp4_bytes(1, M, K) == 0) return 0;
+  return tokens_bytes(M, K);
 }
 
 int mxfp4_linear(const void* x, int x_dtype, int64_t row_stride, const void* w, const float* bias,
@@ -173,6 +181,7 @@ int mxfp4_linear(const void* x, int x_dtype, int64_t row_stride, const void* w, 
   p.M = p.x_rows = M;
   p.N = N;
   p.K = K;
+  p.x_shift = 7;
   Scratch sc(s);
   cudaError_t e = cudaSuccess;
   if (raw && need == 0) {
@@ -182,7 +191,10 @@ int mxfp4_linear(const void* x, int x_dtype, int64_t row_stride, const void* w, 
     p.share = 1;
   } else if (raw) {
     if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
-    e = launch_quantize(quant_args(x, 1, M, K, 0, row_stride, false, sc.p), x_dtype, false, s);
+    QuantArgs a = quant_args(x, 1, M, K, 0, row_stride, false, sc.p);
+    p.x_shift = product_atom_shift(M, N, K);
+    a.st = store_of(1, M, K, p.x_shift);
+    e = launch_quantize(a, x_dtype, false, s);
     p.x = static_cast<const uint8_t*>(sc.p);
     p.inputs_ready = true;
   }
@@ -192,8 +204,8 @@ int mxfp4_linear(const void* x, int x_dtype, int64_t row_stride, const void* w, 
 
 size_t mxfp4_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (!dims_ok(M, N, K) || !store_ok(1, M, N) || !store_ok(1, K, N) || !store_ok(1, K, M)) return 0;
-  const int64_t sizes[4] = {store_of(1, M, N).bytes, store_of(1, K, N).bytes,
-                            store_of(1, N, M).bytes, store_of(1, K, M).bytes};
+  const int64_t sizes[4] = {(int64_t)tokens_bytes(M, N), store_of(1, K, N).bytes,
+                            (int64_t)tokens_bytes(N, M), store_of(1, K, M).bytes};
   int64_t sum = 0;
   for (int64_t v : sizes) sum += ceil_div(v, 512) * 512;
   return (size_t)sum;
@@ -234,25 +246,33 @@ int mxfp4_linear_backward(const void* grad, const void* x, const void* w, int dt
   if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
   // grad along its rows and, transposed, along its columns: read once for both
   uint8_t* at = static_cast<uint8_t*>(sc.p);
-  auto room = [&](int64_t rows, int64_t depth) {
+  auto room = [&](int64_t bytes) {
     uint8_t* q = at;
-    at += ceil_div(store_of(1, rows, depth).bytes, 512) * 512;
+    at += ceil_div(bytes, 512) * 512;
     return q;
   };
-  uint8_t *g_rows = room(M, N), *g_cols = room(N, M), *w_cols = room(K, N), *x_cols = room(K, M);
+  uint8_t *g_rows = room((int64_t)tokens_bytes(M, N)), *g_cols = room((int64_t)tokens_bytes(N, M)),
+          *w_cols = room(store_of(1, K, N).bytes), *x_cols = room(store_of(1, K, M).bytes);
+  // grad's rows are the tokens of the first product, its columns of the second
+  const int shift_x = product_atom_shift(M, K, N), shift_w = product_atom_shift(N, K, M);
   cudaError_t e;
   if (grad_w) {
     QuantArgs a = quant_args(grad, 1, M, N, 0, N, true, g_cols);
+    a.st = store_of(1, N, M, shift_w);
     a.q_rows = grad_x ? g_rows : nullptr;
+    a.st_rows = store_of(1, M, N, shift_x);
     e = launch_quantize(a, dtype, true, s);
   } else {
-    e = launch_quantize(quant_args(grad, 1, M, N, 0, N, false, g_rows), dtype, false, s);
+    QuantArgs a = quant_args(grad, 1, M, N, 0, N, false, g_rows);
+    a.st = store_of(1, M, N, shift_x);
+    e = launch_quantize(a, dtype, false, s);
   }
   // out[rows, cols]: the contraction of two operands quantised along `depth`
-  auto product = [&](const uint8_t* a, int64_t rows, const uint8_t* c, int64_t cols, int64_t depth,
-                     void* out) {
+  auto product = [&](const uint8_t* a, int shift, int64_t rows, const uint8_t* c, int64_t cols,
+                     int64_t depth, void* out) {
     ProductArgs p = {};
     p.x = a;
+    p.x_shift = shift;
     p.w = c;
     p.out = out;
     p.out_dtype = dtype;
@@ -264,12 +284,12 @@ int mxfp4_linear_backward(const void* grad, const void* x, const void* w, int dt
   if (grad_x) {  // grad [M,N] . w [N,K]
     if (e == cudaSuccess)
       e = launch_quantize(quant_args(w, 1, N, K, 0, K, true, w_cols), dtype, true, s);
-    product(g_rows, M, w_cols, K, N, grad_x);
+    product(g_rows, shift_x, M, w_cols, K, N, grad_x);
   }
   if (grad_w) {  // grad^T [N,M] . x [M,K]
     if (e == cudaSuccess)
       e = launch_quantize(quant_args(x, 1, M, K, 0, K, true, x_cols), dtype, true, s);
-    product(g_cols, N, x_cols, K, M, grad_w);
+    product(g_cols, shift_w, N, x_cols, K, M, grad_w);
   }
   return finish_call(sc.give(e), IMC_KERNEL_MXFP4);
 }
@@ -517,6 +537,7 @@ int mxfp4_experts_weight_grad(const void* grad, const void* x, int dtype, int64_
   p.w = x_cols;
   p.out = grad_w;
   p.out_dtype = dtype;
+  p.x_shift = 7;
   p.M = p.x_rows = N;
   p.N = K;
   p.K = rows;

@@ -31,13 +31,16 @@ __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a
 // tile's scales are one contiguous copy.  The scales of blocks past cols are
 // 0; those of rows past `rows` are not written and no result depends on them
 // (a row's scale enters that row's products only).
-// The sorted rows of the experts' product are kept with fewer rows per atom
-// (atom_rows, the rest of the atom unused) when its tiles are lower than 128
-// rows: the MMA reads scales from a TMEM column that is a multiple of four, so
-// every tile has to begin at an atom.
+// Within a call the tokens' scales may be kept with fewer rows per atom (the rest
+// of the atom unused): the MMA reads scales from a TMEM column that is a multiple
+// of four, so every tile of tokens has to begin at an atom.  atom_shift is log2 of
+// an atom's rows (7; less for the sorted rows of the experts' product, whose tiles
+// may be lower than 128 rows), or TILES_224: tiles of 224 rows, 128 in one atom
+// and 96 in the next.
+constexpr int TILES_224 = 0;
 struct Store {
   int64_t batch, rows, cols, blocks, pitch, row_atoms, block_atoms, codes_bytes, scales_off, bytes;
-  int atom_shift;  // log2 of the rows kept in an atom
+  int atom_shift;
 };
 __host__ __device__ inline Store store_of(int64_t batch, int64_t rows, int64_t cols,
                                           int atom_shift = 7) {
@@ -48,7 +51,8 @@ __host__ __device__ inline Store store_of(int64_t batch, int64_t rows, int64_t c
   s.cols = cols;
   s.blocks = ceil_div(cols, BLOCK);
   s.pitch = s.blocks * 16;
-  s.row_atoms = (rows + (1 << atom_shift) - 1) >> atom_shift;
+  s.row_atoms = atom_shift == TILES_224 ? 2 * ceil_div(rows, 224)
+                                        : (rows + (1 << atom_shift) - 1) >> atom_shift;
   s.block_atoms = ceil_div(s.blocks, ATOM_BLOCKS);
   s.codes_bytes = batch * rows * s.pitch;
   s.scales_off = ceil_div(s.codes_bytes, 512) * 512;
@@ -58,8 +62,14 @@ __host__ __device__ inline Store store_of(int64_t batch, int64_t rows, int64_t c
 // Byte offset, within one matrix's scales, of the 4-byte word of row r and
 // block atom ba.
 __device__ __forceinline__ int64_t scale_word(const Store& st, int64_t r, int64_t ba) {
-  const int rr = (int)r & ((1 << st.atom_shift) - 1);
-  return ((r >> st.atom_shift) * st.block_atoms + ba) * ATOM_BYTES + (rr & 31) * 16 + (rr >> 5) * 4;
+  int64_t atom = r >> st.atom_shift;
+  int rr = (int)r & ((1 << st.atom_shift) - 1);
+  if (st.atom_shift == TILES_224) {
+    const uint32_t tile = (uint32_t)r / 224u, in = (uint32_t)r - tile * 224u;
+    atom = 2 * (int64_t)tile + (in >> 7);
+    rr = (int)(in & 127u);
+  }
+  return (atom * st.block_atoms + ba) * ATOM_BYTES + (rr & 31) * 16 + (rr >> 5) * 4;
 }
 
 struct QuantArgs {
@@ -70,6 +80,7 @@ struct QuantArgs {
   const int32_t* dest;    // rows of the result that row r is written to: dest[r*share ..), or null
   int share;
   uint8_t* q_rows;        // transposed: MXFP4 of x itself as well, or null
+  Store st_rows;          // its layout
   // transposed, rows in expert order: row r of the `rows` padded ones is row
   // order[...] / share of x, or zeros (layout of moe_layout; null: x's own rows)
   const int32_t *offsets, *starts, *order;
@@ -79,6 +90,7 @@ struct QuantArgs {
 // One product: out[token, n] = sum_k x[token, k] * w[n, k] (+ bias[n]) (ReLU).
 struct ProductArgs {
   const uint8_t* x;       // MXFP4 [x_rows, K]
+  int x_shift;            // atom_shift of its scales (dense form)
   const uint8_t* w;       // MXFP4 [E][N, K]
   const float* bias;      // [E][N] or null
   void* out;              // [tokens or slots][N]
@@ -162,6 +174,9 @@ bool product_supported();
 // quantised ones: few tokens, or few slots per expert.
 bool product_fused(int64_t tokens);
 bool experts_fused(int64_t slots, int64_t E);
+// The atom_shift that the dense product of M x N x K wants of tokens that are
+// quantised for it (7: the general layout).
+int product_atom_shift(int64_t M, int64_t N, int64_t K);
 // Token rows of a tile of the experts' product, as log2: the scale atoms of
 // its sorted rows hold that many rows (at most 128).
 int experts_atom_shift(int64_t slots, int64_t E);

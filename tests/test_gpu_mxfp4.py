@@ -6,6 +6,8 @@ product's terms are exact; its sum is rounded at most once per 64 values of K
 partial sum, which sum|a b| bounds), once more for the bias, and once to the
 output's type.
 """
+import random
+
 import numpy as np
 import pytest
 import torch
@@ -162,6 +164,17 @@ MNK = [(1, 1, 1), (1, 129, 33), (2, 7, 64), (31, 128, 256), (32, 127, 257), (33,
        (1537, 2050, 1056), (3000, 2000, 31), (3, 40000, 700), (8, 20500, 2100), (5, 300, 6000)]
 
 
+@pytest.mark.parametrize("M", [224 * 8, 224 * 9 + 1, 224 * 10 - 1, 256 * 8, 256 * 9 + 3])
+@pytest.mark.parametrize("N,K", [(2100, 4096), (2048, 6144 + 32)])
+def test_linear_tiles_of_224_tokens(M, N, K):
+    """Sizes at which tokens quantised by the call are tiled otherwise than an operand
+    quantised before: every output is the same sum."""
+    x, w = spread(M, M, K, torch.bfloat16), binding.quantize_mxfp4(spread(N, N, K))
+    assert torch.equal(binding.linear_mxfp4(x, w, out_dtype=torch.float32),
+                       binding.linear_mxfp4(binding.quantize_mxfp4(x), w))
+    assert binding.check_device_error() == binding.IMC_OK
+
+
 @pytest.mark.parametrize("M,N,K", MNK)
 def test_linear(M, N, K):
     x, w = spread(M + K, M, K), spread(N + K + 1, N, K)
@@ -172,6 +185,16 @@ def test_linear(M, N, K):
     # operands quantised before the call are the same operands
     assert torch.equal(got, binding.linear_mxfp4(binding.quantize_mxfp4(x), wq))
     assert torch.equal(got, binding.linear_mxfp4(x, w))
+    assert binding.check_device_error() == binding.IMC_OK
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_linear_of_any_sizes(seed):
+    r = random.Random(seed)
+    M, N, K = (int(2 ** r.uniform(0, top)) for top in (11.5, 11, 12))
+    x, w = spread(seed, M, K, torch.bfloat16), spread(seed + 1, N, K)
+    y, s = product_case(mx_blocks(f64(x))[0], mx_blocks(f64(w))[0])
+    check(binding.linear_mxfp4(x, w, out_dtype=torch.float32), y, s, K)
     assert binding.check_device_error() == binding.IMC_OK
 
 
