@@ -271,7 +271,7 @@ constexpr int kLayoutOne = 4096;
 struct LayoutArgs {
   const int32_t* experts;
   int n, E, per;  // per: slots of a warp, a multiple of 32
-  int32_t *offsets, *starts, *order, *dest, *counts;
+  int32_t *offsets, *starts, *order, *dest, *dest224, *counts;
 };
 
 __device__ __forceinline__ int layout_bucket(const LayoutArgs& a, int64_t i, int64_t end) {
@@ -399,7 +399,9 @@ __device__ __forceinline__ void layout_place(const LayoutArgs& a, int64_t w0, in
       if (i >= w1) break;
       const int pos = first[e] + mine[e] + ranked[u];
       a.order[pos] = (int32_t)i;
-      a.dest[i] = e < a.E ? pos + shift[e] : -1;
+      const int start = first[e] + shift[e], in = pos - first[e];
+      a.dest[i] = e < a.E ? start + in : -1;
+      a.dest224[i] = e < a.E ? (int)sorted_at(start, TILES_224) + in : -1;
     }
   }
 }
@@ -604,7 +606,8 @@ int layout_ctas(int64_t n) {
 }
 
 cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets, int32_t* starts,
-                          int32_t* order, int32_t* dest, int32_t* counts, cudaStream_t s) {
+                          int32_t* order, int32_t* dest, int32_t* dest224, int32_t* counts,
+                          cudaStream_t s) {
   note_kernel_name("k_layout");
   static std::atomic<bool> ready[64];
   int dev = 0;
@@ -619,7 +622,7 @@ cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets
     if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
   const int ctas = layout_ctas(n);
-  LayoutArgs a = {experts, n, E, 0, offsets, starts, order, dest, counts};
+  LayoutArgs a = {experts, n, E, 0, offsets, starts, order, dest, dest224, counts};
   a.per = (int)(ceil_div(n, (int64_t)32 * kLayoutWarps * ctas) * 32);
   const size_t smem = (size_t)(kLayoutWarps + 3) * (E + 1) * 4;
   if (ctas == 1) {

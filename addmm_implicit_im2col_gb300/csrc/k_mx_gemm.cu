@@ -33,8 +33,9 @@
 // scales: the epilogue drains the shared columns first and hands them back.  The
 // MMAs run at 9.2 PFLOP/s (7.5 us per 1024 of K at 8192 x 4096, with the
 // epilogue taken out); what is left is the hand-over, ~1.2 us per tile.  Tokens
-// that are quantised within the call can be tiled by 224 instead: two accumulators
-// of 224 columns leave room for the scales without overlapping.
+// that are quantised within the call, and the experts' sorted rows, are tiled by
+// 224 instead: two accumulators of 224 columns leave room for the scales without
+// overlapping.
 //
 // Few tokens and a long K: the sum over K is split over a cluster of S <= 8 CTAs.
 // Each takes a run of K, writes its partial tile to the others' shared memory
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
       const int mt = in % mts;  // the expert's token tiles share a weight tile
       r.e = lo;
       r.n0 = in / mts * F::BNW + rank * BM;
-      r.m0 = lo < p.E ? ctl->start[lo] + mt * BN : 0;
+      r.m0 = lo < p.E ? (int)sorted_at(ctl->start[lo], BN == 224 ? TILES_224 : 7) + mt * BN : 0;
       r.rows = count - mt * BN < BN ? count - mt * BN : BN;
       r.first = ctl->offset[lo] + mt * BN;
     }
@@ -578,12 +579,14 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
       auto chunk = [&](int i) {
         return 32 * (F::OVERLAP && buf == 0 ? (i + BN / 32 - F::SHARED) % (BN / 32) : i);
       };
-      // the slots of a chunk's tokens, loaded one chunk ahead
+      // the slots of a chunk's tokens, those of both chunks that a warp may have
+      // before it waits for the accumulator
       auto slots = [&](int i) {
         const int c = chunk(i) + lane;
         return EXPERTS && i < BN / 32 && c < r.rows ? __ldg(p.order + r.first + c) : 0;
       };
-      int slot = slots(turn);
+      static_assert(!EXPERTS || BN / 32 <= 2 * TURNS, "two chunks a warp");
+      const int slot0 = slots(turn), slot1 = slots(turn + TURNS);
       if (FUSED && !QUANTISERS && !none) {
         static_assert(!FUSED || EXPERTS || EPI_WARPS == STAGES, "a stage belongs to one warp");
         if (!quantize_tile(r, tl * (own_kb - kb0), warp - 2)) break;
@@ -605,8 +608,7 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
         const int c = chunk(i);
         const int live = min(32, r.rows - c);  // the same for all lanes
         uint32_t v[32];
-        const int this_slot = slot;
-        slot = slots(i + TURNS);
+        const int this_slot = i == turn ? slot0 : slot1;
         if (live > 0 && !none) {
           ptx::tmem_ld32(tbase + (uint32_t)c, v);
           ptx::tmem_ld_wait();
@@ -621,7 +623,8 @@ __global__ void __launch_bounds__(threads_of(EXPERTS), 1)
           __syncwarp();
           if (lane == 0) {
             if (PAIR)
-              ptx::mbar_arrive_cluster(ptx::cluster_addr(&ctl->acce[F::OVERLAP ? 0 : buf], 0));
+              ptx::mbar_arrive_cluster_tmem(
+                  ptx::cluster_addr(&ctl->acce[F::OVERLAP ? 0 : buf], 0));
             else ptx::mbar_arrive(&ctl->acce[buf]);
           }
         }
@@ -843,7 +846,7 @@ bool experts_fused(int64_t slots, int64_t E) { return slots <= 4 * E && slots <=
 
 int experts_atom_shift(int64_t slots, int64_t E) {
   const int t = tile_shift(ceil_div(slots, E));
-  return t < 7 ? t : 7;
+  return t <= 7 ? t : TILES_224;
 }
 
 namespace {
@@ -884,7 +887,7 @@ cudaError_t launch_product(const ProductArgs& p, cudaStream_t s) {
         return p.raw ? run<32, false, true, false, true>(p, s) : run<32, false, true>(p, s);
       case 6: return run<64, false, true>(p, s);
       case 7: return run<128, false, true>(p, s);
-      default: return run<256, true, true>(p, s);
+      default: return run<224, true, true>(p, s);
     }
   }
   if (p.x_shift == TILES_224) return run<224, true, false>(p, s);

@@ -386,7 +386,7 @@ int64_t moe_layout_size(int64_t T, int64_t k, int64_t E) {
       T * k > kMaxDim - 1)
     return 0;
   const int64_t n = T * k, ctas = layout_ctas(n);
-  return 2 * E + 3 + 2 * n + (ctas > 1 ? ctas * (E + 1) : 0);
+  return 2 * E + 3 + 3 * n + (ctas > 1 ? ctas * (E + 1) : 0);
 }
 
 int moe_layout(const int32_t* experts, int64_t T, int64_t k, int64_t E, int32_t* layout,
@@ -401,7 +401,7 @@ int moe_layout(const int32_t* experts, int64_t T, int64_t k, int64_t E, int32_t*
   if (dev != IMC_OK) return dev;
   int32_t *offsets = layout, *starts = offsets + E + 2, *order = starts + E + 1, *dest = order + n;
   return finish_call(launch_layout(experts, (int)n, (int)E, offsets, starts, order, dest,
-                                   dest + n, (cudaStream_t)stream),
+                                   dest + n, dest + 2 * n, (cudaStream_t)stream),
                      IMC_KERNEL_EXPERTS);
 }
 
@@ -409,8 +409,9 @@ size_t mxfp4_experts_linear_workspace_bytes(int64_t T, int64_t k, int64_t E, int
   if (moe_layout_size(T, k, E) == 0 || T == 0) return 0;
   if (experts_fused(T * k, E)) return 0;
   const int64_t rows = sorted_rows(T * k, E);
-  if (rows > kMaxDim || !dims_ok(0, 0, K) || !store_ok(4, rows, K)) return 0;
-  return (size_t)store_of(1, rows, K, experts_atom_shift(T * k, E)).bytes;
+  if (rows > kMaxDim / 2 || !dims_ok(0, 0, K) || !store_ok(4, rows, K)) return 0;
+  const int shift = experts_atom_shift(T * k, E);
+  return (size_t)store_of(1, sorted_at(rows, shift), K, shift).bytes;
 }
 
 int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row_stride,
@@ -420,7 +421,7 @@ int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row
   if (!float_type(x_dtype) || !float_type(out_dtype) || (flags & ~IMC_ACT_RELU)) return IMC_ERR_ARG;
   const int64_t size = moe_layout_size(T, k, E), n = T * k;
   if (size == 0 || !dims_ok(x_rows, N, K) || K == 0 || (x_rows != T && x_rows != n) ||
-      row_stride < (x_rows > 1 ? K : 0) || sorted_rows(n, E) > kMaxDim ||
+      row_stride < (x_rows > 1 ? K : 0) || sorted_rows(n, E) > kMaxDim / 2 ||
       !store_ok(4, sorted_rows(n, E), K) || !store_ok(E, N, K))
     return IMC_ERR_SHAPE;
   if (T == 0 || N == 0) return finish_empty();
@@ -457,7 +458,8 @@ int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row
   p.offsets = layout;
   p.starts = layout + E + 2;
   p.order = p.starts + E + 1;
-  p.x_rows = sorted_rows(n, E);
+  const int shift = experts_atom_shift(n, E);
+  p.x_rows = sorted_at(sorted_rows(n, E), shift);
   if (need == 0) {
     p.raw = x;
     p.raw_dtype = x_dtype;
@@ -469,8 +471,8 @@ int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row
   if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
   p.x = static_cast<const uint8_t*>(sc.p);
   QuantArgs qa = quant_args(x, 1, x_rows, K, 0, row_stride, false, sc.p);
-  qa.st = store_of(1, p.x_rows, K, experts_atom_shift(n, E));
-  qa.dest = p.order + n;
+  qa.st = store_of(1, p.x_rows, K, shift);
+  qa.dest = p.order + (shift == TILES_224 ? 2 * n : n);
   qa.share = x_rows == n ? 1 : (int)k;
   cudaError_t e = launch_quantize(qa, x_dtype, false, s);
   p.inputs_ready = true;

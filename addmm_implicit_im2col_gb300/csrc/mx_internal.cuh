@@ -177,9 +177,14 @@ bool experts_fused(int64_t slots, int64_t E);
 // The atom_shift that the dense product of M x N x K wants of tokens that are
 // quantised for it (7: the general layout).
 int product_atom_shift(int64_t M, int64_t N, int64_t K);
-// Token rows of a tile of the experts' product, as log2: the scale atoms of
-// its sorted rows hold that many rows (at most 128).
+// The atom_shift of the experts' sorted rows: log2 of the token rows of a tile
+// (at most 7), or TILES_224.
 int experts_atom_shift(int64_t slots, int64_t E);
+// Rows that a matrix with these scale atoms has for `rows` sorted rows, whose runs
+// start at multiples of 128: in tiles of 224 every 128 rows have a tile of their own.
+__host__ __device__ constexpr int64_t sorted_at(int64_t rows, int atom_shift) {
+  return atom_shift == TILES_224 ? rows / ATOM_ROWS * 224 : rows;
+}
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t s);
 cudaError_t product_take_watchdog(int* value);
 
@@ -201,7 +206,8 @@ cudaError_t launch_route_backward(const RouteArgs& a, int dtype, const float* g,
 constexpr int kLayoutMaxCtas = 128;
 int layout_ctas(int64_t n);
 cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets, int32_t* starts,
-                          int32_t* order, int32_t* dest, int32_t* counts, cudaStream_t s);
+                          int32_t* order, int32_t* dest, int32_t* dest224, int32_t* counts,
+                          cudaStream_t s);
 cudaError_t launch_combine(const void* y, const float* w, int dtype, int64_t T, int k, int64_t N,
                            void* out, cudaStream_t s);
 cudaError_t launch_combine_backward(const void* grad, const void* y, const float* w, int dtype,

@@ -104,6 +104,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                : "memory");
 }
 
+// The same without publishing this thread's writes to the other CTA: a release
+// at cluster scope waits until earlier global stores are acknowledged, thousands
+// of cycles in an epilogue.  For a hand-over of tensor memory, whose reads are
+// ordered by tcgen05.wait::ld and tcgen05.fence::before_thread_sync.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 // Makes generic-proxy writes to shared memory visible to the async proxy
 // (tensor core reads of operands written by ordinary st.shared).
 __device__ __forceinline__ void fence_proxy_async_smem() {

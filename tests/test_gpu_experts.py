@@ -273,6 +273,9 @@ def test_layout(T, k, E):
     place[order] = np.arange(T * k)
     want = np.where(key < E, starts[np.minimum(key, E)] + place - offsets[key], -1)
     assert np.array_equal(dest, want)
+    wide = data[2 * E + 3 + 2 * T * k: 2 * E + 3 + 3 * T * k]
+    want = np.where(key < E, starts[np.minimum(key, E)] // 128 * 224 + place - offsets[key], -1)
+    assert np.array_equal(wide, want)
 
 
 def test_layout_one_expert_and_none():

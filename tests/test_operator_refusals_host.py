@@ -139,7 +139,7 @@ def test_sizes():
     assert binding.mxfp4_linear_workspace_bytes(9, 64, 0) == binding.mxfp4_bytes(1, 9, 64)
     assert binding.mxfp4_linear_workspace_bytes(8, 64, 0) == 0  # quantised within the product
     assert binding.mxfp4_linear_workspace_bytes(8, 64, binding.MXFP4) == 0
-    assert binding.moe_layout_size(4, 2, 8) == 2 * 8 + 3 + 16
+    assert binding.moe_layout_size(4, 2, 8) == 2 * 8 + 3 + 24
     assert binding.mxfp4_experts_linear_workspace_bytes(4, 33, 8, 64) == 0
 
 
