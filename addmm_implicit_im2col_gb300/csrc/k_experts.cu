@@ -132,12 +132,12 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
   }
   uint32_t* words = sm_words + warp * padded(a.E);
   __shared__ int groups[kRouteWarps][32];  // the groups that stay, in order
-  const int size = a.E / a.groups;
-  uint32_t inv = 0;
-  int vpt = VPT;  // keys of a lane that the rounds look at
+  const int size = a.size;
+  constexpr int HALF = (VPT + 1) / 2;
+  bool half = false;  // the candidates fill no more than half of the keys
   auto expert_of = [&](int c) {
     if (a.groups == 1) return c;
-    const int g = (int)((c * inv) >> 20);
+    const int g = (int)((c * a.inv_size) >> 20);
     return groups[warp][g] * size + c - g * size;
   };
   if (a.groups > 1) {
@@ -170,14 +170,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
     }
     // The rounds run over the candidates only: candidate c is the c-th expert of
     // the groups that stay.  c / size by a product, exact for c * (size - 1) < 2^20.
-    inv = ((1u << 20) + size - 1) / size;
-    vpt = (a.top_groups * size + 31) >> 5;
+    const int candidates = a.top_groups * size;
+    half = candidates <= 32 * HALF;
     if ((kept >> lane) & 1u) groups[warp][__popc(kept & ((1u << lane) - 1u))] = lane;
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = lane + 32 * j;  // past the candidates: 0, never chosen
-      key[j] = c < a.top_groups * size ? words[padded(expert_of(c))] : 0u;
+      if (j < HALF || !half) key[j] = c < candidates ? words[padded(expert_of(c))] : 0u;
     }
     __syncwarp();
   }
@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteArgs a) {
   for (int j = 0; j < VPT; ++j)
     if (lane + 32 * j < a.E) words[padded(lane + 32 * j)] = __float_as_uint(s[j]);
   __syncwarp();
-  int id = vpt * 2 <= VPT ? choose<(VPT + 1) / 2>(key, a.k) : choose<VPT>(key, a.k);
+  // (the keys past HALF are old ones then, and not looked at)
+  int id = half ? choose<HALF>(key, a.k) : choose<VPT>(key, a.k);
   id = expert_of(id);
   float w = lane < a.k ? __uint_as_float(words[padded(id)]) : 0.0f;
   if (a.renorm) {

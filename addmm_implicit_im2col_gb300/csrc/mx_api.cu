@@ -336,6 +336,8 @@ int moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t row_s
   a.k = (int)k;
   a.groups = (int)groups;
   a.top_groups = (int)top_groups;
+  a.size = (int)(E / groups);
+  a.inv_size = (uint32_t)(((1 << 20) + a.size - 1) / a.size);
   a.sigmoid = score == IMC_SCORE_SIGMOID ? 1 : 0;
   a.renorm = renormalize;
   a.scale = (float)scale;

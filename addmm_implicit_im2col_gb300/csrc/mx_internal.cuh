@@ -192,6 +192,8 @@ struct RouteArgs {
   const void* logits;
   int64_t T, ld;
   int E, k, groups, top_groups, sigmoid, renorm;
+  int size;               // experts of a group, and 2^20 / size rounded up
+  uint32_t inv_size;
   float scale;
   const float* bias;      // [E] or null
   float* weights;         // [T,k]
