@@ -19,10 +19,10 @@
 //               by 32 tokens: tcgen05.ld, bias, ReLU, rounding, and per token one
 //               store of 32 consecutive outputs straight from the registers; in
 //               the experts' form, whose rows are scattered, 32 x 32 outputs
-//               through the warp's own shared memory and 16-byte stores (75
-//               against 90 us for 64 experts, 32768 rows, 2048 x 1024).  One bulk
-//               copy per token row had taken 1.7 times the time: a warp issues
-//               the copies of its lanes one by one, ~130 cycles each
+//               through the warp's own shared memory and 16-byte stores (65
+//               against 78 us for 64 experts, 32768 rows, 2048 x 1024).  One bulk
+//               copy per token row took 1.7 times the time: a warp issues the
+//               copies of its lanes one by one, ~130 cycles each
 //
 // More than 128 tokens run as CTA pairs (cta_group::2): 256 rows of the weight x
 // 256 tokens per pair, each CTA loading its 128 rows and half of the tokens, so
@@ -30,12 +30,15 @@
 // shared memory cannot feed 128 x 256 tiles of 4-bit MMAs (both operands
 // written once and read once: 192 bytes a cycle against 128).  The pair's two
 // accumulators of 256 columns overlap in 64 of them, which leaves room for the
-// scales: the epilogue drains the shared columns first and hands them back.  The
-// MMAs run at 9.2 PFLOP/s (7.5 us per 1024 of K at 8192 x 4096, with the
-// epilogue taken out); what is left is the hand-over, ~1.2 us per tile.  Tokens
-// that are quantised within the call, and the experts' sorted rows, are tiled by
-// 224 instead: two accumulators of 224 columns leave room for the scales without
-// overlapping.
+// scales: the epilogue drains the shared columns first and hands them back.
+// Tokens that are quantised within the call, and the experts' sorted rows, can be
+// tiled by 224 instead: two accumulators of 224 columns leave room for the scales
+// without overlapping (the rule: product_atom_shift).
+//
+// Measured: the MMAs alone run at 9.2 PFLOP/s (7.5 us per 1024 of K at 8192 x 4096,
+// the epilogue taken out); with it 8192 x 4096 x 4096 to bf16 takes 43 us (6.4
+// PFLOP/s, L2 read at 14 TB/s), 8192^3 142 us (7.7, power-capped), K = 1024 to fp32
+// 27.4 us (the output's 134 MB are 20).
 //
 // Few tokens and a long K: the sum over K is split over a cluster of S <= 8 CTAs.
 // Each takes a run of K, writes its partial tile to the others' shared memory
@@ -78,8 +81,8 @@ __device__ int g_watchdog_mx;
 
 // Epilogue warps: four per TMEM lane quadrant in the experts' form, whose tiles
 // are short and whose rows are scattered, two otherwise (measured us with 8 / 16:
-// 64 experts, 32768 rows, 2048 x 1024 82.6 / 74.8, dense 8192 x 4096 x 4096 46.5 /
-// 47.5).
+// 64 experts, 32768 rows, 2048 x 1024, sort apart, 73.0 / 64.9; dense 8192 x 4096 x
+// 4096 43.3 / 44.2, K = 2048 26.9 / 28.6).
 constexpr int epi_warps(bool experts) { return experts ? 16 : 8; }
 constexpr int threads_of(bool experts) { return 64 + 32 * epi_warps(experts); }
 constexpr int ROWS_BYTES = 2048;  // a warp's staged rows (experts' form)
@@ -866,13 +869,16 @@ int pick_splits(const ProductArgs& p) {
 }  // namespace
 
 // Pair tiles of 224 tokens have two accumulators without a shared part, so the
-// MMAs of a tile do not wait for the epilogue of the one before; tiles of 256 do
-// (~2300 cycles) but there are fewer of them.  Taken: the form with the shorter
-// last pair, in cycles of 2 (1.75) per value of K and tile.
+// MMAs of a tile do not wait for the epilogue of the one before; tiles of 256 do,
+// ~700 cycles (fitted: 530 to 780 from the calls below), but may need fewer rounds.
+// Taken: the form whose rounds take fewer cycles, at 2 (1.75) per value of K and 300
+// to hand over.  Whole calls, us with 224 / 256: 8192 x 4096 x 4096 60.4 / 61.9,
+// K = 2048 36.3 / 37.0, K = 512 24.6 / 24.4, 3000 x 4096 x 4096 25.5 / 27.9, 4096 x
+// 1024 x 8192 43.4 / 44.4.
 int product_atom_shift(int64_t M, int64_t N, int64_t K) {
   const int64_t n = ceil_div(N, 256), pairs = device_sm_count() / 2;
   if (tile_shift(M) < 8 || ceil_div(M, 256) * n * 4 <= 2 * pairs) return 7;
-  const double wide = (double)ceil_div(ceil_div(M, 256) * n, pairs) * (2.0 * (double)K + 2300.0);
+  const double wide = (double)ceil_div(ceil_div(M, 256) * n, pairs) * (2.0 * (double)K + 700.0);
   const double narrow = (double)ceil_div(ceil_div(M, 224) * n, pairs) * (1.75 * (double)K + 300.0);
   return narrow < wide ? TILES_224 : 7;
 }
