@@ -30,7 +30,7 @@ constexpr int GROUPS_SHIFT = 5;  // log2 of a CTA's groups of 8 lanes
 // Rows: a group of 8 lanes writes 64 bytes of codes and one scale word per row.
 template <typename T, int U>
 __global__ void __launch_bounds__(256) k_mx_quant_rows(const QuantArgs a, const RowMap map,
-                                                       const bool vec) {
+                                                       const int vec) {
   ptx::griddep_wait();
   ptx::griddep_launch();
   const Store& st = a.st;
@@ -89,13 +89,32 @@ __global__ void __launch_bounds__(256) k_mx_quant_rows(const QuantArgs a, const 
 // Transposed: x [rows, cols] to MXFP4 of x^T [cols, rows], blocks down the
 // columns.  A lane takes one column (two neighbouring ones of 16-bit values) and
 // NB blocks of 32 rows of it: a warp's loads are whole 128-byte row pieces, a
-// block never leaves its lane's registers, and there is no shared memory (through
-// a staged tile, 8192 x 4096 bf16 took 24 us).
+// block never leaves its lane's registers until it is codes (with x staged in
+// shared memory, 8192 x 4096 bf16 took 24 us).
 template <typename T>
 struct ColTile {
   static constexpr int PER = 4 / (int)sizeof(T);  // columns of a lane
   static constexpr int COLS = 32 * PER, CTA_COLS = 8 * COLS;
 };
+
+// The codes of 128 rows in a warp's columns, a lane's column being first + lane * by:
+// exchanged within the warp, so that four neighbouring lanes write one column's 64
+// bytes; a lane alone writes half a sector at a time (8192 x 4096, us: fp32 27.3 / 28.0,
+// bf16 17.6 / 19.3).
+__device__ __forceinline__ void store_columns(uint4 (&buf)[128], const uint4 (&code)[4], uint8_t* to,
+                                              int64_t pitch, int by, int64_t cols, int64_t blocks) {
+  const int lane = threadIdx.x & 31, i = lane & 3;
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) buf[lane * 4 + (k ^ ((lane >> 1) & 3))] = code[k];
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = 8 * k + (lane >> 2);
+    const uint4 v = buf[c * 4 + (i ^ ((c >> 1) & 3))];
+    if (c * by < cols && i < blocks) *reinterpret_cast<uint4*>(to + c * by * pitch + i * 16) = v;
+  }
+}
 
 // GATHER (NB == 4): the rows are slots in expert order, every expert's run padded
 // to a multiple of 128, so that a lane's 128 rows belong to one expert.
@@ -108,6 +127,7 @@ __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, const 
   ptx::griddep_launch();
   const Store& st = a.st;  // of [cols, rows]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ uint4 buf[NB == 4 ? 8 : 1][128];
   // row tiles cover whole scale atoms: the bytes past the last row are 0
   const int64_t tiles_r = ceil_div(a.rows, 128) * (4 / NB), tiles_c = ceil_div(a.cols, C::CTA_COLS);
   const int64_t tiles = a.batch * tiles_r * tiles_c;
@@ -198,11 +218,18 @@ __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, const 
     const int64_t blk = r0 / BLOCK;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
+      if constexpr (NB == 4) {
+        const int64_t cw = c - lane * PER + i;
+        store_columns(buf[warp], code[i], a.q + (b * a.cols + cw) * st.pitch + blk * 16, st.pitch, PER,
+                      a.cols - cw, st.blocks - blk);
+      }
       if (c + i >= a.cols) continue;
-      uint8_t* to = a.q + (b * a.cols + c + i) * st.pitch + blk * 16;
+      if (NB != 4) {
+        uint8_t* to = a.q + (b * a.cols + c + i) * st.pitch + blk * 16;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        if (blk + nb < st.blocks) *reinterpret_cast<uint4*>(to + nb * 16) = code[i][nb];
+        for (int nb = 0; nb < NB; ++nb)
+          if (blk + nb < st.blocks) *reinterpret_cast<uint4*>(to + nb * 16) = code[i][nb];
+      }
       uint8_t* sc = a.q + st.scales_off + atoms + scale_word(st, c + i, blk / ATOM_BLOCKS);
       if (NB == 4) *reinterpret_cast<uint32_t*>(sc) = word[i];
       else
@@ -212,101 +239,105 @@ __global__ void __launch_bounds__(256) k_mx_quant_cols(const QuantArgs a, const 
   }
 }
 
-// x along its columns (as above) and along its rows, read once: a CTA takes 128
-// rows x 64 columns through shared memory; four neighbouring lanes take the four
-// blocks of one column (64 contiguous bytes of codes and one scale word), then a
-// thread one block of one row.  Each 32-row band of the staging tile is shifted
-// by 8 floats, so that the four lanes' column reads fall into different banks.
-// 39 us at 8192 x 4096 fp32, against 53 us for the two kernels apart; with the
-// second reading left to L1 and L2 instead of shared memory 50 us.
-constexpr int TC = 64, TPITCH = 65;
-// tiles over the columns: whole scale atoms of 128 columns (an atom's bytes past
-// the last column are 0)
-__host__ __device__ constexpr int64_t cols_tiles(int64_t cols) { return ceil_div(cols, 128) * (128 / TC); }
-__device__ __forceinline__ int t_index(int r, int c) { return r * TPITCH + (r >> 5) * 8 + c; }
+// x along its columns (as above) and along its rows, read once.  A CTA takes 128
+// rows x 128 columns in two bands of 64 rows: eight lanes hold a row's 128 values,
+// 16 each, and quantise it from their registers (one scale word, 64 contiguous
+// bytes of codes); the band also goes to shared memory, where a thread then reads a
+// column's block of 32.  The 16-byte chunks of a row are permuted by bits 3-4 of
+// their index, so that the writes (eight lanes, every fourth chunk) fall into
+// different banks like the reads.  At 8192 x 4096 fp32 34 us (25 of memory traffic;
+// 32 warps an SM, each waiting for its loads); with the rows' blocks read back from
+// shared memory too 39, with four bands of 32 rows and the next one's loads in flight
+// at 16 warps an SM 38, the two kernels apart 52.
+constexpr int BOTH = 128;  // columns of a tile
+__device__ __forceinline__ int chunk_at(int ch) { return ch ^ ((ch >> 3) & 3); }
 template <typename T>
-__global__ void __launch_bounds__(256) k_mx_quant_both(const QuantArgs a, const bool vec) {
-  __shared__ float tile[128 * TPITCH + 32];
+__global__ void __launch_bounds__(256, 4) k_mx_quant_both(const QuantArgs a, const int vec) {
+  __shared__ __align__(16) float buf[64 * BOTH];
+  __shared__ uint4 out[4 * BOTH];
+  __shared__ __align__(4) uint8_t bytes[4 * BOTH];
   ptx::griddep_wait();
   ptx::griddep_launch();
   const Store &st = a.st, &sr = a.st_rows;  // of [cols, rows] and of [rows, cols]
-  const T* x = static_cast<const T*>(a.x);
-  const int64_t tiles_r = ceil_div(a.rows, 128), tiles_c = cols_tiles(a.cols);
-  const int64_t tiles = a.batch * tiles_r * tiles_c;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t b = t / (tiles_r * tiles_c), rem = t - b * tiles_r * tiles_c;
-    const int64_t r0 = (rem / tiles_c) * 128, c0 = (rem % tiles_c) * TC;
-    const T* base = x + b * a.batch_stride;
-    if (vec && r0 + 128 <= a.rows && c0 + TC <= a.cols) {
-      constexpr int W = 16 / (int)sizeof(T), PER_ROW = TC / W, N = 128 * PER_ROW / 256;
-      uint4 u[N];  // all of a thread's 16-byte loads at once
+  const int64_t tiles_r = ceil_div(a.rows, 128), tiles_c = ceil_div(a.cols, BOTH);
+  const int64_t t = blockIdx.x, b = t / (tiles_r * tiles_c), rem = t - b * tiles_r * tiles_c;
+  const int64_t r0 = (rem / tiles_c) * 128, c0 = (rem % tiles_c) * BOTH;
+  const int j = threadIdx.x & 7, r = threadIdx.x >> 3, c = threadIdx.x & 127, half = threadIdx.x >> 7;
+  const int column = chunk_at(c >> 2) * 4 + (c & 3);
+  const T* x = static_cast<const T*>(a.x) + b * a.batch_stride;
+  const int64_t left = a.cols - c0 - 16 * j;
+  const int n = left < 16 ? (left > 0 ? (int)left : 0) : 16;
+  Raw16<T> raw[2];
+  auto fetch = [&](int band) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int at = threadIdx.x + 256 * i;
-        u[i] = __ldg(reinterpret_cast<const uint4*>(base + (r0 + at / PER_ROW) * a.row_stride + c0) +
-                     at % PER_ROW);
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int64_t row = r0 + band * 64 + h * 32 + r;
+      raw[h].load(x + row * a.row_stride + c0 + 16 * j, row < a.rows ? n : 0, vec);
+    }
+  };
+  fetch(0);
+  uint4 code[2];
+  uint32_t byte[2];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int at = threadIdx.x + 256 * i;
-        alignas(16) T e[W];
-        *reinterpret_cast<uint4*>(e) = u[i];
+  for (int band = 0; band < 2; ++band) {
+    if (band) {
+      fetch(1);
+      __syncthreads();
+    }
 #pragma unroll
-        for (int j = 0; j < W; ++j) tile[t_index(at / PER_ROW, at % PER_ROW * W + j)] = to_f32<T>(e[j]);
+    for (int h = 0; h < 2; ++h) {
+      uint2 cr;
+      uint32_t wr;
+      quantize_128(raw[h], cr, wr);
+      const int64_t row = r0 + band * 64 + h * 32 + r, blk = c0 / BLOCK + (j >> 1);
+      if (row < a.rows) {
+        if (blk < sr.blocks)
+          *reinterpret_cast<uint2*>(a.q_rows + (b * a.rows + row) * sr.pitch + blk * 16 +
+                                    (j & 1) * 8) = cr;
+        if (j == 0)
+          *reinterpret_cast<uint32_t*>(a.q_rows + sr.scales_off +
+                                       b * sr.row_atoms * sr.block_atoms * ATOM_BYTES +
+                                       scale_word(sr, row, c0 / 128)) = wr;
       }
-    } else {
-#pragma unroll 8
-      for (int i = threadIdx.x; i < 128 * TC; i += 256) {
-        const int r = i >> 6, c = i & 63;
-        const bool in = r0 + r < a.rows && c0 + c < a.cols;
-        tile[t_index(r, c)] = in ? to_f32<T>(base[(r0 + r) * a.row_stride + c0 + c]) : 0.0f;
-      }
+      float v[16];
+      raw[h].widen(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(buf + (h * 32 + r) * BOTH + chunk_at(4 * j + i) * 4) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
     __syncthreads();
-    const int c = threadIdx.x >> 2, blk = threadIdx.x & 3;
-    uint32_t m = 0;
     float v[4][8];
+    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      v[j >> 3][j & 7] = tile[t_index(blk * 32 + j, c)];
-      m = max(m, __float_as_uint(v[j >> 3][j & 7]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 32; ++i) {
+      v[i >> 3][i & 7] = buf[(half * 32 + i) * BOTH + column];
+      m = max(m, __float_as_uint(v[i >> 3][i & 7]) & 0x7FFFFFFFu);
     }
-    const uint32_t sb = scale_byte(m);
-    const float up = scale_up(sb);
-    uint32_t word = sb << (blk * 8);
-    word |= __shfl_xor_sync(0xffffffffu, word, 1);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    const int64_t gblk = r0 / BLOCK + blk, row = c0 + c;
-    if (row < a.cols) {
-      if (gblk < st.blocks)
-        *reinterpret_cast<uint4*>(a.q + (b * a.cols + row) * st.pitch + gblk * 16) =
-            make_uint4(codes8(v[0], up), codes8(v[1], up), codes8(v[2], up), codes8(v[3], up));
-      if (blk == 0)
-        *reinterpret_cast<uint32_t*>(a.q + st.scales_off +
-                                     b * st.row_atoms * st.block_atoms * ATOM_BYTES +
-                                     scale_word(st, row, r0 / 128)) = word;
-    }
-    {
-      const int r = threadIdx.x & 127, cb = threadIdx.x >> 7;
-      uint32_t mr = 0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        v[j >> 3][j & 7] = tile[t_index(r, cb * 32 + j)];
-        mr = max(mr, __float_as_uint(v[j >> 3][j & 7]) & 0x7FFFFFFFu);
-      }
-      const uint32_t srb = scale_byte(mr);
-      const float upr = scale_up(srb);
-      const int64_t rblk = c0 / BLOCK + cb, rrow = r0 + r;
-      if (rrow < a.rows) {
-        if (rblk < sr.blocks)
-          *reinterpret_cast<uint4*>(a.q_rows + (b * a.rows + rrow) * sr.pitch + rblk * 16) = make_uint4(
-              codes8(v[0], upr), codes8(v[1], upr), codes8(v[2], upr), codes8(v[3], upr));
-        a.q_rows[sr.scales_off + b * sr.row_atoms * sr.block_atoms * ATOM_BYTES +
-               scale_word(sr, rrow, rblk / ATOM_BLOCKS) + rblk % ATOM_BLOCKS] = (uint8_t)srb;
-      }
-    }
-    __syncthreads();
+    byte[band] = scale_byte(m);
+    const float up = scale_up(byte[band]);
+    code[band] = make_uint4(codes8(v[0], up), codes8(v[1], up), codes8(v[2], up), codes8(v[3], up));
   }
+  // Four neighbouring lanes write a column's 64 bytes (a lane alone would write half
+  // a sector at a time).
+#pragma unroll
+  for (int band = 0; band < 2; ++band) {
+    const int i = 2 * band + half;
+    out[c * 4 + (i ^ ((c >> 1) & 3))] = code[band];
+    bytes[c * 4 + i] = (uint8_t)byte[band];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int cc = k * 64 + (threadIdx.x >> 2), i = threadIdx.x & 3;
+    const uint4 v = out[cc * 4 + (i ^ ((cc >> 1) & 3))];
+    if (c0 + cc < a.cols && r0 / BLOCK + i < st.blocks)
+      *reinterpret_cast<uint4*>(a.q + (b * a.cols + c0 + cc) * st.pitch + (r0 / BLOCK + i) * 16) = v;
+  }
+  if (half == 0 && c0 + c < a.cols)
+    *reinterpret_cast<uint32_t*>(a.q + st.scales_off + b * st.row_atoms * st.block_atoms * ATOM_BYTES +
+                                 scale_word(st, c0 + c, r0 / 128)) =
+        reinterpret_cast<const uint32_t*>(bytes)[c];
 }
 
 // The values of eight codes, the first in the lowest four bits.
@@ -401,9 +432,11 @@ RowGrid row_grid(int64_t rows, int64_t chunks, int groups_shift, int u) {
 
 template <typename T>
 cudaError_t quantize(const QuantArgs& a, bool transpose, cudaStream_t s) {
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
-                   (a.row_stride * (int64_t)sizeof(T)) % 16 == 0 &&
-                   (a.batch_stride * (int64_t)sizeof(T)) % 16 == 0;
+  // the alignment of every row
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) |
+                         (uintptr_t)(a.row_stride * (int64_t)sizeof(T)) |
+                         (uintptr_t)(a.batch_stride * (int64_t)sizeof(T));
+  const int vec = (bits & 31u) == 0 ? 2 : (bits & 15u) == 0 ? 1 : 0;
   cudaError_t e;
   if (transpose) {
     // 32-bit loads of whole columns or pairs of them
@@ -414,10 +447,8 @@ cudaError_t quantize(const QuantArgs& a, bool transpose, cudaStream_t s) {
     const int64_t four = across * ceil_div(a.rows, 128);  // CTAs of four blocks a lane
     const int64_t cap = sms * 8;
     if (a.q_rows) {
-      const int64_t tiles = a.batch * ceil_div(a.rows, 128) * cols_tiles(a.cols);
-      e = launch_after_previous(k_mx_quant_both<T>,
-                                dim3((unsigned)(tiles < sms * 6 ? tiles : sms * 6)), dim3(256), 0, s,
-                                a, vec);
+      const int64_t tiles = a.batch * ceil_div(a.rows, 128) * ceil_div(a.cols, BOTH);
+      e = launch_after_previous(k_mx_quant_both<T>, dim3((unsigned)tiles), dim3(256), 0, s, a, vec);
     } else if (a.order) {
       e = launch_after_previous(k_mx_quant_cols<T, 4, true>,
                                 dim3((unsigned)(four < cap ? four : cap)), dim3(256), 0, s, a, words);

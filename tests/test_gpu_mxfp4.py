@@ -129,6 +129,29 @@ def test_quantize_strides_and_batches(transpose):
         assert np.array_equal(got[e], want)
 
 
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("stride", [160, 168, 164, 162, 161])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_quantize_row_alignments(dtype, stride, transpose):
+    """Rows that begin at multiples of 64, 32, 16, 8 and fewer bytes, whole and at an offset."""
+    big = spread(stride, 133, stride, dtype)
+    for view in (big[:, :160], big[:, 8:160], big[:, 4:132]):
+        want, _, _ = mx_blocks(f64(view).T if transpose else f64(view))
+        got = binding.dequantize_mxfp4(binding.quantize_mxfp4(view, transpose=transpose))
+        assert np.array_equal(f64(got), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(130, 264, 160), (257, 132, 72), (64, 128, 128), (385, 130, 33)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradient_is_quantised_both_ways(M, N, K, dtype):
+    """Against the gradients of the operands quantised one by one: the same products."""
+    dy, x, w = spread(6, M, N, dtype), spread(7, M, K, dtype), spread(8, N, K, dtype)
+    dx, dw = binding.linear_mxfp4_backward(dy, x, w)
+    t = lambda v: binding.quantize_mxfp4(v, transpose=True)  # noqa: E731
+    assert torch.equal(dx, binding.linear_mxfp4(dy, t(w)))
+    assert torch.equal(dw, binding.linear_mxfp4(t(dy), t(x), out_dtype=dtype))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_dequantize_types(dtype):
     x = spread(9, 65, 77)
