@@ -116,6 +116,18 @@ def test_quantize_special_values(transpose):
 
 
 @pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_quantize_every_16_bit_value(dtype, transpose):
+    """Each of the 65536 values, beside 31 others of its size and beside a large one."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    x = torch.cat([bits, bits.view(2048, 32).t().reshape(-1)]).view(4096, 32).view(dtype)
+    want, _, _ = mx_blocks(x.double().numpy())
+    src = x.t().contiguous().cuda() if transpose else x.cuda()
+    got = binding.dequantize_mxfp4(binding.quantize_mxfp4(src, transpose=transpose))
+    assert np.array_equal(f64(got), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
 def test_quantize_strides_and_batches(transpose):
     big = spread(3, 3 * 50, 201)
     for view in (big[:50, 1:98], big[5::3, :64], big[:1, 3:100], big[:, 8:72]):
