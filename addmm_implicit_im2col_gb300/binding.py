@@ -534,6 +534,8 @@ def conv2d_host(x, w, bias=None, stride=1, padding=0, dilation=1, *, mode="defau
 # wrappers avoid what costs microseconds on the host: repeated imports, stream
 # objects, a library call for a size that was asked for before.
 _torch = None
+_raw_stream = None
+_calls = None  # the C entry points without ctypes (csrc/calls.c)
 _DTYPE_IDS = {}
 _size = functools.lru_cache(maxsize=4096)(mxfp4_bytes)
 _linear_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_workspace_bytes)
@@ -544,12 +546,14 @@ _backward_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_backward_workspa
 
 def _setup():
     """Imports torch and loads the library, once."""
-    global _torch
+    global _torch, _calls, _raw_stream
     if _torch is None:
         import torch
         _DTYPE_IDS.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
         load()
-        _torch = torch
+        from . import _calls as calls
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _calls, _torch = calls, torch
     return _torch
 
 
@@ -570,7 +574,10 @@ def _rows_of(t, name, ndim=2):
     stride = t.stride()
     if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return _dtype_id(t.dtype, name), shape, (stride if shape[-2] > 1 else stride[:-2] + (shape[-1], 1))
+    dt = _DTYPE_IDS.get(t.dtype)
+    if dt is None:
+        _dtype_id(t.dtype, name)
+    return dt, shape, (stride if shape[-2] > 1 else stride[:-2] + (shape[-1], 1))
 
 
 def _check_plain(t, name, dtype, shape, like):
@@ -579,7 +586,8 @@ def _check_plain(t, name, dtype, shape, like):
         return
     if not isinstance(t, _torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.device != like.device:
+    if (not t.is_cuda or t.dtype != dtype or not t.is_contiguous()
+            or (t is not like and t.device != like.device)):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor on {like.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -587,7 +595,7 @@ def _check_plain(t, name, dtype, shape, like):
 
 def _stream_of(t):
     """The current stream's handle on t's device (what _stream_ptr returns, without its objects)."""
-    return _torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _raw_stream(t.get_device())
 
 
 class MxFp4:
@@ -619,12 +627,14 @@ def quantize_mxfp4(x, *, transpose=False):
     copy: the operand of a product that sums over the rows of x.
     """
     batched = getattr(x, "ndim", 2) == 3
-    dt, shape, stride = _rows_of(x, "x", 3 if batched else 2)
-    batch, step = (shape[0], stride[0]) if batched else (1, 0)
-    rows, cols = shape[-2:]
+    if batched:
+        dt, (batch, rows, cols), (step, ld, _) = _rows_of(x, "x", 3)
+    else:
+        dt, (rows, cols), (ld, _) = _rows_of(x, "x")
+        batch, step = 1, 0
     r, c = (cols, rows) if transpose else (rows, cols)
     q = _torch.empty(_size(batch, r, c), dtype=_torch.uint8, device=x.device)
-    rc = _lib.mxfp4_quantize(x.data_ptr(), dt, batch, rows, cols, step, stride[-2],
+    rc = _calls.mxfp4_quantize(x.data_ptr(), dt, batch, rows, cols, step, ld,
                              1 if transpose else 0, q.data_ptr(), _stream_of(x))
     if rc:
         raise ImcError(rc, "mxfp4_quantize")
@@ -638,7 +648,7 @@ def dequantize_mxfp4(q, *, dtype=None):
     dtype = _torch.float32 if dtype is None else dtype
     dt, data = _dtype_id(dtype, "dtype"), q.data
     out = _torch.empty(q.shape, dtype=dtype, device=data.device)
-    rc = _lib.mxfp4_dequantize(data.data_ptr(), q.batch, q.rows, q.cols, dt, out.data_ptr(),
+    rc = _calls.mxfp4_dequantize(data.data_ptr(), q.batch, q.rows, q.cols, dt, out.data_ptr(),
                                _stream_of(data))
     if rc:
         raise ImcError(rc, "mxfp4_dequantize")
@@ -679,7 +689,7 @@ def linear_mxfp4(x, w, bias=None, *, relu=False, out_dtype=None, out=None):
         _check_plain(out, "out", out_dtype, (M, N), like)
     nbytes = _linear_size(M, K, dt)
     ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device) if nbytes else None
-    rc = _lib.mxfp4_linear(like.data_ptr(), dt, ld, wd.data_ptr(), _ptr(bias), out.data_ptr(),
+    rc = _calls.mxfp4_linear(like.data_ptr(), dt, ld, wd.data_ptr(), _ptr(bias), out.data_ptr(),
                            _dtype_id(out_dtype, "out_dtype"), M, N, K, ACT_RELU if relu else 0,
                            _ptr(ws), nbytes, _stream_of(like))
     if rc:
@@ -704,7 +714,7 @@ def linear_mxfp4_backward(grad, x, w):
     grad_w = _torch.empty((N, K), dtype=dtype, device=device)
     nbytes = _backward_size(M, N, K)
     ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
-    rc = _lib.mxfp4_linear_backward(grad.data_ptr(), x.data_ptr(), w.data_ptr(), dt, M, N, K,
+    rc = _calls.mxfp4_linear_backward(grad.data_ptr(), x.data_ptr(), w.data_ptr(), dt, M, N, K,
                                     grad_x.data_ptr(), grad_w.data_ptr(), ws.data_ptr(), nbytes,
                                     _stream_of(grad))
     if rc:
@@ -729,7 +739,7 @@ def route_experts(logits, k, bias=None, *, score="softmax", groups=1, top_groups
         _check_plain(bias, "bias", _torch.float32, (E,), logits)
     weights = _torch.empty((T, k), dtype=_torch.float32, device=device)
     experts = _torch.empty((T, k), dtype=_torch.int32, device=device)
-    rc = _lib.moe_route(logits.data_ptr(), dt, T, E, ld, _ptr(bias), k, SCORES[score], groups,
+    rc = _calls.moe_route(logits.data_ptr(), dt, T, E, ld, _ptr(bias), k, SCORES[score], groups,
                         top_groups, 1 if renormalize else 0, scale, weights.data_ptr(),
                         experts.data_ptr(), _stream_of(logits))
     if rc:
@@ -745,7 +755,7 @@ def route_experts_backward(grad_weights, logits, experts, *, score="softmax", re
     _check_plain(experts, "experts", _torch.int32, (T, k), logits)
     _check_plain(grad_weights, "grad_weights", _torch.float32, (T, k), logits)
     grad = _torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    rc = _lib.moe_route_backward(grad_weights.data_ptr(), logits.data_ptr(), dt, T, E, ld,
+    rc = _calls.moe_route_backward(grad_weights.data_ptr(), logits.data_ptr(), dt, T, E, ld,
                                  experts.data_ptr(), k, SCORES[score], 1 if renormalize else 0,
                                  scale, grad.data_ptr(), _stream_of(logits))
     if rc:
@@ -786,7 +796,7 @@ def experts_layout(experts, num_experts):
     T, k = experts.shape
     _check_plain(experts, "experts", _torch.int32, (T, k), experts)
     data = _torch.empty(_layout_size(T, k, num_experts), dtype=_torch.int32, device=experts.device)
-    rc = _lib.moe_layout(experts.data_ptr(), T, k, num_experts, data.data_ptr(), _stream_of(experts))
+    rc = _calls.moe_layout(experts.data_ptr(), T, k, num_experts, data.data_ptr(), _stream_of(experts))
     if rc:
         raise ImcError(rc, "moe_layout")
     return ExpertsLayout(data, T, k, num_experts)
@@ -819,7 +829,7 @@ def experts_linear_mxfp4(x, w, layout, bias=None, *, relu=False, out_dtype=None)
     out = _torch.empty((T * k, N), dtype=out_dtype, device=device)
     nbytes = _experts_size(T, k, E, K)
     ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device) if nbytes else None
-    rc = _lib.mxfp4_experts_linear(x.data_ptr(), dt, rows, ld, wd.data_ptr(), _ptr(bias),
+    rc = _calls.mxfp4_experts_linear(x.data_ptr(), dt, rows, ld, wd.data_ptr(), _ptr(bias),
                                    ld_data.data_ptr(), out.data_ptr(),
                                    _dtype_id(out_dtype, "out_dtype"), T, k, E, N, K,
                                    ACT_RELU if relu else 0, _ptr(ws), nbytes, _stream_of(x))
@@ -854,14 +864,14 @@ def experts_linear_mxfp4_backward(grad, x, w, layout):
     grad_x = experts_linear_mxfp4(grad, quantize_mxfp4(w, transpose=True), layout)
     if rows != T * k:
         slot_grads, grad_x = grad_x, _torch.empty((T, K), dtype=dtype, device=device)
-        rc = _lib.moe_combine(slot_grads.data_ptr(), dt, None, T, k, K, grad_x.data_ptr(),
+        rc = _calls.moe_combine(slot_grads.data_ptr(), dt, None, T, k, K, grad_x.data_ptr(),
                               _stream_of(grad))
         if rc:
             raise ImcError(rc, "moe_combine")
     grad_w = _torch.empty((E, N, K), dtype=dtype, device=device)
     nbytes = mxfp4_experts_weight_grad_workspace_bytes(T, k, E, N, K)
     ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
-    rc = _lib.mxfp4_experts_weight_grad(grad.data_ptr(), x.data_ptr(), dt, rows,
+    rc = _calls.mxfp4_experts_weight_grad(grad.data_ptr(), x.data_ptr(), dt, rows,
                                         layout.data.data_ptr(), grad_w.data_ptr(), T, k, E, N, K,
                                         ws.data_ptr(), nbytes, _stream_of(grad))
     if rc:
@@ -883,7 +893,7 @@ def experts_combine(y, weights):
     """out[t] = sum_i weights[t, i] * y[t * k + i] for y [T * k, N], weights [T, k] float32."""
     dt, T, k, N = _combine_dims(y, weights)
     out = _torch.empty((T, N), dtype=y.dtype, device=y.device)
-    rc = _lib.moe_combine(y.data_ptr(), dt, weights.data_ptr(), T, k, N, out.data_ptr(),
+    rc = _calls.moe_combine(y.data_ptr(), dt, weights.data_ptr(), T, k, N, out.data_ptr(),
                           _stream_of(y))
     if rc:
         raise ImcError(rc, "moe_combine")
@@ -896,7 +906,7 @@ def experts_combine_backward(grad, y, weights):
     _check_plain(grad, "grad", y.dtype, (T, N), y)
     grad_y = _torch.empty((T * k, N), dtype=y.dtype, device=y.device)
     grad_weights = _torch.empty((T, k), dtype=_torch.float32, device=y.device)
-    rc = _lib.moe_combine_backward(grad.data_ptr(), y.data_ptr(), dt, weights.data_ptr(), T, k, N,
+    rc = _calls.moe_combine_backward(grad.data_ptr(), y.data_ptr(), dt, weights.data_ptr(), T, k, N,
                                    grad_y.data_ptr(), grad_weights.data_ptr(), _stream_of(y))
     if rc:
         raise ImcError(rc, "moe_combine_backward")

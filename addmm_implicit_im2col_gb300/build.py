@@ -1,7 +1,7 @@
 """Builds libimc.so (the CUDA library behind include/imc.h) in-tree for sm_103a.
 
 Each translation unit is compiled in parallel with nvcc, then linked into a
-shared library next to this file.  Rebuilds only when a source or header is
+shared library next to this file; _calls.so is the Python module over it.  Rebuilds only when a source or header is
 newer than the library.  Usage: ``python -m addmm_implicit_im2col_gb300.build``.
 """
 from __future__ import annotations
@@ -11,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libimc.so")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "calls.c")
 SOURCES = ["imc_api.cu", "k_simt.cu", "k_tc_gemm.cu", "k_tc_conv.cu", "noalloc.cu", "mx_api.cu",
            "k_mx_quant.cu", "k_mx_gemm.cu", "k_experts.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,6 +48,13 @@ def is_stale(path: str = LIB_PATH) -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+def is_calls_stale() -> bool:
+    if not os.path.exists(CALLS_PATH):
+        return True
+    t = os.path.getmtime(CALLS_PATH)
+    return any(os.path.getmtime(p) > t for p in (CALLS_SOURCE, os.path.join(INCLUDE, "imc.h")))
+
+
 def _compile(src: str, verbose: bool, ptxas_info: bool):
     obj = os.path.join(BUILD_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
     cmd = [nvcc(), *common_flags(), "-c", src, "-o", obj]
@@ -58,20 +68,32 @@ def _compile(src: str, verbose: bool, ptxas_info: bool):
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compiles and links libimc.so; returns its path."""
-    if not force and not is_stale():
-        return LIB_PATH
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose, ptxas_info), srcs))
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"]
+def _link_calls():
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], CALLS_SOURCE, "-o", tmp, "-L", HERE,
+           "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+        raise RuntimeError(f"building _calls.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compiles and links libimc.so; returns its path."""
+    if force or is_stale():
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        srcs = [os.path.join(CSRC, s) for s in SOURCES]
+        with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+            objs = list(ex.map(lambda s: _compile(s, verbose, ptxas_info), srcs))
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB_PATH)
+    if force or is_calls_stale():
+        _link_calls()
     return LIB_PATH
 
 

@@ -187,3 +187,27 @@ def test_torch_level_checks():
         binding.linear_mxfp4_backward(x, x, x)
     with pytest.raises(ValueError):
         binding.experts_linear_mxfp4(x, None, None)
+
+
+def test_python_module_calls_the_same_entry_points():
+    """The module that the torch-level functions call: statuses, counts and types of arguments."""
+    binding._setup()
+    calls = binding._calls
+    assert calls.mxfp4_quantize(P1, 99, 1, 8, 64, 0, 64, 0, P2, None) == ARG
+    assert calls.mxfp4_quantize(P1, 0, 1, 8, 64, 0, 63, 0, P2, 0) == SHAPE
+    assert calls.mxfp4_quantize(None, 0, 1, 8, 64, 0, 64, 0, P2, None) == NULL
+    assert calls.mxfp4_quantize(P1, 0, 1, 8, 64, 0, 64, 0, P1, None) == ALIAS
+    for name in ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_linear_backward",
+                 "moe_route", "moe_route_backward", "moe_layout", "mxfp4_experts_linear",
+                 "mxfp4_experts_weight_grad", "moe_combine", "moe_combine_backward"):
+        args = binding.SIGNATURES[name][1]
+        zeros = [0.0 if t is binding._dbl else 0 for t in args]
+        assert getattr(calls, name)(*zeros) == getattr(binding.load(), name)(*zeros), name
+        with pytest.raises(TypeError, match=name):
+            getattr(calls, name)(*zeros[1:])
+        with pytest.raises(TypeError):
+            getattr(calls, name)("x", *zeros[1:])
+    with pytest.raises(OverflowError):
+        calls.mxfp4_quantize(P1, 1 << 40, 1, 8, 64, 0, 64, 0, P2, None)
+    with pytest.raises(OverflowError):
+        calls.mxfp4_quantize(P1, 0, 1 << 80, 8, 64, 0, 64, 0, P2, None)
