@@ -28,10 +28,12 @@ struct RowMap {
 constexpr int GROUPS_SHIFT = 5;  // log2 of a CTA's groups of 8 lanes
 
 // Rows: a group of 8 lanes writes 64 bytes of codes and one scale word per row.
-// 8192 x 4096: fp32 24.7 us (22.4 of memory traffic), bf16 17.7 (12.5).  Four rows a
+// 8192 x 4096: fp32 24.4 us (22.4 of memory traffic), bf16 17.1 (12.5).  Four rows a
 // group changed nothing at 16 bits; CTAs that stay and load U rows ahead took 30 and
 // 24 us (fewer of them fit, and they drift apart in memory).
-template <typename T, int U>
+// SORTED: row r goes to the rows dest[r * share ..) of the result (4096 x 2048 bf16 to
+// eight places each 13.2 us, 15 with one lane for all scale words).
+template <typename T, int U, bool SORTED>
 __global__ void __launch_bounds__(256) k_mx_quant_rows(const QuantArgs a, const RowMap map,
                                                        const int vec) {
   ptx::griddep_wait();
@@ -65,12 +67,19 @@ __global__ void __launch_bounds__(256) k_mx_quant_rows(const QuantArgs a, const 
       const int64_t r = row0 + u * step, blk = ba * ATOM_BLOCKS + (l8 >> 1);
       if (r >= all_rows || ba >= map.chunks) continue;
       uint8_t* codes = a.q + blk * 16 + (l8 & 1) * 8;
-      if (a.dest) {
-        for (int d = 0; d < a.share; ++d) {
-          const int64_t to = __ldg(a.dest + r * a.share + d);
-          if (to < 0) continue;
-          if (blk < st.blocks) *reinterpret_cast<uint2*>(codes + to * st.pitch) = code;
-          if (l8 == 0) *reinterpret_cast<uint32_t*>(scales + scale_word(st, to, ba)) = word;
+      if constexpr (SORTED) {
+        // each of the eight lanes reads one place and writes the scale word there
+        const uint32_t eight = 0xFFu << (threadIdx.x & 24);
+        for (int d0 = 0; d0 < a.share; d0 += 8) {
+          const int mine = d0 + l8 < a.share ? __ldg(a.dest + r * a.share + d0 + l8) : -1;
+          if (mine >= 0) *reinterpret_cast<uint32_t*>(scales + scale_word(st, mine, ba)) = word;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            if (d0 + d >= a.share) break;
+            const int to = __shfl_sync(eight, mine, d, 8);
+            if (to >= 0 && blk < st.blocks)
+              *reinterpret_cast<uint2*>(codes + (int64_t)to * st.pitch) = code;
+          }
         }
       } else {
         if (blk < st.blocks) *reinterpret_cast<uint2*>(codes + r * st.pitch) = code;
@@ -474,8 +483,9 @@ cudaError_t quantize(const QuantArgs& a, bool transpose, cudaStream_t s) {
     }
   } else {
     const RowGrid g = row_grid(a.batch * a.rows, a.st.block_atoms, GROUPS_SHIFT, 2);
-    e = launch_after_previous(g.many ? k_mx_quant_rows<T, 2> : k_mx_quant_rows<T, 1>, g.grid,
-                              dim3(256), 0, s, a, g.map, vec);
+    const auto k = a.dest ? (g.many ? k_mx_quant_rows<T, 2, true> : k_mx_quant_rows<T, 1, true>)
+                          : (g.many ? k_mx_quant_rows<T, 2, false> : k_mx_quant_rows<T, 1, false>);
+    e = launch_after_previous(k, g.grid, dim3(256), 0, s, a, g.map, vec);
   }
   note_launch();
   return e;

@@ -60,7 +60,7 @@ struct Raw16 {
   uint4 w[N];
   // vec: 2 when p is 32-byte aligned, 1 when 16.  32-byte loads touch whole sectors: L1
   // is 33 % busy in the rows' kernel, with 16-byte loads 72 %, and the kernel that
-  // quantises both ways takes 3 us less at 8192 x 4096 fp32 (rows alone 24.7 / 25.0).
+  // quantises both ways takes 3 us less at 8192 x 4096 fp32 (rows alone 0.3).
   __device__ __forceinline__ void load(const T* p, int n, int vec) {
     if (vec == 2 && n == 16) {
 #pragma unroll
