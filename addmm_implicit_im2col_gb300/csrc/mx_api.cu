@@ -281,16 +281,13 @@ int mxfp4_linear_backward(const void* grad, const void* x, const void* w, int dt
     p.K = depth;
     if (e == cudaSuccess) e = launch_product(p, s);
   };
-  if (grad_x) {  // grad [M,N] . w [N,K]
-    if (e == cudaSuccess)
-      e = launch_quantize(quant_args(w, 1, N, K, 0, K, true, w_cols), dtype, true, s);
-    product(g_rows, shift_x, M, w_cols, K, N, grad_x);
-  }
-  if (grad_w) {  // grad^T [N,M] . x [M,K]
-    if (e == cudaSuccess)
-      e = launch_quantize(quant_args(x, 1, M, K, 0, K, true, x_cols), dtype, true, s);
-    product(g_cols, shift_w, N, x_cols, K, M, grad_w);
-  }
+  const QuantArgs w_args = quant_args(w, 1, N, K, 0, K, true, w_cols),
+                  x_args = quant_args(x, 1, M, K, 0, K, true, x_cols);
+  if (e == cudaSuccess)
+    e = grad_x && grad_w ? launch_quantize_two(w_args, x_args, dtype, s)
+                         : launch_quantize(grad_x ? w_args : x_args, dtype, true, s);
+  if (grad_x) product(g_rows, shift_x, M, w_cols, K, N, grad_x);  // grad [M,N] . w [N,K]
+  if (grad_w) product(g_cols, shift_w, N, x_cols, K, M, grad_w);  // grad^T [N,M] . x [M,K]
   return finish_call(sc.give(e), IMC_KERNEL_MXFP4);
 }
 

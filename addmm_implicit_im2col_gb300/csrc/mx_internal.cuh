@@ -167,6 +167,8 @@ __device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&v)[8
 inline int dtype_bytes(int dtype) { return dtype == IMC_F32 ? 4 : 2; }
 
 cudaError_t launch_quantize(const QuantArgs& a, int dtype, bool transpose, cudaStream_t s);
+// a and b along their columns, in one launch.
+cudaError_t launch_quantize_two(const QuantArgs& a, const QuantArgs& b, int dtype, cudaStream_t s);
 cudaError_t launch_dequantize(const uint8_t* q, const Store& st, int dtype, void* out,
                               cudaStream_t s);
 bool product_supported();

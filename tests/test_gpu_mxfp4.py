@@ -287,6 +287,22 @@ def test_linear_backward_is_the_formula(M, N, K, dtype):
     check(dw, y, s, M, dtype)
 
 
+@pytest.mark.parametrize("M,N,K", [(77, 130, 96), (700, 513, 2100)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_gradient_alone_is_the_same(M, N, K, dtype):
+    """The C entry point without grad_x, and without grad_w (whose other input may be null)."""
+    dy, x, w = spread(1, M, N, dtype), spread(2, M, K, dtype), spread(3, N, K, dtype)
+    dx, dw = binding.linear_mxfp4_backward(dy, x, w)
+    dx1, dw1 = torch.empty_like(dx), torch.empty_like(dw)
+    dt = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}[dtype]
+    s = torch.cuda.current_stream().cuda_stream
+    assert binding.mxfp4_linear_backward(dy.data_ptr(), None, w.data_ptr(), dt, M, N, K,
+                                         dx1.data_ptr(), None, None, 0, s) == 0
+    assert binding.mxfp4_linear_backward(dy.data_ptr(), x.data_ptr(), None, dt, M, N, K, None,
+                                         dw1.data_ptr(), None, 0, s) == 0
+    assert torch.equal(dx, dx1) and torch.equal(dw, dw1)
+
+
 def test_linear_backward_is_the_difference():
     """On values that MXFP4 holds exactly along both axes, the gradients are the
     exact differences of <dy, linear(x, w)> (a step from one such value to another)."""
