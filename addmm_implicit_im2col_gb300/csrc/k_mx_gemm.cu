@@ -838,9 +838,10 @@ namespace {
 int tile_shift(int64_t rows) { return rows <= 32 ? 5 : (rows <= 64 ? 6 : (rows <= 128 ? 7 : 8)); }
 }  // namespace
 
-// Measured fused / with a quantising launch before, us on the GPU in a graph and
-// per call from Python (bf16, K x N = 4096 x 4096): 1 token 5.9 / 6.3 and 11.5 /
-// 16.0, 4 tokens 6.4 / 6.3, 8 tokens 7.3 / 6.5 and 11.1 / 16.5, 16 tokens 9.1 / 7.1.
+// Measured fused / with a quantising launch before, us on the GPU in a graph (bf16,
+// K x N = 4096 x 4096): 1 token 5.9 / 6.3, 4 tokens 6.4 / 6.3, 8 tokens 7.3 / 6.5, 16
+// tokens 9.1 / 7.1.  Issued from Python a call takes 9.6 us fused and 15 with the
+// other launch and its scratch, so the form with one launch reaches to 8 tokens.
 bool product_fused(int64_t tokens) { return tokens <= 8; }
 // 64 experts, 2048 x 1024, 4 slots a token: 2 tokens 4.8 / 6.7, 8 tokens 7.3 / 9.3,
 // 32 tokens 11.1 / 13.2; 32 tokens of 8 slots, 1024 x 1024 11.0 / 11.1; 8 experts,
