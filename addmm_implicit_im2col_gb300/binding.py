@@ -645,9 +645,10 @@ def dequantize_mxfp4(q, *, dtype=None):
     """The values an MxFp4 stands for, as a tensor of ``dtype`` (default float32)."""
     if not isinstance(q, MxFp4):
         raise TypeError("q must be an MxFp4")
-    dtype = _torch.float32 if dtype is None else dtype
+    torch = _torch or _setup()  # q may have been loaded, and this be the first call
+    dtype = torch.float32 if dtype is None else dtype
     dt, data = _dtype_id(dtype, "dtype"), q.data
-    out = _torch.empty(q.shape, dtype=dtype, device=data.device)
+    out = torch.empty(q.shape, dtype=dtype, device=data.device)
     rc = _calls.mxfp4_dequantize(data.data_ptr(), q.batch, q.rows, q.cols, dt, out.data_ptr(),
                                _stream_of(data))
     if rc:
@@ -666,7 +667,8 @@ def linear_mxfp4(x, w, bias=None, *, relu=False, out_dtype=None, out=None):
     if isinstance(x, MxFp4):
         if x.batched:
             raise ValueError("x must be [M, K]")
-        like, dt, ld, M, K, default = x.data, MXFP4, 0, x.rows, x.cols, _torch.float32
+        torch = _torch or _setup()
+        like, dt, ld, M, K, default = x.data, MXFP4, 0, x.rows, x.cols, torch.float32
     else:
         dt, (M, K), (ld, _) = _rows_of(x, "x")
         like, default = x, x.dtype

@@ -1,0 +1,41 @@
+"""What the torch-level 4-bit and expert functions check before anything is launched,
+and how they start up.  No GPU: tensors stand in for CUDA ones where a check needs one,
+and no call gets as far as a launch."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from addmm_implicit_im2col_gb300 import binding, build
+from conftest import ROOT
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return binding.load()
+
+
+def fresh(code):
+    """Runs code in a new process that sees no GPU; it has to exit with 0."""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                       env=dict(os.environ, CUDA_VISIBLE_DEVICES=""), timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("call", ["binding.dequantize_mxfp4(q)", "binding.linear_mxfp4(q, q)"])
+def test_a_stored_matrix_may_come_first(call):
+    """An MxFp4 made from a stored buffer, before any other call of the process: the call
+    sets the module up and fails for want of a GPU alone."""
+    fresh(f"""
+import torch
+from addmm_implicit_im2col_gb300 import binding
+data = torch.zeros(binding.mxfp4_bytes(1, 4, 64), dtype=torch.uint8)
+q = binding.MxFp4(data, 1, 4, 64, False)
+try:
+    {call}
+except (binding.ImcError, ValueError):
+    pass
+""")
