@@ -36,6 +36,6 @@ data = torch.zeros(binding.mxfp4_bytes(1, 4, 64), dtype=torch.uint8)
 q = binding.MxFp4(data, 1, 4, 64, False)
 try:
     {call}
-except (binding.ImcError, ValueError):
+except (RuntimeError, ValueError):  # no GPU: from torch or the library
     pass
 """)
