@@ -535,6 +535,7 @@ def conv2d_host(x, w, bias=None, stride=1, padding=0, dilation=1, *, mode="defau
 # objects, a library call for a size that was asked for before.
 _torch = None
 _raw_stream = None
+_current_device = None
 _calls = None  # the C entry points without ctypes (csrc/calls.c)
 _DTYPE_IDS = {}
 _size = functools.lru_cache(maxsize=4096)(mxfp4_bytes)
@@ -546,13 +547,14 @@ _backward_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_backward_workspa
 
 def _setup():
     """Imports torch and loads the library, once."""
-    global _torch, _calls, _raw_stream
+    global _torch, _calls, _raw_stream, _current_device
     if _torch is None:
         import torch
         _DTYPE_IDS.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
         load()
         from . import _calls as calls
         _raw_stream = torch._C._cuda_getCurrentRawStream
+        _current_device = torch._C._cuda_getDevice
         _calls, _torch = calls, torch
     return _torch
 
@@ -594,8 +596,15 @@ def _check_plain(t, name, dtype, shape, like):
 
 
 def _stream_of(t):
-    """The current stream's handle on t's device (what _stream_ptr returns, without its objects)."""
-    return _raw_stream(t.get_device())
+    """The current stream's handle on t's device (what _stream_ptr returns, without its objects).
+
+    The library launches on the current device, so t has to lie there.
+    """
+    device = t.get_device()
+    if device != _current_device():
+        raise ValueError(f"the tensors are on {t.device}, which is not the current device "
+                         "(use torch.cuda.device)")
+    return _raw_stream(device)
 
 
 class MxFp4:

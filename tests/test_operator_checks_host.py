@@ -39,3 +39,19 @@ try:
 except (RuntimeError, ValueError):  # no GPU: from torch or the library
     pass
 """)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The library launches on the current device: a tensor of another one (or of the host)
+    may not get its stream."""
+    class Tensor:
+        def __init__(self, device):
+            self.device, self.get_device = f"cuda:{device}", lambda: device
+
+    binding._setup()
+    monkeypatch.setattr(binding, "_current_device", lambda: 1, raising=False)
+    monkeypatch.setattr(binding, "_raw_stream", lambda device: 100 + device)
+    assert binding._stream_of(Tensor(1)) == 101
+    for device in (0, 2, -1):
+        with pytest.raises(ValueError, match="current device"):
+            binding._stream_of(Tensor(device))
