@@ -595,6 +595,14 @@ def _check_plain(t, name, dtype, shape, like):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _check_buffer(data, dtype, count):
+    """A one-dimensional contiguous tensor of this type with `count` values at least."""
+    if not isinstance(data, _torch.Tensor):
+        raise TypeError("data must be a torch.Tensor")
+    if data.dtype != dtype or data.dim() != 1 or not data.is_contiguous() or data.numel() < count:
+        raise ValueError(f"data must be a contiguous {dtype} tensor of {count} values")
+
+
 def _stream_of(t):
     """The current stream's handle on t's device (what _stream_ptr returns, without its objects).
 
@@ -610,14 +618,26 @@ def _stream_of(t):
 class MxFp4:
     """A matrix [rows, cols] (or ``batch`` of them) in MXFP4, as quantize_mxfp4 writes it.
 
-    ``data`` is the device buffer (codes, then scales; imc.h has its layout);
+    ``data`` is the device buffer (codes, then scales; imc.h has its layout), a
+    contiguous uint8 tensor of at least mxfp4_bytes(batch, rows, cols) values;
     ``shape`` the shape of the values it stands for.
     """
 
     __slots__ = ("data", "batch", "rows", "cols", "batched")
 
     def __init__(self, data, batch, rows, cols, batched):
+        torch = _torch or _setup()
+        need = _size(batch, rows, cols)  # 0: empty, or no size at all
+        if min(batch, rows, cols) < 0 or (need == 0 and batch * rows * cols):
+            raise ValueError(f"no MXFP4 matrix has the sizes {batch}, {rows}, {cols}")
+        if not batched and batch != 1:
+            raise ValueError(f"{batch} matrices have to be batched")
+        _check_buffer(data, torch.uint8, need)
+        self._set(data, batch, rows, cols, batched)
+
+    def _set(self, data, batch, rows, cols, batched):
         self.data, self.batch, self.rows, self.cols, self.batched = data, batch, rows, cols, batched
+        return self
 
     @property
     def shape(self):
@@ -647,7 +667,7 @@ def quantize_mxfp4(x, *, transpose=False):
                              1 if transpose else 0, q.data_ptr(), _stream_of(x))
     if rc:
         raise ImcError(rc, "mxfp4_quantize")
-    return MxFp4(q, batch, r, c, batched)
+    return MxFp4.__new__(MxFp4)._set(q, batch, r, c, batched)
 
 
 def dequantize_mxfp4(q, *, dtype=None):

@@ -55,3 +55,30 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     for device in (0, 2, -1):
         with pytest.raises(ValueError, match="current device"):
             binding._stream_of(Tensor(device))
+
+
+def test_a_matrix_needs_the_buffer_of_its_size():
+    """The kernels read as far as the shape says, so a buffer that is too short, of another
+    type or not contiguous is refused when the matrix is made."""
+    def make(data, batch=1, rows=150, cols=300, batched=False):
+        return binding.MxFp4(data, batch, rows, cols, batched)
+
+    need = binding.mxfp4_bytes(1, 150, 300)
+    good = torch.zeros(need, dtype=torch.uint8)
+    assert make(good).shape == (150, 300) and make(good).data is good
+    assert make(torch.zeros(need + 1, dtype=torch.uint8)).shape == (150, 300)
+    assert make(torch.zeros(binding.mxfp4_bytes(3, 150, 300), dtype=torch.uint8), 3, batched=True).shape == (3, 150, 300)
+    assert make(torch.zeros(0, dtype=torch.uint8), rows=0).shape == (0, 300)
+    with pytest.raises(TypeError):
+        make(bytes(need))
+    for data in (good[:-1], good.view(torch.int8), good.float(), good.view(2, -1),
+                 torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError):
+            make(data)
+    for batch, rows, cols, batched in ((2, 150, 300, True), (1, 151, 300, False), (1, 150, 321, False),
+                                       (1, -1, 300, False), (1, 150, -300, False), (-1, -150, 300, True),
+                                       (1, 2 ** 31, 300, False), (1, 2 ** 30, 2 ** 30, False)):
+        with pytest.raises(ValueError):
+            make(good, batch, rows, cols, batched)
+    with pytest.raises(ValueError):  # two matrices that say they are one
+        make(torch.zeros(binding.mxfp4_bytes(2, 150, 300), dtype=torch.uint8), 2, batched=False)
