@@ -798,13 +798,23 @@ class ExpertsLayout:
     """The slots (token * k + i) in expert order, as experts_layout writes them.
 
     ``offsets`` [E + 1]: where each expert's slots begin in ``order`` (slots of no
-    expert come after offsets[E]); ``order`` [T * k].
+    expert come after offsets[E]); ``order`` [T * k].  ``data`` holds them and more
+    (imc.h), at least moe_layout_size(T, k, E) int32 values.
     """
 
     __slots__ = ("data", "T", "k", "E")
 
     def __init__(self, data, T, k, E):
+        torch = _torch or _setup()
+        need = _layout_size(T, k, E)
+        if need == 0:
+            raise ValueError(f"no layout has the sizes {T}, {k}, {E}")
+        _check_buffer(data, torch.int32, need)
+        self._set(data, T, k, E)
+
+    def _set(self, data, T, k, E):
         self.data, self.T, self.k, self.E = data, T, k, E
+        return self
 
     @property
     def offsets(self):
@@ -830,7 +840,7 @@ def experts_layout(experts, num_experts):
     rc = _calls.moe_layout(experts.data_ptr(), T, k, num_experts, data.data_ptr(), _stream_of(experts))
     if rc:
         raise ImcError(rc, "moe_layout")
-    return ExpertsLayout(data, T, k, num_experts)
+    return ExpertsLayout.__new__(ExpertsLayout)._set(data, T, k, num_experts)
 
 
 def experts_linear_mxfp4(x, w, layout, bias=None, *, relu=False, out_dtype=None):

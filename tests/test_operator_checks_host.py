@@ -82,3 +82,24 @@ def test_a_matrix_needs_the_buffer_of_its_size():
             make(good, batch, rows, cols, batched)
     with pytest.raises(ValueError):  # two matrices that say they are one
         make(torch.zeros(binding.mxfp4_bytes(2, 150, 300), dtype=torch.uint8), 2, batched=False)
+
+
+def test_a_layout_needs_the_buffer_of_its_size():
+    def make(data, T=70, k=3, E=5):
+        return binding.ExpertsLayout(data, T, k, E)
+
+    need = binding.moe_layout_size(70, 3, 5)
+    good = torch.zeros(need, dtype=torch.int32)
+    made = make(good)
+    assert made.data is good and made.offsets.numel() == 6 and made.order.numel() == 210
+    assert make(torch.zeros(need + 4, dtype=torch.int32)).T == 70
+    assert make(torch.zeros(binding.moe_layout_size(0, 3, 5), dtype=torch.int32), T=0).order.numel() == 0
+    with pytest.raises(TypeError):
+        make([0] * need)
+    for data in (good[:-1], good.long(), good.view(torch.float32), torch.zeros(2 * need, dtype=torch.int32)[::2],
+                 good[: need // 2 * 2].view(2, -1)):
+        with pytest.raises(ValueError):
+            make(data)
+    for T, k, E in ((71, 3, 5), (70, 4, 5), (70, 3, 6), (-1, 3, 5), (70, 0, 5), (70, 33, 5), (70, 3, 1025), (70, 3, 0)):
+        with pytest.raises(ValueError):
+            make(good, T, k, E)
