@@ -385,6 +385,7 @@ int64_t moe_layout_size(int64_t T, int64_t k, int64_t E) {
       T * k > kMaxDim - 1)
     return 0;
   const int64_t n = T * k, ctas = layout_ctas(n);
+  if (sorted_at(sorted_rows(n, E), TILES_224) > kMaxDim) return 0;  // places are 32-bit
   return 2 * E + 3 + 3 * n + (ctas > 1 ? ctas * (E + 1) : 0);
 }
 

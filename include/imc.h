@@ -464,7 +464,9 @@ int moe_route_backward(const float* grad_weights, const void* logits, int dtype,
  *   order   [T*k]  the slots, by expert, in slot order within one
  *   dest    [T*k]  a slot's row among the filled-up runs, -1 without an expert
  *   dest224 [T*k]  the same when every 128 rows of a run have room for 224
- * and, for many slots, counts that the call itself needs. */
+ * and, for many slots, counts that the call itself needs.  The places are 32-bit:
+ * (T * k + 127 * min(T * k, E)), rounded up to a multiple of 128, times 224 / 128
+ * may not pass 2^31 - 1 (about 1.2e9 slots); the size is 0 otherwise. */
 int64_t moe_layout_size(int64_t T, int64_t k, int64_t E);
 int moe_layout(const int32_t* experts, int64_t T, int64_t k, int64_t E, int32_t* layout,
                void* stream);

@@ -103,3 +103,18 @@ def test_a_layout_needs_the_buffer_of_its_size():
     for T, k, E in ((71, 3, 5), (70, 4, 5), (70, 3, 6), (-1, 3, 5), (70, 0, 5), (70, 33, 5), (70, 3, 1025), (70, 3, 0)):
         with pytest.raises(ValueError):
             make(good, T, k, E)
+
+
+def test_layout_refuses_places_that_pass_32_bits():
+    """A slot's last place among the runs of experts, filled up to 128 rows and those in tiles
+    of 224, is held in 32 bits."""
+    P1, P2 = 0x100000000, 0x10000000000
+    for E in (1, 7, 1024):
+        rows = (2 ** 31 - 1) // 224 * 128  # the largest number of filled-up rows
+        most = rows - 127 * E              # slots that may need as many
+        assert binding.moe_layout_size(most, 1, E) > 0
+        for T, k in ((most + 1, 1), (most // 3 + 1, 3), (2 ** 31 - 2, 1)):
+            assert binding.moe_layout_size(T, k, E) == 0
+            assert binding.moe_layout(P1, T, k, E, P2, None) == binding.IMC_ERR_SHAPE
+            assert binding.mxfp4_experts_linear_workspace_bytes(T, k, E, 64) == 0
+            assert binding.mxfp4_experts_weight_grad_workspace_bytes(T, k, E, 64, 64) == 0
