@@ -733,7 +733,7 @@ def linear_mxfp4_backward(grad, x, w):
 
     Returns (grad_x [M, K], grad_w [N, K]), each a 4-bit product whose operands
     are quantised along the axis that it sums over.  All tensors are contiguous
-    and of one float type.
+    and of one float type.  Without tokens (M = 0) or outputs (N = 0) both are 0.
     """
     dt, (M, N), _ = _rows_of(grad, "grad")
     K = _rows_of(x, "x")[1][1]
@@ -741,6 +741,8 @@ def linear_mxfp4_backward(grad, x, w):
     _check_plain(grad, "grad", dtype, (M, N), grad)
     _check_plain(x, "x", dtype, (M, K), grad)
     _check_plain(w, "w", dtype, (N, K), grad)
+    if M == 0 or N == 0:
+        return _torch.zeros_like(x), _torch.zeros_like(w)
     grad_x = _torch.empty((M, K), dtype=dtype, device=device)
     grad_w = _torch.empty((N, K), dtype=dtype, device=device)
     nbytes = _backward_size(M, N, K)
@@ -900,7 +902,7 @@ def experts_linear_mxfp4_backward(grad, x, w, layout):
     _check_plain(w, "w", dtype, (E, N, K), grad)
     if layout.data.device != device:
         raise ValueError("grad and layout must be on one device")
-    if T == 0:
+    if T == 0 or N == 0:
         return _torch.zeros_like(x), _torch.zeros_like(w)
     grad_x = experts_linear_mxfp4(grad, quantize_mxfp4(w, transpose=True), layout)
     if rows != T * k:

@@ -118,3 +118,31 @@ def test_layout_refuses_places_that_pass_32_bits():
             assert binding.moe_layout(P1, T, k, E, P2, None) == binding.IMC_ERR_SHAPE
             assert binding.mxfp4_experts_linear_workspace_bytes(T, k, E, 64) == 0
             assert binding.mxfp4_experts_weight_grad_workspace_bytes(T, k, E, 64, 64) == 0
+
+
+class OnGpu(torch.Tensor):
+    """A tensor of the host that passes for a CUDA one."""
+    is_cuda = True
+
+
+def on_gpu(*shape, dtype=torch.float32):
+    return torch.ones(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N", [(0, 70), (5, 0), (0, 0)])
+def test_gradients_of_an_empty_product(M, N, dtype):
+    """A product without tokens or without outputs has gradients of 0, and nothing to launch."""
+    dx, dw = binding.linear_mxfp4_backward(on_gpu(M, N, dtype=dtype), on_gpu(M, 64, dtype=dtype),
+                                           on_gpu(N, 64, dtype=dtype))
+    assert dx.shape == (M, 64) and dw.shape == (N, 64) and dx.dtype == dw.dtype == dtype
+    assert bool((dx == 0).all()) and bool((dw == 0).all())
+
+
+@pytest.mark.parametrize("T,N,per_slot", [(0, 20, False), (6, 0, False), (6, 0, True), (0, 0, True)])
+def test_gradients_of_an_empty_product_of_experts(T, N, per_slot):
+    layout = binding.ExpertsLayout(torch.zeros(binding.moe_layout_size(T, 2, 4), dtype=torch.int32), T, 2, 4)
+    x = on_gpu(2 * T if per_slot else T, 64)
+    dx, dw = binding.experts_linear_mxfp4_backward(on_gpu(2 * T, N), x, on_gpu(4, N, 64), layout)
+    assert dx.shape == x.shape and dw.shape == (4, N, 64)
+    assert bool((dx == 0).all()) and bool((dw == 0).all())
