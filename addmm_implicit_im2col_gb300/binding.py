@@ -80,6 +80,7 @@ SIGNATURES = {
     "mxfp4_experts_weight_grad": (_int, [_vp, _vp, _int, _i64, _vp, _vp] + [_i64] * 5
                                   + [_vp, ctypes.c_size_t, _vp]),
     "moe_combine": (_int, [_vp, _int, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "moe_combine_f32": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _int, _vp]),
     "moe_combine_backward": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "imc_status_string": (ctypes.c_char_p, [_int]),
     "imc_last_kernel": (_int, []),
@@ -279,6 +280,10 @@ def mxfp4_experts_weight_grad(grad, x, dtype, x_rows, layout, grad_w, T, k, E, N
 
 def moe_combine(y, dtype, weights, T, k, N, out, stream) -> int:
     return load().moe_combine(y, dtype, weights, T, k, N, out, stream)
+
+
+def moe_combine_f32(y, weights, T, k, N, out, out_dtype, stream) -> int:
+    return load().moe_combine_f32(y, weights, T, k, N, out, out_dtype, stream)
 
 
 def moe_combine_backward(grad, y, dtype, weights, T, k, N, grad_y, grad_weights, stream) -> int:
@@ -887,7 +892,7 @@ def experts_linear_mxfp4_backward(grad, x, w, layout):
     grad [T * k, N], x [T, K] or [T * k, K], w [E, N, K] are contiguous and of one
     float type.  Returns (grad_x of x's shape, grad_w [E, N, K]), 4-bit products whose
     operands are quantised along the axis that they sum over; a token's gradient is the
-    sum over its slots, an expert without slots has a gradient of 0.
+    fp32 sum over its slots, an expert without slots has a gradient of 0.
     """
     dt, (slots, N), _ = _rows_of(grad, "grad")
     if not isinstance(layout, ExpertsLayout):
@@ -904,13 +909,17 @@ def experts_linear_mxfp4_backward(grad, x, w, layout):
         raise ValueError("grad and layout must be on one device")
     if T == 0 or N == 0:
         return _torch.zeros_like(x), _torch.zeros_like(w)
-    grad_x = experts_linear_mxfp4(grad, quantize_mxfp4(w, transpose=True), layout)
-    if rows != T * k:
+    # A token's slots share its row: their products are summed in fp32 and rounded once
+    # (4096 tokens, 8 of 64 experts, 1024 x 2048, bf16: 354 us, 341 with bf16 products).
+    shared = rows != T * k
+    grad_x = experts_linear_mxfp4(grad, quantize_mxfp4(w, transpose=True), layout,
+                                  out_dtype=_torch.float32 if shared else dtype)
+    if shared:
         slot_grads, grad_x = grad_x, _torch.empty((T, K), dtype=dtype, device=device)
-        rc = _calls.moe_combine(slot_grads.data_ptr(), dt, None, T, k, K, grad_x.data_ptr(),
-                              _stream_of(grad))
+        rc = _calls.moe_combine_f32(slot_grads.data_ptr(), None, T, k, K, grad_x.data_ptr(), dt,
+                                    _stream_of(grad))
         if rc:
-            raise ImcError(rc, "moe_combine")
+            raise ImcError(rc, "moe_combine_f32")
     grad_w = _torch.empty((E, N, K), dtype=dtype, device=device)
     nbytes = mxfp4_experts_weight_grad_workspace_bytes(T, k, E, N, K)
     ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)

@@ -76,6 +76,7 @@ ENTRY(mxfp4_experts_linear, "pillppppillllliplp", P(0), I(1), L(2), L(3), P(4), 
 ENTRY(mxfp4_experts_weight_grad, "ppilpplllllplp", P(0), P(1), I(2), L(3), P(4), P(5), L(6), L(7),
       L(8), L(9), L(10), P(11), (size_t)L(12), P(13))
 ENTRY(moe_combine, "piplllpp", P(0), I(1), P(2), L(3), L(4), L(5), P(6), P(7))
+ENTRY(moe_combine_f32, "pplllpip", P(0), P(1), L(2), L(3), L(4), P(5), I(6), P(7))
 ENTRY(moe_combine_backward, "ppiplllppp", P(0), P(1), I(2), P(3), L(4), L(5), L(6), P(7), P(8), P(9))
 
 #define ROW(name) {#name, (PyCFunction)(void (*)(void))call_##name, METH_FASTCALL, NULL}
@@ -84,6 +85,7 @@ static PyMethodDef methods[] = {ROW(mxfp4_quantize),       ROW(mxfp4_dequantize)
                                 ROW(moe_route),            ROW(moe_route_backward),
                                 ROW(moe_layout),           ROW(mxfp4_experts_linear),
                                 ROW(mxfp4_experts_weight_grad), ROW(moe_combine),
+                                ROW(moe_combine_f32),
                                 ROW(moe_combine_backward), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};

@@ -460,12 +460,12 @@ __global__ void __launch_bounds__(kLayoutThreads) k_layout_place(const LayoutArg
 }
 
 // ------------------------------------------------------------ weighted sum
-// out[t] = sum_s w[t,s] * y[t*k + s] (w null: ones), in the order of s, fp32; a
-// thread has 8 columns of one token.
-template <typename T>
+// out[t] = sum_s w[t,s] * y[t*k + s] (w null: ones), in the order of s, fp32, rounded
+// once to out's type O; a thread has 8 columns of one token.
+template <typename T, typename O>
 __global__ void __launch_bounds__(256)
     k_combine(const T* __restrict__ y, const float* __restrict__ w, const int64_t T_, const int k,
-              const int64_t N, T* __restrict__ out, const bool vec) {
+              const int64_t N, O* __restrict__ out, const bool vec) {
   ptx::griddep_wait();
   ptx::griddep_launch();
   const int64_t per = ceil_div(N, 8), items = T_ * per;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = fmaf(ws, v[j], acc[j]);
     }
-    store8<T>(out + t * N + c, n, vec, acc);
+    store8<O>(out + t * N + c, n, vec, acc);
   }
 }
 
@@ -553,15 +553,16 @@ cudaError_t route(const RouteArgs& a, const float* g, void* grad, cudaStream_t s
   return e;
 }
 
-template <typename T>
+template <typename T, typename O = T>
 cudaError_t combine(const void* y, const float* w, int64_t tokens, int k, int64_t N, void* out,
                     cudaStream_t s) {
+  constexpr int64_t narrow = sizeof(T) < sizeof(O) ? sizeof(T) : sizeof(O);
   const bool vec = ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0 &&
-                   (N * (int64_t)sizeof(T)) % 16 == 0;
+                   (N * narrow) % 16 == 0;
   const int64_t blocks = ceil_div(tokens * ceil_div(N, 8), 256), cap = (int64_t)device_sm_count() * 8;
   const cudaError_t e = launch_after_previous(
-      k_combine<T>, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, s,
-      static_cast<const T*>(y), w, tokens, k, N, static_cast<T*>(out), vec);
+      k_combine<T, O>, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, s,
+      static_cast<const T*>(y), w, tokens, k, N, static_cast<O*>(out), vec);
   note_launch();
   return e;
 }
@@ -640,8 +641,11 @@ cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets
 }
 
 cudaError_t launch_combine(const void* y, const float* w, int dtype, int64_t T, int k, int64_t N,
-                           void* out, cudaStream_t s) {
+                           void* out, int out_dtype, cudaStream_t s) {
   note_kernel_name("k_combine");
+  if (dtype == IMC_F32 && out_dtype == IMC_F16) return combine<float, __half>(y, w, T, k, N, out, s);
+  if (dtype == IMC_F32 && out_dtype == IMC_BF16)
+    return combine<float, __nv_bfloat16>(y, w, T, k, N, out, s);
   if (dtype == IMC_F32) return combine<float>(y, w, T, k, N, out, s);
   if (dtype == IMC_F16) return combine<__half>(y, w, T, k, N, out, s);
   return combine<__nv_bfloat16>(y, w, T, k, N, out, s);

@@ -550,22 +550,40 @@ int mxfp4_experts_weight_grad(const void* grad, const void* x, int dtype, int64_
   return finish_call(sc.give(e), IMC_KERNEL_MXFP4);
 }
 
-int moe_combine(const void* y, int dtype, const float* weights, int64_t T, int64_t k, int64_t N,
-                void* out, void* stream) {
-  if (!float_type(dtype)) return IMC_ERR_ARG;
+}  // extern "C"
+
+namespace {
+int combine_call(const void* y, int dtype, const float* weights, int64_t T, int64_t k, int64_t N,
+                 void* out, int out_dtype, void* stream) {
+  if (!float_type(dtype) || !float_type(out_dtype)) return IMC_ERR_ARG;
   if (!dims_ok(T, k, N) || k < 1 || k > kMaxChosen || (double)T * k * N > kMaxBytes)
     return IMC_ERR_SHAPE;
   if (T == 0 || N == 0) return finish_empty();
   if (!y || !out) return IMC_ERR_NULL;
-  const uint64_t b = (uint64_t)dtype_bytes(dtype), out_bytes = (uint64_t)T * N * b;
-  if (!aligned(y, b) || !aligned(out, b) || !aligned(weights, 4)) return IMC_ERR_ARG;
+  const uint64_t b = (uint64_t)dtype_bytes(dtype), ob = (uint64_t)dtype_bytes(out_dtype);
+  const uint64_t out_bytes = (uint64_t)T * N * ob;
+  if (!aligned(y, b) || !aligned(out, ob) || !aligned(weights, 4)) return IMC_ERR_ARG;
   if (ranges_overlap(out, out_bytes, y, (uint64_t)T * k * N * b) ||
       ranges_overlap(out, out_bytes, weights, (uint64_t)T * k * 4))
     return IMC_ERR_ALIAS;
   const int dev = require_device();
   if (dev != IMC_OK) return dev;
-  return finish_call(launch_combine(y, weights, dtype, T, (int)k, N, out, (cudaStream_t)stream),
+  return finish_call(launch_combine(y, weights, dtype, T, (int)k, N, out, out_dtype,
+                                    (cudaStream_t)stream),
                      IMC_KERNEL_EXPERTS);
+}
+}  // namespace
+
+extern "C" {
+
+int moe_combine(const void* y, int dtype, const float* weights, int64_t T, int64_t k, int64_t N,
+                void* out, void* stream) {
+  return combine_call(y, dtype, weights, T, k, N, out, dtype, stream);
+}
+
+int moe_combine_f32(const float* y, const float* weights, int64_t T, int64_t k, int64_t N, void* out,
+                    int out_dtype, void* stream) {
+  return combine_call(y, IMC_F32, weights, T, k, N, out, out_dtype, stream);
 }
 
 int moe_combine_backward(const void* grad, const void* y, int dtype, const float* weights,

@@ -212,8 +212,9 @@ int layout_ctas(int64_t n);
 cudaError_t launch_layout(const int32_t* experts, int n, int E, int32_t* offsets, int32_t* starts,
                           int32_t* order, int32_t* dest, int32_t* dest224, int32_t* counts,
                           cudaStream_t s);
+// out_dtype: dtype, or any type for fp32 y.
 cudaError_t launch_combine(const void* y, const float* w, int dtype, int64_t T, int k, int64_t N,
-                           void* out, cudaStream_t s);
+                           void* out, int out_dtype, cudaStream_t s);
 cudaError_t launch_combine_backward(const void* grad, const void* y, const float* w, int dtype,
                                     int64_t T, int k, int64_t N, void* grad_y, float* grad_w,
                                     cudaStream_t s);

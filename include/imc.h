@@ -492,8 +492,8 @@ int mxfp4_experts_linear(const void* x, int x_dtype, int64_t x_rows, int64_t row
  * slots of one expert).  grad [T*k,N], x [x_rows,K] (T or T*k rows), grad_w
  * [E,N,K] are contiguous and of type dtype; an expert without slots gets 0.
  * T, N, K >= 1; workspace as above.  (The gradient of x is mxfp4_experts_linear
- * of grad with the transposed weights, and for x_rows == T moe_combine of that
- * without weights.) */
+ * of grad with the transposed weights, and for x_rows == T moe_combine_f32 of that,
+ * taken to fp32, without weights.) */
 size_t mxfp4_experts_weight_grad_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t N,
                                                  int64_t K);
 int mxfp4_experts_weight_grad(const void* grad, const void* x, int dtype, int64_t x_rows,
@@ -505,6 +505,11 @@ int mxfp4_experts_weight_grad(const void* grad, const void* x, int dtype, int64_
  * (weights NULL: all 1).  y [T*k,N], out [T,N] contiguous, of type dtype. */
 int moe_combine(const void* y, int dtype, const float* weights, int64_t T, int64_t k, int64_t N,
                 void* out, void* stream);
+
+/* The same of fp32 y, rounded once to out_dtype (the gradient of experts' shared 16-bit rows:
+ * the slots' products stay in fp32 until a token's are summed). */
+int moe_combine_f32(const float* y, const float* weights, int64_t T, int64_t k, int64_t N, void* out,
+                    int out_dtype, void* stream);
 
 /* Its gradients: grad_y[t*k + i] = weights[t,i] * grad[t] (of type dtype),
  * grad_weights[t,i] = sum_n grad[t,n] * y[t*k + i, n] (fp32). */

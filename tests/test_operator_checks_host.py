@@ -146,3 +146,20 @@ def test_gradients_of_an_empty_product_of_experts(T, N, per_slot):
     dx, dw = binding.experts_linear_mxfp4_backward(on_gpu(2 * T, N), x, on_gpu(4, N, 64), layout)
     assert dx.shape == x.shape and dw.shape == (4, N, 64)
     assert bool((dx == 0).all()) and bool((dw == 0).all())
+
+
+def test_sum_of_fp32_rows_checks_its_arguments():
+    def call(y=0x100000000, w=0x200000000, T=4, k=2, N=8, out=0x300000000, dtype=binding.BF16):
+        return binding.moe_combine_f32(y, w, T, k, N, out, dtype, None)
+
+    assert call(dtype=3) == call(dtype=-1) == binding.IMC_ERR_ARG
+    assert call(y=0x100000002) == call(out=0x300000001) == call(w=0x200000001) == binding.IMC_ERR_ARG
+    assert call(dtype=binding.F32, out=0x300000002) == binding.IMC_ERR_ARG
+    assert call(T=-1) == call(k=0) == call(k=33) == call(N=2 ** 31) == binding.IMC_ERR_SHAPE
+    assert call(y=None) == call(out=None) == binding.IMC_ERR_NULL
+    assert call(out=0x100000000 + 4 * 2 * 8 * 4 - 2) == call(out=0x200000000) == binding.IMC_ERR_ALIAS
+    assert call(T=0) == call(N=0) == binding.IMC_OK
+    binding._setup()
+    assert binding._calls.moe_combine_f32(1, 0, 4, 2, 8, 0x300000000, 2, None) == binding.IMC_ERR_ARG
+    with pytest.raises(TypeError):
+        binding._calls.moe_combine_f32(0x100000000, 0, 4, 2, 8, 0x300000000, 2)
