@@ -11,7 +11,9 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
+import sys
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -541,7 +543,7 @@ def conv2d_host(x, w, bias=None, stride=1, padding=0, dilation=1, *, mode="defau
 _torch = None
 _raw_stream = None
 _current_device = None
-_calls = None  # the C entry points without ctypes (csrc/calls.c)
+_calls = None  # the C entry points without ctypes (csrc/calls.c), else this module's mirrors
 _DTYPE_IDS = {}
 _size = functools.lru_cache(maxsize=4096)(mxfp4_bytes)
 _linear_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_workspace_bytes)
@@ -557,7 +559,10 @@ def _setup():
         import torch
         _DTYPE_IDS.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
         load()
-        from . import _calls as calls
+        try:
+            calls = importlib.import_module(__package__ + "._calls")
+        except ModuleNotFoundError:  # built without Python's headers
+            calls = sys.modules[__name__]
         _raw_stream = torch._C._cuda_getCurrentRawStream
         _current_device = torch._C._cuda_getDevice
         _calls, _torch = calls, torch

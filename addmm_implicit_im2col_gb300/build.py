@@ -1,8 +1,10 @@
 """Builds libimc.so (the CUDA library behind include/imc.h) in-tree for sm_103a.
 
 Each translation unit is compiled in parallel with nvcc, then linked into a
-shared library next to this file; _calls.so is the Python module over it.  Rebuilds only when a source or header is
-newer than the library.  Usage: ``python -m addmm_implicit_im2col_gb300.build``.
+shared library next to this file; beside it the Python module over its 4-bit and
+expert entry points (_calls), for the Python that runs the build, where that has
+its headers.  Rebuilds only when a source or header is newer than the library.
+Usage: ``python -m addmm_implicit_im2col_gb300.build``.
 """
 from __future__ import annotations
 
@@ -19,7 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libimc.so")
-CALLS_PATH = os.path.join(HERE, "_calls.so")
+CALLS_PATH = os.path.join(HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALLS_SOURCE = os.path.join(CSRC, "calls.c")
 SOURCES = ["imc_api.cu", "k_simt.cu", "k_tc_gemm.cu", "k_tc_conv.cu", "noalloc.cu", "mx_api.cu",
            "k_mx_quant.cu", "k_mx_gemm.cu", "k_experts.cu"]
@@ -69,13 +71,18 @@ def _compile(src: str, verbose: bool, ptxas_info: bool):
 
 
 def _link_calls():
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        # libimc.so is whole without it, and the binding calls through ctypes instead
+        print(f"no Python.h in {include}: _calls is not built", file=sys.stderr)
+        return
     tmp = CALLS_PATH + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", INCLUDE,
-           "-I", sysconfig.get_paths()["include"], CALLS_SOURCE, "-o", tmp, "-L", HERE,
+           "-I", include, CALLS_SOURCE, "-o", tmp, "-L", HERE,
            "-l:" + os.path.basename(LIB_PATH), "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"building _calls.so failed:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"building _calls failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS_PATH)
 
 

@@ -163,3 +163,41 @@ def test_sum_of_fp32_rows_checks_its_arguments():
     assert binding._calls.moe_combine_f32(1, 0, 4, 2, 8, 0x300000000, 2, None) == binding.IMC_ERR_ARG
     with pytest.raises(TypeError):
         binding._calls.moe_combine_f32(0x100000000, 0, 4, 2, 8, 0x300000000, 2)
+
+
+def test_without_the_python_module_the_calls_go_through_ctypes():
+    """Where the module over the entry points was not built, the same entry points are called
+    through ctypes: the same names, arguments and statuses."""
+    fresh("""
+import sys
+sys.modules["addmm_implicit_im2col_gb300._calls"] = None  # as if it were not there
+import torch
+from addmm_implicit_im2col_gb300 import binding
+binding._setup()
+calls = binding._calls
+for name in ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_linear_backward", "moe_route",
+             "moe_route_backward", "moe_layout", "mxfp4_experts_linear", "mxfp4_experts_weight_grad",
+             "moe_combine", "moe_combine_f32", "moe_combine_backward"):
+    zeros = [0.0 if t is binding._dbl else 0 for t in binding.SIGNATURES[name][1]]
+    assert getattr(calls, name)(*zeros) == getattr(binding.load(), name)(*zeros), name
+P1, P2 = 0x100000000, 0x200000000
+assert calls.mxfp4_quantize(P1, 99, 1, 8, 64, 0, 64, 0, P2, None) == binding.IMC_ERR_ARG
+assert calls.mxfp4_quantize(None, 0, 1, 8, 64, 0, 64, 0, P2, None) == binding.IMC_ERR_NULL
+assert calls.mxfp4_quantize(P1, 0, 1, 8, 64, 0, 64, 0, P1, 0) == binding.IMC_ERR_ALIAS
+""")
+
+
+def test_build_without_python_headers(monkeypatch, tmp_path, capfd):
+    """The C library does not need them: its build goes through, without the module."""
+    monkeypatch.setattr(build, "CALLS_PATH", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    assert build.build() == build.LIB_PATH
+    assert not (tmp_path / "_calls.so").exists() and "Python.h" in capfd.readouterr().err
+
+
+def test_the_module_is_built_for_this_python():
+    """Its name holds the interpreter's version: another one does not take it for its own."""
+    import sysconfig
+    assert os.path.basename(build.CALLS_PATH) == "_calls" + sysconfig.get_config_var("EXT_SUFFIX")
+    binding._setup()
+    assert binding._calls.__file__ == build.CALLS_PATH
