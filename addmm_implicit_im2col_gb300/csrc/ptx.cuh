@@ -157,14 +157,6 @@ __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }
 
-// Untiled bulk copy shared -> global (both addresses and the size multiples of
-// 16 bytes), tracked by the issuing thread's bulk async-groups.
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-               "r"(smem_addr(src)), "r"(bytes)
-               : "memory");
-}
-
 // Tiled loads into this CTA's shared memory whose completion counts on a
 // barrier of either CTA of a pair (its cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, uint32_t cluster_bar,
