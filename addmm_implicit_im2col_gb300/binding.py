@@ -540,6 +540,10 @@ def conv2d_host(x, w, bias=None, stride=1, padding=0, dilation=1, *, mode="defau
 # These calls take a few microseconds on the GPU when a model decodes, so their
 # wrappers avoid what costs microseconds on the host: repeated imports, stream
 # objects, a library call for a size that was asked for before.
+#
+# They record nothing for autograd (a result of a tensor that requires grad is
+# detached, as with the fp32 calls): a training step calls the *_backward functions.
+# All tensors of a call are on the current device.
 _torch = None
 _raw_stream = None
 _current_device = None

@@ -35,8 +35,9 @@
 // tiled by 224 instead: two accumulators of 224 columns leave room for the scales
 // without overlapping (the rule: product_atom_shift).
 //
-// Measured: the MMAs alone run at 9.2 PFLOP/s (7.5 us per 1024 of K at 8192 x 4096,
-// the epilogue taken out); with it 8192 x 4096 x 4096 to bf16 takes 43 us (6.4
+// Measured: these MMAs (K = 64) alone run at 9.2 PFLOP/s (7.5 us per 1024 of K at 8192 x
+// 4096, the epilogue taken out; the instruction's form with K = 96 is not used and was
+// not measured); with the epilogue 8192 x 4096 x 4096 to bf16 takes 43 us (6.4
 // PFLOP/s, L2 read at 14 TB/s), 8192^3 142 us (7.7, power-capped), K = 1024 to fp32
 // 27.4 us (the output's 134 MB are 20).
 //
@@ -841,11 +842,12 @@ int tile_shift(int64_t rows) { return rows <= 32 ? 5 : (rows <= 64 ? 6 : (rows <
 // Measured fused / with a quantising launch before, us on the GPU in a graph (bf16,
 // K x N = 4096 x 4096): 1 token 5.9 / 6.3, 4 tokens 6.4 / 6.3, 8 tokens 7.3 / 6.5, 16
 // tokens 9.1 / 7.1.  Issued from Python a call takes 9.6 us fused and 15 with the
-// other launch and its scratch, so the form with one launch reaches to 8 tokens.
+// other launch and its scratch, so the form with one launch reaches to 8 tokens; a graph,
+// which pays no Python, gives up 0.1 us at 4 tokens and 0.8 at 8 for that.
 bool product_fused(int64_t tokens) { return tokens <= 8; }
 // 64 experts, 2048 x 1024, 4 slots a token: 2 tokens 4.8 / 6.7, 8 tokens 7.3 / 9.3,
 // 32 tokens 11.1 / 13.2; 32 tokens of 8 slots, 1024 x 1024 11.0 / 11.1; 8 experts,
-// 4096 x 2048, 32 slots 9.1 / 8.6.
+// 4096 x 2048, 32 slots 9.1 / 8.6 (the one launch still saves the call its scratch).
 bool experts_fused(int64_t slots, int64_t E) { return slots <= 4 * E && slots <= 256; }
 
 int experts_atom_shift(int64_t slots, int64_t E) {
@@ -857,7 +859,8 @@ namespace {
 // CTAs that share the K of a tile of at most 32 tokens: as many as find an SM
 // each and at least eight blocks of 256 values.  Measured in a row, weights
 // larger than L2 (us for 1 / 2 / 4 CTAs): 1 x 1024 x 8192 8.1 / 6.9 / 6.0,
-// 1 x 4096 x 16384 15.0 / 11.6 / 10.6, 1 x 4096 x 4096 5.5 / 5.7 / 5.7.  More
+// 1 x 4096 x 16384 15.0 / 11.6 / 10.6, 1 x 4096 x 4096 5.5 / 5.7 / 5.7 (where the rule
+// begins to split: nothing won yet, 0.2 us lost).  More
 // tokens make the sum of the partial tiles cost more than the split saves (64 x
 // 4096 x 4096 5.6 / 9.5 / 7.5, 128 x 1024 x 8192 9.4 / 15.3 / 10.5).
 int pick_splits(const ProductArgs& p) {

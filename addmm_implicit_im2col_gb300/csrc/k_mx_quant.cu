@@ -6,7 +6,7 @@
 // (ties to the even code, magnitudes above 6 become 6).  floor(log2) is the
 // exponent field of the fp32 maximum and 2^-e a float built from it, so every
 // step but the final rounding is exact.  A block that holds an infinity or a
-// NaN gets the scale byte 255 (NaN): it stands for 32 NaNs.
+// NaN gets the scale byte 255 (NaN): it stands for 32 NaNs, whatever its codes.
 #include "mx_internal.cuh"
 #include "mx_quant.cuh"
 #include "ptx.cuh"

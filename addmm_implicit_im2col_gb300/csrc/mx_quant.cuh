@@ -15,8 +15,8 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits) {
   const uint32_t e = max_bits >> 23;
   return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
 }
-// 2^(127 - byte), the factor that brings a block into [0, 8); 0 for a NaN
-// block (its codes are then 0).
+// 2^(127 - byte), the factor that brings a block into [0, 8); 0 for a NaN block, whose
+// codes mean nothing (0 for its numbers, some other code for its infinities and NaNs).
 __device__ __forceinline__ float scale_up(uint32_t byte) {
   return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }

@@ -367,7 +367,7 @@ int conv2d_gemm_f32_host(const float* x, const float* w, const float* bias, floa
  *          magnitudes above 6 to 6
  *
  * A block that holds an infinity or a NaN gets the scale NaN and stands for 32
- * NaNs.  A row's last block is filled up with zeros.  Element types of the
+ * NaNs; its codes are not specified.  A row's last block is filled up with zeros.  Element types of the
  * unquantised operands: IMC_F32, IMC_F16, IMC_BF16.
  *
  * Storage: one device buffer of mxfp4_bytes(batch, rows, cols), 16-byte
