@@ -33,7 +33,7 @@ NOALLOC_SCRATCH_BYTES = 32 << 20
 MODES = {"default": 0, "tf32": 1, "simt": 2, "force_tc3": 3, "force_tc1": 4, "direct": 5}
 ACT_RELU = 0x100
 KERNELS = {0: "none", 1: "tc3", 2: "tc1", 3: "simt", 4: "fill", 5: "direct", 6: "mxfp4",
-           7: "experts"}
+           7: "experts", 8: "adapters"}
 F32, F16, BF16, MXFP4 = 0, 1, 2, 3
 SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -84,6 +84,13 @@ SIGNATURES = {
     "moe_combine": (_int, [_vp, _int, _vp, _i64, _i64, _i64, _vp, _vp]),
     "moe_combine_f32": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _int, _vp]),
     "moe_combine_backward": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "moe_balance": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp]),
+    "moe_balance_backward": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _vp,
+                                    _i64, _vp, _int, _dbl, _vp, _vp]),
+    "lowrank_linear": (_int, [_vp, _int, _i64] + [_vp] * 6 + [_i64] * 5 + [_vp]),
+    "lowrank_linear_backward_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
+    "lowrank_linear_backward": (_int, [_vp] * 4 + [_int] + [_vp] * 6 + [_i64] * 5
+                                 + [_vp, ctypes.c_size_t, _vp]),
     "imc_status_string": (ctypes.c_char_p, [_int]),
     "imc_last_kernel": (_int, []),
     "imc_last_kernel_name": (ctypes.c_char_p, []),
@@ -291,6 +298,35 @@ def moe_combine_f32(y, weights, T, k, N, out, out_dtype, stream) -> int:
 def moe_combine_backward(grad, y, dtype, weights, T, k, N, grad_y, grad_weights, stream) -> int:
     return load().moe_combine_backward(grad, y, dtype, weights, T, k, N, grad_y, grad_weights,
                                        stream)
+
+
+def moe_balance(logits, dtype, T, E, row_stride, experts, k, score, offsets, S, loss, counts,
+                stream) -> int:
+    return load().moe_balance(logits, dtype, T, E, row_stride, experts, k, score, offsets, S, loss,
+                              counts, stream)
+
+
+def moe_balance_backward(grad_loss, logits, dtype, T, E, row_stride, experts, k, score, counts,
+                         offsets, S, grad_weights, renormalize, scale, grad_logits, stream) -> int:
+    return load().moe_balance_backward(grad_loss, logits, dtype, T, E, row_stride, experts, k,
+                                       score, counts, offsets, S, grad_weights, renormalize, scale,
+                                       grad_logits, stream)
+
+
+def lowrank_linear(x, dtype, row_stride, a, b, scale, layout, base, out, T, L, r, K, N,
+                   stream) -> int:
+    return load().lowrank_linear(x, dtype, row_stride, a, b, scale, layout, base, out, T, L, r, K,
+                                 N, stream)
+
+
+def lowrank_linear_backward_workspace_bytes(T, r) -> int:
+    return int(load().lowrank_linear_backward_workspace_bytes(T, r))
+
+
+def lowrank_linear_backward(grad, x, a, b, dtype, scale, layout, base, grad_x, grad_a, grad_b, T,
+                            L, r, K, N, workspace, workspace_bytes, stream) -> int:
+    return load().lowrank_linear_backward(grad, x, a, b, dtype, scale, layout, base, grad_x, grad_a,
+                                          grad_b, T, L, r, K, N, workspace, workspace_bytes, stream)
 
 
 def selftest_wait_timeout(limit_us, stream=None) -> int:
@@ -536,7 +572,7 @@ def conv2d_host(x, w, bias=None, stride=1, padding=0, dilation=1, *, mode="defau
     return out
 
 
-# -------------------------------------- 4-bit products and experts (torch level)
+# ---------------------------- 4-bit products, experts and adapters (torch level)
 # These calls take a few microseconds on the GPU when a model decodes, so their
 # wrappers avoid what costs microseconds on the host: repeated imports, stream
 # objects, a library call for a size that was asked for before.
@@ -553,6 +589,7 @@ _size = functools.lru_cache(maxsize=4096)(mxfp4_bytes)
 _linear_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_workspace_bytes)
 _layout_size = functools.lru_cache(maxsize=4096)(moe_layout_size)
 _experts_size = functools.lru_cache(maxsize=4096)(mxfp4_experts_linear_workspace_bytes)
+_lowrank_size = functools.lru_cache(maxsize=4096)(lowrank_linear_backward_workspace_bytes)
 _backward_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_backward_workspace_bytes)
 
 
@@ -972,3 +1009,134 @@ def experts_combine_backward(grad, y, weights):
     if rc:
         raise ImcError(rc, "moe_combine_backward")
     return grad_y, grad_weights
+
+
+def _check_balance(logits, experts, score, offsets):
+    dt, (T, E), (ld, _) = _rows_of(logits, "logits")
+    if not isinstance(experts, _torch.Tensor) or experts.dim() != 2:
+        raise ValueError("experts must be a tensor [T, k]")
+    k = experts.shape[1]
+    _check_plain(experts, "experts", _torch.int32, (T, k), logits)
+    S = 1
+    if offsets is not None:
+        if not isinstance(offsets, _torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
+            raise ValueError("offsets must be a tensor [S + 1]")
+        S = offsets.shape[0] - 1
+        _check_plain(offsets, "offsets", _torch.int32, (S + 1,), logits)
+    return dt, T, E, ld, k, SCORES[score], S
+
+
+def balance_loss(logits, experts, *, score="softmax", offsets=None):
+    """How unevenly a router spreads its tokens over the experts, and the experts' counts.
+
+    logits [T, E] and the experts [T, k] int32 that route_experts chose.  Sequence s holds
+    the n tokens offsets[s] .. offsets[s + 1] (offsets [S + 1] int32, ascending; None: all
+    tokens are one sequence); tokens of no sequence count nowhere.  Returns (loss [S]
+    float32, counts [S, E] int32):
+
+        loss[s] = E / (k n^2) * sum_e counts[s, e] * sum_t p[t, e]
+
+    with p the softmax of the logits, or their sigmoids divided by their sum; 1 for an even
+    choice, 0 for an empty sequence.
+    """
+    dt, T, E, ld, k, score, S = _check_balance(logits, experts, score, offsets)
+    device = logits.device
+    loss = _torch.empty((S,), dtype=_torch.float32, device=device)
+    counts = _torch.empty((S, E), dtype=_torch.int32, device=device)
+    rc = _calls.moe_balance(logits.data_ptr(), dt, T, E, ld, experts.data_ptr(), k, score,
+                          _ptr(offsets), S, loss.data_ptr(), counts.data_ptr(), _stream_of(logits))
+    if rc:
+        raise ImcError(rc, "moe_balance")
+    return loss, counts
+
+
+def balance_loss_backward(grad_loss, logits, experts, counts, *, score="softmax", offsets=None,
+                          grad_weights=None, renormalize=True, scale=1.0):
+    """Gradient of balance_loss with respect to the logits, [T, E] of their type.
+
+    grad_loss [S] float32, counts as balance_loss returned them (constant).  With
+    grad_weights [T, k] float32 the gradient of route_experts' weights (of the same score,
+    and this renormalize and scale) is added in the same pass: the sum of this and
+    route_experts_backward, rounded once.
+    """
+    dt, T, E, ld, k, score, S = _check_balance(logits, experts, score, offsets)
+    _check_plain(grad_loss, "grad_loss", _torch.float32, (S,), logits)
+    _check_plain(counts, "counts", _torch.int32, (S, E), logits)
+    _check_plain(grad_weights, "grad_weights", _torch.float32, (T, k), logits)
+    grad = _torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    rc = _calls.moe_balance_backward(grad_loss.data_ptr(), logits.data_ptr(), dt, T, E, ld,
+                                   experts.data_ptr(), k, score, counts.data_ptr(), _ptr(offsets), S,
+                                   _ptr(grad_weights), 1 if renormalize else 0, scale,
+                                   grad.data_ptr(), _stream_of(logits))
+    if rc:
+        raise ImcError(rc, "moe_balance_backward")
+    return grad
+
+
+def _check_adapters(x, a, b, layout, scale):
+    dt, (T, K), (ld, _) = _rows_of(x, "x")
+    if not isinstance(layout, ExpertsLayout):
+        raise TypeError("layout must be an ExpertsLayout")
+    if layout.k != 1 or layout.T != T:
+        raise ValueError(f"layout must be of {T} rows with one adapter each")
+    _, (L, r, _), _ = _rows_of(a, "a", 3)
+    _, (_, N, _), _ = _rows_of(b, "b", 3)
+    if layout.E != L:
+        raise ValueError(f"layout must be of {L} adapters")
+    _check_plain(a, "a", x.dtype, (L, r, K), x)
+    _check_plain(b, "b", x.dtype, (L, N, r), x)
+    _check_plain(scale, "scale", _torch.float32, (L,), x)
+    if layout.data.device != x.device:
+        raise ValueError("x and layout must be on one device")
+    return dt, T, L, r, K, N, ld
+
+
+def adapters_linear(x, a, b, layout, base=None, *, scale=None, out=None):
+    """Low-rank adapters of many requests: out[t] = base[t] + scale[l] * (x[t] @ a[l]^T) @ b[l]^T.
+
+    x [T, K] (rows may be strided), a [L, r, K], b [L, N, r] and base [T, N], the shared
+    projection's result (None: zeros), are of one float type; scale [L] float32 (None: ones).
+    layout is experts_layout(which[:, None], L) for which [T] int32, row t's adapter l; a
+    row whose number is outside [0, L) has none, and out[t] = base[t].  One layout serves
+    every projection of a step.  Returns out [T, N]; ``out`` may be ``base`` (in place:
+    rows without an adapter are left alone).
+    """
+    dt, T, L, r, K, N, ld = _check_adapters(x, a, b, layout, scale)
+    _check_plain(base, "base", x.dtype, (T, N), x)
+    if out is None:
+        out = _torch.empty((T, N), dtype=x.dtype, device=x.device)
+    else:
+        _check_plain(out, "out", x.dtype, (T, N), x)
+    rc = _calls.lowrank_linear(x.data_ptr(), dt, ld, a.data_ptr(), b.data_ptr(), _ptr(scale),
+                             layout.data.data_ptr(), _ptr(base), out.data_ptr(), T, L, r, K, N,
+                             _stream_of(x))
+    if rc:
+        raise ImcError(rc, "lowrank_linear")
+    return out
+
+
+def adapters_linear_backward(grad, x, a, b, layout, base=None, *, scale=None):
+    """Gradients of ``adapters_linear(x, a, b, layout, scale=scale)`` for grad [T, N].
+
+    Returns (grad_x [T, K], grad_a [L, r, K], grad_b [L, N, r]).  base [T, K] is added to
+    grad_x (the gradient through the shared projection).  All tensors are contiguous and
+    of one float type; an adapter without rows has gradients of 0.
+    """
+    dt, T, L, r, K, N, _ = _check_adapters(x, a, b, layout, scale)
+    dtype, device = x.dtype, x.device
+    _check_plain(x, "x", dtype, (T, K), x)
+    _check_plain(grad, "grad", dtype, (T, N), x)
+    _check_plain(base, "base", dtype, (T, K), x)
+    if T == 0 or N == 0:
+        grad_x = _torch.zeros_like(x) if base is None else base.clone()
+        return grad_x, _torch.zeros_like(a), _torch.zeros_like(b)
+    grad_x, grad_a, grad_b = _torch.empty_like(x), _torch.empty_like(a), _torch.empty_like(b)
+    nbytes = _lowrank_size(T, r)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    rc = _calls.lowrank_linear_backward(grad.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), dt,
+                                      _ptr(scale), layout.data.data_ptr(), _ptr(base),
+                                      grad_x.data_ptr(), grad_a.data_ptr(), grad_b.data_ptr(), T, L,
+                                      r, K, N, ws.data_ptr(), nbytes, _stream_of(x))
+    if rc:
+        raise ImcError(rc, "lowrank_linear_backward")
+    return grad_x, grad_a, grad_b

@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(HERE, "libimc.so")
 CALLS_PATH = os.path.join(HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALLS_SOURCE = os.path.join(CSRC, "calls.c")
 SOURCES = ["imc_api.cu", "k_simt.cu", "k_tc_gemm.cu", "k_tc_conv.cu", "noalloc.cu", "mx_api.cu",
-           "k_mx_quant.cu", "k_mx_gemm.cu", "k_experts.cu"]
+           "k_mx_quant.cu", "k_mx_gemm.cu", "k_experts.cu", "k_balance.cu", "k_adapters.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

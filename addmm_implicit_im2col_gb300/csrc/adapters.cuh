@@ -1,0 +1,62 @@
+// Internal declarations of the low-rank adapters and of the routers' balance loss:
+// argument structs shared by the C entry points (mx_api.cu) and the kernel files.
+#pragma once
+
+#include "mx_internal.cuh"
+
+namespace imc {
+namespace mx {
+
+constexpr int kMaxRank = 128;
+
+// Rows of x in adapter order: bucket l of `offsets` [L + 2] holds the places in
+// `order` of adapter l's rows, bucket L those of the rows without an adapter
+// (the layout of moe_layout with one choice per row).
+struct AdapterArgs {
+  const void* x;        // [T, K], rows ld elements apart
+  int64_t ld;
+  const void *a, *b;    // [L, r, K], [L, N, r]
+  const float* scale;   // [L] or null: ones
+  const int32_t *offsets, *order;
+  const void* base;     // [T, N] or null: zeros
+  void* out;            // [T, N]; may be base
+  int64_t T, K, N;
+  int L, r;
+};
+cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t s);
+
+struct AdapterGradArgs {
+  const void *grad, *x;  // [T, N], [T, K]
+  const void *a, *b;
+  const float* scale;
+  const int32_t *offsets, *order;
+  const void* base;      // [T, K] or null: zeros
+  void *grad_x, *grad_a, *grad_b;  // each may be null
+  int64_t T, K, N;
+  int L, r;
+  void* workspace;       // adapters_backward_bytes
+};
+size_t adapters_backward_bytes(int64_t T, int64_t r);
+cudaError_t launch_adapters_backward(const AdapterGradArgs& a, int dtype, cudaStream_t s);
+
+struct BalanceArgs {
+  const void* logits;    // [T, E], rows ld elements apart
+  int64_t T, ld;
+  int E, k, S, sigmoid;
+  const int32_t* experts;  // [T, k]
+  const int32_t* offsets;  // [S + 1] or null: one sequence of all tokens
+  float* loss;             // [S]
+  int32_t* counts;         // [S, E]
+  // backward
+  const float* grad_loss;     // [S]
+  const float* grad_weights;  // [T, k] or null
+  int renorm;
+  float scale;
+  void* grad;              // [T, E]
+  void* workspace;
+};
+cudaError_t launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_balance_backward(const BalanceArgs& a, int dtype, cudaStream_t s);
+
+}  // namespace mx
+}  // namespace imc

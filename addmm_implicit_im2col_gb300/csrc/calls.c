@@ -1,4 +1,4 @@
-// The 4-bit and expert entry points of include/imc.h as functions of a Python
+// The 4-bit, expert and adapter entry points of include/imc.h as functions of a Python
 // module: a call of a few tokens is bound by its way through Python, and ctypes
 // takes 1.2 us to convert fourteen arguments, this 0.2 (whole calls, us: quantising
 // 7.9 / 6.2, the 4-bit product 8.6 / 6.8, routing 9.6 / 7.6).
@@ -78,6 +78,14 @@ ENTRY(mxfp4_experts_weight_grad, "ppilpplllllplp", P(0), P(1), I(2), L(3), P(4),
 ENTRY(moe_combine, "piplllpp", P(0), I(1), P(2), L(3), L(4), L(5), P(6), P(7))
 ENTRY(moe_combine_f32, "pplllpip", P(0), P(1), L(2), L(3), L(4), P(5), I(6), P(7))
 ENTRY(moe_combine_backward, "ppiplllppp", P(0), P(1), I(2), P(3), L(4), L(5), L(6), P(7), P(8), P(9))
+ENTRY(lowrank_linear, "pilpppppplllllp", P(0), I(1), L(2), P(3), P(4), P(5), P(6), P(7), P(8), L(9),
+      L(10), L(11), L(12), L(13), P(14))
+ENTRY(lowrank_linear_backward, "ppppipppppplllllplp", P(0), P(1), P(2), P(3), I(4), P(5), P(6), P(7),
+      P(8), P(9), P(10), L(11), L(12), L(13), L(14), L(15), P(16), (size_t)L(17), P(18))
+ENTRY(moe_balance, "pilllpliplppp", P(0), I(1), L(2), L(3), L(4), P(5), L(6), I(7), P(8), L(9), P(10),
+      P(11), P(12))
+ENTRY(moe_balance_backward, "ppilllplipplpidpp", P(0), P(1), I(2), L(3), L(4), L(5), P(6), L(7), I(8),
+      P(9), P(10), L(11), P(12), I(13), v[14].d, P(15), P(16))
 
 #define ROW(name) {#name, (PyCFunction)(void (*)(void))call_##name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {ROW(mxfp4_quantize),       ROW(mxfp4_dequantize),
@@ -86,7 +94,9 @@ static PyMethodDef methods[] = {ROW(mxfp4_quantize),       ROW(mxfp4_dequantize)
                                 ROW(moe_layout),           ROW(mxfp4_experts_linear),
                                 ROW(mxfp4_experts_weight_grad), ROW(moe_combine),
                                 ROW(moe_combine_f32),
-                                ROW(moe_combine_backward), {NULL, NULL, 0, NULL}};
+                                ROW(moe_combine_backward), ROW(lowrank_linear),
+                                ROW(lowrank_linear_backward), ROW(moe_balance),
+                                ROW(moe_balance_backward), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", NULL, -1, methods,
                                     NULL, NULL, NULL, NULL};
 

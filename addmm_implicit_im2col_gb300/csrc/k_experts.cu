@@ -5,23 +5,11 @@
 
 #include "mx_internal.cuh"
 #include "ptx.cuh"
+#include "scores.cuh"
 
 namespace imc {
 namespace mx {
 namespace {
-
-constexpr uint32_t kAll = 0xffffffffu;
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
-  return v;
-}
 
 // A float as an unsigned number in the same order; NaN below every number.
 // 0 stays free for "not to be chosen".
@@ -33,46 +21,6 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 __device__ __forceinline__ float from_ordered(uint32_t u) {
   if (u <= 1u) return __uint_as_float(u ? 0x7FC00000u : 0xFF800000u);
   return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
-}
-
-// Scores of one token: lane l holds experts l, l + 32, ... (VPT of them).
-// softmax: exp(x - max) / sum; a row of -inf alone has scores 0.
-template <int VPT, typename T>
-__device__ __forceinline__ void scores(const T* row, int E, int sigmoid, float (&s)[VPT]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int e = lane + 32 * j;
-    s[j] = e < E ? to_f32<T>(row[e]) : -INFINITY;
-  }
-  if (sigmoid) {
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) s[j] = 1.0f / (1.0f + expf(-s[j]));
-  } else {
-    float m = s[0];
-#pragma unroll
-    for (int j = 1; j < VPT; ++j) m = fmaxf(m, s[j]);
-    m = warp_max(m);
-    float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      s[j] = m == -INFINITY && s[j] == m ? 0.0f : expf(s[j] - m);
-      sum += s[j];
-    }
-    sum = warp_sum(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) s[j] *= inv;
-  }
-}
-
-template <int VPT>
-__device__ __forceinline__ float pick(const float (&s)[VPT], int j) {
-  float v = s[0];
-#pragma unroll
-  for (int i = 1; i < VPT; ++i)
-    if (i == j) v = s[i];
-  return v;
 }
 
 constexpr int kRouteWarps = 4;

@@ -1,8 +1,9 @@
-// C entry points of the 4-bit (MXFP4) product and of expert routing
-// (include/imc.h): argument checks, scratch, launches.  As everywhere in the
+// C entry points of the 4-bit (MXFP4) product, of expert routing with its balance
+// loss and of the low-rank adapters (include/imc.h): argument checks, scratch, launches.  As everywhere in the
 // library, every check runs before anything is enqueued.
 #include <cmath>
 
+#include "adapters.cuh"
 #include "mx_internal.cuh"
 
 using namespace imc;
@@ -611,6 +612,220 @@ int moe_combine_backward(const void* grad, const void* y, int dtype, const float
   return finish_call(launch_combine_backward(grad, y, weights, dtype, T, (int)k, N, grad_y,
                                              grad_weights, (cudaStream_t)stream),
                      IMC_KERNEL_EXPERTS);
+}
+
+}  // extern "C"
+
+namespace {
+constexpr int64_t kMaxRows = 1 << 27;  // of the calls that launch a block for a few rows
+
+bool adapter_dims_ok(int64_t T, int64_t L, int64_t r, int64_t K, int64_t N) {
+  return T >= 0 && T <= kMaxRows && L >= 1 && L <= kMaxExperts && r >= 1 && r <= kMaxRank &&
+         dims_ok(0, K, N) && K >= 1 && (double)T * K < kMaxBytes && (double)T * N < kMaxBytes &&
+         (double)L * r * K < kMaxBytes && (double)L * r * N < kMaxBytes;
+}
+struct Range {
+  const void* p;
+  uint64_t bytes;
+};
+bool overlaps_any(const Range& out, const Range* in, int n) {
+  for (int i = 0; i < n; ++i)
+    if (ranges_overlap(out.p, out.bytes, in[i].p, in[i].bytes)) return true;
+  return false;
+}
+}  // namespace
+
+extern "C" {
+
+int lowrank_linear(const void* x, int dtype, int64_t row_stride, const void* a, const void* b,
+                    const float* scale, const int32_t* layout, const void* base, void* out,
+                    int64_t T, int64_t L, int64_t r, int64_t K, int64_t N, void* stream) {
+  if (!float_type(dtype)) return IMC_ERR_ARG;
+  if (!adapter_dims_ok(T, L, r, K, N) || row_stride < (T > 1 ? K : 0)) return IMC_ERR_SHAPE;
+  if (T == 0 || N == 0) return finish_empty();
+  if (!x || !a || !b || !layout || !out) return IMC_ERR_NULL;
+  const uint64_t e = (uint64_t)dtype_bytes(dtype);
+  if (!aligned(x, e) || !aligned(a, e) || !aligned(b, e) || !aligned(scale, 4) ||
+      !aligned(layout, 4) || !aligned(base, e) || !aligned(out, e))
+    return IMC_ERR_ARG;
+  const uint64_t out_bytes = (uint64_t)T * N * e;
+  const Range in[6] = {{x, span(dtype, 1, T, K, 0, row_stride)},
+                       {a, (uint64_t)L * r * K * e},
+                       {b, (uint64_t)L * N * r * e},
+                       {scale, (uint64_t)L * 4},
+                       {layout, (uint64_t)moe_layout_size(T, 1, L) * 4},
+                       {base == out ? nullptr : base, out_bytes}};
+  if (overlaps_any({out, out_bytes}, in, 6)) return IMC_ERR_ALIAS;
+  const int dev = require_device();
+  if (dev != IMC_OK) return dev;
+  AdapterArgs p = {};
+  p.x = x;
+  p.ld = row_stride;
+  p.a = a;
+  p.b = b;
+  p.scale = scale;
+  p.offsets = layout;
+  p.order = layout + 2 * L + 3;
+  p.base = base;
+  p.out = out;
+  p.T = T;
+  p.K = K;
+  p.N = N;
+  p.L = (int)L;
+  p.r = (int)r;
+  return finish_call(launch_adapters(p, dtype, (cudaStream_t)stream), IMC_KERNEL_ADAPTERS);
+}
+
+size_t lowrank_linear_backward_workspace_bytes(int64_t T, int64_t r) {
+  if (T < 1 || T > kMaxRows || r < 1 || r > kMaxRank) return 0;
+  return adapters_backward_bytes(T, r);
+}
+
+int lowrank_linear_backward(const void* grad, const void* x, const void* a, const void* b,
+                             int dtype, const float* scale, const int32_t* layout,
+                             const void* base, void* grad_x, void* grad_a, void* grad_b, int64_t T,
+                             int64_t L, int64_t r, int64_t K, int64_t N, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!float_type(dtype)) return IMC_ERR_ARG;
+  if (!adapter_dims_ok(T, L, r, K, N) || T == 0 || N == 0) return IMC_ERR_SHAPE;
+  if (!grad_x && !grad_a && !grad_b) return finish_empty();
+  if (!grad || !x || !a || !b || !layout) return IMC_ERR_NULL;
+  const uint64_t e = (uint64_t)dtype_bytes(dtype);
+  if (!aligned(grad, e) || !aligned(x, e) || !aligned(a, e) || !aligned(b, e) ||
+      !aligned(scale, 4) || !aligned(layout, 4) || !aligned(base, e) || !aligned(grad_x, e) ||
+      !aligned(grad_a, e) || !aligned(grad_b, e))
+    return IMC_ERR_ARG;
+  const size_t need = lowrank_linear_backward_workspace_bytes(T, r);
+  const int ws = check_workspace(workspace, workspace_bytes, need);
+  if (ws != IMC_OK) return ws;
+  const uint64_t row_bytes = (uint64_t)T * K * e;
+  const Range in[7] = {{grad, (uint64_t)T * N * e},
+                       {x, row_bytes},
+                       {a, (uint64_t)L * r * K * e},
+                       {b, (uint64_t)L * N * r * e},
+                       {scale, (uint64_t)L * 4},
+                       {layout, (uint64_t)moe_layout_size(T, 1, L) * 4},
+                       {base, grad_x ? row_bytes : 0}};
+  const Range out[4] = {{grad_x, row_bytes},
+                        {grad_a, (uint64_t)L * r * K * e},
+                        {grad_b, (uint64_t)L * N * r * e},
+                        {workspace, need}};
+  for (int i = 0; i < 4; ++i) {
+    const bool in_place = i == 0 && base == grad_x;
+    if (out[i].p && (overlaps_any(out[i], in, in_place ? 6 : 7) || overlaps_any(out[i], out, i)))
+      return IMC_ERR_ALIAS;
+  }
+  const int dev = require_device();
+  if (dev != IMC_OK) return dev;
+  cudaStream_t s = (cudaStream_t)stream;
+  Scratch sc(s);
+  if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
+  AdapterGradArgs p = {};
+  p.grad = grad;
+  p.x = x;
+  p.a = a;
+  p.b = b;
+  p.scale = scale;
+  p.offsets = layout;
+  p.order = layout + 2 * L + 3;
+  p.base = base;
+  p.grad_x = grad_x;
+  p.grad_a = grad_a;
+  p.grad_b = grad_b;
+  p.T = T;
+  p.K = K;
+  p.N = N;
+  p.L = (int)L;
+  p.r = (int)r;
+  p.workspace = sc.p;
+  return finish_call(sc.give(launch_adapters_backward(p, dtype, s)), IMC_KERNEL_ADAPTERS);
+}
+
+}  // extern "C"
+
+namespace {
+// What moe_balance and its gradient have in common; IMC_OK or the status.
+int balance_args(BalanceArgs& p, const void* logits, int dtype, int64_t T, int64_t E,
+                 int64_t row_stride, const int32_t* experts, int64_t k, int score,
+                 const int32_t* offsets, int64_t S) {
+  if (!float_type(dtype) || (score != IMC_SCORE_SOFTMAX && score != IMC_SCORE_SIGMOID))
+    return IMC_ERR_ARG;
+  if (T < 0 || T > kMaxRows || !route_dims_ok(T, E, k) || row_stride < (T > 1 ? E : 0) || S < 0 ||
+      S > kMaxRows || S * E > kMaxDim || (!offsets && S != 1))
+    return IMC_ERR_SHAPE;
+  if (!aligned(logits, (uintptr_t)dtype_bytes(dtype)) || !aligned(experts, 4) ||
+      !aligned(offsets, 4))
+    return IMC_ERR_ARG;
+  p = {};
+  p.logits = logits;
+  p.T = T;
+  p.ld = row_stride;
+  p.E = (int)E;
+  p.k = (int)k;
+  p.S = (int)S;
+  p.sigmoid = score == IMC_SCORE_SIGMOID ? 1 : 0;
+  p.experts = experts;
+  p.offsets = offsets;
+  return IMC_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t row_stride,
+                const int32_t* experts, int64_t k, int score, const int32_t* offsets, int64_t S,
+                float* loss, int32_t* counts, void* stream) {
+  BalanceArgs p;
+  const int rc = balance_args(p, logits, dtype, T, E, row_stride, experts, k, score, offsets, S);
+  if (rc != IMC_OK) return rc;
+  if (S == 0) return finish_empty();
+  if ((T > 0 && (!logits || !experts)) || !loss || !counts) return IMC_ERR_NULL;
+  if (!aligned(loss, 4) || !aligned(counts, 4)) return IMC_ERR_ARG;
+  const Range in[3] = {{logits, span(dtype, 1, T, E, 0, row_stride)},
+                       {experts, (uint64_t)(T * k) * 4},
+                       {offsets, (uint64_t)(S + 1) * 4}};
+  const Range out[2] = {{loss, (uint64_t)S * 4}, {counts, (uint64_t)(S * E) * 4}};
+  if (overlaps_any(out[0], in, 3) || overlaps_any(out[1], in, 3) || overlaps_any(out[1], out, 1))
+    return IMC_ERR_ALIAS;
+  const int dev = require_device();
+  if (dev != IMC_OK) return dev;
+  p.loss = loss;
+  p.counts = counts;
+  return finish_call(launch_balance(p, dtype, (cudaStream_t)stream), IMC_KERNEL_EXPERTS);
+}
+
+int moe_balance_backward(const float* grad_loss, const void* logits, int dtype, int64_t T,
+                         int64_t E, int64_t row_stride, const int32_t* experts, int64_t k,
+                         int score, const int32_t* counts, const int32_t* offsets, int64_t S,
+                         const float* grad_weights, int renormalize, double scale,
+                         void* grad_logits, void* stream) {
+  BalanceArgs p;
+  const int rc = balance_args(p, logits, dtype, T, E, row_stride, experts, k, score, offsets, S);
+  if (rc != IMC_OK) return rc;
+  if ((renormalize != 0 && renormalize != 1) || !std::isfinite(scale)) return IMC_ERR_ARG;
+  if (T == 0) return finish_empty();
+  if (!logits || !grad_logits || (S > 0 && (!grad_loss || !counts)) || (grad_weights && !experts))
+    return IMC_ERR_NULL;
+  const uint64_t b = (uint64_t)dtype_bytes(dtype);
+  if (!aligned(grad_loss, 4) || !aligned(counts, 4) || !aligned(grad_weights, 4) ||
+      !aligned(grad_logits, b))
+    return IMC_ERR_ARG;
+  const Range in[6] = {{logits, span(dtype, 1, T, E, 0, row_stride)},
+                       {experts, (uint64_t)(T * k) * 4},
+                       {offsets, (uint64_t)(S + 1) * 4},
+                       {grad_loss, (uint64_t)S * 4},
+                       {counts, (uint64_t)(S * E) * 4},
+                       {grad_weights, (uint64_t)(T * k) * 4}};
+  if (overlaps_any({grad_logits, (uint64_t)(T * E) * b}, in, 6)) return IMC_ERR_ALIAS;
+  const int dev = require_device();
+  if (dev != IMC_OK) return dev;
+  p.grad_loss = grad_loss;
+  p.counts = const_cast<int32_t*>(counts);
+  p.grad_weights = grad_weights;
+  p.renorm = renormalize;
+  p.scale = (float)scale;
+  p.grad = grad_logits;
+  return finish_call(launch_balance_backward(p, dtype, (cudaStream_t)stream), IMC_KERNEL_EXPERTS);
 }
 
 }  // extern "C"

@@ -1,0 +1,64 @@
+// A token's scores in the registers of a warp: what routing, its gradient and the
+// balance loss share.
+#pragma once
+
+#include "mx_internal.cuh"
+
+namespace imc {
+namespace mx {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+// Scores of one token: lane l holds experts l, l + 32, ... (VPT of them).
+// softmax: exp(x - max) / sum; a row of -inf alone has scores 0.
+template <int VPT, typename T>
+__device__ __forceinline__ void scores(const T* row, int E, int sigmoid, float (&s)[VPT]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int e = lane + 32 * j;
+    s[j] = e < E ? to_f32<T>(row[e]) : -INFINITY;
+  }
+  if (sigmoid) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) s[j] = 1.0f / (1.0f + expf(-s[j]));
+  } else {
+    float m = s[0];
+#pragma unroll
+    for (int j = 1; j < VPT; ++j) m = fmaxf(m, s[j]);
+    m = warp_max(m);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      s[j] = m == -INFINITY && s[j] == m ? 0.0f : expf(s[j] - m);
+      sum += s[j];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) s[j] *= inv;
+  }
+}
+
+template <int VPT>
+__device__ __forceinline__ float pick(const float (&s)[VPT], int j) {
+  float v = s[0];
+#pragma unroll
+  for (int i = 1; i < VPT; ++i)
+    if (i == j) v = s[i];
+  return v;
+}
+
+}  // namespace mx
+}  // namespace imc

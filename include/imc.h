@@ -1,12 +1,13 @@
 /*
  * imc.h -- C ABI of libimc: fp32 addmm and groups==1 NCHW conv2d, both run as
  * one tiled GEMM with a fused epilogue on NVIDIA sm_103a (GB300); 4-bit
- * (MXFP4) products; routing to experts and the experts' products.
+ * (MXFP4) products; routing to experts, its balance loss and the experts'
+ * products; low-rank adapters beside a projection.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - All tensor pointers are DEVICE pointers to contiguous row-major fp32
- *    data owned by the caller (the 4-bit and expert entry points also take
+ *    data owned by the caller (the 4-bit, expert and adapter entry points also take
  *    fp16 and bf16 data and row strides, as they say).  The library never frees or keeps a pointer to
  *    them beyond the call; it may cache CUDA function attributes per device.
  *  - Device memory: the tensor-core kernels need scratch -- addmm a copy of
@@ -104,7 +105,8 @@ extern "C" {
 #define IMC_KERNEL_FILL 4 /* epilogue only: K == 0 or alpha == 0           */
 #define IMC_KERNEL_DIRECT 5 /* direct conv2d kernel (IMC_MODE_DIRECT)      */
 #define IMC_KERNEL_MXFP4 6 /* 4-bit quantisation or product                */
-#define IMC_KERNEL_EXPERTS 7 /* routing, layout or weighted sum of experts */
+#define IMC_KERNEL_EXPERTS 7 /* routing, balance loss, layout or weighted sum of experts */
+#define IMC_KERNEL_ADAPTERS 8 /* low-rank adapters                          */
 
 /* ---------------------------------------- element types of the 4-bit and expert operators */
 #define IMC_F32 0
@@ -516,6 +518,74 @@ int moe_combine_f32(const float* y, const float* weights, int64_t T, int64_t k, 
 int moe_combine_backward(const void* grad, const void* y, int dtype, const float* weights,
                          int64_t T, int64_t k, int64_t N, void* grad_y, float* grad_weights,
                          void* stream);
+
+/*
+ * Balance loss of a router.  Sequence s holds the n tokens offsets[s] ..
+ * offsets[s + 1] - 1 (offsets [S + 1] ascend; values outside 0 .. T count as the
+ * nearer end; NULL: one sequence of all T tokens, S = 1).  counts[s,e] is the
+ * number of its slots whose expert is e (slots of no expert in [0, E) are not
+ * counted), p[t] the softmax of the logits, or their sigmoids divided by their
+ * sum (0 where that is 0):
+ *
+ *   loss[s] = E / (k * n^2) * sum_e counts[s,e] * sum_t p[t,e]     (0 for n = 0)
+ *
+ * which is 1 for an even choice at even scores.  Tokens in no sequence (padding
+ * behind the last one) count nowhere.  The sums are fp32 over 64 tokens and 64-bit
+ * beyond, in a fixed order.
+ *   logits [T,E], rows row_stride elements apart; experts [T,k] (moe_route's);
+ *   loss [S], counts [S,E].  T <= 2^27, S <= 2^27, S * E < 2^31.
+ */
+int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t row_stride,
+                const int32_t* experts, int64_t k, int score, const int32_t* offsets, int64_t S,
+                float* loss, int32_t* counts, void* stream);
+
+/* grad_logits [T,E] (contiguous, of type dtype): gradient of sum_s grad_loss[s] *
+ * loss[s], the counts taken as constant; 0 for tokens in no sequence.
+ * grad_weights [T,k] (may be NULL): the gradient of moe_route's weights with this
+ * renormalize and scale, as moe_route_backward gives it, is added before the one
+ * rounding to dtype.  experts may be NULL without grad_weights. */
+int moe_balance_backward(const float* grad_loss, const void* logits, int dtype, int64_t T,
+                         int64_t E, int64_t row_stride, const int32_t* experts, int64_t k,
+                         int score, const int32_t* counts, const int32_t* offsets, int64_t S,
+                         const float* grad_weights, int renormalize, double scale,
+                         void* grad_logits, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection (linear_f32,
+ * mxfp4_linear).  Row t has adapter l of L <= 1024, or none:
+ *
+ *   out[t] = base[t] + scale[l] * (x[t] a[l]^T) b[l]^T      (none: base[t])
+ *
+ *   layout  moe_layout of the rows' adapters: T tokens, k = 1, E = L; a row whose
+ *         number is outside [0, L) has none.  One layout serves every projection
+ *         of a step.
+ *   x     [T,K], rows row_stride elements apart.   a [L,r,K], b [L,N,r], 1 <= r <=
+ *         128.   scale [L] fp32 or NULL (ones).
+ *   base  [T,N] or NULL (zeros); out [T,N].  out may be base itself: then the rows
+ *         without an adapter are neither read nor written.  No other overlap.
+ * x, a, b, base and out are of type dtype; K >= 1, T <= 2^27.  Sums are fp32, and
+ * x a^T is kept to 16 bits of precision (fp32: 24) for the second product; an output
+ * is rounded once.  Non-finite values reach their own row only.
+ */
+int lowrank_linear(const void* x, int dtype, int64_t row_stride, const void* a, const void* b,
+                    const float* scale, const int32_t* layout, const void* base, void* out,
+                    int64_t T, int64_t L, int64_t r, int64_t K, int64_t N, void* stream);
+
+/* Gradients for grad [T,N]; with g[t] = scale[l] * (grad[t] b[l]):
+ *   grad_x[t] = base[t] + g[t] a[l]      (none: base[t]; base [T,K] or NULL: zeros)
+ *   grad_a[l] = sum over l's rows of g[t]^T x[t]
+ *   grad_b[l] = sum over l's rows of grad[t]^T (scale[l] * x[t] a[l]^T)
+ * All tensors are contiguous and of type dtype; T, K, N >= 1.  grad_x may be base
+ * itself.  Each of grad_x, grad_a and grad_b may be NULL (not computed).  An adapter
+ * without rows has gradients of 0.  Results do not depend on timing.
+ * workspace: lowrank_linear_backward_workspace_bytes(T, r) bytes, 16-byte aligned;
+ * NULL: from the library's pool. */
+size_t lowrank_linear_backward_workspace_bytes(int64_t T, int64_t r);
+int lowrank_linear_backward(const void* grad, const void* x, const void* a, const void* b,
+                             int dtype, const float* scale, const int32_t* layout,
+                             const void* base, void* grad_x, void* grad_a, void* grad_b, int64_t T,
+                             int64_t L, int64_t r, int64_t K, int64_t N, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* imc_status_string(int status);
