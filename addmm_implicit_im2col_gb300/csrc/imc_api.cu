@@ -701,12 +701,13 @@ uint64_t imc_launch_count(void) { return g_launches.load(std::memory_order_relax
 int imc_check_device_error(void* stream) {
   const int dev = check_device();
   if (dev != IMC_OK) return dev;
-  int vg = 0, vc = 0, vm = 0;
+  int vg = 0, vc = 0, vm = 0, va = 0;
   if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess ||
       gemm_take_watchdog(&vg) != cudaSuccess || conv_take_watchdog(&vc) != cudaSuccess ||
-      mx::product_take_watchdog(&vm) != cudaSuccess)
+      mx::product_take_watchdog(&vm) != cudaSuccess ||
+      mx::adapters_take_watchdog(&va) != cudaSuccess)
     return IMC_ERR_CUDA;
-  return (vg != 0 || vc != 0 || vm != 0) ? IMC_ERR_TIMEOUT : IMC_OK;
+  return (vg != 0 || vc != 0 || vm != 0 || va != 0) ? IMC_ERR_TIMEOUT : IMC_OK;
 }
 
 int imc_version(void) { return 104; }

@@ -106,13 +106,14 @@ int require_device();
 // Used by the 4-bit and expert entry points (mx_api.cu): the end of a call
 // (records the kernel for imc_last_kernel*), the end of one with nothing to
 // do, the overlap test of the argument checks, scratch from the library's
-// stream-ordered pool, and the watchdog word of the 4-bit product.
+// stream-ordered pool, and the watchdog words of the 4-bit product and the adapters.
 int finish_call(cudaError_t e, int kernel);
 int finish_empty();
 bool ranges_overlap(const void* a, uint64_t abytes, const void* b, uint64_t bbytes);
 cudaError_t scratch_alloc(void** p, size_t bytes, cudaStream_t s);
 namespace mx {
 cudaError_t product_take_watchdog(int* value);
+cudaError_t adapters_take_watchdog(int* value);
 }
 
 // Number of SMs of the current device (cached per device).
