@@ -87,7 +87,9 @@ SIGNATURES = {
     "moe_balance": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp]),
     "moe_balance_backward": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _vp,
                                     _i64, _vp, _int, _dbl, _vp, _vp]),
-    "lowrank_linear": (_int, [_vp, _int, _i64] + [_vp] * 6 + [_i64] * 5 + [_vp]),
+    "lowrank_linear_workspace_bytes": (ctypes.c_size_t, [_i64] * 3),
+    "lowrank_linear": (_int, [_vp, _int, _i64] + [_vp] * 6 + [_i64] * 5
+                       + [_vp, ctypes.c_size_t, _vp]),
     "lowrank_linear_backward_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "lowrank_linear_backward": (_int, [_vp] * 4 + [_int] + [_vp] * 6 + [_i64] * 5
                                  + [_vp, ctypes.c_size_t, _vp]),
@@ -313,10 +315,14 @@ def moe_balance_backward(grad_loss, logits, dtype, T, E, row_stride, experts, k,
                                        grad_logits, stream)
 
 
-def lowrank_linear(x, dtype, row_stride, a, b, scale, layout, base, out, T, L, r, K, N,
-                   stream) -> int:
+def lowrank_linear_workspace_bytes(T, L, r) -> int:
+    return int(load().lowrank_linear_workspace_bytes(T, L, r))
+
+
+def lowrank_linear(x, dtype, row_stride, a, b, scale, layout, base, out, T, L, r, K, N, workspace,
+                   workspace_bytes, stream) -> int:
     return load().lowrank_linear(x, dtype, row_stride, a, b, scale, layout, base, out, T, L, r, K,
-                                 N, stream)
+                                 N, workspace, workspace_bytes, stream)
 
 
 def lowrank_linear_backward_workspace_bytes(T, r) -> int:
@@ -589,7 +595,8 @@ _size = functools.lru_cache(maxsize=4096)(mxfp4_bytes)
 _linear_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_workspace_bytes)
 _layout_size = functools.lru_cache(maxsize=4096)(moe_layout_size)
 _experts_size = functools.lru_cache(maxsize=4096)(mxfp4_experts_linear_workspace_bytes)
-_lowrank_size = functools.lru_cache(maxsize=4096)(lowrank_linear_backward_workspace_bytes)
+_lowrank_size = functools.lru_cache(maxsize=4096)(lowrank_linear_workspace_bytes)
+_lowrank_back_size = functools.lru_cache(maxsize=4096)(lowrank_linear_backward_workspace_bytes)
 _backward_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_backward_workspace_bytes)
 
 
@@ -1107,9 +1114,11 @@ def adapters_linear(x, a, b, layout, base=None, *, scale=None, out=None):
         out = _torch.empty((T, N), dtype=x.dtype, device=x.device)
     else:
         _check_plain(out, "out", x.dtype, (T, N), x)
+    nbytes = _lowrank_size(T, L, r)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=x.device) if nbytes else None
     rc = _calls.lowrank_linear(x.data_ptr(), dt, ld, a.data_ptr(), b.data_ptr(), _ptr(scale),
                              layout.data.data_ptr(), _ptr(base), out.data_ptr(), T, L, r, K, N,
-                             _stream_of(x))
+                             _ptr(ws), nbytes, _stream_of(x))
     if rc:
         raise ImcError(rc, "lowrank_linear")
     return out
@@ -1131,7 +1140,7 @@ def adapters_linear_backward(grad, x, a, b, layout, base=None, *, scale=None):
         grad_x = _torch.zeros_like(x) if base is None else base.clone()
         return grad_x, _torch.zeros_like(a), _torch.zeros_like(b)
     grad_x, grad_a, grad_b = _torch.empty_like(x), _torch.empty_like(a), _torch.empty_like(b)
-    nbytes = _lowrank_size(T, r)
+    nbytes = _lowrank_back_size(T, r)
     ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
     rc = _calls.lowrank_linear_backward(grad.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), dt,
                                       _ptr(scale), layout.data.data_ptr(), _ptr(base),

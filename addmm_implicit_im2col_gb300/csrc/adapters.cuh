@@ -22,7 +22,9 @@ struct AdapterArgs {
   void* out;            // [T, N]; may be base
   int64_t T, K, N;
   int L, r;
+  void* workspace;      // adapters_bytes
 };
+size_t adapters_bytes(int64_t T, int64_t L, int64_t r);
 cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t s);
 
 struct AdapterGradArgs {

@@ -210,43 +210,48 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------------- tiles
-// More rows: 128 rows of one adapter per cluster, on the tensor cores (tcgen05, bf16
-// operands, fp32 accumulators).  CTA q of C takes a run of K for the tile's h = x a^T
-// [128, r]; the cluster's sums are taken in the order of the CTAs, each CTA for 128 / C
-// rows, which it gives to all of them; then every CTA takes a run of the N outputs.
-// x is read once, base and out once, and h never leaves the cluster.
+// More rows: tiles of 128 rows of one adapter on the tensor cores (tcgen05, fp32
+// accumulators), in two launches.  The first computes h = x a^T, a cluster of C CTAs for
+// each tile: CTA q takes a run of K, and the cluster's sums are taken in the order of the
+// CTAs.  The second adds h b^T to base, a CTA for each 128 x 128 outputs.  Both stream
+// (x; base and out), and many small CTAs on an SM hide the memory's latency.  One launch
+// for both (h stayed in the cluster) took 66 us for 8192 rows, 8 adapters, r 32, 4096 x
+// 4096, bf16, where these take
 //
-// A value is P bf16 numbers (bf16 1, fp16 2, fp32 3: exact) and an element of h PH (2 for
-// the 16-bit types, 3 for fp32), one "plane" each.  The planes of the small operand lie
-// one after the other along the MMA's N, so a plane of x is read once by the tensor core
-// for all of them; the sums over the planes are taken in fp32 afterwards.
+// A value is a sum of bf16 numbers ("planes"): bf16 1, fp16 2, fp32 3, exactly; an element
+// of h is kept as PH of them (2 for the 16-bit types: to 2^-17 of its value; 3 for fp32).
+// The planes of the operand that lies along the MMA's N follow one another there, so
+// that the tensor core reads a plane of the other operand once for all of them; the sums
+// over those planes are taken in fp32 afterwards.
 constexpr int TILE = 128;            // rows of a tile: the MMA's M
 constexpr int KB = 64;               // values of K per stage: 128 bytes of a plane's row
 constexpr int XP = TILE * KB * 2;    // bytes of a plane of a stage's x
 constexpr int UP_N = 128;            // outputs of one step of the second product
-constexpr int EPI_PITCH = 36;        // floats per staged row of the epilogue
-constexpr int EPI_BYTES = kWarps * 32 * EPI_PITCH * 4;
-// Core matrices (8 rows x 16 bytes) of the operands along r: 144 bytes apart over the
-// rows, so that writes along either axis spread over the banks.
-constexpr int CORE = 144;
-constexpr int CORES = TILE / 8;
-constexpr int CORE_K = CORE * CORES;  // apart over r
+// Core matrices (8 rows x 16 bytes) of the operands along r: CORE bytes apart over the
+// rows and CORE_K over r.  The 16-bit types' are spread over the banks, fp32's planes have
+// to fit for r = 128.
+template <typename T>
+constexpr int CORE = sizeof(T) == 2 ? 144 : 128;
+template <typename T>
+constexpr int CORE_K = CORE<T> * (TILE / 8) + 32;
 
 __device__ int g_watchdog_adapters;
 
 template <typename T>
 struct Planes;
+// P: planes of a value; PD: of one in the first product, which takes fp16 as it is (its
+// format FD); STAGES of that one's ring.
 template <>
 struct Planes<__nv_bfloat16> {
-  static constexpr int P = 1, PH = 2, DEPTH = 2, STAGES = 3;
+  static constexpr int P = 1, PD = 1, PH = 2, FD = 1, STAGES = 4, GRAD_STAGES = 3;
 };
 template <>
 struct Planes<__half> {
-  static constexpr int P = 2, PH = 2, DEPTH = 2, STAGES = 2;
+  static constexpr int P = 2, PD = 1, PH = 2, FD = 0, STAGES = 4, GRAD_STAGES = 2;
 };
 template <>
 struct Planes<float> {
-  static constexpr int P = 3, PH = 3, DEPTH = 1, STAGES = 1;
+  static constexpr int P = 3, PD = 3, PH = 3, FD = 1, STAGES = 2, GRAD_STAGES = 2;
 };
 
 // Eight values of a row as they lie in memory.
@@ -295,232 +300,239 @@ __device__ __forceinline__ void split8(float (&v)[8], uint4 (&out)[Q]) {
     out[q] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-template <typename T>
-__device__ __forceinline__ void planes_of(const Raw8<T>& raw, uint4 (&out)[Planes<T>::P]) {
-  if constexpr (Planes<T>::P == 1) {
+// Eight values in Q planes; one: as they are.
+template <typename T, int Q>
+__device__ __forceinline__ void planes_of(const Raw8<T>& raw, uint4 (&out)[Q]) {
+  if constexpr (Q == 1) {
     out[0] = raw.w[0];
   } else {
     float v[8];
     raw.widen(v);
-    split8<Planes<T>::P>(v, out);
+    split8<Q>(v, out);
   }
 }
-__device__ __forceinline__ uint16_t half_of(const uint4& u, int i) {
-  const uint32_t w = i < 2 ? u.x : (i < 4 ? u.y : (i < 6 ? u.z : u.w));
-  return (uint16_t)(i & 1 ? w >> 16 : w);
-}
-
-struct TileProblem {
-  const void* x;        // [T, K], rows ld elements apart
+struct DownProblem {
+  const void* x;   // [T, K], rows ld elements apart
   int64_t ld, K;
-  const void* w1;       // of an adapter [r, K]; turned: [K, r]
-  uint16_t* h;          // planes [PH][T][R] of h in adapter order, or null
-  const void* w2;       // of an adapter [N, r]; turned: [r, N]
-  const void* base;
-  void* out;            // null: h alone
-  int64_t N;
-  int turned, vec;      // vec: 1 x, 2 w1, 4 w2, 8 base and out
+  const void* w;   // of an adapter [r, K]; turned: [K, r]
+  uint16_t* h;     // planes [PH][T][R], in adapter order
+  int turned, vec; // vec: 1 x, 2 w
 };
-struct TileArgs {
-  TileProblem prob[2];
+struct DownArgs {
+  DownProblem prob[2];
   const float* scale;
   const int32_t *offsets, *order;
   int64_t T;
-  int L, r, R;          // R: r rounded up to 16
-  int log_ctas, stages, area, cols;  // area: bytes of the stages and what follows them there
+  int L, r, R, log_ctas, cols;  // R: r rounded up to 16
 };
-
-struct TileCtl {
-  uint64_t empty[4], up, drain;
+struct RingCtl {
+  uint64_t empty[4], drain;
   uint32_t tmem_base;
   int abort;
-  int rows[TILE];
 };
 
-template <typename T, int RU>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && RU == 1 ? 3 : 1)
-    k_adapters_tile(const __grid_constant__ TileArgs g) {
-  using PL = Planes<T>;
-  constexpr int P = PL::P, PH = PL::PH, DEPTH = PL::DEPTH;
-  extern __shared__ uint8_t sm_raw[];
-  __shared__ TileCtl ctl;
-  uint8_t* sm = tc::smem_align1024(sm_raw);
-  const TileProblem& p = g.prob[blockIdx.y];
-  const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R, r = g.r;
-  int* wd = &g_watchdog_adapters;
-  if (tid == 0) {
-    for (int i = 0; i < 4; ++i) ptx::mbar_init(&ctl.empty[i], 1);
-    ptx::mbar_init(&ctl.up, 1);
-    ptx::mbar_init(&ctl.drain, 1);
+// Barriers and tensor memory of a block.  The memory is taken before the stream's next
+// kernel may start: a block of that one that had it would wait for this kernel's end.
+template <typename Ctl>
+__device__ __forceinline__ uint32_t set_up(Ctl& ctl, int barriers, uint64_t* bars, int cols) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < barriers; ++i) ptx::mbar_init(bars + i, 1);
     ctl.abort = 0;
     ptx::fence_mbar_init();
   }
-  // Tensor memory before the stream's next kernel may start: a block of that one that had
-  // taken it would wait for this kernel's end.
-  if (warp == 0) {
-    ptx::tmem_alloc(&ctl.tmem_base, g.cols);
+  if (threadIdx.x < 32) {
+    ptx::tmem_alloc(&ctl.tmem_base, cols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl.tmem_base;
-  ptx::cluster_arrive();  // this CTA runs: its shared memory may be accessed
+  return ctl.tmem_base;
+}
+// After a wait that gave up, no MMA may run on into freed memory.
+template <typename Ctl>
+__device__ __forceinline__ void tear_down(Ctl& ctl, uint32_t tmem, int cols) {
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  ptx::tc_fence_after();
+  if (ctl.abort) {
+    if (ptx::elect_one()) ptx::mma_commit(&ctl.drain);
+    __syncwarp();
+    tc::drain_wait(&ctl.drain, 0);
+  }
+  ptx::tmem_dealloc(tmem, cols);
+}
+
+// Bytes of w in a stage: n rows of 128 bytes, or units of 64 of them turned.
+__host__ __device__ constexpr int down_w_bytes(int n) { return (n + 63) / 64 * (KB * 128); }
+
+template <typename T, int RU>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    k_adapters_down(const __grid_constant__ DownArgs g) {
+  using PL = Planes<T>;
+  constexpr int P = PL::PD, PH = PL::PH, S = PL::STAGES;
+  constexpr bool ASYNC = sizeof(T) == 2;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ RingCtl ctl;
+  __shared__ int rows[TILE];
+  uint8_t* sm = tc::smem_align1024(sm_raw);
+  const DownProblem& p = g.prob[blockIdx.y];
+  const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R, r = g.r;
+  int* wd = &g_watchdog_adapters;
+  const uint32_t tmem = set_up(ctl, 5, ctl.empty, g.cols);
   ptx::griddep_wait();
   ptx::griddep_launch();
-  const bool none = p.out && p.base != p.out;
-  const RowTile t = find_tile(g.offsets, g.L, none, TILE, blockIdx.x >> g.log_ctas);
-  if (tid < TILE) ctl.rows[tid] = tid < t.rows ? g.order[t.p0 + tid] : -1;
-  __syncthreads();
-  const int stage_bytes = P * (XP + R * 128);
-  uint8_t* hp = sm + g.area;  // planes of h
-  const int h_plane = (R >> 3) * CORE_K;
-  const int steps = (int)ceil_div(p.N, UP_N), per = (int)ceil_div(steps, C);
-  const int s0 = min(rank * per, steps), s1 = p.out ? min(s0 + per, steps) : s0;
-  const T* base = static_cast<const T*>(p.base);
-  T* out = static_cast<T*>(p.out);
-  bool work = t.rows > 0;
-  if (work && t.l == g.L) {  // rows without an adapter
-    const int64_t n0 = (int64_t)s0 * UP_N, n1 = (int64_t)s1 * UP_N < p.N ? (int64_t)s1 * UP_N : p.N;
-    for (int i = warp; i < t.rows; i += kWarps) {
-      const int64_t at = ctl.rows[i] * p.N;
-      for (int64_t n = n0 + lane * 8; n < n1; n += 256) {
-        float v[8];
-        const int left = (int)(n1 - n < 8 ? n1 - n : 8);
-        if (base) {
-          Raw8<T> raw;
-          raw.load(base + at + n, left, p.vec & 8);
-          if ((p.vec & 8) && left == 8) {
-#pragma unroll
-            for (int w = 0; w < Raw8<T>::W; ++w) reinterpret_cast<uint4*>(out + at + n)[w] = raw.w[w];
-          } else {
-            for (int u = 0; u < left; ++u) out[at + n + u] = base[at + n + u];
-          }
-        } else {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = 0.0f;
-          store8<T>(out + at + n, left, p.vec & 8, v);
-        }
-      }
-    }
-    work = false;
-  }
-  ptx::cluster_wait();
-  if (work) {
-    // ---- h = x a^T over this CTA's run of K
-    const int blocks = (int)ceil_div(p.K, KB), kper = (int)ceil_div(blocks, C);
-    const int b0 = min(rank * kper, blocks), b1 = min(b0 + kper, blocks);
-    const T* w1 = static_cast<const T*>(p.w1) + (int64_t)t.l * r * p.K;
+  const RowTile t = find_tile(g.offsets, g.L, false, TILE, blockIdx.x >> g.log_ctas);
+  if (t.rows > 0) {  // else the whole cluster has no tile
+    if (tid < TILE) rows[tid] = tid < t.rows ? g.order[t.p0 + tid] : -1;
+    __syncthreads();
+    const int stage_bytes = P * XP + down_w_bytes(P * R);
+    const int blocks = (int)ceil_div(p.K, KB), per = (blocks + C - 1) >> g.log_ctas;
+    const int b0 = min(rank * per, blocks), b1 = min(b0 + per, blocks);
+    const T* w = static_cast<const T*>(p.w) + (int64_t)t.l * r * p.K;
     const int u = tid & 7;
     const T* xr[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = ctl.rows[(tid >> 3) + 32 * i];
+      const int row = rows[(tid >> 3) + 32 * i];
       xr[i] = row < 0 ? nullptr : static_cast<const T*>(p.x) + row * p.ld + u * 8;
     }
-    struct Regs {
-      Raw8<T> x[4], w[RU];
+    // x and w of a block go straight to shared memory, or (fp32, and rows that 16-byte
+    // copies cannot reach) through registers.  w lies by its rows j with 64 k each, or
+    // turned (r contiguous) by k with the planes' j in units of 64, as the MMA's "MN-major"
+    // operand.
+    const bool copy_x = ASYNC && (p.vec & 1), copy_w = ASYNC && (p.vec & 2);
+    Raw8<T> held_w[RU], held_x[ASYNC ? 1 : 4];
+    const int ru = R >> 3;
+    int wj[RU], wk[RU];  // this thread's units of w
+#pragma unroll
+    for (int i = 0; i < RU; ++i) {
+      const int idx = tid + i * kThreads;
+      wk[i] = p.turned ? idx / ru : u * 8;
+      wj[i] = p.turned ? (idx - wk[i] * ru) * 8 : idx >> 3;
+    }
+    auto w_unit = [&](int i, int64_t k, int left, int& n) {
+      const bool in = wj[i] < r && wk[i] < left;
+      n = !in ? 0 : (p.turned ? r - wj[i] : left - wk[i]);
+      return p.turned ? w + (k + wk[i]) * r + wj[i] : w + wj[i] * p.K + k + wk[i];
     };
-    auto load = [&](Regs& q, int b) {
+    auto fetch = [&](int b) {
       const int64_t k = (int64_t)b * KB;
       const int left = (int)(p.K - k < KB ? p.K - k : KB);
+      if (!ASYNC) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q.x[i].load(xr[i] ? xr[i] + k : nullptr, xr[i] ? left - u * 8 : 0, p.vec & 1);
+        for (int i = 0; i < 4; ++i) held_x[ASYNC ? 0 : i].load(xr[i] + k, xr[i] ? left - u * 8 : 0, p.vec & 1);
+      }
+      if (!copy_w) {
 #pragma unroll
-      for (int i = 0; i < RU; ++i) {
-        if (p.turned) {  // eight j of one k
-          const int idx = tid + i * kThreads, kk = idx & 63, j = (idx >> 6) * 8;
-          q.w[i].load(w1 + (k + kk) * r + j, kk < left ? r - j : 0, p.vec & 2);
-        } else {  // eight k of one j
-          const int j = (tid >> 3) + 32 * i;
-          q.w[i].load(w1 + j * p.K + k + u * 8, j < r ? left - u * 8 : 0, p.vec & 2);
+        for (int i = 0; i < RU; ++i) {
+          int n;
+          const T* from = w_unit(i, k, left, n);
+          held_w[i].load(from, n, p.vec & 2);
         }
       }
     };
-    auto stage = [&](const Regs& q, uint8_t* to) {
+    auto put = [&](int b, uint8_t* to) {
+      const int64_t k = (int64_t)b * KB;
+      const int left = (int)(p.K - k < KB ? p.K - k : KB);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = (tid >> 3) + 32 * i;
-        uint4 v[P];
-        planes_of<T>(q.x[i], v);
+        const int row = (tid >> 3) + 32 * i, at = row * 128 + ((u ^ (row & 7)) << 4);
+        if (copy_x) {  // K is a multiple of 8: a unit of 16 bytes is whole or missing
+          const bool in = xr[i] && u * 8 < left;
+          ptx::copy16(to + at, in ? xr[i] + k : static_cast<const T*>(p.x), in);
+        } else {
+          Raw8<T> raw;
+          if (ASYNC) raw.load(xr[i] + k, xr[i] ? left - u * 8 : 0, false);
+          else raw = held_x[ASYNC ? 0 : i];
+          uint4 v[P];
+          planes_of<T, P>(raw, v);
 #pragma unroll
-        for (int c = 0; c < P; ++c)
-          *reinterpret_cast<uint4*>(to + c * XP + row * 128 + ((u ^ (row & 7)) << 4)) = v[c];
+          for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(to + c * XP + at) = v[c];
+        }
       }
       uint8_t* wt = to + P * XP;
 #pragma unroll
       for (int i = 0; i < RU; ++i) {
+        if (wj[i] >= R || wk[i] >= KB) continue;
         uint4 v[P];
-        planes_of<T>(q.w[i], v);
-        if (p.turned) {
-          const int idx = tid + i * kThreads, kk = idx & 63, j = (idx >> 6) * 8;
-          if (j < R) {
+        if (!copy_w) planes_of<T, P>(held_w[i], v);
 #pragma unroll
-            for (int c = 0; c < P; ++c)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint16_t*>(wt + (c * R + j + e) * 128 + (((kk >> 3) ^ e) << 4) +
-                                             (kk & 7) * 2) = half_of(v[c], e);
-          }
-        } else {
-          const int j = (tid >> 3) + 32 * i;
-          if (j < R) {
-#pragma unroll
-            for (int c = 0; c < P; ++c)
-              *reinterpret_cast<uint4*>(wt + (c * R + j) * 128 + ((u ^ (j & 7)) << 4)) = v[c];
+        for (int c = 0; c < P; ++c) {
+          const int j = c * R + wj[i];
+          uint8_t* at = wt + (p.turned ? (j >> 6) * (KB * 128) + wk[i] * 128 + ((((j >> 3) ^ wk[i]) & 7) << 4)
+                                       : j * 128 + ((u ^ (j & 7)) << 4));
+          if (copy_w) {
+            int n;
+            const T* from = w_unit(i, k, left, n);
+            ptx::copy16(at, n > 0 ? from : w, n > 0);
+          } else {
+            *reinterpret_cast<uint4*>(at) = v[c];
           }
         }
       }
     };
-    Regs q[DEPTH];
+    if (b0 < b1) fetch(b0);
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (b0 + d < b1) load(q[d], b0 + d);
-    int slot = 0, use = 0;
-    for (int b = b0; b < b1; b += DEPTH) {
+    for (int i = 0; i < S - 1; ++i) {
+      if (b0 + i < b1) {
+        put(b0 + i, sm + i * stage_bytes);
+        if (b0 + i + 1 < b1) fetch(b0 + i + 1);
+      }
+      ptx::copy_commit();
+    }
+    int slot = 0, use = 0;  // of block b
+    for (int b = b0; b < b1; ++b) {
+      ptx::copy_wait<S - 2>();
+      ptx::fence_proxy_async_smem();
+      __syncthreads();
+      if (warp == 0) {
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t xa = ptx::smem_addr(sm + slot * stage_bytes), wa = xa + P * XP;
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        if (b + d < b1) {
-          if (use > 0) tc::warp_wait_bar(&ctl.empty[slot], (use - 1) & 1, &ctl.abort, 1, wd);
-          uint8_t* to = sm + slot * stage_bytes;
-          stage(q[d], to);
-          if (b + d + DEPTH < b1) load(q[d], b + d + DEPTH);
-          ptx::fence_proxy_async_smem();
-          __syncthreads();
-          if (warp == 0 && ptx::elect_one()) {
-            ptx::tc_fence_after();
-            const uint32_t xa = ptx::smem_addr(to), wa = xa + P * XP;
+          for (int c = 0; c < P; ++c) {
+            const int n = (P - c) * R;  // fp32: the smallest products are left out
+            for (int n0 = 0; n0 < n; n0 += 256) {
+              const int nn = min(256, n - n0);
+              const uint32_t id = ptx::idesc_f16(PL::FD, TILE, nn, false, p.turned);
+              // (n0 is a multiple of 64; 64 rows of j and 64 k by 64 j both take 8 KB)
 #pragma unroll
-            for (int c = 0; c < P; ++c) {
-              const int n = (P == 3 ? 3 - c : P) * R;  // fp32: the smallest products are left out
-              for (int n0 = 0; n0 < n; n0 += 256) {
-                const int nn = min(256, n - n0);
-                const uint32_t id = ptx::idesc_bf16(TILE, nn, false, false);
-#pragma unroll
-                for (int ks = 0; ks < KB / 16; ++ks)
-                  ptx::mma_f16(tmem + n0, ptx::smem_desc(xa + c * XP + ks * 32, 16, 1024, ptx::kSwizzle128B),
-                               ptx::smem_desc(wa + n0 * 128 + ks * 32, 16, 1024, ptx::kSwizzle128B), id,
-                               b + d > b0 || c > 0 || ks > 0);
-              }
+              for (int ks = 0; ks < KB / 16; ++ks)
+                ptx::mma_f16(tmem + n0, ptx::smem_desc(xa + c * XP + ks * 32, 16, 1024, ptx::kSwizzle128B),
+                             ptx::smem_desc(wa + n0 * 128 + ks * (p.turned ? 2048 : 32), KB * 128, 1024,
+                                            ptx::kSwizzle128B),
+                             id, b > b0 || c > 0 || ks > 0);
             }
-            ptx::mma_commit(&ctl.empty[slot]);
           }
-          __syncwarp();
-          if (++slot == g.stages) {
-            slot = 0;
-            ++use;
-          }
+          ptx::mma_commit(&ctl.empty[slot]);
         }
+        __syncwarp();
+      }
+      // the next block to load goes where the block before this one was
+      if (b + S - 1 < b1) {
+        const int last = slot ? slot - 1 : S - 1;
+        if (b > b0) tc::warp_wait_bar(&ctl.empty[last], (slot ? use : use - 1) & 1, &ctl.abort, 1, wd);
+        put(b + S - 1, sm + last * stage_bytes);
+        if (b + S < b1) fetch(b + S);
+      }
+      ptx::copy_commit();
+      if (++slot == S) {
+        slot = 0;
+        ++use;
       }
     }
+    ptx::copy_wait<0>();
     // ---- this CTA's sums to its shared memory
     const int q4 = warp & 3, pitch = R * 4 + 16;
     if (b1 > b0) {
-      const int done = (b1 - b0 - 1) % g.stages, uses = (b1 - b0 - 1) / g.stages;
+      const int done = (b1 - b0 - 1) % S, uses = (b1 - b0 - 1) / S;
       tc::warp_wait_bar(&ctl.empty[done], uses & 1, &ctl.abort, 2, wd);
       ptx::tc_fence_after();
     }
+    __syncthreads();
     for (int j = (warp >> 2) * 16; j < R; j += 32) {
       float v[16];
 #pragma unroll
@@ -528,26 +540,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && RU == 1 ? 3 : 1)
       if (b1 > b0) {
 #pragma unroll
         for (int c = 0; c < P; ++c) {
-          uint32_t w[16];
-          ptx::tmem_ld16(tmem + ((uint32_t)(q4 * 32) << 16) + c * R + j, w);
+          uint32_t s[16];
+          ptx::tmem_ld16(tmem + ((uint32_t)(q4 * 32) << 16) + c * R + j, s);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(w[i]);
+          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(s[i]);
         }
       }
       float4* to = reinterpret_cast<float4*>(sm + (q4 * 32 + lane) * pitch + j * 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
-    ptx::tc_fence_before();
-  }
-  ptx::cluster_sync();
-  if (work) {
-    // ---- h of 128 / C rows: the sums of all CTAs, in planes to all CTAs
-    const int pitch = R * 4 + 16, mine = TILE >> g.log_ctas, units = mine * (R >> 3);
     const float scale = g.scale ? g.scale[t.l] : 1.0f;
+    ptx::cluster_sync();
+    // ---- h of 128 / C rows: the sums of all CTAs
+    const int mine = TILE >> g.log_ctas, units = mine * (R >> 3);
     for (int i = tid; i < units; i += kThreads) {
-      const int row = rank * mine + (i & (mine - 1)), ju = i >> (7 - g.log_ctas);
+      const int row = rank * mine + i / (R >> 3), ju = i % (R >> 3);
+      if (row >= t.rows) break;
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.0f;
@@ -559,147 +569,396 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && RU == 1 ? 3 : 1)
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= scale;
-      uint4 w[PH];
-      split8<PH>(v, w);
-      if (p.h && row < t.rows) {
+      uint4 w8[PH];
+      split8<PH>(v, w8);
 #pragma unroll
-        for (int c = 0; c < PH; ++c)
-          *reinterpret_cast<uint4*>(p.h + ((int64_t)c * g.T + t.p0 + row) * R + ju * 8) = w[c];
-      }
-      if (p.out) {
-        uint8_t* to = hp + ju * CORE_K + (row >> 3) * CORE + (row & 7) * 16;
-        for (int d = 0; d < C; ++d)
-#pragma unroll
-          for (int c = 0; c < PH; ++c) ptx::st_cluster4(ptx::cluster_addr(to + c * h_plane, d), w[c]);
-      }
+      for (int c = 0; c < PH; ++c)
+        *reinterpret_cast<uint4*>(p.h + ((int64_t)c * g.T + t.p0 + row) * R + ju * 8) = w8[c];
     }
-    ptx::fence_proxy_async();  // these writes are for the tensor cores
+    ptx::cluster_sync();  // no CTA ends while another reads its sums
   }
-  ptx::cluster_sync();
-  if (work && s1 > s0) {
-    // ---- out = base + h b^T, UP_N columns at a time
-    ptx::fence_proxy_async();
-    const T* w2 = static_cast<const T*>(p.w2) + (int64_t)t.l * r * p.N;
+  tear_down(ctl, tmem, g.cols);
+}
+
+struct UpArgs {
+  const uint16_t* h;  // planes [PH][T][R]
+  const void* w;      // of an adapter [N, r]; turned: [r, N]
+  const void* base;
+  void* out;
+  const int32_t *offsets, *order;
+  int64_t T, N;
+  int L, r, R, steps, turned, vec;  // vec: 1 w, 2 base and out (32 bytes)
+  int slots, h_slots, w_bytes, h_bytes;  // of the rings of w and h; bytes of one
+};
+constexpr int UP_EPI = 8, UP_LOAD = 4;  // warps
+constexpr int UP_THREADS = (UP_EPI + UP_LOAD + 1) * 32;
+constexpr int UP_SLOTS = 4;
+constexpr int kAdapters = 1024;  // the most that a layout has
+struct UpCtl {
+  uint64_t wfull[UP_SLOTS], wempty[UP_SLOTS], hfull[2], hempty[2], accf[2], acce[2], drain;
+  uint32_t tmem_base;
+  int abort;
+  int sums[UP_THREADS / 32];
+  int before[kAdapters + 2], first[kAdapters + 2];  // tiles before a bucket, its first row
+};
+
+// Tile t of the counted buckets.
+__device__ __forceinline__ RowTile tile_of(const UpCtl& ctl, int B, int t) {
+  int low = 0, high = B;  // before[low] <= t < before[high]
+  while (high - low > 1) {
+    const int mid = (low + high) >> 1;
+    if (ctl.before[mid] <= t) low = mid;
+    else high = mid;
+  }
+  const int p0 = ctl.first[low] + (t - ctl.before[low]) * TILE;
+  return {low, p0, min(TILE, ctl.first[low + 1] - p0)};
+}
+
+__device__ __forceinline__ uint32_t add_pair(__nv_bfloat16, uint32_t base, float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(base << 16) + a,
+                                                 __uint_as_float(base & 0xFFFF0000u) + b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t add_pair(__half, uint32_t base, float a, float b) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&base));
+  const __half2 v = __floats2half2_rn(f.x + a, f.y + b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Columns that a warp stages at once where rows are not written 32 bytes at a time.
+template <typename T>
+constexpr int STAGED_COLS = sizeof(T) == 2 ? 32 : 16;
+
+// Persistent blocks, each with an equal run of the (tile, 128 outputs) items:
+//   warps 0-7   epilogue: a thread has a row and half of an item's columns: base (read an
+//               item ahead), the product from tensor memory, one rounding, 32-byte stores;
+//               rows that those cannot reach go through the warp's shared memory
+//   warps 8-11  h of a tile and w of an item to shared memory
+//   warp 12     tensor memory, MMAs (two accumulators of 128 columns)
+template <typename T>
+__global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_constant__ UpArgs g) {
+  using PL = Planes<T>;
+  constexpr int P = PL::P, PH = PL::PH;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ UpCtl ctl;
+  uint8_t* sm = tc::smem_align1024(sm_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R, r = g.r;
+  int* wd = &g_watchdog_adapters;
+  if (tid == 0) {
+    for (int i = 0; i < UP_SLOTS; ++i) {
+      ptx::mbar_init(&ctl.wfull[i], UP_LOAD * 32);
+      ptx::mbar_init(&ctl.wempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&ctl.hfull[i], UP_LOAD * 32);
+      ptx::mbar_init(&ctl.hempty[i], 1);
+      ptx::mbar_init(&ctl.accf[i], 1);
+      ptx::mbar_init(&ctl.acce[i], UP_EPI * 32);
+    }
+    ptx::mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == UP_EPI + UP_LOAD) {
+    ptx::tmem_alloc(&ctl.tmem_base, 2 * UP_N);
+    ptx::tmem_relinquish();
+  }
+  // The call's inputs are there already (the first launch has waited for them); h is not.
+  const T* base = static_cast<const T*>(g.base);
+  T* out = static_cast<T*>(g.out);
+  const int B = g.L + (g.base != g.out ? 1 : 0);  // rows without an adapter: copied, or left
+  {
+    const int per = (B + UP_THREADS - 1) / UP_THREADS, e0 = tid * per;
+    int tiles = 0;
+    for (int e = e0; e < e0 + per && e < B; ++e) {
+      const int first = __ldg(g.offsets + e);
+      ctl.first[e] = first;
+      tiles += (__ldg(g.offsets + e + 1) - first + TILE - 1) / TILE;
+    }
+    if (tid == 0) ctl.first[B] = __ldg(g.offsets + B);
+    int upto = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kAll, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (lane == 31) ctl.sums[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += ctl.sums[w];
+    int at = upto - tiles;
+    for (int e = e0; e < e0 + per && e < B; ++e) {
+      ctl.before[e] = at;
+      at += (__ldg(g.offsets + e + 1) - ctl.first[e] + TILE - 1) / TILE;
+    }
+    if (tid == UP_THREADS - 1) ctl.before[B] = upto;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  ptx::griddep_launch();
+  const int64_t items = (int64_t)ctl.before[B] * g.steps;
+  const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  uint8_t* hs = sm + g.slots * g.w_bytes;
+  const int plane = (R >> 3) * CORE_K<T>;
+
+  if (warp >= UP_EPI && warp < UP_EPI + UP_LOAD) {
+    // ------------------------------------------------------------- loaders
+    ptx::griddep_wait();
+    const int lt = tid - UP_EPI * 32, ru = R >> 3;
+    constexpr int LT = UP_LOAD * 32;
+    const bool copy_w = P == 1 && (g.vec & 1);
+    int last = -1, seg = 0, n = 0;
+    uint64_t *pending_w = nullptr, *pending_h = nullptr;
+    auto arrived = [&] {  // (the copies have been waited for)
+      ptx::fence_proxy_async_smem();
+      if (pending_h) ptx::mbar_arrive(pending_h);
+      if (pending_w) ptx::mbar_arrive(pending_w);
+      pending_w = pending_h = nullptr;
+    };
+    for (int64_t it = i0; it < i1; ++it) {
+      const int tile = (int)(it / g.steps);
+      const int64_t n0 = (it - (int64_t)tile * g.steps) * UP_N;
+      const RowTile t = tile_of(ctl, B, tile);
+      if (t.l == g.L) continue;
+      uint64_t* now_h = nullptr;
+      if (tile != last) {
+        last = tile;
+        const int hb = seg % g.h_slots;
+        uint8_t* ht = hs + hb * g.h_bytes;
+        if (seg >= g.h_slots) {
+          if (g.h_slots == 1) {  // the MMAs that free it wait for the item before this one
+            ptx::copy_wait<0>();
+            arrived();
+          }
+          tc::warp_wait_bar(&ctl.hempty[hb], (seg / g.h_slots - 1) & 1, &ctl.abort, 6, wd);
+        }
+        for (int i = lt; i < TILE * ru; i += LT) {
+          const int row = i / ru, ju = i - row * ru;
+          const bool in = row < t.rows;
+#pragma unroll
+          for (int c = 0; c < PH; ++c)
+            ptx::copy16(ht + c * plane + ju * CORE_K<T> + (row >> 3) * CORE<T> + (row & 7) * 16,
+                        in ? g.h + ((int64_t)c * g.T + t.p0 + row) * R + ju * 8 : g.h, in);
+        }
+        ++seg;
+        now_h = &ctl.hfull[hb];
+      }
+      const int slot = n % g.slots, use = n / g.slots;
+      if (use > 0) {
+        if (g.slots == 1) {
+          ptx::copy_wait<0>();
+          arrived();
+        }
+        tc::warp_wait_bar(&ctl.wempty[slot], (use - 1) & 1, &ctl.abort, 7, wd);
+      }
+      uint8_t* to = sm + slot * g.w_bytes;
+      const T* w = static_cast<const T*>(g.w) + (int64_t)t.l * r * g.N;
+      const int left = (int)(g.N - n0 < UP_N ? g.N - n0 : UP_N);
+#pragma unroll 4
+      for (int i = lt; i < TILE / 8 * R; i += LT) {
+        const T* from;
+        uint8_t* at;
+        int have, pitch;
+        if (g.turned) {  // eight n of one j; n lies along the operand's N
+          const int nu = i & 15, j = i >> 4;
+          from = w + j * g.N + n0 + nu * 8;
+          have = j < r ? left - nu * 8 : 0;
+          at = to + (nu >> 3) * (R * 128) + j * 128 + (((nu ^ j) & 7) << 4);
+          pitch = R * 256;
+        } else {  // eight j of one n
+          const int nn = i / ru, ju = i - nn * ru;
+          from = w + (n0 + nn) * r + ju * 8;
+          have = nn < left ? r - ju * 8 : 0;
+          at = to + ju * CORE_K<T> + (nn >> 3) * CORE<T> + (nn & 7) * 16;
+          pitch = plane;
+        }
+        if (copy_w) {
+          ptx::copy16(at, have > 0 ? from : w, have > 0);
+        } else {
+          Raw8<T> raw;
+          raw.load(from, have, g.vec & 1);
+          uint4 v[P];
+          planes_of<T, P>(raw, v);
+#pragma unroll
+          for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(at + c * pitch) = v[c];
+        }
+      }
+      ptx::copy_commit();
+      if (pending_w) {  // the item before this one has arrived
+        ptx::copy_wait<1>();
+        arrived();
+      }
+      pending_w = &ctl.wfull[slot];
+      pending_h = now_h;
+      ++n;
+      if (ctl.abort) break;
+    }
+    ptx::copy_wait<0>();
+    arrived();
+  } else if (warp == UP_EPI + UP_LOAD) {
+    // ---------------------------------------------------------------- MMAs
+    int last = -1, seg = 0, n = 0, hb = 0;
+    const uint32_t id = ptx::idesc_f16(1, TILE, UP_N, false, g.turned);
+    for (int64_t it = i0; it < i1; ++it) {
+      const int tile = (int)(it / g.steps);
+      if (tile_of(ctl, B, tile).l == g.L) continue;
+      if (tile != last) {
+        last = tile;
+        hb = seg % g.h_slots;
+        if (!tc::warp_wait_bar(&ctl.hfull[hb], (seg / g.h_slots) & 1, &ctl.abort, 8, wd)) break;
+        ++seg;
+      }
+      const int slot = n % g.slots, buf = n & 1;
+      if (!tc::warp_wait_bar(&ctl.wfull[slot], (n / g.slots) & 1, &ctl.abort, 9, wd)) break;
+      if (n > 1 && !tc::warp_wait_bar(&ctl.acce[buf], (n / 2 - 1) & 1, &ctl.abort, 10, wd)) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        const uint32_t ha = ptx::smem_addr(hs + hb * g.h_bytes), wa = ptx::smem_addr(sm + slot * g.w_bytes);
+        uint32_t more = 0;
+        for (int ks = 0; ks < R / 16; ++ks)
+#pragma unroll
+          for (int d = 0; d < P; ++d) {
+            const uint64_t wdesc =
+                g.turned ? ptx::smem_desc(wa + d * (R * 256) + ks * 2048, R * 128, 1024, ptx::kSwizzle128B)
+                         : ptx::smem_desc(wa + d * plane + ks * 2 * CORE_K<T>, CORE_K<T>, CORE<T>, 0);
+#pragma unroll
+            for (int c = 0; c < PH; ++c) {
+              if (P == 3 && c + d > 2) continue;  // fp32: the smallest products are left out
+              ptx::mma_f16(tmem + buf * UP_N,
+                           ptx::smem_desc(ha + c * plane + ks * 2 * CORE_K<T>, CORE_K<T>, CORE<T>, 0), wdesc, id, more);
+              more = 1;
+            }
+          }
+        ptx::mma_commit(&ctl.wempty[slot]);
+        ptx::mma_commit(&ctl.accf[buf]);
+        if (it + 1 == i1 || (int)((it + 1) / g.steps) != tile) ptx::mma_commit(&ctl.hempty[hb]);
+      }
+      __syncwarp();
+      ++n;
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
     const int q4 = warp & 3, half = warp >> 2;
-    float* rows = reinterpret_cast<float*>(sm) + warp * 32 * EPI_PITCH;
-    const int er = lane >> 2, ec = (lane & 3) * 8;
-    for (int s = s0; s < s1; ++s) {
-      const int64_t n0 = (int64_t)s * UP_N;
-      const int left = (int)(p.N - n0 < UP_N ? p.N - n0 : UP_N);
-      Raw8<T> held[2][4];  // base
-      auto fetch = [&](int h) {
+    constexpr int W = UP_N / 2 * (int)sizeof(T) / 32;  // 32-byte words of a thread's columns
+    constexpr bool AHEAD = sizeof(T) == 2;
+    const bool wide = g.vec & 2;
+    uint32_t held[W][8];
+    int row = -1, at_tile = -1;
+    RowTile t = {0, 0, 0};
+    // An item's row of this thread and its part of base.
+    auto fetch = [&](int64_t it) {
+      const int tile = (int)(it / g.steps);
+      const int64_t col = (it - (int64_t)tile * g.steps) * UP_N + half * 64;
+      if (tile != at_tile) {
+        at_tile = tile;
+        t = tile_of(ctl, B, tile);
+        const int in = q4 * 32 + lane;
+        row = in < t.rows ? __ldg(g.order + t.p0 + in) : -1;
+      }
+      if (wide) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = ctl.rows[q4 * 32 + i * 8 + er], col = half * 64 + h * 32 + ec;
-          const bool in = base && row >= 0;
-          const T* from = in ? base + row * p.N + n0 + col : nullptr;
-          if ((p.vec & 8) && in && left - col >= 8) {  // not __ldg: out may be base
-#pragma unroll
-            for (int w = 0; w < Raw8<T>::W; ++w)
-              held[h][i].w[w] = reinterpret_cast<const uint4*>(from)[w];
+        for (int i = 0; i < W; ++i) {
+          if (base && row >= 0 && col + i * (32 / (int)sizeof(T)) < g.N) {
+            ptx::ld_global_v8_rw(held[i], base + row * g.N + col + i * (32 / (int)sizeof(T)));
           } else {
-            alignas(16) T v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = in && e < left - col ? from[e] : from_f32<T>(0.0f);
-#pragma unroll
-            for (int w = 0; w < Raw8<T>::W; ++w) held[h][i].w[w] = reinterpret_cast<const uint4*>(v)[w];
+            for (int e = 0; e < 8; ++e) held[i][e] = 0;
           }
         }
-      };
-      fetch(0);
-      if (sizeof(T) == 2) fetch(1);
-      const int units = CORES * R;  // of eight values
-      for (int i = tid; i < units; i += kThreads) {
-        Raw8<T> raw;
-        uint4 v[P];
-        if (p.turned) {  // eight n of one j
-          const int j = i % R, nu = i / R;
-          raw.load(w2 + j * p.N + n0 + nu * 8, j < r ? left - nu * 8 : 0, p.vec & 4);
-          planes_of<T>(raw, v);
-#pragma unroll
-          for (int c = 0; c < P; ++c)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint16_t*>(sm + c * h_plane + (j >> 3) * CORE_K + nu * CORE + e * 16 +
-                                           (j & 7) * 2) = half_of(v[c], e);
-        } else {  // eight j of one n
-          const int n = i & (UP_N - 1), j = (i >> 7) * 8;
-          raw.load(w2 + (n0 + n) * r + j, n < left ? r - j : 0, p.vec & 4);
-          planes_of<T>(raw, v);
-#pragma unroll
-          for (int c = 0; c < P; ++c)
-            *reinterpret_cast<uint4*>(sm + c * h_plane + (j >> 3) * CORE_K + (n >> 3) * CORE + (n & 7) * 16) = v[c];
-        }
       }
-      ptx::fence_proxy_async_smem();
-      __syncthreads();
-      if (warp == 0) {
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint32_t id = ptx::idesc_bf16(TILE, UP_N, false, false);
-          const uint32_t ha = ptx::smem_addr(hp), wa = ptx::smem_addr(sm);
-          uint32_t more = 0;
-          for (int ks = 0; ks < R / 16; ++ks)
-#pragma unroll
-            for (int c = 0; c < PH; ++c)
-#pragma unroll
-              for (int d = 0; d < P; ++d) {
-                if (P == 3 && c + d > 2) continue;
-                ptx::mma_f16(tmem, ptx::smem_desc(ha + c * h_plane + ks * 2 * CORE_K, CORE_K, CORE, 0),
-                             ptx::smem_desc(wa + d * h_plane + ks * 2 * CORE_K, CORE_K, CORE, 0), id, more);
-                more = 1;
-              }
-          ptx::mma_commit(&ctl.up);
-        }
-        __syncwarp();
-      }
-      tc::warp_wait_bar(&ctl.up, (s - s0) & 1, &ctl.abort, 3, wd);
+    };
+    if (AHEAD && i0 < i1) fetch(i0);
+    int n = 0;
+    for (int64_t it = i0; it < i1; ++it) {
+      if (!AHEAD) fetch(it);
+      const int64_t col = (it - it / g.steps * g.steps) * UP_N + half * 64;
+      const int to_row = row;
+      const bool product = t.l < g.L;
+      const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + (n & 1) * UP_N + half * 64;
+      if (product && !tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
       ptx::tc_fence_after();
-      __syncthreads();  // every warp past the wait: the operand's place is free
+      T* to = out + to_row * g.N + col;
+      if (wide) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (sizeof(T) == 4 && h == 1) fetch(1);
-        uint32_t w[32];
-        ptx::tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + half * 64 + h * 32, w);
-        ptx::tmem_ld_wait();
-        float4* to = reinterpret_cast<float4*>(rows + lane * EPI_PITCH);
+        for (int b = 0; b < 2; ++b) {
+          uint32_t s[32];
+          if (product) {
+            ptx::tmem_ld32(acc + b * 32, s);
+            ptx::tmem_ld_wait();
+          }
+          if (product && b) {
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&ctl.acce[n & 1]);
+          }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          to[i] = make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]),
-                              __uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3]));
-        __syncwarp();
+          for (int i = 0; i < W / 2; ++i) {
+            uint32_t(&h)[8] = held[b * (W / 2) + i];
+            if (product) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = ctl.rows[q4 * 32 + i * 8 + er], col = half * 64 + h * 32 + ec;
-          const float4 a = *reinterpret_cast<const float4*>(rows + (i * 8 + er) * EPI_PITCH + ec);
-          const float4 b = *reinterpret_cast<const float4*>(rows + (i * 8 + er) * EPI_PITCH + ec + 4);
-          float v[8];
-          held[h][i].widen(v);
-          v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-          v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-          if (row >= 0 && col < left) store8<T>(out + row * p.N + n0 + col, left - col, p.vec & 8, v);
+              for (int e = 0; e < 8; ++e) {
+                if constexpr (sizeof(T) == 2)
+                  h[e] = add_pair(T(), h[e], __uint_as_float(s[i * 16 + 2 * e]), __uint_as_float(s[i * 16 + 2 * e + 1]));
+                else
+                  h[e] = __float_as_uint(__uint_as_float(h[e]) + __uint_as_float(s[i * 8 + e]));
+              }
+            }
+            const int c = b * 32 + i * (32 / (int)sizeof(T));
+            if (to_row >= 0 && col + c < g.N) ptx::st_global_v8(to + c, h);
+          }
         }
-        __syncwarp();
+        if (AHEAD && it + 1 < i1) fetch(it + 1);
+      } else {
+        constexpr int SC = STAGED_COLS<T>, ROWS = 32 / SC;  // columns, and rows at once
+        float* mine = reinterpret_cast<float*>(hs + g.h_slots * g.h_bytes) + warp * 32 * (SC + 1);
+#pragma unroll 1
+        for (int b = 0; b < 64 / SC; ++b) {
+          if (product) {
+            uint32_t s[SC];
+            if constexpr (SC == 32) ptx::tmem_ld32(acc + b * SC, s);
+            else ptx::tmem_ld16(acc + b * SC, s);
+            ptx::tmem_ld_wait();
+            if (b + 1 == 64 / SC) {
+              ptx::tc_fence_before();
+              ptx::mbar_arrive(&ctl.acce[n & 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < SC; ++e) mine[lane * (SC + 1) + e] = __uint_as_float(s[e]);
+            __syncwarp();
+          }
+          const int64_t c = col + b * SC + lane % SC;  // a lane has a column of its rows
+#pragma unroll 8
+          for (int i = lane / SC; i < 32; i += ROWS) {
+            const int64_t at = (int64_t)__shfl_sync(kAll, to_row, i) * g.N + c;
+            if (at < 0 || c >= g.N) continue;
+            if (!product) out[at] = base ? base[at] : from_f32<T>(0.0f);
+            else out[at] = from_f32<T>((base ? to_f32<T>(base[at]) : 0.0f) + mine[i * (SC + 1) + lane % SC]);
+          }
+          __syncwarp();
+        }
+        if (AHEAD && it + 1 < i1) fetch(it + 1);
       }
-      ptx::tc_fence_before();
-      __syncthreads();
+      if (product) ++n;
     }
   }
-  if (ctl.abort && warp == 0) {  // a wait gave up: no MMA may run on into freed memory
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp != UP_EPI + UP_LOAD) return;
+  ptx::tc_fence_after();
+  if (ctl.abort) {  // after a wait that gave up, no MMA may run on into freed memory
     if (ptx::elect_one()) ptx::mma_commit(&ctl.drain);
     __syncwarp();
     tc::drain_wait(&ctl.drain, 0);
   }
-  __syncthreads();
-  if (warp == 0) ptx::tmem_dealloc(tmem, g.cols);
+  ptx::tmem_dealloc(tmem, 2 * UP_N);
 }
 
 // ------------------------------------------------------- weights' gradients
 // grad_a[l][j][k] = sum over l's rows of g[p][j] x[row][k], and grad_b[l][n][j] with h and
 // grad.  A cluster has one adapter and 128 columns of x (or grad): they are the MMA's M,
 // the r columns of g its N, the rows its K.  CTA q of S takes a run of the rows; the
-// cluster's sums are taken in the order of the CTAs.  A tile of x is loaded by rows, so its
-// columns lie along the operand's M ("MN-major"); g's planes are turned on the way.
+// cluster's sums are taken in the order of the CTAs.  Tiles of x and of g's planes are
+// loaded by rows, so their columns lie along the operands' M and N ("MN-major").
 constexpr int GRAD_ROWS = 64;  // rows per stage
 constexpr int GRAD_COLS = 128;
 
@@ -714,21 +973,19 @@ struct GradArgs {
   GradProblem prob[2];
   const int32_t *offsets, *order;
   int64_t T;
-  int L, r, R, log_ctas, stages, cols;
+  int L, r, R, log_ctas, cols;
 };
-struct GradCtl {
-  uint64_t empty[4], drain;
-  uint32_t tmem_base;
-  int abort;
-};
+// Bytes of h's n columns in a stage: GRAD_ROWS rows in units of 64 columns.
+__host__ __device__ constexpr int grad_h_bytes(int n) { return (n + 63) / 64 * (GRAD_ROWS * 128); }
 
-template <typename T, int RU>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && RU == 1 ? 3 : 1)
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     k_adapters_grad(const __grid_constant__ GradArgs g) {
   using PL = Planes<T>;
-  constexpr int P = PL::P, PH = PL::PH;
+  constexpr int P = PL::P, PH = PL::PH, S = PL::GRAD_STAGES;
+  constexpr bool HELD = P > 1;  // x goes through registers, a block ahead
   extern __shared__ uint8_t sm_raw[];
-  __shared__ GradCtl ctl;
+  __shared__ RingCtl ctl;
   uint8_t* sm = tc::smem_align1024(sm_raw);
   const GradProblem& p = g.prob[blockIdx.z];
   const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank();
@@ -736,20 +993,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && RU == 1 ? 3 : 1)
   const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * GRAD_COLS;
   const int l = blockIdx.y;
   int* wd = &g_watchdog_adapters;
-  if (tid == 0) {
-    for (int i = 0; i < 4; ++i) ptx::mbar_init(&ctl.empty[i], 1);
-    ptx::mbar_init(&ctl.drain, 1);
-    ctl.abort = 0;
-    ptx::fence_mbar_init();
-  }
-  if (warp == 0) {
-    ptx::tmem_alloc(&ctl.tmem_base, g.cols);
-    ptx::tmem_relinquish();
-  }
-  ptx::tc_fence_before();
-  __syncthreads();
-  ptx::tc_fence_after();
-  const uint32_t tmem = ctl.tmem_base;
+  const uint32_t tmem = set_up(ctl, 5, ctl.empty, g.cols);
   ptx::griddep_wait();
   ptx::griddep_launch();
   // (the problems may have different numbers of columns)
@@ -758,88 +1002,88 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && RU == 1 ? 3 : 1)
   const int blocks = (rows + GRAD_ROWS - 1) / GRAD_ROWS, per = (blocks + C - 1) >> g.log_ctas;
   const int b0 = min(rank * per, blocks), b1 = work ? min(b0 + per, blocks) : b0;
   constexpr int XG = GRAD_ROWS * GRAD_COLS * 2;  // bytes of a plane of a stage's x
-  const int core_k = (PH * R / 8) * 128 + 16;     // 16 bytes more: writes spread over the banks
-  const int stage_bytes = (P * XG + 8 * core_k + 1023) & ~1023;
+  const int stage_bytes = P * XG + grad_h_bytes(PH * R);
   const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
-  const int u = tid & 15, xrow = tid >> 4;
+  const int u = tid & 15, xrow = tid >> 4, ru = R >> 3;
   const T* x = static_cast<const T*>(p.x) + col0 + u * 8;
-  struct Regs {
-    Raw8<T> x[4];
-    uint4 h[RU][PH];
-  };
-  int at[4];  // rows of the next block to be loaded
+  const bool copy = !HELD && p.vec;
+  int next[4];  // rows of the next block whose x is asked for
   auto rows_of = [&](int b) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int in = b * GRAD_ROWS + xrow + 16 * i;
-      at[i] = b < b1 && in < rows ? __ldg(g.order + first + in) : -1;
+      next[i] = b < b1 && in < rows ? __ldg(g.order + first + in) : -1;
     }
   };
-  auto load = [&](Regs& q, int b) {
+  Raw8<T> held[HELD ? 4 : 1];
+  auto fetch = [&](int b) {  // block b's x, then the rows of the next one
+    if (HELD) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q.x[i].load(x + at[i] * p.cols, at[i] >= 0 ? left - u * 8 : 0, p.vec);
-#pragma unroll
-    for (int i = 0; i < RU; ++i) {
-      const int idx = tid + i * kThreads, t = idx & 63, j = (idx >> 6) * 8, in = b * GRAD_ROWS + t;
-#pragma unroll
-      for (int c = 0; c < PH; ++c)
-        q.h[i][c] = j < R && in < rows
-                        ? __ldg(reinterpret_cast<const uint4*>(p.h + ((int64_t)c * g.T + first + in) * R + j))
-                        : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i)
+        held[HELD ? i : 0].load(x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, p.vec);
+      rows_of(b + 1);
     }
   };
-  Regs q;
-  rows_of(b0);
-  if (b0 < b1) load(q, b0);
-  rows_of(b0 + 1);
-  int slot = 0, use = 0;
-  for (int b = b0; b < b1; ++b) {
-    if (use > 0) tc::warp_wait_bar(&ctl.empty[slot], (use - 1) & 1, &ctl.abort, 4, wd);
-    uint8_t* to = sm + slot * stage_bytes;
+  auto put = [&](int b, uint8_t* to) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = xrow + 16 * i;
-      uint4 v[P];
-      planes_of<T>(q.x[i], v);
+      uint8_t* at = to + (u >> 3) * (GRAD_ROWS * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+      if (copy) {
+        const bool in = next[i] >= 0 && u * 8 < left;
+        ptx::copy16(at, in ? x + next[i] * p.cols : static_cast<const T*>(p.x), in);
+      } else {
+        Raw8<T> raw;
+        if (HELD) raw = held[HELD ? i : 0];
+        else raw.load(x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, false);
+        uint4 v[P];
+        planes_of<T, P>(raw, v);
 #pragma unroll
-      for (int c = 0; c < P; ++c)
-        *reinterpret_cast<uint4*>(to + c * XG + (u >> 3) * (GRAD_ROWS * 128) + row * 128 +
-                                  (((u & 7) ^ (row & 7)) << 4)) = v[c];
-    }
-    uint8_t* ht = to + P * XG;
-#pragma unroll
-    for (int i = 0; i < RU; ++i) {
-      const int idx = tid + i * kThreads, t = idx & 63, j = (idx >> 6) * 8;
-      if (j < R) {
-#pragma unroll
-        for (int c = 0; c < PH; ++c)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint16_t*>(ht + (t >> 3) * core_k + ((c * R + j) >> 3) * 128 + e * 16 +
-                                         (t & 7) * 2) = half_of(q.h[i][c], e);
+        for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(at + c * XG) = v[c];
       }
     }
-    if (b + 1 < b1) {
-      load(q, b + 1);
-      rows_of(b + 2);
+    uint8_t* ht = to + P * XG;
+    for (int i = tid; i < GRAD_ROWS * ru; i += kThreads) {
+      const int t = i / ru, ju = i - t * ru, in = b * GRAD_ROWS + t;
+#pragma unroll
+      for (int c = 0; c < PH; ++c) {
+        const int j = c * ru + ju;  // unit of the planes one after the other
+        ptx::copy16(ht + (j >> 3) * (GRAD_ROWS * 128) + t * 128 + (((j ^ t) & 7) << 4),
+                    in < rows ? p.h + ((int64_t)c * g.T + first + in) * R + ju * 8 : p.h, in < rows);
+      }
     }
+    if (!HELD) rows_of(b + 1);
+  };
+  rows_of(b0);
+  if (b0 < b1) fetch(b0);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    if (b0 + i < b1) {
+      put(b0 + i, sm + i * stage_bytes);
+      if (b0 + i + 1 < b1) fetch(b0 + i + 1);
+    }
+    ptx::copy_commit();
+  }
+  int slot = 0, use = 0;  // of block b
+  for (int b = b0; b < b1; ++b) {
+    ptx::copy_wait<S - 2>();
     ptx::fence_proxy_async_smem();
     __syncthreads();
     if (warp == 0) {
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
-        const uint32_t xa = ptx::smem_addr(to), ha = xa + P * XG;
+        const uint32_t xa = ptx::smem_addr(sm + slot * stage_bytes), ha = xa + P * XG;
 #pragma unroll
         for (int c = 0; c < P; ++c) {
-          const int n = (P == 3 ? 3 - c : PH) * R;
+          const int n = (P == 3 ? 3 - c : PH) * R;  // fp32: the smallest products are left out
           for (int n0 = 0; n0 < n; n0 += 256) {
             const int nn = min(256, n - n0);
-            const uint32_t id = ptx::idesc_bf16(GRAD_COLS, nn, true, false);
+            const uint32_t id = ptx::idesc_f16(1, GRAD_COLS, nn, true, true);
 #pragma unroll
             for (int ks = 0; ks < GRAD_ROWS / 16; ++ks)
               ptx::mma_f16(tmem + n0,
                            ptx::smem_desc(xa + c * XG + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B),
-                           ptx::smem_desc(ha + (n0 >> 3) * 128 + ks * 2 * core_k, core_k, 128, 0), id,
+                           ptx::smem_desc(ha + n0 * 128 + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B), id,
                            b > b0 || c > 0 || ks > 0);
           }
         }
@@ -847,15 +1091,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && RU == 1 ? 3 : 1)
       }
       __syncwarp();
     }
-    if (++slot == g.stages) {
+    // the next block to load goes where the block before this one was
+    if (b + S - 1 < b1) {
+      const int last = slot ? slot - 1 : S - 1;
+      if (b > b0) tc::warp_wait_bar(&ctl.empty[last], (slot ? use : use - 1) & 1, &ctl.abort, 4, wd);
+      put(b + S - 1, sm + last * stage_bytes);
+      if (b + S < b1) fetch(b + S);
+    }
+    ptx::copy_commit();
+    if (++slot == S) {
       slot = 0;
       ++use;
     }
   }
+  ptx::copy_wait<0>();
   const int pitch = R + 1;  // words of a column's sums
   float* part = reinterpret_cast<float*>(sm);
   if (b1 > b0) {
-    const int done = (b1 - b0 - 1) % g.stages, uses = (b1 - b0 - 1) / g.stages;
+    const int done = (b1 - b0 - 1) % S, uses = (b1 - b0 - 1) / S;
     tc::warp_wait_bar(&ctl.empty[done], uses & 1, &ctl.abort, 5, wd);
     ptx::tc_fence_after();
   }
@@ -895,13 +1148,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && RU == 1 ? 3 : 1)
     }
   }
   ptx::cluster_sync();  // no CTA ends while another reads its sums
-  if (ctl.abort && warp == 0) {
-    if (ptx::elect_one()) ptx::mma_commit(&ctl.drain);
-    __syncwarp();
-    tc::drain_wait(&ctl.drain, 0);
-  }
-  __syncthreads();
-  if (warp == 0) ptx::tmem_dealloc(tmem, g.cols);
+  tear_down(ctl, tmem, g.cols);
 }
 
 // ------------------------------------------------------------------- host
@@ -971,66 +1218,68 @@ cudaError_t adapters_few(const AdapterArgs& a, cudaStream_t s) {
     CALL(4);                 \
   } while (0)
 
-int log2_up(int64_t v) {
-  int n = 0;
-  while (((int64_t)1 << n) < v) ++n;
-  return n;
-}
-
 template <typename T>
-cudaError_t run_tiles(TileArgs g, int problems, cudaStream_t s) {
+cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
   using PL = Planes<T>;
-  g.R = (g.r + 15) / 16 * 16;
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
   // about three blocks per SM
   const int64_t want = 3 * (int64_t)device_sm_count() / (ceil_div(g.T, TILE) * problems);
-  g.log_ctas = want >= 8 ? 3 : log2_up(want < 1 ? 1 : want);
-  const int stage = PL::P * (XP + g.R * 128), h_plane = g.R / 8 * CORE_K;
-  g.stages = g.R > 64 && PL::STAGES > 2 ? 2 : PL::STAGES;
-  if (PL::P == 2 && g.R > 64) g.stages = 1;
-  int area = g.stages * stage;
-  const int others[3] = {TILE * (g.R * 4 + 16), PL::P * h_plane, EPI_BYTES};
-  for (int o : others) area = area > o ? area : o;
-  g.area = (area + 1023) / 1024 * 1024;
-  g.cols = tmem_cols(PL::P * g.R > UP_N ? PL::P * g.R : UP_N);
-  const size_t smem = smem_for((size_t)g.area + PL::PH * h_plane + 1024, g.cols);
+  g.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
+  const int ring = PL::STAGES * (PL::PD * XP + down_w_bytes(PL::PD * g.R)), sums = TILE * (g.R * 4 + 16);
+  g.cols = tmem_cols(PL::PD * g.R);
+  const size_t smem = smem_for((size_t)(ring > sums ? ring : sums) + 1024, g.cols);
   const dim3 grid((unsigned)(tiles << g.log_ctas), problems);
-#define IMC_TILES(RU) return launch_clusters(k_adapters_tile<T, RU>, grid, 1 << g.log_ctas, smem, s, g)
-  IMC_BY_RANK(g.R, IMC_TILES);
-#undef IMC_TILES
+#define IMC_DOWN(RU) return launch_clusters(k_adapters_down<T, RU>, grid, 1 << g.log_ctas, smem, s, g)
+  IMC_BY_RANK(g.R, IMC_DOWN);
+#undef IMC_DOWN
 }
 
-// Alignment for 16-byte accesses of each operand of a problem.
 template <typename T>
-int tile_vec(const TileProblem& p, int r) {
+cudaError_t run_up(UpArgs& g, cudaStream_t s) {
+  using PL = Planes<T>;
   const int64_t b = sizeof(T);
-  return (aligned16(p.x, p.ld * b) ? 1 : 0) | (aligned16(p.w1, (p.turned ? r : p.K) * b) ? 2 : 0) |
-         (aligned16(p.w2, (p.turned ? p.N : r) * b) ? 4 : 0) |
-         (aligned16(p.out, p.N * b) && aligned16(p.base, 0) ? 8 : 0);
+  g.steps = (int)ceil_div(g.N, UP_N);
+  const uintptr_t wide = reinterpret_cast<uintptr_t>(g.out) | reinterpret_cast<uintptr_t>(g.base) | (uintptr_t)(g.N * b);
+  g.vec = (aligned16(g.w, (g.turned ? g.N : g.r) * b) ? 1 : 0) | (wide % 32 == 0 ? 2 : 0);
+  const int plane = g.R / 8 * CORE_K<T>, staged = g.vec & 2 ? 0 : UP_EPI * 32 * (STAGED_COLS<T> + 1) * 4;
+  g.w_bytes = (PL::P * (g.turned ? g.R * 256 : plane) + 1023) / 1024 * 1024;
+  g.h_bytes = PL::PH * plane;
+  const int most = 232448 - (int)sizeof(UpCtl) - 256, room = most - 1024 - staged;
+  g.h_slots = room >= 2 * (g.h_bytes + g.w_bytes) ? 2 : 1;
+  g.slots = (room - g.h_slots * g.h_bytes) / g.w_bytes;
+  g.slots = g.slots < UP_SLOTS ? g.slots : UP_SLOTS;
+  const int smem = g.slots * g.w_bytes + g.h_slots * g.h_bytes + staged + 1024;
+  if (g.slots < 1) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(k_adapters_up<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t items = most_tiles(g.T, g.L, TILE) * g.steps, sms = device_sm_count();
+  e = launch_after_previous(k_adapters_up<T>, dim3((unsigned)(items < sms ? items : sms)), dim3(UP_THREADS),
+                            smem, s, g);
+  note_launch();
+  return e;
 }
+
+int round16(int r) { return (r + 15) / 16 * 16; }
 
 template <typename T>
 cudaError_t adapters(const AdapterArgs& a, cudaStream_t s) {
   if (a.T <= 64) return adapters_few<T>(a, s);
-  note_kernel_name("k_adapters_tile");
-  TileArgs g = {};
-  TileProblem& p = g.prob[0];
-  p.x = a.x;
-  p.ld = a.ld;
-  p.K = a.K;
-  p.w1 = a.a;
-  p.w2 = a.b;
-  p.base = a.base;
-  p.out = a.out;
-  p.N = a.N;
-  p.vec = tile_vec<T>(p, a.r);
+  note_kernel_name("k_adapters_up");
+  const int64_t b = sizeof(T);
+  DownArgs g = {};
   g.scale = a.scale;
   g.offsets = a.offsets;
   g.order = a.order;
   g.T = a.T;
   g.L = a.L;
   g.r = a.r;
-  return run_tiles<T>(g, 1, s);
+  g.R = round16(a.r);
+  g.prob[0] = {a.x, a.ld, a.K, a.a, static_cast<uint16_t*>(a.workspace), 0,
+               (aligned16(a.x, a.ld * b) && a.K % 8 == 0 ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0)};
+  const cudaError_t e = run_down<T>(g, 1, s);
+  if (e != cudaSuccess) return e;
+  UpArgs up = {g.prob[0].h, a.b, a.base, a.out, a.offsets, a.order, a.T, a.N, a.L, a.r, g.R, 0, 0, 0, 0, 0, 0, 0};
+  return run_up<T>(up, s);
 }
 
 size_t planes_bytes(int64_t T, int64_t r) {  // of h or g, whatever their type
@@ -1043,36 +1292,27 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
   note_kernel_name("k_adapters_grad");
   uint16_t* h = static_cast<uint16_t*>(a.workspace);
   uint16_t* d = h + planes_bytes(a.T, a.r) / 2;
-  TileArgs g = {};
+  DownArgs g = {};
   g.scale = a.scale;
   g.offsets = a.offsets;
   g.order = a.order;
   g.T = a.T;
   g.L = a.L;
   g.r = a.r;
+  g.R = round16(a.r);
+  const int64_t size = sizeof(T);
   int problems = 0;
-  if (a.grad_x || a.grad_a) {  // g = scale * grad b, and grad_x = base + g a
-    TileProblem& p = g.prob[problems++];
-    p.x = a.grad;
-    p.ld = p.K = a.N;
-    p.w1 = a.b;
-    p.w2 = a.a;
-    p.h = a.grad_a ? d : nullptr;
-    p.base = a.base;
-    p.out = a.grad_x;
-    p.N = a.grad_x ? a.K : 0;
-    p.turned = 1;
-    p.vec = tile_vec<T>(p, a.r);
+  if (a.grad_x || a.grad_a)  // g = scale * grad b
+    g.prob[problems++] = {a.grad, a.N, a.N, a.b, d, 1,
+                          (aligned16(a.grad, a.N * size) ? 1 : 0) | (aligned16(a.b, a.r * size) ? 2 : 0)};
+  if (a.grad_b)  // h = scale * x a^T
+    g.prob[problems++] = {a.x, a.K, a.K, a.a, h, 0,
+                          (aligned16(a.x, a.K * size) ? 1 : 0) | (aligned16(a.a, a.K * size) ? 2 : 0)};
+  cudaError_t e = run_down<T>(g, problems, s);
+  if (e == cudaSuccess && a.grad_x) {
+    UpArgs up = {d, a.a, a.base, a.grad_x, a.offsets, a.order, a.T, a.K, a.L, a.r, g.R, 0, 1, 0, 0, 0, 0, 0};
+    e = run_up<T>(up, s);
   }
-  if (a.grad_b) {  // h = scale * x a^T
-    TileProblem& p = g.prob[problems++];
-    p.x = a.x;
-    p.ld = p.K = a.K;
-    p.w1 = a.a;
-    p.h = h;
-    p.vec = tile_vec<T>(p, a.r);
-  }
-  cudaError_t e = run_tiles<T>(g, problems, s);
   if (e != cudaSuccess || (!a.grad_a && !a.grad_b)) return e;
   GradArgs w = {};
   w.offsets = a.offsets;
@@ -1080,7 +1320,7 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
   w.T = a.T;
   w.L = a.L;
   w.r = a.r;
-  w.R = (a.r + 15) / 16 * 16;
+  w.R = g.R;
   int parts = 0;
   int64_t chunks = 0, all = 0;
   auto add = [&](const void* x, int64_t cols, const uint16_t* planes, void* out, int turned) {
@@ -1101,17 +1341,13 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
   int64_t want = 3 * (int64_t)device_sm_count() / (all * a.L);
   const int64_t most = a.T / a.L / (4 * GRAD_ROWS);
   want = want < most ? want : most;
-  w.log_ctas = want >= 8 ? 3 : log2_up(want < 1 ? 1 : want);
-  const int stage = (PL::P * GRAD_ROWS * GRAD_COLS * 2 + 8 * (PL::PH * w.R / 8 * 128 + 16) + 1023) / 1024 * 1024;
-  w.stages = PL::P == 1 && w.R <= 64 ? 3 : (PL::P == 3 || w.R > 64 ? 1 : 2);
-  size_t bytes = (size_t)w.stages * stage, sums = (size_t)GRAD_COLS * (w.R + 1) * 4;
-  bytes = bytes > sums ? bytes : sums;
+  w.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
+  const size_t ring = (size_t)PL::GRAD_STAGES * (PL::P * GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R));
+  const size_t sums = (size_t)GRAD_COLS * (w.R + 1) * 4;
   w.cols = tmem_cols(PL::PH * w.R);
-  const size_t smem = smem_for(bytes + 1024, w.cols);
-  const dim3 grid((unsigned)(chunks << w.log_ctas), a.L, parts);
-#define IMC_GRADS(RU) return launch_clusters(k_adapters_grad<T, RU>, grid, 1 << w.log_ctas, smem, s, w)
-  IMC_BY_RANK(w.R, IMC_GRADS);
-#undef IMC_GRADS
+  const size_t smem = smem_for((ring > sums ? ring : sums) + 1024, w.cols);
+  return launch_clusters(k_adapters_grad<T>, dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
+                         smem, s, w);
 }
 
 }  // namespace
@@ -1122,6 +1358,9 @@ cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t s) {
   return adapters<__nv_bfloat16>(a, s);
 }
 
+size_t adapters_bytes(int64_t T, int64_t L, int64_t r) {
+  return T <= 64 ? 0 : planes_bytes(T, r);
+}
 size_t adapters_backward_bytes(int64_t T, int64_t r) { return 2 * planes_bytes(T, r); }
 
 cudaError_t launch_adapters_backward(const AdapterGradArgs& a, int dtype, cudaStream_t s) {

@@ -617,11 +617,11 @@ int moe_combine_backward(const void* grad, const void* y, int dtype, const float
 }  // extern "C"
 
 namespace {
-constexpr int64_t kMaxRows = 1 << 27;  // of the calls that launch a block for a few rows
+constexpr int64_t kMaxRows = 1 << 27, kMaxWidth = 1 << 20;  // grids stay below 2^31 blocks
 
 bool adapter_dims_ok(int64_t T, int64_t L, int64_t r, int64_t K, int64_t N) {
   return T >= 0 && T <= kMaxRows && L >= 1 && L <= kMaxExperts && r >= 1 && r <= kMaxRank &&
-         dims_ok(0, K, N) && K >= 1 && (double)T * K < kMaxBytes && (double)T * N < kMaxBytes &&
+         K >= 1 && K <= kMaxWidth && N >= 0 && N <= kMaxWidth && (double)T * K < kMaxBytes && (double)T * N < kMaxBytes &&
          (double)L * r * K < kMaxBytes && (double)L * r * N < kMaxBytes;
 }
 struct Range {
@@ -637,9 +637,15 @@ bool overlaps_any(const Range& out, const Range* in, int n) {
 
 extern "C" {
 
+size_t lowrank_linear_workspace_bytes(int64_t T, int64_t L, int64_t r) {
+  if (T < 1 || T > kMaxRows || L < 1 || L > kMaxExperts || r < 1 || r > kMaxRank) return 0;
+  return adapters_bytes(T, L, r);
+}
+
 int lowrank_linear(const void* x, int dtype, int64_t row_stride, const void* a, const void* b,
                     const float* scale, const int32_t* layout, const void* base, void* out,
-                    int64_t T, int64_t L, int64_t r, int64_t K, int64_t N, void* stream) {
+                    int64_t T, int64_t L, int64_t r, int64_t K, int64_t N, void* workspace,
+                    size_t workspace_bytes, void* stream) {
   if (!float_type(dtype)) return IMC_ERR_ARG;
   if (!adapter_dims_ok(T, L, r, K, N) || row_stride < (T > 1 ? K : 0)) return IMC_ERR_SHAPE;
   if (T == 0 || N == 0) return finish_empty();
@@ -656,9 +662,20 @@ int lowrank_linear(const void* x, int dtype, int64_t row_stride, const void* a, 
                        {layout, (uint64_t)moe_layout_size(T, 1, L) * 4},
                        {base == out ? nullptr : base, out_bytes}};
   if (overlaps_any({out, out_bytes}, in, 6)) return IMC_ERR_ALIAS;
+  const size_t need = lowrank_linear_workspace_bytes(T, L, r);
+  if (need) {
+    const int ws = check_workspace(workspace, workspace_bytes, need);
+    if (ws != IMC_OK) return ws;
+    const Range room = {workspace, need}, res[2] = {{base, out_bytes}, {out, out_bytes}};
+    if (workspace && (overlaps_any(room, in, 5) || overlaps_any(room, res, 2))) return IMC_ERR_ALIAS;
+  }
   const int dev = require_device();
   if (dev != IMC_OK) return dev;
+  cudaStream_t s = (cudaStream_t)stream;
+  Scratch sc(s);
+  if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
   AdapterArgs p = {};
+  p.workspace = sc.p;
   p.x = x;
   p.ld = row_stride;
   p.a = a;
@@ -673,7 +690,7 @@ int lowrank_linear(const void* x, int dtype, int64_t row_stride, const void* a, 
   p.N = N;
   p.L = (int)L;
   p.r = (int)r;
-  return finish_call(launch_adapters(p, dtype, (cudaStream_t)stream), IMC_KERNEL_ADAPTERS);
+  return finish_call(sc.give(launch_adapters(p, dtype, s)), IMC_KERNEL_ADAPTERS);
 }
 
 size_t lowrank_linear_backward_workspace_bytes(int64_t T, int64_t r) {

@@ -182,6 +182,30 @@ __device__ __forceinline__ void ld_global_v8(uint32_t (&w)[8], const void* p) {
                : "l"(p));
 }
 
+// The same of memory that this kernel writes.
+__device__ __forceinline__ void ld_global_v8_rw(uint32_t (&w)[8], const void* p) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+                 "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
+// ----------------------------------------------------------- async copies
+// Sixteen bytes from global to shared memory, both 16-byte aligned; zeros where !in (from
+// is not read then).  Counted in the thread's groups.
+__device__ __forceinline__ void copy16(void* to, const void* from, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(to)), "l"(from),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's groups are under way.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
@@ -524,11 +548,11 @@ __host__ __device__ constexpr uint32_t idesc_tf32(uint32_t M, uint32_t N, bool a
          ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// Instruction descriptor for kind::f16 with bf16 operands and an fp32 accumulator:
-// the fields of kind::tf32, operand format 1 = bf16 (0 = fp16).
-__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, bool a_mn_major,
-                                                  bool b_mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+// Instruction descriptor for kind::f16 with an fp32 accumulator: the fields of
+// kind::tf32, the format of both operands 0 (fp16) or 1 (bf16).
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t format, uint32_t M, uint32_t N,
+                                                 bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | (format << 7) | (format << 10) | ((a_mn_major ? 1u : 0u) << 15) |
          ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 

@@ -563,13 +563,17 @@ int moe_balance_backward(const float* grad_loss, const void* logits, int dtype, 
  *         128.   scale [L] fp32 or NULL (ones).
  *   base  [T,N] or NULL (zeros); out [T,N].  out may be base itself: then the rows
  *         without an adapter are neither read nor written.  No other overlap.
- * x, a, b, base and out are of type dtype; K >= 1, T <= 2^27.  Sums are fp32, and
- * x a^T is kept to 16 bits of precision (fp32: 24) for the second product; an output
- * is rounded once.  Non-finite values reach their own row only.
+ * x, a, b, base and out are of type dtype; T <= 2^27, 1 <= K <= 2^20, N <= 2^20.
+ * Sums are fp32, and x a^T is kept to 16 bits of precision (fp32: 24) for the second
+ * product; an output is rounded once.  Non-finite values reach their own row only.
+ * workspace: lowrank_linear_workspace_bytes(T, L, r) bytes (0 for few rows), 16-byte
+ * aligned; NULL: from the library's pool.
  */
+size_t lowrank_linear_workspace_bytes(int64_t T, int64_t L, int64_t r);
 int lowrank_linear(const void* x, int dtype, int64_t row_stride, const void* a, const void* b,
-                    const float* scale, const int32_t* layout, const void* base, void* out,
-                    int64_t T, int64_t L, int64_t r, int64_t K, int64_t N, void* stream);
+                   const float* scale, const int32_t* layout, const void* base, void* out,
+                   int64_t T, int64_t L, int64_t r, int64_t K, int64_t N, void* workspace,
+                   size_t workspace_bytes, void* stream);
 
 /* Gradients for grad [T,N]; with g[t] = scale[l] * (grad[t] b[l]):
  *   grad_x[t] = base[t] + g[t] a[l]      (none: base[t]; base [T,K] or NULL: zeros)

@@ -18,9 +18,9 @@ def lib():
     return binding.load()
 
 
-def lowrank(x=P[0], dtype=0, ld=64, a=P[1], b=P[2], scale=P[3], layout=P[4], base=P[5], out=P[6], T=9, L=3, r=8,
-            K=64, N=32):
-    return binding.lowrank_linear(x, dtype, ld, a, b, scale, layout, base, out, T, L, r, K, N, None)
+def lowrank(x=P[0], dtype=0, ld=64, a=P[1], b=P[2], scale=P[3], layout=P[4], base=P[5], out=P[6], T=900, L=3, r=8,
+            K=64, N=32, ws=P[7], nbytes=1 << 20):
+    return binding.lowrank_linear(x, dtype, ld, a, b, scale, layout, base, out, T, L, r, K, N, ws, nbytes, None)
 
 
 def lowrank_back(grad=P[0], x=P[1], a=P[2], b=P[3], dtype=0, scale=P[4], layout=P[5], base=P[6], gx=P[7], ga=P[8],
@@ -51,6 +51,9 @@ BAD = [
     (lowrank, dict(out=P[6] + 2), ARG), (lowrank, dict(out=P[0] + 4), ALIAS), (lowrank, dict(out=P[1]), ALIAS),
     (lowrank, dict(out=P[2]), ALIAS), (lowrank, dict(out=P[3]), ALIAS), (lowrank, dict(out=P[4]), ALIAS),
     (lowrank, dict(out=P[5] + 4), ALIAS), (lowrank, dict(out=P[5] - 4), ALIAS),
+    (lowrank, dict(K=2 ** 20 + 1, ld=2 ** 20 + 1), SHAPE), (lowrank, dict(N=2 ** 20 + 1), SHAPE),
+    (lowrank, dict(nbytes=64), ARG), (lowrank, dict(ws=P[7] + 8), ARG), (lowrank, dict(ws=P[0]), ALIAS),
+    (lowrank, dict(ws=P[4]), ALIAS), (lowrank, dict(ws=P[5]), ALIAS), (lowrank, dict(ws=P[6]), ALIAS),
     (lowrank_back, dict(dtype=-1), ARG), (lowrank_back, dict(T=0), SHAPE), (lowrank_back, dict(N=0), SHAPE),
     (lowrank_back, dict(r=129), SHAPE), (lowrank_back, dict(L=0), SHAPE), (lowrank_back, dict(grad=None), NULL),
     (lowrank_back, dict(x=None), NULL), (lowrank_back, dict(a=None), NULL), (lowrank_back, dict(b=None), NULL),
@@ -96,8 +99,8 @@ def test_sizes():
 
 
 def test_without_a_gpu_calls_fail_loudly():
-    calls = [("lowrank_linear", [P[0], 0, 64, P[1], P[2], None, P[4], None, P[6], 9, 3, 8, 64, 32, None]),
-             ("lowrank_linear", [P[0], 0, 64, P[1], P[2], P[3], P[4], P[6], P[6], 9, 3, 8, 64, 32, None]),
+    calls = [("lowrank_linear", [P[0], 0, 64, P[1], P[2], None, P[4], None, P[6], 9, 3, 8, 64, 32, None, 0, None]),
+             ("lowrank_linear", [P[0], 0, 64, P[1], P[2], P[3], P[4], P[6], P[6], 900, 3, 8, 64, 32, P[7], 1 << 20, None]),
              ("lowrank_linear_backward", [P[0], P[1], P[2], P[3], 0, P[4], P[5], P[7], P[7], P[8], P[9], 9, 3, 8, 64, 32,
                                           P[10], 1 << 20, None]),
              ("moe_balance", [P[0], 0, 9, 16, 16, P[1], 2, 0, None, 1, P[3], P[4], None]),
@@ -129,5 +132,5 @@ def test_python_module_calls_the_same_entry_points():
             getattr(binding, name)(*zeros), name
         with pytest.raises(TypeError, match=name):
             getattr(binding._calls, name)(*zeros[1:])
-    assert binding._calls.lowrank_linear(P[0], 0, 64, P[1], P[2], P[3], P[4], P[5], P[1], 9, 3, 8, 64, 32, None) == ALIAS
+    assert binding._calls.lowrank_linear(P[0], 0, 64, P[1], P[2], P[3], P[4], P[5], P[1], 9, 3, 8, 64, 32, None, 0, None) == ALIAS
     assert binding._calls.moe_balance(P[0], 0, 9, 16, 16, P[1], 2, 0, None, 1, P[0], P[4], None) == ALIAS
