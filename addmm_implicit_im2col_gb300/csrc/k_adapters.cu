@@ -3,6 +3,8 @@
 //   out[t] = base[t] + scale[l] * (x[t] a[l]^T) b[l]^T,   l the adapter of row t,
 //
 // and their gradients.  The rows come in adapter order (moe_layout).
+#include <mutex>
+
 #include "adapters.cuh"
 #include "ptx.cuh"
 #include "scores.cuh"
@@ -21,11 +23,12 @@ struct RowTile {
   int l, p0, rows;
 };
 // All threads of the block.  Every thread counts the tiles of a run of buckets.
+template <int THREADS = kThreads>
 __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int L, bool none, int height,
                                              int t) {
-  __shared__ int sums[kWarps];
+  __shared__ int sums[THREADS / 32];
   __shared__ RowTile found;
-  const int B = L + (none ? 1 : 0), per = (B + kThreads - 1) / kThreads;
+  const int B = L + (none ? 1 : 0), per = (B + THREADS - 1) / THREADS;
   const int e0 = threadIdx.x * per, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int tiles = 0;
   for (int e = e0; e < e0 + per && e < B; ++e)
@@ -40,7 +43,7 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int L, bool
   if (lane == 31) sums[warp] = upto;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w)
+  for (int w = 0; w < THREADS / 32; ++w)
     if (w < warp) upto += sums[w];
   int at = upto - tiles;
   if (t >= at && t < upto) {
@@ -315,7 +318,7 @@ struct DownProblem {
   const void* x;   // [T, K], rows ld elements apart
   int64_t ld, K;
   const void* w;   // of an adapter [r, K]; turned: [K, r]
-  uint16_t* h;     // planes [PH][T][R], in adapter order
+  uint16_t* h;     // [T][PH][R], its planes, in adapter order
   int turned, vec; // vec: 1 x, 2 w
 };
 struct DownArgs {
@@ -323,13 +326,67 @@ struct DownArgs {
   const float* scale;
   const int32_t *offsets, *order;
   int64_t T;
-  int L, r, R, log_ctas, cols;  // R: r rounded up to 16
+  int L, r, R, log_ctas, cols, stages;  // R: r rounded up to 16
 };
 struct RingCtl {
   uint64_t empty[4], drain;
   uint32_t tmem_base;
   int abort;
 };
+
+// This CTA's sums of h, from tensor memory to its shared memory; the P planes' sums are
+// added.  Warps in groups of four: group `part` of `parts` takes every parts-th 16 columns.
+template <int P>
+__device__ __forceinline__ void own_sums(uint8_t* sm, uint32_t tmem, int R, bool any, int part, int parts) {
+  const int row = (threadIdx.x >> 5 & 3) * 32 + (threadIdx.x & 31), pitch = R * 4 + 16;
+  for (int j = part * 16; j < R; j += parts * 16) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    if (any) {
+#pragma unroll
+      for (int c = 0; c < P; ++c) {
+        uint32_t s[16];
+        ptx::tmem_ld16(tmem + ((uint32_t)(row & ~31) << 16) + c * R + j, s);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(s[i]);
+      }
+    }
+    float4* to = reinterpret_cast<float4*>(sm + row * pitch + j * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+}
+// h of this CTA's 128 / C rows of the tile: the sums of all CTAs in their order, scaled,
+// in planes.
+template <int PH, int THREADS>
+__device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, uint16_t* h, const RowTile& t,
+                                         int rank) {
+  const int R = g.R, C = 1 << g.log_ctas, pitch = R * 4 + 16;
+  const int mine = TILE >> g.log_ctas, units = mine * (R >> 3);
+  const float scale = g.scale ? g.scale[t.l] : 1.0f;
+  for (int i = threadIdx.x; i < units; i += THREADS) {
+    const int row = rank * mine + i / (R >> 3), ju = i % (R >> 3);
+    if (row >= t.rows) break;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    for (int c = 0; c < C; ++c) {
+      const uint32_t at = ptx::cluster_addr(sm + row * pitch + ju * 32, c);
+      const float4 a = ptx::ld_cluster4(at), b = ptx::ld_cluster4(at + 16);
+      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+      v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= scale;
+    uint4 w[PH];
+    split8<PH>(v, w);
+#pragma unroll
+    for (int c = 0; c < PH; ++c)
+      *reinterpret_cast<uint4*>(h + ((int64_t)(t.p0 + row) * PH + c) * R + ju * 8) = w[c];
+  }
+}
 
 // Barriers and tensor memory of a block.  The memory is taken before the stream's next
 // kernel may start: a block of that one that had it would wait for this kernel's end.
@@ -379,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
   uint8_t* sm = tc::smem_align1024(sm_raw);
   const DownProblem& p = g.prob[blockIdx.y];
   const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R, r = g.r;
+  const int tid = threadIdx.x, warp = tid >> 5, R = g.R, r = g.r;
   int* wd = &g_watchdog_adapters;
   const uint32_t tmem = set_up(ctl, 5, ctl.empty, g.cols);
   ptx::griddep_wait();
@@ -525,77 +582,140 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       }
     }
     ptx::copy_wait<0>();
-    // ---- this CTA's sums to its shared memory
-    const int q4 = warp & 3, pitch = R * 4 + 16;
-    if (b1 > b0) {
+    const bool any = b1 > b0;
+    if (any) {
       const int done = (b1 - b0 - 1) % S, uses = (b1 - b0 - 1) / S;
       tc::warp_wait_bar(&ctl.empty[done], uses & 1, &ctl.abort, 2, wd);
       ptx::tc_fence_after();
     }
     __syncthreads();
-    for (int j = (warp >> 2) * 16; j < R; j += 32) {
-      float v[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-      if (b1 > b0) {
-#pragma unroll
-        for (int c = 0; c < P; ++c) {
-          uint32_t s[16];
-          ptx::tmem_ld16(tmem + ((uint32_t)(q4 * 32) << 16) + c * R + j, s);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(s[i]);
-        }
-      }
-      float4* to = reinterpret_cast<float4*>(sm + (q4 * 32 + lane) * pitch + j * 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    }
-    const float scale = g.scale ? g.scale[t.l] : 1.0f;
+    own_sums<P>(sm, tmem, R, any, warp >> 2, kWarps / 4);
     ptx::cluster_sync();
-    // ---- h of 128 / C rows: the sums of all CTAs
-    const int mine = TILE >> g.log_ctas, units = mine * (R >> 3);
-    for (int i = tid; i < units; i += kThreads) {
-      const int row = rank * mine + i / (R >> 3), ju = i % (R >> 3);
-      if (row >= t.rows) break;
-      float v[8];
+    all_sums<PH, kThreads>(sm, g, p.h, t, rank);
+    ptx::cluster_sync();  // no CTA ends while another reads its sums
+  }
+  tear_down(ctl, tmem, g.cols);
+}
+
+// The same for 16-bit rows that TMA can load: one warp issues the loads (a box where the
+// tile's rows lie one after the other, four rows at a time where they do not), one the
+// MMAs, and nothing passes through registers.  8192 rows, 8 adapters, r 32, K 4096: us
+// with / without.
+constexpr int DOWN_THREADS = 192, DOWN_STAGES = 8;
+struct DownMaps {
+  CUtensorMap x[2], rows[2], w[2];  // of each problem: x by tiles, by rows; w
+};
+struct DownCtl {
+  uint64_t full[DOWN_STAGES], empty[DOWN_STAGES], accf, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(DOWN_THREADS)
+    k_adapters_down_tma(const __grid_constant__ DownMaps maps, const __grid_constant__ DownArgs g) {
+  using PL = Planes<T>;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ DownCtl ctl;
+  __shared__ __align__(16) int rows[TILE];
+  uint8_t* sm = tc::smem_align1024(sm_raw);
+  const DownProblem& p = g.prob[blockIdx.y];
+  const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank(), S = g.stages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R;
+  int* wd = &g_watchdog_adapters;
+  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 2, ctl.full, g.cols);
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const RowTile t = find_tile<DOWN_THREADS>(g.offsets, g.L, false, TILE, blockIdx.x >> g.log_ctas);
+  if (t.rows > 0) {  // else the whole cluster has no tile
+    // rows of the tile; past its end the last one again (their sums are not used)
+    if (tid < TILE) rows[tid] = g.order[t.p0 + min(tid, t.rows - 1)];
+    __syncthreads();
+    const int wb = p.turned ? down_w_bytes(R) : R * 128, stage_bytes = XP + down_w_bytes(R);
+    const int blocks = (int)ceil_div(p.K, KB), per = (blocks + C - 1) >> g.log_ctas;
+    const int b0 = min(rank * per, blocks), b1 = min(b0 + per, blocks);
+    if (warp == 0) {
+      const void *mx = &maps.x[blockIdx.y], *mr = &maps.rows[blockIdx.y], *mw = &maps.w[blockIdx.y];
+      int4 four = *reinterpret_cast<const int4*>(rows + lane * 4);
+      bool run = true;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-      for (int c = 0; c < C; ++c) {
-        const uint32_t at = ptx::cluster_addr(sm + row * pitch + ju * 32, c);
-        const float4 a = ptx::ld_cluster4(at), b = ptx::ld_cluster4(at + 16);
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      for (int i = 0; i < 4; ++i) {
+        const int at = lane * 4 + i;
+        if (at < t.rows) run = run && rows[at] == rows[0] + at;
       }
+      run = __all_sync(kAll, run);
+      int b = b0;
+      for (; b < b1; ++b) {
+        const int i = b - b0, slot = i % S, use = i / S;
+        if (use > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (use - 1) & 1, &ctl.abort, 1, wd)) break;
+        uint8_t* to = sm + slot * stage_bytes;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(&ctl.full[slot], XP + wb);
+          if (p.turned) {
+            for (int j = 0; j < R; j += 64) ptx::tma_load_3d(to + XP + j * 128, mw, &ctl.full[slot], j, b * KB, t.l);
+          } else {
+            ptx::tma_load_3d(to + XP, mw, &ctl.full[slot], b * KB, 0, t.l);
+          }
+          if (run) ptx::tma_load_2d(to, mx, &ctl.full[slot], b * KB, rows[0]);
+        }
+        __syncwarp();
+        if (!run)
+          ptx::tma_gather4(to + lane * 512, mr, &ctl.full[slot], b * KB, four.x, four.y, four.z, four.w);
+      }
+      if (ctl.abort)  // the copies under way land before the block ends
+        for (int i = b - b0 > S ? b - b0 - S : 0; i < b - b0; ++i)
+          tc::drain_wait(&ctl.full[i % S], (i / S) & 1);
+    } else if (warp == 1) {
+      for (int b = b0; b < b1; ++b) {
+        const int i = b - b0, slot = i % S;
+        if (!tc::warp_wait_bar(&ctl.full[slot], (i / S) & 1, &ctl.abort, 12, wd)) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t xa = ptx::smem_addr(sm + slot * stage_bytes), wa = xa + XP;
+          const uint32_t id = ptx::idesc_f16(PL::FD, TILE, R, false, p.turned);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= scale;
-      uint4 w8[PH];
-      split8<PH>(v, w8);
-#pragma unroll
-      for (int c = 0; c < PH; ++c)
-        *reinterpret_cast<uint4*>(p.h + ((int64_t)c * g.T + t.p0 + row) * R + ju * 8) = w8[c];
+          for (int ks = 0; ks < KB / 16; ++ks)
+            ptx::mma_f16(tmem, ptx::smem_desc(xa + ks * 32, 16, 1024, ptx::kSwizzle128B),
+                         ptx::smem_desc(wa + ks * (p.turned ? 2048 : 32), KB * 128, 1024, ptx::kSwizzle128B),
+                         id, b > b0 || ks > 0);
+          ptx::mma_commit(&ctl.empty[slot]);
+          if (b + 1 == b1) ptx::mma_commit(&ctl.accf);
+        }
+        __syncwarp();
+      }
+    } else {
+      if (b1 > b0) tc::warp_wait_bar(&ctl.accf, 0, &ctl.abort, 2, wd);
+      ptx::tc_fence_after();
+      own_sums<1>(sm, tmem, R, b1 > b0, 0, 1);
     }
+    __syncwarp();
+    ptx::cluster_sync();
+    all_sums<PL::PH, DOWN_THREADS>(sm, g, p.h, t, rank);
     ptx::cluster_sync();  // no CTA ends while another reads its sums
   }
   tear_down(ctl, tmem, g.cols);
 }
 
 struct UpArgs {
-  const uint16_t* h;  // planes [PH][T][R]
+  const uint16_t* h;  // [T][PH][R]
   const void* w;      // of an adapter [N, r]; turned: [r, N]
   const void* base;
   void* out;
   const int32_t *offsets, *order;
   int64_t T, N;
-  int L, r, R, steps, turned, vec;  // vec: 1 w, 2 base and out (32 bytes)
-  int slots, h_slots, w_bytes, h_bytes;  // of the rings of w and h; bytes of one
+  int L, r, R, steps, turned, vec;  // vec: 1 w, 2 base and out (by TMA)
+  int slots, h_slots, b_slots, w_bytes, h_bytes;  // of the rings of w, h and base; bytes of one
+};
+struct UpMaps {
+  CUtensorMap base, rows, out;  // base by 32 rows, by rows; out by 32 rows; 128 bytes of columns
 };
 constexpr int UP_EPI = 8, UP_LOAD = 4;  // warps
 constexpr int UP_THREADS = (UP_EPI + UP_LOAD + 1) * 32;
-constexpr int UP_SLOTS = 4;
+constexpr int UP_SLOTS = 4, BASE_SLOTS = 4;
 constexpr int kAdapters = 1024;  // the most that a layout has
 struct UpCtl {
   uint64_t wfull[UP_SLOTS], wempty[UP_SLOTS], hfull[2], hempty[2], accf[2], acce[2], drain;
+  uint64_t bfull[UP_EPI][BASE_SLOTS];
   uint32_t tmem_base;
   int abort;
   int sums[UP_THREADS / 32];
@@ -630,13 +750,17 @@ template <typename T>
 constexpr int STAGED_COLS = sizeof(T) == 2 ? 32 : 16;
 
 // Persistent blocks, each with an equal run of the (tile, 128 outputs) items:
-//   warps 0-7   epilogue: a thread has a row and half of an item's columns: base (read an
-//               item ahead), the product from tensor memory, one rounding, 32-byte stores;
-//               rows that those cannot reach go through the warp's shared memory
+//   warps 0-7   epilogue: a warp has 32 rows and half of an item's columns: it asks TMA
+//               for its part of base some items ahead (a box, or four rows at a time where
+//               they do not lie one after the other), adds the product from tensor memory in
+//               place, rounds once, and has TMA store it (row by row itself where the box
+//               would reach other rows); without TMA (unaligned rows, no room) it adds
+//               column by column through shared memory
 //   warps 8-11  h of a tile and w of an item to shared memory
 //   warp 12     tensor memory, MMAs (two accumulators of 128 columns)
 template <typename T>
-__global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_constant__ UpArgs g) {
+__global__ void __launch_bounds__(UP_THREADS, 1)
+    k_adapters_up(const __grid_constant__ UpMaps maps, const __grid_constant__ UpArgs g) {
   using PL = Planes<T>;
   constexpr int P = PL::P, PH = PL::PH;
   extern __shared__ uint8_t sm_raw[];
@@ -656,6 +780,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_cons
       ptx::mbar_init(&ctl.acce[i], UP_EPI * 32);
     }
     ptx::mbar_init(&ctl.drain, 1);
+    for (int i = 0; i < UP_EPI * BASE_SLOTS; ++i) ptx::mbar_init(&ctl.bfull[0][0] + i, 1);
     ctl.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -699,7 +824,9 @@ __global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_cons
   ptx::griddep_launch();
   const int64_t items = (int64_t)ctl.before[B] * g.steps;
   const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
-  uint8_t* hs = sm + g.slots * g.w_bytes;
+  constexpr int SB = 32 * 64 * (int)sizeof(T);  // bytes of a warp's part of an item
+  uint8_t* ws = sm + UP_EPI * g.b_slots * SB;
+  uint8_t* hs = ws + g.slots * g.w_bytes;
   const int plane = (R >> 3) * CORE_K<T>;
 
   if (warp >= UP_EPI && warp < UP_EPI + UP_LOAD) {
@@ -739,7 +866,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_cons
 #pragma unroll
           for (int c = 0; c < PH; ++c)
             ptx::copy16(ht + c * plane + ju * CORE_K<T> + (row >> 3) * CORE<T> + (row & 7) * 16,
-                        in ? g.h + ((int64_t)c * g.T + t.p0 + row) * R + ju * 8 : g.h, in);
+                        in ? g.h + ((int64_t)(t.p0 + row) * PH + c) * R + ju * 8 : g.h, in);
         }
         ++seg;
         now_h = &ctl.hfull[hb];
@@ -752,7 +879,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_cons
         }
         tc::warp_wait_bar(&ctl.wempty[slot], (use - 1) & 1, &ctl.abort, 7, wd);
       }
-      uint8_t* to = sm + slot * g.w_bytes;
+      uint8_t* to = ws + slot * g.w_bytes;
       const T* w = static_cast<const T*>(g.w) + (int64_t)t.l * r * g.N;
       const int left = (int)(g.N - n0 < UP_N ? g.N - n0 : UP_N);
 #pragma unroll 4
@@ -814,7 +941,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_cons
       if (n > 1 && !tc::warp_wait_bar(&ctl.acce[buf], (n / 2 - 1) & 1, &ctl.abort, 10, wd)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
-        const uint32_t ha = ptx::smem_addr(hs + hb * g.h_bytes), wa = ptx::smem_addr(sm + slot * g.w_bytes);
+        const uint32_t ha = ptx::smem_addr(hs + hb * g.h_bytes), wa = ptx::smem_addr(ws + slot * g.w_bytes);
         uint32_t more = 0;
         for (int ks = 0; ks < R / 16; ++ks)
 #pragma unroll
@@ -839,78 +966,135 @@ __global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_cons
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const int q4 = warp & 3, half = warp >> 2;
-    constexpr int W = UP_N / 2 * (int)sizeof(T) / 32;  // 32-byte words of a thread's columns
-    constexpr bool AHEAD = sizeof(T) == 2;
-    const bool wide = g.vec & 2;
-    uint32_t held[W][8];
-    int row = -1, at_tile = -1;
-    RowTile t = {0, 0, 0};
-    // An item's row of this thread and its part of base.
-    auto fetch = [&](int64_t it) {
+    const int q4 = warp & 3, half = warp >> 2, NS = g.b_slots;
+    uint8_t* ring = sm + warp * NS * SB;
+    constexpr int BOX = 128 / (int)sizeof(T);  // columns of a box
+    // An item's tile, the row of this lane in it, its columns.  For loads and for stores:
+    // the first run ahead.
+    struct Place {
+      int tile = -1, row = 0, rows = 0, l = 0;
+      bool run = false;  // the warp's rows lie one after the other
+      int64_t col = 0;
+    };
+    auto place = [&](Place& q, int64_t it) {
       const int tile = (int)(it / g.steps);
-      const int64_t col = (it - (int64_t)tile * g.steps) * UP_N + half * 64;
-      if (tile != at_tile) {
-        at_tile = tile;
-        t = tile_of(ctl, B, tile);
-        const int in = q4 * 32 + lane;
-        row = in < t.rows ? __ldg(g.order + t.p0 + in) : -1;
-      }
-      if (wide) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          if (base && row >= 0 && col + i * (32 / (int)sizeof(T)) < g.N) {
-            ptx::ld_global_v8_rw(held[i], base + row * g.N + col + i * (32 / (int)sizeof(T)));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) held[i][e] = 0;
-          }
+      q.col = (it - (int64_t)tile * g.steps) * UP_N + half * 64;
+      if (tile == q.tile) return;
+      q.tile = tile;
+      const RowTile t = tile_of(ctl, B, tile);
+      q.l = t.l;
+      q.rows = t.rows - q4 * 32 < 0 ? 0 : min(32, t.rows - q4 * 32);  // of this warp
+      if (q.rows == 0) return;
+      q.row = __ldg(g.order + t.p0 + q4 * 32 + min(lane, q.rows - 1));
+      const int first = __shfl_sync(kAll, q.row, 0);
+      q.run = __all_sync(kAll, lane >= q.rows || q.row == first + lane);
+    };
+    Place ahead, now;
+    auto load = [&](int64_t it) {  // base of an item to its place in the ring
+      place(ahead, it);
+      if (!base || ahead.rows == 0 || ahead.col >= g.N) return;
+      const int slot = (int)((it - i0) % NS);
+      uint64_t* bar = &ctl.bfull[warp][slot];
+      uint8_t* to = ring + slot * SB;
+      const int boxes = ahead.col + BOX < g.N ? 64 / BOX : 1;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, boxes * 4096);
+      __syncwarp();
+      for (int b = 0; b < boxes; ++b) {
+        const int x = (int)ahead.col + b * BOX;
+        if (ahead.run) {
+          if (lane == 0) ptx::tma_load_2d(to + b * 4096, &maps.base, bar, x, ahead.row);
+        } else {
+          const int r0 = __shfl_sync(kAll, ahead.row, (lane * 4) & 31), r1 = __shfl_sync(kAll, ahead.row, (lane * 4 + 1) & 31),
+                    r2 = __shfl_sync(kAll, ahead.row, (lane * 4 + 2) & 31), r3 = __shfl_sync(kAll, ahead.row, (lane * 4 + 3) & 31);
+          if (lane < 8) ptx::tma_gather4(to + b * 4096 + lane * 512, &maps.rows, bar, x, r0, r1, r2, r3);
         }
       }
     };
-    if (AHEAD && i0 < i1) fetch(i0);
+    const bool wide = g.vec & 2;
     int n = 0;
-    for (int64_t it = i0; it < i1; ++it) {
-      if (!AHEAD) fetch(it);
-      const int64_t col = (it - it / g.steps * g.steps) * UP_N + half * 64;
-      const int to_row = row;
-      const bool product = t.l < g.L;
+    uint32_t phases = 0;  // of the ring's barriers
+    if (wide)
+      for (int64_t it = i0; it < i1 && it < i0 + NS - 1; ++it) load(it);
+    int64_t it = i0;
+    for (; it < i1; ++it) {
+      place(now, it);
+      const bool product = now.l < g.L, live = now.rows > 0 && now.col < g.N;
       const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + (n & 1) * UP_N + half * 64;
-      if (product && !tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
-      ptx::tc_fence_after();
-      T* to = out + to_row * g.N + col;
       if (wide) {
+        const int slot = (int)((it - i0) % NS);
+        uint8_t* mine = ring + slot * SB;
+        if (base && live) {
+          if (!tc::warp_wait_bar(&ctl.bfull[warp][slot], phases >> slot & 1, &ctl.abort, 13, wd)) break;
+          phases ^= 1u << slot;
+          __syncwarp();
+        }
+        if (product) {
+          if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
+          ptx::tc_fence_after();
+        }
+        if (live && (product || !base)) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint32_t s[32];
-          if (product) {
-            ptx::tmem_ld32(acc + b * 32, s);
-            ptx::tmem_ld_wait();
-          }
-          if (product && b) {
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(&ctl.acce[n & 1]);
-          }
-#pragma unroll
-          for (int i = 0; i < W / 2; ++i) {
-            uint32_t(&h)[8] = held[b * (W / 2) + i];
+          for (int b = 0; b < 2; ++b) {
+            uint32_t s[32];
             if (product) {
+              ptx::tmem_ld32(acc + b * 32, s);
+              ptx::tmem_ld_wait();
+            } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if constexpr (sizeof(T) == 2)
-                  h[e] = add_pair(T(), h[e], __uint_as_float(s[i * 16 + 2 * e]), __uint_as_float(s[i * 16 + 2 * e + 1]));
-                else
-                  h[e] = __float_as_uint(__uint_as_float(h[e]) + __uint_as_float(s[i * 8 + e]));
-              }
+              for (int e = 0; e < 32; ++e) s[e] = 0;
             }
-            const int c = b * 32 + i * (32 / (int)sizeof(T));
-            if (to_row >= 0 && col + c < g.N) ptx::st_global_v8(to + c, h);
+            constexpr int V = 16 / (int)sizeof(T);  // values of 16 bytes
+#pragma unroll
+            for (int i = 0; i < 32 / V; ++i) {
+              const int unit = (b * 32 / V + i) & 7, box = (b * 32 / V + i) >> 3;
+              uint4* at = reinterpret_cast<uint4*>(mine + box * 4096 + lane * 128 + ((unit ^ (lane & 7)) << 4));
+              uint4 h = base ? *at : make_uint4(0, 0, 0, 0);
+              uint32_t* hw = reinterpret_cast<uint32_t*>(&h);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(T) == 2)
+                  hw[e] = add_pair(T(), hw[e], __uint_as_float(s[i * 8 + 2 * e]), __uint_as_float(s[i * 8 + 2 * e + 1]));
+                else
+                  hw[e] = __float_as_uint(__uint_as_float(hw[e]) + __uint_as_float(s[i * 4 + e]));
+              }
+              *at = h;
+            }
           }
         }
-        if (AHEAD && it + 1 < i1) fetch(it + 1);
+        if (product) {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&ctl.acce[n & 1]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (live) {
+          if (now.run && now.rows == 32) {
+            if (lane == 0)
+              for (int b = 0; b < 64 / BOX && now.col + b * BOX < g.N; ++b)
+                ptx::tma_store_2d(&maps.out, mine + b * 4096, (int)now.col + b * BOX, now.row);
+          } else if (lane < now.rows) {
+            T* to = out + now.row * g.N + now.col;
+            const int units = (int)(g.N - now.col < 64 ? g.N - now.col : 64) * (int)sizeof(T) / 16;
+            for (int i = 0; i < units; ++i)
+              reinterpret_cast<uint4*>(to)[i] = *reinterpret_cast<const uint4*>(
+                  mine + (i >> 3) * 4096 + lane * 128 + (((i & 7) ^ (lane & 7)) << 4));
+          }
+        }
+        if (lane == 0) {
+          ptx::bulk_commit();
+          ptx::bulk_wait_read1();  // the item before this one has been stored
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (it + NS - 1 < i1) load(it + NS - 1);
       } else {
+        if (product) {
+          if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
+          ptx::tc_fence_after();
+        }
         constexpr int SC = STAGED_COLS<T>, ROWS = 32 / SC;  // columns, and rows at once
         float* mine = reinterpret_cast<float*>(hs + g.h_slots * g.h_bytes) + warp * 32 * (SC + 1);
+        const int to_row = lane < now.rows ? now.row : -1;
 #pragma unroll 1
         for (int b = 0; b < 64 / SC; ++b) {
           if (product) {
@@ -926,7 +1110,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_cons
             for (int e = 0; e < SC; ++e) mine[lane * (SC + 1) + e] = __uint_as_float(s[e]);
             __syncwarp();
           }
-          const int64_t c = col + b * SC + lane % SC;  // a lane has a column of its rows
+          const int64_t c = now.col + b * SC + lane % SC;  // a lane has a column of its rows
 #pragma unroll 8
           for (int i = lane / SC; i < 32; i += ROWS) {
             const int64_t at = (int64_t)__shfl_sync(kAll, to_row, i) * g.N + c;
@@ -936,9 +1120,21 @@ __global__ void __launch_bounds__(UP_THREADS, 1) k_adapters_up(const __grid_cons
           }
           __syncwarp();
         }
-        if (AHEAD && it + 1 < i1) fetch(it + 1);
       }
       if (product) ++n;
+    }
+    if (wide) {
+      if (ctl.abort) {  // the copies under way land before the block ends
+        Place q;
+        for (int64_t i = it; i < i1 && i < it + NS - 1 && base; ++i) {
+          place(q, i);
+          if (q.rows == 0 || q.col >= g.N) continue;
+          const int slot = (int)((i - i0) % NS);
+          tc::drain_wait(&ctl.bfull[warp][slot], phases >> slot & 1);
+        }
+      }
+      if (lane == 0) ptx::bulk_wait_all();
+      __syncwarp();
     }
   }
   ptx::tc_fence_before();
@@ -965,7 +1161,7 @@ constexpr int GRAD_COLS = 128;
 struct GradProblem {
   const void* x;      // [T, cols]
   int64_t cols;
-  const uint16_t* h;  // planes [PH][T][R]
+  const uint16_t* h;  // [T][PH][R]
   void* out;          // of an adapter [r, cols]; turned: [cols, r]
   int turned, vec;
 };
@@ -973,8 +1169,51 @@ struct GradArgs {
   GradProblem prob[2];
   const int32_t *offsets, *order;
   int64_t T;
-  int L, r, R, log_ctas, cols;
+  int L, r, R, log_ctas, cols, stages;
 };
+// A CTA's sums, from tensor memory to its shared memory: a column's r sums after another's,
+// one word apart.
+template <int PH>
+__device__ __forceinline__ void grad_sums(uint8_t* sm, uint32_t tmem, int R, bool any, int part, int parts) {
+  float* to = reinterpret_cast<float*>(sm);
+  const int col = (threadIdx.x >> 5 & 3) * 32 + (threadIdx.x & 31);
+  for (int j = part * 16; j < R; j += parts * 16) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+    if (any) {
+#pragma unroll
+      for (int c = 0; c < PH; ++c) {
+        uint32_t w[16];
+        ptx::tmem_ld16(tmem + ((uint32_t)(col & ~31) << 16) + c * R + j, w);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(w[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) to[col * (R + 1) + j + i] = v[i];
+  }
+}
+// This CTA's share of the gradient: the sums of all CTAs in their order.
+template <typename T, int THREADS>
+__device__ __forceinline__ void grad_out(uint8_t* sm, const GradArgs& g, const GradProblem& p, int l,
+                                         int rank, int64_t col0) {
+  const int C = 1 << g.log_ctas, r = g.r, pitch = g.R + 1;
+  const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
+  const int n = left * r, share = (n + C - 1) >> g.log_ctas;
+  const int e0 = rank * share, e1 = min(e0 + share, n);
+  const float* part = reinterpret_cast<const float*>(sm);
+  T* out = static_cast<T*>(p.out) + (int64_t)l * r * p.cols;
+  for (int e = e0 + threadIdx.x; e < e1; e += THREADS) {
+    const int col = p.turned ? e / r : e % left, j = p.turned ? e - col * r : e / left;
+    float sum = 0.0f;
+    for (int c = 0; c < C; ++c)
+      sum += __uint_as_float(ptx::ld_cluster(ptx::cluster_addr(part + col * pitch + j, c)));
+    out[p.turned ? (col0 + col) * r + j : (int64_t)j * p.cols + col0 + col] = from_f32<T>(sum);
+  }
+}
+
 // Bytes of h's n columns in a stage: GRAD_ROWS rows in units of 64 columns.
 __host__ __device__ constexpr int grad_h_bytes(int n) { return (n + 63) / 64 * (GRAD_ROWS * 128); }
 
@@ -989,7 +1228,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   uint8_t* sm = tc::smem_align1024(sm_raw);
   const GradProblem& p = g.prob[blockIdx.z];
   const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R, r = g.r;
+  const int tid = threadIdx.x, warp = tid >> 5, R = g.R;
   const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * GRAD_COLS;
   const int l = blockIdx.y;
   int* wd = &g_watchdog_adapters;
@@ -1049,7 +1288,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
       for (int c = 0; c < PH; ++c) {
         const int j = c * ru + ju;  // unit of the planes one after the other
         ptx::copy16(ht + (j >> 3) * (GRAD_ROWS * 128) + t * 128 + (((j ^ t) & 7) << 4),
-                    in < rows ? p.h + ((int64_t)c * g.T + first + in) * R + ju * 8 : p.h, in < rows);
+                    in < rows ? p.h + ((int64_t)(first + in) * PH + c) * R + ju * 8 : p.h, in < rows);
       }
     }
     if (!HELD) rows_of(b + 1);
@@ -1105,48 +1344,130 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     }
   }
   ptx::copy_wait<0>();
-  const int pitch = R + 1;  // words of a column's sums
-  float* part = reinterpret_cast<float*>(sm);
   if (b1 > b0) {
     const int done = (b1 - b0 - 1) % S, uses = (b1 - b0 - 1) / S;
     tc::warp_wait_bar(&ctl.empty[done], uses & 1, &ctl.abort, 5, wd);
     ptx::tc_fence_after();
   }
   __syncthreads();
-  if (work) {
-    const int q4 = warp & 3;
-    for (int j = (warp >> 2) * 16; j < R; j += 32) {
-      float v[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-      if (b1 > b0) {
-#pragma unroll
-        for (int c = 0; c < PH; ++c) {
-          uint32_t w[16];
-          ptx::tmem_ld16(tmem + ((uint32_t)(q4 * 32) << 16) + c * R + j, w);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(w[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) part[(q4 * 32 + lane) * pitch + j + i] = v[i];
-    }
-  }
-  ptx::tc_fence_before();
+  if (work) grad_sums<PH>(sm, tmem, R, b1 > b0, warp >> 2, kWarps / 4);
   ptx::cluster_sync();
-  if (work) {
-    const int n = left * r, share = (n + C - 1) >> g.log_ctas;
-    const int e0 = rank * share, e1 = min(e0 + share, n);
-    T* out = static_cast<T*>(p.out) + (int64_t)l * r * p.cols;
-    for (int e = e0 + tid; e < e1; e += kThreads) {
-      const int col = p.turned ? e / r : e % left, j = p.turned ? e - col * r : e / left;
-      float sum = 0.0f;
-      for (int c = 0; c < C; ++c)
-        sum += __uint_as_float(ptx::ld_cluster(ptx::cluster_addr(part + col * pitch + j, c)));
-      out[p.turned ? (col0 + col) * r + j : (int64_t)j * p.cols + col0 + col] = from_f32<T>(sum);
+  if (work) grad_out<T, kThreads>(sm, g, p, l, rank, col0);
+  ptx::cluster_sync();  // no CTA ends while another reads its sums
+  tear_down(ctl, tmem, g.cols);
+}
+
+// The same for bf16 rows that TMA can load.
+struct GradMaps {
+  CUtensorMap x[2], rows[2], h[2], h_rows[2];  // of each problem, by 64 rows and by rows
+};
+struct GradCtl {
+  uint64_t full[DOWN_STAGES], empty[DOWN_STAGES], accf, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__global__ void __launch_bounds__(DOWN_THREADS)
+    k_adapters_grad_tma(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs g) {
+  using T = __nv_bfloat16;
+  constexpr int PH = Planes<T>::PH, XG = GRAD_ROWS * GRAD_COLS * 2;
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ GradCtl ctl;
+  uint8_t* sm = tc::smem_align1024(sm_raw);
+  const GradProblem& p = g.prob[blockIdx.z];
+  const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank(), S = g.stages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R;
+  const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * GRAD_COLS;
+  const int l = blockIdx.y;
+  int* wd = &g_watchdog_adapters;
+  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 2, ctl.full, g.cols);
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const bool work = col0 < p.cols;
+  const int first = __ldg(g.offsets + l), rows = __ldg(g.offsets + l + 1) - first;
+  const int blocks = (rows + GRAD_ROWS - 1) / GRAD_ROWS, per = (blocks + C - 1) >> g.log_ctas;
+  const int b0 = min(rank * per, blocks), b1 = work ? min(b0 + per, blocks) : b0;
+  const int hb = grad_h_bytes(PH * R), stage_bytes = XG + hb;
+  const int boxes = col0 + 64 < p.cols ? 2 : 1;  // of 64 columns
+  if (warp == 0) {
+    const void *mx = &maps.x[blockIdx.z], *mr = &maps.rows[blockIdx.z], *mh = &maps.h[blockIdx.z],
+               *mhr = &maps.h_rows[blockIdx.z];
+    // this lane's two rows of a block, the next block's asked for early; past the end: a
+    // row that the tensors do not have, which reads zeros
+    auto row_of = [&](int b, int i) {
+      const int in = b * GRAD_ROWS + i;
+      return b < b1 && in < rows ? __ldg(g.order + first + in) : (int)g.T;
+    };
+    int r0 = row_of(b0, lane), r1 = row_of(b0, lane + 32);
+    int b = b0;
+    for (; b < b1; ++b) {
+      const int i = b - b0, slot = i % S, use = i / S;
+      const int n0 = row_of(b + 1, lane), n1 = row_of(b + 1, lane + 32);
+      const int at = __shfl_sync(kAll, r0, 0), have = min(GRAD_ROWS, rows - b * GRAD_ROWS);
+      const bool run = have == GRAD_ROWS && __all_sync(kAll, r0 == at + lane && r1 == at + 32 + lane);
+      if (use > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (use - 1) & 1, &ctl.abort, 4, wd)) break;
+      uint8_t* to = sm + slot * stage_bytes;
+      uint64_t* bar = &ctl.full[slot];
+      const int place = first + b * GRAD_ROWS;
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(bar, boxes * (XG / 2) + hb);
+        if (run)
+          for (int c = 0; c < boxes; ++c) ptx::tma_load_2d(to + c * (XG / 2), mx, bar, (int)col0 + c * 64, at);
+        if (have == GRAD_ROWS)
+          for (int j = 0; j < PH * R; j += 64) ptx::tma_load_2d(to + XG + j * 128, mh, bar, j, place);
+      }
+      __syncwarp();
+      if (!run) {  // sixteen lanes, four rows each
+        int q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int from = lane * 4 + e;
+          const int lo = __shfl_sync(kAll, r0, from & 31), hi = __shfl_sync(kAll, r1, from & 31);
+          q[e] = from & 32 ? hi : lo;
+        }
+        if (lane < 16)
+          for (int c = 0; c < boxes; ++c)
+            ptx::tma_gather4(to + c * (XG / 2) + lane * 512, mr, bar, (int)col0 + c * 64, q[0], q[1], q[2], q[3]);
+      }
+      if (have < GRAD_ROWS && lane < 16) {
+        int q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = lane * 4 + e < have ? place + lane * 4 + e : (int)g.T;
+        for (int j = 0; j < PH * R; j += 64)
+          ptx::tma_gather4(to + XG + j * 128 + lane * 512, mhr, bar, j, q[0], q[1], q[2], q[3]);
+      }
+      __syncwarp();
+      r0 = n0;
+      r1 = n1;
     }
+    if (ctl.abort)  // the copies under way land before the block ends
+      for (int i = b - b0 > S ? b - b0 - S : 0; i < b - b0; ++i) tc::drain_wait(&ctl.full[i % S], (i / S) & 1);
+  } else if (warp == 1) {
+    const uint32_t id = ptx::idesc_f16(1, GRAD_COLS, PH * R, true, true);
+    for (int b = b0; b < b1; ++b) {
+      const int i = b - b0, slot = i % S;
+      if (!tc::warp_wait_bar(&ctl.full[slot], (i / S) & 1, &ctl.abort, 14, wd)) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        const uint32_t xa = ptx::smem_addr(sm + slot * stage_bytes), ha = xa + XG;
+#pragma unroll
+        for (int ks = 0; ks < GRAD_ROWS / 16; ++ks)
+          ptx::mma_f16(tmem, ptx::smem_desc(xa + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B),
+                       ptx::smem_desc(ha + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B), id,
+                       b > b0 || ks > 0);
+        ptx::mma_commit(&ctl.empty[slot]);
+        if (b + 1 == b1) ptx::mma_commit(&ctl.accf);
+      }
+      __syncwarp();
+    }
+  } else {
+    if (b1 > b0) tc::warp_wait_bar(&ctl.accf, 0, &ctl.abort, 5, wd);
+    ptx::tc_fence_after();
+    if (work) grad_sums<PH>(sm, tmem, R, b1 > b0, 0, 1);
   }
+  __syncwarp();
+  ptx::cluster_sync();
+  if (work) grad_out<T, DOWN_THREADS>(sm, g, p, l, rank, col0);
   ptx::cluster_sync();  // no CTA ends while another reads its sums
   tear_down(ctl, tmem, g.cols);
 }
@@ -1157,13 +1478,13 @@ bool aligned16(const void* p, int64_t pitch_bytes) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int ctas, size_t smem, cudaStream_t s,
-                            Args... args) {
+cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int ctas, size_t smem, int threads,
+                            cudaStream_t s, Args... args) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -1206,8 +1527,8 @@ cudaError_t adapters_few(const AdapterArgs& a, cudaStream_t s) {
   const int flags = (aligned16(a.x, a.ld * b) ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0) |
                     (aligned16(a.b, a.r * b) ? 4 : 0);
   const size_t smem = (size_t)(FEW * KC + (FEW + (FEW << log_ctas)) * a.r) * 4;
-  return launch_clusters(k_adapters_few<T>, dim3((unsigned)(tiles << log_ctas)), 1 << log_ctas, smem, s, a,
-                         log_ctas, none, flags);
+  return launch_clusters(k_adapters_few<T>, dim3((unsigned)(tiles << log_ctas)), 1 << log_ctas, smem, kThreads, s,
+                         a, log_ctas, none, flags);
 }
 
 // The kernel form by r rounded up to 16.
@@ -1218,9 +1539,69 @@ cudaError_t adapters_few(const AdapterArgs& a, cudaStream_t s) {
     CALL(4);                 \
   } while (0)
 
+// Tensor maps.  TMA reads rows that are 16-byte aligned.
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                             CUtensorMapFloatOOBfill);
+EncodeFn encode_fn() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+// [batch][rows][cols], rows ld elements apart, boxes of box_rows x 128 bytes, 128-byte swizzle.
+template <typename T>
+bool encode(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows,
+            int64_t batch = 0) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * sizeof(T)), (cuuint64_t)(rows * ld * sizeof(T))};
+  const cuuint32_t box[3] = {128 / sizeof(T), (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+  const CUtensorMapDataType type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+  return encode_fn()(m, type, batch ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+cudaError_t run_down_tma(DownArgs& g, int problems, cudaStream_t s) {
+  DownMaps maps = {};
+  for (int i = 0; i < problems; ++i) {
+    const DownProblem& p = g.prob[i];
+    const bool w = p.turned ? encode<T>(&maps.w[i], p.w, g.r, p.K, g.r, KB, g.L)
+                            : encode<T>(&maps.w[i], p.w, p.K, g.r, p.K, g.R, g.L);
+    if (!w || !encode<T>(&maps.x[i], p.x, p.K, g.T, p.ld, TILE) || !encode<T>(&maps.rows[i], p.x, p.K, g.T, p.ld, 1))
+      return cudaErrorInvalidValue;
+  }
+  const int64_t tiles = most_tiles(g.T, g.L, TILE);
+  // about two blocks per SM, with a ring of up to 104 KB each
+  const int64_t want = 2 * (int64_t)device_sm_count() / (ceil_div(g.T, TILE) * problems);
+  g.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
+  const int stage = XP + down_w_bytes(g.R), sums = TILE * (g.R * 4 + 16);
+  g.stages = (104 << 10) / stage < DOWN_STAGES ? (104 << 10) / stage : DOWN_STAGES;
+  const int bytes = g.stages * stage > sums ? g.stages * stage : sums;
+  g.cols = tmem_cols(g.R);
+  return launch_clusters(k_adapters_down_tma<T>, dim3((unsigned)(tiles << g.log_ctas), problems), 1 << g.log_ctas,
+                         smem_for((size_t)bytes + 1024, g.cols), DOWN_THREADS, s, maps, g);
+}
+
 template <typename T>
 cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
   using PL = Planes<T>;
+  if constexpr (sizeof(T) == 2) {
+    bool tma = encode_fn() != nullptr;
+    for (int i = 0; i < problems; ++i) tma = tma && g.prob[i].vec == 3;
+    if (tma) return run_down_tma<T>(g, problems, s);
+  }
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
   // about three blocks per SM
   const int64_t want = 3 * (int64_t)device_sm_count() / (ceil_div(g.T, TILE) * problems);
@@ -1229,7 +1610,7 @@ cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
   g.cols = tmem_cols(PL::PD * g.R);
   const size_t smem = smem_for((size_t)(ring > sums ? ring : sums) + 1024, g.cols);
   const dim3 grid((unsigned)(tiles << g.log_ctas), problems);
-#define IMC_DOWN(RU) return launch_clusters(k_adapters_down<T, RU>, grid, 1 << g.log_ctas, smem, s, g)
+#define IMC_DOWN(RU) return launch_clusters(k_adapters_down<T, RU>, grid, 1 << g.log_ctas, smem, kThreads, s, g)
   IMC_BY_RANK(g.R, IMC_DOWN);
 #undef IMC_DOWN
 }
@@ -1239,22 +1620,44 @@ cudaError_t run_up(UpArgs& g, cudaStream_t s) {
   using PL = Planes<T>;
   const int64_t b = sizeof(T);
   g.steps = (int)ceil_div(g.N, UP_N);
-  const uintptr_t wide = reinterpret_cast<uintptr_t>(g.out) | reinterpret_cast<uintptr_t>(g.base) | (uintptr_t)(g.N * b);
-  g.vec = (aligned16(g.w, (g.turned ? g.N : g.r) * b) ? 1 : 0) | (wide % 32 == 0 ? 2 : 0);
-  const int plane = g.R / 8 * CORE_K<T>, staged = g.vec & 2 ? 0 : UP_EPI * 32 * (STAGED_COLS<T> + 1) * 4;
+  const int plane = g.R / 8 * CORE_K<T>, part = 32 * 64 * (int)sizeof(T);
   g.w_bytes = (PL::P * (g.turned ? g.R * 256 : plane) + 1023) / 1024 * 1024;
   g.h_bytes = PL::PH * plane;
-  const int most = 232448 - (int)sizeof(UpCtl) - 256, room = most - 1024 - staged;
-  g.h_slots = room >= 2 * (g.h_bytes + g.w_bytes) ? 2 : 1;
-  g.slots = (room - g.h_slots * g.h_bytes) / g.w_bytes;
-  g.slots = g.slots < UP_SLOTS ? g.slots : UP_SLOTS;
-  const int smem = g.slots * g.w_bytes + g.h_slots * g.h_bytes + staged + 1024;
-  if (g.slots < 1) return cudaErrorInvalidValue;
+  const int most = 232448 - (int)sizeof(UpCtl) - 256 - 1024;
+  // rings: at least two parts of base, one h, one w; then more parts, w, h
+  const bool tma = encode_fn() && aligned16(g.out, g.N * b) && aligned16(g.base, 0) &&
+                   2 * UP_EPI * part + g.h_bytes + g.w_bytes <= most;
+  g.vec = (aligned16(g.w, (g.turned ? g.N : g.r) * b) ? 1 : 0) | (tma ? 2 : 0);
+  g.slots = g.h_slots = 1;
+  g.b_slots = tma ? 2 : 0;
+  const int staged = tma ? 0 : UP_EPI * 32 * (STAGED_COLS<T> + 1) * 4;
+  auto bytes = [&] {
+    return UP_EPI * g.b_slots * part + g.slots * g.w_bytes + g.h_slots * g.h_bytes + staged;
+  };
+  auto grow = [&](int& n, int to) {
+    while (n < to) {
+      ++n;
+      if (bytes() <= most) continue;
+      --n;
+      break;
+    }
+  };
+  if (bytes() > most) return cudaErrorInvalidValue;
+  grow(g.slots, 2);
+  if (tma) grow(g.b_slots, BASE_SLOTS);
+  grow(g.h_slots, 2);
+  grow(g.slots, UP_SLOTS);
+  const int smem = bytes() + 1024;
+  UpMaps maps = {};
+  if (tma && ((g.base && (!encode<T>(&maps.base, g.base, g.N, g.T, g.N, 32) ||
+                          !encode<T>(&maps.rows, g.base, g.N, g.T, g.N, 1))) ||
+              !encode<T>(&maps.out, g.out, g.N, g.T, g.N, 32)))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(k_adapters_up<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t items = most_tiles(g.T, g.L, TILE) * g.steps, sms = device_sm_count();
   e = launch_after_previous(k_adapters_up<T>, dim3((unsigned)(items < sms ? items : sms)), dim3(UP_THREADS),
-                            smem, s, g);
+                            smem, s, maps, g);
   note_launch();
   return e;
 }
@@ -1278,7 +1681,7 @@ cudaError_t adapters(const AdapterArgs& a, cudaStream_t s) {
                (aligned16(a.x, a.ld * b) && a.K % 8 == 0 ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0)};
   const cudaError_t e = run_down<T>(g, 1, s);
   if (e != cudaSuccess) return e;
-  UpArgs up = {g.prob[0].h, a.b, a.base, a.out, a.offsets, a.order, a.T, a.N, a.L, a.r, g.R, 0, 0, 0, 0, 0, 0, 0};
+  UpArgs up = {g.prob[0].h, a.b, a.base, a.out, a.offsets, a.order, a.T, a.N, a.L, a.r, g.R, 0, 0, 0, 0, 0, 0, 0, 0};
   return run_up<T>(up, s);
 }
 
@@ -1310,7 +1713,7 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
                           (aligned16(a.x, a.K * size) ? 1 : 0) | (aligned16(a.a, a.K * size) ? 2 : 0)};
   cudaError_t e = run_down<T>(g, problems, s);
   if (e == cudaSuccess && a.grad_x) {
-    UpArgs up = {d, a.a, a.base, a.grad_x, a.offsets, a.order, a.T, a.K, a.L, a.r, g.R, 0, 1, 0, 0, 0, 0, 0};
+    UpArgs up = {d, a.a, a.base, a.grad_x, a.offsets, a.order, a.T, a.K, a.L, a.r, g.R, 0, 1, 0, 0, 0, 0, 0, 0};
     e = run_up<T>(up, s);
   }
   if (e != cudaSuccess || (!a.grad_a && !a.grad_b)) return e;
@@ -1342,12 +1745,32 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
   const int64_t most = a.T / a.L / (4 * GRAD_ROWS);
   want = want < most ? want : most;
   w.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
+  if constexpr (PL::P == 1) {
+    bool tma = encode_fn() != nullptr;
+    for (int i = 0; i < parts; ++i) tma = tma && w.prob[i].vec;
+    if (tma) {
+      GradMaps maps = {};
+      for (int i = 0; i < parts; ++i) {
+        const GradProblem& p = w.prob[i];
+        if (!encode<T>(&maps.x[i], p.x, p.cols, a.T, p.cols, GRAD_ROWS) || !encode<T>(&maps.rows[i], p.x, p.cols, a.T, p.cols, 1) ||
+            !encode<T>(&maps.h[i], p.h, PL::PH * w.R, a.T, PL::PH * w.R, GRAD_ROWS) ||
+            !encode<T>(&maps.h_rows[i], p.h, PL::PH * w.R, a.T, PL::PH * w.R, 1))
+          return cudaErrorInvalidValue;
+      }
+      const int stage = GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R), sums = GRAD_COLS * (w.R + 1) * 4;
+      w.stages = (104 << 10) / stage < DOWN_STAGES ? (104 << 10) / stage : DOWN_STAGES;
+      const int bytes = w.stages * stage > sums ? w.stages * stage : sums;
+      w.cols = tmem_cols(PL::PH * w.R);
+      return launch_clusters(k_adapters_grad_tma, dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
+                             smem_for((size_t)bytes + 1024, w.cols), DOWN_THREADS, s, maps, w);
+    }
+  }
   const size_t ring = (size_t)PL::GRAD_STAGES * (PL::P * GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R));
   const size_t sums = (size_t)GRAD_COLS * (w.R + 1) * 4;
   w.cols = tmem_cols(PL::PH * w.R);
   const size_t smem = smem_for((ring > sums ? ring : sums) + 1024, w.cols);
   return launch_clusters(k_adapters_grad<T>, dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
-                         smem, s, w);
+                         smem, kThreads, s, w);
 }
 
 }  // namespace
