@@ -388,6 +388,18 @@ __device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, uint16_
   }
 }
 
+// A place in a ring and the parity of its current round.
+struct Slot {
+  int i = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      ++round;
+    }
+  }
+};
+
 // Barriers and tensor memory of a block.  The memory is taken before the stream's next
 // kernel may start: a block of that one that had it would wait for this kernel's end.
 template <typename Ctl>
@@ -597,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
   tear_down(ctl, tmem, g.cols);
 }
 
-// The same for 16-bit rows that TMA can load: one warp issues the loads (a box where the
-// tile's rows lie one after the other, four rows at a time where they do not), one the
+// The same for 16-bit rows that TMA can load: one warp issues the loads (a box for 32
+// rows that lie one after the other, four rows at a time where they do not), one the
 // MMAs, and nothing passes through registers.  8192 rows, 8 adapters, r 32, K 4096: us
 // with / without.
 constexpr int DOWN_THREADS = 192, DOWN_STAGES = 8;
@@ -636,18 +648,22 @@ __global__ void __launch_bounds__(DOWN_THREADS)
     const int b0 = min(rank * per, blocks), b1 = min(b0 + per, blocks);
     if (warp == 0) {
       const void *mx = &maps.x[blockIdx.y], *mr = &maps.rows[blockIdx.y], *mw = &maps.w[blockIdx.y];
-      int4 four = *reinterpret_cast<const int4*>(rows + lane * 4);
+      // lane 8 q + i has rows 4 i .. 4 i + 3 of quarter q
+      const int4 four = *reinterpret_cast<const int4*>(rows + lane * 4);
+      const int head = rows[(lane >> 3) * 32];
       bool run = true;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int at = lane * 4 + i;
-        if (at < t.rows) run = run && rows[at] == rows[0] + at;
+        if (at < t.rows) run = run && rows[at] == head + (at & 31);
       }
-      run = __all_sync(kAll, run);
+      const uint32_t runs = __ballot_sync(kAll, run);
+      run = ((runs >> (lane & 24)) & 255u) == 255u;  // the quarter's rows lie one after the other
       int b = b0;
-      for (; b < b1; ++b) {
-        const int i = b - b0, slot = i % S, use = i / S;
-        if (use > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (use - 1) & 1, &ctl.abort, 1, wd)) break;
+      Slot ring;
+      for (; b < b1; ++b, ring.next(S)) {
+        const int slot = ring.i;
+        if (ring.round > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (ring.round - 1) & 1, &ctl.abort, 1, wd)) break;
         uint8_t* to = sm + slot * stage_bytes;
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(&ctl.full[slot], XP + wb);
@@ -656,19 +672,21 @@ __global__ void __launch_bounds__(DOWN_THREADS)
           } else {
             ptx::tma_load_3d(to + XP, mw, &ctl.full[slot], b * KB, 0, t.l);
           }
-          if (run) ptx::tma_load_2d(to, mx, &ctl.full[slot], b * KB, rows[0]);
         }
         __syncwarp();
         if (!run)
           ptx::tma_gather4(to + lane * 512, mr, &ctl.full[slot], b * KB, four.x, four.y, four.z, four.w);
+        else if ((lane & 7) == 0)
+          ptx::tma_load_2d(to + lane * 512, mx, &ctl.full[slot], b * KB, head);
       }
       if (ctl.abort)  // the copies under way land before the block ends
         for (int i = b - b0 > S ? b - b0 - S : 0; i < b - b0; ++i)
           tc::drain_wait(&ctl.full[i % S], (i / S) & 1);
     } else if (warp == 1) {
-      for (int b = b0; b < b1; ++b) {
-        const int i = b - b0, slot = i % S;
-        if (!tc::warp_wait_bar(&ctl.full[slot], (i / S) & 1, &ctl.abort, 12, wd)) break;
+      Slot ring;
+      for (int b = b0; b < b1; ++b, ring.next(S)) {
+        const int slot = ring.i;
+        if (!tc::warp_wait_bar(&ctl.full[slot], ring.round & 1, &ctl.abort, 12, wd)) break;
         ptx::tc_fence_after();
         if (ptx::elect_one()) {
           const uint32_t xa = ptx::smem_addr(sm + slot * stage_bytes), wa = xa + XP;
@@ -722,6 +740,21 @@ struct UpCtl {
   int before[kAdapters + 2], first[kAdapters + 2];  // tiles before a bucket, its first row
 };
 
+// An item: 128 outputs (from `step` on) of the tile's rows.  Walked by counting: a 64-bit
+// division takes longer than an item's other instructions.
+struct Item {
+  int tile, step;
+  __device__ __forceinline__ void at(int64_t item, int steps) {
+    tile = (int)(item / steps);
+    step = (int)(item - (int64_t)tile * steps);
+  }
+  __device__ __forceinline__ void next(int steps) {
+    if (++step == steps) {
+      step = 0;
+      ++tile;
+    }
+  }
+};
 // Tile t of the counted buckets.
 __device__ __forceinline__ RowTile tile_of(const UpCtl& ctl, int B, int t) {
   int low = 0, high = B;  // before[low] <= t < before[high]
@@ -834,8 +867,13 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
     ptx::griddep_wait();
     const int lt = tid - UP_EPI * 32, ru = R >> 3;
     constexpr int LT = UP_LOAD * 32;
+    const int row_by = LT / ru, ju_by = LT - row_by * ru;  // from one of a thread's units to its next
     const bool copy_w = P == 1 && (g.vec & 1);
-    int last = -1, seg = 0, n = 0;
+    int last = -1;
+    Slot hslot, wslot;
+    Item item;
+    item.at(i0, g.steps);
+    RowTile t = {0, 0, 0};
     uint64_t *pending_w = nullptr, *pending_h = nullptr;
     auto arrived = [&] {  // (the copies have been waited for)
       ptx::fence_proxy_async_smem();
@@ -843,47 +881,57 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
       if (pending_w) ptx::mbar_arrive(pending_w);
       pending_w = pending_h = nullptr;
     };
-    for (int64_t it = i0; it < i1; ++it) {
-      const int tile = (int)(it / g.steps);
-      const int64_t n0 = (it - (int64_t)tile * g.steps) * UP_N;
-      const RowTile t = tile_of(ctl, B, tile);
-      if (t.l == g.L) continue;
+    for (int64_t it = i0; it < i1; ++it, item.next(g.steps)) {
+      const int64_t n0 = (int64_t)item.step * UP_N;
       uint64_t* now_h = nullptr;
-      if (tile != last) {
-        last = tile;
-        const int hb = seg % g.h_slots;
+      const bool other = item.tile != last;
+      if (other) t = tile_of(ctl, B, item.tile);
+      last = item.tile;
+      if (t.l == g.L) continue;
+      if (other) {
+        const int hb = hslot.i;
         uint8_t* ht = hs + hb * g.h_bytes;
-        if (seg >= g.h_slots) {
+        if (hslot.round > 0) {
           if (g.h_slots == 1) {  // the MMAs that free it wait for the item before this one
             ptx::copy_wait<0>();
             arrived();
           }
-          tc::warp_wait_bar(&ctl.hempty[hb], (seg / g.h_slots - 1) & 1, &ctl.abort, 6, wd);
+          tc::warp_wait_bar(&ctl.hempty[hb], (hslot.round - 1) & 1, &ctl.abort, 6, wd);
         }
-        for (int i = lt; i < TILE * ru; i += LT) {
-          const int row = i / ru, ju = i - row * ru;
+        int row = lt / ru, ju = lt - row * ru;
+        for (; row < TILE; row += row_by, ju += ju_by) {
+          if (ju >= ru) {
+            ju -= ru;
+            ++row;
+            if (row >= TILE) break;
+          }
           const bool in = row < t.rows;
 #pragma unroll
           for (int c = 0; c < PH; ++c)
             ptx::copy16(ht + c * plane + ju * CORE_K<T> + (row >> 3) * CORE<T> + (row & 7) * 16,
                         in ? g.h + ((int64_t)(t.p0 + row) * PH + c) * R + ju * 8 : g.h, in);
         }
-        ++seg;
+        hslot.next(g.h_slots);
         now_h = &ctl.hfull[hb];
       }
-      const int slot = n % g.slots, use = n / g.slots;
-      if (use > 0) {
+      const int slot = wslot.i;
+      if (wslot.round > 0) {
         if (g.slots == 1) {
           ptx::copy_wait<0>();
           arrived();
         }
-        tc::warp_wait_bar(&ctl.wempty[slot], (use - 1) & 1, &ctl.abort, 7, wd);
+        tc::warp_wait_bar(&ctl.wempty[slot], (wslot.round - 1) & 1, &ctl.abort, 7, wd);
       }
       uint8_t* to = ws + slot * g.w_bytes;
       const T* w = static_cast<const T*>(g.w) + (int64_t)t.l * r * g.N;
       const int left = (int)(g.N - n0 < UP_N ? g.N - n0 : UP_N);
+      int un = lt / ru, uj = lt - un * ru;
 #pragma unroll 4
-      for (int i = lt; i < TILE / 8 * R; i += LT) {
+      for (int i = lt; i < TILE / 8 * R; i += LT, un += row_by, uj += ju_by) {
+        if (uj >= ru) {
+          uj -= ru;
+          ++un;
+        }
         const T* from;
         uint8_t* at;
         int have, pitch;
@@ -894,7 +942,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
           at = to + (nu >> 3) * (R * 128) + j * 128 + (((nu ^ j) & 7) << 4);
           pitch = R * 256;
         } else {  // eight j of one n
-          const int nn = i / ru, ju = i - nn * ru;
+          const int nn = un, ju = uj;
           from = w + (n0 + nn) * r + ju * 8;
           have = nn < left ? r - ju * 8 : 0;
           at = to + ju * CORE_K<T> + (nn >> 3) * CORE<T> + (nn & 7) * 16;
@@ -918,27 +966,34 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
       }
       pending_w = &ctl.wfull[slot];
       pending_h = now_h;
-      ++n;
+      wslot.next(g.slots);
       if (ctl.abort) break;
     }
     ptx::copy_wait<0>();
     arrived();
   } else if (warp == UP_EPI + UP_LOAD) {
     // ---------------------------------------------------------------- MMAs
-    int last = -1, seg = 0, n = 0, hb = 0;
+    int last = -1, hb = 0;
+    Slot hslot, wslot, aslot;
+    Item item;
+    item.at(i0, g.steps);
+    bool product = false;
     const uint32_t id = ptx::idesc_f16(1, TILE, UP_N, false, g.turned);
-    for (int64_t it = i0; it < i1; ++it) {
-      const int tile = (int)(it / g.steps);
-      if (tile_of(ctl, B, tile).l == g.L) continue;
-      if (tile != last) {
-        last = tile;
-        hb = seg % g.h_slots;
-        if (!tc::warp_wait_bar(&ctl.hfull[hb], (seg / g.h_slots) & 1, &ctl.abort, 8, wd)) break;
-        ++seg;
+    for (int64_t it = i0; it < i1; ++it, item.next(g.steps)) {
+      const bool other = item.tile != last;
+      if (other) product = tile_of(ctl, B, item.tile).l < g.L;
+      last = item.tile;
+      if (!product) continue;
+      if (other) {
+        hb = hslot.i;
+        if (!tc::warp_wait_bar(&ctl.hfull[hb], hslot.round & 1, &ctl.abort, 8, wd)) break;
+        hslot.next(g.h_slots);
       }
-      const int slot = n % g.slots, buf = n & 1;
-      if (!tc::warp_wait_bar(&ctl.wfull[slot], (n / g.slots) & 1, &ctl.abort, 9, wd)) break;
-      if (n > 1 && !tc::warp_wait_bar(&ctl.acce[buf], (n / 2 - 1) & 1, &ctl.abort, 10, wd)) break;
+      const int slot = wslot.i, buf = aslot.i;
+      if (!tc::warp_wait_bar(&ctl.wfull[slot], wslot.round & 1, &ctl.abort, 9, wd)) break;
+      if (aslot.round > 0 && !tc::warp_wait_bar(&ctl.acce[buf], (aslot.round - 1) & 1, &ctl.abort, 10, wd)) break;
+      wslot.next(g.slots);
+      aslot.next(2);
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         const uint32_t ha = ptx::smem_addr(hs + hb * g.h_bytes), wa = ptx::smem_addr(ws + slot * g.w_bytes);
@@ -959,10 +1014,9 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
           }
         ptx::mma_commit(&ctl.wempty[slot]);
         ptx::mma_commit(&ctl.accf[buf]);
-        if (it + 1 == i1 || (int)((it + 1) / g.steps) != tile) ptx::mma_commit(&ctl.hempty[hb]);
+        if (it + 1 == i1 || item.step + 1 == g.steps) ptx::mma_commit(&ctl.hempty[hb]);
       }
       __syncwarp();
-      ++n;
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -976,12 +1030,11 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
       bool run = false;  // the warp's rows lie one after the other
       int64_t col = 0;
     };
-    auto place = [&](Place& q, int64_t it) {
-      const int tile = (int)(it / g.steps);
-      q.col = (it - (int64_t)tile * g.steps) * UP_N + half * 64;
-      if (tile == q.tile) return;
-      q.tile = tile;
-      const RowTile t = tile_of(ctl, B, tile);
+    auto place = [&](Place& q, const Item& item) {
+      q.col = (int64_t)item.step * UP_N + half * 64;
+      if (item.tile == q.tile) return;
+      q.tile = item.tile;
+      const RowTile t = tile_of(ctl, B, item.tile);
       q.l = t.l;
       q.rows = t.rows - q4 * 32 < 0 ? 0 : min(32, t.rows - q4 * 32);  // of this warp
       if (q.rows == 0) return;
@@ -990,10 +1043,16 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
       q.run = __all_sync(kAll, lane >= q.rows || q.row == first + lane);
     };
     Place ahead, now;
-    auto load = [&](int64_t it) {  // base of an item to its place in the ring
-      place(ahead, it);
+    Item item, next;
+    Slot nslot;
+    item.at(i0, g.steps);
+    next = item;
+    auto load = [&] {  // base of the next item to its place in the ring
+      place(ahead, next);
+      next.next(g.steps);
+      const int slot = nslot.i;
+      nslot.next(NS);
       if (!base || ahead.rows == 0 || ahead.col >= g.N) return;
-      const int slot = (int)((it - i0) % NS);
       uint64_t* bar = &ctl.bfull[warp][slot];
       uint8_t* to = ring + slot * SB;
       const int boxes = ahead.col + BOX < g.N ? 64 / BOX : 1;
@@ -1014,14 +1073,15 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
     int n = 0;
     uint32_t phases = 0;  // of the ring's barriers
     if (wide)
-      for (int64_t it = i0; it < i1 && it < i0 + NS - 1; ++it) load(it);
+      for (int64_t it = i0; it < i1 && it < i0 + NS - 1; ++it) load();
     int64_t it = i0;
-    for (; it < i1; ++it) {
-      place(now, it);
+    Slot slot_of;
+    for (; it < i1; ++it, item.next(g.steps), slot_of.next(NS)) {
+      place(now, item);
       const bool product = now.l < g.L, live = now.rows > 0 && now.col < g.N;
       const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + (n & 1) * UP_N + half * 64;
       if (wide) {
-        const int slot = (int)((it - i0) % NS);
+        const int slot = slot_of.i;
         uint8_t* mine = ring + slot * SB;
         if (base && live) {
           if (!tc::warp_wait_bar(&ctl.bfull[warp][slot], phases >> slot & 1, &ctl.abort, 13, wd)) break;
@@ -1086,7 +1146,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (it + NS - 1 < i1) load(it + NS - 1);
+        if (it + NS - 1 < i1) load();
       } else {
         if (product) {
           if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
@@ -1125,12 +1185,10 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
     }
     if (wide) {
       if (ctl.abort) {  // the copies under way land before the block ends
-        Place q;
-        for (int64_t i = it; i < i1 && i < it + NS - 1 && base; ++i) {
-          place(q, i);
-          if (q.rows == 0 || q.col >= g.N) continue;
-          const int slot = (int)((i - i0) % NS);
-          tc::drain_wait(&ctl.bfull[warp][slot], phases >> slot & 1);
+        for (int64_t i = it; i < i1 && i < it + NS - 1 && base; ++i, item.next(g.steps), slot_of.next(NS)) {
+          place(now, item);
+          if (now.rows == 0 || now.col >= g.N) continue;
+          tc::drain_wait(&ctl.bfull[warp][slot_of.i], phases >> slot_of.i & 1);
         }
       }
       if (lane == 0) ptx::bulk_wait_all();
@@ -1400,12 +1458,13 @@ __global__ void __launch_bounds__(DOWN_THREADS)
     };
     int r0 = row_of(b0, lane), r1 = row_of(b0, lane + 32);
     int b = b0;
-    for (; b < b1; ++b) {
-      const int i = b - b0, slot = i % S, use = i / S;
+    Slot ring;
+    for (; b < b1; ++b, ring.next(S)) {
+      const int slot = ring.i;
       const int n0 = row_of(b + 1, lane), n1 = row_of(b + 1, lane + 32);
       const int at = __shfl_sync(kAll, r0, 0), have = min(GRAD_ROWS, rows - b * GRAD_ROWS);
       const bool run = have == GRAD_ROWS && __all_sync(kAll, r0 == at + lane && r1 == at + 32 + lane);
-      if (use > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (use - 1) & 1, &ctl.abort, 4, wd)) break;
+      if (ring.round > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (ring.round - 1) & 1, &ctl.abort, 4, wd)) break;
       uint8_t* to = sm + slot * stage_bytes;
       uint64_t* bar = &ctl.full[slot];
       const int place = first + b * GRAD_ROWS;
@@ -1444,9 +1503,10 @@ __global__ void __launch_bounds__(DOWN_THREADS)
       for (int i = b - b0 > S ? b - b0 - S : 0; i < b - b0; ++i) tc::drain_wait(&ctl.full[i % S], (i / S) & 1);
   } else if (warp == 1) {
     const uint32_t id = ptx::idesc_f16(1, GRAD_COLS, PH * R, true, true);
-    for (int b = b0; b < b1; ++b) {
-      const int i = b - b0, slot = i % S;
-      if (!tc::warp_wait_bar(&ctl.full[slot], (i / S) & 1, &ctl.abort, 14, wd)) break;
+    Slot ring;
+    for (int b = b0; b < b1; ++b, ring.next(S)) {
+      const int slot = ring.i;
+      if (!tc::warp_wait_bar(&ctl.full[slot], ring.round & 1, &ctl.abort, 14, wd)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         const uint32_t xa = ptx::smem_addr(sm + slot * stage_bytes), ha = xa + XG;
@@ -1579,7 +1639,7 @@ cudaError_t run_down_tma(DownArgs& g, int problems, cudaStream_t s) {
     const DownProblem& p = g.prob[i];
     const bool w = p.turned ? encode<T>(&maps.w[i], p.w, g.r, p.K, g.r, KB, g.L)
                             : encode<T>(&maps.w[i], p.w, p.K, g.r, p.K, g.R, g.L);
-    if (!w || !encode<T>(&maps.x[i], p.x, p.K, g.T, p.ld, TILE) || !encode<T>(&maps.rows[i], p.x, p.K, g.T, p.ld, 1))
+    if (!w || !encode<T>(&maps.x[i], p.x, p.K, g.T, p.ld, 32) || !encode<T>(&maps.rows[i], p.x, p.K, g.T, p.ld, 1))
       return cudaErrorInvalidValue;
   }
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
