@@ -223,6 +223,8 @@ __global__ void __launch_bounds__(kThreads)
 //
 // A value is a sum of bf16 numbers ("planes"): bf16 1, fp16 2, fp32 3, exactly; an element
 // of h is kept as PH of them (2 for the 16-bit types: to 2^-17 of its value; 3 for fp32).
+// Beside fp16 b, h is two fp16 numbers instead, its row scaled by a power of two that
+// brings its largest value to 2^14 .. 2^15: to 2^-22 of that, whatever its size.
 // The planes of the operand that lies along the MMA's N follow one another there, so
 // that the tensor core reads a plane of the other operand once for all of them; the sums
 // over those planes are taken in fp32 afterwards.
@@ -230,31 +232,24 @@ constexpr int TILE = 128;            // rows of a tile: the MMA's M
 constexpr int KB = 64;               // values of K per stage: 128 bytes of a plane's row
 constexpr int XP = TILE * KB * 2;    // bytes of a plane of a stage's x
 constexpr int UP_N = 128;            // outputs of one step of the second product
-// Core matrices (8 rows x 16 bytes) of the operands along r: CORE bytes apart over the
-// rows and CORE_K over r.  The 16-bit types' are spread over the banks, fp32's planes have
-// to fit for r = 128.
-template <typename T>
-constexpr int CORE = sizeof(T) == 2 ? 144 : 128;
-template <typename T>
-constexpr int CORE_K = CORE<T> * (TILE / 8) + 32;
-
 __device__ int g_watchdog_adapters;
 
 template <typename T>
 struct Planes;
-// P: planes of a value; PD: of one in the first product, which takes fp16 as it is (its
-// format FD); STAGES of that one's ring.
+// P: planes of a value where it has to be bf16 (gradients of the weights); PD and FD: planes
+// and format (0 fp16, 1 bf16) of one in the two products with a and b, which take fp16 as
+// it is; PH: planes of an element of h; stages of the rings.
 template <>
 struct Planes<__nv_bfloat16> {
-  static constexpr int P = 1, PD = 1, PH = 2, FD = 1, STAGES = 4, GRAD_STAGES = 3;
+  static constexpr int P = 1, PD = 1, FD = 1, PH = 2, STAGES = 4, GRAD_STAGES = 3;
 };
 template <>
 struct Planes<__half> {
-  static constexpr int P = 2, PD = 1, PH = 2, FD = 0, STAGES = 4, GRAD_STAGES = 2;
+  static constexpr int P = 2, PD = 1, FD = 0, PH = 2, STAGES = 4, GRAD_STAGES = 2;
 };
 template <>
 struct Planes<float> {
-  static constexpr int P = 3, PD = 3, PH = 3, FD = 1, STAGES = 2, GRAD_STAGES = 2;
+  static constexpr int P = 3, PD = 3, FD = 1, PH = 3, STAGES = 2, GRAD_STAGES = 2;
 };
 
 // Eight values of a row as they lie in memory.
@@ -318,7 +313,9 @@ struct DownProblem {
   const void* x;   // [T, K], rows ld elements apart
   int64_t ld, K;
   const void* w;   // of an adapter [r, K]; turned: [K, r]
-  uint16_t* h;     // [T][PH][R], its planes, in adapter order
+  uint16_t* h;     // [T][PH][R], its planes, in adapter order; or null
+  uint16_t* h16;   // [T][2][R] of scaled fp16 rows, and what they are to be multiplied by
+  float* row_scale;  // [T]; or null
   int turned, vec; // vec: 1 x, 2 w
 };
 struct DownArgs {
@@ -359,17 +356,16 @@ __device__ __forceinline__ void own_sums(uint8_t* sm, uint32_t tmem, int R, bool
   }
 }
 // h of this CTA's 128 / C rows of the tile: the sums of all CTAs in their order, scaled,
-// in planes.
-template <int PH, int THREADS>
-__device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, uint16_t* h, const RowTile& t,
-                                         int rank) {
+// in planes.  All threads of the block.
+template <typename T, int THREADS>
+__device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, const DownProblem& p,
+                                         const RowTile& t, int rank) {
+  constexpr int PH = Planes<T>::PH;
+  __shared__ uint32_t top[sizeof(T) == 2 ? TILE : 1];  // a row's largest magnitude
   const int R = g.R, C = 1 << g.log_ctas, pitch = R * 4 + 16;
   const int mine = TILE >> g.log_ctas, units = mine * (R >> 3);
   const float scale = g.scale ? g.scale[t.l] : 1.0f;
-  for (int i = threadIdx.x; i < units; i += THREADS) {
-    const int row = rank * mine + i / (R >> 3), ju = i % (R >> 3);
-    if (row >= t.rows) break;
-    float v[8];
+  auto sums = [&](int row, int ju, float (&v)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
     for (int c = 0; c < C; ++c) {
@@ -380,11 +376,52 @@ __device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, uint16_
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= scale;
-    uint4 w[PH];
-    split8<PH>(v, w);
+  };
+  const bool scaled = sizeof(T) == 2 && Planes<T>::FD == 0 && p.h16;
+  if (scaled) {
+    for (int i = threadIdx.x; i < mine; i += THREADS) top[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < units; i += THREADS) {
+      const int row = i / (R >> 3);
+      float v[8];
+      sums(rank * mine + row, i % (R >> 3), v);
+      uint32_t m = 0;
 #pragma unroll
-    for (int c = 0; c < PH; ++c)
-      *reinterpret_cast<uint4*>(h + ((int64_t)(t.p0 + row) * PH + c) * R + ju * 8) = w[c];
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      atomicMax(top + row, m);  // whatever the order
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < units; i += THREADS) {
+    const int row = rank * mine + i / (R >> 3), ju = i % (R >> 3);
+    if (row >= t.rows) break;
+    float v[8];
+    sums(row, ju, v);
+    if (scaled) {
+      // 2^14 over the largest value's power of two; rows of zeros, and those with
+      // infinities or NaN, as they are
+      uint32_t e8 = top[row - rank * mine] >> 23;
+      e8 = e8 == 255u || top[row - rank * mine] == 0 ? 141u : max(e8, 15u);
+      const float up = __uint_as_float((268u - e8) << 23);
+      alignas(16) __half hi[8], lo[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        hi[e] = __float2half_rn(v[e] * up);
+        const float f = __half2float(hi[e]);
+        lo[e] = __float2half_rn(fabsf(f) == INFINITY ? 0.0f : v[e] * up - f);
+      }
+      uint4* to = reinterpret_cast<uint4*>(p.h16 + (int64_t)(t.p0 + row) * 2 * R + ju * 8);
+      to[0] = *reinterpret_cast<const uint4*>(hi);
+      to[R / 8] = *reinterpret_cast<const uint4*>(lo);
+      if (ju == 0) p.row_scale[t.p0 + row] = __uint_as_float((e8 - 14u) << 23);
+    }
+    if (p.h) {
+      uint4 w[PH];
+      split8<PH>(v, w);
+#pragma unroll
+      for (int c = 0; c < PH; ++c)
+        *reinterpret_cast<uint4*>(p.h + ((int64_t)(t.p0 + row) * PH + c) * R + ju * 8) = w[c];
+    }
   }
 }
 
@@ -440,7 +477,7 @@ template <typename T, int RU>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     k_adapters_down(const __grid_constant__ DownArgs g) {
   using PL = Planes<T>;
-  constexpr int P = PL::PD, PH = PL::PH, S = PL::STAGES;
+  constexpr int P = PL::PD, S = PL::STAGES;
   constexpr bool ASYNC = sizeof(T) == 2;
   extern __shared__ uint8_t sm_raw[];
   __shared__ RingCtl ctl;
@@ -603,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     __syncthreads();
     own_sums<P>(sm, tmem, R, any, warp >> 2, kWarps / 4);
     ptx::cluster_sync();
-    all_sums<PH, kThreads>(sm, g, p.h, t, rank);
+    all_sums<T, kThreads>(sm, g, p, t, rank);
     ptx::cluster_sync();  // no CTA ends while another reads its sums
   }
   tear_down(ctl, tmem, g.cols);
@@ -708,27 +745,52 @@ __global__ void __launch_bounds__(DOWN_THREADS)
     }
     __syncwarp();
     ptx::cluster_sync();
-    all_sums<PL::PH, DOWN_THREADS>(sm, g, p.h, t, rank);
+    all_sums<T, DOWN_THREADS>(sm, g, p, t, rank);
     ptx::cluster_sync();  // no CTA ends while another reads its sums
   }
   tear_down(ctl, tmem, g.cols);
 }
 
+// Rows of an operand along r in shared memory: r rounded up to 16, 32 or 64 values, swizzled
+// accordingly, or two such blocks of 64.
+struct Along {
+  int bytes, blocks;  // of a row; of 64 values
+  __host__ __device__ explicit Along(int R)
+      : bytes(R <= 16 ? 32 : (R <= 32 ? 64 : 128)), blocks(R > 64 ? 2 : 1) {}
+  __host__ __device__ int plane() const { return TILE * bytes * blocks; }
+  // 16-byte unit u of row n
+  __device__ __forceinline__ int at(int n, int u) const {
+    if (bytes == 32) return n * 32 + ((u ^ (n >> 2 & 1)) << 4);
+    if (bytes == 64) return n * 64 + ((u ^ (n >> 1 & 3)) << 4);
+    return (u >> 3) * (TILE * 128) + n * 128 + (((u ^ n) & 7) << 4);
+  }
+  // the matrix descriptor of sixteen values from 16 ks on
+  __device__ __forceinline__ uint64_t desc(uint32_t base, int ks) const {
+    const int in = ks * 32, block = in / bytes;
+    return ptx::smem_desc(base + block * (TILE * bytes) + in - block * bytes, 16, 8 * bytes,
+                          bytes == 32 ? 6 : (bytes == 64 ? ptx::kSwizzle64B : ptx::kSwizzle128B));
+  }
+};
+
 struct UpArgs {
-  const uint16_t* h;  // [T][PH][R]
+  const float* row_scale;  // of scaled h, else null
   const void* w;      // of an adapter [N, r]; turned: [r, N]
   const void* base;
   void* out;
   const int32_t *offsets, *order;
   int64_t T, N;
-  int L, r, R, steps, turned, vec;  // vec: 1 w, 2 base and out (by TMA)
+  int L, r, R, steps, turned, vec;  // vec: 1 w, 2 base and out, by TMA
   int slots, h_slots, b_slots, w_bytes, h_bytes;  // of the rings of w, h and base; bytes of one
 };
 struct UpMaps {
   CUtensorMap base, rows, out;  // base by 32 rows, by rows; out by 32 rows; 128 bytes of columns
+  CUtensorMap h, w;             // a plane of 128 rows; 128 outputs (turned: 64) and r
 };
-constexpr int UP_EPI = 8, UP_LOAD = 4;  // warps
-constexpr int UP_THREADS = (UP_EPI + UP_LOAD + 1) * 32;
+constexpr int UP_EPI = 8;  // warps; beside them loaders and one for the MMAs
+template <typename T>
+constexpr int UP_LOAD = sizeof(T) == 2 ? 1 : 4;
+template <typename T>
+constexpr int UP_THREADS = (UP_EPI + UP_LOAD<T> + 1) * 32;
 constexpr int UP_SLOTS = 4, BASE_SLOTS = 4;
 constexpr int kAdapters = 1024;  // the most that a layout has
 struct UpCtl {
@@ -736,7 +798,7 @@ struct UpCtl {
   uint64_t bfull[UP_EPI][BASE_SLOTS];
   uint32_t tmem_base;
   int abort;
-  int sums[UP_THREADS / 32];
+  int sums[16];
   int before[kAdapters + 2], first[kAdapters + 2];  // tiles before a bucket, its first row
 };
 
@@ -767,14 +829,15 @@ __device__ __forceinline__ RowTile tile_of(const UpCtl& ctl, int B, int t) {
   return {low, p0, min(TILE, ctl.first[low + 1] - p0)};
 }
 
-__device__ __forceinline__ uint32_t add_pair(__nv_bfloat16, uint32_t base, float a, float b) {
+// Two values of base and of the product (fp16: times its row's scale).
+__device__ __forceinline__ uint32_t add_pair(__nv_bfloat16, uint32_t base, float a, float b, float) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(base << 16) + a,
                                                  __uint_as_float(base & 0xFFFF0000u) + b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t add_pair(__half, uint32_t base, float a, float b) {
+__device__ __forceinline__ uint32_t add_pair(__half, uint32_t base, float a, float b, float scale) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&base));
-  const __half2 v = __floats2half2_rn(f.x + a, f.y + b);
+  const __half2 v = __floats2half2_rn(fmaf(a, scale, f.x), fmaf(b, scale, f.y));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -789,13 +852,14 @@ constexpr int STAGED_COLS = sizeof(T) == 2 ? 32 : 16;
 //               place, rounds once, and has TMA store it (row by row itself where the box
 //               would reach other rows); without TMA (unaligned rows, no room) it adds
 //               column by column through shared memory
-//   warps 8-11  h of a tile and w of an item to shared memory
-//   warp 12     tensor memory, MMAs (two accumulators of 128 columns)
+//   then        one warp (fp32: four, which cut w into its planes) that loads h of a tile
+//               and w of an item, and one for tensor memory and the MMAs (two accumulators
+//               of 128 columns)
 template <typename T>
-__global__ void __launch_bounds__(UP_THREADS, 1)
+__global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     k_adapters_up(const __grid_constant__ UpMaps maps, const __grid_constant__ UpArgs g) {
   using PL = Planes<T>;
-  constexpr int P = PL::P, PH = PL::PH;
+  constexpr int P = PL::PD, PH = PL::PH, LOAD = UP_LOAD<T>, THREADS = UP_THREADS<T>;
   extern __shared__ uint8_t sm_raw[];
   __shared__ UpCtl ctl;
   uint8_t* sm = tc::smem_align1024(sm_raw);
@@ -803,11 +867,11 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
   int* wd = &g_watchdog_adapters;
   if (tid == 0) {
     for (int i = 0; i < UP_SLOTS; ++i) {
-      ptx::mbar_init(&ctl.wfull[i], UP_LOAD * 32);
+      ptx::mbar_init(&ctl.wfull[i], (g.vec & 1) ? 1 : LOAD * 32);
       ptx::mbar_init(&ctl.wempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ctl.hfull[i], UP_LOAD * 32);
+      ptx::mbar_init(&ctl.hfull[i], 1);
       ptx::mbar_init(&ctl.hempty[i], 1);
       ptx::mbar_init(&ctl.accf[i], 1);
       ptx::mbar_init(&ctl.acce[i], UP_EPI * 32);
@@ -817,7 +881,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
     ctl.abort = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == UP_EPI + UP_LOAD) {
+  if (warp == UP_EPI + LOAD) {
     ptx::tmem_alloc(&ctl.tmem_base, 2 * UP_N);
     ptx::tmem_relinquish();
   }
@@ -826,7 +890,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
   T* out = static_cast<T*>(g.out);
   const int B = g.L + (g.base != g.out ? 1 : 0);  // rows without an adapter: copied, or left
   {
-    const int per = (B + UP_THREADS - 1) / UP_THREADS, e0 = tid * per;
+    const int per = (B + THREADS - 1) / THREADS, e0 = tid * per;
     int tiles = 0;
     for (int e = e0; e < e0 + per && e < B; ++e) {
       const int first = __ldg(g.offsets + e);
@@ -848,7 +912,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
       ctl.before[e] = at;
       at += (__ldg(g.offsets + e + 1) - ctl.first[e] + TILE - 1) / TILE;
     }
-    if (tid == UP_THREADS - 1) ctl.before[B] = upto;
+    if (tid == THREADS - 1) ctl.before[B] = upto;
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -860,125 +924,108 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
   constexpr int SB = 32 * 64 * (int)sizeof(T);  // bytes of a warp's part of an item
   uint8_t* ws = sm + UP_EPI * g.b_slots * SB;
   uint8_t* hs = ws + g.slots * g.w_bytes;
-  const int plane = (R >> 3) * CORE_K<T>;
+  const Along along(R);
+  const int plane = along.plane();
 
-  if (warp >= UP_EPI && warp < UP_EPI + UP_LOAD) {
+  if (warp >= UP_EPI && warp < UP_EPI + LOAD) {
     // ------------------------------------------------------------- loaders
     ptx::griddep_wait();
     const int lt = tid - UP_EPI * 32, ru = R >> 3;
-    constexpr int LT = UP_LOAD * 32;
+    constexpr int LT = LOAD * 32;
     const int row_by = LT / ru, ju_by = LT - row_by * ru;  // from one of a thread's units to its next
-    const bool copy_w = P == 1 && (g.vec & 1);
     int last = -1;
     Slot hslot, wslot;
     Item item;
     item.at(i0, g.steps);
     RowTile t = {0, 0, 0};
-    uint64_t *pending_w = nullptr, *pending_h = nullptr;
-    auto arrived = [&] {  // (the copies have been waited for)
-      ptx::fence_proxy_async_smem();
-      if (pending_h) ptx::mbar_arrive(pending_h);
-      if (pending_w) ptx::mbar_arrive(pending_w);
-      pending_w = pending_h = nullptr;
-    };
     for (int64_t it = i0; it < i1; ++it, item.next(g.steps)) {
       const int64_t n0 = (int64_t)item.step * UP_N;
-      uint64_t* now_h = nullptr;
       const bool other = item.tile != last;
       if (other) t = tile_of(ctl, B, item.tile);
       last = item.tile;
       if (t.l == g.L) continue;
       if (other) {
         const int hb = hslot.i;
-        uint8_t* ht = hs + hb * g.h_bytes;
-        if (hslot.round > 0) {
-          if (g.h_slots == 1) {  // the MMAs that free it wait for the item before this one
-            ptx::copy_wait<0>();
-            arrived();
-          }
-          tc::warp_wait_bar(&ctl.hempty[hb], (hslot.round - 1) & 1, &ctl.abort, 6, wd);
-        }
-        int row = lt / ru, ju = lt - row * ru;
-        for (; row < TILE; row += row_by, ju += ju_by) {
-          if (ju >= ru) {
-            ju -= ru;
-            ++row;
-            if (row >= TILE) break;
-          }
-          const bool in = row < t.rows;
+        if (hslot.round > 0 && !tc::warp_wait_bar(&ctl.hempty[hb], (hslot.round - 1) & 1, &ctl.abort, 6, wd)) break;
+        if (lt == 0) {
+          uint8_t* to = hs + hb * g.h_bytes;
+          ptx::mbar_arrive_expect_tx(&ctl.hfull[hb], PH * plane);
 #pragma unroll
           for (int c = 0; c < PH; ++c)
-            ptx::copy16(ht + c * plane + ju * CORE_K<T> + (row >> 3) * CORE<T> + (row & 7) * 16,
-                        in ? g.h + ((int64_t)(t.p0 + row) * PH + c) * R + ju * 8 : g.h, in);
+            for (int k = 0; k < along.blocks; ++k)
+              ptx::tma_load_3d(to + c * plane + k * (TILE * 128), &maps.h, &ctl.hfull[hb], k * 64, c, t.p0);
         }
         hslot.next(g.h_slots);
-        now_h = &ctl.hfull[hb];
       }
       const int slot = wslot.i;
-      if (wslot.round > 0) {
-        if (g.slots == 1) {
-          ptx::copy_wait<0>();
-          arrived();
-        }
-        tc::warp_wait_bar(&ctl.wempty[slot], (wslot.round - 1) & 1, &ctl.abort, 7, wd);
-      }
+      if (wslot.round > 0 && !tc::warp_wait_bar(&ctl.wempty[slot], (wslot.round - 1) & 1, &ctl.abort, 7, wd)) break;
       uint8_t* to = ws + slot * g.w_bytes;
-      const T* w = static_cast<const T*>(g.w) + (int64_t)t.l * r * g.N;
-      const int left = (int)(g.N - n0 < UP_N ? g.N - n0 : UP_N);
-      int un = lt / ru, uj = lt - un * ru;
+      if (P == 1 && (g.vec & 1)) {
+        if (lt == 0) {
+          uint64_t* bar = &ctl.wfull[slot];
+          ptx::mbar_arrive_expect_tx(bar, g.turned ? R * 256 : plane);
+          if (g.turned) {
+            const int boxes = 2;
+            for (int k = 0; k < boxes; ++k) ptx::tma_load_3d(to + k * (R * 128), &maps.w, bar, (int)n0 + k * 64, 0, t.l);
+          } else {
+            for (int k = 0; k < along.blocks; ++k)
+              ptx::tma_load_3d(to + k * (TILE * 128), &maps.w, bar, k * 64, (int)n0, t.l);
+          }
+        }
+        __syncwarp();
+      } else {
+        const T* w = static_cast<const T*>(g.w) + (int64_t)t.l * r * g.N;
+        const int left = (int)(g.N - n0 < UP_N ? g.N - n0 : UP_N);
+        int un = lt / ru, uj = lt - un * ru;
 #pragma unroll 4
-      for (int i = lt; i < TILE / 8 * R; i += LT, un += row_by, uj += ju_by) {
-        if (uj >= ru) {
-          uj -= ru;
-          ++un;
-        }
-        const T* from;
-        uint8_t* at;
-        int have, pitch;
-        if (g.turned) {  // eight n of one j; n lies along the operand's N
-          const int nu = i & 15, j = i >> 4;
-          from = w + j * g.N + n0 + nu * 8;
-          have = j < r ? left - nu * 8 : 0;
-          at = to + (nu >> 3) * (R * 128) + j * 128 + (((nu ^ j) & 7) << 4);
-          pitch = R * 256;
-        } else {  // eight j of one n
-          const int nn = un, ju = uj;
-          from = w + (n0 + nn) * r + ju * 8;
-          have = nn < left ? r - ju * 8 : 0;
-          at = to + ju * CORE_K<T> + (nn >> 3) * CORE<T> + (nn & 7) * 16;
-          pitch = plane;
-        }
-        if (copy_w) {
-          ptx::copy16(at, have > 0 ? from : w, have > 0);
-        } else {
+        for (int i = lt; i < TILE / 8 * R; i += LT, un += row_by, uj += ju_by) {
+          if (uj >= ru) {
+            uj -= ru;
+            ++un;
+          }
+          const T* from;
+          uint8_t* at;
+          int have, pitch;
+          if (g.turned) {  // eight n of one j; n lies along the operand's N
+            const int nu = i & 15, j = i >> 4;
+            from = w + j * g.N + n0 + nu * 8;
+            have = j < r ? left - nu * 8 : 0;
+            at = to + (nu >> 3) * (R * 128) + j * 128 + (((nu ^ j) & 7) << 4);
+            pitch = R * 256;
+          } else {  // eight j of one n
+            from = w + (n0 + un) * r + uj * 8;
+            have = un < left ? r - uj * 8 : 0;
+            at = to + along.at(un, uj);
+            pitch = plane;
+          }
           Raw8<T> raw;
-          raw.load(from, have, g.vec & 1);
+          raw.load(from, have, g.vec & 4);
           uint4 v[P];
           planes_of<T, P>(raw, v);
 #pragma unroll
           for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(at + c * pitch) = v[c];
         }
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&ctl.wfull[slot]);
       }
-      ptx::copy_commit();
-      if (pending_w) {  // the item before this one has arrived
-        ptx::copy_wait<1>();
-        arrived();
-      }
-      pending_w = &ctl.wfull[slot];
-      pending_h = now_h;
       wslot.next(g.slots);
-      if (ctl.abort) break;
     }
-    ptx::copy_wait<0>();
-    arrived();
-  } else if (warp == UP_EPI + UP_LOAD) {
+    if (ctl.abort && lt == 0) {  // the copies under way land before the block ends
+      auto drain = [](uint64_t* bars, const Slot& next, int n) {
+        for (int i = 0; i < n; ++i)
+          if (i < next.i || next.round > 0) tc::drain_wait(bars + i, (i < next.i ? next.round : next.round - 1) & 1);
+      };
+      drain(ctl.hfull, hslot, g.h_slots);
+      if (g.vec & 1) drain(ctl.wfull, wslot, g.slots);
+    }
+  } else if (warp == UP_EPI + LOAD) {
     // ---------------------------------------------------------------- MMAs
     int last = -1, hb = 0;
     Slot hslot, wslot, aslot;
     Item item;
     item.at(i0, g.steps);
     bool product = false;
-    const uint32_t id = ptx::idesc_f16(1, TILE, UP_N, false, g.turned);
+    const uint32_t id = ptx::idesc_f16(PL::FD, TILE, UP_N, false, g.turned);
     for (int64_t it = i0; it < i1; ++it, item.next(g.steps)) {
       const bool other = item.tile != last;
       if (other) product = tile_of(ctl, B, item.tile).l < g.L;
@@ -1003,12 +1050,11 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
           for (int d = 0; d < P; ++d) {
             const uint64_t wdesc =
                 g.turned ? ptx::smem_desc(wa + d * (R * 256) + ks * 2048, R * 128, 1024, ptx::kSwizzle128B)
-                         : ptx::smem_desc(wa + d * plane + ks * 2 * CORE_K<T>, CORE_K<T>, CORE<T>, 0);
+                         : along.desc(wa + d * plane, ks);
 #pragma unroll
             for (int c = 0; c < PH; ++c) {
               if (P == 3 && c + d > 2) continue;  // fp32: the smallest products are left out
-              ptx::mma_f16(tmem + buf * UP_N,
-                           ptx::smem_desc(ha + c * plane + ks * 2 * CORE_K<T>, CORE_K<T>, CORE<T>, 0), wdesc, id, more);
+              ptx::mma_f16(tmem + buf * UP_N, along.desc(ha + c * plane, ks), wdesc, id, more);
               more = 1;
             }
           }
@@ -1026,7 +1072,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
     // An item's tile, the row of this lane in it, its columns.  For loads and for stores:
     // the first run ahead.
     struct Place {
-      int tile = -1, row = 0, rows = 0, l = 0;
+      int tile = -1, row = 0, rows = 0, l = 0, place = 0;
       bool run = false;  // the warp's rows lie one after the other
       int64_t col = 0;
     };
@@ -1038,7 +1084,8 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
       q.l = t.l;
       q.rows = t.rows - q4 * 32 < 0 ? 0 : min(32, t.rows - q4 * 32);  // of this warp
       if (q.rows == 0) return;
-      q.row = __ldg(g.order + t.p0 + q4 * 32 + min(lane, q.rows - 1));
+      q.place = t.p0 + q4 * 32 + min(lane, q.rows - 1);
+      q.row = __ldg(g.order + q.place);
       const int first = __shfl_sync(kAll, q.row, 0);
       q.run = __all_sync(kAll, lane >= q.rows || q.row == first + lane);
     };
@@ -1070,7 +1117,13 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
       }
     };
     const bool wide = g.vec & 2;
-    int n = 0;
+    float scale = 1.0f;  // of this lane's row of h; there once an accumulator is
+    int scale_of = -1, n = 0;
+    auto scale_it = [&] {
+      if (PL::FD == 1 || now.tile == scale_of) return;
+      scale_of = now.tile;
+      scale = now.rows > 0 ? __ldcg(g.row_scale + now.place) : 1.0f;
+    };
     uint32_t phases = 0;  // of the ring's barriers
     if (wide)
       for (int64_t it = i0; it < i1 && it < i0 + NS - 1; ++it) load();
@@ -1091,6 +1144,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
         if (product) {
           if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
           ptx::tc_fence_after();
+          scale_it();
         }
         if (live && (product || !base)) {
 #pragma unroll
@@ -1113,7 +1167,8 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 if constexpr (sizeof(T) == 2)
-                  hw[e] = add_pair(T(), hw[e], __uint_as_float(s[i * 8 + 2 * e]), __uint_as_float(s[i * 8 + 2 * e + 1]));
+                  hw[e] = add_pair(T(), hw[e], __uint_as_float(s[i * 8 + 2 * e]), __uint_as_float(s[i * 8 + 2 * e + 1]),
+                                   scale);
                 else
                   hw[e] = __float_as_uint(__uint_as_float(hw[e]) + __uint_as_float(s[i * 4 + e]));
               }
@@ -1151,6 +1206,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
         if (product) {
           if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
           ptx::tc_fence_after();
+          scale_it();
         }
         constexpr int SC = STAGED_COLS<T>, ROWS = 32 / SC;  // columns, and rows at once
         float* mine = reinterpret_cast<float*>(hs + g.h_slots * g.h_bytes) + warp * 32 * (SC + 1);
@@ -1167,7 +1223,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
               ptx::mbar_arrive(&ctl.acce[n & 1]);
             }
 #pragma unroll
-            for (int e = 0; e < SC; ++e) mine[lane * (SC + 1) + e] = __uint_as_float(s[e]);
+            for (int e = 0; e < SC; ++e) mine[lane * (SC + 1) + e] = __uint_as_float(s[e]) * scale;
             __syncwarp();
           }
           const int64_t c = now.col + b * SC + lane % SC;  // a lane has a column of its rows
@@ -1197,7 +1253,7 @@ __global__ void __launch_bounds__(UP_THREADS, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp != UP_EPI + UP_LOAD) return;
+  if (warp != UP_EPI + LOAD) return;
   ptx::tc_fence_after();
   if (ctl.abort) {  // after a wait that gave up, no MMA may run on into freed memory
     if (ptx::elect_one()) ptx::mma_commit(&ctl.drain);
@@ -1619,17 +1675,32 @@ EncodeFn encode_fn() {
   });
   return fn;
 }
-// [batch][rows][cols], rows ld elements apart, boxes of box_rows x 128 bytes, 128-byte swizzle.
+// [batch][rows][cols], rows ld elements apart (batch 0: two dimensions), in boxes of box_rows
+// x box_bytes (32, 64 or 128) of columns, swizzled by as much.
 template <typename T>
 bool encode(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows,
-            int64_t batch = 0) {
+            int64_t batch = 0, int box_bytes = 128) {
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
   const cuuint64_t strides[2] = {(cuuint64_t)(ld * sizeof(T)), (cuuint64_t)(rows * ld * sizeof(T))};
-  const cuuint32_t box[3] = {128 / sizeof(T), (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {box_bytes / (cuuint32_t)sizeof(T), (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
   const CUtensorMapDataType type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+  const CUtensorMapSwizzle swizzle =
+      box_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : (box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   return encode_fn()(m, type, batch ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// h: a box is one plane of 128 rows, 128 bytes at most.
+bool encode_h(CUtensorMap* m, const uint16_t* h, int64_t T, int R, int planes) {
+  const Along along(R);
+  const cuuint64_t dims[3] = {(cuuint64_t)R, (cuuint64_t)planes, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)R * 2, (cuuint64_t)planes * R * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)along.bytes / 2, 1, TILE}, es[3] = {1, 1, 1};
+  const CUtensorMapSwizzle swizzle = along.bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                                       : (along.bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<uint16_t*>(h), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T>
@@ -1676,28 +1747,42 @@ cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t run_up(UpArgs& g, cudaStream_t s) {
+cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   using PL = Planes<T>;
   const int64_t b = sizeof(T);
+  const Along along(g.R);
+  if (!encode_fn()) return cudaErrorNotSupported;
   g.steps = (int)ceil_div(g.N, UP_N);
-  const int plane = g.R / 8 * CORE_K<T>, part = 32 * 64 * (int)sizeof(T);
-  g.w_bytes = (PL::P * (g.turned ? g.R * 256 : plane) + 1023) / 1024 * 1024;
-  g.h_bytes = PL::PH * plane;
+  const int part = 32 * 64 * (int)sizeof(T);
+  g.w_bytes = PL::PD * (g.turned ? g.R * 256 : along.plane());
+  g.h_bytes = PL::PH * along.plane();
   const int most = 232448 - (int)sizeof(UpCtl) - 256 - 1024;
   // rings: at least two parts of base, one h, one w; then more parts, w, h
-  const bool tma = encode_fn() && aligned16(g.out, g.N * b) && aligned16(g.base, 0) &&
+  const bool tma = aligned16(g.out, g.N * b) && aligned16(g.base, 0) &&
                    2 * UP_EPI * part + g.h_bytes + g.w_bytes <= most;
-  g.vec = (aligned16(g.w, (g.turned ? g.N : g.r) * b) ? 1 : 0) | (tma ? 2 : 0);
+  const bool vec_w = aligned16(g.w, (g.turned ? g.N : g.r) * b);
+  g.vec = (vec_w ? 4 : 0) | (vec_w && PL::PD == 1 ? 1 : 0) | (tma ? 2 : 0);
   g.slots = g.h_slots = 1;
   g.b_slots = tma ? 2 : 0;
   const int staged = tma ? 0 : UP_EPI * 32 * (STAGED_COLS<T> + 1) * 4;
   auto bytes = [&] {
     return UP_EPI * g.b_slots * part + g.slots * g.w_bytes + g.h_slots * g.h_bytes + staged;
   };
+  // two blocks on an SM where both find room with two slots for w
+  int limit = most, blocks = 1;
+  if (sizeof(T) == 2) {
+    const int half = (228 << 9) - 1024 - (int)sizeof(UpCtl) - 256 - 1024;
+    g.slots = 2;
+    if (bytes() <= half) {
+      limit = half;
+      blocks = 2;
+    }
+    g.slots = 1;
+  }
   auto grow = [&](int& n, int to) {
     while (n < to) {
       ++n;
-      if (bytes() <= most) continue;
+      if (bytes() <= limit) continue;
       --n;
       break;
     }
@@ -1709,20 +1794,35 @@ cudaError_t run_up(UpArgs& g, cudaStream_t s) {
   grow(g.slots, UP_SLOTS);
   const int smem = bytes() + 1024;
   UpMaps maps = {};
-  if (tma && ((g.base && (!encode<T>(&maps.base, g.base, g.N, g.T, g.N, 32) ||
-                          !encode<T>(&maps.rows, g.base, g.N, g.T, g.N, 1))) ||
-              !encode<T>(&maps.out, g.out, g.N, g.T, g.N, 32)))
-    return cudaErrorInvalidValue;
+  bool ok = encode_h(&maps.h, h, g.T, g.R, PL::PH);
+  if (tma && g.base)
+    ok = ok && encode<T>(&maps.base, g.base, g.N, g.T, g.N, 32) && encode<T>(&maps.rows, g.base, g.N, g.T, g.N, 1);
+  if (tma) ok = ok && encode<T>(&maps.out, g.out, g.N, g.T, g.N, 32);
+  if (g.vec & 1)
+    ok = ok && (g.turned ? encode<T>(&maps.w, g.w, g.N, g.r, g.N, g.R, g.L)
+                         : encode<T>(&maps.w, g.w, g.r, g.N, g.r, UP_N, g.L, along.bytes));
+  if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(k_adapters_up<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t items = most_tiles(g.T, g.L, TILE) * g.steps, sms = device_sm_count();
-  e = launch_after_previous(k_adapters_up<T>, dim3((unsigned)(items < sms ? items : sms)), dim3(UP_THREADS),
+  const int64_t items = most_tiles(g.T, g.L, TILE) * g.steps, room = (int64_t)device_sm_count() * blocks;
+  e = launch_after_previous(k_adapters_up<T>, dim3((unsigned)(items < room ? items : room)), dim3(UP_THREADS<T>),
                             smem, s, maps, g);
   note_launch();
   return e;
 }
 
 int round16(int r) { return (r + 15) / 16 * 16; }
+
+// The workspace of one h (of g): its planes, its scaled fp16 rows, their scales.
+size_t room_bytes(int64_t T, int64_t R) { return (size_t)(T * R * (6 + 4) + (T + 3) / 4 * 16); }
+struct Room {
+  uint16_t *h, *h16;
+  float* row_scale;
+};
+Room room_of(void* workspace, int i, int64_t T, int64_t R) {
+  uint16_t* h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + i * room_bytes(T, R));
+  return {h, h + 3 * T * R, reinterpret_cast<float*>(h + 5 * T * R)};
+}
 
 template <typename T>
 cudaError_t adapters(const AdapterArgs& a, cudaStream_t s) {
@@ -1737,24 +1837,21 @@ cudaError_t adapters(const AdapterArgs& a, cudaStream_t s) {
   g.L = a.L;
   g.r = a.r;
   g.R = round16(a.r);
-  g.prob[0] = {a.x, a.ld, a.K, a.a, static_cast<uint16_t*>(a.workspace), 0,
+  const Room room = room_of(a.workspace, 0, a.T, g.R);
+  constexpr bool F16 = Planes<T>::FD == 0;
+  g.prob[0] = {a.x, a.ld, a.K, a.a, F16 ? nullptr : room.h, F16 ? room.h16 : nullptr, F16 ? room.row_scale : nullptr, 0,
                (aligned16(a.x, a.ld * b) && a.K % 8 == 0 ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0)};
   const cudaError_t e = run_down<T>(g, 1, s);
   if (e != cudaSuccess) return e;
-  UpArgs up = {g.prob[0].h, a.b, a.base, a.out, a.offsets, a.order, a.T, a.N, a.L, a.r, g.R, 0, 0, 0, 0, 0, 0, 0, 0};
-  return run_up<T>(up, s);
-}
-
-size_t planes_bytes(int64_t T, int64_t r) {  // of h or g, whatever their type
-  return (size_t)(3 * T * ((r + 15) / 16 * 16) * 2);
+  UpArgs up = {g.prob[0].row_scale, a.b, a.base, a.out, a.offsets, a.order, a.T, a.N, a.L, a.r, g.R};
+  return run_up<T>(up, F16 ? room.h16 : room.h, s);
 }
 
 template <typename T>
 cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
   using PL = Planes<T>;
   note_kernel_name("k_adapters_grad");
-  uint16_t* h = static_cast<uint16_t*>(a.workspace);
-  uint16_t* d = h + planes_bytes(a.T, a.r) / 2;
+  constexpr bool F16 = PL::FD == 0;
   DownArgs g = {};
   g.scale = a.scale;
   g.offsets = a.offsets;
@@ -1764,17 +1861,21 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
   g.r = a.r;
   g.R = round16(a.r);
   const int64_t size = sizeof(T);
+  const Room h = room_of(a.workspace, 0, a.T, g.R), d = room_of(a.workspace, 1, a.T, g.R);
+  const bool scaled = F16 && a.grad_x;
   int problems = 0;
   if (a.grad_x || a.grad_a)  // g = scale * grad b
-    g.prob[problems++] = {a.grad, a.N, a.N, a.b, d, 1,
+    g.prob[problems++] = {a.grad, a.N, a.N, a.b, F16 && !a.grad_a ? nullptr : d.h, scaled ? d.h16 : nullptr,
+                          scaled ? d.row_scale : nullptr, 1,
                           (aligned16(a.grad, a.N * size) ? 1 : 0) | (aligned16(a.b, a.r * size) ? 2 : 0)};
   if (a.grad_b)  // h = scale * x a^T
-    g.prob[problems++] = {a.x, a.K, a.K, a.a, h, 0,
+    g.prob[problems++] = {a.x, a.K, a.K, a.a, h.h, nullptr, nullptr, 0,
                           (aligned16(a.x, a.K * size) ? 1 : 0) | (aligned16(a.a, a.K * size) ? 2 : 0)};
   cudaError_t e = run_down<T>(g, problems, s);
   if (e == cudaSuccess && a.grad_x) {
-    UpArgs up = {d, a.a, a.base, a.grad_x, a.offsets, a.order, a.T, a.K, a.L, a.r, g.R, 0, 1, 0, 0, 0, 0, 0, 0};
-    e = run_up<T>(up, s);
+    UpArgs up = {scaled ? d.row_scale : nullptr, a.a, a.base, a.grad_x, a.offsets, a.order, a.T, a.K, a.L, a.r, g.R};
+    up.turned = 1;
+    e = run_up<T>(up, scaled ? d.h16 : d.h, s);
   }
   if (e != cudaSuccess || (!a.grad_a && !a.grad_b)) return e;
   GradArgs w = {};
@@ -1798,8 +1899,8 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
     chunks = chunks > n ? chunks : n;
     all += n;
   };
-  if (a.grad_a) add(a.x, a.K, d, a.grad_a, 0);
-  if (a.grad_b) add(a.grad, a.N, h, a.grad_b, 1);
+  if (a.grad_a) add(a.x, a.K, d.h, a.grad_a, 0);
+  if (a.grad_b) add(a.grad, a.N, h.h, a.grad_b, 1);
   // about three blocks per SM, of four stages of rows on average at least
   int64_t want = 3 * (int64_t)device_sm_count() / (all * a.L);
   const int64_t most = a.T / a.L / (4 * GRAD_ROWS);
@@ -1842,9 +1943,11 @@ cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t s) {
 }
 
 size_t adapters_bytes(int64_t T, int64_t L, int64_t r) {
-  return T <= 64 ? 0 : planes_bytes(T, r);
+  return T <= 64 ? 0 : room_bytes(T, round16((int)r));
 }
-size_t adapters_backward_bytes(int64_t T, int64_t r) { return 2 * planes_bytes(T, r); }
+size_t adapters_backward_bytes(int64_t T, int64_t r) {
+  return 2 * room_bytes(T, round16((int)r));
+}
 
 cudaError_t launch_adapters_backward(const AdapterGradArgs& a, int dtype, cudaStream_t s) {
   if (dtype == IMC_F32) return backward<float>(a, s);
