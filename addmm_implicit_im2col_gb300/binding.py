@@ -84,7 +84,9 @@ SIGNATURES = {
     "moe_combine": (_int, [_vp, _int, _vp, _i64, _i64, _i64, _vp, _vp]),
     "moe_combine_f32": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _int, _vp]),
     "moe_combine_backward": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
-    "moe_balance": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp]),
+    "moe_balance_workspace_bytes": (ctypes.c_size_t, [_i64] * 3),
+    "moe_balance": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp,
+                           ctypes.c_size_t, _vp]),
     "moe_balance_backward": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _vp, _i64, _int, _vp, _vp,
                                     _i64, _vp, _int, _dbl, _vp, _vp]),
     "lowrank_linear_workspace_bytes": (ctypes.c_size_t, [_i64] * 3),
@@ -302,10 +304,14 @@ def moe_combine_backward(grad, y, dtype, weights, T, k, N, grad_y, grad_weights,
                                        stream)
 
 
+def moe_balance_workspace_bytes(T, S, E) -> int:
+    return int(load().moe_balance_workspace_bytes(T, S, E))
+
+
 def moe_balance(logits, dtype, T, E, row_stride, experts, k, score, offsets, S, loss, counts,
-                stream) -> int:
+                workspace, workspace_bytes, stream) -> int:
     return load().moe_balance(logits, dtype, T, E, row_stride, experts, k, score, offsets, S, loss,
-                              counts, stream)
+                              counts, workspace, workspace_bytes, stream)
 
 
 def moe_balance_backward(grad_loss, logits, dtype, T, E, row_stride, experts, k, score, counts,
@@ -595,6 +601,7 @@ _size = functools.lru_cache(maxsize=4096)(mxfp4_bytes)
 _linear_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_workspace_bytes)
 _layout_size = functools.lru_cache(maxsize=4096)(moe_layout_size)
 _experts_size = functools.lru_cache(maxsize=4096)(mxfp4_experts_linear_workspace_bytes)
+_balance_size = functools.lru_cache(maxsize=4096)(moe_balance_workspace_bytes)
 _lowrank_size = functools.lru_cache(maxsize=4096)(lowrank_linear_workspace_bytes)
 _lowrank_back_size = functools.lru_cache(maxsize=4096)(lowrank_linear_backward_workspace_bytes)
 _backward_size = functools.lru_cache(maxsize=4096)(mxfp4_linear_backward_workspace_bytes)
@@ -1050,8 +1057,11 @@ def balance_loss(logits, experts, *, score="softmax", offsets=None):
     device = logits.device
     loss = _torch.empty((S,), dtype=_torch.float32, device=device)
     counts = _torch.empty((S, E), dtype=_torch.int32, device=device)
+    nbytes = _balance_size(T, S, E)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device) if nbytes else None
     rc = _calls.moe_balance(logits.data_ptr(), dt, T, E, ld, experts.data_ptr(), k, score,
-                          _ptr(offsets), S, loss.data_ptr(), counts.data_ptr(), _stream_of(logits))
+                          _ptr(offsets), S, loss.data_ptr(), counts.data_ptr(), _ptr(ws), nbytes,
+                          _stream_of(logits))
     if rc:
         raise ImcError(rc, "moe_balance")
     return loss, counts

@@ -55,8 +55,9 @@ struct BalanceArgs {
   int renorm;
   float scale;
   void* grad;              // [T, E]
-  void* workspace;
+  void* workspace;         // balance_bytes
 };
+size_t balance_bytes(int64_t T, int64_t S, int64_t E);
 cudaError_t launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_balance_backward(const BalanceArgs& a, int dtype, cudaStream_t s);
 

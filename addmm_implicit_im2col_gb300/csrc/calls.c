@@ -82,8 +82,8 @@ ENTRY(lowrank_linear, "pilpppppplllllplp", P(0), I(1), L(2), P(3), P(4), P(5), P
       L(10), L(11), L(12), L(13), P(14), (size_t)L(15), P(16))
 ENTRY(lowrank_linear_backward, "ppppipppppplllllplp", P(0), P(1), P(2), P(3), I(4), P(5), P(6), P(7),
       P(8), P(9), P(10), L(11), L(12), L(13), L(14), L(15), P(16), (size_t)L(17), P(18))
-ENTRY(moe_balance, "pilllpliplppp", P(0), I(1), L(2), L(3), L(4), P(5), L(6), I(7), P(8), L(9), P(10),
-      P(11), P(12))
+ENTRY(moe_balance, "pilllpliplppplp", P(0), I(1), L(2), L(3), L(4), P(5), L(6), I(7), P(8), L(9), P(10),
+      P(11), P(12), (size_t)L(13), P(14))
 ENTRY(moe_balance_backward, "ppilllplipplpidpp", P(0), P(1), I(2), L(3), L(4), L(5), P(6), L(7), I(8),
       P(9), P(10), L(11), P(12), I(13), v[14].d, P(15), P(16))
 

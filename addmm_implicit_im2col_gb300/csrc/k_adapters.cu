@@ -780,6 +780,7 @@ struct UpArgs {
   const int32_t *offsets, *order;
   int64_t T, N;
   int L, r, R, steps, turned, vec;  // vec: 1 w, 2 base and out, by TMA
+  int group;                                      // items that a block takes at once
   int slots, h_slots, b_slots, w_bytes, h_bytes;  // of the rings of w, h and base; bytes of one
 };
 struct UpMaps {
@@ -802,21 +803,35 @@ struct UpCtl {
   int before[kAdapters + 2], first[kAdapters + 2];  // tiles before a bucket, its first row
 };
 
-// An item: 128 outputs (from `step` on) of the tile's rows.  Walked by counting: a 64-bit
-// division takes longer than an item's other instructions.
-struct Item {
-  int tile, step;
-  __device__ __forceinline__ void at(int64_t item, int steps) {
-    tile = (int)(item / steps);
-    step = (int)(item - (int64_t)tile * steps);
+// A block's items, each 128 outputs (`step`) of a tile's rows: runs of `group` items, the
+// blocks' runs interleaved, so that what all blocks read and write at one time lies
+// together.  Walked by counting: a 64-bit division takes longer than an item's other work.
+struct Walk {
+  int tile, step, in, steps, group, jump_tiles, jump_steps;
+  int64_t left;  // items from this one on
+  __device__ __forceinline__ Walk(int64_t items, int steps_, int group_) : in(0), steps(steps_), group(group_) {
+    const int64_t runs = (items + group - 1) / group, G = gridDim.x, b = blockIdx.x;
+    left = b < runs ? (runs - b + G - 1) / G * group : 0;
+    if (left && (runs - 1) % G == b) left -= runs * group - items;  // the last run may be short
+    const int64_t first = b * group, jump = (G - 1) * group + 1;
+    tile = (int)(first / steps);
+    step = (int)(first - (int64_t)tile * steps);
+    jump_tiles = (int)(jump / steps);
+    jump_steps = (int)(jump - (int64_t)jump_tiles * steps);
   }
-  __device__ __forceinline__ void next(int steps) {
-    if (++step == steps) {
-      step = 0;
+  __device__ __forceinline__ void next() {
+    --left;
+    const bool jump = ++in == group;
+    if (jump) in = 0;
+    tile += jump ? jump_tiles : 0;
+    step += jump ? jump_steps : 1;
+    if (step >= steps) {
+      step -= steps;
       ++tile;
     }
   }
 };
+
 // Tile t of the counted buckets.
 __device__ __forceinline__ RowTile tile_of(const UpCtl& ctl, int B, int t) {
   int low = 0, high = B;  // before[low] <= t < before[high]
@@ -920,7 +935,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
   const uint32_t tmem = ctl.tmem_base;
   ptx::griddep_launch();
   const int64_t items = (int64_t)ctl.before[B] * g.steps;
-  const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  const Walk walk(items, g.steps, g.group);
   constexpr int SB = 32 * 64 * (int)sizeof(T);  // bytes of a warp's part of an item
   uint8_t* ws = sm + UP_EPI * g.b_slots * SB;
   uint8_t* hs = ws + g.slots * g.w_bytes;
@@ -935,10 +950,8 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     const int row_by = LT / ru, ju_by = LT - row_by * ru;  // from one of a thread's units to its next
     int last = -1;
     Slot hslot, wslot;
-    Item item;
-    item.at(i0, g.steps);
     RowTile t = {0, 0, 0};
-    for (int64_t it = i0; it < i1; ++it, item.next(g.steps)) {
+    for (Walk item = walk; item.left > 0; item.next()) {
       const int64_t n0 = (int64_t)item.step * UP_N;
       const bool other = item.tile != last;
       if (other) t = tile_of(ctl, B, item.tile);
@@ -1022,14 +1035,13 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     // ---------------------------------------------------------------- MMAs
     int last = -1, hb = 0;
     Slot hslot, wslot, aslot;
-    Item item;
-    item.at(i0, g.steps);
     bool product = false;
     const uint32_t id = ptx::idesc_f16(PL::FD, TILE, UP_N, false, g.turned);
-    for (int64_t it = i0; it < i1; ++it, item.next(g.steps)) {
+    for (Walk item = walk; item.left > 0;) {
       const bool other = item.tile != last;
       if (other) product = tile_of(ctl, B, item.tile).l < g.L;
       last = item.tile;
+      item.next();
       if (!product) continue;
       if (other) {
         hb = hslot.i;
@@ -1060,7 +1072,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
           }
         ptx::mma_commit(&ctl.wempty[slot]);
         ptx::mma_commit(&ctl.accf[buf]);
-        if (it + 1 == i1 || item.step + 1 == g.steps) ptx::mma_commit(&ctl.hempty[hb]);
+        if (item.left == 0 || item.tile != last) ptx::mma_commit(&ctl.hempty[hb]);
       }
       __syncwarp();
     }
@@ -1076,7 +1088,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       bool run = false;  // the warp's rows lie one after the other
       int64_t col = 0;
     };
-    auto place = [&](Place& q, const Item& item) {
+    auto place = [&](Place& q, const Walk& item) {
       q.col = (int64_t)item.step * UP_N + half * 64;
       if (item.tile == q.tile) return;
       q.tile = item.tile;
@@ -1090,13 +1102,11 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       q.run = __all_sync(kAll, lane >= q.rows || q.row == first + lane);
     };
     Place ahead, now;
-    Item item, next;
+    Walk item = walk, next = walk;
     Slot nslot;
-    item.at(i0, g.steps);
-    next = item;
     auto load = [&] {  // base of the next item to its place in the ring
       place(ahead, next);
-      next.next(g.steps);
+      next.next();
       const int slot = nslot.i;
       nslot.next(NS);
       if (!base || ahead.rows == 0 || ahead.col >= g.N) return;
@@ -1126,10 +1136,9 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     };
     uint32_t phases = 0;  // of the ring's barriers
     if (wide)
-      for (int64_t it = i0; it < i1 && it < i0 + NS - 1; ++it) load();
-    int64_t it = i0;
+      for (int i = 0; i < NS - 1 && next.left > 0; ++i) load();
     Slot slot_of;
-    for (; it < i1; ++it, item.next(g.steps), slot_of.next(NS)) {
+    for (; item.left > 0; item.next(), slot_of.next(NS)) {
       place(now, item);
       const bool product = now.l < g.L, live = now.rows > 0 && now.col < g.N;
       const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + (n & 1) * UP_N + half * 64;
@@ -1146,6 +1155,10 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
           ptx::tc_fence_after();
           scale_it();
         }
+        // the item before this one has been stored: its place takes the next one to load
+        if (lane == 0) ptx::bulk_wait_read0();
+        __syncwarp();
+        if (next.left > 0) load();
         if (live && (product || !base)) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -1187,21 +1200,23 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
             if (lane == 0)
               for (int b = 0; b < 64 / BOX && now.col + b * BOX < g.N; ++b)
                 ptx::tma_store_2d(&maps.out, mine + b * 4096, (int)now.col + b * BOX, now.row);
-          } else if (lane < now.rows) {
-            T* to = out + now.row * g.N + now.col;
-            const int units = (int)(g.N - now.col < 64 ? g.N - now.col : 64) * (int)sizeof(T) / 16;
-            for (int i = 0; i < units; ++i)
-              reinterpret_cast<uint4*>(to)[i] = *reinterpret_cast<const uint4*>(
-                  mine + (i >> 3) * 4096 + lane * 128 + (((i & 7) ^ (lane & 7)) << 4));
+          } else {  // four rows at a time, eight lanes each
+            const int64_t width = g.N - now.col < 64 ? g.N - now.col : 64;
+#pragma unroll
+            for (int b = 0; b < 64 / BOX; ++b)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const int from = i + (lane >> 3), unit = lane & 7, c = b * BOX + unit * (16 / (int)sizeof(T));
+                const int64_t to_row = __shfl_sync(kAll, now.row, from);
+                if (from < now.rows && c < width)
+                  *reinterpret_cast<uint4*>(out + to_row * g.N + now.col + c) = *reinterpret_cast<const uint4*>(
+                      mine + b * 4096 + from * 128 + ((unit ^ (from & 7)) << 4));
+              }
+            ptx::fence_proxy_async_smem();  // read before TMA writes there again
+            __syncwarp();
           }
         }
-        if (lane == 0) {
-          ptx::bulk_commit();
-          ptx::bulk_wait_read1();  // the item before this one has been stored
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (it + NS - 1 < i1) load();
+        if (lane == 0) ptx::bulk_commit();
       } else {
         if (product) {
           if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
@@ -1241,7 +1256,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     }
     if (wide) {
       if (ctl.abort) {  // the copies under way land before the block ends
-        for (int64_t i = it; i < i1 && i < it + NS - 1 && base; ++i, item.next(g.steps), slot_of.next(NS)) {
+        for (; item.left > next.left && base; item.next(), slot_of.next(NS)) {
           place(now, item);
           if (now.rows == 0 || now.col >= g.N) continue;
           tc::drain_wait(&ctl.bfull[warp][slot_of.i], phases >> slot_of.i & 1);
@@ -1753,6 +1768,7 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   const Along along(g.R);
   if (!encode_fn()) return cudaErrorNotSupported;
   g.steps = (int)ceil_div(g.N, UP_N);
+  g.group = 2;
   const int part = 32 * 64 * (int)sizeof(T);
   g.w_bytes = PL::PD * (g.turned ? g.R * 256 : along.plane());
   g.h_bytes = PL::PH * along.plane();

@@ -17,41 +17,32 @@ constexpr int kFlush = 64;  // tokens whose scores a lane sums in fp32
 
 __device__ __forceinline__ int64_t clamped(int64_t v, int64_t T) { return v < 0 ? 0 : (v > T ? T : v); }
 
-// Divides the scores of a token by their sum (sigmoid; softmax scores have the sum 1).
-// Returns 1 / sum.
-template <int VPT>
-__device__ __forceinline__ float normalise(float (&s)[VPT]) {
-  float sum = 0.0f;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) sum += s[j];
-  sum = warp_sum(sum);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) s[j] *= inv;
-  return inv;
+// The sequence of token t: the number of offsets that are at most t, less one (a warp's
+// lanes look at 32 places at once).
+__device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int low = 0, n = S + 1;
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const bool in = lane * step < n;
+    const int c = __popc(__ballot_sync(kAll, in && __ldg(offsets + low + lane * step) <= t));
+    if (c == 0) break;
+    const int past = (c - 1) * step + 1;
+    low += past;
+    n = min(step - 1, n - past);
+  }
+  return low - 1;
 }
 
-// One cluster of CTAs per sequence, a warp per token.  A lane sums its experts' scores
-// of kFlush tokens in fp32, then in 64 bits: an error of a few fp32 roundings however
-// long the sequence is.  Every sum has a fixed order; the counts are whole numbers.
+// The tokens first, first + step, ... before `last`, two of them at a time (their loads and
+// sums overlap): their scores are added to mine [E], their slots counted in count [E].  A
+// lane sums its experts' scores of kFlush tokens in fp32, then in 64 bits: an error of a
+// few fp32 roundings however long the sequence is.
 template <int VPT, typename T>
-__global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a, const int log_ctas) {
-  extern __shared__ double sm_sums[];  // [warp][E], then (CTA 0) [CTA][E]
-  const int E = a.E, C = 1 << log_ctas, rank = (int)ptx::cluster_rank();
-  double* gathered = sm_sums + kWarps * E;
-  int32_t* count = reinterpret_cast<int32_t*>(gathered + C * E);  // [E], then (CTA 0) [CTA][E]
-  int32_t* counts = count + E;
-  __shared__ double loss[kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, s = blockIdx.x >> log_ctas;
-  ptx::cluster_arrive();
-  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) sm_sums[i] = 0.0;
-  for (int i = threadIdx.x; i < E; i += kThreads) count[i] = 0;
-  __syncthreads();
-  ptx::griddep_wait();
-  ptx::griddep_launch();
-  const int64_t t0 = a.offsets ? clamped(a.offsets[s], a.T) : 0;
-  const int64_t t1 = a.offsets ? clamped(a.offsets[s + 1], a.T) : a.T;
-  double* mine = sm_sums + warp * E;
+__device__ __forceinline__ void add_tokens(const BalanceArgs& a, int64_t first, int64_t last, int64_t step,
+                                           double* mine, int32_t* count) {
+  constexpr int U = VPT <= 8 ? 2 : 1;
+  const int lane = threadIdx.x & 31, E = a.E;
   float acc[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) acc[j] = 0.0f;
@@ -63,31 +54,53 @@ __global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a, const
     }
   };
   int held = 0;
-  for (int64_t t = t0 + rank * kWarps + warp; t < t1; t += (int64_t)C * kWarps) {
-    if (lane < a.k) {
-      const int e = __ldg(a.experts + t * a.k + lane);
-      if (e >= 0 && e < E) atomicAdd(count + e, 1);
-    }
-    float v[VPT];
-    scores<VPT, T>(static_cast<const T*>(a.logits) + t * a.ld, E, a.sigmoid, v);
-    if (a.sigmoid) normalise<VPT>(v);
+  for (int64_t t0 = first; t0 < last; t0 += U * step) {
+    float v[U][VPT];
+    int e[U];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) acc[j] += v[j];
-    if (++held == kFlush) {
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * step;
+      const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+      e[u] = t < last && lane < a.k ? __ldg(a.experts + t * a.k + lane) : -1;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) v[u][j] = t < last && lane + 32 * j < E ? to_f32<T>(row[lane + 32 * j]) : -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (e[u] >= 0 && e[u] < E) atomicAdd(count + e[u], 1);
+      scores_of<VPT>(a.sigmoid, v[u]);
+      if (a.sigmoid) {  // over their sum
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) sum += v[u][j];
+        sum = warp_sum(sum);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) v[u][j] *= inv;
+      }
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) acc[j] += v[u][j];  // (no token: scores of 0)
+    }
+    held += U;
+    if (held >= kFlush) {
       flush();
       held = 0;
     }
   }
   flush();
-  __syncthreads();
-  ptx::cluster_wait();
+}
+
+// What a cluster's CTAs have summed for sequence s (sums and counts [E] of each, in its
+// shared memory), in the order of the CTAs: counts and loss, by CTA 0.  All threads of the
+// cluster; n tokens.
+__device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, int C, int rank, const double* sums,
+                                       const int32_t* count, double* gathered, int32_t* counts) {
+  __shared__ double loss[kWarps];
+  const int E = a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < E; e += kThreads) {
-    double sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += sm_sums[w * E + e];
     const uint32_t at = ptx::cluster_addr(gathered + rank * E + e, 0);
-    ptx::st_cluster(at, (uint32_t)__double2loint(sum));
-    ptx::st_cluster(at + 4, (uint32_t)__double2hiint(sum));
+    ptx::st_cluster(at, (uint32_t)__double2loint(sums[e]));
+    ptx::st_cluster(at + 4, (uint32_t)__double2hiint(sums[e]));
     ptx::st_cluster(ptx::cluster_addr(counts + rank * E + e, 0), (uint32_t)count[e]);
   }
   ptx::cluster_sync();
@@ -111,26 +124,115 @@ __global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a, const
     double sum = 0.0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += loss[w];
-    const double n = (double)(t1 - t0);
-    a.loss[s] = t1 > t0 ? (float)(sum * E / (a.k * n * n)) : 0.0f;
+    a.loss[s] = n > 0 ? (float)(sum * E / ((double)a.k * n * n)) : 0.0f;
   }
 }
 
-// The sequence of token t: the number of offsets that are at most t, less one (a warp's
-// lanes look at 32 places at once).
-__device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_t t) {
-  const int lane = threadIdx.x & 31;
-  int low = 0, n = S + 1;
-  while (n > 0) {
-    const int step = (n + 31) / 32;
-    const bool in = lane * step < n;
-    const int c = __popc(__ballot_sync(kAll, in && __ldg(offsets + low + lane * step) <= t));
-    if (c == 0) break;
-    const int past = (c - 1) * step + 1;
-    low += past;
-    n = min(step - 1, n - past);
+// Sums of the block's warps [warp][E], into the first one's place.
+__device__ __forceinline__ void over_warps(double* sums, int E) {
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += sums[w * E + e];
+    sums[e] = sum;
   }
-  return low - 1;
+}
+
+// One cluster of CTAs per sequence.  Every sum has a fixed order; counts are whole numbers.
+template <int VPT, typename T>
+__global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a, const int log_ctas) {
+  extern __shared__ double sm_sums[];  // [warp][E], then (CTA 0) [CTA][E]
+  const int E = a.E, C = 1 << log_ctas, rank = (int)ptx::cluster_rank();
+  double* gathered = sm_sums + kWarps * E;
+  int32_t* count = reinterpret_cast<int32_t*>(gathered + C * E);  // [E], then (CTA 0) [CTA][E]
+  const int warp = threadIdx.x >> 5, s = blockIdx.x >> log_ctas;
+  ptx::cluster_arrive();  // this CTA runs: its shared memory may be written
+  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) sm_sums[i] = 0.0;
+  for (int i = threadIdx.x; i < E; i += kThreads) count[i] = 0;
+  __syncthreads();
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int64_t t0 = a.offsets ? clamped(a.offsets[s], a.T) : 0;
+  const int64_t t1 = a.offsets ? clamped(a.offsets[s + 1], a.T) : a.T;
+  add_tokens<VPT, T>(a, t0 + rank * kWarps + warp, t1, C * kWarps, sm_sums + warp * E, count);
+  __syncthreads();
+  over_warps(sm_sums, E);
+  ptx::cluster_wait();
+  finish(a, s, t1 - t0, C, rank, sm_sums, count, gathered, count + E);
+}
+
+// Many tokens: a CTA for each `chunk` of them.  Where chunk c and sequence s meet, their
+// sums and counts go to row c + s of the workspace; along the tokens c or s grows from one
+// meeting to the next, so a row is written once.
+template <int VPT, typename T>
+__global__ void __launch_bounds__(kThreads) k_balance_chunks(const BalanceArgs a, const int chunk) {
+  extern __shared__ double sm_sums[];  // [warp][E]
+  const int E = a.E, warp = threadIdx.x >> 5;
+  int32_t* count = reinterpret_cast<int32_t*>(sm_sums + kWarps * E);
+  const int64_t rows = (int64_t)gridDim.x + a.S;
+  double* sums = static_cast<double*>(a.workspace);
+  int32_t* counts = reinterpret_cast<int32_t*>(sums + rows * E);
+  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) sm_sums[i] = 0.0;
+  for (int i = threadIdx.x; i < E; i += kThreads) count[i] = 0;
+  __syncthreads();
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int64_t end = (int64_t)(blockIdx.x + 1) * chunk < a.T ? (int64_t)(blockIdx.x + 1) * chunk : a.T;
+  int64_t t = (int64_t)blockIdx.x * chunk;
+  if (a.offsets && t < clamped(a.offsets[0], a.T)) t = clamped(a.offsets[0], a.T);
+  while (t < end) {
+    const int s = a.offsets ? sequence_of(a.offsets, a.S, t) : 0;
+    if (s < 0 || s >= a.S) break;  // behind the last sequence
+    int64_t last = a.offsets ? clamped(a.offsets[s + 1], a.T) : a.T;
+    last = last < end ? last : end;
+    if (last <= t) break;  // (offsets that do not ascend)
+    add_tokens<VPT, T>(a, t + warp, last, kWarps, sm_sums + warp * E, count);
+    __syncthreads();
+    over_warps(sm_sums, E);
+    const int64_t row = blockIdx.x + (int64_t)s;
+    for (int e = threadIdx.x; e < E; e += kThreads) {  // (each thread's own sums)
+      sums[row * E + e] = sm_sums[e];
+      counts[row * E + e] = count[e];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sm_sums[w * E + e] = 0.0;
+      count[e] = 0;
+    }
+    __syncthreads();
+    t = last;
+  }
+}
+// ... and a cluster per sequence that joins its rows.
+__global__ void __launch_bounds__(kThreads)
+    k_balance_join(const BalanceArgs a, const int chunk, const int chunks, const int log_ctas) {
+  extern __shared__ double sm_sums[];  // [E], then (CTA 0) [CTA][E]
+  const int E = a.E, C = 1 << log_ctas, rank = (int)ptx::cluster_rank(), s = blockIdx.x >> log_ctas;
+  double* gathered = sm_sums + E;
+  int32_t* count = reinterpret_cast<int32_t*>(gathered + C * E);
+  const int64_t rows = (int64_t)chunks + a.S;
+  const double* sums = static_cast<const double*>(a.workspace);
+  const int32_t* counts = reinterpret_cast<const int32_t*>(sums + rows * E);
+  ptx::cluster_arrive();
+  const int64_t t0 = a.offsets ? clamped(a.offsets[s], a.T) : 0;
+  const int64_t t1 = a.offsets ? clamped(a.offsets[s + 1], a.T) : a.T;
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int c0 = (int)(t0 / chunk), c1 = t1 > t0 ? (int)((t1 - 1) / chunk) + 1 : c0;
+  const int per = (c1 - c0 + C - 1) >> log_ctas;
+  const int from = min(c0 + rank * per, c1), to = min(from + per, c1);
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    double sum = 0.0;
+    int32_t n = 0;
+#pragma unroll 8
+    for (int c = from; c < to; ++c) {
+      const int64_t row = (int64_t)c + s;
+      sum += sums[row * E + e];
+      n += counts[row * E + e];
+    }
+    sm_sums[e] = sum;
+    count[e] = n;
+  }
+  ptx::cluster_wait();
+  finish(a, s, t1 - t0, C, rank, sm_sums, count, gathered, count + E);
 }
 
 // A warp per token.  With u_e = grad_loss[s] * E / (k n^2) * c[s,e], the counts constant,
@@ -231,15 +333,12 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
 }
 
 // ------------------------------------------------------------------- host
-template <int VPT, typename T>
-cudaError_t forward(const BalanceArgs& a, cudaStream_t s) {
-  const int log_ctas = 3;
-  const size_t smem = (size_t)a.E * (kWarps + (1 << log_ctas)) * 8 + (size_t)a.E * (1 + (1 << log_ctas)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_balance<VPT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), int64_t grid, int ctas, size_t smem, cudaStream_t s, Args... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.S << log_ctas);
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -247,14 +346,39 @@ cudaError_t forward(const BalanceArgs& a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1u << log_ctas;
+  attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, k_balance<VPT, T>, a, log_ctas);
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, args...);
   note_launch();
   return e;
+}
+
+// Tokens of a CTA of the form for many of them (whatever the GPU: the workspace's size
+// depends on it): 256 to 511 CTAs, of sixteen tokens at least.
+int64_t chunk_of(int64_t T) {
+  int64_t chunk = 16;
+  while (ceil_div(T, chunk) > 511) chunk *= 2;
+  return chunk;
+}
+bool many(int64_t T, int64_t S) { return T > 2048 && S <= 1024; }
+
+template <int VPT, typename T>
+cudaError_t forward(const BalanceArgs& a, cudaStream_t s) {
+  const size_t E = (size_t)a.E;
+  if (!many(a.T, a.S)) {
+    const int64_t mean = a.T / a.S;  // tokens of a sequence
+    const int log_ctas = mean >= 64 ? 3 : (mean >= 32 ? 2 : (mean >= 16 ? 1 : 0)), C = 1 << log_ctas;
+    return launch(k_balance<VPT, T>, (int64_t)a.S << log_ctas, C, E * (kWarps + C) * 8 + E * (1 + C) * 4, s, a,
+                  log_ctas);
+  }
+  const int chunk = (int)chunk_of(a.T), chunks = (int)ceil_div(a.T, chunk);
+  const cudaError_t e = launch(k_balance_chunks<VPT, T>, chunks, 1, E * (kWarps * 8 + 4), s, a, chunk);
+  if (e != cudaSuccess) return e;
+  const int log_ctas = chunks / a.S >= 16 ? 3 : 0, C = 1 << log_ctas;
+  return launch(k_balance_join, (int64_t)a.S << log_ctas, C, E * (1 + C) * 12, s, a, chunk, chunks, log_ctas);
 }
 
 template <int VPT, typename T>
@@ -284,6 +408,10 @@ cudaError_t of_type(const BalanceArgs& a, int dtype, bool back, cudaStream_t s) 
 }
 
 }  // namespace
+
+size_t balance_bytes(int64_t T, int64_t S, int64_t E) {
+  return many(T, S) ? (size_t)((ceil_div(T, chunk_of(T)) + S) * E * 12) : 0;
+}
 
 cudaError_t launch_balance(const BalanceArgs& a, int dtype, cudaStream_t s) {
   note_kernel_name("k_balance");

@@ -789,9 +789,16 @@ int balance_args(BalanceArgs& p, const void* logits, int dtype, int64_t T, int64
 
 extern "C" {
 
+size_t moe_balance_workspace_bytes(int64_t T, int64_t S, int64_t E) {
+  if (T < 0 || T > kMaxRows || S < 1 || S > kMaxRows || E < 1 || E > kMaxExperts || S * E > kMaxDim)
+    return 0;
+  return balance_bytes(T, S, E);
+}
+
 int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t row_stride,
                 const int32_t* experts, int64_t k, int score, const int32_t* offsets, int64_t S,
-                float* loss, int32_t* counts, void* stream) {
+                float* loss, int32_t* counts, void* workspace, size_t workspace_bytes,
+                void* stream) {
   BalanceArgs p;
   const int rc = balance_args(p, logits, dtype, T, E, row_stride, experts, k, score, offsets, S);
   if (rc != IMC_OK) return rc;
@@ -804,11 +811,22 @@ int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t row
   const Range out[2] = {{loss, (uint64_t)S * 4}, {counts, (uint64_t)(S * E) * 4}};
   if (overlaps_any(out[0], in, 3) || overlaps_any(out[1], in, 3) || overlaps_any(out[1], out, 1))
     return IMC_ERR_ALIAS;
+  const size_t need = moe_balance_workspace_bytes(T, S, E);
+  if (need) {
+    const int ws = check_workspace(workspace, workspace_bytes, need);
+    if (ws != IMC_OK) return ws;
+    const Range room = {workspace, need};
+    if (workspace && (overlaps_any(room, in, 3) || overlaps_any(room, out, 2))) return IMC_ERR_ALIAS;
+  }
   const int dev = require_device();
   if (dev != IMC_OK) return dev;
+  cudaStream_t s = (cudaStream_t)stream;
+  Scratch sc(s);
+  if (sc.take(workspace, need) != IMC_OK) return IMC_ERR_CUDA;
+  p.workspace = sc.p;
   p.loss = loss;
   p.counts = counts;
-  return finish_call(launch_balance(p, dtype, (cudaStream_t)stream), IMC_KERNEL_EXPERTS);
+  return finish_call(sc.give(launch_balance(p, dtype, s)), IMC_KERNEL_EXPERTS);
 }
 
 int moe_balance_backward(const float* grad_loss, const void* logits, int dtype, int64_t T,

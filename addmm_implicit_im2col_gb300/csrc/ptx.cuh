@@ -182,15 +182,6 @@ __device__ __forceinline__ void ld_global_v8(uint32_t (&w)[8], const void* p) {
                : "l"(p));
 }
 
-// The same of memory that this kernel writes.
-__device__ __forceinline__ void ld_global_v8_rw(uint32_t (&w)[8], const void* p) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
-                 "=r"(w[7])
-               : "l"(p)
-               : "memory");
-}
-
 // ----------------------------------------------------------- async copies
 // Sixteen bytes from global to shared memory, both 16-byte aligned; zeros where !in (from
 // is not read then).  Counted in the thread's groups.

@@ -20,16 +20,10 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Scores of one token: lane l holds experts l, l + 32, ... (VPT of them).
-// softmax: exp(x - max) / sum; a row of -inf alone has scores 0.
-template <int VPT, typename T>
-__device__ __forceinline__ void scores(const T* row, int E, int sigmoid, float (&s)[VPT]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int e = lane + 32 * j;
-    s[j] = e < E ? to_f32<T>(row[e]) : -INFINITY;
-  }
+// Scores of one token from its logits (-inf where there is no expert): lane l holds experts
+// l, l + 32, ... (VPT of them).  softmax: exp(x - max) / sum; a row of -inf alone has scores 0.
+template <int VPT>
+__device__ __forceinline__ void scores_of(int sigmoid, float (&s)[VPT]) {
   if (sigmoid) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) s[j] = 1.0f / (1.0f + expf(-s[j]));
@@ -49,6 +43,16 @@ __device__ __forceinline__ void scores(const T* row, int E, int sigmoid, float (
 #pragma unroll
     for (int j = 0; j < VPT; ++j) s[j] *= inv;
   }
+}
+template <int VPT, typename T>
+__device__ __forceinline__ void scores(const T* row, int E, int sigmoid, float (&s)[VPT]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int e = lane + 32 * j;
+    s[j] = e < E ? to_f32<T>(row[e]) : -INFINITY;
+  }
+  scores_of<VPT>(sigmoid, s);
 }
 
 template <int VPT>

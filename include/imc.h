@@ -534,10 +534,14 @@ int moe_combine_backward(const void* grad, const void* y, int dtype, const float
  * beyond, in a fixed order.
  *   logits [T,E], rows row_stride elements apart; experts [T,k] (moe_route's);
  *   loss [S], counts [S,E].  T <= 2^27, S <= 2^27, S * E < 2^31.
+ *   workspace  moe_balance_workspace_bytes(T, S, E) bytes (0 for few tokens), 16-byte
+ *         aligned; NULL: from the library's pool.
  */
+size_t moe_balance_workspace_bytes(int64_t T, int64_t S, int64_t E);
 int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t row_stride,
                 const int32_t* experts, int64_t k, int score, const int32_t* offsets, int64_t S,
-                float* loss, int32_t* counts, void* stream);
+                float* loss, int32_t* counts, void* workspace, size_t workspace_bytes,
+                void* stream);
 
 /* grad_logits [T,E] (contiguous, of type dtype): gradient of sum_s grad_loss[s] *
  * loss[s], the counts taken as constant; 0 for tokens in no sequence.

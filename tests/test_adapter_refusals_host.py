@@ -29,9 +29,9 @@ def lowrank_back(grad=P[0], x=P[1], a=P[2], b=P[3], dtype=0, scale=P[4], layout=
                                            nbytes, None)
 
 
-def balance(logits=P[0], dtype=0, T=9, E=16, ld=16, experts=P[1], k=2, score=0, offsets=P[2], S=3, loss=P[3],
-            counts=P[4]):
-    return binding.moe_balance(logits, dtype, T, E, ld, experts, k, score, offsets, S, loss, counts, None)
+def balance(logits=P[0], dtype=0, T=9000, E=16, ld=16, experts=P[1], k=2, score=0, offsets=P[2], S=3, loss=P[3],
+            counts=P[4], ws=P[5], nbytes=1 << 20):
+    return binding.moe_balance(logits, dtype, T, E, ld, experts, k, score, offsets, S, loss, counts, ws, nbytes, None)
 
 
 def balance_back(gl=P[0], logits=P[1], dtype=0, T=9, E=16, ld=16, experts=P[2], k=2, score=0, counts=P[3],
@@ -70,7 +70,8 @@ BAD = [
     (balance, dict(experts=None), NULL), (balance, dict(loss=None), NULL), (balance, dict(counts=None), NULL),
     (balance, dict(logits=P[0] + 2), ARG), (balance, dict(loss=P[3] + 1), ARG), (balance, dict(offsets=P[2] + 2), ARG),
     (balance, dict(loss=P[0]), ALIAS), (balance, dict(counts=P[1]), ALIAS), (balance, dict(counts=P[2]), ALIAS),
-    (balance, dict(loss=P[4] + 4), ALIAS),
+    (balance, dict(loss=P[4] + 4), ALIAS), (balance, dict(nbytes=64), ARG), (balance, dict(ws=P[5] + 4), ARG),
+    (balance, dict(ws=P[0]), ALIAS), (balance, dict(ws=P[4]), ALIAS),
     (balance_back, dict(dtype=3), ARG), (balance_back, dict(score=-1), ARG), (balance_back, dict(renorm=2), ARG),
     (balance_back, dict(scale=float("inf")), ARG), (balance_back, dict(E=0), SHAPE), (balance_back, dict(ld=3), SHAPE),
     (balance_back, dict(offsets=None), SHAPE), (balance_back, dict(gl=None), NULL), (balance_back, dict(logits=None), NULL),
@@ -103,7 +104,7 @@ def test_without_a_gpu_calls_fail_loudly():
              ("lowrank_linear", [P[0], 0, 64, P[1], P[2], P[3], P[4], P[6], P[6], 900, 3, 8, 64, 32, P[7], 1 << 20, None]),
              ("lowrank_linear_backward", [P[0], P[1], P[2], P[3], 0, P[4], P[5], P[7], P[7], P[8], P[9], 9, 3, 8, 64, 32,
                                           P[10], 1 << 20, None]),
-             ("moe_balance", [P[0], 0, 9, 16, 16, P[1], 2, 0, None, 1, P[3], P[4], None]),
+             ("moe_balance", [P[0], 0, 9, 16, 16, P[1], 2, 0, None, 1, P[3], P[4], None, 0, None]),
              ("moe_balance_backward", [P[0], P[1], 0, 9, 16, 16, None, 2, 0, P[3], None, 1, None, 1, 1.0, P[6], None])]
     assert without_gpu(calls) == [binding.IMC_ERR_DEVICE] * len(calls)
 
@@ -133,4 +134,4 @@ def test_python_module_calls_the_same_entry_points():
         with pytest.raises(TypeError, match=name):
             getattr(binding._calls, name)(*zeros[1:])
     assert binding._calls.lowrank_linear(P[0], 0, 64, P[1], P[2], P[3], P[4], P[5], P[1], 9, 3, 8, 64, 32, None, 0, None) == ALIAS
-    assert binding._calls.moe_balance(P[0], 0, 9, 16, 16, P[1], 2, 0, None, 1, P[0], P[4], None) == ALIAS
+    assert binding._calls.moe_balance(P[0], 0, 9, 16, 16, P[1], 2, 0, None, 1, P[0], P[4], None, 0, None) == ALIAS

@@ -153,6 +153,14 @@ def test_long():
     Case(2, 40000, 40, 2, "softmax", torch.float32, [0, 30000, 1, 9000]).check()
 
 
+@pytest.mark.parametrize("lengths", [[0] + [17] * 150, [5, 0, 0, 1500, 0, 1, 1, 1, 900, 0, 64, 0], [2900, 10, 20],
+                                     [0] + [1] * 900 + [2000], [0] + [0] * 400 + [2500] + [0] * 300])
+def test_many_tokens_in_sequences(lengths):
+    """The form for many tokens, whose blocks each meet several sequences, or none."""
+    T = sum(lengths) + 40
+    Case(T, T, 24, 3, "sigmoid", torch.float32, lengths).check()
+
+
 def test_offsets_outside_the_tokens():
     c = Case(3, 50, 16, 2, "softmax", torch.float32, [0, 20, 30])
     want = c.forward()
