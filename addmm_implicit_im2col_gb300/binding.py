@@ -1029,15 +1029,15 @@ def _check_balance(logits, experts, score, offsets):
     dt, (T, E), (ld, _) = _rows_of(logits, "logits")
     if not isinstance(experts, _torch.Tensor) or experts.dim() != 2:
         raise ValueError("experts must be a tensor [T, k]")
-    k = experts.shape[1]
-    _check_plain(experts, "experts", _torch.int32, (T, k), logits)
+    k, device = experts.shape[1], logits.get_device()
+    _check_like(experts, "experts", _torch.int32, (T, k), device)
     S = 1
     if offsets is not None:
         if not isinstance(offsets, _torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
             raise ValueError("offsets must be a tensor [S + 1]")
         S = offsets.shape[0] - 1
-        _check_plain(offsets, "offsets", _torch.int32, (S + 1,), logits)
-    return dt, T, E, ld, k, SCORES[score], S
+        _check_like(offsets, "offsets", _torch.int32, (S + 1,), device)
+    return dt, T, E, ld, k, SCORES[score], S, device
 
 
 def balance_loss(logits, experts, *, score="softmax", offsets=None):
@@ -1053,7 +1053,7 @@ def balance_loss(logits, experts, *, score="softmax", offsets=None):
     with p the softmax of the logits, or their sigmoids divided by their sum; 1 for an even
     choice, 0 for an empty sequence.
     """
-    dt, T, E, ld, k, score, S = _check_balance(logits, experts, score, offsets)
+    dt, T, E, ld, k, score, S, _ = _check_balance(logits, experts, score, offsets)
     device = logits.device
     loss = _torch.empty((S,), dtype=_torch.float32, device=device)
     counts = _torch.empty((S, E), dtype=_torch.int32, device=device)
@@ -1076,10 +1076,11 @@ def balance_loss_backward(grad_loss, logits, experts, counts, *, score="softmax"
     and this renormalize and scale) is added in the same pass: the sum of this and
     route_experts_backward, rounded once.
     """
-    dt, T, E, ld, k, score, S = _check_balance(logits, experts, score, offsets)
-    _check_plain(grad_loss, "grad_loss", _torch.float32, (S,), logits)
-    _check_plain(counts, "counts", _torch.int32, (S, E), logits)
-    _check_plain(grad_weights, "grad_weights", _torch.float32, (T, k), logits)
+    dt, T, E, ld, k, score, S, device = _check_balance(logits, experts, score, offsets)
+    _check_like(grad_loss, "grad_loss", _torch.float32, (S,), device)
+    _check_like(counts, "counts", _torch.int32, (S, E), device)
+    if grad_weights is not None:
+        _check_like(grad_weights, "grad_weights", _torch.float32, (T, k), device)
     grad = _torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     rc = _calls.moe_balance_backward(grad_loss.data_ptr(), logits.data_ptr(), dt, T, E, ld,
                                    experts.data_ptr(), k, score, counts.data_ptr(), _ptr(offsets), S,
@@ -1090,22 +1091,36 @@ def balance_loss_backward(grad_loss, logits, experts, counts, *, score="softmax"
     return grad
 
 
+def _check_like(t, name, dtype, shape, device):
+    """_check_plain for the calls with many tensors: 0.35 us for 0.6."""
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
 def _check_adapters(x, a, b, layout, scale):
     dt, (T, K), (ld, _) = _rows_of(x, "x")
     if not isinstance(layout, ExpertsLayout):
         raise TypeError("layout must be an ExpertsLayout")
     if layout.k != 1 or layout.T != T:
         raise ValueError(f"layout must be of {T} rows with one adapter each")
-    _, (L, r, _), _ = _rows_of(a, "a", 3)
-    _, (_, N, _), _ = _rows_of(b, "b", 3)
+    for t, name in ((a, "a"), (b, "b")):
+        if not isinstance(t, _torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{name} must be a tensor of 3 dimensions")
+    L, N, r = b.shape
     if layout.E != L:
         raise ValueError(f"layout must be of {L} adapters")
-    _check_plain(a, "a", x.dtype, (L, r, K), x)
-    _check_plain(b, "b", x.dtype, (L, N, r), x)
-    _check_plain(scale, "scale", _torch.float32, (L,), x)
-    if layout.data.device != x.device:
+    dtype, device = x.dtype, x.get_device()
+    _check_like(a, "a", dtype, (L, r, K), device)
+    _check_like(b, "b", dtype, (L, N, r), device)
+    if scale is not None:
+        _check_like(scale, "scale", _torch.float32, (L,), device)
+    if layout.data.get_device() != device:
         raise ValueError("x and layout must be on one device")
-    return dt, T, L, r, K, N, ld
+    return dt, T, L, r, K, N, ld, dtype, device
 
 
 def adapters_linear(x, a, b, layout, base=None, *, scale=None, out=None):
@@ -1118,12 +1133,13 @@ def adapters_linear(x, a, b, layout, base=None, *, scale=None, out=None):
     every projection of a step.  Returns out [T, N]; ``out`` may be ``base`` (in place:
     rows without an adapter are left alone).
     """
-    dt, T, L, r, K, N, ld = _check_adapters(x, a, b, layout, scale)
-    _check_plain(base, "base", x.dtype, (T, N), x)
+    dt, T, L, r, K, N, ld, dtype, device = _check_adapters(x, a, b, layout, scale)
+    if base is not None:
+        _check_like(base, "base", dtype, (T, N), device)
     if out is None:
-        out = _torch.empty((T, N), dtype=x.dtype, device=x.device)
+        out = x.new_empty((T, N)) if base is None else _torch.empty_like(base)
     else:
-        _check_plain(out, "out", x.dtype, (T, N), x)
+        _check_like(out, "out", dtype, (T, N), device)
     nbytes = _lowrank_size(T, L, r)
     ws = _torch.empty(nbytes, dtype=_torch.uint8, device=x.device) if nbytes else None
     rc = _calls.lowrank_linear(x.data_ptr(), dt, ld, a.data_ptr(), b.data_ptr(), _ptr(scale),
@@ -1141,17 +1157,17 @@ def adapters_linear_backward(grad, x, a, b, layout, base=None, *, scale=None):
     grad_x (the gradient through the shared projection).  All tensors are contiguous and
     of one float type; an adapter without rows has gradients of 0.
     """
-    dt, T, L, r, K, N, _ = _check_adapters(x, a, b, layout, scale)
-    dtype, device = x.dtype, x.device
-    _check_plain(x, "x", dtype, (T, K), x)
-    _check_plain(grad, "grad", dtype, (T, N), x)
-    _check_plain(base, "base", dtype, (T, K), x)
+    dt, T, L, r, K, N, _, dtype, device = _check_adapters(x, a, b, layout, scale)
+    _check_like(x, "x", dtype, (T, K), device)
+    _check_like(grad, "grad", dtype, (T, N), device)
+    if base is not None:
+        _check_like(base, "base", dtype, (T, K), device)
     if T == 0 or N == 0:
         grad_x = _torch.zeros_like(x) if base is None else base.clone()
         return grad_x, _torch.zeros_like(a), _torch.zeros_like(b)
     grad_x, grad_a, grad_b = _torch.empty_like(x), _torch.empty_like(a), _torch.empty_like(b)
     nbytes = _lowrank_back_size(T, r)
-    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=device)
+    ws = _torch.empty(nbytes, dtype=_torch.uint8, device=x.device)
     rc = _calls.lowrank_linear_backward(grad.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), dt,
                                       _ptr(scale), layout.data.data_ptr(), _ptr(base),
                                       grad_x.data_ptr(), grad_a.data_ptr(), grad_b.data_ptr(), T, L,

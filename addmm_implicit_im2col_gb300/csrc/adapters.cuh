@@ -2,12 +2,47 @@
 // argument structs shared by the C entry points (mx_api.cu) and the kernel files.
 #pragma once
 
+#include <atomic>
+
 #include "mx_internal.cuh"
 
 namespace imc {
 namespace mx {
 
 constexpr int kMaxRank = 128;
+
+// Launches Kernel in clusters of `ctas` blocks (1: none) as the programmatic dependent of
+// the stream's previous kernel.  What the kernel may take of shared memory is set once per
+// device and size (0.5 us a call).
+template <auto Kernel, typename... Args>
+cudaError_t launch_clusters(dim3 grid, int ctas, int threads, size_t smem, cudaStream_t s, Args... args) {
+  static std::atomic<int> set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || set[dev].load(std::memory_order_acquire) < (int)smem) {
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) set[dev].store((int)smem, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, Kernel, args...);
+  note_launch();
+  return e;
+}
 
 // Rows of x in adapter order: bucket l of `offsets` [L + 2] holds the places in
 // `order` of adapter l's rows, bucket L those of the rows without an adapter

@@ -1242,12 +1242,22 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
             __syncwarp();
           }
           const int64_t c = now.col + b * SC + lane % SC;  // a lane has a column of its rows
-#pragma unroll 8
-          for (int i = lane / SC; i < 32; i += ROWS) {
-            const int64_t at = (int64_t)__shfl_sync(kAll, to_row, i) * g.N + c;
-            if (at < 0 || c >= g.N) continue;
-            if (!product) out[at] = base ? base[at] : from_f32<T>(0.0f);
-            else out[at] = from_f32<T>((base ? to_f32<T>(base[at]) : 0.0f) + mine[i * (SC + 1) + lane % SC]);
+          const bool in = c < g.N;
+#pragma unroll 1
+          for (int i0 = lane / SC; i0 < 32; i0 += 8 * ROWS) {
+            int64_t at[8];
+            T v[8];  // (out may be base: all eight are read before one is written)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int64_t to = __shfl_sync(kAll, to_row, i0 + k * ROWS);
+              at[k] = in && to >= 0 ? to * g.N + c : -1;
+              v[k] = base && at[k] >= 0 ? base[at[k]] : from_f32<T>(0.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (at[k] < 0) continue;
+              out[at[k]] = product ? from_f32<T>(to_f32<T>(v[k]) + mine[(i0 + k * ROWS) * (SC + 1) + lane % SC]) : v[k];
+            }
           }
           __syncwarp();
         }
@@ -1608,30 +1618,6 @@ bool aligned16(const void* p, int64_t pitch_bytes) {
   return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes) & 15u) == 0;
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int ctas, size_t smem, int threads,
-                            cudaStream_t s, Args... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  note_launch();
-  return e;
-}
-
 // Tensor-memory columns of a block: a power of two that holds `need`.
 int tmem_cols(int need) {
   int c = 32;
@@ -1658,8 +1644,8 @@ cudaError_t adapters_few(const AdapterArgs& a, cudaStream_t s) {
   const int flags = (aligned16(a.x, a.ld * b) ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0) |
                     (aligned16(a.b, a.r * b) ? 4 : 0);
   const size_t smem = (size_t)(FEW * KC + (FEW + (FEW << log_ctas)) * a.r) * 4;
-  return launch_clusters(k_adapters_few<T>, dim3((unsigned)(tiles << log_ctas)), 1 << log_ctas, smem, kThreads, s,
-                         a, log_ctas, none, flags);
+  return launch_clusters<k_adapters_few<T>>(dim3((unsigned)(tiles << log_ctas)), 1 << log_ctas, kThreads, smem, s,
+                                            a, log_ctas, none, flags);
 }
 
 // The kernel form by r rounded up to 16.
@@ -1736,8 +1722,8 @@ cudaError_t run_down_tma(DownArgs& g, int problems, cudaStream_t s) {
   g.stages = (104 << 10) / stage < DOWN_STAGES ? (104 << 10) / stage : DOWN_STAGES;
   const int bytes = g.stages * stage > sums ? g.stages * stage : sums;
   g.cols = tmem_cols(g.R);
-  return launch_clusters(k_adapters_down_tma<T>, dim3((unsigned)(tiles << g.log_ctas), problems), 1 << g.log_ctas,
-                         smem_for((size_t)bytes + 1024, g.cols), DOWN_THREADS, s, maps, g);
+  return launch_clusters<k_adapters_down_tma<T>>(dim3((unsigned)(tiles << g.log_ctas), problems), 1 << g.log_ctas,
+                                                 DOWN_THREADS, smem_for((size_t)bytes + 1024, g.cols), s, maps, g);
 }
 
 template <typename T>
@@ -1756,7 +1742,7 @@ cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
   g.cols = tmem_cols(PL::PD * g.R);
   const size_t smem = smem_for((size_t)(ring > sums ? ring : sums) + 1024, g.cols);
   const dim3 grid((unsigned)(tiles << g.log_ctas), problems);
-#define IMC_DOWN(RU) return launch_clusters(k_adapters_down<T, RU>, grid, 1 << g.log_ctas, smem, kThreads, s, g)
+#define IMC_DOWN(RU) return launch_clusters<k_adapters_down<T, RU>>(grid, 1 << g.log_ctas, kThreads, smem, s, g)
   IMC_BY_RANK(g.R, IMC_DOWN);
 #undef IMC_DOWN
 }
@@ -1818,13 +1804,9 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
     ok = ok && (g.turned ? encode<T>(&maps.w, g.w, g.N, g.r, g.N, g.R, g.L)
                          : encode<T>(&maps.w, g.w, g.r, g.N, g.r, UP_N, g.L, along.bytes));
   if (!ok) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_adapters_up<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t items = most_tiles(g.T, g.L, TILE) * g.steps, room = (int64_t)device_sm_count() * blocks;
-  e = launch_after_previous(k_adapters_up<T>, dim3((unsigned)(items < room ? items : room)), dim3(UP_THREADS<T>),
-                            smem, s, maps, g);
-  note_launch();
-  return e;
+  const int64_t items = most_tiles(g.T, g.L, TILE) * g.steps, most_blocks = (int64_t)device_sm_count() * blocks;
+  return launch_clusters<k_adapters_up<T>>(dim3((unsigned)(items < most_blocks ? items : most_blocks)), 1,
+                                           UP_THREADS<T>, smem, s, maps, g);
 }
 
 int round16(int r) { return (r + 15) / 16 * 16; }
@@ -1938,16 +1920,16 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
       w.stages = (104 << 10) / stage < DOWN_STAGES ? (104 << 10) / stage : DOWN_STAGES;
       const int bytes = w.stages * stage > sums ? w.stages * stage : sums;
       w.cols = tmem_cols(PL::PH * w.R);
-      return launch_clusters(k_adapters_grad_tma, dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
-                             smem_for((size_t)bytes + 1024, w.cols), DOWN_THREADS, s, maps, w);
+      return launch_clusters<k_adapters_grad_tma>(dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
+                                                  DOWN_THREADS, smem_for((size_t)bytes + 1024, w.cols), s, maps, w);
     }
   }
   const size_t ring = (size_t)PL::GRAD_STAGES * (PL::P * GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R));
   const size_t sums = (size_t)GRAD_COLS * (w.R + 1) * 4;
   w.cols = tmem_cols(PL::PH * w.R);
   const size_t smem = smem_for((ring > sums ? ring : sums) + 1024, w.cols);
-  return launch_clusters(k_adapters_grad<T>, dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
-                         smem, kThreads, s, w);
+  return launch_clusters<k_adapters_grad<T>>(dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
+                                             kThreads, smem, s, w);
 }
 
 }  // namespace

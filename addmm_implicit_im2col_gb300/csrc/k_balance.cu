@@ -34,13 +34,36 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_
   return low - 1;
 }
 
+// A sum as two fp32 numbers, exact to 2^-46 or so of its terms' magnitudes: 64-bit adds run
+// at a 64th of the fp32 rate here (with them a chunk's sums took 2 us more).
+struct Sum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v) {
+    const float t = hi + v, z = t - hi;
+    lo += (hi - (t - z)) + (v - z);
+    hi = t;
+  }
+  __device__ __forceinline__ void add(const Sum& o) {
+    add(o.hi);
+    lo += o.lo;
+  }
+};
+
+// 1 / (1 + e^-x) and, times e^-x over 1 + e^-x, its derivative: 1 - s is taken from
+// e^-|x|, not from s, which is 1 to fp32's precision for x of 17.
+__device__ __forceinline__ float sigmoid(float x, float& rest) {
+  const float small = expf(-fabsf(x)), inv = __fdividef(1.0f, 1.0f + small), low = small * inv;
+  rest = low * inv;
+  return x < 0.0f ? low : inv;
+}
+
 // The tokens first, first + step, ... before `last`, two of them at a time (their loads and
 // sums overlap): their scores are added to mine [E], their slots counted in count [E].  A
-// lane sums its experts' scores of kFlush tokens in fp32, then in 64 bits: an error of a
-// few fp32 roundings however long the sequence is.
+// lane sums its experts' scores of kFlush tokens in fp32 before: an error of a few fp32
+// roundings however long the sequence is.
 template <int VPT, typename T>
 __device__ __forceinline__ void add_tokens(const BalanceArgs& a, int64_t first, int64_t last, int64_t step,
-                                           double* mine, int32_t* count) {
+                                           Sum* mine, int32_t* count) {
   constexpr int U = VPT <= 8 ? 2 : 1;
   const int lane = threadIdx.x & 31, E = a.E;
   float acc[VPT];
@@ -49,7 +72,7 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& a, int64_t first, 
   auto flush = [&] {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if (lane + 32 * j < E) mine[lane + 32 * j] += acc[j];
+      if (lane + 32 * j < E) mine[lane + 32 * j].add(acc[j]);
       acc[j] = 0.0f;
     }
   };
@@ -68,15 +91,16 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& a, int64_t first, 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (e[u] >= 0 && e[u] < E) atomicAdd(count + e[u], 1);
-      scores_of<VPT>(a.sigmoid, v[u]);
       if (a.sigmoid) {  // over their sum
-        float sum = 0.0f;
+        float sum = 0.0f, rest;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) sum += v[u][j];
+        for (int j = 0; j < VPT; ++j) sum += v[u][j] = sigmoid(v[u][j], rest);
         sum = warp_sum(sum);
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) v[u][j] *= inv;
+      } else {
+        scores_of<VPT>(0, v[u]);
       }
 #pragma unroll
       for (int j = 0; j < VPT; ++j) acc[j] += v[u][j];  // (no token: scores of 0)
@@ -93,28 +117,28 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& a, int64_t first, 
 // What a cluster's CTAs have summed for sequence s (sums and counts [E] of each, in its
 // shared memory), in the order of the CTAs: counts and loss, by CTA 0.  All threads of the
 // cluster; n tokens.
-__device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, int C, int rank, const double* sums,
-                                       const int32_t* count, double* gathered, int32_t* counts) {
+__device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, int C, int rank, const Sum* sums,
+                                       const int32_t* count, Sum* gathered, int32_t* counts) {
   __shared__ double loss[kWarps];
   const int E = a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < E; e += kThreads) {
     const uint32_t at = ptx::cluster_addr(gathered + rank * E + e, 0);
-    ptx::st_cluster(at, (uint32_t)__double2loint(sums[e]));
-    ptx::st_cluster(at + 4, (uint32_t)__double2hiint(sums[e]));
+    ptx::st_cluster(at, __float_as_uint(sums[e].hi));
+    ptx::st_cluster(at + 4, __float_as_uint(sums[e].lo));
     ptx::st_cluster(ptx::cluster_addr(counts + rank * E + e, 0), (uint32_t)count[e]);
   }
   ptx::cluster_sync();
   if (rank) return;
   double part = 0.0;
   for (int e = threadIdx.x; e < E; e += kThreads) {
-    double sum = 0.0;
+    Sum sum = {0.0f, 0.0f};
     int32_t c = 0;
     for (int q = 0; q < C; ++q) {
-      sum += gathered[q * E + e];
+      sum.add(gathered[q * E + e]);
       c += counts[q * E + e];
     }
     a.counts[(int64_t)s * E + e] = c;
-    part += sum * c;
+    part += ((double)sum.hi + sum.lo) * c;
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(kAll, part, d);
@@ -129,11 +153,11 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, i
 }
 
 // Sums of the block's warps [warp][E], into the first one's place.
-__device__ __forceinline__ void over_warps(double* sums, int E) {
+__device__ __forceinline__ void over_warps(Sum* sums, int E) {
   for (int e = threadIdx.x; e < E; e += kThreads) {
-    double sum = 0.0;
+    Sum sum = sums[e];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += sums[w * E + e];
+    for (int w = 1; w < kWarps; ++w) sum.add(sums[w * E + e]);
     sums[e] = sum;
   }
 }
@@ -141,13 +165,13 @@ __device__ __forceinline__ void over_warps(double* sums, int E) {
 // One cluster of CTAs per sequence.  Every sum has a fixed order; counts are whole numbers.
 template <int VPT, typename T>
 __global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a, const int log_ctas) {
-  extern __shared__ double sm_sums[];  // [warp][E], then (CTA 0) [CTA][E]
+  extern __shared__ Sum sm_sums[];  // [warp][E], then (CTA 0) [CTA][E]
   const int E = a.E, C = 1 << log_ctas, rank = (int)ptx::cluster_rank();
-  double* gathered = sm_sums + kWarps * E;
+  Sum* gathered = sm_sums + kWarps * E;
   int32_t* count = reinterpret_cast<int32_t*>(gathered + C * E);  // [E], then (CTA 0) [CTA][E]
   const int warp = threadIdx.x >> 5, s = blockIdx.x >> log_ctas;
   ptx::cluster_arrive();  // this CTA runs: its shared memory may be written
-  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) sm_sums[i] = 0.0;
+  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) sm_sums[i] = {0.0f, 0.0f};
   for (int i = threadIdx.x; i < E; i += kThreads) count[i] = 0;
   __syncthreads();
   ptx::griddep_wait();
@@ -166,13 +190,13 @@ __global__ void __launch_bounds__(kThreads) k_balance(const BalanceArgs a, const
 // meeting to the next, so a row is written once.
 template <int VPT, typename T>
 __global__ void __launch_bounds__(kThreads) k_balance_chunks(const BalanceArgs a, const int chunk) {
-  extern __shared__ double sm_sums[];  // [warp][E]
+  extern __shared__ Sum sm_sums[];  // [warp][E]
   const int E = a.E, warp = threadIdx.x >> 5;
   int32_t* count = reinterpret_cast<int32_t*>(sm_sums + kWarps * E);
   const int64_t rows = (int64_t)gridDim.x + a.S;
-  double* sums = static_cast<double*>(a.workspace);
+  Sum* sums = static_cast<Sum*>(a.workspace);
   int32_t* counts = reinterpret_cast<int32_t*>(sums + rows * E);
-  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) sm_sums[i] = 0.0;
+  for (int i = threadIdx.x; i < kWarps * E; i += kThreads) sm_sums[i] = {0.0f, 0.0f};
   for (int i = threadIdx.x; i < E; i += kThreads) count[i] = 0;
   __syncthreads();
   ptx::griddep_wait();
@@ -194,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) k_balance_chunks(const BalanceArgs a
       sums[row * E + e] = sm_sums[e];
       counts[row * E + e] = count[e];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sm_sums[w * E + e] = 0.0;
+      for (int w = 0; w < kWarps; ++w) sm_sums[w * E + e] = {0.0f, 0.0f};
       count[e] = 0;
     }
     __syncthreads();
@@ -204,12 +228,14 @@ __global__ void __launch_bounds__(kThreads) k_balance_chunks(const BalanceArgs a
 // ... and a cluster per sequence that joins its rows.
 __global__ void __launch_bounds__(kThreads)
     k_balance_join(const BalanceArgs a, const int chunk, const int chunks, const int log_ctas) {
-  extern __shared__ double sm_sums[];  // [E], then (CTA 0) [CTA][E]
+  extern __shared__ Sum sm_sums[];  // [E], then (CTA 0) [CTA][E]
+  __shared__ Sum part_sums[1024];
+  __shared__ int32_t part_counts[1024];
   const int E = a.E, C = 1 << log_ctas, rank = (int)ptx::cluster_rank(), s = blockIdx.x >> log_ctas;
-  double* gathered = sm_sums + E;
+  Sum* gathered = sm_sums + E;
   int32_t* count = reinterpret_cast<int32_t*>(gathered + C * E);
   const int64_t rows = (int64_t)chunks + a.S;
-  const double* sums = static_cast<const double*>(a.workspace);
+  const Sum* sums = static_cast<const Sum*>(a.workspace);
   const int32_t* counts = reinterpret_cast<const int32_t*>(sums + rows * E);
   ptx::cluster_arrive();
   const int64_t t0 = a.offsets ? clamped(a.offsets[s], a.T) : 0;
@@ -219,14 +245,27 @@ __global__ void __launch_bounds__(kThreads)
   const int c0 = (int)(t0 / chunk), c1 = t1 > t0 ? (int)((t1 - 1) / chunk) + 1 : c0;
   const int per = (c1 - c0 + C - 1) >> log_ctas;
   const int from = min(c0 + rank * per, c1), to = min(from + per, c1);
-  for (int e = threadIdx.x; e < E; e += kThreads) {
-    double sum = 0.0;
+  // the threads are `parts` groups of E or more, group p of which takes every parts-th row
+  const int parts = E <= kThreads / 2 ? kThreads / E : 1, p = parts > 1 ? threadIdx.x / E : 0;
+  for (int e = threadIdx.x - p * E; e < E && p < parts; e += kThreads) {
+    Sum sum = {0.0f, 0.0f};
     int32_t n = 0;
 #pragma unroll 8
-    for (int c = from; c < to; ++c) {
+    for (int c = from + p; c < to; c += parts) {
       const int64_t row = (int64_t)c + s;
-      sum += sums[row * E + e];
+      sum.add(sums[row * E + e]);
       n += counts[row * E + e];
+    }
+    part_sums[p * E + e] = sum;
+    part_counts[p * E + e] = n;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    Sum sum = part_sums[e];
+    int32_t n = part_counts[e];
+    for (int q = 1; q < parts; ++q) {
+      sum.add(part_sums[q * E + e]);
+      n += part_counts[q * E + e];
     }
     sm_sums[e] = sum;
     count[e] = n;
@@ -244,6 +283,8 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
   ptx::griddep_wait();
   ptx::griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
+  __shared__ float words[4][32 * VPT];
+  float* mine = words[warp];
   const int64_t t = (int64_t)blockIdx.x * 4 + warp;
   if (t >= a.T) return;
   int id = -1;
@@ -253,23 +294,11 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
     gi = a.grad_weights[t * a.k + lane];
     if (id < 0 || id >= E) id = -1;
   }
-  // rest: the derivative of a score with respect to its logit without the softmax's sum.
-  // 1 - s is taken from exp(-|x|), not from s, which is 1 to fp32's precision for x of 17.
+  // rest: the derivative of a score with respect to its logit without the softmax's sum
   float s[VPT], u[VPT], rest[VPT];
   const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-  if (a.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const float x = lane + 32 * j < E ? to_f32<T>(row[lane + 32 * j]) : -INFINITY;
-      const float small = expf(-fabsf(x)), inv = 1.0f / (1.0f + small);
-      s[j] = x < 0.0f ? small * inv : inv;
-      rest[j] = small * inv * inv;
-    }
-  } else {
-    scores<VPT, T>(row, E, 0, s);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) rest[j] = s[j];
-  }
+  for (int j = 0; j < VPT; ++j) s[j] = lane + 32 * j < E ? to_f32<T>(row[lane + 32 * j]) : -INFINITY;
   const int q = a.offsets ? sequence_of(a.offsets, a.S, t) : 0;
   float coef = 0.0f;
   if (q >= 0 && q < a.S) {
@@ -282,6 +311,14 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
   for (int j = 0; j < VPT; ++j) {
     const int e = lane + 32 * j;
     u[j] = coef != 0.0f && e < E ? coef * (float)__ldg(a.counts + (int64_t)q * E + e) : 0.0f;
+  }
+  if (a.sigmoid) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) s[j] = sigmoid(s[j], rest[j]);
+  } else {
+    scores_of<VPT>(0, s);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) rest[j] = s[j];
   }
   // the balance loss: d = u - sum u p, over the sum of the scores
   float sum = 0.0f, dot = 0.0f;
@@ -301,28 +338,32 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
   for (int j = 0; j < VPT; ++j) u[j] = (u[j] - dot) * inv;
   // the weights
   if (a.grad_weights) {
-    float total = 0.0f, along = 0.0f, si = 0.0f;
-    for (int i = 0; i < a.k; ++i) {
-      const int e = __shfl_sync(kAll, id, i);
-      if (e < 0) continue;
-      const float p = __shfl_sync(kAll, pick<VPT>(s, e >> 5), e & 31);
-      total += p;
-      along += p * __shfl_sync(kAll, gi, i);
-      if (lane == i) si = p;
-    }
+    // The chosen scores are picked up from shared memory, and their gradients added there.
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) mine[lane + 32 * j] = s[j];
+    __syncwarp();
+    const float si = id >= 0 ? mine[id] : 0.0f;
+    const float total = warp_sum(si), along = warp_sum(si * gi);
     float di = id >= 0 ? gi : 0.0f;
     if (a.renorm) di = total == 0.0f || id < 0 ? 0.0f : (gi - along / total) / total;
     di *= a.scale;
     const float inner = a.sigmoid ? 0.0f : warp_sum(di * si);
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) u[j] -= inner;
-    for (int i = 0; i < a.k; ++i) {
-      const int e = __shfl_sync(kAll, id, i);
-      const float v = __shfl_sync(kAll, di, i);
-#pragma unroll
-      for (int j = 0; j < VPT; ++j)
-        if (e == lane + 32 * j) u[j] += v;
+    for (int j = 0; j < VPT; ++j) mine[lane + 32 * j] = u[j] - inner;
+    __syncwarp();
+    const uint32_t same = __match_any_sync(kAll, id >= 0 ? id : -1 - lane);
+    if (__all_sync(kAll, (same & (same - 1)) == 0)) {
+      if (id >= 0) mine[id] += di;
+    } else {  // an expert twice: in the order of the choices
+      for (int i = 0; i < a.k; ++i) {
+        if (lane == i && id >= 0) mine[id] += di;
+        __syncwarp();
+      }
     }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) u[j] = mine[lane + 32 * j];
   }
   T* grad = static_cast<T*>(a.grad) + t * E;
 #pragma unroll
@@ -333,34 +374,11 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
 }
 
 // ------------------------------------------------------------------- host
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kernel)(KArgs...), int64_t grid, int ctas, size_t smem, cudaStream_t s, Args... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ctas > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  note_launch();
-  return e;
-}
-
 // Tokens of a CTA of the form for many of them (whatever the GPU: the workspace's size
-// depends on it): 256 to 511 CTAs, of sixteen tokens at least.
+// depends on it): 512 to 1023 CTAs, of sixteen tokens at least.
 int64_t chunk_of(int64_t T) {
   int64_t chunk = 16;
-  while (ceil_div(T, chunk) > 511) chunk *= 2;
+  while (ceil_div(T, chunk) > 1023) chunk *= 2;
   return chunk;
 }
 bool many(int64_t T, int64_t S) { return T > 2048 && S <= 1024; }
@@ -371,14 +389,16 @@ cudaError_t forward(const BalanceArgs& a, cudaStream_t s) {
   if (!many(a.T, a.S)) {
     const int64_t mean = a.T / a.S;  // tokens of a sequence
     const int log_ctas = mean >= 64 ? 3 : (mean >= 32 ? 2 : (mean >= 16 ? 1 : 0)), C = 1 << log_ctas;
-    return launch(k_balance<VPT, T>, (int64_t)a.S << log_ctas, C, E * (kWarps + C) * 8 + E * (1 + C) * 4, s, a,
-                  log_ctas);
+    return launch_clusters<k_balance<VPT, T>>(dim3((unsigned)a.S << log_ctas), C, kThreads,
+                                              E * (kWarps + C) * 8 + E * (1 + C) * 4, s, a, log_ctas);
   }
   const int chunk = (int)chunk_of(a.T), chunks = (int)ceil_div(a.T, chunk);
-  const cudaError_t e = launch(k_balance_chunks<VPT, T>, chunks, 1, E * (kWarps * 8 + 4), s, a, chunk);
+  const cudaError_t e =
+      launch_clusters<k_balance_chunks<VPT, T>>(dim3(chunks), 1, kThreads, E * (kWarps * 8 + 4), s, a, chunk);
   if (e != cudaSuccess) return e;
   const int log_ctas = chunks / a.S >= 16 ? 3 : 0, C = 1 << log_ctas;
-  return launch(k_balance_join, (int64_t)a.S << log_ctas, C, E * (1 + C) * 12, s, a, chunk, chunks, log_ctas);
+  return launch_clusters<k_balance_join>(dim3((unsigned)a.S << log_ctas), C, kThreads, E * (1 + C) * 12, s, a, chunk,
+                                         chunks, log_ctas);
 }
 
 template <int VPT, typename T>
