@@ -4,6 +4,7 @@
 //
 // and their gradients.  The rows come in adapter order (moe_layout).
 #include <mutex>
+#include <type_traits>
 
 #include "adapters.cuh"
 #include "ptx.cuh"
@@ -67,173 +68,6 @@ int64_t most_tiles(int64_t T, int64_t L, int height) {
   return (T + (height - 1) * buckets) / height;
 }
 
-// ---------------------------------------------------------------- few rows
-// Up to FEW rows of one adapter per cluster of CTAs.  CTA q takes a run of K for
-// h = x a^T, gives its partial sums to every CTA of the cluster (summed in the order
-// of the CTAs), and then a run of the N outputs.
-constexpr int FEW = 8;
-constexpr int KC = 1024;  // values of K staged at once
-
-template <typename T, int NR>
-__device__ __forceinline__ void few_down(const T* a, int64_t K, int r, int64_t k0, int len, bool vec,
-                                         const float* xs, float* part) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int j = 2 * warp; j < r; j += 2 * kWarps) {
-    float acc[2][NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) acc[0][i] = acc[1][i] = 0.0f;
-    const T* w = a + (int64_t)j * K + k0;
-    const bool two = j + 1 < r;
-#pragma unroll 2
-    for (int k = lane * 8; k < len; k += 256) {
-      float v[2][8];
-      load8<T>(w + k, len - k, vec, v[0]);
-      load8<T>(w + K + k, two ? len - k : 0, vec, v[1]);
-#pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const float4 p = *reinterpret_cast<const float4*>(xs + i * KC + k);
-        const float4 q = *reinterpret_cast<const float4*>(xs + i * KC + k + 4);
-        const float x[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          acc[0][i] = fmaf(x[u], v[0][u], acc[0][i]);
-          acc[1][i] = fmaf(x[u], v[1][u], acc[1][i]);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      const float s0 = warp_sum(acc[0][i]), s1 = warp_sum(acc[1][i]);
-      if (lane == 0) {
-        part[i * r + j] += s0;
-        if (two) part[i * r + j + 1] += s1;
-      }
-    }
-  }
-}
-
-template <typename T, int NR>
-__device__ __forceinline__ void few_up(const AdapterArgs& p, const RowTile& t, int64_t n0, int64_t n1,
-                                       bool vec, const float* h, const int* rows) {
-  const T* b = static_cast<const T*>(p.b) + (int64_t)t.l * p.N * p.r;
-  const T* base = static_cast<const T*>(p.base);
-  T* out = static_cast<T*>(p.out);
-  for (int64_t n = n0 + threadIdx.x; n < n1; n += kThreads) {
-    float acc[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-      acc[i] = base && i < t.rows ? to_f32<T>(base[rows[i] * p.N + n]) : 0.0f;
-    float sum[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) sum[i] = 0.0f;
-    for (int j = 0; j < p.r; j += 8) {
-      float v[8];
-      load8<T>(b + n * p.r + j, p.r - j, vec, v);
-#pragma unroll
-      for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (j + u < p.r) sum[i] = fmaf(h[i * p.r + j + u], v[u], sum[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-      if (i < t.rows) out[rows[i] * p.N + n] = from_f32<T>(acc[i] + sum[i]);
-  }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    k_adapters_few(const AdapterArgs p, const int log_ctas, const int none, const int flags) {
-  extern __shared__ float4 sm4[];
-  const int C = 1 << log_ctas, rank = (int)ptx::cluster_rank();
-  float* xs = reinterpret_cast<float*>(sm4);  // [FEW][KC]
-  float* part = xs + FEW * KC;                // [FEW][r] this CTA's sums, then h
-  float* gathered = part + FEW * p.r;         // [C][FEW][r]
-  __shared__ int rows[FEW];
-  const bool vec_x = flags & 1, vec_a = flags & 2, vec_b = flags & 4;
-  ptx::griddep_wait();
-  ptx::griddep_launch();
-  const RowTile t = find_tile(p.offsets, p.L, none != 0, FEW, blockIdx.x >> log_ctas);
-  if (t.rows == 0) return;  // the whole cluster
-  ptx::cluster_arrive();    // this CTA runs: its shared memory may be written
-  if (threadIdx.x < FEW) rows[threadIdx.x] = threadIdx.x < t.rows ? p.order[t.p0 + threadIdx.x] : 0;
-  for (int i = threadIdx.x; i < FEW * p.r; i += kThreads) part[i] = 0.0f;
-  __syncthreads();
-  const int64_t n_per = (ceil_div(p.N, C) + 7) / 8 * 8, n0 = rank * n_per < p.N ? rank * n_per : p.N;
-  const int64_t n1 = n0 + n_per < p.N ? n0 + n_per : p.N;
-  const T* base = static_cast<const T*>(p.base);
-  T* out = static_cast<T*>(p.out);
-  if (t.l == p.L) {  // no adapter
-    ptx::cluster_wait();
-    for (int i = 0; i < t.rows; ++i)
-      for (int64_t n = n0 + threadIdx.x; n < n1; n += kThreads)
-        out[rows[i] * p.N + n] = base ? base[rows[i] * p.N + n] : from_f32<T>(0.0f);
-    return;
-  }
-  const int64_t k_per = (ceil_div(p.K, C) + 7) / 8 * 8, k0 = rank * k_per < p.K ? rank * k_per : p.K;
-  const int64_t k1 = k0 + k_per < p.K ? k0 + k_per : p.K;
-  const T* a = static_cast<const T*>(p.a) + (int64_t)t.l * p.r * p.K;
-  const int NR = t.rows <= 1 ? 1 : (t.rows <= 2 ? 2 : (t.rows <= 4 ? 4 : 8));
-  for (int64_t k = k0; k < k1; k += KC) {
-    const int len = (int)(k1 - k < KC ? k1 - k : KC), units = (len + 7) / 8;
-    for (int i = threadIdx.x; i < units * NR; i += kThreads) {
-      const int row = i / units, u = i - row * units;
-      float v[8];
-      load8<T>(static_cast<const T*>(p.x) + rows[row] * p.ld + k + u * 8,
-               row < t.rows ? len - u * 8 : 0, vec_x, v);
-      float4* to = reinterpret_cast<float4*>(xs + row * KC + u * 8);
-      to[0] = make_float4(v[0], v[1], v[2], v[3]);
-      to[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-    __syncthreads();
-    if (NR == 1) few_down<T, 1>(a, p.K, p.r, k, len, vec_a, xs, part);
-    else if (NR == 2) few_down<T, 2>(a, p.K, p.r, k, len, vec_a, xs, part);
-    else if (NR == 4) few_down<T, 4>(a, p.K, p.r, k, len, vec_a, xs, part);
-    else few_down<T, 8>(a, p.K, p.r, k, len, vec_a, xs, part);
-    __syncthreads();
-  }
-  ptx::cluster_wait();
-  const int sums = NR * p.r;
-  for (int i = threadIdx.x; i < sums * C; i += kThreads) {
-    const int q = i / sums, e = i - q * sums;
-    ptx::st_cluster(ptx::cluster_addr(gathered + rank * FEW * p.r + e, q), __float_as_uint(part[e]));
-  }
-  ptx::cluster_sync();
-  const float scale = p.scale ? p.scale[t.l] : 1.0f;
-  for (int i = threadIdx.x; i < sums; i += kThreads) {
-    float h = 0.0f;
-    for (int q = 0; q < C; ++q) h += gathered[q * FEW * p.r + i];
-    part[i] = h * scale;
-  }
-  __syncthreads();
-  if (NR == 1) few_up<T, 1>(p, t, n0, n1, vec_b, part, rows);
-  else if (NR == 2) few_up<T, 2>(p, t, n0, n1, vec_b, part, rows);
-  else if (NR == 4) few_up<T, 4>(p, t, n0, n1, vec_b, part, rows);
-  else few_up<T, 8>(p, t, n0, n1, vec_b, part, rows);
-}
-
-// ------------------------------------------------------------------- tiles
-// More rows: tiles of 128 rows of one adapter on the tensor cores (tcgen05, fp32
-// accumulators), in two launches.  The first computes h = x a^T, a cluster of C CTAs for
-// each tile: CTA q takes a run of K, and the cluster's sums are taken in the order of the
-// CTAs.  The second adds h b^T to base, a CTA for each 128 x 128 outputs.  Both stream
-// (x; base and out), and many small CTAs on an SM hide the memory's latency.  One launch
-// for both (h stayed in the cluster) took 66 us for 8192 rows, 8 adapters, r 32, 4096 x
-// 4096, bf16, where these take
-//
-// A value is a sum of bf16 numbers ("planes"): bf16 1, fp16 2, fp32 3, exactly; an element
-// of h is kept as PH of them (2 for the 16-bit types: to 2^-17 of its value; 3 for fp32).
-// Beside fp16 b, h is two fp16 numbers instead, its row scaled by a power of two that
-// brings its largest value to 2^14 .. 2^15: to 2^-22 of that, whatever its size.
-// The planes of the operand that lies along the MMA's N follow one another there, so
-// that the tensor core reads a plane of the other operand once for all of them; the sums
-// over those planes are taken in fp32 afterwards.
-constexpr int TILE = 128;            // rows of a tile: the MMA's M
-constexpr int KB = 64;               // values of K per stage: 128 bytes of a plane's row
-constexpr int XP = TILE * KB * 2;    // bytes of a plane of a stage's x
-constexpr int UP_N = 128;            // outputs of one step of the second product
-__device__ int g_watchdog_adapters;
-
 template <typename T>
 struct Planes;
 // P: planes of a value where it has to be bf16 (gradients of the weights); PD and FD: planes
@@ -277,6 +111,323 @@ struct Raw8 {
     for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(t[i]);
   }
 };
+
+// ---------------------------------------------------------------- few rows
+// Up to FEW rows of one adapter per cluster of CTAs, in one launch.  CTA q takes a run of K
+// for h = x a^T, gives its partial sums to every CTA of the cluster (summed in the order of
+// the CTAs), and then a run of the N outputs.  Such a call is bound by latency: of the loads
+// that wait for one another, and of fetching instructions that run once.  So the loops are
+// short: both products use mma.sync (a warp's small tiles need no shared memory and no
+// barriers, unlike tcgen05's), whose operands come straight from global memory, sixteen
+// bytes a lane: the order of the values along the summed axis is the same for both operands,
+// whatever it is.  The same with fp32 FMAs, unrolled for 1, 2, 4 or 8 rows, took 30 us where
+// this takes
+constexpr int FEW = 8;
+constexpr int FEW_ROWS = 1024;  // rows whose numbers are asked for before the tile is known
+constexpr int FEW_N = 512;      // outputs staged at once
+constexpr int FEW_PITCH = FEW_N + 8;
+
+// Four values of a row.
+template <typename T>
+struct Raw4 {
+  uint32_t w[sizeof(T)];
+  __device__ __forceinline__ void load(const T* p, int n, bool vec) {
+    if (vec && n >= 4) {
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(p));
+      else *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(p));
+    } else {
+      T t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = i < n ? p[i] : from_f32<T>(0.0f);
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w[i] = *reinterpret_cast<const uint16_t*>(t + 2 * i) | (uint32_t)*reinterpret_cast<const uint16_t*>(t + 2 * i + 1) << 16;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(t + i);
+      }
+    }
+  }
+};
+// d += A B of a warp: sixteen rows of A (this lane's words of row lane / 4 in a, of the eighth
+// after it in a8) and eight columns of B (of column lane / 4 in b).  16-bit types: K = 16, two
+// words of two values; fp32: K = 8, two words, as three products of TF32 parts.
+__device__ __forceinline__ void few_mma(__nv_bfloat16, float (&d)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
+  ptx::mma_sync_bf16(d, a[0], a8[0], a[1], a8[1], b[0], b[1]);
+}
+__device__ __forceinline__ void few_mma(__half, float (&d)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
+  ptx::mma_sync_f16(d, a[0], a8[0], a[1], a8[1], b[0], b[1]);
+}
+__device__ __forceinline__ void few_mma(float, float (&d)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
+  auto hi = [](uint32_t v) { return __float_as_uint(tc::tf32_hi(__uint_as_float(v))); };
+  auto lo = [](uint32_t v) { return __float_as_uint(tc::tf32_lo(__uint_as_float(v))); };
+  ptx::mma_sync_tf32(d, lo(a[0]), lo(a8[0]), lo(a[1]), lo(a8[1]), hi(b[0]), hi(b[1]));
+  ptx::mma_sync_tf32(d, hi(a[0]), hi(a8[0]), hi(a[1]), hi(a8[1]), lo(b[0]), lo(b[1]));
+  ptx::mma_sync_tf32(d, hi(a[0]), hi(a8[0]), hi(a[1]), hi(a8[1]), hi(b[0]), hi(b[1]));
+}
+
+struct FewArgs {
+  AdapterArgs a;
+  int log_ctas, none, vec;  // vec: 1 x, 2 a (16 bytes), 4 b (four values)
+  int R, blocks, parts;     // r rounded up to 16; blocks of 16 of it; warps that share one
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_constant__ FewArgs g) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  __shared__ int order[FEW_ROWS], rows[FEW];
+  __shared__ float row_scale[FEW];
+  using O = std::conditional_t<sizeof(T) == 4, float, T>;  // of h's two parts
+  const AdapterArgs& p = g.a;
+  const int rank = (int)ptx::cluster_rank(), C = 1 << g.log_ctas, R = g.R, r = p.r;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row8 = lane >> 2, quad = lane & 3;
+  float* part = reinterpret_cast<float*>(sm);     // [parts][FEW][R]
+  float* gathered = part + g.parts * FEW * R;     // [C][FEW][R]
+  const int h_pitch = R + 16 / (int)sizeof(O);
+  O* hs = reinterpret_cast<O*>(gathered + C * FEW * R);                   // two parts of [FEW][h_pitch]
+  float* outs = reinterpret_cast<float*>(hs + 2 * FEW * h_pitch);         // [FEW][FEW_PITCH]
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+#pragma unroll
+  for (int i = 0; i < FEW_ROWS / kThreads; ++i) {
+    const int at = tid + i * kThreads;
+    if (at < p.T) order[at] = __ldg(p.order + at);
+  }
+  const RowTile t = find_tile(p.offsets, p.L, g.none != 0, FEW, blockIdx.x >> g.log_ctas);
+  if (t.rows == 0) return;  // the whole cluster
+  ptx::cluster_arrive();    // this CTA runs: its shared memory may be written
+  if (tid < FEW) {          // past the tile's end the last one again
+    const int at = t.p0 + min(tid, t.rows - 1);
+    rows[tid] = at < FEW_ROWS ? order[at] : __ldg(p.order + at);
+  }
+  __syncthreads();
+  const T* base = static_cast<const T*>(p.base);
+  T* out = static_cast<T*>(p.out);
+  const int64_t n_per = (ceil_div(p.N, C) + 15) / 16 * 16, n0 = rank * n_per < p.N ? rank * n_per : p.N;
+  const int64_t n1 = n0 + n_per < p.N ? n0 + n_per : p.N;
+  const bool product = t.l < p.L;
+  if (product) {
+    const T* a = static_cast<const T*>(p.a) + (int64_t)t.l * r * p.K;
+    const T* b = static_cast<const T*>(p.b) + (int64_t)t.l * p.N * r;
+    // The second product's units, sixteen outputs by sixteen j each, four at a time: the
+    // first four are asked for here, as well as the first of base.  The rest of b is on its
+    // way to L2.
+    const int live0 = (int)(n1 - n0 < FEW_N ? n1 - n0 : FEW_N);
+    constexpr int Q = 4;
+    Raw4<T> w[Q], w8[Q];
+    const T* from;  // this lane's values of the next unit to be asked for
+    int ask_nb, ask_j;
+    auto start_b = [&](int64_t n) {
+      ask_nb = warp * 16;
+      ask_j = 0;
+      from = b + (n + ask_nb + row8) * r + quad * 4;
+    };
+    // (`full`: sixteen outputs, sixteen j, aligned; a third of the other's instructions)
+    auto load_b = [&](auto full, int64_t n, int live) {
+#pragma unroll
+      for (int u = 0; u < Q; ++u) {
+        if (ask_nb < live) {
+          if constexpr (full) {
+            w[u].load(from, 4, true);
+            w8[u].load(from + 8 * r, 4, true);
+          } else {
+            const int64_t row = n + ask_nb + row8;
+            const int left = r - ask_j - quad * 4;
+            w[u].load(from, row < n1 ? left : 0, g.vec & 4);
+            w8[u].load(from + 8 * r, row + 8 < n1 ? left : 0, g.vec & 4);
+          }
+          from += 16;
+          ask_j += 16;
+          if (ask_j == R) {
+            ask_j = 0;
+            ask_nb += kWarps * 16;
+            from += (int64_t)kWarps * 16 * r - R;
+          }
+        }
+      }
+    };
+    const bool whole_b = (g.vec & 4) && r == R;
+    auto any_b = [&](int64_t n, int live) {
+      if (whole_b && live % 16 == 0) load_b(std::true_type{}, n, live);
+      else load_b(std::false_type{}, n, live);
+    };
+    start_b(n0);
+    any_b(n0, live0);
+    T was[Q];
+#pragma unroll
+    for (int u = 0; u < Q; ++u) {
+      const int i = tid + u * kThreads, row = live0 ? i / live0 : FEW;
+      was[u] = base && row < t.rows ? base[rows[row & (FEW - 1)] * p.N + n0 + i - row * live0] : from_f32<T>(0.0f);
+    }
+    const int64_t bytes = (n1 - n0) * r * (int64_t)sizeof(T);
+    for (int64_t i = tid * 128; i < bytes; i += kThreads * 128)
+      ptx::prefetch_l2(reinterpret_cast<const uint8_t*>(b + n0 * r) + i);
+    // ---- h = x a^T over this CTA's run of K: a warp has sixteen j and a part of the run
+    const int64_t k_per = (ceil_div(p.K, C) + 31) / 32 * 32, k0 = rank * k_per < p.K ? rank * k_per : p.K;
+    const int64_t k1 = k0 + k_per < p.K ? k0 + k_per : p.K;
+    if (warp < g.blocks * g.parts) {
+      const int block = warp % g.blocks, share = warp / g.blocks, j = block * 16 + row8;
+      const T *wa = a + j * p.K, *wa8 = wa + 8 * p.K, *x = static_cast<const T*>(p.x) + rows[row8] * p.ld;
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      auto step = [&](const Raw8<T>& u, const Raw8<T>& u8, const Raw8<T>& v) {
+        const uint32_t *aw = reinterpret_cast<const uint32_t*>(u.w), *aw8 = reinterpret_cast<const uint32_t*>(u8.w),
+                       *bw = reinterpret_cast<const uint32_t*>(v.w);
+#pragma unroll
+        for (int i = 0; i < 2 * (int)sizeof(T); i += 2) few_mma(T(), d, aw + i, aw8 + i, bw + i);
+      };
+      const int first = share * 32, len = (int)(k1 - k0), stride = g.parts * 32;
+      int at = first;
+      wa += k0 + quad * 8, wa8 += k0 + quad * 8, x += k0 + quad * 8;
+      if ((g.vec & 3) == 3 && r == R) {  // whole units
+#pragma unroll 4
+        for (; at + 32 <= len; at += stride) {
+          Raw8<T> u, u8, v;
+          u.load(wa + at, 8, true);
+          u8.load(wa8 + at, 8, true);
+          v.load(x + at, 8, true);
+          step(u, u8, v);
+        }
+      }
+#pragma unroll 1
+      for (; at < len; at += stride) {
+        const int left = len - at - quad * 8;
+        Raw8<T> u, u8, v;
+        u.load(wa + at, j < r ? left : 0, g.vec & 2);
+        u8.load(wa8 + at, j + 8 < r ? left : 0, g.vec & 2);
+        v.load(x + at, left, g.vec & 1);
+        step(u, u8, v);
+      }
+      float* to = part + (share * FEW + quad * 2) * R + j;
+      to[0] = d[0], to[R] = d[1], to[8] = d[2], to[R + 8] = d[3];
+    }
+    const float scale = p.scale ? p.scale[t.l] : 1.0f;
+    __syncthreads();
+    ptx::cluster_wait();
+    const int units = FEW * R / 4;
+    for (int i = tid; i < units * C; i += kThreads) {
+      const int q = i / units, e = (i - q * units) * 4;
+      float4 s = *reinterpret_cast<const float4*>(part + e);
+      for (int u = 1; u < g.parts; ++u) {
+        const float4 v = *reinterpret_cast<const float4*>(part + u * FEW * R + e);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      ptx::st_cluster4(ptx::cluster_addr(gathered + rank * FEW * R + e, q),
+                       make_uint4(__float_as_uint(s.x), __float_as_uint(s.y), __float_as_uint(s.z), __float_as_uint(s.w)));
+    }
+    ptx::cluster_sync();
+    // ---- h in two parts (fp16: the row's largest value brought to 2^14 .. 2^15); a warp a row
+    {
+      float top = 0.0f;
+      float* mine = gathered + warp * R;
+      for (int i = lane; i < R; i += 32) {
+        float s = 0.0f;
+        for (int q = 0; q < C; ++q) s += mine[q * FEW * R + i];
+        s = i < r ? s * scale : 0.0f;  // past r: zeros times x, which may be infinite
+        mine[i] = s;
+        top = fmaxf(top, fabsf(s));
+      }
+      float up = 1.0f;
+      if (Planes<T>::FD == 0) {
+        top = warp_max(top);
+        uint32_t e8 = __float_as_uint(top) >> 23;
+        e8 = e8 == 255u || top == 0.0f ? 141u : max(e8, 15u);
+        up = __uint_as_float((268u - e8) << 23);
+        if (lane == 0) row_scale[warp] = __uint_as_float((e8 - 14u) << 23);
+      } else if (lane == 0) {
+        row_scale[warp] = 1.0f;
+      }
+      for (int i = lane; i < R; i += 32) {
+        const float s = mine[i] * up;
+        if constexpr (sizeof(T) == 4) {  // few_mma takes it apart
+          hs[warp * h_pitch + i] = s;
+        } else {
+          const O hi = from_f32<O>(s);
+          const float f = to_f32<O>(hi);
+          hs[warp * h_pitch + i] = hi;
+          hs[(FEW + warp) * h_pitch + i] = from_f32<O>(fabsf(f) == INFINITY ? 0.0f : s - f);
+        }
+      }
+    }
+    __syncthreads();
+    for (int64_t n = n0; n < n1; n += FEW_N) {
+      const int live = (int)(n1 - n < FEW_N ? n1 - n : FEW_N);
+      if (n > n0) {
+        start_b(n);
+        any_b(n, live);
+      }
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      int nb = warp * 16, j = 0;
+#pragma unroll 1
+      while (nb < live) {
+#pragma unroll
+        for (int u = 0; u < Q; ++u) {
+          if (nb < live) {  // the whole warp
+            const O* h = hs + row8 * h_pitch + j + quad * 4;
+            const uint32_t* hw = reinterpret_cast<const uint32_t*>(h);
+            few_mma(T(), d, w[u].w, w8[u].w, hw);
+            if constexpr (sizeof(T) == 2) few_mma(T(), d, w[u].w, w8[u].w, reinterpret_cast<const uint32_t*>(h + FEW * h_pitch));
+            else few_mma(T(), d, w[u].w + 2, w8[u].w + 2, hw + 2);
+            j += 16;
+            if (j == R) {
+              float* to = outs + quad * 2 * FEW_PITCH + nb + row8;
+              to[0] = d[0], to[FEW_PITCH] = d[1], to[8] = d[2], to[FEW_PITCH + 8] = d[3];
+              d[0] = d[1] = d[2] = d[3] = 0.0f;
+              j = 0;
+              nb += kWarps * 16;
+            }
+          }
+        }
+        any_b(n, live);
+      }
+      __syncthreads();
+      auto put = [&](int i, int row, int64_t at, T base_value) {
+        out[at] = from_f32<T>(fmaf(outs[row * FEW_PITCH + i - row * live], row_scale[row], to_f32<T>(base_value)));
+      };
+      int i = tid;
+      if (n == n0) {
+#pragma unroll
+        for (int u = 0; u < Q; ++u, i += kThreads) {
+          const int row = i / live;
+          if (row < t.rows) put(i, row, rows[row] * p.N + n + i - row * live, was[u]);
+        }
+      }
+      for (; i < live * t.rows; i += kThreads) {
+        const int row = i / live;
+        const int64_t at = rows[row] * p.N + n + i - row * live;
+        put(i, row, at, base ? base[at] : from_f32<T>(0.0f));
+      }
+      __syncthreads();
+    }
+  } else {  // no adapter
+    ptx::cluster_wait();
+    for (int i = 0; i < t.rows; ++i)
+      for (int64_t n = n0 + tid; n < n1; n += kThreads)
+        out[rows[i] * p.N + n] = base ? base[rows[i] * p.N + n] : from_f32<T>(0.0f);
+  }
+}
+
+// ------------------------------------------------------------------- tiles
+// More rows: tiles of 128 rows of one adapter on the tensor cores (tcgen05, fp32
+// accumulators), in two launches.  The first computes h = x a^T, a cluster of C CTAs for
+// each tile: CTA q takes a run of K, and the cluster's sums are taken in the order of the
+// CTAs.  The second adds h b^T to base, a CTA for each 128 x 128 outputs.  Both stream
+// (x; base and out), and many small CTAs on an SM hide the memory's latency.  One launch
+// for both (h stayed in the cluster) took 66 us for 8192 rows, 8 adapters, r 32, 4096 x
+// 4096, bf16, where these take
+//
+// A value is a sum of bf16 numbers ("planes"): bf16 1, fp16 2, fp32 3, exactly; an element
+// of h is kept as PH of them (2 for the 16-bit types: to 2^-17 of its value; 3 for fp32).
+// Beside fp16 b, h is two fp16 numbers instead, its row scaled by a power of two that
+// brings its largest value to 2^14 .. 2^15: to 2^-22 of that, whatever its size.
+// The planes of the operand that lies along the MMA's N follow one another there, so
+// that the tensor core reads a plane of the other operand once for all of them; the sums
+// over those planes are taken in fp32 afterwards.
+constexpr int TILE = 128;            // rows of a tile: the MMA's M
+constexpr int KB = 64;               // values of K per stage: 128 bytes of a plane's row
+constexpr int XP = TILE * KB * 2;    // bytes of a plane of a stage's x
+constexpr int UP_N = 128;            // outputs of one step of the second product
+__device__ int g_watchdog_adapters;
 
 // v as the sum of Q bf16 numbers, each the nearest to what is left: 8, 16 or 24 bits.
 // An infinity stays in the first.
@@ -1634,18 +1785,26 @@ size_t smem_for(size_t bytes, int cols) {
   return bytes < most ? bytes : most;
 }
 
+int round16(int r) { return (r + 15) / 16 * 16; }
+
 template <typename T>
 cudaError_t adapters_few(const AdapterArgs& a, cudaStream_t s) {
   note_kernel_name("k_adapters_few");
-  const int log_ctas = 3;
-  const int none = a.base != a.out ? 1 : 0;
-  const int64_t tiles = most_tiles(a.T, a.L, FEW);
-  const int64_t b = sizeof(T);
-  const int flags = (aligned16(a.x, a.ld * b) ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0) |
-                    (aligned16(a.b, a.r * b) ? 4 : 0);
-  const size_t smem = (size_t)(FEW * KC + (FEW + (FEW << log_ctas)) * a.r) * 4;
-  return launch_clusters<k_adapters_few<T>>(dim3((unsigned)(tiles << log_ctas)), 1 << log_ctas, kThreads, smem, s,
-                                            a, log_ctas, none, flags);
+  const int64_t tiles = most_tiles(a.T, a.L, FEW), b = sizeof(T);
+  FewArgs g = {};
+  g.a = a;
+  // Eight CTAs a tile; four where those are more than 3.5 an SM (us with 8 / 4, bf16, r 16, 4096 x
+  // 4096: 64 rows of 64 adapters 9.5 / 11.7, 512 rows of 8 22.2 / 19.0, 1000 rows of 64 34.0 / 31.8).
+  g.log_ctas = tiles * 16 <= 7 * device_sm_count() ? 3 : 2;
+  g.none = a.base != a.out ? 1 : 0;
+  g.vec = (aligned16(a.x, a.ld * b) ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0) |
+          (a.r % 4 == 0 && reinterpret_cast<uintptr_t>(a.b) % (4 * b) == 0 ? 4 : 0);
+  g.R = round16(a.r);
+  g.blocks = g.R / 16;
+  g.parts = kWarps / g.blocks;
+  const int C = 1 << g.log_ctas;
+  const size_t smem = (size_t)((g.parts + C) * FEW * g.R + FEW * FEW_PITCH) * 4 + (size_t)2 * FEW * (g.R * b + 16);
+  return launch_clusters<k_adapters_few<T>>(dim3((unsigned)(tiles << g.log_ctas)), C, kThreads, smem, s, g);
 }
 
 // The kernel form by r rounded up to 16.
@@ -1809,7 +1968,12 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
                                            UP_THREADS<T>, smem, s, maps, g);
 }
 
-int round16(int r) { return (r + 15) / 16 * 16; }
+// The form for few rows: an adapter has sixteen on average at most, whose tiles of 128 would
+// be nearly empty, or there are few altogether, and one launch is over sooner than two.  us
+// with it / in tiles, bf16, 4096 x 4096: 64 rows of 64 adapters, r 16, 9.5 / 29.2; 1000 of 64
+// 31.8 / 45.8; 2000 of 64 57.2 / 49.5; 512 of 8 19.0 / 21.9; 1000 of 8 35.2 / 23.9; r 64: 64 of 8
+// 15.4 / 18.4, 256 of 8 19.3 / 19.6.
+bool few_rows(int64_t T, int64_t L, int64_t r) { return T <= 16 * L || T * r <= 8192; }
 
 // The workspace of one h (of g): its planes, its scaled fp16 rows, their scales.
 size_t room_bytes(int64_t T, int64_t R) { return (size_t)(T * R * (6 + 4) + (T + 3) / 4 * 16); }
@@ -1824,7 +1988,7 @@ Room room_of(void* workspace, int i, int64_t T, int64_t R) {
 
 template <typename T>
 cudaError_t adapters(const AdapterArgs& a, cudaStream_t s) {
-  if (a.T <= 64) return adapters_few<T>(a, s);
+  if (few_rows(a.T, a.L, a.r)) return adapters_few<T>(a, s);
   note_kernel_name("k_adapters_up");
   const int64_t b = sizeof(T);
   DownArgs g = {};
@@ -1941,7 +2105,7 @@ cudaError_t launch_adapters(const AdapterArgs& a, int dtype, cudaStream_t s) {
 }
 
 size_t adapters_bytes(int64_t T, int64_t L, int64_t r) {
-  return T <= 64 ? 0 : room_bytes(T, round16((int)r));
+  return few_rows(T, L, r) ? 0 : room_bytes(T, round16((int)r));
 }
 size_t adapters_backward_bytes(int64_t T, int64_t r) {
   return 2 * room_bytes(T, round16((int)r));
