@@ -175,9 +175,10 @@ struct FewArgs {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_constant__ FewArgs g) {
-  extern __shared__ __align__(16) uint8_t sm[];
+  extern __shared__ uint8_t sm_raw[];
   __shared__ int order[FEW_ROWS], rows[FEW];
   __shared__ float row_scale[FEW];
+  uint8_t* sm = sm_raw;
   using O = std::conditional_t<sizeof(T) == 4, float, T>;  // of h's two parts
   const AdapterArgs& p = g.a;
   const int rank = (int)ptx::cluster_rank(), C = 1 << g.log_ctas, R = g.R, r = p.r;
@@ -630,14 +631,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
   using PL = Planes<T>;
   constexpr int P = PL::PD, S = PL::STAGES;
   constexpr bool ASYNC = sizeof(T) == 2;
-  extern __shared__ uint8_t sm_raw[];
+  extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ RingCtl ctl;
   __shared__ int rows[TILE];
-  uint8_t* sm = tc::smem_align1024(sm_raw);
   const DownProblem& p = g.prob[blockIdx.y];
   const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank();
   const int tid = threadIdx.x, warp = tid >> 5, R = g.R, r = g.r;
   int* wd = &g_watchdog_adapters;
+  if (ptx::smem_addr(sm) & 1023u) {  // (no room to align it: two blocks fill an SM)
+    if (tid == 0) atomicCAS(wd, 0, 15);
+    return;
+  }
   const uint32_t tmem = set_up(ctl, 5, ctl.empty, g.cols);
   ptx::griddep_wait();
   ptx::griddep_launch();
@@ -1513,15 +1517,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   using PL = Planes<T>;
   constexpr int P = PL::P, PH = PL::PH, S = PL::GRAD_STAGES;
   constexpr bool HELD = P > 1;  // x goes through registers, a block ahead
-  extern __shared__ uint8_t sm_raw[];
+  extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ RingCtl ctl;
-  uint8_t* sm = tc::smem_align1024(sm_raw);
   const GradProblem& p = g.prob[blockIdx.z];
   const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank();
   const int tid = threadIdx.x, warp = tid >> 5, R = g.R;
   const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * GRAD_COLS;
   const int l = blockIdx.y;
   int* wd = &g_watchdog_adapters;
+  if (ptx::smem_addr(sm) & 1023u) {  // (no room to align it: two blocks fill an SM)
+    if (tid == 0) atomicCAS(wd, 0, 15);
+    return;
+  }
   const uint32_t tmem = set_up(ctl, 5, ctl.empty, g.cols);
   ptx::griddep_wait();
   ptx::griddep_launch();
@@ -1863,6 +1870,15 @@ bool encode_h(CUtensorMap* m, const uint16_t* h, int64_t T, int R, int planes) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Blocks of `smem` bytes (and under 1 KB of static shared memory) that an SM holds.
+int64_t resident(size_t smem) { return (228 << 10) / (int64_t)((smem + 1023) / 1024 * 1024 + 2048); }
+// CTAs of a cluster, as log2: as many as keep the tiles' clusters, about T / 128 and half a
+// tile for each adapter, resident at once.
+int cluster_log(int64_t room, int64_t T, int64_t L, int problems) {
+  const int64_t tiles = ceil_div(T, TILE) + (T < L ? T : L) / 2, want = room / (tiles * problems);
+  return want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
+}
+
 template <typename T>
 cudaError_t run_down_tma(DownArgs& g, int problems, cudaStream_t s) {
   DownMaps maps = {};
@@ -1874,9 +1890,8 @@ cudaError_t run_down_tma(DownArgs& g, int problems, cudaStream_t s) {
       return cudaErrorInvalidValue;
   }
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
-  // about two blocks per SM, with a ring of up to 104 KB each
-  const int64_t want = 2 * (int64_t)device_sm_count() / (ceil_div(g.T, TILE) * problems);
-  g.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
+  // two blocks per SM, with a ring of up to 104 KB each
+  g.log_ctas = cluster_log(2 * (int64_t)device_sm_count(), g.T, g.L, problems);
   const int stage = XP + down_w_bytes(g.R), sums = TILE * (g.R * 4 + 16);
   g.stages = (104 << 10) / stage < DOWN_STAGES ? (104 << 10) / stage : DOWN_STAGES;
   const int bytes = g.stages * stage > sums ? g.stages * stage : sums;
@@ -1894,12 +1909,10 @@ cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
     if (tma) return run_down_tma<T>(g, problems, s);
   }
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
-  // about three blocks per SM
-  const int64_t want = 3 * (int64_t)device_sm_count() / (ceil_div(g.T, TILE) * problems);
-  g.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
   const int ring = PL::STAGES * (PL::PD * XP + down_w_bytes(PL::PD * g.R)), sums = TILE * (g.R * 4 + 16);
   g.cols = tmem_cols(PL::PD * g.R);
-  const size_t smem = smem_for((size_t)(ring > sums ? ring : sums) + 1024, g.cols);
+  const size_t smem = smem_for((size_t)(ring > sums ? ring : sums), g.cols);
+  g.log_ctas = cluster_log(resident(smem) * device_sm_count(), g.T, g.L, problems);
   const dim3 grid((unsigned)(tiles << g.log_ctas), problems);
 #define IMC_DOWN(RU) return launch_clusters<k_adapters_down<T, RU>>(grid, 1 << g.log_ctas, kThreads, smem, s, g)
   IMC_BY_RANK(g.R, IMC_DOWN);
@@ -2010,43 +2023,15 @@ cudaError_t adapters(const AdapterArgs& a, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
+cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const uint16_t* d, cudaStream_t s) {
   using PL = Planes<T>;
-  note_kernel_name("k_adapters_grad");
-  constexpr bool F16 = PL::FD == 0;
-  DownArgs g = {};
-  g.scale = a.scale;
-  g.offsets = a.offsets;
-  g.order = a.order;
-  g.T = a.T;
-  g.L = a.L;
-  g.r = a.r;
-  g.R = round16(a.r);
-  const int64_t size = sizeof(T);
-  const Room h = room_of(a.workspace, 0, a.T, g.R), d = room_of(a.workspace, 1, a.T, g.R);
-  const bool scaled = F16 && a.grad_x;
-  int problems = 0;
-  if (a.grad_x || a.grad_a)  // g = scale * grad b
-    g.prob[problems++] = {a.grad, a.N, a.N, a.b, F16 && !a.grad_a ? nullptr : d.h, scaled ? d.h16 : nullptr,
-                          scaled ? d.row_scale : nullptr, 1,
-                          (aligned16(a.grad, a.N * size) ? 1 : 0) | (aligned16(a.b, a.r * size) ? 2 : 0)};
-  if (a.grad_b)  // h = scale * x a^T
-    g.prob[problems++] = {a.x, a.K, a.K, a.a, h.h, nullptr, nullptr, 0,
-                          (aligned16(a.x, a.K * size) ? 1 : 0) | (aligned16(a.a, a.K * size) ? 2 : 0)};
-  cudaError_t e = run_down<T>(g, problems, s);
-  if (e == cudaSuccess && a.grad_x) {
-    UpArgs up = {scaled ? d.row_scale : nullptr, a.a, a.base, a.grad_x, a.offsets, a.order, a.T, a.K, a.L, a.r, g.R};
-    up.turned = 1;
-    e = run_up<T>(up, scaled ? d.h16 : d.h, s);
-  }
-  if (e != cudaSuccess || (!a.grad_a && !a.grad_b)) return e;
   GradArgs w = {};
   w.offsets = a.offsets;
   w.order = a.order;
   w.T = a.T;
   w.L = a.L;
   w.r = a.r;
-  w.R = g.R;
+  w.R = R;
   int parts = 0;
   int64_t chunks = 0, all = 0;
   auto add = [&](const void* x, int64_t cols, const uint16_t* planes, void* out, int turned) {
@@ -2061,8 +2046,8 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
     chunks = chunks > n ? chunks : n;
     all += n;
   };
-  if (a.grad_a) add(a.x, a.K, d.h, a.grad_a, 0);
-  if (a.grad_b) add(a.grad, a.N, h.h, a.grad_b, 1);
+  if (a.grad_a) add(a.x, a.K, d, a.grad_a, 0);
+  if (a.grad_b) add(a.grad, a.N, h, a.grad_b, 1);
   // about three blocks per SM, of four stages of rows on average at least
   int64_t want = 3 * (int64_t)device_sm_count() / (all * a.L);
   const int64_t most = a.T / a.L / (4 * GRAD_ROWS);
@@ -2091,9 +2076,44 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
   const size_t ring = (size_t)PL::GRAD_STAGES * (PL::P * GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R));
   const size_t sums = (size_t)GRAD_COLS * (w.R + 1) * 4;
   w.cols = tmem_cols(PL::PH * w.R);
-  const size_t smem = smem_for((ring > sums ? ring : sums) + 1024, w.cols);
+  const size_t smem = smem_for(ring > sums ? ring : sums, w.cols);
   return launch_clusters<k_adapters_grad<T>>(dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
                                              kThreads, smem, s, w);
+}
+
+template <typename T>
+cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
+  using PL = Planes<T>;
+  note_kernel_name("k_adapters_grad");
+  constexpr bool F16 = PL::FD == 0;
+  DownArgs g = {};
+  g.scale = a.scale;
+  g.offsets = a.offsets;
+  g.order = a.order;
+  g.T = a.T;
+  g.L = a.L;
+  g.r = a.r;
+  g.R = round16(a.r);
+  const int64_t size = sizeof(T);
+  const Room h = room_of(a.workspace, 0, a.T, g.R), d = room_of(a.workspace, 1, a.T, g.R);
+  const bool scaled = F16 && a.grad_x;
+  int problems = 0;
+  if (a.grad_x || a.grad_a)  // g = scale * grad b
+    g.prob[problems++] = {a.grad, a.N, a.N, a.b, F16 && !a.grad_a ? nullptr : d.h, scaled ? d.h16 : nullptr,
+                          scaled ? d.row_scale : nullptr, 1,
+                          (aligned16(a.grad, a.N * size) ? 1 : 0) | (aligned16(a.b, a.r * size) ? 2 : 0)};
+  if (a.grad_b)  // h = scale * x a^T
+    g.prob[problems++] = {a.x, a.K, a.K, a.a, h.h, nullptr, nullptr, 0,
+                          (aligned16(a.x, a.K * size) ? 1 : 0) | (aligned16(a.a, a.K * size) ? 2 : 0)};
+  cudaError_t e = run_down<T>(g, problems, s);
+  // the weights' gradients first: they read x and grad again, some of which L2 still has
+  if (e == cudaSuccess && (a.grad_a || a.grad_b)) e = run_grads<T>(a, g.R, h.h, d.h, s);
+  if (e == cudaSuccess && a.grad_x) {
+    UpArgs up = {scaled ? d.row_scale : nullptr, a.a, a.base, a.grad_x, a.offsets, a.order, a.T, a.K, a.L, a.r, g.R};
+    up.turned = 1;
+    e = run_up<T>(up, scaled ? d.h16 : d.h, s);
+  }
+  return e;
 }
 
 }  // namespace

@@ -117,11 +117,12 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& a, int64_t first, 
 // What a cluster's CTAs have summed for sequence s (sums and counts [E] of each, in its
 // shared memory), in the order of the CTAs: counts and loss, by CTA 0.  All threads of the
 // cluster; n tokens.
+template <int THREADS = kThreads>
 __device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, int C, int rank, const Sum* sums,
                                        const int32_t* count, Sum* gathered, int32_t* counts) {
-  __shared__ double loss[kWarps];
+  __shared__ double loss[THREADS / 32];
   const int E = a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < E; e += kThreads) {
+  for (int e = threadIdx.x; e < E; e += THREADS) {
     const uint32_t at = ptx::cluster_addr(gathered + rank * E + e, 0);
     ptx::st_cluster(at, __float_as_uint(sums[e].hi));
     ptx::st_cluster(at + 4, __float_as_uint(sums[e].lo));
@@ -130,7 +131,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, i
   ptx::cluster_sync();
   if (rank) return;
   double part = 0.0;
-  for (int e = threadIdx.x; e < E; e += kThreads) {
+  for (int e = threadIdx.x; e < E; e += THREADS) {
     Sum sum = {0.0f, 0.0f};
     int32_t c = 0;
     for (int q = 0; q < C; ++q) {
@@ -147,7 +148,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, i
   if (threadIdx.x == 0) {
     double sum = 0.0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += loss[w];
+    for (int w = 0; w < THREADS / 32; ++w) sum += loss[w];
     a.loss[s] = n > 0 ? (float)(sum * E / ((double)a.k * n * n)) : 0.0f;
   }
 }
@@ -226,7 +227,8 @@ __global__ void __launch_bounds__(kThreads) k_balance_chunks(const BalanceArgs a
   }
 }
 // ... and a cluster per sequence that joins its rows.
-__global__ void __launch_bounds__(kThreads)
+constexpr int kJoin = 1024;
+__global__ void __launch_bounds__(kJoin)
     k_balance_join(const BalanceArgs a, const int chunk, const int chunks, const int log_ctas) {
   extern __shared__ Sum sm_sums[];  // [E], then (CTA 0) [CTA][E]
   __shared__ Sum part_sums[1024];
@@ -246,8 +248,8 @@ __global__ void __launch_bounds__(kThreads)
   const int per = (c1 - c0 + C - 1) >> log_ctas;
   const int from = min(c0 + rank * per, c1), to = min(from + per, c1);
   // the threads are `parts` groups of E or more, group p of which takes every parts-th row
-  const int parts = E <= kThreads / 2 ? kThreads / E : 1, p = parts > 1 ? threadIdx.x / E : 0;
-  for (int e = threadIdx.x - p * E; e < E && p < parts; e += kThreads) {
+  const int parts = E <= kJoin / 2 ? kJoin / E : 1, p = parts > 1 ? threadIdx.x / E : 0;
+  for (int e = threadIdx.x - p * E; e < E && p < parts; e += kJoin) {
     Sum sum = {0.0f, 0.0f};
     int32_t n = 0;
 #pragma unroll 8
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kThreads)
     part_counts[p * E + e] = n;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kThreads) {
+  for (int e = threadIdx.x; e < E; e += kJoin) {
     Sum sum = part_sums[e];
     int32_t n = part_counts[e];
     for (int q = 1; q < parts; ++q) {
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads)
     count[e] = n;
   }
   ptx::cluster_wait();
-  finish(a, s, t1 - t0, C, rank, sm_sums, count, gathered, count + E);
+  finish<kJoin>(a, s, t1 - t0, C, rank, sm_sums, count, gathered, count + E);
 }
 
 // A warp per token.  With u_e = grad_loss[s] * E / (k n^2) * c[s,e], the counts constant,
@@ -375,13 +377,15 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
 
 // ------------------------------------------------------------------- host
 // Tokens of a CTA of the form for many of them (whatever the GPU: the workspace's size
-// depends on it): 512 to 1023 CTAs, of sixteen tokens at least.
+// depends on it): 257 to 512 CTAs, of sixteen tokens at least.
 int64_t chunk_of(int64_t T) {
   int64_t chunk = 16;
-  while (ceil_div(T, chunk) > 1023) chunk *= 2;
+  while (ceil_div(T, chunk) > 512) chunk *= 2;
   return chunk;
 }
-bool many(int64_t T, int64_t S) { return T > 2048 && S <= 1024; }
+// The form in chunks takes two launches (us, one sequence of 64 experts, with it / without:
+// 512 tokens 8.7 / 6.6, 2048 9.0 / 16.8).
+bool many(int64_t T, int64_t S) { return T > 768 && S <= 1024; }
 
 template <int VPT, typename T>
 cudaError_t forward(const BalanceArgs& a, cudaStream_t s) {
@@ -397,7 +401,7 @@ cudaError_t forward(const BalanceArgs& a, cudaStream_t s) {
       launch_clusters<k_balance_chunks<VPT, T>>(dim3(chunks), 1, kThreads, E * (kWarps * 8 + 4), s, a, chunk);
   if (e != cudaSuccess) return e;
   const int log_ctas = chunks / a.S >= 16 ? 3 : 0, C = 1 << log_ctas;
-  return launch_clusters<k_balance_join>(dim3((unsigned)a.S << log_ctas), C, kThreads, E * (1 + C) * 12, s, a, chunk,
+  return launch_clusters<k_balance_join>(dim3((unsigned)a.S << log_ctas), C, kJoin, E * (1 + C) * 12, s, a, chunk,
                                          chunks, log_ctas);
 }
 
