@@ -62,6 +62,37 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int L, bool
   __syncthreads();
   return found;
 }
+// All tiles of the buckets 0 .. B - 1: first [B + 1], the buckets' first places, and before
+// [B + 1], the tiles before each.  All threads of the block; ends with a barrier.
+template <int THREADS>
+__device__ __forceinline__ void count_tiles(const int32_t* offsets, int B, int height, int* first, int* before,
+                                            int* sums) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (B + THREADS - 1) / THREADS, e0 = tid * per;
+  int tiles = 0;
+  for (int e = e0; e < e0 + per && e < B; ++e) {
+    const int at = __ldg(offsets + e);
+    first[e] = at;
+    tiles += (__ldg(offsets + e + 1) - at + height - 1) / height;
+  }
+  if (tid == 0) first[B] = __ldg(offsets + B);
+  int upto = tiles;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(kAll, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += sums[w];
+  int at = upto - tiles;
+  for (int e = e0; e < e0 + per && e < B; ++e) {
+    before[e] = at;
+    at += (__ldg(offsets + e + 1) - first[e] + height - 1) / height;
+  }
+  if (tid == THREADS - 1) before[B] = upto;
+  __syncthreads();
+}
 // At least as many tiles as any distribution of T rows over the buckets has.
 int64_t most_tiles(int64_t T, int64_t L, int height) {
   const int64_t buckets = T < L + 1 ? T : L + 1;
@@ -1059,31 +1090,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
   const T* base = static_cast<const T*>(g.base);
   T* out = static_cast<T*>(g.out);
   const int B = g.L + (g.base != g.out ? 1 : 0);  // rows without an adapter: copied, or left
-  {
-    const int per = (B + THREADS - 1) / THREADS, e0 = tid * per;
-    int tiles = 0;
-    for (int e = e0; e < e0 + per && e < B; ++e) {
-      const int first = __ldg(g.offsets + e);
-      ctl.first[e] = first;
-      tiles += (__ldg(g.offsets + e + 1) - first + TILE - 1) / TILE;
-    }
-    if (tid == 0) ctl.first[B] = __ldg(g.offsets + B);
-    int upto = tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(kAll, upto, d);
-      if (lane >= d) upto += o;
-    }
-    if (lane == 31) ctl.sums[warp] = upto;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) upto += ctl.sums[w];
-    int at = upto - tiles;
-    for (int e = e0; e < e0 + per && e < B; ++e) {
-      ctl.before[e] = at;
-      at += (__ldg(g.offsets + e + 1) - ctl.first[e] + TILE - 1) / TILE;
-    }
-    if (tid == THREADS - 1) ctl.before[B] = upto;
-  }
+  count_tiles<THREADS>(g.offsets, B, TILE, ctl.first, ctl.before, ctl.sums);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -1654,14 +1661,22 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   tear_down(ctl, tmem, g.cols);
 }
 
-// The same for bf16 rows that TMA can load.
+// The same for bf16 rows that TMA can load, with equal shares however the rows are spread
+// over the adapters: a cluster has 128 columns for all adapters, and its CTAs equal runs of
+// the blocks of 64 rows, counted over the adapters one after the other.  Two accumulators:
+// the next adapter's MMAs run while one's sums are written.  An adapter that lies within a
+// run is that CTA's to write; one that several runs share (a run has two such at most) is
+// summed at the end, in the order of the CTAs, each taking a part of its gradient.  8192 rows
+// of 8 adapters, r 16, 4096 x 4096, an adapter's rows to each cluster: us for
 struct GradMaps {
   CUtensorMap x[2], rows[2], h[2], h_rows[2];  // of each problem, by 64 rows and by rows
 };
 struct GradCtl {
-  uint64_t full[DOWN_STAGES], empty[DOWN_STAGES], accf, drain;
+  uint64_t full[DOWN_STAGES], empty[DOWN_STAGES], accf[2], acce[2], drain;
   uint32_t tmem_base;
   int abort;
+  int sums[16];
+  int before[kAdapters + 2], first[kAdapters + 2];  // row blocks before an adapter, its first row
 };
 
 __global__ void __launch_bounds__(DOWN_THREADS)
@@ -1671,48 +1686,75 @@ __global__ void __launch_bounds__(DOWN_THREADS)
   extern __shared__ uint8_t sm_raw[];
   __shared__ GradCtl ctl;
   uint8_t* sm = tc::smem_align1024(sm_raw);
-  const GradProblem& p = g.prob[blockIdx.z];
+  const GradProblem& p = g.prob[blockIdx.y];
   const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank(), S = g.stages;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R, r = g.r, L = g.L;
   const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * GRAD_COLS;
-  const int l = blockIdx.y;
+  const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
   int* wd = &g_watchdog_adapters;
-  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 2, ctl.full, g.cols);
+  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 5, ctl.full, g.cols);
+  if (left <= 0) {  // the whole cluster (the problems may have different numbers of columns)
+    ptx::griddep_wait();
+    tear_down(ctl, tmem, g.cols);
+    return;
+  }
   ptx::griddep_wait();
   ptx::griddep_launch();
-  const bool work = col0 < p.cols;
-  const int first = __ldg(g.offsets + l), rows = __ldg(g.offsets + l + 1) - first;
-  const int blocks = (rows + GRAD_ROWS - 1) / GRAD_ROWS, per = (blocks + C - 1) >> g.log_ctas;
-  const int b0 = min(rank * per, blocks), b1 = work ? min(b0 + per, blocks) : b0;
+  count_tiles<DOWN_THREADS>(g.offsets, L, GRAD_ROWS, ctl.first, ctl.before, ctl.sums);
+  const int blocks = ctl.before[L];
+  auto run_of = [&](int q) { return (int)((int64_t)blocks * q >> g.log_ctas); };
+  const int b0 = run_of(rank), b1 = run_of(rank + 1);
   const int hb = grad_h_bytes(PH * R), stage_bytes = XG + hb;
-  const int boxes = col0 + 64 < p.cols ? 2 : 1;  // of 64 columns
+  const int boxes = left > 64 ? 2 : 1;  // of 64 columns
+  const int pitch = R + 1;
+  float* head = reinterpret_cast<float*>(sm + S * stage_bytes);  // sums of the run's first adapter
+  float* tail = reinterpret_cast<float*>(sm);                    // of its last, when the ring is done
+  // the adapter of row block b
+  auto adapter_of = [&](int b) {
+    int low = 0, high = L;  // before[low] <= b < before[high]
+    while (high - low > 1) {
+      const int mid = (low + high) >> 1;
+      if (ctl.before[mid] <= b) low = mid;
+      else high = mid;
+    }
+    return low;
+  };
+  T* out = static_cast<T*>(p.out);
   if (warp == 0) {
-    const void *mx = &maps.x[blockIdx.z], *mr = &maps.rows[blockIdx.z], *mh = &maps.h[blockIdx.z],
-               *mhr = &maps.h_rows[blockIdx.z];
-    // this lane's two rows of a block, the next block's asked for early; past the end: a
-    // row that the tensors do not have, which reads zeros
-    auto row_of = [&](int b, int i) {
-      const int in = b * GRAD_ROWS + i;
-      return b < b1 && in < rows ? __ldg(g.order + first + in) : (int)g.T;
+    const void *mx = &maps.x[blockIdx.y], *mr = &maps.rows[blockIdx.y], *mh = &maps.h[blockIdx.y],
+               *mhr = &maps.h_rows[blockIdx.y];
+    // a block's place and rows, this lane's two of them asked for a block early; past the
+    // adapter's end: a row that the tensors do not have, which reads zeros
+    struct {
+      int l = -1, place = 0, have = 0, r0 = 0, r1 = 0;
+    } now, next;
+    auto look = [&](int b) {
+      next.l = now.l;
+      if (next.l < 0) next.l = adapter_of(b);
+      while (ctl.before[next.l + 1] <= b) ++next.l;
+      next.place = ctl.first[next.l] + (b - ctl.before[next.l]) * GRAD_ROWS;
+      next.have = min(GRAD_ROWS, ctl.first[next.l + 1] - next.place);
+      next.r0 = lane < next.have ? __ldg(g.order + next.place + lane) : (int)g.T;
+      next.r1 = lane + 32 < next.have ? __ldg(g.order + next.place + lane + 32) : (int)g.T;
     };
-    int r0 = row_of(b0, lane), r1 = row_of(b0, lane + 32);
-    int b = b0;
+    if (b0 < b1) look(b0);
     Slot ring;
+    int b = b0;
     for (; b < b1; ++b, ring.next(S)) {
       const int slot = ring.i;
-      const int n0 = row_of(b + 1, lane), n1 = row_of(b + 1, lane + 32);
-      const int at = __shfl_sync(kAll, r0, 0), have = min(GRAD_ROWS, rows - b * GRAD_ROWS);
-      const bool run = have == GRAD_ROWS && __all_sync(kAll, r0 == at + lane && r1 == at + 32 + lane);
+      now = next;
+      if (b + 1 < b1) look(b + 1);
+      const int at = __shfl_sync(kAll, now.r0, 0);
+      const bool run = now.have == GRAD_ROWS && __all_sync(kAll, now.r0 == at + lane && now.r1 == at + 32 + lane);
       if (ring.round > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (ring.round - 1) & 1, &ctl.abort, 4, wd)) break;
       uint8_t* to = sm + slot * stage_bytes;
       uint64_t* bar = &ctl.full[slot];
-      const int place = first + b * GRAD_ROWS;
       if (lane == 0) {
         ptx::mbar_arrive_expect_tx(bar, boxes * (XG / 2) + hb);
         if (run)
           for (int c = 0; c < boxes; ++c) ptx::tma_load_2d(to + c * (XG / 2), mx, bar, (int)col0 + c * 64, at);
-        if (have == GRAD_ROWS)
-          for (int j = 0; j < PH * R; j += 64) ptx::tma_load_2d(to + XG + j * 128, mh, bar, j, place);
+        if (now.have == GRAD_ROWS)
+          for (int j = 0; j < PH * R; j += 64) ptx::tma_load_2d(to + XG + j * 128, mh, bar, j, now.place);
       }
       __syncwarp();
       if (!run) {  // sixteen lanes, four rows each
@@ -1720,53 +1762,144 @@ __global__ void __launch_bounds__(DOWN_THREADS)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int from = lane * 4 + e;
-          const int lo = __shfl_sync(kAll, r0, from & 31), hi = __shfl_sync(kAll, r1, from & 31);
+          const int lo = __shfl_sync(kAll, now.r0, from & 31), hi = __shfl_sync(kAll, now.r1, from & 31);
           q[e] = from & 32 ? hi : lo;
         }
         if (lane < 16)
           for (int c = 0; c < boxes; ++c)
             ptx::tma_gather4(to + c * (XG / 2) + lane * 512, mr, bar, (int)col0 + c * 64, q[0], q[1], q[2], q[3]);
       }
-      if (have < GRAD_ROWS && lane < 16) {
+      if (now.have < GRAD_ROWS && lane < 16) {
         int q[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q[e] = lane * 4 + e < have ? place + lane * 4 + e : (int)g.T;
+        for (int e = 0; e < 4; ++e) q[e] = lane * 4 + e < now.have ? now.place + lane * 4 + e : (int)g.T;
         for (int j = 0; j < PH * R; j += 64)
           ptx::tma_gather4(to + XG + j * 128 + lane * 512, mhr, bar, j, q[0], q[1], q[2], q[3]);
       }
       __syncwarp();
-      r0 = n0;
-      r1 = n1;
     }
     if (ctl.abort)  // the copies under way land before the block ends
       for (int i = b - b0 > S ? b - b0 - S : 0; i < b - b0; ++i) tc::drain_wait(&ctl.full[i % S], (i / S) & 1);
   } else if (warp == 1) {
     const uint32_t id = ptx::idesc_f16(1, GRAD_COLS, PH * R, true, true);
-    Slot ring;
+    Slot ring, acc;
+    int l = b0 < b1 ? adapter_of(b0) : 0, end = 0;
     for (int b = b0; b < b1; ++b, ring.next(S)) {
       const int slot = ring.i;
+      const bool fresh = b >= end;  // the first block of an adapter's segment
+      if (fresh) {
+        while (ctl.before[l + 1] <= b) ++l;
+        end = min(ctl.before[l + 1], b1);
+        if (acc.round > 0 && !tc::warp_wait_bar(&ctl.acce[acc.i], (acc.round - 1) & 1, &ctl.abort, 15, wd)) break;
+      }
       if (!tc::warp_wait_bar(&ctl.full[slot], ring.round & 1, &ctl.abort, 14, wd)) break;
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         const uint32_t xa = ptx::smem_addr(sm + slot * stage_bytes), ha = xa + XG;
 #pragma unroll
         for (int ks = 0; ks < GRAD_ROWS / 16; ++ks)
-          ptx::mma_f16(tmem, ptx::smem_desc(xa + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B),
+          ptx::mma_f16(tmem + acc.i * PH * R, ptx::smem_desc(xa + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B),
                        ptx::smem_desc(ha + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B), id,
-                       b > b0 || ks > 0);
+                       !fresh || ks > 0);
         ptx::mma_commit(&ctl.empty[slot]);
-        if (b + 1 == b1) ptx::mma_commit(&ctl.accf);
+        if (b + 1 == end) ptx::mma_commit(&ctl.accf[acc.i]);
       }
       __syncwarp();
+      if (b + 1 == end) acc.next(2);
     }
   } else {
-    if (b1 > b0) tc::warp_wait_bar(&ctl.accf, 0, &ctl.abort, 5, wd);
-    ptx::tc_fence_after();
-    if (work) grad_sums<PH>(sm, tmem, R, b1 > b0, 0, 1);
+    // a thread has a column's sums
+    const int col = (warp & 3) * 32 + lane;
+    const bool vec = r == R && (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    Slot acc;
+    int l = b0 < b1 ? adapter_of(b0) : 0;
+    for (int b = b0; b < b1;) {
+      while (ctl.before[l + 1] <= b) ++l;
+      const int end = min(ctl.before[l + 1], b1);
+      const bool begins = ctl.before[l] >= b0, ends = ctl.before[l + 1] <= b1;
+      if (!tc::warp_wait_bar(&ctl.accf[acc.i], acc.round & 1, &ctl.abort, 5, wd)) break;
+      ptx::tc_fence_after();
+      const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc.i * PH * R;
+      T* to = out + (int64_t)l * r * p.cols;
+      for (int j = 0; j < R; j += 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < PH; ++c) {
+          uint32_t w[16];
+          ptx::tmem_ld16(from + c * R + j, w);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(w[i]);
+        }
+        if (!begins || !ends) {
+          float* part = (begins ? tail : head) + col * pitch + j;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[i] = v[i];
+        } else if (col < left) {
+          if (!p.turned) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (j + i < r) to[(int64_t)(j + i) * p.cols + col0 + col] = from_f32<T>(v[i]);
+          } else {
+            float lo[8], hi[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) lo[i] = v[i], hi[i] = v[8 + i];
+            T* at = to + (col0 + col) * r + j;
+            store8<T>(at, r - j, vec, lo);
+            store8<T>(at + 8, r - j - 8, vec, hi);
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      tc::epi_sync();  // (the barrier counts one arrival)
+      if (tid == 64) ptx::mbar_arrive(&ctl.acce[acc.i]);
+      acc.next(2);
+      b = end;
+    }
   }
   __syncwarp();
   ptx::cluster_sync();
-  if (work) grad_out<T, DOWN_THREADS>(sm, g, p, l, rank, col0);
+  // ---- the shared adapters: the run's first, if it began before; its last, if it goes on
+  if (b0 < b1) {
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const int l = adapter_of(which ? b1 - 1 : b0);
+      const int begin = ctl.before[l], end = ctl.before[l + 1];
+      const bool begins = begin >= b0, ends = end <= b1;
+      if (which ? !begins || ends : begins) continue;
+      int ra = rank, rb = rank;  // the CTAs that share it
+      while (ra > 0 && run_of(ra) > begin) --ra;
+      while (rb + 1 < C && run_of(rb + 1) < end) ++rb;
+      int sharers = 0, before = 0;  // without those that have no row blocks
+      for (int q = ra; q <= rb; ++q)
+        if (run_of(q) < run_of(q + 1)) {
+          ++sharers;
+          before += q < rank ? 1 : 0;
+        }
+      const int n = left * r, share = (n + sharers - 1) / sharers, e0 = before * share, e1 = min(e0 + share, n);
+      for (int e = e0 + tid; e < e1; e += DOWN_THREADS) {
+        const int col = p.turned ? e / r : e % left, j = p.turned ? e - col * r : e / left;
+        float sum = 0.0f;
+        for (int q = ra; q <= rb; ++q) {
+          if (run_of(q) == run_of(q + 1)) continue;  // (no row blocks)
+          sum += __uint_as_float(ptx::ld_cluster(ptx::cluster_addr((q == ra ? tail : head) + col * pitch + j, q)));
+        }
+        out[(int64_t)l * r * p.cols + (p.turned ? (col0 + col) * r + j : (int64_t)j * p.cols + col0 + col)] =
+            from_f32<T>(sum);
+      }
+    }
+  }
+  // ---- adapters without rows: zeros
+  for (int l = rank; l < L; l += C) {
+    if (ctl.first[l + 1] > ctl.first[l]) continue;
+    for (int e = tid; e < left * r; e += DOWN_THREADS) {
+      const int col = p.turned ? e / r : e % left, j = p.turned ? e - col * r : e / left;
+      out[(int64_t)l * r * p.cols + (p.turned ? (col0 + col) * r + j : (int64_t)j * p.cols + col0 + col)] =
+          from_f32<T>(0.0f);
+    }
+  }
   ptx::cluster_sync();  // no CTA ends while another reads its sums
   tear_down(ctl, tmem, g.cols);
 }
@@ -1786,8 +1919,8 @@ int tmem_cols(int need) {
 // that share of the SM's 228 KB.  Blocks that fit on an SM together then find their tensor
 // memory too, so none waits for it inside a cluster whose other blocks hold theirs on an SM
 // where another cluster's block waits.
-size_t smem_for(size_t bytes, int cols) {
-  const size_t share = (size_t)(228 << 10) * cols / 512 - 1024, most = 232448 - 2048;
+size_t smem_for(size_t bytes, int cols, size_t fixed = 2048) {  // fixed: static shared memory, at most
+  const size_t share = (size_t)(228 << 10) * cols / 512 - 1024, most = 232448 - fixed;
   bytes = bytes > share ? bytes : share;
   return bytes < most ? bytes : most;
 }
@@ -2066,11 +2199,18 @@ cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const 
           return cudaErrorInvalidValue;
       }
       const int stage = GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R), sums = GRAD_COLS * (w.R + 1) * 4;
-      w.stages = (104 << 10) / stage < DOWN_STAGES ? (104 << 10) / stage : DOWN_STAGES;
-      const int bytes = w.stages * stage > sums ? w.stages * stage : sums;
-      w.cols = tmem_cols(PL::PH * w.R);
-      return launch_clusters<k_adapters_grad_tma>(dim3((unsigned)(chunks << w.log_ctas), a.L, parts), 1 << w.log_ctas,
-                                                  DOWN_THREADS, smem_for((size_t)bytes + 1024, w.cols), s, maps, w);
+      // two blocks per SM where three stages and a set of sums fit in half of it
+      const int fixed = (int)(sizeof(GradCtl) + 1023) / 1024 * 1024 + 256;  // static shared memory
+      const int half = (114 << 10) - 1024 - fixed - 1024, most = 232448 - fixed - 1024;
+      const int room = 3 * stage + sums <= half ? half : most;
+      w.stages = (room - sums) / stage < DOWN_STAGES ? (room - sums) / stage : DOWN_STAGES;
+      while (w.stages * stage < sums) ++w.stages;  // (the ring holds a set of sums, too, in the end)
+      w.cols = tmem_cols(2 * PL::PH * w.R);
+      const int64_t blocks = ceil_div(a.T, GRAD_ROWS), per_chunk = (room == half ? 2 : 1) * (int64_t)device_sm_count() / all;
+      const int64_t ctas = per_chunk < blocks ? per_chunk : blocks;
+      w.log_ctas = ctas >= 8 ? 3 : (ctas >= 4 ? 2 : (ctas >= 2 ? 1 : 0));
+      return launch_clusters<k_adapters_grad_tma>(dim3((unsigned)(chunks << w.log_ctas), parts), 1 << w.log_ctas, DOWN_THREADS,
+                                                  smem_for((size_t)w.stages * stage + sums + 1024, w.cols, fixed), s, maps, w);
     }
   }
   const size_t ring = (size_t)PL::GRAD_STAGES * (PL::P * GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R));

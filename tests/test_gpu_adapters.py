@@ -353,3 +353,19 @@ def test_refused_by_the_torch_level():
         call(c.x, a, torch.zeros(2, 8, 129, device="cuda"), c.layout)
     with pytest.raises(ValueError):
         binding.adapters_linear_backward(c.grad[:, :4], c.x, c.a, c.b, c.layout)
+
+
+@pytest.mark.parametrize("rows", [[5000], [0, 3000, 0, 0, 1], [64, 64, 64, 64, 64, 64], [1] * 40, [2, 700, 63, 65, 0, 128, 1500, 9],
+                                  [640, 0, 1], [127, 130], [65]])
+@pytest.mark.parametrize("r", [8, 40, 128])
+def test_gradients_of_unequal_adapters(rows, r):
+    """Adapters whose rows fill several blocks' runs, parts of them or none, in any order."""
+    L, T = len(rows), sum(rows) + 3
+    c = Case(T + r, T, L, r, 264, 392, torch.bfloat16)
+    which = torch.cat([torch.full((n,), l) for l, n in enumerate(rows)] + [torch.full((3,), -1)])
+    for order in (torch.arange(T), torch.randperm(T, generator=torch.Generator().manual_seed(T))):
+        c.which = which[order].to(torch.int32).cuda()
+        c.layout = binding.experts_layout(c.which[:, None].contiguous(), L)
+        for got, (want, tol) in zip(c.backward(), c.backward64()):
+            within(got, want, tol, c.dtype)
+    assert binding.check_device_error(None) == binding.IMC_OK
