@@ -622,10 +622,12 @@ struct Slot {
 
 // Barriers and tensor memory of a block.  The memory is taken before the stream's next
 // kernel may start: a block of that one that had it would wait for this kernel's end.
+// The first `loaded` barriers take that many arrivals a phase, the others one.
 template <typename Ctl>
-__device__ __forceinline__ uint32_t set_up(Ctl& ctl, int barriers, uint64_t* bars, int cols) {
+__device__ __forceinline__ uint32_t set_up(Ctl& ctl, int barriers, uint64_t* bars, int cols, int loaded = 0,
+                                           int arrivals = 1) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < barriers; ++i) ptx::mbar_init(bars + i, 1);
+    for (int i = 0; i < barriers; ++i) ptx::mbar_init(bars + i, i < loaded ? arrivals : 1);
     ctl.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -681,8 +683,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     if (tid < TILE) rows[tid] = tid < t.rows ? g.order[t.p0 + tid] : -1;
     __syncthreads();
     const int stage_bytes = P * XP + down_w_bytes(P * R);
-    const int blocks = (int)ceil_div(p.K, KB), per = (blocks + C - 1) >> g.log_ctas;
-    const int b0 = min(rank * per, blocks), b1 = min(b0 + per, blocks);
+    // every C-th block of K is this CTA's: what the cluster reads at one time lies together
+    const int blocks = (int)ceil_div(p.K, KB), b0 = 0, b1 = (blocks - rank + C - 1) >> g.log_ctas;
+    auto k_of = [&](int b) { return ((b << g.log_ctas) + rank) * KB; };
     const T* w = static_cast<const T*>(p.w) + (int64_t)t.l * r * p.K;
     const int u = tid & 7;
     const T* xr[4];
@@ -711,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       return p.turned ? w + (k + wk[i]) * r + wj[i] : w + wj[i] * p.K + k + wk[i];
     };
     auto fetch = [&](int b) {
-      const int64_t k = (int64_t)b * KB;
+      const int64_t k = k_of(b);
       const int left = (int)(p.K - k < KB ? p.K - k : KB);
       if (!ASYNC) {
 #pragma unroll
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       }
     };
     auto put = [&](int b, uint8_t* to) {
-      const int64_t k = (int64_t)b * KB;
+      const int64_t k = k_of(b);
       const int left = (int)(p.K - k < KB ? p.K - k : KB);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -832,13 +835,47 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
   tear_down(ctl, tmem, g.cols);
 }
 
-// The same for 16-bit rows that TMA can load: one warp issues the loads (a box for 32
-// rows that lie one after the other, four rows at a time where they do not), one the
-// MMAs, and nothing passes through registers.  8192 rows, 8 adapters, r 32, K 4096: us
-// with / without.
+// The same for 16-bit rows that 16-byte copies can reach, without a barrier of the whole block
+// in the loop: four warps load 32 rows of x each, by TMA where they lie one after the other
+// and by asynchronous copies where they do not (TMA takes ~130 cycles to issue four rows as
+// well as a box), one has TMA load w, one issues the MMAs, and nothing passes through registers.
 constexpr int DOWN_THREADS = 192, DOWN_STAGES = 8;
 struct DownMaps {
-  CUtensorMap x[2], rows[2], w[2];  // of each problem: x by tiles, by rows; w
+  CUtensorMap x[2], w[2];  // of each problem, x by 32 rows
+};
+// A warp's asynchronous copies to a ring of S stages: each stage's barrier gets the warp's
+// arrival when its copies have landed, AHEAD stages later.
+struct Landing {
+  Slot late;
+  int behind = 0;
+  const int ahead;
+  __device__ explicit Landing(int S) : ahead(S > 3 ? 3 : 2) {}
+  __device__ __forceinline__ void arrive(uint64_t* full, int S) {
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(full + late.i);
+    late.next(S);
+  }
+  // after the copies to one more stage
+  __device__ __forceinline__ void next(uint64_t* full, int S) {
+    ptx::copy_commit();
+    if (behind < ahead) {
+      ++behind;
+      return;
+    }
+    if (ahead == 3) ptx::copy_wait<3>();
+    else ptx::copy_wait<2>();
+    arrive(full, S);
+  }
+  __device__ __forceinline__ void finish(uint64_t* full, int S) {
+    ptx::copy_wait<0>();
+    for (; behind > 0; --behind) arrive(full, S);
+  }
+  // a stage that the warp arrives at by itself
+  __device__ __forceinline__ void skip(uint64_t* full, int S) {
+    if (behind) finish(full, S);
+    late.next(S);
+  }
 };
 struct DownCtl {
   uint64_t full[DOWN_STAGES], empty[DOWN_STAGES], accf, drain;
@@ -852,13 +889,13 @@ __global__ void __launch_bounds__(DOWN_THREADS)
   using PL = Planes<T>;
   extern __shared__ uint8_t sm_raw[];
   __shared__ DownCtl ctl;
-  __shared__ __align__(16) int rows[TILE];
+  __shared__ int rows[TILE];
   uint8_t* sm = tc::smem_align1024(sm_raw);
   const DownProblem& p = g.prob[blockIdx.y];
   const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank(), S = g.stages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R;
   int* wd = &g_watchdog_adapters;
-  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 2, ctl.full, g.cols);
+  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 2, ctl.full, g.cols, DOWN_STAGES, 5);
   ptx::griddep_wait();
   ptx::griddep_launch();
   const RowTile t = find_tile<DOWN_THREADS>(g.offsets, g.L, false, TILE, blockIdx.x >> g.log_ctas);
@@ -867,40 +904,26 @@ __global__ void __launch_bounds__(DOWN_THREADS)
     if (tid < TILE) rows[tid] = g.order[t.p0 + min(tid, t.rows - 1)];
     __syncthreads();
     const int wb = p.turned ? down_w_bytes(R) : R * 128, stage_bytes = XP + down_w_bytes(R);
-    const int blocks = (int)ceil_div(p.K, KB), per = (blocks + C - 1) >> g.log_ctas;
-    const int b0 = min(rank * per, blocks), b1 = min(b0 + per, blocks);
+    // every C-th block of K is this CTA's: what the cluster reads at one time lies together
+    const int blocks = (int)ceil_div(p.K, KB), b0 = 0, b1 = (blocks - rank + C - 1) >> g.log_ctas;
+    auto k_of = [&](int b) { return ((b << g.log_ctas) + rank) * KB; };
     if (warp == 0) {
-      const void *mx = &maps.x[blockIdx.y], *mr = &maps.rows[blockIdx.y], *mw = &maps.w[blockIdx.y];
-      // lane 8 q + i has rows 4 i .. 4 i + 3 of quarter q
-      const int4 four = *reinterpret_cast<const int4*>(rows + lane * 4);
-      const int head = rows[(lane >> 3) * 32];
-      bool run = true;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = lane * 4 + i;
-        if (at < t.rows) run = run && rows[at] == head + (at & 31);
-      }
-      const uint32_t runs = __ballot_sync(kAll, run);
-      run = ((runs >> (lane & 24)) & 255u) == 255u;  // the quarter's rows lie one after the other
-      int b = b0;
+      const void* mw = &maps.w[blockIdx.y];
       Slot ring;
+      int b = b0;
       for (; b < b1; ++b, ring.next(S)) {
         const int slot = ring.i;
         if (ring.round > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (ring.round - 1) & 1, &ctl.abort, 1, wd)) break;
-        uint8_t* to = sm + slot * stage_bytes;
         if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&ctl.full[slot], XP + wb);
+          uint8_t* to = sm + slot * stage_bytes + XP;
+          ptx::mbar_arrive_expect_tx(&ctl.full[slot], wb);
           if (p.turned) {
-            for (int j = 0; j < R; j += 64) ptx::tma_load_3d(to + XP + j * 128, mw, &ctl.full[slot], j, b * KB, t.l);
+            for (int j = 0; j < R; j += 64) ptx::tma_load_3d(to + j * 128, mw, &ctl.full[slot], j, k_of(b), t.l);
           } else {
-            ptx::tma_load_3d(to + XP, mw, &ctl.full[slot], b * KB, 0, t.l);
+            ptx::tma_load_3d(to, mw, &ctl.full[slot], k_of(b), 0, t.l);
           }
         }
         __syncwarp();
-        if (!run)
-          ptx::tma_gather4(to + lane * 512, mr, &ctl.full[slot], b * KB, four.x, four.y, four.z, four.w);
-        else if ((lane & 7) == 0)
-          ptx::tma_load_2d(to + lane * 512, mx, &ctl.full[slot], b * KB, head);
       }
       if (ctl.abort)  // the copies under way land before the block ends
         for (int i = b - b0 > S ? b - b0 - S : 0; i < b - b0; ++i)
@@ -925,6 +948,40 @@ __global__ void __launch_bounds__(DOWN_THREADS)
         __syncwarp();
       }
     } else {
+      const int first = (warp - 2) * 32 + (lane >> 3), unit = lane & 7;
+      const T* from[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) from[i] = static_cast<const T*>(p.x) + rows[first + i * 4] * p.ld + unit * 8;
+      const int some = min(32, t.rows - (warp - 2) * 32);  // of these rows
+      const int head = rows[(warp - 2) * 32];
+      const bool run = some > 0 && __all_sync(kAll, lane >= some || rows[(warp - 2) * 32 + lane] == head + lane);
+      const void* mx = &maps.x[blockIdx.y];
+      Slot ring;
+      Landing land(S);
+      for (int b = b0; b < b1; ++b, ring.next(S)) {
+        const int slot = ring.i;
+        if (ring.round > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (ring.round - 1) & 1, &ctl.abort, 16, wd)) break;
+        const int k = k_of(b);
+        uint8_t* to = sm + slot * stage_bytes + first * 128;
+        if (run) {  // one box
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(&ctl.full[slot], 4096);
+            ptx::tma_load_2d(sm + slot * stage_bytes + (warp - 2) * 4096, mx, &ctl.full[slot], k, head);
+          }
+          __syncwarp();
+          continue;
+        }
+        const bool in = k + unit * 8 < p.K;  // K is a multiple of 8
+        if (some > 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = first + i * 4;
+            ptx::copy16(to + i * 512 + ((unit ^ (row & 7)) << 4), in ? from[i] + k : from[i] - unit * 8, in);
+          }
+        }
+        land.next(ctl.full, S);
+      }
+      if (!run) land.finish(ctl.full, S);
       if (b1 > b0) tc::warp_wait_bar(&ctl.accf, 0, &ctl.abort, 2, wd);
       ptx::tc_fence_after();
       own_sums<1>(sm, tmem, R, b1 > b0, 0, 1);
@@ -970,7 +1027,7 @@ struct UpArgs {
   int slots, h_slots, b_slots, w_bytes, h_bytes;  // of the rings of w, h and base; bytes of one
 };
 struct UpMaps {
-  CUtensorMap base, rows, out;  // base by 32 rows, by rows; out by 32 rows; 128 bytes of columns
+  CUtensorMap base, out;  // by 32 rows, 128 bytes of columns
   CUtensorMap h, w;             // a plane of 128 rows; 128 outputs (turned: 64) and r
 };
 constexpr int UP_EPI = 8;  // warps; beside them loaders and one for the MMAs
@@ -1047,9 +1104,9 @@ template <typename T>
 constexpr int STAGED_COLS = sizeof(T) == 2 ? 32 : 16;
 
 // Persistent blocks, each with an equal run of the (tile, 128 outputs) items:
-//   warps 0-7   epilogue: a warp has 32 rows and half of an item's columns: it asks TMA
-//               for its part of base some items ahead (a box, or four rows at a time where
-//               they do not lie one after the other), adds the product from tensor memory in
+//   warps 0-7   epilogue: a warp has 32 rows and half of an item's columns: it asks for
+//               its part of base some items ahead (a TMA box, or asynchronous copies where the
+//               rows do not lie one after the other), adds the product from tensor memory in
 //               place, rounds once, and has TMA store it (row by row itself where the box
 //               would reach other rows); without TMA (unaligned rows, no room) it adds
 //               column by column through shared memory
@@ -1267,26 +1324,38 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     Walk item = walk, next = walk;
     Slot nslot;
     auto load = [&] {  // base of the next item to its place in the ring
+      if (next.left <= 0) {
+        ptx::copy_commit();
+        return;
+      }
       place(ahead, next);
       next.next();
       const int slot = nslot.i;
       nslot.next(NS);
-      if (!base || ahead.rows == 0 || ahead.col >= g.N) return;
-      uint64_t* bar = &ctl.bfull[warp][slot];
-      uint8_t* to = ring + slot * SB;
-      const int boxes = ahead.col + BOX < g.N ? 64 / BOX : 1;
-      if (lane == 0) ptx::mbar_arrive_expect_tx(bar, boxes * 4096);
-      __syncwarp();
-      for (int b = 0; b < boxes; ++b) {
-        const int x = (int)ahead.col + b * BOX;
+      if (base && ahead.rows > 0 && ahead.col < g.N) {
+        uint8_t* to = ring + slot * SB;
+        const int boxes = ahead.col + BOX < g.N ? 64 / BOX : 1;
         if (ahead.run) {
-          if (lane == 0) ptx::tma_load_2d(to + b * 4096, &maps.base, bar, x, ahead.row);
-        } else {
-          const int r0 = __shfl_sync(kAll, ahead.row, (lane * 4) & 31), r1 = __shfl_sync(kAll, ahead.row, (lane * 4 + 1) & 31),
-                    r2 = __shfl_sync(kAll, ahead.row, (lane * 4 + 2) & 31), r3 = __shfl_sync(kAll, ahead.row, (lane * 4 + 3) & 31);
-          if (lane < 8) ptx::tma_gather4(to + b * 4096 + lane * 512, &maps.rows, bar, x, r0, r1, r2, r3);
+          uint64_t* bar = &ctl.bfull[warp][slot];
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(bar, boxes * 4096);
+            for (int b = 0; b < boxes; ++b)
+              ptx::tma_load_2d(to + b * 4096, &maps.base, bar, (int)ahead.col + b * BOX, ahead.row);
+          }
+        } else {  // four rows at a time, eight lanes each
+          const int unit = lane & 7;
+          for (int b = 0; b < boxes; ++b) {
+            const int64_t c = ahead.col + b * BOX + unit * (16 / (int)sizeof(T));
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const int at = i + (lane >> 3);
+              const int64_t row = __shfl_sync(kAll, ahead.row, at);
+              ptx::copy16(to + b * 4096 + at * 128 + ((unit ^ (at & 7)) << 4), c < g.N ? base + row * g.N + c : base, c < g.N);
+            }
+          }
         }
       }
+      ptx::copy_commit();  // (of every item, so that they can be counted)
     };
     const bool wide = g.vec & 2;
     float scale = 1.0f;  // of this lane's row of h; there once an accumulator is
@@ -1298,7 +1367,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     };
     uint32_t phases = 0;  // of the ring's barriers
     if (wide)
-      for (int i = 0; i < NS - 1 && next.left > 0; ++i) load();
+      for (int i = 0; i < NS - 1; ++i) load();
     Slot slot_of;
     for (; item.left > 0; item.next(), slot_of.next(NS)) {
       place(now, item);
@@ -1308,8 +1377,16 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
         const int slot = slot_of.i;
         uint8_t* mine = ring + slot * SB;
         if (base && live) {
-          if (!tc::warp_wait_bar(&ctl.bfull[warp][slot], phases >> slot & 1, &ctl.abort, 13, wd)) break;
-          phases ^= 1u << slot;
+          if (now.run) {
+            if (!tc::warp_wait_bar(&ctl.bfull[warp][slot], phases >> slot & 1, &ctl.abort, 13, wd)) break;
+            phases ^= 1u << slot;
+          } else if (NS == 4) {  // NS - 2 items have been asked for since
+            ptx::copy_wait<2>();
+          } else if (NS == 3) {
+            ptx::copy_wait<1>();
+          } else {
+            ptx::copy_wait<0>();
+          }
           __syncwarp();
         }
         if (product) {
@@ -1320,7 +1397,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
         // the item before this one has been stored: its place takes the next one to load
         if (lane == 0) ptx::bulk_wait_read0();
         __syncwarp();
-        if (next.left > 0) load();
+        load();
         if (live && (product || !base)) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -1430,10 +1507,11 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       if (ctl.abort) {  // the copies under way land before the block ends
         for (; item.left > next.left && base; item.next(), slot_of.next(NS)) {
           place(now, item);
-          if (now.rows == 0 || now.col >= g.N) continue;
+          if (now.rows == 0 || now.col >= g.N || !now.run) continue;
           tc::drain_wait(&ctl.bfull[warp][slot_of.i], phases >> slot_of.i & 1);
         }
       }
+      ptx::copy_wait<0>();
       if (lane == 0) ptx::bulk_wait_all();
       __syncwarp();
     }
@@ -1661,7 +1739,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   tear_down(ctl, tmem, g.cols);
 }
 
-// The same for bf16 rows that TMA can load, with equal shares however the rows are spread
+// The same for bf16 rows that 16-byte copies can reach, with equal shares however the rows are spread
 // over the adapters: a cluster has 128 columns for all adapters, and its CTAs equal runs of
 // the blocks of 64 rows, counted over the adapters one after the other.  Two accumulators:
 // the next adapter's MMAs run while one's sums are written.  An adapter that lies within a
@@ -1669,8 +1747,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 // summed at the end, in the order of the CTAs, each taking a part of its gradient.  8192 rows
 // of 8 adapters, r 16, 4096 x 4096, an adapter's rows to each cluster: us for
 struct GradMaps {
-  CUtensorMap x[2], rows[2], h[2], h_rows[2];  // of each problem, by 64 rows and by rows
+  CUtensorMap x[2], h[2];  // of each problem, by 64 rows
 };
+constexpr int GRAD_LOAD = 4, GRAD_THREADS = (GRAD_LOAD + 1 + 4) * 32;  // loaders, MMAs, epilogue
 struct GradCtl {
   uint64_t full[DOWN_STAGES], empty[DOWN_STAGES], accf[2], acce[2], drain;
   uint32_t tmem_base;
@@ -1679,8 +1758,8 @@ struct GradCtl {
   int before[kAdapters + 2], first[kAdapters + 2];  // row blocks before an adapter, its first row
 };
 
-__global__ void __launch_bounds__(DOWN_THREADS)
-    k_adapters_grad_tma(const __grid_constant__ GradMaps maps, const __grid_constant__ GradArgs g) {
+__global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __grid_constant__ GradMaps maps,
+                                                                          const __grid_constant__ GradArgs g) {
   using T = __nv_bfloat16;
   constexpr int PH = Planes<T>::PH, XG = GRAD_ROWS * GRAD_COLS * 2;
   extern __shared__ uint8_t sm_raw[];
@@ -1692,7 +1771,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
   const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * GRAD_COLS;
   const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
   int* wd = &g_watchdog_adapters;
-  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 5, ctl.full, g.cols);
+  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 5, ctl.full, g.cols, DOWN_STAGES, GRAD_LOAD);
   if (left <= 0) {  // the whole cluster (the problems may have different numbers of columns)
     ptx::griddep_wait();
     tear_down(ctl, tmem, g.cols);
@@ -1700,12 +1779,11 @@ __global__ void __launch_bounds__(DOWN_THREADS)
   }
   ptx::griddep_wait();
   ptx::griddep_launch();
-  count_tiles<DOWN_THREADS>(g.offsets, L, GRAD_ROWS, ctl.first, ctl.before, ctl.sums);
+  count_tiles<GRAD_THREADS>(g.offsets, L, GRAD_ROWS, ctl.first, ctl.before, ctl.sums);
   const int blocks = ctl.before[L];
   auto run_of = [&](int q) { return (int)((int64_t)blocks * q >> g.log_ctas); };
   const int b0 = run_of(rank), b1 = run_of(rank + 1);
   const int hb = grad_h_bytes(PH * R), stage_bytes = XG + hb;
-  const int boxes = left > 64 ? 2 : 1;  // of 64 columns
   const int pitch = R + 1;
   float* head = reinterpret_cast<float*>(sm + S * stage_bytes);  // sums of the run's first adapter
   float* tail = reinterpret_cast<float*>(sm);                    // of its last, when the ring is done
@@ -1720,67 +1798,80 @@ __global__ void __launch_bounds__(DOWN_THREADS)
     return low;
   };
   T* out = static_cast<T*>(p.out);
-  if (warp == 0) {
-    const void *mx = &maps.x[blockIdx.y], *mr = &maps.rows[blockIdx.y], *mh = &maps.h[blockIdx.y],
-               *mhr = &maps.h_rows[blockIdx.y];
-    // a block's place and rows, this lane's two of them asked for a block early; past the
-    // adapter's end: a row that the tensors do not have, which reads zeros
-    struct {
-      int l = -1, place = 0, have = 0, r0 = 0, r1 = 0;
-    } now, next;
-    auto look = [&](int b) {
-      next.l = now.l;
-      if (next.l < 0) next.l = adapter_of(b);
-      while (ctl.before[next.l + 1] <= b) ++next.l;
-      next.place = ctl.first[next.l] + (b - ctl.before[next.l]) * GRAD_ROWS;
-      next.have = min(GRAD_ROWS, ctl.first[next.l + 1] - next.place);
-      next.r0 = lane < next.have ? __ldg(g.order + next.place + lane) : (int)g.T;
-      next.r1 = lane + 32 < next.have ? __ldg(g.order + next.place + lane + 32) : (int)g.T;
+  if (warp < GRAD_LOAD) {
+    // A full block of rows that lie one after the other: a box of 64 columns of x by each of
+    // the first two warps, h by the third.  Else sixteen rows and their h by each warp, x two
+    // rows at a time; zeros past the adapter's end.  The rows' numbers (a lane has two) are
+    // asked for two blocks early.
+    const void *mx = &maps.x[blockIdx.y], *mh = &maps.h[blockIdx.y];
+    const int unit = lane & 15, hu = PH * R / 8, mine = warp * 16;
+    const int h_row = lane / hu, h_by = 32 / hu;
+    const T* x = static_cast<const T*>(p.x) + col0 + unit * 8;
+    const bool in_x = unit * 8 < left;
+    int l = b0 < b1 ? adapter_of(b0) : 0;
+    struct Rows {
+      int place, have, lo, hi;  // first place, rows, this lane's rows of the two halves
     };
-    if (b0 < b1) look(b0);
+    auto rows_of = [&](int b) {
+      Rows q = {0, 0, -1, -1};
+      if (b >= b1) return q;
+      while (ctl.before[l + 1] <= b) ++l;
+      q.place = ctl.first[l] + (b - ctl.before[l]) * GRAD_ROWS;
+      q.have = min(GRAD_ROWS, ctl.first[l + 1] - q.place);
+      if (lane < q.have) q.lo = __ldg(g.order + q.place + lane);
+      if (lane + 32 < q.have) q.hi = __ldg(g.order + q.place + lane + 32);
+      return q;
+    };
+    Rows now = rows_of(b0), next = rows_of(b0 + 1);
     Slot ring;
-    int b = b0;
-    for (; b < b1; ++b, ring.next(S)) {
+    Landing land(S);
+    for (int b = b0; b < b1; ++b, ring.next(S)) {
       const int slot = ring.i;
-      now = next;
-      if (b + 1 < b1) look(b + 1);
-      const int at = __shfl_sync(kAll, now.r0, 0);
-      const bool run = now.have == GRAD_ROWS && __all_sync(kAll, now.r0 == at + lane && now.r1 == at + 32 + lane);
+      const Rows after = rows_of(b + 2);
       if (ring.round > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (ring.round - 1) & 1, &ctl.abort, 4, wd)) break;
       uint8_t* to = sm + slot * stage_bytes;
       uint64_t* bar = &ctl.full[slot];
-      if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(bar, boxes * (XG / 2) + hb);
-        if (run)
-          for (int c = 0; c < boxes; ++c) ptx::tma_load_2d(to + c * (XG / 2), mx, bar, (int)col0 + c * 64, at);
-        if (now.have == GRAD_ROWS)
-          for (int j = 0; j < PH * R; j += 64) ptx::tma_load_2d(to + XG + j * 128, mh, bar, j, now.place);
-      }
-      __syncwarp();
-      if (!run) {  // sixteen lanes, four rows each
-        int q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int from = lane * 4 + e;
-          const int lo = __shfl_sync(kAll, now.r0, from & 31), hi = __shfl_sync(kAll, now.r1, from & 31);
-          q[e] = from & 32 ? hi : lo;
+      const int head = __shfl_sync(kAll, now.lo, 0);
+      if (now.have == GRAD_ROWS && __all_sync(kAll, now.lo == head + lane && now.hi == head + 32 + lane)) {
+        land.skip(ctl.full, S);
+        if (lane == 0) {
+          if (warp < 2 && warp * 64 < left) {
+            ptx::mbar_arrive_expect_tx(bar, XG / 2);
+            ptx::tma_load_2d(to + warp * (XG / 2), mx, bar, (int)col0 + warp * 64, head);
+          } else if (warp == 2) {
+            ptx::mbar_arrive_expect_tx(bar, hb);
+            for (int j = 0; j < PH * R; j += 64) ptx::tma_load_2d(to + XG + j * 128, mh, bar, j, now.place);
+          } else {
+            ptx::mbar_arrive(bar);
+          }
         }
-        if (lane < 16)
-          for (int c = 0; c < boxes; ++c)
-            ptx::tma_gather4(to + c * (XG / 2) + lane * 512, mr, bar, (int)col0 + c * 64, q[0], q[1], q[2], q[3]);
-      }
-      if (now.have < GRAD_ROWS && lane < 16) {
-        int q[4];
+        __syncwarp();
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q[e] = lane * 4 + e < now.have ? now.place + lane * 4 + e : (int)g.T;
-        for (int j = 0; j < PH * R; j += 64)
-          ptx::tma_gather4(to + XG + j * 128 + lane * 512, mhr, bar, j, q[0], q[1], q[2], q[3]);
+        for (int i = 0; i < 16; i += 2) {
+          const int at = mine + i + (lane >> 4);
+          const int lo = __shfl_sync(kAll, now.lo, at & 31), hi = __shfl_sync(kAll, now.hi, at & 31);
+          const int64_t row = at & 32 ? hi : lo;
+          const bool have = row >= 0 && in_x;
+          ptx::copy16(to + (unit >> 3) * (GRAD_ROWS * 128) + at * 128 + (((unit ^ at) & 7) << 4),
+                      have ? x + row * p.cols : static_cast<const T*>(p.x), have);
+        }
+        if (h_row < h_by) {
+          const int u = lane - h_row * hu;
+          for (int i = h_row; i < 16; i += h_by) {
+            const int at = mine + i;
+            const bool have = at < now.have;
+            ptx::copy16(to + XG + (u >> 3) * (GRAD_ROWS * 128) + at * 128 + (((u ^ at) & 7) << 4),
+                        have ? p.h + (int64_t)(now.place + at) * PH * R + u * 8 : p.h, have);
+          }
+        }
+        land.next(ctl.full, S);
       }
-      __syncwarp();
+      now = next;
+      next = after;
     }
-    if (ctl.abort)  // the copies under way land before the block ends
-      for (int i = b - b0 > S ? b - b0 - S : 0; i < b - b0; ++i) tc::drain_wait(&ctl.full[i % S], (i / S) & 1);
-  } else if (warp == 1) {
+    land.finish(ctl.full, S);
+  } else if (warp == GRAD_LOAD) {
     const uint32_t id = ptx::idesc_f16(1, GRAD_COLS, PH * R, true, true);
     Slot ring, acc;
     int l = b0 < b1 ? adapter_of(b0) : 0, end = 0;
@@ -1854,7 +1945,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
       }
       ptx::tc_fence_before();
       tc::epi_sync();  // (the barrier counts one arrival)
-      if (tid == 64) ptx::mbar_arrive(&ctl.acce[acc.i]);
+      if (warp == GRAD_LOAD + 1 && lane == 0) ptx::mbar_arrive(&ctl.acce[acc.i]);
       acc.next(2);
       b = end;
     }
@@ -1879,7 +1970,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
           before += q < rank ? 1 : 0;
         }
       const int n = left * r, share = (n + sharers - 1) / sharers, e0 = before * share, e1 = min(e0 + share, n);
-      for (int e = e0 + tid; e < e1; e += DOWN_THREADS) {
+      for (int e = e0 + tid; e < e1; e += GRAD_THREADS) {
         const int col = p.turned ? e / r : e % left, j = p.turned ? e - col * r : e / left;
         float sum = 0.0f;
         for (int q = ra; q <= rb; ++q) {
@@ -1894,7 +1985,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
   // ---- adapters without rows: zeros
   for (int l = rank; l < L; l += C) {
     if (ctl.first[l + 1] > ctl.first[l]) continue;
-    for (int e = tid; e < left * r; e += DOWN_THREADS) {
+    for (int e = tid; e < left * r; e += GRAD_THREADS) {
       const int col = p.turned ? e / r : e % left, j = p.turned ? e - col * r : e / left;
       out[(int64_t)l * r * p.cols + (p.turned ? (col0 + col) * r + j : (int64_t)j * p.cols + col0 + col)] =
           from_f32<T>(0.0f);
@@ -2019,8 +2110,7 @@ cudaError_t run_down_tma(DownArgs& g, int problems, cudaStream_t s) {
     const DownProblem& p = g.prob[i];
     const bool w = p.turned ? encode<T>(&maps.w[i], p.w, g.r, p.K, g.r, KB, g.L)
                             : encode<T>(&maps.w[i], p.w, p.K, g.r, p.K, g.R, g.L);
-    if (!w || !encode<T>(&maps.x[i], p.x, p.K, g.T, p.ld, 32) || !encode<T>(&maps.rows[i], p.x, p.K, g.T, p.ld, 1))
-      return cudaErrorInvalidValue;
+    if (!w || !encode<T>(&maps.x[i], p.x, p.K, g.T, p.ld, 32)) return cudaErrorInvalidValue;
   }
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
   // two blocks per SM, with a ring of up to 104 KB each
@@ -2103,7 +2193,7 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   UpMaps maps = {};
   bool ok = encode_h(&maps.h, h, g.T, g.R, PL::PH);
   if (tma && g.base)
-    ok = ok && encode<T>(&maps.base, g.base, g.N, g.T, g.N, 32) && encode<T>(&maps.rows, g.base, g.N, g.T, g.N, 1);
+    ok = ok && encode<T>(&maps.base, g.base, g.N, g.T, g.N, 32);
   if (tma) ok = ok && encode<T>(&maps.out, g.out, g.N, g.T, g.N, 32);
   if (g.vec & 1)
     ok = ok && (g.turned ? encode<T>(&maps.w, g.w, g.N, g.r, g.N, g.R, g.L)
@@ -2187,17 +2277,14 @@ cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const 
   want = want < most ? want : most;
   w.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
   if constexpr (PL::P == 1) {
-    bool tma = encode_fn() != nullptr;
-    for (int i = 0; i < parts; ++i) tma = tma && w.prob[i].vec;
-    if (tma) {
+    bool copies = encode_fn() != nullptr;
+    for (int i = 0; i < parts; ++i) copies = copies && w.prob[i].vec;
+    if (copies) {
       GradMaps maps = {};
-      for (int i = 0; i < parts; ++i) {
-        const GradProblem& p = w.prob[i];
-        if (!encode<T>(&maps.x[i], p.x, p.cols, a.T, p.cols, GRAD_ROWS) || !encode<T>(&maps.rows[i], p.x, p.cols, a.T, p.cols, 1) ||
-            !encode<T>(&maps.h[i], p.h, PL::PH * w.R, a.T, PL::PH * w.R, GRAD_ROWS) ||
-            !encode<T>(&maps.h_rows[i], p.h, PL::PH * w.R, a.T, PL::PH * w.R, 1))
+      for (int i = 0; i < parts; ++i)
+        if (!encode<T>(&maps.x[i], w.prob[i].x, w.prob[i].cols, a.T, w.prob[i].cols, GRAD_ROWS) ||
+            !encode<T>(&maps.h[i], w.prob[i].h, PL::PH * w.R, a.T, PL::PH * w.R, GRAD_ROWS))
           return cudaErrorInvalidValue;
-      }
       const int stage = GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R), sums = GRAD_COLS * (w.R + 1) * 4;
       // two blocks per SM where three stages and a set of sums fit in half of it
       const int fixed = (int)(sizeof(GradCtl) + 1023) / 1024 * 1024 + 256;  // static shared memory
@@ -2209,7 +2296,7 @@ cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const 
       const int64_t blocks = ceil_div(a.T, GRAD_ROWS), per_chunk = (room == half ? 2 : 1) * (int64_t)device_sm_count() / all;
       const int64_t ctas = per_chunk < blocks ? per_chunk : blocks;
       w.log_ctas = ctas >= 8 ? 3 : (ctas >= 4 ? 2 : (ctas >= 2 ? 1 : 0));
-      return launch_clusters<k_adapters_grad_tma>(dim3((unsigned)(chunks << w.log_ctas), parts), 1 << w.log_ctas, DOWN_THREADS,
+      return launch_clusters<k_adapters_grad_runs>(dim3((unsigned)(chunks << w.log_ctas), parts), 1 << w.log_ctas, GRAD_THREADS,
                                                   smem_for((size_t)w.stages * stage + sums + 1024, w.cols, fixed), s, maps, w);
     }
   }

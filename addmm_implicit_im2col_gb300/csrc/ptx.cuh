@@ -242,17 +242,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
-// Four rows y[0..3] of a 2-D tensor (box {columns, 1}) from column x on, one after the
-// other in shared memory; rows past the tensor's end read zeros.
-__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, uint64_t* bar, int32_t x,
-                                            int32_t y0, int32_t y1, int32_t y2, int32_t y3) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(tmap), "r"(smem_addr(bar)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3)
-      : "memory");
-}
-
 // 4-D tiled bulk tensor load global -> shared, completion counted in bytes on
 // bar; c0 is the innermost coordinate (a negative or out-of-range coordinate
 // reads zeros, c0 * element size a multiple of 16 bytes).
