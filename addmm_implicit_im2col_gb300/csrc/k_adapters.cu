@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_const
   __syncthreads();
   const T* base = static_cast<const T*>(p.base);
   T* out = static_cast<T*>(p.out);
-  const int64_t n_per = (ceil_div(p.N, C) + 15) / 16 * 16, n0 = rank * n_per < p.N ? rank * n_per : p.N;
+  const int64_t n_per = (((p.N + C - 1) >> g.log_ctas) + 15) & ~15ll, n0 = rank * n_per < p.N ? rank * n_per : p.N;
   const int64_t n1 = n0 + n_per < p.N ? n0 + n_per : p.N;
   const bool product = t.l < p.L;
   if (product) {
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_const
     for (int64_t i = tid * 128; i < bytes; i += kThreads * 128)
       ptx::prefetch_l2(reinterpret_cast<const uint8_t*>(b + n0 * r) + i);
     // ---- h = x a^T over this CTA's run of K: a warp has sixteen j and a part of the run
-    const int64_t k_per = (ceil_div(p.K, C) + 31) / 32 * 32, k0 = rank * k_per < p.K ? rank * k_per : p.K;
+    const int64_t k_per = (((p.K + C - 1) >> g.log_ctas) + 31) & ~31ll, k0 = rank * k_per < p.K ? rank * k_per : p.K;
     const int64_t k1 = k0 + k_per < p.K ? k0 + k_per : p.K;
     if (warp < g.blocks * g.parts) {
       const int block = warp % g.blocks, share = warp / g.blocks, j = block * 16 + row8;
@@ -549,14 +549,23 @@ __device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, const D
   const int mine = TILE >> g.log_ctas, units = mine * (R >> 3);
   const float scale = g.scale ? g.scale[t.l] : 1.0f;
   auto sums = [&](int row, int ju, float (&v)[8]) {
+    // (loads of up to eight CTAs in flight together; the sum in their order)
+    float4 a[8], b[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) {
+        const uint32_t at = ptx::cluster_addr(sm + row * pitch + ju * 32, c);
+        a[c] = ptx::ld_cluster4(at);
+        b[c] = ptx::ld_cluster4(at + 16);
+      }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-    for (int c = 0; c < C; ++c) {
-      const uint32_t at = ptx::cluster_addr(sm + row * pitch + ju * 32, c);
-      const float4 a = ptx::ld_cluster4(at), b = ptx::ld_cluster4(at + 16);
-      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-      v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < C) {
+        v[0] += a[c].x, v[1] += a[c].y, v[2] += a[c].z, v[3] += a[c].w;
+        v[4] += b[c].x, v[5] += b[c].y, v[6] += b[c].z, v[7] += b[c].w;
+      }
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= scale;
   };
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     __syncthreads();
     const int stage_bytes = P * XP + down_w_bytes(P * R);
     // every C-th block of K is this CTA's: what the cluster reads at one time lies together
-    const int blocks = (int)ceil_div(p.K, KB), b0 = 0, b1 = (blocks - rank + C - 1) >> g.log_ctas;
+    const int blocks = (int)((p.K + KB - 1) / KB), b0 = 0, b1 = (blocks - rank + C - 1) >> g.log_ctas;
     auto k_of = [&](int b) { return ((b << g.log_ctas) + rank) * KB; };
     const T* w = static_cast<const T*>(p.w) + (int64_t)t.l * r * p.K;
     const int u = tid & 7;
@@ -830,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     own_sums<P>(sm, tmem, R, any, warp >> 2, kWarps / 4);
     ptx::cluster_sync();
     all_sums<T, kThreads>(sm, g, p, t, rank);
-    ptx::cluster_sync();  // no CTA ends while another reads its sums
+    ptx::cluster_sync_reads();  // no CTA ends while another reads its sums
   }
   tear_down(ctl, tmem, g.cols);
 }
@@ -896,6 +905,10 @@ __global__ void __launch_bounds__(DOWN_THREADS)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = g.R;
   int* wd = &g_watchdog_adapters;
   const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 2, ctl.full, g.cols, DOWN_STAGES, 5);
+  if (tid == 32) {
+    ptx::tma_prefetch_desc(&maps.x[blockIdx.y]);
+    ptx::tma_prefetch_desc(&maps.w[blockIdx.y]);
+  }
   ptx::griddep_wait();
   ptx::griddep_launch();
   const RowTile t = find_tile<DOWN_THREADS>(g.offsets, g.L, false, TILE, blockIdx.x >> g.log_ctas);
@@ -905,7 +918,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
     __syncthreads();
     const int wb = p.turned ? down_w_bytes(R) : R * 128, stage_bytes = XP + down_w_bytes(R);
     // every C-th block of K is this CTA's: what the cluster reads at one time lies together
-    const int blocks = (int)ceil_div(p.K, KB), b0 = 0, b1 = (blocks - rank + C - 1) >> g.log_ctas;
+    const int blocks = (int)((p.K + KB - 1) / KB), b0 = 0, b1 = (blocks - rank + C - 1) >> g.log_ctas;
     auto k_of = [&](int b) { return ((b << g.log_ctas) + rank) * KB; };
     if (warp == 0) {
       const void* mw = &maps.w[blockIdx.y];
@@ -989,7 +1002,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
     __syncwarp();
     ptx::cluster_sync();
     all_sums<T, DOWN_THREADS>(sm, g, p, t, rank);
-    ptx::cluster_sync();  // no CTA ends while another reads its sums
+    ptx::cluster_sync_reads();  // no CTA ends while another reads its sums
   }
   tear_down(ctl, tmem, g.cols);
 }
@@ -1048,19 +1061,22 @@ struct UpCtl {
 
 // A block's items, each 128 outputs (`step`) of a tile's rows: runs of `group` items, the
 // blocks' runs interleaved, so that what all blocks read and write at one time lies
-// together.  Walked by counting: a 64-bit division takes longer than an item's other work.
+// together.  Walked by counting, and in 32 bits (entry points keep the items below 2^31): a
+// 64-bit division takes half a microsecond.
 struct Walk {
   int tile, step, in, steps, group, jump_tiles, jump_steps;
-  int64_t left;  // items from this one on
-  __device__ __forceinline__ Walk(int64_t items, int steps_, int group_) : in(0), steps(steps_), group(group_) {
-    const int64_t runs = (items + group - 1) / group, G = gridDim.x, b = blockIdx.x;
-    left = b < runs ? (runs - b + G - 1) / G * group : 0;
-    if (left && (runs - 1) % G == b) left -= runs * group - items;  // the last run may be short
-    const int64_t first = b * group, jump = (G - 1) * group + 1;
-    tile = (int)(first / steps);
-    step = (int)(first - (int64_t)tile * steps);
-    jump_tiles = (int)(jump / steps);
-    jump_steps = (int)(jump - (int64_t)jump_tiles * steps);
+  int left;  // items from this one on
+  __device__ __forceinline__ Walk(uint32_t items, uint32_t steps_, uint32_t group_)
+      : in(0), steps((int)steps_), group((int)group_) {
+    const uint32_t runs = (items + group_ - 1) / group_, G = gridDim.x, b = blockIdx.x;
+    const uint32_t mine = b < runs ? (runs - b + G - 1) / G : 0;
+    left = (int)(mine * group_);
+    if (mine && b + (mine - 1) * G == runs - 1) left -= (int)(runs * group_ - items);  // the last run may be short
+    const uint32_t first = b * group_, jump = (G - 1) * group_ + 1;
+    tile = (int)(first / steps_);
+    step = (int)(first - (uint32_t)tile * steps_);
+    jump_tiles = (int)(jump / steps_);
+    jump_steps = (int)(jump - (uint32_t)jump_tiles * steps_);
   }
   __device__ __forceinline__ void next() {
     --left;
@@ -1143,6 +1159,14 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     ptx::tmem_alloc(&ctl.tmem_base, 2 * UP_N);
     ptx::tmem_relinquish();
   }
+  if (tid == 32) {
+    ptx::tma_prefetch_desc(&maps.h);
+    if (g.vec & 1) ptx::tma_prefetch_desc(&maps.w);
+    if (g.vec & 2) {
+      if (g.base) ptx::tma_prefetch_desc(&maps.base);
+      ptx::tma_prefetch_desc(&maps.out);
+    }
+  }
   // The call's inputs are there already (the first launch has waited for them); h is not.
   const T* base = static_cast<const T*>(g.base);
   T* out = static_cast<T*>(g.out);
@@ -1153,8 +1177,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   ptx::griddep_launch();
-  const int64_t items = (int64_t)ctl.before[B] * g.steps;
-  const Walk walk(items, g.steps, g.group);
+  const Walk walk((uint32_t)ctl.before[B] * (uint32_t)g.steps, g.steps, g.group);
   constexpr int SB = 32 * 64 * (int)sizeof(T);  // bytes of a warp's part of an item
   uint8_t* ws = sm + UP_EPI * g.b_slots * SB;
   uint8_t* hs = ws + g.slots * g.w_bytes;
@@ -1735,7 +1758,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   if (work) grad_sums<PH>(sm, tmem, R, b1 > b0, warp >> 2, kWarps / 4);
   ptx::cluster_sync();
   if (work) grad_out<T, kThreads>(sm, g, p, l, rank, col0);
-  ptx::cluster_sync();  // no CTA ends while another reads its sums
+  ptx::cluster_sync_reads();  // no CTA ends while another reads its sums
   tear_down(ctl, tmem, g.cols);
 }
 
@@ -1772,6 +1795,10 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
   const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
   int* wd = &g_watchdog_adapters;
   const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 5, ctl.full, g.cols, DOWN_STAGES, GRAD_LOAD);
+  if (tid == 32) {
+    ptx::tma_prefetch_desc(&maps.x[blockIdx.y]);
+    ptx::tma_prefetch_desc(&maps.h[blockIdx.y]);
+  }
   if (left <= 0) {  // the whole cluster (the problems may have different numbers of columns)
     ptx::griddep_wait();
     tear_down(ctl, tmem, g.cols);
@@ -1991,7 +2018,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
           from_f32<T>(0.0f);
     }
   }
-  ptx::cluster_sync();  // no CTA ends while another reads its sums
+  ptx::cluster_sync_reads();  // no CTA ends while another reads its sums
   tear_down(ctl, tmem, g.cols);
 }
 

@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kJoin)
   const int64_t t1 = a.offsets ? clamped(a.offsets[s + 1], a.T) : a.T;
   ptx::griddep_wait();
   ptx::griddep_launch();
-  const int c0 = (int)(t0 / chunk), c1 = t1 > t0 ? (int)((t1 - 1) / chunk) + 1 : c0;
+  // (T <= 2^27; a 64-bit division takes half a microsecond)
+  const int c0 = (int)t0 / chunk, c1 = t1 > t0 ? (int)(t1 - 1) / chunk + 1 : c0;
   const int per = (c1 - c0 + C - 1) >> log_ctas;
   const int from = min(c0 + rank * per, c1), to = min(from + per, c1);
   // the threads are `parts` groups of E or more, group p of which takes every parts-th row
