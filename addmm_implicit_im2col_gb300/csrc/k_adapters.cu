@@ -1036,7 +1036,8 @@ struct UpArgs {
   const int32_t *offsets, *order;
   int64_t T, N;
   int L, r, R, steps, turned, vec;  // vec: 1 w, 2 base and out, by TMA
-  int group;                                      // items that a block takes at once
+  int group;                              // items that a block takes at once
+  int jump, jump_tiles, jump_steps;       // from the last of them to its next: items, the same as tiles and steps
   int slots, h_slots, b_slots, w_bytes, h_bytes;  // of the rings of w, h and base; bytes of one
 };
 struct UpMaps {
@@ -1064,28 +1065,21 @@ struct UpCtl {
 // together.  Walked by counting, and in 32 bits (entry points keep the items below 2^31): a
 // 64-bit division takes half a microsecond.
 struct Walk {
-  int tile, step, in, steps, group, jump_tiles, jump_steps;
-  int left;  // items from this one on
-  __device__ __forceinline__ Walk(uint32_t items, uint32_t steps_, uint32_t group_)
-      : in(0), steps((int)steps_), group((int)group_) {
-    const uint32_t runs = (items + group_ - 1) / group_, G = gridDim.x, b = blockIdx.x;
-    const uint32_t mine = b < runs ? (runs - b + G - 1) / G : 0;
-    left = (int)(mine * group_);
-    if (mine && b + (mine - 1) * G == runs - 1) left -= (int)(runs * group_ - items);  // the last run may be short
-    const uint32_t first = b * group_, jump = (G - 1) * group_ + 1;
-    tile = (int)(first / steps_);
-    step = (int)(first - (uint32_t)tile * steps_);
-    jump_tiles = (int)(jump / steps_);
-    jump_steps = (int)(jump - (uint32_t)jump_tiles * steps_);
+  int tile, step, in;
+  uint32_t at, items;
+  __device__ __forceinline__ Walk(const UpArgs& g, uint32_t items_) : in(0), at(blockIdx.x * g.group), items(items_) {
+    tile = (int)(at / (uint32_t)g.steps);
+    step = (int)at - tile * g.steps;
   }
-  __device__ __forceinline__ void next() {
-    --left;
-    const bool jump = ++in == group;
+  __device__ __forceinline__ bool more() const { return at < items; }
+  __device__ __forceinline__ void next(const UpArgs& g) {
+    const bool jump = ++in == g.group;
     if (jump) in = 0;
-    tile += jump ? jump_tiles : 0;
-    step += jump ? jump_steps : 1;
-    if (step >= steps) {
-      step -= steps;
+    at += jump ? g.jump : 1;
+    tile += jump ? g.jump_tiles : 0;
+    step += jump ? g.jump_steps : 1;
+    if (step >= g.steps) {
+      step -= g.steps;
       ++tile;
     }
   }
@@ -1177,7 +1171,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   ptx::griddep_launch();
-  const Walk walk((uint32_t)ctl.before[B] * (uint32_t)g.steps, g.steps, g.group);
+  const Walk walk(g, (uint32_t)ctl.before[B] * (uint32_t)g.steps);
   constexpr int SB = 32 * 64 * (int)sizeof(T);  // bytes of a warp's part of an item
   uint8_t* ws = sm + UP_EPI * g.b_slots * SB;
   uint8_t* hs = ws + g.slots * g.w_bytes;
@@ -1193,7 +1187,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     int last = -1;
     Slot hslot, wslot;
     RowTile t = {0, 0, 0};
-    for (Walk item = walk; item.left > 0; item.next()) {
+    for (Walk item = walk; item.more(); item.next(g)) {
       const int64_t n0 = (int64_t)item.step * UP_N;
       const bool other = item.tile != last;
       if (other) t = tile_of(ctl, B, item.tile);
@@ -1279,11 +1273,11 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     Slot hslot, wslot, aslot;
     bool product = false;
     const uint32_t id = ptx::idesc_f16(PL::FD, TILE, UP_N, false, g.turned);
-    for (Walk item = walk; item.left > 0;) {
+    for (Walk item = walk; item.more();) {
       const bool other = item.tile != last;
       if (other) product = tile_of(ctl, B, item.tile).l < g.L;
       last = item.tile;
-      item.next();
+      item.next(g);
       if (!product) continue;
       if (other) {
         hb = hslot.i;
@@ -1314,7 +1308,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
           }
         ptx::mma_commit(&ctl.wempty[slot]);
         ptx::mma_commit(&ctl.accf[buf]);
-        if (item.left == 0 || item.tile != last) ptx::mma_commit(&ctl.hempty[hb]);
+        if (!item.more() || item.tile != last) ptx::mma_commit(&ctl.hempty[hb]);
       }
       __syncwarp();
     }
@@ -1347,12 +1341,12 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     Walk item = walk, next = walk;
     Slot nslot;
     auto load = [&] {  // base of the next item to its place in the ring
-      if (next.left <= 0) {
+      if (!next.more()) {
         ptx::copy_commit();
         return;
       }
       place(ahead, next);
-      next.next();
+      next.next(g);
       const int slot = nslot.i;
       nslot.next(NS);
       if (base && ahead.rows > 0 && ahead.col < g.N) {
@@ -1392,7 +1386,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     if (wide)
       for (int i = 0; i < NS - 1; ++i) load();
     Slot slot_of;
-    for (; item.left > 0; item.next(), slot_of.next(NS)) {
+    for (; item.more(); item.next(g), slot_of.next(NS)) {
       place(now, item);
       const bool product = now.l < g.L, live = now.rows > 0 && now.col < g.N;
       const uint32_t acc = tmem + ((uint32_t)(q4 * 32) << 16) + (n & 1) * UP_N + half * 64;
@@ -1528,7 +1522,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     }
     if (wide) {
       if (ctl.abort) {  // the copies under way land before the block ends
-        for (; item.left > next.left && base; item.next(), slot_of.next(NS)) {
+        for (; item.at < next.at && base; item.next(g), slot_of.next(NS)) {
           place(now, item);
           if (now.rows == 0 || now.col >= g.N || !now.run) continue;
           tc::drain_wait(&ctl.bfull[warp][slot_of.i], phases >> slot_of.i & 1);
@@ -2227,8 +2221,11 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
                          : encode<T>(&maps.w, g.w, g.r, g.N, g.r, UP_N, g.L, along.bytes));
   if (!ok) return cudaErrorInvalidValue;
   const int64_t items = most_tiles(g.T, g.L, TILE) * g.steps, most_blocks = (int64_t)device_sm_count() * blocks;
-  return launch_clusters<k_adapters_up<T>>(dim3((unsigned)(items < most_blocks ? items : most_blocks)), 1,
-                                           UP_THREADS<T>, smem, s, maps, g);
+  const int grid = (int)(items < most_blocks ? items : most_blocks);
+  g.jump = (grid - 1) * g.group + 1;
+  g.jump_tiles = g.jump / g.steps;
+  g.jump_steps = g.jump % g.steps;
+  return launch_clusters<k_adapters_up<T>>(dim3(grid), 1, UP_THREADS<T>, smem, s, maps, g);
 }
 
 // The form for few rows: an adapter has sixteen on average at most, whose tiles of 128 would
