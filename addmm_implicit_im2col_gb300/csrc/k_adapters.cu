@@ -566,8 +566,9 @@ __device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, const D
         v[0] += a[c].x, v[1] += a[c].y, v[2] += a[c].z, v[3] += a[c].w;
         v[4] += b[c].x, v[5] += b[c].y, v[6] += b[c].z, v[7] += b[c].w;
       }
+    // (past r: zeros times x, which may be infinite)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= scale;
+    for (int e = 0; e < 8; ++e) v[e] = ju * 8 + e < g.r ? v[e] * scale : 0.0f;
   };
   const bool scaled = sizeof(T) == 2 && Planes<T>::FD == 0 && p.h16;
   if (scaled) {
@@ -628,6 +629,12 @@ struct Slot {
     }
   }
 };
+
+// After a wait that gave up: the copies that a warp has under way, one use of its ring's
+// barriers after the other, `asked` in all, land before the block ends.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int S, int asked) {
+  for (int i = asked > S ? asked - S : 0; i < asked; ++i) tc::drain_wait(full + i % S, (i / S) & 1);
+}
 
 // Barriers and tensor memory of a block.  The memory is taken before the stream's next
 // kernel may start: a block of that one that had it would wait for this kernel's end.
@@ -938,9 +945,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
         }
         __syncwarp();
       }
-      if (ctl.abort)  // the copies under way land before the block ends
-        for (int i = b - b0 > S ? b - b0 - S : 0; i < b - b0; ++i)
-          tc::drain_wait(&ctl.full[i % S], (i / S) & 1);
+      if (ctl.abort) drain_ring(ctl.full, S, b - b0);
     } else if (warp == 1) {
       Slot ring;
       for (int b = b0; b < b1; ++b, ring.next(S)) {
@@ -971,7 +976,8 @@ __global__ void __launch_bounds__(DOWN_THREADS)
       const void* mx = &maps.x[blockIdx.y];
       Slot ring;
       Landing land(S);
-      for (int b = b0; b < b1; ++b, ring.next(S)) {
+      int b = b0;
+      for (; b < b1; ++b, ring.next(S)) {
         const int slot = ring.i;
         if (ring.round > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (ring.round - 1) & 1, &ctl.abort, 16, wd)) break;
         const int k = k_of(b);
@@ -996,6 +1002,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
       }
       if (!run) land.finish(ctl.full, S);
       if (b1 > b0) tc::warp_wait_bar(&ctl.accf, 0, &ctl.abort, 2, wd);
+      if (ctl.abort && run) drain_ring(ctl.full, S, b - b0);
       ptx::tc_fence_after();
       own_sums<1>(sm, tmem, R, b1 > b0, 0, 1);
     }
@@ -1062,8 +1069,9 @@ struct UpCtl {
 
 // A block's items, each 128 outputs (`step`) of a tile's rows: runs of `group` items, the
 // blocks' runs interleaved, so that what all blocks read and write at one time lies
-// together.  Walked by counting, and in 32 bits (entry points keep the items below 2^31): a
-// 64-bit division takes half a microsecond.
+// together.  Walked by counting, in 32 bits (T N < 2^40, with sixteen rows a tile on average at
+// least, makes fewer than 2^31 items), with the divisions on the host: a 64-bit one takes half
+// a microsecond here.
 struct Walk {
   int tile, step, in;
   uint32_t at, items;
@@ -1846,7 +1854,8 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
     Rows now = rows_of(b0), next = rows_of(b0 + 1);
     Slot ring;
     Landing land(S);
-    for (int b = b0; b < b1; ++b, ring.next(S)) {
+    int b = b0;
+    for (; b < b1; ++b, ring.next(S)) {
       const int slot = ring.i;
       const Rows after = rows_of(b + 2);
       if (ring.round > 0 && !tc::warp_wait_bar(&ctl.empty[slot], (ring.round - 1) & 1, &ctl.abort, 4, wd)) break;
@@ -1892,6 +1901,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
       next = after;
     }
     land.finish(ctl.full, S);
+    if (ctl.abort) drain_ring(ctl.full, S, b - b0);
   } else if (warp == GRAD_LOAD) {
     const uint32_t id = ptx::idesc_f16(1, GRAD_COLS, PH * R, true, true);
     Slot ring, acc;

@@ -530,8 +530,8 @@ int moe_combine_backward(const void* grad, const void* y, int dtype, const float
  *   loss[s] = E / (k * n^2) * sum_e counts[s,e] * sum_t p[t,e]     (0 for n = 0)
  *
  * which is 1 for an even choice at even scores.  Tokens in no sequence (padding
- * behind the last one) count nowhere.  The sums are fp32 over 64 tokens and 64-bit
- * beyond, in a fixed order.
+ * behind the last one) count nowhere.  The sums are fp32 over 64 tokens and pairs of
+ * fp32 numbers beyond, in a fixed order.
  *   logits [T,E], rows row_stride elements apart; experts [T,k] (moe_route's);
  *   loss [S], counts [S,E].  T <= 2^27, S <= 2^27, S * E < 2^31.
  *   workspace  moe_balance_workspace_bytes(T, S, E) bytes (0 for few tokens), 16-byte
@@ -569,7 +569,8 @@ int moe_balance_backward(const float* grad_loss, const void* logits, int dtype, 
  *         without an adapter are neither read nor written.  No other overlap.
  * x, a, b, base and out are of type dtype; T <= 2^27, 1 <= K <= 2^20, N <= 2^20.
  * Sums are fp32, and x a^T is kept to 16 bits of precision (fp32: 24) for the second
- * product; an output is rounded once.  Non-finite values reach their own row only.
+ * product; an output is rounded once.  Non-finite values (fp32: above 3.38e38 too) reach their own
+ * row only, where an infinity may come out as NaN.
  * workspace: lowrank_linear_workspace_bytes(T, L, r) bytes (0 for few rows), 16-byte
  * aligned; NULL: from the library's pool.
  */
