@@ -134,6 +134,18 @@ struct Raw8 {
       for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint4*>(t)[i];
     }
   }
+  // the same from rows aligned to `piece` bytes
+  __device__ __forceinline__ void load_by(const T* p, int n, int piece) {
+    if (n >= 8 && piece == 8) {
+#pragma unroll
+      for (int i = 0; i < 2 * W; ++i) reinterpret_cast<uint2*>(w)[i] = __ldg(reinterpret_cast<const uint2*>(p) + i);
+    } else if (n >= 8 && piece == 4) {
+#pragma unroll
+      for (int i = 0; i < 4 * W; ++i) reinterpret_cast<uint32_t*>(w)[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    } else {
+      load(p, n, piece == 16);
+    }
+  }
   __device__ __forceinline__ void widen(float (&v)[8]) const {
     alignas(16) T t[8];
 #pragma unroll
@@ -492,6 +504,20 @@ __device__ __forceinline__ void planes_of(const Raw8<T>& raw, uint4 (&out)[Q]) {
     split8<Q>(v, out);
   }
 }
+// An asynchronous copy of the first n (whole pieces) of eight 16-bit values of a row that is
+// aligned to `piece` bytes; zeros for the others.  (`any`: some address.)
+template <typename T>
+__device__ __forceinline__ void copy_unit(uint8_t* to, const T* from, int n, int piece, const void* any) {
+  if (piece == 16) {
+    ptx::copy16(to, n > 0 ? from : any, n > 0);
+  } else if (piece == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) ptx::copy_small<8>(to + 8 * i, 4 * i < n ? from + 4 * i : any, 4 * i < n);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ptx::copy_small<4>(to + 4 * i, 2 * i < n ? from + 2 * i : any, 2 * i < n);
+  }
+}
 struct DownProblem {
   const void* x;   // [T, K], rows ld elements apart
   int64_t ld, K;
@@ -499,7 +525,7 @@ struct DownProblem {
   uint16_t* h;     // [T][PH][R], its planes, in adapter order; or null
   uint16_t* h16;   // [T][2][R] of scaled fp16 rows, and what they are to be multiplied by
   float* row_scale;  // [T]; or null
-  int turned, vec; // vec: 1 x, 2 w
+  int turned, x_piece, w_piece;  // alignment of the rows of x and w, up to 16 bytes
 };
 struct DownArgs {
   DownProblem prob[2];
@@ -710,11 +736,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       const int row = rows[(tid >> 3) + 32 * i];
       xr[i] = row < 0 ? nullptr : static_cast<const T*>(p.x) + row * p.ld + u * 8;
     }
-    // x and w of a block go straight to shared memory, or (fp32, and rows that 16-byte
-    // copies cannot reach) through registers.  w lies by its rows j with 64 k each, or
+    // x and w of a block go straight to shared memory, or (fp32, and rows that copies of 4
+    // bytes cannot reach) through registers.  w lies by its rows j with 64 k each, or
     // turned (r contiguous) by k with the planes' j in units of 64, as the MMA's "MN-major"
     // operand.
-    const bool copy_x = ASYNC && (p.vec & 1), copy_w = ASYNC && (p.vec & 2);
+    const bool copy_x = ASYNC && p.x_piece >= 4, copy_w = ASYNC && p.w_piece >= 4;
     Raw8<T> held_w[RU], held_x[ASYNC ? 1 : 4];
     const int ru = R >> 3;
     int wj[RU], wk[RU];  // this thread's units of w
@@ -734,14 +760,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       const int left = (int)(p.K - k < KB ? p.K - k : KB);
       if (!ASYNC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) held_x[ASYNC ? 0 : i].load(xr[i] + k, xr[i] ? left - u * 8 : 0, p.vec & 1);
+        for (int i = 0; i < 4; ++i) held_x[ASYNC ? 0 : i].load(xr[i] + k, xr[i] ? left - u * 8 : 0, p.x_piece == 16);
       }
       if (!copy_w) {
 #pragma unroll
         for (int i = 0; i < RU; ++i) {
           int n;
           const T* from = w_unit(i, k, left, n);
-          held_w[i].load(from, n, p.vec & 2);
+          held_w[i].load(from, n, p.w_piece == 16);
         }
       }
     };
@@ -751,9 +777,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = (tid >> 3) + 32 * i, at = row * 128 + ((u ^ (row & 7)) << 4);
-        if (copy_x) {  // K is a multiple of 8: a unit of 16 bytes is whole or missing
-          const bool in = xr[i] && u * 8 < left;
-          ptx::copy16(to + at, in ? xr[i] + k : static_cast<const T*>(p.x), in);
+        if (copy_x) {
+          copy_unit(to + at, xr[i] + k, xr[i] ? left - u * 8 : 0, p.x_piece, p.x);
         } else {
           Raw8<T> raw;
           if (ASYNC) raw.load(xr[i] + k, xr[i] ? left - u * 8 : 0, false);
@@ -778,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
           if (copy_w) {
             int n;
             const T* from = w_unit(i, k, left, n);
-            ptx::copy16(at, n > 0 ? from : w, n > 0);
+            copy_unit(at, from, n, p.w_piece, w);
           } else {
             *reinterpret_cast<uint4*>(at) = v[c];
           }
@@ -1042,7 +1067,8 @@ struct UpArgs {
   void* out;
   const int32_t *offsets, *order;
   int64_t T, N;
-  int L, r, R, steps, turned, vec;  // vec: 1 w, 2 base and out, by TMA
+  int L, r, R, steps, turned, vec;  // vec: w by TMA
+  int w_piece, piece;  // alignment of the rows of w, and of base and out, up to 16 bytes
   int group;                              // items that a block takes at once
   int jump, jump_tiles, jump_steps;       // from the last of them to its next: items, the same as tiles and steps
   int slots, h_slots, b_slots, w_bytes, h_bytes;  // of the rings of w, h and base; bytes of one
@@ -1117,21 +1143,26 @@ __device__ __forceinline__ uint32_t add_pair(__half, uint32_t base, float a, flo
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Columns that a warp stages at once where rows are not written 32 bytes at a time.
-template <typename T>
-constexpr int STAGED_COLS = sizeof(T) == 2 ? 32 : 16;
+// Bytes of a warp's part of base: 32 rows of 64 columns, in boxes of 128 bytes a row.  Without
+// TMA a row of 16-bit values may start in the middle of a word: one more word for each.
+template <typename T, bool TMA>
+constexpr int UP_PART = 32 * 64 * (int)sizeof(T) + (!TMA && sizeof(T) == 2 ? 128 : 0);
+// Columns that a warp stages at once where there is no room for that.
+constexpr int STAGED_COLS = 16;
 
 // Persistent blocks, each with an equal run of the (tile, 128 outputs) items:
 //   warps 0-7   epilogue: a warp has 32 rows and half of an item's columns: it asks for
 //               its part of base some items ahead (a TMA box, or asynchronous copies where the
 //               rows do not lie one after the other), adds the product from tensor memory in
 //               place, rounds once, and has TMA store it (row by row itself where the box
-//               would reach other rows); without TMA (unaligned rows, no room) it adds
-//               column by column through shared memory
+//               would reach other rows).  Form TMA: rows aligned to 16 bytes; the other
+//               copies by 8 or 4 bytes (16-bit rows at odd elements: by the words that hold
+//               them), or, with no room for parts of base (fp32, high ranks), adds column by
+//               column through shared memory
 //   then        one warp (fp32: four, which cut w into its planes) that loads h of a tile
 //               and w of an item, and one for tensor memory and the MMAs (two accumulators
 //               of 128 columns)
-template <typename T>
+template <typename T, bool TMA>
 __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     k_adapters_up(const __grid_constant__ UpMaps maps, const __grid_constant__ UpArgs g) {
   using PL = Planes<T>;
@@ -1143,7 +1174,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
   int* wd = &g_watchdog_adapters;
   if (tid == 0) {
     for (int i = 0; i < UP_SLOTS; ++i) {
-      ptx::mbar_init(&ctl.wfull[i], (g.vec & 1) ? 1 : LOAD * 32);
+      ptx::mbar_init(&ctl.wfull[i], g.vec ? 1 : LOAD * 32);
       ptx::mbar_init(&ctl.wempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1163,8 +1194,8 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
   }
   if (tid == 32) {
     ptx::tma_prefetch_desc(&maps.h);
-    if (g.vec & 1) ptx::tma_prefetch_desc(&maps.w);
-    if (g.vec & 2) {
+    if (g.vec) ptx::tma_prefetch_desc(&maps.w);
+    if (TMA) {
       if (g.base) ptx::tma_prefetch_desc(&maps.base);
       ptx::tma_prefetch_desc(&maps.out);
     }
@@ -1180,7 +1211,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
   const uint32_t tmem = ctl.tmem_base;
   ptx::griddep_launch();
   const Walk walk(g, (uint32_t)ctl.before[B] * (uint32_t)g.steps);
-  constexpr int SB = 32 * 64 * (int)sizeof(T);  // bytes of a warp's part of an item
+  constexpr int SB = UP_PART<T, TMA>;
   uint8_t* ws = sm + UP_EPI * g.b_slots * SB;
   uint8_t* hs = ws + g.slots * g.w_bytes;
   const Along along(R);
@@ -1217,7 +1248,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       const int slot = wslot.i;
       if (wslot.round > 0 && !tc::warp_wait_bar(&ctl.wempty[slot], (wslot.round - 1) & 1, &ctl.abort, 7, wd)) break;
       uint8_t* to = ws + slot * g.w_bytes;
-      if (P == 1 && (g.vec & 1)) {
+      if (P == 1 && g.vec) {
         if (lt == 0) {
           uint64_t* bar = &ctl.wfull[slot];
           ptx::mbar_arrive_expect_tx(bar, g.turned ? R * 256 : plane);
@@ -1256,7 +1287,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
             pitch = plane;
           }
           Raw8<T> raw;
-          raw.load(from, have, g.vec & 4);
+          raw.load_by(from, have, g.w_piece);
           uint4 v[P];
           planes_of<T, P>(raw, v);
 #pragma unroll
@@ -1273,7 +1304,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
           if (i < next.i || next.round > 0) tc::drain_wait(bars + i, (i < next.i ? next.round : next.round - 1) & 1);
       };
       drain(ctl.hfull, hslot, g.h_slots);
-      if (g.vec & 1) drain(ctl.wfull, wslot, g.slots);
+      if (g.vec) drain(ctl.wfull, wslot, g.slots);
     }
   } else if (warp == UP_EPI + LOAD) {
     // ---------------------------------------------------------------- MMAs
@@ -1343,7 +1374,14 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       q.place = t.p0 + q4 * 32 + min(lane, q.rows - 1);
       q.row = __ldg(g.order + q.place);
       const int first = __shfl_sync(kAll, q.row, 0);
-      q.run = __all_sync(kAll, lane >= q.rows || q.row == first + lane);
+      q.run = TMA && __all_sync(kAll, lane >= q.rows || q.row == first + lane);
+    };
+    // without TMA: lanes of a row of 128 bytes, by 8 or 4 bytes
+    const int piece = g.piece, lanes_log = piece == 8 ? 4 : 5, rows_by = 32 >> lanes_log;
+    const int sub_row = lane >> lanes_log, sub = (lane - (sub_row << lanes_log)) * (piece == 8 ? 8 : 4);
+    // does a row's part start in the middle of a word
+    auto odd = [&](int64_t row, int64_t col) {
+      return sizeof(T) == 2 && !TMA ? (int)((reinterpret_cast<uintptr_t>(base) >> 1) + row * g.N + col) & 1 : 0;
     };
     Place ahead, now;
     Walk item = walk, next = walk;
@@ -1367,6 +1405,26 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
             for (int b = 0; b < boxes; ++b)
               ptx::tma_load_2d(to + b * 4096, &maps.base, bar, (int)ahead.col + b * BOX, ahead.row);
           }
+        } else if (!TMA) {  // one or two rows at a time
+          // (A word that holds an element of base is within its allocation; what else it holds
+          // is dropped.)
+          for (int b = 0; b < boxes; ++b) {
+            const int64_t c = ahead.col + b * BOX + sub / (int)sizeof(T);
+#pragma unroll 4
+            for (int i = 0; i < 32; i += rows_by) {
+              const int at = i + sub_row;
+              const int64_t row = __shfl_sync(kAll, ahead.row, at), first = c - odd(row, ahead.col);
+              uint8_t* place = to + b * 4096 + at * 128 + ((((sub >> 4) ^ at) & 7) << 4) + (sub & 15);
+              const bool in = first < g.N;
+              const T* from = base + row * g.N + first;
+              if (piece == 8) ptx::copy_small<8>(place, in ? from : base, in);
+              else ptx::copy_small<4>(place, in ? static_cast<const void*>(from) : g.order, in);
+            }
+          }
+          if (sizeof(T) == 2 && odd(ahead.row, ahead.col)) {  // the last element's word
+            const bool in = ahead.col + 63 < g.N;
+            ptx::copy_small<4>(to + 4096 + lane * 4, in ? static_cast<const void*>(base + (int64_t)ahead.row * g.N + ahead.col + 63) : g.order, in);
+          }
         } else {  // four rows at a time, eight lanes each
           const int unit = lane & 7;
           for (int b = 0; b < boxes; ++b) {
@@ -1382,7 +1440,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       }
       ptx::copy_commit();  // (of every item, so that they can be counted)
     };
-    const bool wide = g.vec & 2;
+    const bool wide = TMA || sizeof(T) == 2 || NS > 0;
     float scale = 1.0f;  // of this lane's row of h; there once an accumulator is
     int scale_of = -1, n = 0;
     auto scale_it = [&] {
@@ -1423,7 +1481,8 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
         if (lane == 0) ptx::bulk_wait_read0();
         __syncwarp();
         load();
-        if (live && (product || !base)) {
+        const int shift = base ? odd(now.row, now.col) * 16 : 0;
+        if (live && (product || !base || (!TMA && sizeof(T) == 2))) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             uint32_t s[32];
@@ -1441,6 +1500,12 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
               uint4* at = reinterpret_cast<uint4*>(mine + box * 4096 + lane * 128 + ((unit ^ (lane & 7)) << 4));
               uint4 h = base ? *at : make_uint4(0, 0, 0, 0);
               uint32_t* hw = reinterpret_cast<uint32_t*>(&h);
+              if (!TMA && sizeof(T) == 2) {
+                const uint8_t* next = i + b * (32 / V) == 7 ? mine + 4096 + lane * 4 : mine + lane * 128 + (((unit + 1) ^ (lane & 7)) << 4);
+                const uint32_t after = base ? *reinterpret_cast<const uint32_t*>(next) : 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) hw[e] = __funnelshift_r(hw[e], e < 3 ? hw[e + 1] : after, shift);
+              }
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 if constexpr (sizeof(T) == 2)
@@ -1464,6 +1529,27 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
             if (lane == 0)
               for (int b = 0; b < 64 / BOX && now.col + b * BOX < g.N; ++b)
                 ptx::tma_store_2d(&maps.out, mine + b * 4096, (int)now.col + b * BOX, now.row);
+          } else if (!TMA) {
+            const int64_t width = g.N - now.col < 64 ? g.N - now.col : 64;
+#pragma unroll
+            for (int b = 0; b < 64 / BOX; ++b) {
+              const int c = b * BOX + sub / (int)sizeof(T);
+#pragma unroll 4
+              for (int i = 0; i < 32; i += rows_by) {
+                const int at = i + sub_row;
+                const int64_t to_row = __shfl_sync(kAll, now.row, at);
+                const uint8_t* from = mine + b * 4096 + at * 128 + ((((sub >> 4) ^ at) & 7) << 4) + (sub & 15);
+                T* to = out + to_row * g.N + now.col + c;
+                if (at < now.rows && c < width) {
+                  if (sizeof(T) == 2 && piece == 2) {
+                    to[0] = reinterpret_cast<const T*>(from)[0];
+                    if (c + 1 < width) to[1] = reinterpret_cast<const T*>(from)[1];
+                  } else if (piece == 8) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
+                  else *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+                }
+              }
+            }
+            __syncwarp();
           } else {  // four rows at a time, eight lanes each
             const int64_t width = g.N - now.col < 64 ? g.N - now.col : 64;
 #pragma unroll
@@ -1481,21 +1567,20 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
           }
         }
         if (lane == 0) ptx::bulk_commit();
-      } else {
+      } else if constexpr (!TMA && sizeof(T) == 4) {
         if (product) {
           if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
           ptx::tc_fence_after();
           scale_it();
         }
-        constexpr int SC = STAGED_COLS<T>, ROWS = 32 / SC;  // columns, and rows at once
+        constexpr int SC = STAGED_COLS, ROWS = 32 / SC;  // columns, and rows at once
         float* mine = reinterpret_cast<float*>(hs + g.h_slots * g.h_bytes) + warp * 32 * (SC + 1);
         const int to_row = lane < now.rows ? now.row : -1;
 #pragma unroll 1
         for (int b = 0; b < 64 / SC; ++b) {
           if (product) {
             uint32_t s[SC];
-            if constexpr (SC == 32) ptx::tmem_ld32(acc + b * SC, s);
-            else ptx::tmem_ld16(acc + b * SC, s);
+            ptx::tmem_ld16(acc + b * SC, s);
             ptx::tmem_ld_wait();
             if (b + 1 == 64 / SC) {
               ptx::tc_fence_before();
@@ -1567,7 +1652,7 @@ struct GradProblem {
   int64_t cols;
   const uint16_t* h;  // [T][PH][R]
   void* out;          // of an adapter [r, cols]; turned: [cols, r]
-  int turned, vec;
+  int turned, piece;  // alignment of x's rows, up to 16 bytes
 };
 struct GradArgs {
   GradProblem prob[2];
@@ -1652,7 +1737,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
   const int u = tid & 15, xrow = tid >> 4, ru = R >> 3;
   const T* x = static_cast<const T*>(p.x) + col0 + u * 8;
-  const bool copy = !HELD && p.vec;
+  const bool copy = !HELD && p.piece >= 4;
   int next[4];  // rows of the next block whose x is asked for
   auto rows_of = [&](int b) {
 #pragma unroll
@@ -1666,7 +1751,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     if (HELD) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        held[HELD ? i : 0].load(x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, p.vec);
+        held[HELD ? i : 0].load(x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, p.piece == 16);
       rows_of(b + 1);
     }
   };
@@ -1676,8 +1761,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
       const int row = xrow + 16 * i;
       uint8_t* at = to + (u >> 3) * (GRAD_ROWS * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4);
       if (copy) {
-        const bool in = next[i] >= 0 && u * 8 < left;
-        ptx::copy16(at, in ? x + next[i] * p.cols : static_cast<const T*>(p.x), in);
+        copy_unit(at, x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, p.piece, p.x);
       } else {
         Raw8<T> raw;
         if (HELD) raw = held[HELD ? i : 0];
@@ -2027,9 +2111,12 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
 }
 
 // ------------------------------------------------------------------- host
-bool aligned16(const void* p, int64_t pitch_bytes) {
-  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes) & 15u) == 0;
+// What rows at p, `pitch` bytes apart, are aligned to: 16, 8, 4 or 2 bytes.
+int piece_of(const void* p, int64_t pitch) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch;
+  return bits & 3 ? 2 : (bits & 7 ? 4 : (bits & 15 ? 8 : 16));
 }
+bool aligned16(const void* p, int64_t pitch) { return piece_of(p, pitch) == 16; }
 
 // Tensor-memory columns of a block: a power of two that holds `need`.
 int tmem_cols(int need) {
@@ -2159,7 +2246,7 @@ cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
   using PL = Planes<T>;
   if constexpr (sizeof(T) == 2) {
     bool tma = encode_fn() != nullptr;
-    for (int i = 0; i < problems; ++i) tma = tma && g.prob[i].vec == 3;
+    for (int i = 0; i < problems; ++i) tma = tma && g.prob[i].x_piece == 16 && g.prob[i].w_piece == 16;
     if (tma) return run_down_tma<T>(g, problems, s);
   }
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
@@ -2173,29 +2260,17 @@ cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
 #undef IMC_DOWN
 }
 
-template <typename T>
-cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
+template <typename T, bool TMA>
+cudaError_t run_up_as(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   using PL = Planes<T>;
-  const int64_t b = sizeof(T);
   const Along along(g.R);
-  if (!encode_fn()) return cudaErrorNotSupported;
-  g.steps = (int)ceil_div(g.N, UP_N);
-  g.group = 2;
-  const int part = 32 * 64 * (int)sizeof(T);
-  g.w_bytes = PL::PD * (g.turned ? g.R * 256 : along.plane());
-  g.h_bytes = PL::PH * along.plane();
-  const int most = 232448 - (int)sizeof(UpCtl) - 256 - 1024;
+  constexpr int part = UP_EPI * UP_PART<T, TMA>, staged = UP_EPI * 32 * (STAGED_COLS + 1) * 4;
   // rings: at least two parts of base, one h, one w; then more parts, w, h
-  const bool tma = aligned16(g.out, g.N * b) && aligned16(g.base, 0) &&
-                   2 * UP_EPI * part + g.h_bytes + g.w_bytes <= most;
-  const bool vec_w = aligned16(g.w, (g.turned ? g.N : g.r) * b);
-  g.vec = (vec_w ? 4 : 0) | (vec_w && PL::PD == 1 ? 1 : 0) | (tma ? 2 : 0);
+  const int most = 232448 - (int)sizeof(UpCtl) - 256 - 1024;
+  const bool ring = 2 * part + g.h_bytes + g.w_bytes <= most;
   g.slots = g.h_slots = 1;
-  g.b_slots = tma ? 2 : 0;
-  const int staged = tma ? 0 : UP_EPI * 32 * (STAGED_COLS<T> + 1) * 4;
-  auto bytes = [&] {
-    return UP_EPI * g.b_slots * part + g.slots * g.w_bytes + g.h_slots * g.h_bytes + staged;
-  };
+  g.b_slots = ring ? 2 : 0;
+  auto bytes = [&] { return g.b_slots * part + g.slots * g.w_bytes + g.h_slots * g.h_bytes + (ring ? 0 : staged); };
   // two blocks on an SM where both find room with two slots for w
   int limit = most, blocks = 1;
   if (sizeof(T) == 2) {
@@ -2215,27 +2290,43 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
       break;
     }
   };
-  if (bytes() > most) return cudaErrorInvalidValue;
+  if (bytes() > most || (TMA && !ring)) return cudaErrorInvalidValue;
   grow(g.slots, 2);
-  if (tma) grow(g.b_slots, BASE_SLOTS);
+  if (ring) grow(g.b_slots, BASE_SLOTS);
   grow(g.h_slots, 2);
   grow(g.slots, UP_SLOTS);
-  const int smem = bytes() + 1024;
   UpMaps maps = {};
   bool ok = encode_h(&maps.h, h, g.T, g.R, PL::PH);
-  if (tma && g.base)
-    ok = ok && encode<T>(&maps.base, g.base, g.N, g.T, g.N, 32);
-  if (tma) ok = ok && encode<T>(&maps.out, g.out, g.N, g.T, g.N, 32);
-  if (g.vec & 1)
+  if (TMA && g.base) ok = ok && encode<T>(&maps.base, g.base, g.N, g.T, g.N, 32);
+  if (TMA) ok = ok && encode<T>(&maps.out, g.out, g.N, g.T, g.N, 32);
+  if (g.vec)
     ok = ok && (g.turned ? encode<T>(&maps.w, g.w, g.N, g.r, g.N, g.R, g.L)
                          : encode<T>(&maps.w, g.w, g.r, g.N, g.r, UP_N, g.L, along.bytes));
   if (!ok) return cudaErrorInvalidValue;
   const int64_t items = most_tiles(g.T, g.L, TILE) * g.steps, most_blocks = (int64_t)device_sm_count() * blocks;
+  g.group = items > most_blocks ? 2 : 1;
   const int grid = (int)(items < most_blocks ? items : most_blocks);
   g.jump = (grid - 1) * g.group + 1;
   g.jump_tiles = g.jump / g.steps;
   g.jump_steps = g.jump % g.steps;
-  return launch_clusters<k_adapters_up<T>>(dim3(grid), 1, UP_THREADS<T>, smem, s, maps, g);
+  return launch_clusters<k_adapters_up<T, TMA>>(dim3(grid), 1, UP_THREADS<T>, (size_t)bytes() + 1024, s, maps, g);
+}
+
+template <typename T>
+cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
+  using PL = Planes<T>;
+  const int64_t b = sizeof(T);
+  const Along along(g.R);
+  if (!encode_fn()) return cudaErrorNotSupported;
+  g.steps = (int)ceil_div(g.N, UP_N);
+  g.w_bytes = PL::PD * (g.turned ? g.R * 256 : along.plane());
+  g.h_bytes = PL::PH * along.plane();
+  g.piece = piece_of(g.out, g.N * b | (int64_t)(reinterpret_cast<uintptr_t>(g.base) & 15));
+  g.w_piece = piece_of(g.w, (g.turned ? g.N : g.r) * b);
+  g.vec = g.w_piece == 16 && PL::PD == 1 ? 1 : 0;
+  // TMA: two parts of base have to fit beside h and w (fp32: not at ranks above 64 or so)
+  const bool fits = 2 * UP_EPI * UP_PART<T, true> + g.h_bytes + g.w_bytes <= 232448 - (int)sizeof(UpCtl) - 256 - 1024;
+  return g.piece == 16 && fits ? run_up_as<T, true>(g, h, s) : run_up_as<T, false>(g, h, s);
 }
 
 // The form for few rows: an adapter has sixteen on average at most, whose tiles of 128 would
@@ -2272,7 +2363,7 @@ cudaError_t adapters(const AdapterArgs& a, cudaStream_t s) {
   const Room room = room_of(a.workspace, 0, a.T, g.R);
   constexpr bool F16 = Planes<T>::FD == 0;
   g.prob[0] = {a.x, a.ld, a.K, a.a, F16 ? nullptr : room.h, F16 ? room.h16 : nullptr, F16 ? room.row_scale : nullptr, 0,
-               (aligned16(a.x, a.ld * b) && a.K % 8 == 0 ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0)};
+               piece_of(a.x, a.ld * b | a.K * b), piece_of(a.a, a.K * b)};
   const cudaError_t e = run_down<T>(g, 1, s);
   if (e != cudaSuccess) return e;
   UpArgs up = {g.prob[0].row_scale, a.b, a.base, a.out, a.offsets, a.order, a.T, a.N, a.L, a.r, g.R};
@@ -2298,7 +2389,7 @@ cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const 
     p.h = planes;
     p.out = out;
     p.turned = turned;
-    p.vec = aligned16(x, cols * (int64_t)sizeof(T)) ? 1 : 0;
+    p.piece = piece_of(x, cols * (int64_t)sizeof(T));
     const int64_t n = ceil_div(cols, GRAD_COLS);
     chunks = chunks > n ? chunks : n;
     all += n;
@@ -2312,7 +2403,7 @@ cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const 
   w.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
   if constexpr (PL::P == 1) {
     bool copies = encode_fn() != nullptr;
-    for (int i = 0; i < parts; ++i) copies = copies && w.prob[i].vec;
+    for (int i = 0; i < parts; ++i) copies = copies && w.prob[i].piece == 16;
     if (copies) {
       GradMaps maps = {};
       for (int i = 0; i < parts; ++i)
@@ -2362,10 +2453,10 @@ cudaError_t backward(const AdapterGradArgs& a, cudaStream_t s) {
   if (a.grad_x || a.grad_a)  // g = scale * grad b
     g.prob[problems++] = {a.grad, a.N, a.N, a.b, F16 && !a.grad_a ? nullptr : d.h, scaled ? d.h16 : nullptr,
                           scaled ? d.row_scale : nullptr, 1,
-                          (aligned16(a.grad, a.N * size) ? 1 : 0) | (aligned16(a.b, a.r * size) ? 2 : 0)};
+                          piece_of(a.grad, a.N * size), piece_of(a.b, a.r * size)};
   if (a.grad_b)  // h = scale * x a^T
     g.prob[problems++] = {a.x, a.K, a.K, a.a, h.h, nullptr, nullptr, 0,
-                          (aligned16(a.x, a.K * size) ? 1 : 0) | (aligned16(a.a, a.K * size) ? 2 : 0)};
+                          piece_of(a.x, a.K * size), piece_of(a.a, a.K * size)};
   cudaError_t e = run_down<T>(g, problems, s);
   // the weights' gradients first: they read x and grad again, some of which L2 still has
   if (e == cudaSuccess && (a.grad_a || a.grad_b)) e = run_grads<T>(a, g.R, h.h, d.h, s);

@@ -195,6 +195,13 @@ __device__ __forceinline__ void copy16(void* to, const void* from, bool in) {
                "r"(in ? 16 : 0)
                : "memory");
 }
+// The same by 8 or 4 bytes, for rows that are aligned to no more.
+template <int BYTES>
+__device__ __forceinline__ void copy_small(void* to, const void* from, bool take) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(smem_addr(to)), "l"(from), "n"(BYTES),
+               "r"(take ? BYTES : 0)
+               : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most N of this thread's groups are under way.
 template <int N>
