@@ -134,9 +134,18 @@ struct Raw8 {
       for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint4*>(t)[i];
     }
   }
-  // the same from rows aligned to `piece` bytes
+  // The same from rows aligned to `piece` bytes; 16-bit values at odd places by the words that
+  // hold them, the halves that are not theirs dropped.
   __device__ __forceinline__ void load_by(const T* p, int n, int piece) {
-    if (n >= 8 && piece == 8) {
+    if (sizeof(T) == 2 && n >= 8 && piece == 2) {
+      const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 2);
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) - odd);
+      uint32_t v[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) v[i] = i < 4 || odd ? __ldg(from + i) : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(w)[i] = __funnelshift_r(v[i], v[i + 1], odd * 8);
+    } else if (n >= 8 && piece == 8) {
 #pragma unroll
       for (int i = 0; i < 2 * W; ++i) reinterpret_cast<uint2*>(w)[i] = __ldg(reinterpret_cast<const uint2*>(p) + i);
     } else if (n >= 8 && piece == 4) {
@@ -191,6 +200,13 @@ struct Raw4 {
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(t + i);
       }
     }
+  }
+  __device__ __forceinline__ void widen(float (&v)[4]) const {
+    alignas(16) T t[4];
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) reinterpret_cast<uint32_t*>(t)[i] = w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = to_f32<T>(t[i]);
   }
 };
 // d += A B of a warp: sixteen rows of A (this lane's words of row lane / 4 in a, of the eighth
@@ -760,14 +776,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
       const int left = (int)(p.K - k < KB ? p.K - k : KB);
       if (!ASYNC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) held_x[ASYNC ? 0 : i].load(xr[i] + k, xr[i] ? left - u * 8 : 0, p.x_piece == 16);
+        for (int i = 0; i < 4; ++i) held_x[ASYNC ? 0 : i].load_by(xr[i] + k, xr[i] ? left - u * 8 : 0, p.x_piece);
       }
       if (!copy_w) {
 #pragma unroll
         for (int i = 0; i < RU; ++i) {
           int n;
           const T* from = w_unit(i, k, left, n);
-          held_w[i].load(from, n, p.w_piece == 16);
+          held_w[i].load_by(from, n, p.w_piece);
         }
       }
     };
@@ -781,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
           copy_unit(to + at, xr[i] + k, xr[i] ? left - u * 8 : 0, p.x_piece, p.x);
         } else {
           Raw8<T> raw;
-          if (ASYNC) raw.load(xr[i] + k, xr[i] ? left - u * 8 : 0, false);
+          if (ASYNC) raw.load_by(xr[i] + k, xr[i] ? left - u * 8 : 0, 2);
           else raw = held_x[ASYNC ? 0 : i];
           uint4 v[P];
           planes_of<T, P>(raw, v);
@@ -1264,34 +1280,49 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       } else {
         const T* w = static_cast<const T*>(g.w) + (int64_t)t.l * r * g.N;
         const int left = (int)(g.N - n0 < UP_N ? g.N - n0 : UP_N);
-        int un = lt / ru, uj = lt - un * ru;
-#pragma unroll 4
-        for (int i = lt; i < TILE / 8 * R; i += LT, un += row_by, uj += ju_by) {
+        const int un0 = lt / ru, uj0 = lt - un0 * ru;
+        int un = un0, uj = uj0;
+        // unit i of this thread: where it is, how many of its values, where it goes
+        auto unit = [&](int i, const T*& from, int& have, uint8_t*& at) {
           if (uj >= ru) {
             uj -= ru;
             ++un;
           }
-          const T* from;
-          uint8_t* at;
-          int have, pitch;
           if (g.turned) {  // eight n of one j; n lies along the operand's N
             const int nu = i & 15, j = i >> 4;
             from = w + j * g.N + n0 + nu * 8;
             have = j < r ? left - nu * 8 : 0;
             at = to + (nu >> 3) * (R * 128) + j * 128 + (((nu ^ j) & 7) << 4);
-            pitch = R * 256;
           } else {  // eight j of one n
             from = w + (n0 + un) * r + uj * 8;
             have = un < left ? r - uj * 8 : 0;
             at = to + along.at(un, uj);
-            pitch = plane;
           }
-          Raw8<T> raw;
-          raw.load_by(from, have, g.w_piece);
-          uint4 v[P];
-          planes_of<T, P>(raw, v);
+          un += row_by;
+          uj += ju_by;
+        };
+        const T* from;
+        int have;
+        uint8_t* at;
+        if (P == 1 && g.w_piece >= 4) {  // all of it under way at once
+          for (int i = lt; i < TILE / 8 * R; i += LT) {
+            unit(i, from, have, at);
+            copy_unit(at, from, have, g.w_piece, g.order);
+          }
+          ptx::copy_commit();
+          ptx::copy_wait<0>();
+        } else {
+          const int pitch = g.turned ? R * 256 : plane;
+#pragma unroll 4
+          for (int i = lt; i < TILE / 8 * R; i += LT) {
+            unit(i, from, have, at);
+            Raw8<T> raw;
+            raw.load(from, have, g.w_piece == 16);
+            uint4 v[P];
+            planes_of<T, P>(raw, v);
 #pragma unroll
-          for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(at + c * pitch) = v[c];
+            for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(at + c * pitch) = v[c];
+          }
         }
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive(&ctl.wfull[slot]);
@@ -1658,7 +1689,7 @@ struct GradArgs {
   GradProblem prob[2];
   const int32_t *offsets, *order;
   int64_t T;
-  int L, r, R, log_ctas, cols, stages;
+  int L, r, R, log_ctas, cols, stages, blocks;  // blocks of 16 of R
 };
 // A CTA's sums, from tensor memory to its shared memory: a column's r sums after another's,
 // one word apart.
@@ -1751,7 +1782,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     if (HELD) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        held[HELD ? i : 0].load(x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, p.piece == 16);
+        held[HELD ? i : 0].load_by(x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, p.piece);
       rows_of(b + 1);
     }
   };
@@ -1765,7 +1796,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
       } else {
         Raw8<T> raw;
         if (HELD) raw = held[HELD ? i : 0];
-        else raw.load(x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, false);
+        else raw.load_by(x + next[i] * p.cols, next[i] >= 0 ? left - u * 8 : 0, 2);
         uint4 v[P];
         planes_of<T, P>(raw, v);
 #pragma unroll
@@ -1846,6 +1877,93 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   if (work) grad_out<T, kThreads>(sm, g, p, l, rank, col0);
   ptx::cluster_sync_reads();  // no CTA ends while another reads its sums
   tear_down(ctl, tmem, g.cols);
+}
+
+// The same by fp32 FMAs, for little work: nothing is staged but h, no tensor memory is set up,
+// and a block has sixteen j's of 256 columns, four by four for each thread.
+constexpr int FMA_J = 16, FMA_COLS = 256, FMA_ROWS = 64, FMA_THREADS = 256;
+template <typename T>
+__global__ void __launch_bounds__(FMA_THREADS) k_adapters_grad_fma(const __grid_constant__ GradArgs g) {
+  constexpr int PH = Planes<T>::PH, U = 8;
+  __shared__ __align__(16) float hs[FMA_ROWS][FMA_J];
+  __shared__ int rows[FMA_ROWS];
+  __shared__ __align__(16) float sums[FMA_J][FMA_COLS];
+  const int problem = blockIdx.z / g.blocks;
+  const GradProblem& p = g.prob[problem];
+  const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank(), R = g.R, r = g.r;
+  const int tid = threadIdx.x, lane = tid & 63, l = blockIdx.y;
+  const int j0 = (blockIdx.z - problem * g.blocks) * FMA_J, j4 = (tid >> 6) * 4;
+  const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * FMA_COLS;
+  const bool work = col0 < p.cols;  // (the problems may have different numbers of columns)
+  const int left = work ? (int)(p.cols - col0 < FMA_COLS ? p.cols - col0 : FMA_COLS) : 0;
+  ptx::griddep_wait();
+  ptx::griddep_launch();
+  const int first = __ldg(g.offsets + l), n = __ldg(g.offsets + l + 1) - first;
+  const int per = (n + C - 1) >> g.log_ctas, t0 = min(rank * per, n), t1 = work ? min(t0 + per, n) : t0;
+  const T* x = static_cast<const T*>(p.x) + col0 + lane * 4;
+  const int mine = left - lane * 4;
+  const bool vec = p.piece >= 4 * (int)sizeof(T);
+  float acc[4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+  for (int t = t0; t < t1; t += FMA_ROWS) {
+    const int live = min(FMA_ROWS, t1 - t);
+    if (tid < FMA_ROWS) rows[tid] = tid < live ? __ldg(g.order + first + t + tid) : 0;
+    for (int i = tid; i < FMA_ROWS * (FMA_J / 2); i += FMA_THREADS) {  // two j's; zeros past the end
+      const int row = i / (FMA_J / 2), j = i % (FMA_J / 2) * 2;
+      float a = 0.0f, b = 0.0f;
+      if (row < live) {
+        const uint32_t* h = reinterpret_cast<const uint32_t*>(p.h + (int64_t)(first + t + row) * PH * R + j0 + j);
+#pragma unroll
+        for (int c = 0; c < PH; ++c) {
+          const uint32_t w = __ldcg(h + c * (R / 2));
+          a += __uint_as_float(w << 16);
+          b += __uint_as_float(w & 0xFFFF0000u);
+        }
+      }
+      hs[row][j] = a;
+      hs[row][j + 1] = b;
+    }
+    __syncthreads();
+    if (mine > 0) {
+#pragma unroll 1
+      for (int i = 0; i < live; i += U) {
+        Raw4<T> raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u].load(x + rows[i + u] * p.cols, i + u < live ? mine : 0, vec);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float4 h = *reinterpret_cast<const float4*>(&hs[i + u][j4]);
+          float v[4];
+          raw[u].widen(v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[0][e] = fmaf(h.x, v[e], acc[0][e]);
+            acc[1][e] = fmaf(h.y, v[e], acc[1][e]);
+            acc[2][e] = fmaf(h.z, v[e], acc[2][e]);
+            acc[3][e] = fmaf(h.w, v[e], acc[3][e]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<float4*>(&sums[j4 + j][lane * 4]) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+  ptx::cluster_sync();
+  const int js = min(FMA_J, r - j0), all = left * js, share = (all + C - 1) >> g.log_ctas;
+  const int e0 = rank * share, e1 = min(e0 + share, all);
+  T* out = static_cast<T*>(p.out) + (int64_t)l * r * p.cols;
+  for (int e = e0 + tid; e < e1; e += FMA_THREADS) {
+    const int col = p.turned ? e / js : e % left, j = p.turned ? e - col * js : e / left;
+    float sum = 0.0f;
+    for (int c = 0; c < C; ++c) sum += __uint_as_float(ptx::ld_cluster(ptx::cluster_addr(&sums[j][col], c)));
+    out[p.turned ? (col0 + col) * r + j0 + j : (int64_t)(j0 + j) * p.cols + col0 + col] = from_f32<T>(sum);
+  }
+  ptx::cluster_sync_reads();  // no CTA ends while another reads its sums
 }
 
 // The same for bf16 rows that 16-byte copies can reach, with equal shares however the rows are spread
@@ -2396,9 +2514,25 @@ cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const 
   };
   if (a.grad_a) add(a.x, a.K, d, a.grad_a, 0);
   if (a.grad_b) add(a.grad, a.N, h, a.grad_b, 1);
-  // about three blocks per SM, of four stages of rows on average at least
-  int64_t want = 3 * (int64_t)device_sm_count() / (all * a.L);
-  const int64_t most = a.T / a.L / (4 * GRAD_ROWS);
+  w.blocks = R / FMA_J;
+  // Sixteen rows an adapter on average at most: FMAs (all of a gradient, us with them / in tiles:
+  // bf16 318 rows of 61 adapters, r 16, 344 x 120, 29.1 / 55.2; fp32 270 of 48, 2048 x 145, 49.6 /
+  // 64.4; fp32 512 of 64, r 64, 2048 x 2048, 235 / 348; but fp32 308 of 15, 1045 x 439, 39.5 / 36.0,
+  // bf16 512 of 8, 4096 x 4096, 45.3 / 36.8).
+  if (a.T <= 16 * a.L) {
+    int64_t most_chunks = 0;
+    for (int i = 0; i < parts; ++i) {
+      const int64_t n = ceil_div(w.prob[i].cols, FMA_COLS);
+      most_chunks = most_chunks > n ? most_chunks : n;
+    }
+    return launch_clusters<k_adapters_grad_fma<T>>(dim3((unsigned)most_chunks, a.L, parts * w.blocks), 1, FMA_THREADS, 0,
+                                                   s, w);
+  }
+  // About four blocks per SM, of a stage of rows on average at least (fp32 2047 rows of 4 adapters,
+  // r 8, 1000 x 2048: 41.4 us for 52.8 with four stages at least; fp32 4096 of 8, r 16, 2048 x
+  // 2048: 79 for 95 with three blocks).
+  int64_t want = 4 * (int64_t)device_sm_count() / (all * a.L);
+  const int64_t most = a.T / a.L / GRAD_ROWS;
   want = want < most ? want : most;
   w.log_ctas = want >= 8 ? 3 : (want >= 4 ? 2 : (want >= 2 ? 1 : 0));
   if constexpr (PL::P == 1) {
