@@ -35,7 +35,8 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_
 }
 
 // A sum as two fp32 numbers, exact to 2^-46 or so of its terms' magnitudes: 64-bit adds run
-// at a 64th of the fp32 rate here (with them a chunk's sums took 2 us more).
+// at a 64th of the fp32 rate here (with them a chunk's sums took 2 us more, and a sequence's
+// loss 1 to 2.5).
 struct Sum {
   float hi, lo;
   __device__ __forceinline__ void add(float v) {
@@ -46,6 +47,19 @@ struct Sum {
   __device__ __forceinline__ void add(const Sum& o) {
     add(o.hi);
     lo += o.lo;
+  }
+  __device__ __forceinline__ void add_times(const Sum& o, float c) {
+    const float v = o.hi * c;
+    add(v);
+    lo += fmaf(o.hi, c, -v) + o.lo * c;
+  }
+  // the warp's sum, the same in lane 0 whatever the timing
+  __device__ __forceinline__ void over_lanes() {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const Sum o = {__shfl_xor_sync(kAll, hi, d), __shfl_xor_sync(kAll, lo, d)};
+      add(o);
+    }
   }
 };
 
@@ -120,7 +134,7 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& a, int64_t first, 
 template <int THREADS = kThreads>
 __device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, int C, int rank, const Sum* sums,
                                        const int32_t* count, Sum* gathered, int32_t* counts) {
-  __shared__ double loss[THREADS / 32];
+  __shared__ Sum loss[THREADS / 32];
   const int E = a.E, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < E; e += THREADS) {
     const uint32_t at = ptx::cluster_addr(gathered + rank * E + e, 0);
@@ -130,7 +144,7 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, i
   }
   ptx::cluster_sync();
   if (rank) return;
-  double part = 0.0;
+  Sum part = {0.0f, 0.0f};
   for (int e = threadIdx.x; e < E; e += THREADS) {
     Sum sum = {0.0f, 0.0f};
     int32_t c = 0;
@@ -139,18 +153,15 @@ __device__ __forceinline__ void finish(const BalanceArgs& a, int s, int64_t n, i
       c += counts[q * E + e];
     }
     a.counts[(int64_t)s * E + e] = c;
-    part += ((double)sum.hi + sum.lo) * c;
+    part.add_times(sum, (float)c);
   }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) part += __shfl_xor_sync(kAll, part, d);
+  part.over_lanes();
   if (lane == 0) loss[warp] = part;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) sum += loss[w];
-    a.loss[s] = n > 0 ? (float)(sum * E / ((double)a.k * n * n)) : 0.0f;
-  }
+  if (warp) return;
+  part = lane < THREADS / 32 ? loss[lane] : Sum{0.0f, 0.0f};
+  part.over_lanes();
+  if (lane == 0) a.loss[s] = n > 0 ? (part.hi + part.lo) * ((float)E / ((float)a.k * (float)n) / (float)n) : 0.0f;
 }
 
 // Sums of the block's warps [warp][E], into the first one's place.
