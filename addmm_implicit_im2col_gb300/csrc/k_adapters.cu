@@ -62,8 +62,8 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int L, bool
   __syncthreads();
   return found;
 }
-// All tiles of the buckets 0 .. B - 1: first [B + 1], the buckets' first places, and before
-// [B + 1], the tiles before each.  All threads of the block; ends with a barrier.
+// All tiles of the buckets 0 .. B - 1: first [B + 1] (or null), the buckets' first places, and
+// before [B + 1], the tiles before each.  All threads of the block; ends with a barrier.
 template <int THREADS>
 __device__ __forceinline__ void count_tiles(const int32_t* offsets, int B, int height, int* first, int* before,
                                             int* sums) {
@@ -72,10 +72,10 @@ __device__ __forceinline__ void count_tiles(const int32_t* offsets, int B, int h
   int tiles = 0;
   for (int e = e0; e < e0 + per && e < B; ++e) {
     const int at = __ldg(offsets + e);
-    first[e] = at;
+    if (first) first[e] = at;
     tiles += (__ldg(offsets + e + 1) - at + height - 1) / height;
   }
-  if (tid == 0) first[B] = __ldg(offsets + B);
+  if (tid == 0 && first) first[B] = __ldg(offsets + B);
   int upto = tiles;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -88,7 +88,7 @@ __device__ __forceinline__ void count_tiles(const int32_t* offsets, int B, int h
   int at = upto - tiles;
   for (int e = e0; e < e0 + per && e < B; ++e) {
     before[e] = at;
-    at += (__ldg(offsets + e + 1) - first[e] + height - 1) / height;
+    at += (__ldg(offsets + e + 1) - __ldg(offsets + e) + height - 1) / height;
   }
   if (tid == THREADS - 1) before[B] = upto;
   __syncthreads();
@@ -548,7 +548,7 @@ struct DownArgs {
   const float* scale;
   const int32_t *offsets, *order;
   int64_t T;
-  int L, r, R, log_ctas, cols, stages;  // R: r rounded up to 16
+  int L, r, R, log_ctas, cols, stages, w_bytes;  // R: r rounded up to 16; w_bytes: of w in a stage
 };
 struct RingCtl {
   uint64_t empty[4], drain;
@@ -964,7 +964,7 @@ __global__ void __launch_bounds__(DOWN_THREADS)
     // rows of the tile; past its end the last one again (their sums are not used)
     if (tid < TILE) rows[tid] = g.order[t.p0 + min(tid, t.rows - 1)];
     __syncthreads();
-    const int wb = p.turned ? down_w_bytes(R) : R * 128, stage_bytes = XP + down_w_bytes(R);
+    const int wb = p.turned ? down_w_bytes(R) : R * 128, stage_bytes = XP + g.w_bytes;
     // every C-th block of K is this CTA's: what the cluster reads at one time lies together
     const int blocks = (int)((p.K + KB - 1) / KB), b0 = 0, b1 = (blocks - rank + C - 1) >> g.log_ctas;
     auto k_of = [&](int b) { return ((b << g.log_ctas) + rank) * KB; };
@@ -1982,7 +1982,7 @@ struct GradCtl {
   uint32_t tmem_base;
   int abort;
   int sums[16];
-  int before[kAdapters + 2], first[kAdapters + 2];  // row blocks before an adapter, its first row
+  int before[kAdapters + 2];  // row blocks before an adapter
 };
 
 __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __grid_constant__ GradMaps maps,
@@ -2010,7 +2010,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
   }
   ptx::griddep_wait();
   ptx::griddep_launch();
-  count_tiles<GRAD_THREADS>(g.offsets, L, GRAD_ROWS, ctl.first, ctl.before, ctl.sums);
+  count_tiles<GRAD_THREADS>(g.offsets, L, GRAD_ROWS, nullptr, ctl.before, ctl.sums);
   const int blocks = ctl.before[L];
   auto run_of = [&](int q) { return (int)((int64_t)blocks * q >> g.log_ctas); };
   const int b0 = run_of(rank), b1 = run_of(rank + 1);
@@ -2047,8 +2047,8 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
       Rows q = {0, 0, -1, -1};
       if (b >= b1) return q;
       while (ctl.before[l + 1] <= b) ++l;
-      q.place = ctl.first[l] + (b - ctl.before[l]) * GRAD_ROWS;
-      q.have = min(GRAD_ROWS, ctl.first[l + 1] - q.place);
+      q.place = __ldg(g.offsets + l) + (b - ctl.before[l]) * GRAD_ROWS;
+      q.have = min(GRAD_ROWS, __ldg(g.offsets + l + 1) - q.place);
       if (lane < q.have) q.lo = __ldg(g.order + q.place + lane);
       if (lane + 32 < q.have) q.hi = __ldg(g.order + q.place + lane + 32);
       return q;
@@ -2217,7 +2217,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
   }
   // ---- adapters without rows: zeros
   for (int l = rank; l < L; l += C) {
-    if (ctl.first[l + 1] > ctl.first[l]) continue;
+    if (ctl.before[l + 1] > ctl.before[l]) continue;
     for (int e = tid; e < left * r; e += GRAD_THREADS) {
       const int col = p.turned ? e / r : e % left, j = p.turned ? e - col * r : e / left;
       out[(int64_t)l * r * p.cols + (p.turned ? (col0 + col) * r + j : (int64_t)j * p.cols + col0 + col)] =
@@ -2351,7 +2351,10 @@ cudaError_t run_down_tma(DownArgs& g, int problems, cudaStream_t s) {
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
   // two blocks per SM, with a ring of up to 104 KB each
   g.log_ctas = cluster_log(2 * (int64_t)device_sm_count(), g.T, g.L, problems);
-  const int stage = XP + down_w_bytes(g.R), sums = TILE * (g.R * 4 + 16);
+  g.w_bytes = g.R * 128;
+  for (int i = 0; i < problems; ++i)
+    if (g.prob[i].turned) g.w_bytes = down_w_bytes(g.R);
+  const int stage = XP + g.w_bytes, sums = TILE * (g.R * 4 + 16);
   g.stages = (104 << 10) / stage < DOWN_STAGES ? (104 << 10) / stage : DOWN_STAGES;
   const int bytes = g.stages * stage > sums ? g.stages * stage : sums;
   g.cols = tmem_cols(g.R);
