@@ -2349,7 +2349,9 @@ cudaError_t run_down_tma(DownArgs& g, int problems, cudaStream_t s) {
     if (!w || !encode<T>(&maps.x[i], p.x, p.K, g.T, p.ld, 32)) return cudaErrorInvalidValue;
   }
   const int64_t tiles = most_tiles(g.T, g.L, TILE);
-  // two blocks per SM, with a ring of up to 104 KB each
+  // Two blocks per SM, with a ring of up to 104 KB each (what is under way decides: 8192 rows of
+  // 8 adapters, r 32, 4096 x 4096, bf16, take 44.9 us, 48.2 with 60 KB); three stages at least,
+  // as Landing needs.
   g.log_ctas = cluster_log(2 * (int64_t)device_sm_count(), g.T, g.L, problems);
   g.w_bytes = g.R * 128;
   for (int i = 0; i < problems; ++i)
