@@ -2,7 +2,10 @@
 //
 //   out[t] = base[t] + scale[l] * (x[t] a[l]^T) b[l]^T,   l the adapter of row t,
 //
-// and their gradients.  The rows come in adapter order (moe_layout).
+// and their gradients.  The rows come in adapter order (moe_layout).  Forms: few rows, one
+// launch (k_adapters_few); tiles of 128 rows, two (k_adapters_down or _down_tma, then _up);
+// the gradient of x the same two with the weights' roles exchanged; the weights' gradients
+// k_adapters_grad, _grad_runs or, for a handful of rows each, _grad_fma.
 #include <mutex>
 #include <type_traits>
 
@@ -172,8 +175,8 @@ struct Raw8 {
 // short: both products use mma.sync (a warp's small tiles need no shared memory and no
 // barriers, unlike tcgen05's), whose operands come straight from global memory, sixteen
 // bytes a lane: the order of the values along the summed axis is the same for both operands,
-// whatever it is.  The same with fp32 FMAs, unrolled for 1, 2, 4 or 8 rows, took 30 us where
-// this takes
+// whatever it is.  One row of 8 adapters, r 16, 4096 x 4096, bf16, takes 6.0 us, 64 rows of 64
+// adapters, 4096 x 1024, 7.4 (10.5 MB of weights: 1.4 TB/s).
 constexpr int FEW = 8;
 constexpr int FEW_ROWS = 1024;  // rows whose numbers are asked for before the tile is known
 constexpr int FEW_N = 512;      // outputs staged at once
@@ -474,7 +477,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_const
 // CTAs.  The second adds h b^T to base, a CTA for each 128 x 128 outputs.  Both stream
 // (x; base and out), and many small CTAs on an SM hide the memory's latency.  One launch
 // for both (h stayed in the cluster) took 66 us for 8192 rows, 8 adapters, r 32, 4096 x
-// 4096, bf16, where these take
+// 4096, bf16, where these take 44.9: 18 for the first (3.7 TB/s of x; all but 10 us of it are
+// the launch, the two loads that wait for one another before x can be asked for, and the
+// cluster's sums), 27 for the second (5 TB/s of base and out).
 //
 // A value is a sum of bf16 numbers ("planes"): bf16 1, fp16 2, fp32 3, exactly; an element
 // of h is kept as PH of them (2 for the 16-bit types: to 2^-17 of its value; 3 for fp32).
@@ -1672,9 +1677,11 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
 // ------------------------------------------------------- weights' gradients
 // grad_a[l][j][k] = sum over l's rows of g[p][j] x[row][k], and grad_b[l][n][j] with h and
 // grad.  A cluster has one adapter and 128 columns of x (or grad): they are the MMA's M,
-// the r columns of g its N, the rows its K.  CTA q of S takes a run of the rows; the
+// the r columns of g its N, the rows its K.  CTA q of C takes a run of the rows; the
 // cluster's sums are taken in the order of the CTAs.  Tiles of x and of g's planes are
-// loaded by rows, so their columns lie along the operands' M and N ("MN-major").
+// loaded by rows, so their columns lie along the operands' M and N ("MN-major").  fp32 and
+// fp16, whose planes pass through registers, and bf16 rows not aligned to 16 bytes: fp32
+// 2047 rows of 4 adapters, r 8, 1000 x 2048, all gradients 37.7 us.
 constexpr int GRAD_ROWS = 64;  // rows per stage
 constexpr int GRAD_COLS = 128;
 
@@ -1879,27 +1886,27 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   tear_down(ctl, tmem, g.cols);
 }
 
-// The same by fp32 FMAs, for little work: nothing is staged but h, no tensor memory is set up,
-// and a block has sixteen j's of 256 columns, four by four for each thread.
+// The same by fp32 FMAs, for adapters with few rows: nothing is staged but h, no tensor memory
+// is set up, and a block has sixteen j's of 256 columns of one adapter, four by four for each
+// thread, with all its rows in their order.  (The rule and its figures: run_grads.)
 constexpr int FMA_J = 16, FMA_COLS = 256, FMA_ROWS = 64, FMA_THREADS = 256;
 template <typename T>
 __global__ void __launch_bounds__(FMA_THREADS) k_adapters_grad_fma(const __grid_constant__ GradArgs g) {
   constexpr int PH = Planes<T>::PH, U = 8;
   __shared__ __align__(16) float hs[FMA_ROWS][FMA_J];
   __shared__ int rows[FMA_ROWS];
-  __shared__ __align__(16) float sums[FMA_J][FMA_COLS];
+  __shared__ __align__(16) float sums[FMA_J][FMA_COLS + 4];
   const int problem = blockIdx.z / g.blocks;
   const GradProblem& p = g.prob[problem];
-  const int C = 1 << g.log_ctas, rank = (int)ptx::cluster_rank(), R = g.R, r = g.r;
+  const int R = g.R, r = g.r;
   const int tid = threadIdx.x, lane = tid & 63, l = blockIdx.y;
   const int j0 = (blockIdx.z - problem * g.blocks) * FMA_J, j4 = (tid >> 6) * 4;
-  const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * FMA_COLS;
-  const bool work = col0 < p.cols;  // (the problems may have different numbers of columns)
-  const int left = work ? (int)(p.cols - col0 < FMA_COLS ? p.cols - col0 : FMA_COLS) : 0;
+  const int64_t col0 = (int64_t)blockIdx.x * FMA_COLS;
   ptx::griddep_wait();
   ptx::griddep_launch();
+  if (col0 >= p.cols) return;  // (the problems may have different numbers of columns)
+  const int left = (int)(p.cols - col0 < FMA_COLS ? p.cols - col0 : FMA_COLS);
   const int first = __ldg(g.offsets + l), n = __ldg(g.offsets + l + 1) - first;
-  const int per = (n + C - 1) >> g.log_ctas, t0 = min(rank * per, n), t1 = work ? min(t0 + per, n) : t0;
   const T* x = static_cast<const T*>(p.x) + col0 + lane * 4;
   const int mine = left - lane * 4;
   const bool vec = p.piece >= 4 * (int)sizeof(T);
@@ -1908,8 +1915,8 @@ __global__ void __launch_bounds__(FMA_THREADS) k_adapters_grad_fma(const __grid_
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-  for (int t = t0; t < t1; t += FMA_ROWS) {
-    const int live = min(FMA_ROWS, t1 - t);
+  for (int t = 0; t < n; t += FMA_ROWS) {
+    const int live = min(FMA_ROWS, n - t);
     if (tid < FMA_ROWS) rows[tid] = tid < live ? __ldg(g.order + first + t + tid) : 0;
     for (int i = tid; i < FMA_ROWS * (FMA_J / 2); i += FMA_THREADS) {  // two j's; zeros past the end
       const int row = i / (FMA_J / 2), j = i % (FMA_J / 2) * 2;
@@ -1953,17 +1960,13 @@ __global__ void __launch_bounds__(FMA_THREADS) k_adapters_grad_fma(const __grid_
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     *reinterpret_cast<float4*>(&sums[j4 + j][lane * 4]) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-  ptx::cluster_sync();
-  const int js = min(FMA_J, r - j0), all = left * js, share = (all + C - 1) >> g.log_ctas;
-  const int e0 = rank * share, e1 = min(e0 + share, all);
+  __syncthreads();
+  const int js = min(FMA_J, r - j0), all = left * js;
   T* out = static_cast<T*>(p.out) + (int64_t)l * r * p.cols;
-  for (int e = e0 + tid; e < e1; e += FMA_THREADS) {
+  for (int e = tid; e < all; e += FMA_THREADS) {
     const int col = p.turned ? e / js : e % left, j = p.turned ? e - col * js : e / left;
-    float sum = 0.0f;
-    for (int c = 0; c < C; ++c) sum += __uint_as_float(ptx::ld_cluster(ptx::cluster_addr(&sums[j][col], c)));
-    out[p.turned ? (col0 + col) * r + j0 + j : (int64_t)(j0 + j) * p.cols + col0 + col] = from_f32<T>(sum);
+    out[p.turned ? (col0 + col) * r + j0 + j : (int64_t)(j0 + j) * p.cols + col0 + col] = from_f32<T>(sums[j][col]);
   }
-  ptx::cluster_sync_reads();  // no CTA ends while another reads its sums
 }
 
 // The same for bf16 rows that 16-byte copies can reach, with equal shares however the rows are spread
@@ -1971,8 +1974,10 @@ __global__ void __launch_bounds__(FMA_THREADS) k_adapters_grad_fma(const __grid_
 // the blocks of 64 rows, counted over the adapters one after the other.  Two accumulators:
 // the next adapter's MMAs run while one's sums are written.  An adapter that lies within a
 // run is that CTA's to write; one that several runs share (a run has two such at most) is
-// summed at the end, in the order of the CTAs, each taking a part of its gradient.  8192 rows
-// of 8 adapters, r 16, 4096 x 4096, an adapter's rows to each cluster: us for
+// summed at the end, in the order of the CTAs, each taking a part of its gradient.  All
+// gradients of 8192 rows of 8 adapters, r 16, 4096 x 4096: 105 us, 113 with an adapter's rows to
+// each cluster (one adapter: 90, 85).  This launch takes 31 of the 90 (134 MB, a third of them
+// from L2): 0.75 us for each block of a CTA, whatever the number of stages beyond three.
 struct GradMaps {
   CUtensorMap x[2], h[2];  // of each problem, by 64 rows
 };
@@ -2455,11 +2460,16 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
 }
 
 // The form for few rows: an adapter has sixteen on average at most, whose tiles of 128 would
-// be nearly empty, or there are few altogether, and one launch is over sooner than two.  us
-// with it / in tiles, bf16, 4096 x 4096: 64 rows of 64 adapters, r 16, 9.5 / 29.2; 1000 of 64
-// 31.8 / 45.8; 2000 of 64 57.2 / 49.5; 512 of 8 19.0 / 21.9; 1000 of 8 35.2 / 23.9; r 64: 64 of 8
-// 15.4 / 18.4, 256 of 8 19.3 / 19.6.
-bool few_rows(int64_t T, int64_t L, int64_t r) { return T <= 16 * L || T * r <= 8192; }
+// be nearly empty, or there are few altogether, and one launch is over sooner than two; but not
+// more tiles of eight than 256, whose clusters run one after the other.  us with it / in tiles
+// (bf16, 4096 x 4096 where nothing else is said): 64 rows of 64 adapters, r 16, 9.1 / 27.0; 1000
+// of 64 30.5 / 34.5; 2000 of 64 50.0 / 35.2; 8000 of 600, r 8, 512 x 512 78.9 / 41.1; 600 of 60,
+// 1024 x 2048 11.6 / 26.7; 128 of 1 9.7 / 11.9; 512 of 1 21.9 / 12.8, 1024 x 1024 10.6 / 10.2;
+// 256 of 1, r 32, 1024 x 1024 7.5 / 10.4; 256 of 8, r 64, 19.2 / 19.4; fp32 777 of 5, r 9, 1100 x
+// 1001 12.6 / 17.4.
+bool few_rows(int64_t T, int64_t L, int64_t r) {
+  return (T <= 16 * L || T * r <= 8192) && most_tiles(T, L, FEW) <= 256;
+}
 
 // The workspace of one h (of g): its planes, its scaled fp16 rows, their scales.
 size_t room_bytes(int64_t T, int64_t R) { return (size_t)(T * R * (6 + 4) + (T + 3) / 4 * 16); }
