@@ -1895,7 +1895,6 @@ __global__ void __launch_bounds__(FMA_THREADS) k_adapters_grad_fma(const __grid_
   constexpr int PH = Planes<T>::PH, U = 8;
   __shared__ __align__(16) float hs[FMA_ROWS][FMA_J];
   __shared__ int rows[FMA_ROWS];
-  __shared__ __align__(16) float sums[FMA_J][FMA_COLS + 4];
   const int problem = blockIdx.z / g.blocks;
   const GradProblem& p = g.prob[problem];
   const int R = g.R, r = g.r;
@@ -1957,15 +1956,30 @@ __global__ void __launch_bounds__(FMA_THREADS) k_adapters_grad_fma(const __grid_
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<float4*>(&sums[j4 + j][lane * 4]) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-  __syncthreads();
-  const int js = min(FMA_J, r - j0), all = left * js;
+  if (mine <= 0) return;
   T* out = static_cast<T*>(p.out) + (int64_t)l * r * p.cols;
-  for (int e = tid; e < all; e += FMA_THREADS) {
-    const int col = p.turned ? e / js : e % left, j = p.turned ? e - col * js : e / left;
-    out[p.turned ? (col0 + col) * r + j0 + j : (int64_t)(j0 + j) * p.cols + col0 + col] = from_f32<T>(sums[j][col]);
+  const int64_t col = col0 + lane * 4;
+  auto put = [&](T* to, const float (&v)[4], int have, bool whole) {
+    if (whole && have >= 4) {
+      alignas(16) T t[4] = {from_f32<T>(v[0]), from_f32<T>(v[1]), from_f32<T>(v[2]), from_f32<T>(v[3])};
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(t);
+      else *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < have) to[i] = from_f32<T>(v[i]);
+    }
+  };
+  const bool units = (reinterpret_cast<uintptr_t>(p.out) & (4 * sizeof(T) - 1)) == 0 &&
+                     ((p.turned ? (int64_t)r : p.cols) & 3) == 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (p.turned) {  // four j's of a column
+      const float v[4] = {acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+      if (i < mine) put(out + (col + i) * r + j0 + j4, v, r - j0 - j4, units);
+    } else if (j0 + j4 + i < r) {  // four columns of a j
+      put(out + (int64_t)(j0 + j4 + i) * p.cols + col, acc[i], mine, units);
+    }
   }
 }
 
