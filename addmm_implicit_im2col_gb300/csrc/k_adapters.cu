@@ -2546,11 +2546,14 @@ cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const 
   if (a.grad_a) add(a.x, a.K, d, a.grad_a, 0);
   if (a.grad_b) add(a.grad, a.N, h, a.grad_b, 1);
   w.blocks = R / FMA_J;
-  // Sixteen rows an adapter on average at most: FMAs (all of a gradient, us with them / in tiles:
-  // bf16 318 rows of 61 adapters, r 16, 344 x 120, 29.1 / 55.2; fp32 270 of 48, 2048 x 145, 49.6 /
-  // 64.4; fp32 512 of 64, r 64, 2048 x 2048, 235 / 348; but fp32 308 of 15, 1045 x 439, 39.5 / 36.0,
-  // bf16 512 of 8, 4096 x 4096, 45.3 / 36.8).
-  if (a.T <= 16 * a.L) {
+  // Adapters of up to 48 rows on average (16 where x cannot be read by four values): FMAs (all
+  // gradients, us with them / in tiles, r 16: bf16 318 rows of 61 adapters, 344 x 120, 21.2 / 55.2;
+  // bf16 1200 of 42, 1024 x 1024, 30.6 / 38.3; fp32 1636 of 42, 448 x 3232, 56.9 / 69.7; but bf16 512
+  // of 8, 4096 x 4096, 45.1 / 34.1, fp16 2048 of 32, 1024 x 1024, 44.1 / 32.7, and fp32 308 of 15, 1045
+  // x 439, 33.0 / 28.7).
+  bool units = true;
+  for (int i = 0; i < parts; ++i) units = units && w.prob[i].piece >= 4 * (int)sizeof(T);
+  if (a.T <= (units ? 48 : 16) * a.L) {
     int64_t most_chunks = 0;
     for (int i = 0; i < parts; ++i) {
       const int64_t n = ceil_div(w.prob[i].cols, FMA_COLS);
