@@ -214,18 +214,19 @@ struct Raw4 {
 };
 // d += A B of a warp: sixteen rows of A (this lane's words of row lane / 4 in a, of the eighth
 // after it in a8) and eight columns of B (of column lane / 4 in b).  16-bit types: K = 16, two
-// words of two values; fp32: K = 8, two words, as three products of TF32 parts.
-__device__ __forceinline__ void few_mma(__nv_bfloat16, float (&d)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
+// words of two values; fp32: K = 8, two words, as three products of TF32 parts, the small ones
+// summed apart (e): the tensor core truncates its sums.
+__device__ __forceinline__ void few_mma(__nv_bfloat16, float (&d)[4], float (&)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
   ptx::mma_sync_bf16(d, a[0], a8[0], a[1], a8[1], b[0], b[1]);
 }
-__device__ __forceinline__ void few_mma(__half, float (&d)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
+__device__ __forceinline__ void few_mma(__half, float (&d)[4], float (&)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
   ptx::mma_sync_f16(d, a[0], a8[0], a[1], a8[1], b[0], b[1]);
 }
-__device__ __forceinline__ void few_mma(float, float (&d)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
+__device__ __forceinline__ void few_mma(float, float (&d)[4], float (&e)[4], const uint32_t* a, const uint32_t* a8, const uint32_t* b) {
   auto hi = [](uint32_t v) { return __float_as_uint(tc::tf32_hi(__uint_as_float(v))); };
   auto lo = [](uint32_t v) { return __float_as_uint(tc::tf32_lo(__uint_as_float(v))); };
-  ptx::mma_sync_tf32(d, lo(a[0]), lo(a8[0]), lo(a[1]), lo(a8[1]), hi(b[0]), hi(b[1]));
-  ptx::mma_sync_tf32(d, hi(a[0]), hi(a8[0]), hi(a[1]), hi(a8[1]), lo(b[0]), lo(b[1]));
+  ptx::mma_sync_tf32(e, lo(a[0]), lo(a8[0]), lo(a[1]), lo(a8[1]), hi(b[0]), hi(b[1]));
+  ptx::mma_sync_tf32(e, hi(a[0]), hi(a8[0]), hi(a[1]), hi(a8[1]), lo(b[0]), lo(b[1]));
   ptx::mma_sync_tf32(d, hi(a[0]), hi(a8[0]), hi(a[1]), hi(a8[1]), hi(b[0]), hi(b[1]));
 }
 
@@ -332,12 +333,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_const
     if (warp < g.blocks * g.parts) {
       const int block = warp % g.blocks, share = warp / g.blocks, j = block * 16 + row8;
       const T *wa = a + j * p.K, *wa8 = wa + 8 * p.K, *x = static_cast<const T*>(p.x) + rows[row8] * p.ld;
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       auto step = [&](const Raw8<T>& u, const Raw8<T>& u8, const Raw8<T>& v) {
         const uint32_t *aw = reinterpret_cast<const uint32_t*>(u.w), *aw8 = reinterpret_cast<const uint32_t*>(u8.w),
                        *bw = reinterpret_cast<const uint32_t*>(v.w);
 #pragma unroll
-        for (int i = 0; i < 2 * (int)sizeof(T); i += 2) few_mma(T(), d, aw + i, aw8 + i, bw + i);
+        for (int i = 0; i < 2 * (int)sizeof(T); i += 2) few_mma(T(), d, e, aw + i, aw8 + i, bw + i);
       };
       const int first = share * 32, len = (int)(k1 - k0), stride = g.parts * 32;
       int at = first;
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_const
         step(u, u8, v);
       }
       float* to = part + (share * FEW + quad * 2) * R + j;
-      to[0] = d[0], to[R] = d[1], to[8] = d[2], to[R + 8] = d[3];
+      to[0] = d[0] + e[0], to[R] = d[1] + e[1], to[8] = d[2] + e[2], to[R + 8] = d[3] + e[3];
     }
     const float scale = p.scale ? p.scale[t.l] : 1.0f;
     __syncthreads();
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_const
         start_b(n);
         any_b(n, live);
       }
-      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       int nb = warp * 16, j = 0;
 #pragma unroll 1
       while (nb < live) {
@@ -428,14 +429,15 @@ __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_const
           if (nb < live) {  // the whole warp
             const O* h = hs + row8 * h_pitch + j + quad * 4;
             const uint32_t* hw = reinterpret_cast<const uint32_t*>(h);
-            few_mma(T(), d, w[u].w, w8[u].w, hw);
-            if constexpr (sizeof(T) == 2) few_mma(T(), d, w[u].w, w8[u].w, reinterpret_cast<const uint32_t*>(h + FEW * h_pitch));
-            else few_mma(T(), d, w[u].w + 2, w8[u].w + 2, hw + 2);
+            few_mma(T(), d, e, w[u].w, w8[u].w, hw);
+            if constexpr (sizeof(T) == 2) few_mma(T(), d, e, w[u].w, w8[u].w, reinterpret_cast<const uint32_t*>(h + FEW * h_pitch));
+            else few_mma(T(), d, e, w[u].w + 2, w8[u].w + 2, hw + 2);
             j += 16;
             if (j == R) {
               float* to = outs + quad * 2 * FEW_PITCH + nb + row8;
-              to[0] = d[0], to[FEW_PITCH] = d[1], to[8] = d[2], to[FEW_PITCH + 8] = d[3];
+              to[0] = d[0] + e[0], to[FEW_PITCH] = d[1] + e[1], to[8] = d[2] + e[2], to[FEW_PITCH + 8] = d[3] + e[3];
               d[0] = d[1] = d[2] = d[3] = 0.0f;
+              e[0] = e[1] = e[2] = e[3] = 0.0f;
               j = 0;
               nb += kWarps * 16;
             }
@@ -486,8 +488,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_const
 // Beside fp16 b, h is two fp16 numbers instead, its row scaled by a power of two that
 // brings its largest value to 2^14 .. 2^15: to 2^-22 of that, whatever its size.
 // The planes of the operand that lies along the MMA's N follow one another there, so
-// that the tensor core reads a plane of the other operand once for all of them; the sums
-// over those planes are taken in fp32 afterwards.
+// that the tensor core reads a plane of the other operand once for all of them.  fp32: what
+// plane c of one and plane d of the other give goes to the sums of order c + d, so that the
+// largest are added to once for sixteen terms (the tensor core's sums are truncated; with all
+// orders in one sum gradients were off by 1.6e-6, now by 4.4e-7, 2047 rows of 4 adapters,
+// r 8, 1000 x 2048).  The orders are added in
+// fp32 afterwards, the second product takes them from the smallest on.
 constexpr int TILE = 128;            // rows of a tile: the MMA's M
 constexpr int KB = 64;               // values of K per stage: 128 bytes of a plane's row
 constexpr int XP = TILE * KB * 2;    // bytes of a plane of a stage's x
@@ -572,7 +578,7 @@ __device__ __forceinline__ void own_sums(uint8_t* sm, uint32_t tmem, int R, bool
     for (int i = 0; i < 16; ++i) v[i] = 0.0f;
     if (any) {
 #pragma unroll
-      for (int c = 0; c < P; ++c) {
+      for (int c = P - 1; c >= 0; --c) {
         uint32_t s[16];
         ptx::tmem_ld16(tmem + ((uint32_t)(row & ~31) << 16) + c * R + j, s);
         ptx::tmem_ld_wait();
@@ -858,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
               // (n0 is a multiple of 64; 64 rows of j and 64 k by 64 j both take 8 KB)
 #pragma unroll
               for (int ks = 0; ks < KB / 16; ++ks)
-                ptx::mma_f16(tmem + n0, ptx::smem_desc(xa + c * XP + ks * 32, 16, 1024, ptx::kSwizzle128B),
+                ptx::mma_f16(tmem + c * R + n0, ptx::smem_desc(xa + c * XP + ks * 32, 16, 1024, ptx::kSwizzle128B),
                              ptx::smem_desc(wa + n0 * 128 + ks * (p.turned ? 2048 : 32), KB * 128, 1024,
                                             ptx::kSwizzle128B),
                              id, b > b0 || c > 0 || ks > 0);
@@ -1368,15 +1374,16 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       if (ptx::elect_one()) {
         const uint32_t ha = ptx::smem_addr(hs + hb * g.h_bytes), wa = ptx::smem_addr(ws + slot * g.w_bytes);
         uint32_t more = 0;
-        for (int ks = 0; ks < R / 16; ++ks)
+#pragma unroll
+        for (int order = P == 3 ? 2 : PH - 1; order >= 0; --order)
 #pragma unroll
           for (int d = 0; d < P; ++d) {
-            const uint64_t wdesc =
-                g.turned ? ptx::smem_desc(wa + d * (R * 256) + ks * 2048, R * 128, 1024, ptx::kSwizzle128B)
-                         : along.desc(wa + d * plane, ks);
-#pragma unroll
-            for (int c = 0; c < PH; ++c) {
-              if (P == 3 && c + d > 2) continue;  // fp32: the smallest products are left out
+            const int c = order - d;
+            if (c < 0 || c >= PH) continue;
+            for (int ks = 0; ks < R / 16; ++ks) {
+              const uint64_t wdesc =
+                  g.turned ? ptx::smem_desc(wa + d * (R * 256) + ks * 2048, R * 128, 1024, ptx::kSwizzle128B)
+                           : along.desc(wa + d * plane, ks);
               ptx::mma_f16(tmem + buf * UP_N, along.desc(ha + c * plane, ks), wdesc, id, more);
               more = 1;
             }
@@ -1710,7 +1717,7 @@ __device__ __forceinline__ void grad_sums(uint8_t* sm, uint32_t tmem, int R, boo
     for (int i = 0; i < 16; ++i) v[i] = 0.0f;
     if (any) {
 #pragma unroll
-      for (int c = 0; c < PH; ++c) {
+      for (int c = PH - 1; c >= 0; --c) {
         uint32_t w[16];
         ptx::tmem_ld16(tmem + ((uint32_t)(col & ~31) << 16) + c * R + j, w);
         ptx::tmem_ld_wait();
@@ -1849,7 +1856,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
             const uint32_t id = ptx::idesc_f16(1, GRAD_COLS, nn, true, true);
 #pragma unroll
             for (int ks = 0; ks < GRAD_ROWS / 16; ++ks)
-              ptx::mma_f16(tmem + n0,
+              ptx::mma_f16(tmem + (P == 3 ? c * R : 0) + n0,
                            ptx::smem_desc(xa + c * XG + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B),
                            ptx::smem_desc(ha + n0 * 128 + ks * 2048, GRAD_ROWS * 128, 1024, ptx::kSwizzle128B), id,
                            b > b0 || c > 0 || ks > 0);
