@@ -170,3 +170,65 @@ def test_graph_replays_with_other_adapters():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(outs, eager))
         c.layout = layout
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,L,r,K,N", [(1500, 1, 4, 72, 56), (1200, 75, 16, 96, 133), (1100, 70, 24, 200, 64),
+                                       (2000, 130, 8, 64, 72), (256, 1, 32, 128, 96), (257, 1, 32, 128, 96),
+                                       (272, 17, 100, 80, 40), (273, 17, 100, 80, 40)])
+def test_around_the_rules_for_few_rows(T, L, r, K, N, dtype):
+    Case(T + L, T, L, r, K, N, dtype).check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,L,r,K,N,which", [(480, 10, 33, 100, 264, "one"), (480, 10, 16, 1028, 36, "mixed"),
+                                             (481, 10, 16, 1028, 36, "mixed"), (160, 10, 5, 77, 91, "runs"),
+                                             (161, 10, 5, 77, 91, "runs"), (40, 9, 128, 130, 8, "none"),
+                                             (900, 60, 18, 515, 258, "outside")])
+def test_gradients_of_adapters_with_few_rows(T, L, r, K, N, which, dtype):
+    """Around the rules for the gradients' form: 48 rows an adapter, 16 where rows are not aligned."""
+    c = Case(T, T, L, r, K, N, dtype, which=which)
+    for got, (want, tol) in zip(c.backward(), c.backward64()):
+        within(got, want, tol, dtype)
+    assert binding.check_device_error(None) == binding.IMC_OK
+
+
+def test_places_beyond_32_bits():
+    """More than 2^31 elements of x, of out and of the gradients, checked at both ends."""
+    T, wide, L, r, n = 270000, 8192, 3, 16, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def normal(*shape, size=1.0):
+        return (size * torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16))
+
+    which = torch.randint(-1, L, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    layout = binding.experts_layout(which, L)
+    some = torch.cat([torch.arange(40), torch.arange(T - 40, T)]).cuda()
+    l = which[some, 0]
+    big, small = normal(T, wide), normal(T, n)
+    wide_w, narrow_w = normal(L, r, wide, size=wide ** -0.5), normal(L, n, r, size=r ** -0.5)
+
+    def close(got, want):
+        # an output's rounding of 2^-9, and h's 2^-17 times the terms' sizes, some units beside it
+        off = (got.double() - want).abs().max().item()
+        assert off <= 2.0 ** -8 * want.abs().max().item(), off
+
+    def plain(x, a, b, base):
+        out = base[some].double()
+        for i in range(L):
+            mine = (l == i).double()[:, None]
+            out += mine * (x[some].double() @ a[i].double().t() @ b[i].double().t())
+        return out
+
+    close(binding.adapters_linear(big, wide_w, narrow_w, layout, small)[some], plain(big, wide_w, narrow_w, small))
+    up_a, up_b = normal(L, r, n, size=n ** -0.5), normal(L, wide, r, size=r ** -0.5)
+    close(binding.adapters_linear(small, up_a, up_b, layout, big)[some], plain(small, up_a, up_b, big))
+    gx, ga, gb = binding.adapters_linear_backward(big, small, up_a, up_b, layout, small)  # grad is wide
+    close(gx[some], plain(big, up_b.transpose(1, 2).contiguous(), up_a.transpose(1, 2).contiguous(), small))
+    rows = (which[:, 0] == 1).nonzero().flatten()
+    h = small[rows].float() @ up_a[1].float().t()
+    close(gb[1, -128:], big[rows, -128:].double().t() @ h.double())
+    gx, ga, gb = binding.adapters_linear_backward(small, big, wide_w, narrow_w, layout, big)  # x is wide
+    close(gx[some], plain(small, narrow_w.transpose(1, 2).contiguous(), wide_w.transpose(1, 2).contiguous(), big))
+    close(ga[1, :, -128:], (small[rows].double() @ narrow_w[1].double()).t() @ big[rows, -128:].double())
+    assert binding.check_device_error(None) == binding.IMC_OK
