@@ -624,6 +624,7 @@ __device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, const D
     for (int e = 0; e < 8; ++e) v[e] = ju * 8 + e < g.r ? v[e] * scale : 0.0f;
   };
   const bool scaled = sizeof(T) == 2 && Planes<T>::FD == 0 && p.h16;
+  float held[Planes<T>::FD == 0 ? 8 : 1];  // the first unit's, which is all that most threads have
   if (scaled) {
     for (int i = threadIdx.x; i < mine; i += THREADS) top[i] = 0;
     __syncthreads();
@@ -633,7 +634,10 @@ __device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, const D
       sums(rank * mine + row, i % (R >> 3), v);
       uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      for (int e = 0; e < 8; ++e) {
+        m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+        if (Planes<T>::FD == 0 && i == (int)threadIdx.x) held[Planes<T>::FD == 0 ? e : 0] = v[e];
+      }
       atomicMax(top + row, m);  // whatever the order
     }
     __syncthreads();
@@ -642,7 +646,12 @@ __device__ __forceinline__ void all_sums(uint8_t* sm, const DownArgs& g, const D
     const int row = rank * mine + i / (R >> 3), ju = i % (R >> 3);
     if (row >= t.rows) break;
     float v[8];
-    sums(row, ju, v);
+    if (Planes<T>::FD == 0 && scaled && i == (int)threadIdx.x) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = held[Planes<T>::FD == 0 ? e : 0];
+    } else {
+      sums(row, ju, v);
+    }
     if (scaled) {
       // 2^14 over the largest value's power of two; rows of zeros, and those with
       // infinities or NaN, as they are

@@ -297,3 +297,16 @@ def test_refused_by_the_torch_level():
     with pytest.raises(ValueError):
         binding.balance_loss_backward(c.grad_loss, c.logits, c.experts, counts, offsets=c.offsets,
                                       grad_weights=c.grad_weights.half())
+
+
+@pytest.mark.parametrize("T", [767, 768, 769, 770])
+def test_around_the_rule_for_many_tokens(T):
+    """One launch up to 768 tokens, chunks and a join beyond; sequences up to 1024 in chunks."""
+    assert (binding.moe_balance_workspace_bytes(T, 1, 40) > 0) == (T > 768)
+    Case(T, T, 40, 3, "softmax").check()
+
+
+@pytest.mark.parametrize("S", [1024, 1025])
+def test_around_the_rule_for_many_sequences(S):
+    assert (binding.moe_balance_workspace_bytes(2 * S, S, 24) > 0) == (S == 1024)
+    Case(S, 2 * S, 24, 2, "sigmoid", lengths=[0] + [1, 3] * (S // 2) + [2] * (S % 2)).check()
