@@ -1774,6 +1774,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * GRAD_COLS;
   const int l = blockIdx.y;
   int* wd = &g_watchdog_adapters;
+  if (col0 >= p.cols) return;  // the whole cluster (the problems may have different numbers of columns)
   if (ptx::smem_addr(sm) & 1023u) {  // (no room to align it: two blocks fill an SM)
     if (tid == 0) atomicCAS(wd, 0, 15);
     return;
@@ -1781,11 +1782,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   const uint32_t tmem = set_up(ctl, 5, ctl.empty, g.cols);
   ptx::griddep_wait();
   ptx::griddep_launch();
-  // (the problems may have different numbers of columns)
-  const bool work = col0 < p.cols;
   const int first = __ldg(g.offsets + l), rows = __ldg(g.offsets + l + 1) - first;
   const int blocks = (rows + GRAD_ROWS - 1) / GRAD_ROWS, per = (blocks + C - 1) >> g.log_ctas;
-  const int b0 = min(rank * per, blocks), b1 = work ? min(b0 + per, blocks) : b0;
+  const int b0 = min(rank * per, blocks), b1 = min(b0 + per, blocks);
   constexpr int XG = GRAD_ROWS * GRAD_COLS * 2;  // bytes of a plane of a stage's x
   const int stage_bytes = P * XG + grad_h_bytes(PH * R);
   const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
@@ -1895,9 +1894,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     ptx::tc_fence_after();
   }
   __syncthreads();
-  if (work) grad_sums<PH>(sm, tmem, R, b1 > b0, warp >> 2, kWarps / 4);
+  grad_sums<PH>(sm, tmem, R, b1 > b0, warp >> 2, kWarps / 4);
   ptx::cluster_sync();
-  if (work) grad_out<T, kThreads>(sm, g, p, l, rank, col0);
+  grad_out<T, kThreads>(sm, g, p, l, rank, col0);
   ptx::cluster_sync_reads();  // no CTA ends while another reads its sums
   tear_down(ctl, tmem, g.cols);
 }
@@ -2033,15 +2032,11 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
   const int64_t col0 = (int64_t)(blockIdx.x >> g.log_ctas) * GRAD_COLS;
   const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
   int* wd = &g_watchdog_adapters;
+  if (left <= 0) return;  // the whole cluster (the problems may have different numbers of columns)
   const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 5, ctl.full, g.cols, DOWN_STAGES, GRAD_LOAD);
   if (tid == 32) {
     ptx::tma_prefetch_desc(&maps.x[blockIdx.y]);
     ptx::tma_prefetch_desc(&maps.h[blockIdx.y]);
-  }
-  if (left <= 0) {  // the whole cluster (the problems may have different numbers of columns)
-    ptx::griddep_wait();
-    tear_down(ctl, tmem, g.cols);
-    return;
   }
   ptx::griddep_wait();
   ptx::griddep_launch();
