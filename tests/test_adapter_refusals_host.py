@@ -18,8 +18,8 @@ def lib():
     return binding.load()
 
 
-def lowrank(x=P[0], dtype=0, ld=64, a=P[1], b=P[2], scale=P[3], layout=P[4], base=P[5], out=P[6], T=900, L=3, r=8,
-            K=64, N=32, ws=P[7], nbytes=1 << 20):
+def lowrank(x=P[0], dtype=0, ld=64, a=P[1], b=P[2], scale=P[3], layout=P[4], base=P[5], out=P[6], T=9000, L=3, r=8,
+            K=64, N=32, ws=P[7], nbytes=1 << 22):
     return binding.lowrank_linear(x, dtype, ld, a, b, scale, layout, base, out, T, L, r, K, N, ws, nbytes, None)
 
 
