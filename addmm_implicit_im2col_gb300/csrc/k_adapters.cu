@@ -1193,7 +1193,7 @@ constexpr int STAGED_COLS = 16;
 //               place, rounds once, and has TMA store it (row by row itself where the box
 //               would reach other rows).  Form TMA: rows aligned to 16 bytes; the other
 //               copies by 8 or 4 bytes (16-bit rows at odd elements: by the words that hold
-//               them), or, with no room for parts of base (fp32, high ranks), adds column by
+//               them), or, with no room for parts of base (fp32, ranks above 32), adds column by
 //               column through shared memory
 //   then        one warp (fp32: four, which cut w into its planes) that loads h of a tile
 //               and w of an item, and one for tensor memory and the MMAs (two accumulators
@@ -2479,7 +2479,7 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   g.piece = piece_of(g.out, g.N * b | (int64_t)(reinterpret_cast<uintptr_t>(g.base) & 15));
   g.w_piece = piece_of(g.w, (g.turned ? g.N : g.r) * b);
   g.vec = g.w_piece == 16 && PL::PD == 1 ? 1 : 0;
-  // TMA: two parts of base have to fit beside h and w (fp32: not at ranks above 64 or so)
+  // TMA: two parts of base have to fit beside h and w (fp32: up to rank 32)
   const bool fits = 2 * UP_EPI * UP_PART<T, true> + g.h_bytes + g.w_bytes <= 232448 - (int)sizeof(UpCtl) - 256 - 1024;
   return g.piece == 16 && fits ? run_up_as<T, true>(g, h, s) : run_up_as<T, false>(g, h, s);
 }

@@ -395,16 +395,28 @@ int64_t chunk_of(int64_t T) {
   while (ceil_div(T, chunk) > 512) chunk *= 2;
   return chunk;
 }
-// The form in chunks takes two launches (us, one sequence of 64 experts, with it / without:
-// 512 tokens 8.7 / 6.6, 2048 9.0 / 16.8).
-bool many(int64_t T, int64_t S) { return T > 768 && S <= 1024; }
+// The form in chunks takes two launches, and a row of sums for each chunk and sequence (us with
+// it / without: 512 tokens of 64 experts 6.2 / 5.8, 768 6.1 / 7.5, 2048 6.1 / 15.9; 4096 in 64
+// sequences 9.8 / 5.7, 16384 in 256 15.1 / 12.4, in 64, 256 experts, 19.6 / 23.2, in 8 17.2 / 46.8).
+bool many(int64_t T, int64_t S) { return T > 640 && T > 64 * S && S <= 1024; }
+// CTAs of a sequence's cluster, as log2, without chunks: by its tokens on average (64 are one
+// for each warp of eight CTAs), and as many as leave two CTAs an SM (us with 1 / 2 / 4 / 8:
+// 600 tokens in 100 sequences 4.6 / 4.0 / 3.7 / 5.3, in 40 5.5 / 4.2 / 3.5 / 3.9, in 20 8.1 / 5.8 /
+// 4.1 / 3.6, in 10 10.6 / 6.5 / 4.8 / 5.0).
+int few_log(int64_t T, int64_t S) {
+  int log = T >= 64 * S ? 3 : (T >= 32 * S ? 2 : (T >= 16 * S ? 1 : 0));
+  while (log < 3 && S << (log + 1) <= 2 * device_sm_count()) ++log;
+  return log;
+}
+// CTAs that join a sequence's chunks (us with 1 / 4 / 8: 16384 tokens in 64 sequences 19.2 / 16.9 /
+// 22.5, in 8 23.9 / 16.3 / 17.2; 8191 in one, 128 experts, with the gradient, 23.3 / 12.0 / 10.1).
+int join_log(int64_t chunks, int64_t S) { return chunks >= 128 * S ? 3 : (chunks >= 8 * S ? 2 : 0); }
 
 template <int VPT, typename T>
 cudaError_t forward(const BalanceArgs& a, cudaStream_t s) {
   const size_t E = (size_t)a.E;
   if (!many(a.T, a.S)) {
-    const int64_t mean = a.T / a.S;  // tokens of a sequence
-    const int log_ctas = mean >= 64 ? 3 : (mean >= 32 ? 2 : (mean >= 16 ? 1 : 0)), C = 1 << log_ctas;
+    const int log_ctas = few_log(a.T, a.S), C = 1 << log_ctas;
     return launch_clusters<k_balance<VPT, T>>(dim3((unsigned)a.S << log_ctas), C, kThreads,
                                               E * (kWarps + C) * 8 + E * (1 + C) * 4, s, a, log_ctas);
   }
@@ -412,7 +424,7 @@ cudaError_t forward(const BalanceArgs& a, cudaStream_t s) {
   const cudaError_t e =
       launch_clusters<k_balance_chunks<VPT, T>>(dim3(chunks), 1, kThreads, E * (kWarps * 8 + 4), s, a, chunk);
   if (e != cudaSuccess) return e;
-  const int log_ctas = chunks / a.S >= 16 ? 3 : 0, C = 1 << log_ctas;
+  const int log_ctas = join_log(chunks, a.S), C = 1 << log_ctas;
   return launch_clusters<k_balance_join>(dim3((unsigned)a.S << log_ctas), C, kJoin, E * (1 + C) * 12, s, a, chunk,
                                          chunks, log_ctas);
 }

@@ -299,14 +299,15 @@ def test_refused_by_the_torch_level():
                                       grad_weights=c.grad_weights.half())
 
 
-@pytest.mark.parametrize("T", [767, 768, 769, 770])
+@pytest.mark.parametrize("T", [639, 640, 641, 642])
 def test_around_the_rule_for_many_tokens(T):
-    """One launch up to 768 tokens, chunks and a join beyond; sequences up to 1024 in chunks."""
-    assert (binding.moe_balance_workspace_bytes(T, 1, 40) > 0) == (T > 768)
+    """One launch up to 640 tokens, chunks and a join beyond."""
+    assert (binding.moe_balance_workspace_bytes(T, 1, 40) > 0) == (T > 640)
     Case(T, T, 40, 3, "softmax").check()
 
 
-@pytest.mark.parametrize("S", [1024, 1025])
-def test_around_the_rule_for_many_sequences(S):
-    assert (binding.moe_balance_workspace_bytes(2 * S, S, 24) > 0) == (S == 1024)
-    Case(S, 2 * S, 24, 2, "sigmoid", lengths=[0] + [1, 3] * (S // 2) + [2] * (S % 2)).check()
+@pytest.mark.parametrize("S,T", [(15, 960), (15, 961), (40, 2561), (1025, 2050), (400, 401)])
+def test_around_the_rule_for_many_sequences(S, T):
+    """Chunks where a sequence has more than 64 tokens on average; one of them has most here."""
+    assert (binding.moe_balance_workspace_bytes(T, S, 24) > 0) == (T in (961, 2561))
+    Case(S, T, 24, 2, "sigmoid", lengths=[0] + [1] * (S - 1) + [T - S + 1]).check()
