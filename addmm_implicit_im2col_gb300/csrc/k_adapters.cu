@@ -1108,6 +1108,7 @@ struct UpArgs {
   int group;                              // items that a block takes at once
   int jump, jump_tiles, jump_steps;       // from the last of them to its next: items, the same as tiles and steps
   int slots, h_slots, b_slots, w_bytes, h_bytes;  // of the rings of w, h and base; bytes of one
+  int buckets;                                    // where the table of the buckets is
 };
 struct UpMaps {
   CUtensorMap base, out;  // by 32 rows, 128 bytes of columns
@@ -1126,7 +1127,6 @@ struct UpCtl {
   uint32_t tmem_base;
   int abort;
   int sums[16];
-  int before[kAdapters + 2], first[kAdapters + 2];  // tiles before a bucket, its first row
 };
 
 // A block's items, each 128 outputs (`step`) of a tile's rows: runs of `group` items, the
@@ -1155,16 +1155,22 @@ struct Walk {
   }
 };
 
+// Tiles before each bucket, and its first row: in shared memory behind the rings.
+struct Buckets {
+  int *before, *first;
+  __device__ __forceinline__ Buckets(uint8_t* at, int L) : before(reinterpret_cast<int*>(at)), first(before + L + 2) {}
+};
+constexpr int buckets_bytes(int L) { return (L + 2) * 8; }
 // Tile t of the counted buckets.
-__device__ __forceinline__ RowTile tile_of(const UpCtl& ctl, int B, int t) {
+__device__ __forceinline__ RowTile tile_of(const Buckets& in, int B, int t) {
   int low = 0, high = B;  // before[low] <= t < before[high]
   while (high - low > 1) {
     const int mid = (low + high) >> 1;
-    if (ctl.before[mid] <= t) low = mid;
+    if (in.before[mid] <= t) low = mid;
     else high = mid;
   }
-  const int p0 = ctl.first[low] + (t - ctl.before[low]) * TILE;
-  return {low, p0, min(TILE, ctl.first[low + 1] - p0)};
+  const int p0 = in.first[low] + (t - in.before[low]) * TILE;
+  return {low, p0, min(TILE, in.first[low + 1] - p0)};
 }
 
 // Two values of base and of the product (fp16: times its row's scale).
@@ -1193,7 +1199,7 @@ constexpr int STAGED_COLS = 16;
 //               place, rounds once, and has TMA store it (row by row itself where the box
 //               would reach other rows).  Form TMA: rows aligned to 16 bytes; the other
 //               copies by 8 or 4 bytes (16-bit rows at odd elements: by the words that hold
-//               them), or, with no room for parts of base (fp32, ranks above 32), adds column by
+//               them), or, with no room for parts of base (fp32, ranks above 64), adds column by
 //               column through shared memory
 //   then        one warp (fp32: four, which cut w into its planes) that loads h of a tile
 //               and w of an item, and one for tensor memory and the MMAs (two accumulators
@@ -1240,13 +1246,14 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
   const T* base = static_cast<const T*>(g.base);
   T* out = static_cast<T*>(g.out);
   const int B = g.L + (g.base != g.out ? 1 : 0);  // rows without an adapter: copied, or left
-  count_tiles<THREADS>(g.offsets, B, TILE, ctl.first, ctl.before, ctl.sums);
+  const Buckets buckets(sm + g.buckets, g.L);
+  count_tiles<THREADS>(g.offsets, B, TILE, buckets.first, buckets.before, ctl.sums);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   ptx::griddep_launch();
-  const Walk walk(g, (uint32_t)ctl.before[B] * (uint32_t)g.steps);
+  const Walk walk(g, (uint32_t)buckets.before[B] * (uint32_t)g.steps);
   constexpr int SB = UP_PART<T, TMA>;
   uint8_t* ws = sm + UP_EPI * g.b_slots * SB;
   uint8_t* hs = ws + g.slots * g.w_bytes;
@@ -1265,7 +1272,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     for (Walk item = walk; item.more(); item.next(g)) {
       const int64_t n0 = (int64_t)item.step * UP_N;
       const bool other = item.tile != last;
-      if (other) t = tile_of(ctl, B, item.tile);
+      if (other) t = tile_of(buckets, B, item.tile);
       last = item.tile;
       if (t.l == g.L) continue;
       if (other) {
@@ -1365,7 +1372,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     const uint32_t id = ptx::idesc_f16(PL::FD, TILE, UP_N, false, g.turned);
     for (Walk item = walk; item.more();) {
       const bool other = item.tile != last;
-      if (other) product = tile_of(ctl, B, item.tile).l < g.L;
+      if (other) product = tile_of(buckets, B, item.tile).l < g.L;
       last = item.tile;
       item.next(g);
       if (!product) continue;
@@ -1419,7 +1426,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       q.col = (int64_t)item.step * UP_N + half * 64;
       if (item.tile == q.tile) return;
       q.tile = item.tile;
-      const RowTile t = tile_of(ctl, B, item.tile);
+      const RowTile t = tile_of(buckets, B, item.tile);
       q.l = t.l;
       q.rows = t.rows - q4 * 32 < 0 ? 0 : min(32, t.rows - q4 * 32);  // of this warp
       if (q.rows == 0) return;
@@ -2419,7 +2426,7 @@ cudaError_t run_up_as(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   const Along along(g.R);
   constexpr int part = UP_EPI * UP_PART<T, TMA>, staged = UP_EPI * 32 * (STAGED_COLS + 1) * 4;
   // rings: at least two parts of base, one h, one w; then more parts, w, h
-  const int most = 232448 - (int)sizeof(UpCtl) - 256 - 1024;
+  const int table = buckets_bytes(g.L), most = 232448 - (int)sizeof(UpCtl) - 256 - 1024 - table;
   const bool ring = 2 * part + g.h_bytes + g.w_bytes <= most;
   g.slots = g.h_slots = 1;
   g.b_slots = ring ? 2 : 0;
@@ -2427,7 +2434,7 @@ cudaError_t run_up_as(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   // two blocks on an SM where both find room with two slots for w
   int limit = most, blocks = 1;
   if (sizeof(T) == 2) {
-    const int half = (228 << 9) - 1024 - (int)sizeof(UpCtl) - 256 - 1024;
+    const int half = (228 << 9) - 1024 - (int)sizeof(UpCtl) - 256 - 1024 - table;
     g.slots = 2;
     if (bytes() <= half) {
       limit = half;
@@ -2448,6 +2455,7 @@ cudaError_t run_up_as(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   if (ring) grow(g.b_slots, BASE_SLOTS);
   grow(g.h_slots, 2);
   grow(g.slots, UP_SLOTS);
+  g.buckets = bytes();
   UpMaps maps = {};
   bool ok = encode_h(&maps.h, h, g.T, g.R, PL::PH);
   if (TMA && g.base) ok = ok && encode<T>(&maps.base, g.base, g.N, g.T, g.N, 32);
@@ -2464,7 +2472,7 @@ cudaError_t run_up_as(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   g.jump = (grid - 1) * g.group + 1;
   g.jump_tiles = g.jump / g.steps;
   g.jump_steps = g.jump % g.steps;
-  return launch_clusters<k_adapters_up<T, TMA>>(dim3(grid), 1, UP_THREADS<T>, (size_t)bytes() + 1024, s, maps, g);
+  return launch_clusters<k_adapters_up<T, TMA>>(dim3(grid), 1, UP_THREADS<T>, (size_t)bytes() + table + 1024, s, maps, g);
 }
 
 template <typename T>
@@ -2479,8 +2487,9 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   g.piece = piece_of(g.out, g.N * b | (int64_t)(reinterpret_cast<uintptr_t>(g.base) & 15));
   g.w_piece = piece_of(g.w, (g.turned ? g.N : g.r) * b);
   g.vec = g.w_piece == 16 && PL::PD == 1 ? 1 : 0;
-  // TMA: two parts of base have to fit beside h and w (fp32: up to rank 32)
-  const bool fits = 2 * UP_EPI * UP_PART<T, true> + g.h_bytes + g.w_bytes <= 232448 - (int)sizeof(UpCtl) - 256 - 1024;
+  // TMA: two parts of base have to fit beside h and w (fp32: up to rank 64, and 160 adapters)
+  const bool fits = 2 * UP_EPI * UP_PART<T, true> + g.h_bytes + g.w_bytes <=
+                    232448 - (int)sizeof(UpCtl) - 256 - 1024 - buckets_bytes(g.L);
   return g.piece == 16 && fits ? run_up_as<T, true>(g, h, s) : run_up_as<T, false>(g, h, s);
 }
 

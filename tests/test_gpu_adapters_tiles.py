@@ -232,3 +232,10 @@ def test_places_beyond_32_bits():
     close(gx[some], plain(small, narrow_w.transpose(1, 2).contiguous(), wide_w.transpose(1, 2).contiguous(), big))
     close(ga[1, :, -128:], (small[rows].double() @ narrow_w[1].double()).t() @ big[rows, -128:].double())
     assert binding.check_device_error(None) == binding.IMC_OK
+
+
+@pytest.mark.parametrize("L", [4, 40, 180])
+@pytest.mark.parametrize("r", [33, 64, 65, 128])
+def test_high_ranks_in_fp32(r, L):
+    """Ranks whose operands leave two parts of base their room, or none; with and without a long table of adapters."""
+    Case(r + L, 16 * L + 300, L, r, 72, 264, torch.float32, which="runs" if L == 4 else "mixed").check()
