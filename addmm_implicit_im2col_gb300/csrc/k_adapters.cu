@@ -236,8 +236,9 @@ struct FewArgs {
   int R, blocks, parts;     // r rounded up to 16; blocks of 16 of it; warps that share one
 };
 
+// (fp32 with three blocks an SM spills registers: 512 rows of 4 adapters, r 16, 1024 x 1024, 11.4 us for 8.5)
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) k_adapters_few(const __grid_constant__ FewArgs g) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) k_adapters_few(const __grid_constant__ FewArgs g) {
   extern __shared__ uint8_t sm_raw[];
   __shared__ int order[FEW_ROWS], rows[FEW];
   __shared__ float row_scale[FEW];
@@ -2299,7 +2300,8 @@ cudaError_t adapters_few(const AdapterArgs& a, cudaStream_t s) {
   g.a = a;
   // Eight CTAs a tile; four where those are more than 3.5 an SM (us with 8 / 4, bf16, r 16, 4096 x
   // 4096: 64 rows of 64 adapters 9.5 / 11.7, 512 rows of 8 22.2 / 19.0, 1000 rows of 64 34.0 / 31.8).
-  g.log_ctas = tiles * 16 <= 7 * device_sm_count() ? 3 : 2;
+  // fp32, two CTAs an SM: four where eight do not run at once (64 rows of 64, 4096 x 1024: 13.2 / 8.7).
+  g.log_ctas = tiles * 16 <= (sizeof(T) == 4 ? 4 : 7) * device_sm_count() ? 3 : 2;
   g.none = a.base != a.out ? 1 : 0;
   g.vec = (aligned16(a.x, a.ld * b) ? 1 : 0) | (aligned16(a.a, a.K * b) ? 2 : 0) |
           (a.r % 4 == 0 && reinterpret_cast<uintptr_t>(a.b) % (4 * b) == 0 ? 4 : 0);

@@ -147,9 +147,6 @@ __device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_bar) {
 
 // Makes generic-proxy writes to shared memory visible to the async proxy
 // (tensor core reads of operands written by ordinary st.shared).
-__device__ __forceinline__ void fence_proxy_async() {  // any shared memory of the cluster
-  asm volatile("fence.proxy.async;" ::: "memory");
-}
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
