@@ -33,6 +33,19 @@ std::mutex g_dev_mu;
 int g_sm_count[kMaxDevices];
 int g_dev_ok[kMaxDevices];  // 0 unknown, 1 sm_103, -1 other
 
+// A host thread has no current context before a runtime call that needs one, and encoding a
+// tensor map, which goes past the runtime, fails without.  Asking for a limit binds the
+// device's primary context where none is current, and leaves any other as it is; it is no
+// work on a stream, so it may fall within a capture.
+cudaError_t bind_context() {
+  static thread_local bool bound = false;
+  if (bound) return cudaSuccess;
+  size_t limit;
+  const cudaError_t e = cudaDeviceGetLimit(&limit, cudaLimitStackSize);
+  bound = e == cudaSuccess;
+  return e;
+}
+
 // IMC_OK when the current device is compute capability 10.3.
 int check_device() {
   int dev = -1;
@@ -53,7 +66,8 @@ int check_device() {
     g_sm_count[dev] = sms;
     g_dev_ok[dev] = (major == 10 && minor == 3) ? 1 : -1;
   }
-  return g_dev_ok[dev] == 1 ? IMC_OK : IMC_ERR_DEVICE;
+  if (g_dev_ok[dev] != 1) return IMC_ERR_DEVICE;
+  return bind_context() == cudaSuccess ? IMC_OK : IMC_ERR_CUDA;
 }
 
 bool overlaps(const void* a, uint64_t abytes, const void* b, uint64_t bbytes) {
