@@ -11,19 +11,26 @@ namespace mx {
 
 constexpr int kMaxRank = 128;
 
+constexpr int kBlockSharedMemory = 232448;  // bytes that a block may take, static ones included
+
 // Launches Kernel in clusters of `ctas` blocks (1: none) as the programmatic dependent of
 // the stream's previous kernel.  What the kernel may take of shared memory is set once per
-// device and size (0.5 us a call).
+// device (0.5 us a call), to the most there is: the same value whichever call comes first, so
+// that host threads may make first calls of different sizes at once.
 template <auto Kernel, typename... Args>
 cudaError_t launch_clusters(dim3 grid, int ctas, int threads, size_t smem, cudaStream_t s, Args... args) {
-  static std::atomic<int> set[64];
+  static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || set[dev].load(std::memory_order_acquire) < (int)smem) {
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    cudaFuncAttributes own;
+    e = cudaFuncGetAttributes(&own, Kernel);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kBlockSharedMemory - (int)own.sharedSizeBytes);
     if (e != cudaSuccess) return e;
-    if (dev < 64) set[dev].store((int)smem, std::memory_order_release);
+    if (dev < 64) ready[dev].store(true, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
