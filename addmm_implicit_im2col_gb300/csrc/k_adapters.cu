@@ -2018,9 +2018,10 @@ __global__ void __launch_bounds__(FMA_THREADS) k_adapters_grad_fma(const __grid_
 struct GradMaps {
   CUtensorMap x[2], h[2];  // of each problem, by 64 rows
 };
-constexpr int GRAD_LOAD = 4, GRAD_THREADS = (GRAD_LOAD + 1 + 4) * 32;  // loaders, MMAs, epilogue
+constexpr int GRAD_LOAD = 4, GRAD_EPI = 4, GRAD_THREADS = (GRAD_LOAD + 1 + GRAD_EPI) * 32;  // loaders, MMAs, epilogue
 struct GradCtl {
-  uint64_t full[DOWN_STAGES], empty[DOWN_STAGES], accf[2], acce[2], drain;
+  // (full and acce take an arrival of each of four warps, the others one)
+  uint64_t full[DOWN_STAGES], acce[2], empty[DOWN_STAGES], accf[2], drain;
   uint32_t tmem_base;
   int abort;
   int sums[16];
@@ -2041,7 +2042,8 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
   const int left = (int)(p.cols - col0 < GRAD_COLS ? p.cols - col0 : GRAD_COLS);
   int* wd = &g_watchdog_adapters;
   if (left <= 0) return;  // the whole cluster (the problems may have different numbers of columns)
-  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 5, ctl.full, g.cols, DOWN_STAGES, GRAD_LOAD);
+  static_assert(GRAD_LOAD == GRAD_EPI, "arrivals");
+  const uint32_t tmem = set_up(ctl, 2 * DOWN_STAGES + 5, ctl.full, g.cols, DOWN_STAGES + 2, GRAD_LOAD);
   if (tid == 32) {
     ptx::tma_prefetch_desc(&maps.x[blockIdx.y]);
     ptx::tma_prefetch_desc(&maps.h[blockIdx.y]);
@@ -2214,9 +2216,11 @@ __global__ void __launch_bounds__(GRAD_THREADS) k_adapters_grad_runs(const __gri
           }
         }
       }
+      // Each warp arrives for itself: one may leave this loop (its wait gave up) while another
+      // goes on, so nothing here may wait for all of them.
       ptx::tc_fence_before();
-      tc::epi_sync();  // (the barrier counts one arrival)
-      if (warp == GRAD_LOAD + 1 && lane == 0) ptx::mbar_arrive(&ctl.acce[acc.i]);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ctl.acce[acc.i]);
       acc.next(2);
       b = end;
     }
