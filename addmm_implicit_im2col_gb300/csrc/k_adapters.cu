@@ -533,7 +533,8 @@ __device__ __forceinline__ void planes_of(const Raw8<T>& raw, uint4 (&out)[Q]) {
   }
 }
 // An asynchronous copy of the first n (whole pieces) of eight 16-bit values of a row that is
-// aligned to `piece` bytes; zeros for the others.  (`any`: some address.)
+// aligned to `piece` bytes; zeros for the others.  (`any`: some address as aligned as that; a copy
+// asks for it even where it reads nothing.)
 template <typename T>
 __device__ __forceinline__ void copy_unit(uint8_t* to, const T* from, int n, int piece, const void* any) {
   if (piece == 16) {
@@ -1335,7 +1336,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
         if (P == 1 && g.w_piece >= 4) {  // all of it under way at once
           for (int i = lt; i < TILE / 8 * R; i += LT) {
             unit(i, from, have, at);
-            copy_unit(at, from, have, g.w_piece, g.order);
+            copy_unit(at, from, have, g.w_piece, w);
           }
           ptx::copy_commit();
           ptx::copy_wait<0>();
