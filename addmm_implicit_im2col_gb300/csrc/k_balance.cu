@@ -71,6 +71,19 @@ __device__ __forceinline__ float sigmoid(float x, float& rest) {
   return x < 0.0f ? low : inv;
 }
 
+// Sigmoids that sum to less than this are e^x to fp32's precision each, and divided by their sum
+// the softmax, which is what such a token's scores are made by: the sigmoids lose bits below
+// 2^-126, and a sum below 2^-128 has no reciprocal in fp32.  (A row of -inf alone: zeros.)
+constexpr float kSmallSum = 0x1p-100f;
+
+// The logits of one token, -inf where there is no expert: lane l has experts l, l + 32, ...
+template <int VPT, typename T>
+__device__ __forceinline__ void load_logits(const T* row, int E, float (&v)[VPT]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) v[j] = lane + 32 * j < E ? to_f32<T>(row[lane + 32 * j]) : -INFINITY;
+}
+
 // The tokens first, first + step, ... before `last`, two of them at a time (their loads and
 // sums overlap): their scores are added to mine [E], their slots counted in count [E].  A
 // lane sums its experts' scores of kFlush tokens in fp32 before: an error of a few fp32
@@ -110,9 +123,15 @@ __device__ __forceinline__ void add_tokens(const BalanceArgs& a, int64_t first, 
 #pragma unroll
         for (int j = 0; j < VPT; ++j) sum += v[u][j] = sigmoid(v[u][j], rest);
         sum = warp_sum(sum);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t t = t0 + u * step;
+        if (sum < kSmallSum && t < last) {  // the whole warp
+          load_logits<VPT>(static_cast<const T*>(a.logits) + t * a.ld, E, v[u]);
+          scores_of<VPT>(0, v[u]);
+        } else {
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // (0: no token)
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) v[u][j] *= inv;
+          for (int j = 0; j < VPT; ++j) v[u][j] *= inv;
+        }
       } else {
         scores_of<VPT>(0, v[u]);
       }
@@ -311,8 +330,7 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
   // rest: the derivative of a score with respect to its logit without the softmax's sum
   float s[VPT], u[VPT], rest[VPT];
   const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) s[j] = lane + 32 * j < E ? to_f32<T>(row[lane + 32 * j]) : -INFINITY;
+  load_logits<VPT>(row, E, s);
   const int q = a.offsets ? sequence_of(a.offsets, a.S, t) : 0;
   float coef = 0.0f;
   if (q >= 0 && q < a.S) {
@@ -345,7 +363,23 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
   float inv = 1.0f;
   if (a.sigmoid) {
     sum = warp_sum(sum);
-    inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (sum < kSmallSum) {  // the whole warp
+      // (the weights, of the sigmoids themselves: sum times the scores used here, or their
+      // quotients; where the sigmoids are 0 in fp32, the weights are 0, too)
+      if (sum == 0.0f) id = -1;
+      if (!a.renorm) gi *= sum;
+      load_logits<VPT>(row, E, s);
+      scores_of<VPT>(0, s);
+      dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        rest[j] = s[j];
+        dot += u[j] * s[j];
+      }
+      dot = warp_sum(dot);
+    } else {
+      inv = 1.0f / sum;
+    }
   }
   dot *= inv;
 #pragma unroll

@@ -525,7 +525,7 @@ int moe_combine_backward(const void* grad, const void* y, int dtype, const float
  * nearer end; NULL: one sequence of all T tokens, S = 1).  counts[s,e] is the
  * number of its slots whose expert is e (slots of no expert in [0, E) are not
  * counted), p[t] the softmax of the logits, or their sigmoids divided by their
- * sum (0 where that is 0):
+ * sum, also where fp32 holds neither (0 for a row of -inf alone):
  *
  *   loss[s] = E / (k * n^2) * sum_e counts[s,e] * sum_t p[t,e]     (0 for n = 0)
  *
@@ -546,8 +546,9 @@ int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t row
 /* grad_logits [T,E] (contiguous, of type dtype): gradient of sum_s grad_loss[s] *
  * loss[s], the counts taken as constant; 0 for tokens in no sequence.
  * grad_weights [T,k] (may be NULL): the gradient of moe_route's weights with this
- * renormalize and scale, as moe_route_backward gives it, is added before the one
- * rounding to dtype.  experts may be NULL without grad_weights. */
+ * renormalize and scale, as moe_route_backward gives it (0 where all sigmoids are 0
+ * in fp32, and with them the weights), is added before the one rounding to dtype.
+ * experts may be NULL without grad_weights. */
 int moe_balance_backward(const float* grad_loss, const void* logits, int dtype, int64_t T,
                          int64_t E, int64_t row_stride, const int32_t* experts, int64_t k,
                          int score, const int32_t* counts, const int32_t* offsets, int64_t S,
