@@ -332,12 +332,16 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
   const T* row = static_cast<const T*>(a.logits) + t * a.ld;
   load_logits<VPT>(row, E, s);
   const int q = a.offsets ? sequence_of(a.offsets, a.S, t) : 0;
+  T* grad = static_cast<T*>(a.grad) + t * E;
   float coef = 0.0f;
   if (q >= 0 && q < a.S) {
     const int64_t t0 = a.offsets ? clamped(a.offsets[q], a.T) : 0;
     const int64_t t1 = a.offsets ? clamped(a.offsets[q + 1], a.T) : a.T;
     const float n = (float)(t1 - t0);
     coef = a.grad_loss[q] * ((float)E / ((float)a.k * n) / n);
+  } else if (!a.grad_weights) {  // padding, whose logits may be anything
+    for (int e = lane; e < E; e += 32) grad[e] = from_f32<T>(0.0f);
+    return;
   }
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -413,7 +417,6 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) u[j] = mine[lane + 32 * j];
   }
-  T* grad = static_cast<T*>(a.grad) + t * E;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int e = lane + 32 * j;
