@@ -397,7 +397,18 @@ __global__ void __launch_bounds__(128) k_balance_backward(const BalanceArgs a) {
     const float si = id >= 0 ? mine[id] : 0.0f;
     const float total = warp_sum(si), along = warp_sum(si * gi);
     float di = id >= 0 ? gi : 0.0f;
-    if (a.renorm) di = total == 0.0f || id < 0 ? 0.0f : (gi - along / total) / total;
+    if (a.renorm) {
+      if (total < kSmallChosen && total > 0.0f) {  // the whole warp
+        di = id < 0 ? 0.0f : (gi - along / total) / (total * 0x1p64f);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          u[j] *= 0x1p-64f;
+          rest[j] *= 0x1p64f;
+        }
+      } else {
+        di = total == 0.0f || id < 0 ? 0.0f : (gi - along / total) / total;
+      }
+    }
     di *= a.scale;
     const float inner = a.sigmoid ? 0.0f : warp_sum(di * si);
     __syncwarp();

@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     if (lane == i) si = p;
   }
   float di = id >= 0 ? gi : 0.0f;
-  if (a.renorm) di = total == 0.0f || id < 0 ? 0.0f : (gi - dot / total) / total;
+  const bool small = a.renorm && total < kSmallChosen;  // the whole warp
+  if (a.renorm) di = total == 0.0f || id < 0 ? 0.0f : (gi - dot / total) / (small ? total * 0x1p64f : total);
   di *= a.scale;
   const float inner = a.sigmoid ? 0.0f : warp_sum(di * si);
   float d[VPT];
@@ -190,6 +191,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
       if (e == lane + 32 * j) d[j] += v;
+  }
+  if (small) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int e = lane + 32 * j;
+      if (e < a.E)
+        grad[t * a.E + e] = from_f32<T>((a.sigmoid ? d[j] * s[j] * (1.0f - s[j]) : s[j] * (d[j] - inner)) * 0x1p64f);
+    }
+    return;
   }
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {

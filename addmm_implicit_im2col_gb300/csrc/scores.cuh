@@ -55,6 +55,11 @@ __device__ __forceinline__ void scores(const T* row, int E, int sigmoid, float (
   scores_of<VPT>(sigmoid, s);
 }
 
+// The chosen experts' scores may be far below 1 (chosen by a bias, say): one over their sum, in
+// the gradient of the weights, passes fp32's range for sums below 2^-128, the product with a score
+// does not.  Below this sum the gradient of a weight is divided by 2^64 until it has met its score.
+constexpr float kSmallChosen = 0x1p-64f;
+
 template <int VPT>
 __device__ __forceinline__ float pick(const float (&s)[VPT], int j) {
   float v = s[0];

@@ -444,7 +444,7 @@ int mxfp4_linear_backward(const void* grad, const void* x, const void* w, int dt
  * index, NaN counts as lower than every number.
  * weights[t,i] = scale * s[experts[t,i]], divided by the sum of the k chosen s
  * when renormalize is 1 (0 where that sum is 0).  A softmax row of -inf alone
- * has scores 0.
+ * has scores 0, and so has a logit below -88.7 with sigmoids (1 / (1 + e^-x) in fp32).
  *   logits [T,E], rows row_stride elements apart; weights, experts [T,k]. */
 int moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t row_stride,
               const float* bias, int64_t k, int score, int64_t groups, int64_t top_groups,
@@ -546,8 +546,9 @@ int moe_balance(const void* logits, int dtype, int64_t T, int64_t E, int64_t row
 /* grad_logits [T,E] (contiguous, of type dtype): gradient of sum_s grad_loss[s] *
  * loss[s], the counts taken as constant; 0 for tokens in no sequence.
  * grad_weights [T,k] (may be NULL): the gradient of moe_route's weights with this
- * renormalize and scale, as moe_route_backward gives it (0 where all sigmoids are 0
- * in fp32, and with them the weights), is added before the one rounding to dtype.
+ * renormalize and scale is added before the one rounding to dtype: what
+ * moe_route_backward gives, but for sigmoids of logits below -88.7, which are e^x
+ * here (and 0 with their gradients where a token has none above 2^-149).
  * experts may be NULL without grad_weights. */
 int moe_balance_backward(const float* grad_loss, const void* logits, int dtype, int64_t T,
                          int64_t E, int64_t row_stride, const int32_t* experts, int64_t k,
