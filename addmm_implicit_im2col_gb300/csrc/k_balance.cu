@@ -36,12 +36,13 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_
 
 // A sum as two fp32 numbers, exact to 2^-46 or so of its terms' magnitudes: 64-bit adds run
 // at a 64th of the fp32 rate here (with them a chunk's sums took 2 us more, and a sequence's
-// loss 1 to 2.5).
+// loss 1 to 2.5).  The steps that give a rounding error exactly are not the compiler's to
+// contract: a product taken unrounded into one of them would enter its error twice.
 struct Sum {
   float hi, lo;
   __device__ __forceinline__ void add(float v) {
-    const float t = hi + v, z = t - hi;
-    lo += (hi - (t - z)) + (v - z);
+    const float t = __fadd_rn(hi, v), z = __fsub_rn(t, hi);
+    lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(t, z)), __fsub_rn(v, z));
     hi = t;
   }
   __device__ __forceinline__ void add(const Sum& o) {
@@ -49,7 +50,7 @@ struct Sum {
     lo += o.lo;
   }
   __device__ __forceinline__ void add_times(const Sum& o, float c) {
-    const float v = o.hi * c;
+    const float v = __fmul_rn(o.hi, c);
     add(v);
     lo += fmaf(o.hi, c, -v) + o.lo * c;
   }
