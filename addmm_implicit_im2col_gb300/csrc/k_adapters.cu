@@ -1244,7 +1244,9 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
       ptx::tma_prefetch_desc(&maps.out);
     }
   }
-  // The call's inputs are there already (the first launch has waited for them); h is not.
+  // The call's inputs are there already (the first launch has waited for them); h is not.  Every
+  // role waits for the launch before this one by itself: what it then waits for with a limit is
+  // this block's work alone, however long that launch still ran.
   const T* base = static_cast<const T*>(g.base);
   T* out = static_cast<T*>(g.out);
   const int B = g.L + (g.base != g.out ? 1 : 0);  // rows without an adapter: copied, or left
@@ -1368,6 +1370,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
     }
   } else if (warp == UP_EPI + LOAD) {
     // ---------------------------------------------------------------- MMAs
+    ptx::griddep_wait();
     int last = -1, hb = 0;
     Slot hslot, wslot, aslot;
     bool product = false;
@@ -1534,6 +1537,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
           __syncwarp();
         }
         if (product) {
+          if (n == 0) ptx::griddep_wait();
           if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
           ptx::tc_fence_after();
           scale_it();
@@ -1630,6 +1634,7 @@ __global__ void __launch_bounds__(UP_THREADS<T>, sizeof(T) == 2 ? 2 : 1)
         if (lane == 0) ptx::bulk_commit();
       } else if constexpr (!TMA && sizeof(T) == 4) {
         if (product) {
+          if (n == 0) ptx::griddep_wait();
           if (!tc::warp_wait_bar(&ctl.accf[n & 1], (n >> 1) & 1, &ctl.abort, 11, wd)) break;
           ptx::tc_fence_after();
           scale_it();

@@ -37,3 +37,15 @@ def test_barriers_of_a_role_come_with_a_vote(path):
 @pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
 def test_named_barriers_are_the_common_ones(path):
     assert not re.search(r"\bbar\.(sync|red|arrive)\b", code(path))
+
+
+def test_roles_of_the_adapters_wait_for_the_launch_before_by_themselves():
+    """The weights' gradients may run for seconds where one adapter has all of many rows: the second
+    product, which starts beside their end, may not count that against its own waits' limit."""
+    body = kernels(code(os.path.join(build.CSRC, "k_adapters.cu")))["k_adapters_up"]
+    roles = re.split(r"\}\s*else if \(warp == UP_EPI \+ LOAD\) \{|\}\s*else \{\s*const int q4", body)
+    assert len(roles) == 3
+    for role in roles:
+        # what another role makes of the launch before: h, w and the accumulators
+        limited = [m.start() for m in re.finditer(r"warp_wait_bar\(&ctl\.(accf|acce|hfull|hempty|wfull|wempty)", role)]
+        assert limited and 0 <= role.find("griddep_wait()") < limited[0]
