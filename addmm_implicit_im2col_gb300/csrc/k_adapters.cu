@@ -2295,7 +2295,7 @@ int tmem_cols(int need) {
 // memory too, so none waits for it inside a cluster whose other blocks hold theirs on an SM
 // where another cluster's block waits.
 size_t smem_for(size_t bytes, int cols, size_t fixed = 2048) {  // fixed: static shared memory, at most
-  const size_t share = (size_t)(228 << 10) * cols / 512 - 1024, most = 232448 - fixed;
+  const size_t share = (size_t)(228 << 10) * cols / 512 - 1024, most = kBlockSharedMemory - fixed;
   bytes = bytes > share ? bytes : share;
   return bytes < most ? bytes : most;
 }
@@ -2432,13 +2432,17 @@ cudaError_t run_down(DownArgs& g, int problems, cudaStream_t s) {
 #undef IMC_DOWN
 }
 
+// Shared memory of a second product's block: what the kernel declares (in whole KB, since the
+// rings behind it are aligned to one), and a KB to align them by itself.
+constexpr int UP_STATIC = ((int)sizeof(UpCtl) + 1023) / 1024 * 1024, UP_ROOM = kBlockSharedMemory - UP_STATIC - 1024;
+
 template <typename T, bool TMA>
 cudaError_t run_up_as(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   using PL = Planes<T>;
   const Along along(g.R);
   constexpr int part = UP_EPI * UP_PART<T, TMA>, staged = UP_EPI * 32 * (STAGED_COLS + 1) * 4;
   // rings: at least two parts of base, one h, one w; then more parts, w, h
-  const int table = buckets_bytes(g.L), most = 232448 - (int)sizeof(UpCtl) - 256 - 1024 - table;
+  const int table = buckets_bytes(g.L), most = UP_ROOM - table;
   const bool ring = 2 * part + g.h_bytes + g.w_bytes <= most;
   g.slots = g.h_slots = 1;
   g.b_slots = ring ? 2 : 0;
@@ -2446,7 +2450,7 @@ cudaError_t run_up_as(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   // two blocks on an SM where both find room with two slots for w
   int limit = most, blocks = 1;
   if (sizeof(T) == 2) {
-    const int half = (228 << 9) - 1024 - (int)sizeof(UpCtl) - 256 - 1024 - table;
+    const int half = (228 << 9) - 1024 - UP_STATIC - 1024 - table;
     g.slots = 2;
     if (bytes() <= half) {
       limit = half;
@@ -2499,9 +2503,8 @@ cudaError_t run_up(UpArgs& g, const uint16_t* h, cudaStream_t s) {
   g.piece = piece_of(g.out, g.N * b | (int64_t)(reinterpret_cast<uintptr_t>(g.base) & 15));
   g.w_piece = piece_of(g.w, (g.turned ? g.N : g.r) * b);
   g.vec = g.w_piece == 16 && PL::PD == 1 ? 1 : 0;
-  // TMA: two parts of base have to fit beside h and w (fp32: up to rank 64, and 160 adapters)
-  const bool fits = 2 * UP_EPI * UP_PART<T, true> + g.h_bytes + g.w_bytes <=
-                    232448 - (int)sizeof(UpCtl) - 256 - 1024 - buckets_bytes(g.L);
+  // TMA: two parts of base have to fit beside h and w (fp32: up to rank 32, or 64 and 126 adapters)
+  const bool fits = 2 * UP_EPI * UP_PART<T, true> + g.h_bytes + g.w_bytes <= UP_ROOM - buckets_bytes(g.L);
   return g.piece == 16 && fits ? run_up_as<T, true>(g, h, s) : run_up_as<T, false>(g, h, s);
 }
 
@@ -2613,7 +2616,7 @@ cudaError_t run_grads(const AdapterGradArgs& a, int R, const uint16_t* h, const 
       const int stage = GRAD_ROWS * GRAD_COLS * 2 + grad_h_bytes(PL::PH * w.R), sums = GRAD_COLS * (w.R + 1) * 4;
       // two blocks per SM where three stages and a set of sums fit in half of it
       const int fixed = (int)(sizeof(GradCtl) + 1023) / 1024 * 1024 + 256;  // static shared memory
-      const int half = (114 << 10) - 1024 - fixed - 1024, most = 232448 - fixed - 1024;
+      const int half = (114 << 10) - 1024 - fixed - 1024, most = kBlockSharedMemory - fixed - 1024;
       const int room = 3 * stage + sums <= half ? half : most;
       w.stages = (room - sums) / stage < DOWN_STAGES ? (room - sums) / stage : DOWN_STAGES;
       while (w.stages * stage < sums) ++w.stages;  // (the ring holds a set of sums, too, in the end)
