@@ -1051,7 +1051,8 @@ def balance_loss(logits, experts, *, score="softmax", offsets=None):
         loss[s] = E / (k n^2) * sum_e counts[s, e] * sum_t p[t, e]
 
     with p the softmax of the logits, or their sigmoids divided by their sum; 1 for an even
-    choice, 0 for an empty sequence.
+    choice, 0 for an empty sequence.  Scores are fp32; their sums are fp32 over 64 tokens and
+    pairs of fp32 numbers (46 bits) beyond, in a fixed order.
     """
     dt, T, E, ld, k, score, S, _ = _check_balance(logits, experts, score, offsets)
     device = logits.device
@@ -1074,7 +1075,8 @@ def balance_loss_backward(grad_loss, logits, experts, counts, *, score="softmax"
     grad_loss [S] float32, counts as balance_loss returned them (constant).  With
     grad_weights [T, k] float32 the gradient of route_experts' weights (of the same score,
     and this renormalize and scale) is added in the same pass: the sum of this and
-    route_experts_backward, rounded once.
+    route_experts_backward, rounded once.  Tokens in no sequence have a gradient of 0 (of the
+    weights' alone, if that is given), whatever their logits hold.
     """
     dt, T, E, ld, k, score, S, device = _check_balance(logits, experts, score, offsets)
     _check_like(grad_loss, "grad_loss", _torch.float32, (S,), device)
@@ -1131,7 +1133,9 @@ def adapters_linear(x, a, b, layout, base=None, *, scale=None, out=None):
     layout is experts_layout(which[:, None], L) for which [T] int32, row t's adapter l; a
     row whose number is outside [0, L) has none, and out[t] = base[t].  One layout serves
     every projection of a step.  Returns out [T, N]; ``out`` may be ``base`` (in place:
-    rows without an adapter are left alone).
+    rows without an adapter are left alone).  Sums are fp32 and the output is rounded once; in
+    between x @ a^T is kept to 2^-17 of itself for the 16-bit types (two numbers of their size),
+    to 2^-23 for float32, whose products are of three bf16 or TF32 parts with the smallest left out.
     """
     dt, T, L, r, K, N, ld, dtype, device = _check_adapters(x, a, b, layout, scale)
     if base is not None:
@@ -1155,7 +1159,8 @@ def adapters_linear_backward(grad, x, a, b, layout, base=None, *, scale=None):
 
     Returns (grad_x [T, K], grad_a [L, r, K], grad_b [L, N, r]).  base [T, K] is added to
     grad_x (the gradient through the shared projection).  All tensors are contiguous and
-    of one float type; an adapter without rows has gradients of 0.
+    of one float type; an adapter without rows has gradients of 0.  grad @ b and x @ a^T are
+    kept as in adapters_linear (float16 in the weights' gradients: as two bfloat16 numbers).
     """
     dt, T, L, r, K, N, _, dtype, device = _check_adapters(x, a, b, layout, scale)
     _check_like(x, "x", dtype, (T, K), device)

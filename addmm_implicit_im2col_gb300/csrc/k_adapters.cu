@@ -175,8 +175,8 @@ struct Raw8 {
 // short: both products use mma.sync (a warp's small tiles need no shared memory and no
 // barriers, unlike tcgen05's), whose operands come straight from global memory, sixteen
 // bytes a lane: the order of the values along the summed axis is the same for both operands,
-// whatever it is.  One row of 8 adapters, r 16, 4096 x 4096, bf16, takes 6.0 us, 64 rows of 64
-// adapters, 4096 x 1024, 7.4 (10.5 MB of weights: 1.4 TB/s).
+// whatever it is.  One row of 8 adapters, r 16, 4096 x 4096, bf16, takes 5.8 us, 64 rows of 64
+// adapters, 4096 x 1024, 7.2 (10.5 MB of weights: 1.5 TB/s).
 constexpr int FEW = 8;
 constexpr int FEW_ROWS = 1024;  // rows whose numbers are asked for before the tile is known
 constexpr int FEW_N = 512;      // outputs staged at once

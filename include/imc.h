@@ -570,8 +570,8 @@ int moe_balance_backward(const float* grad_loss, const void* logits, int dtype, 
  *   base  [T,N] or NULL (zeros); out [T,N].  out may be base itself: then the rows
  *         without an adapter are neither read nor written.  No other overlap.
  * x, a, b, base and out are of type dtype; T <= 2^27, 1 <= K <= 2^20, N <= 2^20.
- * Sums are fp32, and x a^T is kept to 16 bits of precision (fp32: 24) for the second
- * product; an output is rounded once.  Non-finite values (fp32: above 3.38e38 too) reach their own
+ * Sums are fp32, and x a^T is kept to 16 bits of precision (fp32: 24; magnitudes below
+ * 2^-110 lose bits) for the second product; an output is rounded once.  Non-finite values (fp32: above 3.38e38 too) reach their own
  * row only, where an infinity may come out as NaN.
  * workspace: lowrank_linear_workspace_bytes(T, L, r) bytes (0 for few rows), 16-byte
  * aligned; NULL: from the library's pool.
